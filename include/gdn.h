@@ -45,7 +45,9 @@
  * gdn_gated_rmsnorm, gdn_prefill_norm (the prefill and the norm in one call),
  * gdn_decode_layer (conv -> decode step -> norm in one kernel) and gdn_prefill_layer
  * (conv -> prefill -> norm, the convolution inside the chunk prep; with
- * gdn_prefill_layer_workspace_bytes).
+ * gdn_prefill_layer_workspace_bytes), and the neighbouring state-space layer:
+ * gdn_ssm_prefill (with gdn_ssm_prefill_workspace_bytes) and gdn_ssm_decode, with
+ * gdn_rotary and gdn_rotary_frequencies for positions.
  *  - gdn_last_error_message() gives a human-readable detail of the last
  *    non-OK status returned on the calling thread.
  */
@@ -480,6 +482,138 @@ gdn_status gdn_prefill_layer(const gdn_shape *shape, const gdn_layer_params *lay
 /* gdn_prefill_layer_workspace_bytes -- the workspace gdn_prefill_layer needs for `shape`
  * (0 off the tensor-core shapes); never fails. */
 size_t gdn_prefill_layer_workspace_bytes(const gdn_shape *shape);
+
+/* ------------------------------------------------------------------------------------
+ * The selective state-space scan: the layer that hybrid models put beside gated
+ * delta-rule layers.  For every sequence and head there is a state S[d_state][head_dim] in
+ * fp32 (gdn's own layout, d_k = d_state and d_v = head_dim), and for each token in order
+ *     d_t = clamp(softplus(dt_t + dt_bias), dt_min, dt_max)
+ *     S   = exp(-exp(A_log) d_t) S + d_t B_t (x) x_t
+ *     y_t = S^T C_t + D x_t,   then  y_t *= z_t sigmoid(z_t)  when z is given
+ * Head h reads B and C of group h / (heads / groups).  x, B and C lie in one mixed row
+ * [x (heads x head_dim) | B (groups x d_state) | C (groups x d_state)], which a short causal
+ * convolution (gdn_causal_conv's, dilation 1) may cross first; its result is rounded to the
+ * I/O type, as gdn_causal_conv stores it.
+ * ---------------------------------------------------------------------------------- */
+typedef struct gdn_ssm_shape {
+    int32_t io_dtype;   /* gdn_dtype of xbc, dt, z, the conv's tensors and y               */
+    int32_t batch;      /* B; must be 1 when cu_seqlens is given                           */
+    int64_t seqlen;     /* T per sequence, or the packed token total with cu_seqlens       */
+    int32_t num_seqs;   /* N: equals batch, or len(cu_seqlens) - 1 with cu_seqlens         */
+    int32_t heads;      /* one state per head                                              */
+    int32_t head_dim;   /* 4..256, a multiple of 4                                         */
+    int32_t groups;     /* B / C groups; heads % groups == 0                               */
+    int32_t d_state;    /* 1..256                                                          */
+    /* Elements between the token rows of xbc, dt and z (0: contiguous), so that slices of
+       one projection's output can be given as they lie.  Row b T + t holds token t of
+       sequence b. */
+    int64_t xbc_stride, dt_stride, z_stride;
+} gdn_ssm_shape;
+
+typedef struct gdn_ssm_params {
+    int32_t conv_kernel;       /* K taps, 1..4, or 0: xbc is taken as it is                 */
+    int32_t conv_activation;   /* GDN_ACT_NONE or GDN_ACT_SILU                              */
+    float dt_min, dt_max;      /* 0 <= dt_min <= dt_max; dt_max may be infinite             */
+} gdn_ssm_params;
+
+/*
+ * gdn_ssm_prefill -- whole sequences.
+ *   xbc          [rows, C], C = heads head_dim + 2 groups d_state; dt [rows, heads]; z
+ *                [rows, heads, head_dim] or NULL; each with its own row stride.
+ *   conv_weight  [C, 1, K], conv_bias [C] or NULL, conv_state_in [N, K - 1, C] (oldest first)
+ *                or NULL (zeros), conv_state_out [N, K - 1, C]: the last K - 1 inputs of each
+ *                sequence.  It must not overlap conv_state_in.  All unread with K = 0.
+ *   A_log        [heads] fp32; dt_bias, D [heads] fp32 or NULL (zeros).
+ *   state_in     [N, heads, d_state, head_dim] fp32 or NULL (zeros); state_out the same
+ *                shape, and may be state_in itself.  16-byte aligned.
+ *   cu_seqlens   as gdn_prefill.  A sequence with no tokens keeps its states.
+ *   y            [rows, heads, head_dim], contiguous; must not overlap xbc or z.
+ *   workspace    gdn_ssm_prefill_workspace_bytes(shape, params) bytes, 16-byte aligned; its
+ *                contents need no initialisation and are not preserved.
+ * Inputs are finite, but dt may be -infinity: with dt_min 0 such a token's step is 0, and it
+ * leaves the state as it was.  Errors are found before anything is launched, but for malformed
+ * cu_seqlens (gdn_last_device_status), whose sequences are skipped.
+ */
+size_t gdn_ssm_prefill_workspace_bytes(const gdn_ssm_shape *shape, const gdn_ssm_params *params);
+
+gdn_status gdn_ssm_prefill(const gdn_ssm_shape *shape, const gdn_ssm_params *params, const void *xbc, const void *dt,
+                           const void *z, const void *conv_weight, const void *conv_bias, const void *conv_state_in,
+                           void *conv_state_out, const float *A_log, const float *dt_bias, const float *D,
+                           const float *state_in, const int32_t *cu_seqlens, void *y, float *state_out, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_ssm_decode -- one token per row (seqlen 1, batch = num_seqs), both states in place.
+ *   conv_state   [E, K - 1, C] and state [E, heads, d_state, head_dim] fp32 (16-byte
+ *                aligned), E = pool_size with slots, else batch: row b advances entry
+ *                slots[b] (DEVICE int32 [batch]), or entry b when slots is NULL.  The rows
+ *                should name distinct entries: what a repeated entry, or a row that names
+ *                one, holds afterwards is unspecified.  A slot outside [0, pool_size) skips
+ *                its row (y and both states as they were) and sets the device check word.
+ *   The rest as gdn_ssm_prefill; no workspace.
+ */
+gdn_status gdn_ssm_decode(const gdn_ssm_shape *shape, const gdn_ssm_params *params, const void *xbc, const void *dt,
+                          const void *z, const void *conv_weight, const void *conv_bias, void *conv_state,
+                          const float *A_log, const float *dt_bias, const float *D, float *state, int64_t pool_size,
+                          const int32_t *slots, void *y, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * Rotary positions, for q and k of a linear or gated rule, or C and B of a state-space
+ * layer: the pairs (a, b) of the rotated part become scale (a cos t - b sin t,
+ * b cos t + a sin t), t = position * inv_freq[i]; the head's other dimensions are copied.
+ * ---------------------------------------------------------------------------------- */
+typedef struct gdn_rotary_shape {
+    int32_t io_dtype;
+    int32_t batch;                 /* must be 1 when cu_seqlens is given                     */
+    int64_t seqlen;                /* rows = batch * seqlen                                  */
+    int32_t num_seqs;              /* equals batch, or len(cu_seqlens) - 1                   */
+    int32_t heads_q, heads_k;      /* either may be 0: that tensor is absent                 */
+    int32_t head_dim;              /* 2..1024                                                */
+    int32_t rot_dim, rot_offset;   /* the rotated dimensions [offset, offset + rot_dim);
+                                      rot_dim even, 2..256                                   */
+    int32_t interleaved;           /* 1: pair i is (2i, 2i + 1); 0: (i, i + rot_dim / 2)     */
+    int32_t inverse;               /* 1: turn by -t (the transpose: also the gradient's turn) */
+    float scale;                   /* multiplies cos and sin; finite                         */
+    /* Element strides; a head's dimensions are contiguous, and heads lie inside their row. */
+    int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride;
+    int64_t q_out_row_stride, q_out_head_stride, k_out_row_stride, k_out_head_stride;
+} gdn_rotary_shape;
+
+/*
+ * gdn_rotary -- q [rows, heads_q, head_dim] to q_out and k [rows, heads_k, head_dim] to k_out
+ * in one launch.  An output may be its input itself (same strides); other overlaps give
+ * undefined results.
+ *   inv_freq   DEVICE fp32 [rot_dim / 2], finite (gdn_rotary_frequencies).  The angle is
+ *              reduced in 64-bit binary fractions of a turn, so it keeps its precision at
+ *              every int32 position.
+ *   positions  DEVICE int32 [rows], any sign, or NULL: a row's place in its sequence, which
+ *              cu_seqlens (DEVICE int32 [num_seqs + 1], or NULL) gives.
+ */
+gdn_status gdn_rotary(const gdn_rotary_shape *shape, const void *q, const void *k, const float *inv_freq,
+                      const int32_t *positions, const int32_t *cu_seqlens, void *q_out, void *k_out, void *stream);
+
+typedef enum {
+    GDN_ROTARY_PLAIN = 0,      /* base^(-2i / rot_dim)                                       */
+    GDN_ROTARY_LINEAR = 1,     /* every frequency / factor                                   */
+    GDN_ROTARY_BASE = 2,       /* base factor^(rot_dim / (rot_dim - 2)) in base's place      */
+    GDN_ROTARY_BANDS = 3,      /* / factor below `low` turns over trained_length, as it is above
+                                  `high` turns, a ramp over the indices between; scale
+                                  0.1 ln(factor) + 1                                         */
+    GDN_ROTARY_WAVELENGTH = 4  /* / factor below `low` turns, as it is above `high`, a ramp over
+                                  the turns between                                          */
+} gdn_rotary_kind;
+
+typedef struct gdn_rotary_scaling {
+    int32_t kind;              /* gdn_rotary_kind                                            */
+    double base;               /* > 1                                                        */
+    double factor;             /* >= 1; unread for PLAIN                                     */
+    double trained_length;     /* > 0, tokens; BANDS and WAVELENGTH                          */
+    double low, high;          /* 0 < low < high, turns; BANDS and WAVELENGTH                */
+} gdn_rotary_scaling;
+
+/* gdn_rotary_frequencies -- fills the HOST array inv_freq [rot_dim / 2] and *scale (may be
+ * NULL), gdn_rotary's factor.  Launches nothing. */
+gdn_status gdn_rotary_frequencies(const gdn_rotary_scaling *scaling, int32_t rot_dim, float *inv_freq, float *scale);
 
 /*
  * gdn_last_device_status -- synchronise `stream`, read the device check word

@@ -9,4 +9,6 @@ from .gdn import (GdnError, GdnShape, gdn_causal_conv, gdn_causal_conv_slots,  #
                   gdn_prefill, gdn_prefill_noalloc, gdn_prefill_norm, gdn_prefill_variant,
                   gdn_prefill_variant_plan, gdn_prefill_variant_workspace_bytes,
                   gdn_prefill_workspace_bytes,
-                  gdn_scan_variant, gdn_scan_window, gdn_status_string, load)
+                  gdn_rotary, gdn_rotary_frequencies,
+                  gdn_scan_variant, gdn_scan_window, gdn_ssm_decode, gdn_ssm_prefill,
+                  gdn_ssm_prefill_workspace_bytes, gdn_status_string, load)

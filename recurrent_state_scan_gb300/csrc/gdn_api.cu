@@ -129,6 +129,8 @@ gdn_status report_error(gdn_status status, const char *message) {
     return fail(status, "%s", message);
 }
 
+gdn_status device_check_word(int **out) { return status_word(out); }
+
 }  // namespace gdn
 
 using namespace gdn;

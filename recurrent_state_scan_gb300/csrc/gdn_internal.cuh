@@ -144,6 +144,8 @@ cudaError_t launch_decode_layer(const LayerDecodeParams &p, gdn_dtype io, cudaSt
 
 // Sets the calling thread's last error message; returns `status`.
 gdn_status report_error(gdn_status status, const char *message);
+// Address of the device check word in the current device's context.
+gdn_status device_check_word(int **out);
 
 // Chunked tensor-core prefill (bf16/f16 I/O, d_k = d_v = 128): a chunk-prep kernel
 // that writes one workspace record per (chunk, value head), then a state-scan kernel.

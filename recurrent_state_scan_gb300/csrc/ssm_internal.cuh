@@ -1,0 +1,78 @@
+// ssm_internal.cuh -- what the state-space scan's translation units share.
+#pragma once
+
+#include "gdn_internal.cuh"
+
+namespace gdn {
+
+// One call of the selective state-space scan (validated arguments).  `rows` of x, dt and z
+// are token rows (t of sequence b at b * seqlen + t, or the packed index).
+struct SsmParams {
+    // The rows the scan reads: x of head h at xs + h * x_head, B of group g at
+    // xs + off_b + g * bc_group, C at xs + off_c + g * bc_group, row stride ldx (elements).
+    const void *xs;
+    int64_t ldx;
+    int32_t x_head, off_b, off_c, bc_group;
+    const void *dt, *z;          // z may be null
+    int64_t ld_dt, ld_z;
+    const float *A_log, *dt_bias, *D;   // dt_bias, D may be null
+    float dt_min, dt_max;
+    const float *state_in;       // may be null (zeros); may alias state_out
+    float *state_out;
+    void *y;                     // [rows, H, P]
+    const int32_t *cu_seqlens;   // may be null
+    int64_t seqlen, rows;
+    int32_t num_seqs, heads, groups, head_dim, d_state;
+    int *status;
+};
+
+// The causal convolution of the mixed rows [x | B | C] before the scan, packed-aware:
+// u [rows][..] in the layout SsmParams describes (ld_u, x_head, off_b, off_c, bc_group).
+struct SsmConvParams {
+    const void *x;
+    int64_t ld_x;
+    const void *w, *bias;        // [C][K], [C] or null
+    const void *conv_in;         // [n][K - 1][C] or null (zeros)
+    void *conv_out;              // [n][K - 1][C]
+    void *u;
+    int64_t ld_u;
+    int32_t x_head, off_b, off_c, bc_group;
+    const int32_t *cu_seqlens;
+    int64_t seqlen, rows;
+    int32_t num_seqs, heads, groups, head_dim, d_state;
+    int32_t C, K, silu;          // K = 1 with a null w: a copy (rows re-laid for the scan)
+    int *status;
+};
+
+struct SsmDecodeParams {
+    const void *x, *dt, *z;
+    int64_t ld_x, ld_dt, ld_z;
+    const void *w, *bias;        // w null: x is used as it is
+    void *conv;                  // [pool][K - 1][C], advanced in place
+    const float *A_log, *dt_bias, *D;
+    float dt_min, dt_max;
+    float *state;                // [pool][H][N][P], advanced in place
+    int64_t pool_size;
+    const int32_t *slots;        // may be null: row b is entry b
+    void *y;
+    int32_t batch, heads, groups, head_dim, d_state, C, K, silu;
+    int *status;
+};
+
+cudaError_t launch_ssm_conv(const SsmConvParams &p, gdn_dtype io, cudaStream_t stream);
+cudaError_t launch_ssm_scan_simt(const SsmParams &p, gdn_dtype io, cudaStream_t stream);
+cudaError_t launch_ssm_decode(const SsmDecodeParams &p, gdn_dtype io, cudaStream_t stream);
+
+// silu as the convolution stores it: the correctly scaled exponential and a true divide,
+// so that its rounding to a 16-bit type does not hang on an approximation's last bits.
+__device__ __forceinline__ float silu_exact(float v) { return v / (1.0f + expf(-v)); }
+// silu of the gate z, which only meets the output's own rounding: fast intrinsics.
+__device__ __forceinline__ float silu_gate(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+
+// The step d = clamp(softplus(dt + dt_bias), dt_min, dt_max); a NaN stays one.
+__device__ __forceinline__ float ssm_step(float dt, float bias, float lo, float hi) {
+    const float d = softplus_f(dt + bias);
+    return d < lo ? lo : d > hi ? hi : d;
+}
+
+}  // namespace gdn

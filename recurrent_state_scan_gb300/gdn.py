@@ -8,6 +8,7 @@ loaded every call raises -- there is no CPU or PyTorch fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -28,12 +29,15 @@ EXPORTS = ("gdn_prefill_workspace_bytes", "gdn_prefill", "gdn_decode_step",
            "gdn_scan_window", "gdn_scan_variant", "gdn_causal_conv", "gdn_causal_conv_slots",
            "gdn_gated_rmsnorm", "gdn_set_wait_budget", "gdn_decode_layer", "gdn_prefill_variant",
            "gdn_prefill_norm", "gdn_prefill_variant_workspace_bytes", "gdn_prefill_variant_plan",
-           "gdn_prefill_layer", "gdn_prefill_layer_workspace_bytes")
+           "gdn_prefill_layer", "gdn_prefill_layer_workspace_bytes", "gdn_ssm_prefill_workspace_bytes",
+           "gdn_ssm_prefill", "gdn_ssm_decode", "gdn_rotary", "gdn_rotary_frequencies")
 PATH_SIMT, PATH_TC, PATH_TC_TP = 1, 2, 3
 # gdn_rule codes.
 RULES = {"gated_delta": 0, "delta": 1, "gated": 2, "linear": 3}
 # gdn_activation codes.
 ACTIVATIONS = {"none": 0, "silu": 1, "swish": 1, "sigmoid": 2}
+# gdn_rotary_kind codes.
+ROTARY_KINDS = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "wavelength": 4}
 
 
 class GdnShape(ctypes.Structure):
@@ -59,6 +63,37 @@ class GdnConvShape(ctypes.Structure):
 class GdnLayerParams(ctypes.Structure):
     _fields_ = [("conv_kernel", ctypes.c_int32), ("conv_activation", ctypes.c_int32),
                 ("norm_activation", ctypes.c_int32), ("norm_epsilon", ctypes.c_float)]
+
+
+class GdnSsmShape(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("seqlen", ctypes.c_int64), ("num_seqs", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("d_state", ctypes.c_int32),
+                ("xbc_stride", ctypes.c_int64), ("dt_stride", ctypes.c_int64),
+                ("z_stride", ctypes.c_int64)]
+
+
+class GdnSsmParams(ctypes.Structure):
+    _fields_ = [("conv_kernel", ctypes.c_int32), ("conv_activation", ctypes.c_int32),
+                ("dt_min", ctypes.c_float), ("dt_max", ctypes.c_float)]
+
+
+class GdnRotaryShape(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("seqlen", ctypes.c_int64), ("num_seqs", ctypes.c_int32),
+                ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("rot_offset", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("scale", ctypes.c_float)] + \
+               [(name, ctypes.c_int64) for name in (
+                   "q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride",
+                   "q_out_row_stride", "q_out_head_stride", "k_out_row_stride", "k_out_head_stride")]
+
+
+class GdnRotaryScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("trained_length", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double)]
 
 
 class GdnError(RuntimeError):
@@ -135,6 +170,18 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.gdn_prefill_norm.argtypes = [S, P, P, P, P, P, P, P, P, P, ctypes.c_float, P, P,
                                      ctypes.c_float, ctypes.c_int32, ctypes.c_int32, P, P, P,
                                      ctypes.c_size_t, P]
+    SS, SP = ctypes.POINTER(GdnSsmShape), ctypes.POINTER(GdnSsmParams)
+    lib.gdn_ssm_prefill_workspace_bytes.restype = ctypes.c_size_t
+    lib.gdn_ssm_prefill_workspace_bytes.argtypes = [SS, SP]
+    lib.gdn_ssm_prefill.restype = ctypes.c_int
+    lib.gdn_ssm_prefill.argtypes = [SS, SP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.gdn_ssm_decode.restype = ctypes.c_int
+    lib.gdn_ssm_decode.argtypes = [SS, SP, P, P, P, P, P, P, P, P, P, P, ctypes.c_int64, P, P, P]
+    lib.gdn_rotary.restype = ctypes.c_int
+    lib.gdn_rotary.argtypes = [ctypes.POINTER(GdnRotaryShape), P, P, P, P, P, P, P, P]
+    lib.gdn_rotary_frequencies.restype = ctypes.c_int
+    lib.gdn_rotary_frequencies.argtypes = [ctypes.POINTER(GdnRotaryScaling), ctypes.c_int32, P,
+                                           ctypes.POINTER(ctypes.c_float)]
     lib.gdn_decode_layer.restype = ctypes.c_int
     lib.gdn_decode_layer.argtypes = [S, ctypes.POINTER(GdnLayerParams), P, P, P, P, P, P, P, P, P,
                                      P, ctypes.c_float, P, P, P, P]
@@ -794,3 +841,240 @@ def gdn_prefill_layer(x, conv_weight, conv_bias, conv_state_in, a, b, A_log, dt_
                                  float(scale), _ptr(norm_scale), _ptr(gate), _ptr(y), _ptr(state_out),
                                  int(bool(fuse)), _ptr(workspace), ws_bytes, _stream(stream)))
     return y, state_out, conv_state_out
+
+
+# ------------------------------------------------------------------ the state-space layer
+def _on(device, stream):
+    """The context a call allocates and launches in: its tensors' device, and the stream's own
+    memory pool when it names one (a workspace freed on return is then reused in its order)."""
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        ctx.enter_context(torch.cuda.stream(stream))
+    return ctx
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be on {device}, as the call's first tensor is")
+
+
+def _need_shape(name: str, t, shape, dtype):
+    """A contiguous CUDA tensor of this shape and type; None passes."""
+    if t is None:
+        return
+    _need_cuda(name, t, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _row_stride(name: str, t, B: int, T: int, row: tuple, dtype) -> int:
+    """Elements between the token rows of t [B, T, *row], whose rows are contiguous and evenly spaced."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != (B, T) + row:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be {(B, T) + row}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be {dtype}, got {t.dtype}")
+    step = 1
+    for n, s in zip(reversed(row), reversed(t.stride()[2:])):
+        if n > 1 and s != step:
+            raise GdnError(GDN_ERR_INVALID_ARG, f"{name}'s token rows must be contiguous")
+        step *= n
+    if T > 1:
+        if B > 1 and t.stride(0) != T * t.stride(1):
+            raise GdnError(GDN_ERR_INVALID_ARG, f"{name}'s token rows must be evenly spaced over the batch")
+        return t.stride(1)
+    return t.stride(0) if B > 1 else step
+
+
+def _ssm_geometry(xbc, dt, z, heads, head_dim, groups, d_state, cu_seqlens, conv_weight, conv_activation, dt_min, dt_max):
+    """(shape, params) of the call; the rows are checked."""
+    if not isinstance(xbc, torch.Tensor) or xbc.dim() != 3 or xbc.dtype not in _DTYPE_CODE:
+        raise GdnError(GDN_ERR_INVALID_ARG, "xbc must be [B, T, C] in float32, bfloat16 or float16")
+    if conv_activation not in ("none", "silu"):
+        raise GdnError(GDN_ERR_INVALID_ARG, "the convolution's activation is 'none' or 'silu'")
+    B, T = xbc.shape[:2]
+    C = heads * head_dim + 2 * groups * d_state
+    n = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    K = 0
+    if conv_weight is not None:
+        if C <= 0 or conv_weight.dim() == 0 or conv_weight.shape[0] != C or conv_weight.numel() == 0:
+            raise GdnError(GDN_ERR_INVALID_ARG, f"conv_weight must be [{C}, 1, K]")
+        K = conv_weight.numel() // C
+    shape = GdnSsmShape(_DTYPE_CODE[xbc.dtype], B, T, n, heads, head_dim, groups, d_state,
+                        _row_stride("xbc", xbc, B, T, (C,), xbc.dtype),
+                        _row_stride("dt", dt, B, T, (heads,), xbc.dtype),
+                        0 if z is None else _row_stride("z", z, B, T, (heads, head_dim), xbc.dtype))
+    return shape, GdnSsmParams(K, ACTIVATIONS[conv_activation], float(dt_min), float(dt_max))
+
+
+def gdn_ssm_prefill_workspace_bytes(shape: GdnSsmShape, params: GdnSsmParams) -> int:
+    return int(load().gdn_ssm_prefill_workspace_bytes(ctypes.byref(shape), ctypes.byref(params)))
+
+
+def gdn_ssm_prefill(xbc, dt, A_log, *, heads: int, head_dim: int, d_state: int, groups: int = 1, D=None, dt_bias=None,
+                    z=None, conv_weight=None, conv_bias=None, conv_state_in=None, conv_activation: str = "silu",
+                    state_in=None, cu_seqlens=None, dt_min: float = 0.0, dt_max: float = float("inf"), y=None,
+                    state_out=None, conv_state_out=None, workspace=None, stream=None):
+    """The selective state-space scan over whole sequences, behind its short causal convolution.
+
+    xbc [B, T, C], C = heads head_dim + 2 groups d_state, rows [x | B | C]; dt [B, T, heads]; z
+    [B, T, heads, head_dim] or None: token rows may be slices of wider ones (contiguous in
+    themselves, evenly spaced).  With cu_seqlens (int32 [N + 1]) B is 1 and T the packed total.
+    conv_weight [C, 1, K] (K <= 4) and conv_bias [C], or None: xbc is taken as it is.
+    conv_state_in [N, K - 1, C], state_in [N, heads, d_state, head_dim] fp32: zeros when None.
+    A_log, dt_bias, D [heads] fp32.  Returns (y [B, T, heads, head_dim], state_out,
+    conv_state_out or None)."""
+    lib = load()
+    shape, params = _ssm_geometry(xbc, dt, z, heads, head_dim, groups, d_state, cu_seqlens, conv_weight, conv_activation,
+                                  dt_min, dt_max)
+    io, dev, (B, T, C), n, K = xbc.dtype, xbc.device, xbc.shape, shape.num_seqs, params.conv_kernel
+    states, convs = (max(n, 0), heads, d_state, head_dim), (max(n, 0), max(K - 1, 0), C)
+    if cu_seqlens is not None:
+        _need_shape("cu_seqlens", cu_seqlens, (n + 1,), torch.int32)
+    for name, t in (("A_log", A_log), ("dt_bias", dt_bias), ("D", D)):
+        _need_shape(name, t, (heads,), torch.float32)
+    for name, t in (("conv_weight", conv_weight), ("workspace", workspace)):
+        if t is not None:
+            _need_cuda(name, t, io if name == "conv_weight" else None)
+    _need_shape("conv_bias", conv_bias, (C,), io)
+    _need_shape("state_in", state_in, states, torch.float32)
+    _need_shape("state_out", state_out, states, torch.float32)
+    _need_shape("y", y, (B, T, heads, head_dim), io)
+    _need_shape("conv_state_in", conv_state_in, convs, io)
+    _need_shape("conv_state_out", conv_state_out, convs, io)
+    _same_device(dev, dt=dt, z=z, A_log=A_log, dt_bias=dt_bias, D=D, conv_weight=conv_weight, conv_bias=conv_bias,
+                 conv_state_in=conv_state_in, conv_state_out=conv_state_out, state_in=state_in, state_out=state_out,
+                 cu_seqlens=cu_seqlens, y=y, workspace=workspace)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty((B, T, heads, head_dim), dtype=io, device=dev)
+        if state_out is None:
+            state_out = torch.empty(states, dtype=torch.float32, device=dev)
+        if conv_state_out is None and K:
+            conv_state_out = torch.empty(convs, dtype=io, device=dev)
+        need = gdn_ssm_prefill_workspace_bytes(shape, params)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(lib.gdn_ssm_prefill(ctypes.byref(shape), ctypes.byref(params), _ptr(xbc), _ptr(dt), _ptr(z), _ptr(conv_weight),
+                                   _ptr(conv_bias), _ptr(conv_state_in), _ptr(conv_state_out), _ptr(A_log), _ptr(dt_bias),
+                                   _ptr(D), _ptr(state_in), _ptr(cu_seqlens), _ptr(y), _ptr(state_out), _ptr(workspace),
+                                   ws_bytes, _stream(stream)))
+    return y, state_out, conv_state_out
+
+
+def gdn_ssm_decode(xbc, dt, A_log, state, *, heads: int, head_dim: int, d_state: int, groups: int = 1, D=None, dt_bias=None,
+                   z=None, conv_weight=None, conv_bias=None, conv_state=None, conv_activation: str = "silu", slots=None,
+                   dt_min: float = 0.0, dt_max: float = float("inf"), y=None, stream=None):
+    """One token of the state-space layer per row: gdn_ssm_prefill's arguments at T = 1, with
+    ``state`` [E, heads, d_state, head_dim] fp32 and ``conv_state`` [E, K - 1, C] advanced in
+    place.  With slots (int32 [B], distinct) row b uses entry slots[b], else entry b (E = B).
+    Returns y [B, 1, heads, head_dim]."""
+    lib = load()
+    shape, params = _ssm_geometry(xbc, dt, z, heads, head_dim, groups, d_state, None, conv_weight, conv_activation, dt_min,
+                                  dt_max)
+    io, dev, (B, T, C), K = xbc.dtype, xbc.device, xbc.shape, params.conv_kernel
+    _need_cuda("state", state, torch.float32)
+    E = state.shape[0] if slots is not None and state.dim() == 4 else B
+    _need_shape("state", state, (E, heads, d_state, head_dim), torch.float32)
+    for name, t in (("A_log", A_log), ("dt_bias", dt_bias), ("D", D)):
+        _need_shape(name, t, (heads,), torch.float32)
+    if conv_weight is not None:
+        _need_cuda("conv_weight", conv_weight, io)
+    _need_shape("conv_bias", conv_bias, (C,), io)
+    _need_shape("slots", slots, (B,), torch.int32)
+    _need_shape("y", y, (B, T, heads, head_dim), io)
+    if K > 1 and conv_state is None:
+        raise GdnError(GDN_ERR_INVALID_ARG, "conv_state is needed with conv_weight")
+    if K:
+        _need_shape("conv_state", conv_state, (E, K - 1, C), io)
+    _same_device(dev, dt=dt, z=z, A_log=A_log, dt_bias=dt_bias, D=D, conv_weight=conv_weight, conv_bias=conv_bias,
+                 conv_state=conv_state, state=state, slots=slots, y=y)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty((B, T, heads, head_dim), dtype=io, device=dev)
+        _check(lib.gdn_ssm_decode(ctypes.byref(shape), ctypes.byref(params), _ptr(xbc), _ptr(dt), _ptr(z), _ptr(conv_weight),
+                                  _ptr(conv_bias), _ptr(conv_state), _ptr(A_log), _ptr(dt_bias), _ptr(D), _ptr(state), E,
+                                  _ptr(slots), _ptr(y), _stream(stream)))
+    return y
+
+
+# ------------------------------------------------------------------ rotary positions
+def gdn_rotary_frequencies(rot_dim: int, base: float = 10000.0, kind: str = "plain", *, factor: float = 1.0,
+                           trained_length: float = 0.0, low: float = 1.0, high: float = 32.0, device=None):
+    """(inv_freq [rot_dim / 2] fp32, scale) for gdn_rotary: 'plain'; 'linear' (positions / factor);
+    'base' (the base grown by factor); 'bands' and 'wavelength' (frequencies that turn less than
+    `low` times over trained_length divided by factor, those above `high` times kept)."""
+    if kind not in ROTARY_KINDS:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"kind must be one of {sorted(ROTARY_KINDS)}")
+    inv_freq = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float32)
+    scale = ctypes.c_float()
+    scaling = GdnRotaryScaling(ROTARY_KINDS[kind], base, factor, trained_length, low, high)
+    _check(load().gdn_rotary_frequencies(ctypes.byref(scaling), rot_dim, ctypes.c_void_p(inv_freq.data_ptr()),
+                                         ctypes.byref(scale)))
+    return inv_freq.to(device) if device is not None else inv_freq, scale.value
+
+
+def _head_strides(name: str, t, B: int, T: int, dtype):
+    """(row, head) element strides of t [B, T, H, D], whose rows are evenly spaced."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
+    if t.dim() != 4 or tuple(t.shape[:2]) != (B, T):
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be [{B}, {T}, H, D]")
+    if t.dtype != dtype:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be {dtype}, got {t.dtype}")
+    H, D = t.shape[2:]
+    if D > 1 and t.stride(3) != 1:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name}'s heads must be contiguous")
+    head = t.stride(2) if H > 1 else D
+    if T > 1 and B > 1 and t.stride(0) != T * t.stride(1):
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name}'s token rows must be evenly spaced over the batch")
+    return (t.stride(1) if T > 1 else t.stride(0) if B > 1 else max(H * head, D)), head
+
+
+def gdn_rotary(q, k, inv_freq, *, positions=None, cu_seqlens=None, rot_offset: int = 0, interleaved: bool = False,
+               inverse: bool = False, scale: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Rotary positions on q [B, T, Hq, D] and k [B, T, Hk, D] (or None) in one launch.
+
+    inv_freq [rot_dim / 2] fp32 turns dimensions [rot_offset, rot_offset + rot_dim) in pairs
+    (2i, 2i + 1) when interleaved, else (i, i + rot_dim / 2); the rest is copied.  positions
+    int32 [B, T], or None: a token's place in its sequence (cu_seqlens int32 [N + 1] when packed).
+    Heads may be slices of wider rows.  q_out / k_out may be q / k.  Returns (q_out, k_out)."""
+    lib = load()
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.dtype not in _DTYPE_CODE:
+        raise GdnError(GDN_ERR_INVALID_ARG, "q must be [B, T, H, D] in float32, bfloat16 or float16")
+    B, T, hq, D = q.shape
+    if k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 4 or k.shape[3] != D):
+        raise GdnError(GDN_ERR_INVALID_ARG, f"k must be [{B}, {T}, H, {D}]")
+    hk = 0 if k is None else k.shape[2]
+    _need_cuda("inv_freq", inv_freq, torch.float32)
+    if inv_freq.dim() != 1:
+        raise GdnError(GDN_ERR_INVALID_ARG, "inv_freq must be [rot_dim / 2]")
+    _need_shape("positions", positions, (B, T), torch.int32)
+    if cu_seqlens is not None:
+        _need_shape("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), torch.int32)
+    strides = [*_head_strides("q", q, B, T, q.dtype), *((0, 0) if k is None else _head_strides("k", k, B, T, q.dtype))]
+    _same_device(q.device, k=k, inv_freq=inv_freq, positions=positions, cu_seqlens=cu_seqlens, q_out=q_out, k_out=k_out)
+    with _on(q.device, stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k_out is None and k is not None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+            if like is None:
+                strides += [0, 0]
+                continue
+            strides += _head_strides(name, t, B, T, q.dtype)
+            if t.shape != like.shape:
+                raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be {tuple(like.shape)}")
+        n = B if cu_seqlens is None else cu_seqlens.numel() - 1
+        shape = GdnRotaryShape(_DTYPE_CODE[q.dtype], B, T, n, hq, hk, D, 2 * inv_freq.numel(), rot_offset,
+                               int(bool(interleaved)), int(bool(inverse)), float(scale), *strides)
+        _check(lib.gdn_rotary(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(inv_freq), _ptr(positions), _ptr(cu_seqlens),
+                              _ptr(q_out), _ptr(k_out), _stream(stream)))
+    return q_out, k_out

@@ -1,0 +1,394 @@
+"""The state-space layer (gdn_ssm_prefill, gdn_ssm_decode) against the plain 64-bit definition, its
+refusals (on the CPU), and a run of it with the rotary positions and the layer ops around it.
+
+Tolerances, relative in the 2-norm unless said otherwise, count roundings of half a step,
+u = finfo(t).eps / 2 (bf16 2^-8, f16 2^-11, f32 2^-24).  With q = u / sqrt(3), the root mean square of
+a rounding spread evenly over half a step each way:
+* y of 16-bit types is rounded once, and on the tensor cores its two parts meet one more
+  rounding each (the decay-weighted scores, the state); three independent ones and a margin of
+  two: 2 sqrt(3) q = 2 u.
+* The fp32 state and fp32 y: sums of up to T = 700 terms in fp32 whose errors add as at most
+  T u = 4e-5 in the worst case and sqrt(T) u = 1.6e-6 as they fall; exp and log1p add 2 ulp a
+  step on exponents up to 16: 1e-5 bounds both, and the two-term bf16 split of the tensor
+  cores (2^-16 of each product, at random signs) stays inside it.
+* Behind a convolution in a 16-bit type, x and B are roundings of an fp32 value whose own error, some
+  8 x 2^-24 of it, puts it on the other side of a rounding's border than the 64-bit value with
+  probability 2 x 8 x 2^-24 over a step (bf16 2^-8, f16 2^-11 at least): p = 2^-12, 2^-9.  It is then
+  off by a whole step (2^-7, 2^-10 at most), so the state's mean square error is 2 p step^2 = 2^-25,
+  2^-28 of its square, the few values of a small case seeing up to four times its root: 2^-10.5, 2^-12.
+"""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import recurrent_state_scan_gb300 as lib
+from recurrent_state_scan_gb300 import gdn
+from test_rotary import rel, turn
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+STATE_TOL = 1e-5
+
+
+def state_tol(m):
+    return {torch.bfloat16: 2.0 ** -10.5, torch.float16: 2.0 ** -12}.get(m["io"], STATE_TOL) if m["K"] else STATE_TOL
+
+
+def y_tol(dtype):
+    return 1e-5 if dtype == torch.float32 else 2 * torch.finfo(dtype).eps / 2
+
+
+# ------------------------------------------------------------------ inputs and definitions
+def draw(io, lens, H, P, G, N, K, *, packed=True, z=True, initial=True, seed=0, device="cuda", gap=5):
+    """A layer's tensors; x, dt and z are slices of one row with `gap` unused values behind them."""
+    g = torch.Generator().manual_seed(seed)
+    dt_ = DT[io]
+    B, T = (1, sum(lens)) if packed else (len(lens), lens[0] if lens else 0)
+    C, n = H * P + 2 * G * N, len(lens)
+    rnd = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    row = rnd(B, T, 2 * H * P + 2 * G * N + H + gap).to(dt_).to(device)
+    hp = H * P
+    m = {"lens": lens, "H": H, "P": P, "G": G, "N": N, "K": K, "packed": packed, "io": dt_,
+         "z": row[..., :hp].unflatten(2, (H, P)) if z else None, "xbc": row[..., hp:hp + C], "dt": row[..., hp + C:hp + C + H],
+         "A_log": torch.log(1 + 15 * torch.rand(H, generator=g)).to(device), "dt_bias": (rnd(H) - 3).to(device),
+         "D": rnd(H).to(device), "w": None, "b": None, "conv": None, "state": None, "cu": None}
+    if K:
+        m["w"], m["b"] = (rnd(C, 1, K) * K ** -0.5).to(dt_).to(device), (0.1 * rnd(C)).to(dt_).to(device)
+        m["conv"] = rnd(n, K - 1, C).to(dt_).to(device) if initial else None
+    if initial:
+        m["state"] = (0.5 * rnd(n, H, N, P)).to(device)
+    if packed:
+        m["cu"] = torch.tensor([sum(lens[:i]) for i in range(n + 1)], dtype=torch.int32, device=device)
+    return m
+
+
+def kwargs(m):
+    return dict(heads=m["H"], head_dim=m["P"], groups=m["G"], d_state=m["N"], D=m["D"], dt_bias=m["dt_bias"], z=m["z"],
+                conv_weight=m["w"], conv_bias=m["b"])
+
+
+def prefill(m, **kw):
+    out = lib.gdn_ssm_prefill(m["xbc"], m["dt"], m["A_log"], state_in=m["state"], conv_state_in=m["conv"], cu_seqlens=m["cu"],
+                              **kwargs(m), **kw)
+    torch.cuda.synchronize()
+    assert lib.gdn_last_device_status() == 0
+    return out
+
+
+def define(m, dt_min=0.0, dt_max=math.inf, silu=True):
+    """(y, state, conv state) token by token in 64 bits."""
+    H, P, G, N, K, io = (m[k] for k in ("H", "P", "G", "N", "K", "io"))
+    C = H * P + 2 * G * N
+    x = m["xbc"].reshape(-1, C).double().cpu()
+    dt = m["dt"].reshape(-1, H).double().cpu()
+    z = m["z"].reshape(-1, H, P).double().cpu() if m["z"] is not None else None
+    A, bias, D = (m[k].double().cpu() for k in ("A_log", "dt_bias", "D"))
+    y, states, convs, r = torch.zeros(x.shape[0], H, P, dtype=torch.float64), [], [], 0
+    for i, L in enumerate(m["lens"]):
+        S = m["state"][i].double().cpu().clone() if m["state"] is not None else torch.zeros(H, N, P, dtype=torch.float64)
+        past = m["conv"][i].double().cpu() if m["conv"] is not None else torch.zeros(max(K - 1, 0), C, dtype=torch.float64)
+        pad = torch.cat([past, x[r:r + L]])
+        u = x[r:r + L]
+        if K and L:
+            w = m["w"].double().cpu()[:, 0]
+            u = m["b"].double().cpu() + sum(w[:, j] * pad[j:j + L] for j in range(K))
+            u = (u * torch.sigmoid(u) if silu else u).to(io).double()
+        for t in range(L):
+            d = torch.nn.functional.softplus(dt[r + t] + bias, threshold=100).clamp(dt_min, dt_max)
+            xt = u[t, :H * P].view(H, P)
+            b, c = (u[t, H * P + k * G * N:H * P + (k + 1) * G * N].view(G, N).repeat_interleave(H // G, 0) for k in (0, 1))
+            S = S * torch.exp(-torch.exp(A) * d)[:, None, None] + (d[:, None] * b)[..., None] * xt[:, None]
+            out = (c[..., None] * S).sum(1) + D[:, None] * xt
+            y[r + t] = out * z[r + t] * torch.sigmoid(z[r + t]) if z is not None else out
+        states.append(S)
+        convs.append(pad[L:])
+        r += L
+    empty = torch.zeros(0, max(K - 1, 0), C, dtype=torch.float64)
+    return (y.view(m["xbc"].shape[0], -1, H, P) if y.numel() else y, torch.stack(states) if states else torch.zeros(0, H, N, P),
+            (torch.stack(convs) if convs else empty) if K else None)
+
+
+def check(m, got, want):
+    y, state, conv = got
+    if y.numel():
+        assert rel(y, want[0]) <= y_tol(m["io"]), ("y", rel(y, want[0]))
+    if not want[1].numel():
+        assert state.shape == want[1].shape
+    elif want[1].abs().max() > 0:
+        assert rel(state, want[1]) <= state_tol(m), ("state", rel(state, want[1]))
+    else:
+        assert torch.count_nonzero(state) == 0
+    if m["K"]:
+        assert torch.equal(conv.double().cpu(), want[2])
+
+
+# ------------------------------------------------------------------ prompts
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("H,P,G,N,K", [(4, 64, 1, 128, 4), (4, 64, 2, 64, 4), (6, 32, 3, 16, 2), (2, 48, 2, 100, 3),
+                                       (2, 128, 1, 128, 0), (3, 4, 1, 1, 1), (2, 52, 1, 90, 4), (1, 256, 1, 256, 0),
+                                       (2, 80, 2, 33, 4)])
+def test_prompts_match_the_definition(io, H, P, G, N, K):
+    m = draw(io, [63, 1, 0, 200, 64, 2, 129], H, P, G, N, K, seed=H * P + N)
+    check(m, prefill(m), define(m))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,packed", [([1], False), ([3, 3], False), ([65, 65, 65], False), ([700], True), ([0, 0, 5], True),
+                                         ([0], True), ([], True)])
+@pytest.mark.parametrize("initial,z", [(False, False), (True, True)])
+def test_prompt_lengths(io, lens, packed, initial, z):
+    m = draw(io, lens, 4, 64, 2, 128, 4, packed=packed, initial=initial, z=z, seed=len(lens), gap=8)
+    check(m, prefill(m), define(m))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gap", [0, 1, 8])
+def test_rows_may_be_slices_at_any_stride(gap):
+    m = draw("bf16", [150, 20], 4, 64, 1, 128, 0, gap=gap, seed=3)
+    want = define(m)
+    check(m, prefill(m), want)
+    for name in ("xbc", "dt", "z"):
+        m[name] = m[name].contiguous()
+    check(m, prefill(m), want)
+
+
+@pytest.mark.gpu
+def test_optional_operands_and_bounds_on_the_step():
+    m = draw("f32", [40, 3], 4, 32, 2, 16, 3, seed=4)
+    args = dict(kwargs(m), D=None, dt_bias=None, conv_bias=None)
+    got = lib.gdn_ssm_prefill(m["xbc"], m["dt"], m["A_log"], state_in=m["state"], conv_state_in=m["conv"], cu_seqlens=m["cu"],
+                              dt_min=0.3, dt_max=0.8, conv_activation="none", **args)
+    m["D"], m["dt_bias"], m["b"] = torch.zeros_like(m["D"]), torch.zeros_like(m["D"]), torch.zeros_like(m["b"])
+    check(m, got, define(m, 0.3, 0.8, silu=False))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_extreme_steps(io):
+    """Steps of zero (dt = -inf) leave the state alone; huge decays clear it without NaN."""
+    m = draw(io, [150], 2, 64, 1, 128, 0, z=False, seed=5)
+    dt = m["dt"].clone()
+    dt[:, 10:30] = -math.inf
+    dt[:, 70] = 3e4
+    dt[:, 100:140:7] = 60.0
+    m["dt"] = dt
+    m["A_log"] = torch.tensor([2.5, 0.0], device="cuda")
+    check(m, prefill(m), define(m))
+    m["lens"], m["xbc"], m["dt"], m["cu"] = [20], m["xbc"][:, 10:30], dt[:, 10:30], torch.tensor([0, 20], dtype=torch.int32, device="cuda")
+    _, state, _ = prefill(m)
+    assert torch.equal(state, m["state"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_a_sequence_does_not_see_its_neighbours(io):
+    """Rows of another sequence, infinities and NaN among them, leave a packed sequence's results bit for bit."""
+    m = draw(io, [70, 33, 90], 4, 64, 2, 128, 4, seed=6)
+    y, state, conv = prefill(m)
+    m["xbc"] = m["xbc"].clone()
+    m["xbc"][:, :70] = math.nan
+    m["xbc"][:, 103:] = math.inf
+    y2, state2, conv2 = prefill(m)
+    assert torch.equal(y[:, 70:103], y2[:, 70:103]) and torch.equal(state[1], state2[1]) and torch.equal(conv[1], conv2[1])
+
+
+@pytest.mark.gpu
+def test_chained_calls_and_states_in_place():
+    m = draw("bf16", [300], 4, 64, 1, 128, 4, packed=False, seed=7)
+    y, state, conv = prefill(m)
+    parts = []
+    for a, b in ((0, 101), (101, 165), (165, 300)):
+        p = dict(m, lens=[b - a], **{k: m[k][:, a:b] for k in ("xbc", "dt", "z")})
+        yp, p["state"], p["conv"] = prefill(p, state_out=None if a == 0 else p["state"])
+        m["state"], m["conv"] = p["state"], p["conv"]
+        parts.append(yp)
+    assert rel(torch.cat(parts, 1), y) <= 2 * y_tol(torch.bfloat16)
+    assert rel(m["state"], state) <= 2 * STATE_TOL and torch.equal(m["conv"], conv)
+
+
+@pytest.mark.gpu
+def test_bad_offsets_are_reported_and_skipped():
+    m = draw("bf16", [100, 60, 40], 2, 64, 1, 128, 4, seed=8)
+    good = prefill(m)
+    m["cu"] = torch.tensor([0, 100, 90, 200], dtype=torch.int32, device="cuda")
+    y, state, conv = (torch.full_like(t, 7.0) for t in good)
+    lib.gdn_ssm_prefill(m["xbc"], m["dt"], m["A_log"], state_in=m["state"], conv_state_in=m["conv"], cu_seqlens=m["cu"],
+                        y=y, state_out=state, conv_state_out=conv, **kwargs(m))
+    assert lib.gdn_last_device_status() == gdn.GDN_ERR_DEVICE_CHECK
+    assert torch.equal(state[0], good[1][0]) and (state[1] == 7).all() and (conv[1] == 7).all()
+    assert torch.equal(y[:, :90], good[0][:, :90])
+
+
+# ------------------------------------------------------------------ single tokens
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("B,H,P,G,N,K", [(1, 4, 64, 1, 128, 4), (9, 6, 48, 3, 100, 4), (5, 2, 256, 1, 256, 2), (3, 2, 4, 1, 1, 1),
+                                         (4, 4, 52, 2, 33, 0), (2, 3, 80, 1, 16, 3)])
+@pytest.mark.parametrize("slots", [False, True])
+def test_tokens_match_the_definition(io, B, H, P, G, N, K, slots):
+    m = draw(io, [1] * B, H, P, G, N, K, packed=False, seed=B)
+    want = define(m)
+    E = B + 3 if slots else B
+    at = torch.randperm(E, generator=torch.Generator().manual_seed(B))[:B].cuda() if slots else torch.arange(B, device="cuda")
+    state = torch.full((E, H, N, P), 9.0, device="cuda")
+    state[at] = m["state"]
+    conv = None
+    if K:
+        conv = torch.full((E, K - 1, H * P + 2 * G * N), 9.0, device="cuda", dtype=DT[io])
+        conv[at] = m["conv"]
+    y = lib.gdn_ssm_decode(m["xbc"], m["dt"], m["A_log"], state, conv_state=conv, slots=at.int() if slots else None, **kwargs(m))
+    assert lib.gdn_last_device_status() == 0
+    check(m, (y, state[at], conv[at] if K else None), want)
+    rest = [e for e in range(E) if e not in at.tolist()]
+    assert (state[rest] == 9).all() and (conv is None or (conv[rest] == 9).all())
+
+
+@pytest.mark.gpu
+def test_tokens_continue_a_prompt():
+    m = draw("bf16", [90, 90], 4, 64, 2, 128, 4, packed=False, seed=9)
+    want = define(m)
+    head = dict(m, lens=[84, 84], **{k: m[k][:, :84].contiguous() for k in ("xbc", "dt", "z")})
+    _, state, conv = prefill(head)
+    ys = []
+    for t in range(84, 90):
+        step = dict(m, **{k: m[k][:, t:t + 1] for k in ("xbc", "dt", "z")})
+        ys.append(lib.gdn_ssm_decode(step["xbc"], step["dt"], step["A_log"], state, conv_state=conv, **kwargs(step)))
+    assert rel(torch.cat(ys, 1), want[0][:, 84:]) <= y_tol(torch.bfloat16)
+    assert rel(state, want[1]) <= state_tol(m) and torch.equal(conv.double().cpu(), want[2])
+
+
+@pytest.mark.gpu
+def test_a_slot_outside_the_pool_skips_its_row():
+    m = draw("bf16", [1, 1, 1], 2, 64, 1, 128, 4, packed=False, seed=10)
+    state, conv = m["state"].clone(), m["conv"].clone()
+    y = torch.full((3, 1, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    slots = torch.tensor([2, 3, -1], dtype=torch.int32, device="cuda")
+    lib.gdn_ssm_decode(m["xbc"], m["dt"], m["A_log"], state, conv_state=conv, slots=slots, y=y, **kwargs(m))
+    assert lib.gdn_last_device_status() == gdn.GDN_ERR_DEVICE_CHECK
+    assert (y[1:] == 5).all() and torch.equal(state[:2], m["state"][:2]) and torch.equal(conv[:2], m["conv"][:2])
+    assert not torch.equal(state[2], m["state"][2])
+
+
+# ------------------------------------------------------------------ streams, graphs
+@pytest.mark.gpu
+def test_another_stream_and_a_captured_graph():
+    m = draw("bf16", [200, 50], 4, 64, 1, 128, 4, seed=11)
+    want = prefill(m)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = prefill(m, stream=side)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = lib.gdn_ssm_prefill(m["xbc"], m["dt"], m["A_log"], state_in=m["state"], conv_state_in=m["conv"],
+                                  cu_seqlens=m["cu"], **kwargs(m))
+    for t in out:
+        t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+# ------------------------------------------------------------------ the operators together
+@pytest.mark.gpu
+def test_convolution_turn_scan_norm():
+    """A layer whose B and C turn with the position: conv, rotary in place on the mixed row, scan, gated norm."""
+    H, P, G, N, K, lens = 4, 64, 2, 128, 4, [90, 37]
+    m = draw("bf16", lens, H, P, G, N, 0, z=False, initial=False, seed=12)
+    C = H * P + 2 * G * N
+    w = (torch.randn(C, 1, K, generator=torch.Generator().manual_seed(1)) * 0.5).bfloat16().cuda()
+    u = torch.cat([lib.gdn_causal_conv(part.contiguous(), w, activation="silu")[0] for part in m["xbc"].split(lens, 1)], 1)
+    inv_freq, _ = lib.gdn_rotary_frequencies(64, device="cuda")
+    c, b = (u[..., H * P + i * G * N:H * P + (i + 1) * G * N].unflatten(2, (G, N)) for i in (1, 0))
+    pos = torch.cat([torch.arange(n) for n in lens])[None].int().cuda()
+    want_c, want_b = (turn(t, pos, inv_freq, 64, True, False, 1.0).bfloat16() for t in (c, b))
+    lib.gdn_rotary(c, b, inv_freq, cu_seqlens=m["cu"], rot_offset=64, interleaved=True, q_out=c, k_out=b)
+    assert rel(c, want_c) <= 2 ** -8 and rel(b, want_b) <= 2 ** -8
+    m["xbc"] = u
+    got = prefill(m)
+    check(m, got, define(m))
+    gate = torch.randn(got[0].shape, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    y = lib.gdn_gated_rmsnorm(got[0], torch.ones(P, dtype=torch.bfloat16, device="cuda"), gate)
+    o, gt = got[0].double(), gate.double()
+    assert rel(y, o * (o.square().mean(-1, keepdim=True) + 1e-5).rsqrt() * gt * torch.sigmoid(gt)) <= 2 ** -8
+
+
+# ------------------------------------------------------------------ refusals (no GPU)
+def _ssm(**kw):
+    d = dict(io_dtype=1, batch=1, seqlen=4, num_seqs=1, heads=4, head_dim=64, groups=2, d_state=16, xbc_stride=0, dt_stride=0,
+             z_stride=0)
+    return gdn.GdnSsmShape(**dict(d, **kw))
+
+
+def _params(**kw):
+    return gdn.GdnSsmParams(**dict(dict(conv_kernel=4, conv_activation=1, dt_min=0.0, dt_max=1.0), **kw))
+
+
+BAD_SHAPES = [dict(io_dtype=5), dict(batch=-1, num_seqs=-1), dict(seqlen=-1), dict(num_seqs=2), dict(heads=0), dict(groups=3),
+              dict(groups=0), dict(head_dim=0), dict(head_dim=6), dict(head_dim=260), dict(d_state=0), dict(d_state=257),
+              dict(xbc_stride=5), dict(dt_stride=3), dict(z_stride=1), dict(heads=65536, groups=1), dict(seqlen=2 ** 31)]
+BAD_PARAMS = [dict(conv_kernel=5), dict(conv_kernel=-1), dict(conv_activation=2), dict(dt_min=-1.0), dict(dt_min=math.nan),
+              dict(dt_max=math.nan), dict(dt_min=2.0), dict(dt_min=math.inf, dt_max=math.inf)]
+P64 = [ctypes.c_void_p(1 << 40 | i << 32) for i in range(16)]     # addresses that are never read: every call is refused
+off = lambda i, d: ctypes.c_void_p(P64[i].value + d)  # noqa: E731
+
+
+def call_prefill(shape, params, **over):
+    names = ["xbc", "dt", "z", "w", "b", "conv_in", "conv_out", "A_log", "dt_bias", "D", "state_in", "cu", "y", "state_out", "ws"]
+    a = dict(zip(names, P64), cu=None)
+    a.update(over)
+    return lib.load().gdn_ssm_prefill(ctypes.byref(shape) if shape else None, ctypes.byref(params) if params else None,
+                                      *[a[n] for n in names], a.get("ws_bytes", 1 << 30), None)
+
+
+def call_decode(shape, params, **over):
+    names = ["xbc", "dt", "z", "w", "b", "conv", "A_log", "dt_bias", "D", "state"]
+    a = dict(zip(names, P64), pool=4, slots=None, y=P64[12])
+    a.update(over)
+    return lib.load().gdn_ssm_decode(ctypes.byref(shape) if shape else None, ctypes.byref(params) if params else None,
+                                     *[a[n] for n in names], a["pool"], a["slots"], a["y"], None)
+
+
+@pytest.mark.parametrize("shape,params", [(s, {}) for s in BAD_SHAPES] + [({}, p) for p in BAD_PARAMS])
+def test_bad_geometry_is_refused(shape, params):
+    for call, t in ((call_prefill, 4), (call_decode, 1)):
+        s = _ssm(**dict(dict(seqlen=t), **shape))
+        assert call(s, _params(**params)) in (gdn.GDN_ERR_INVALID_ARG, gdn.GDN_ERR_UNSUPPORTED)
+    if "num_seqs" not in shape or "batch" in shape:      # (batch 1 and two sequences: packed, to the query)
+        assert lib.load().gdn_ssm_prefill_workspace_bytes(ctypes.byref(_ssm(**shape)), ctypes.byref(_params(**params))) == 0
+
+
+@pytest.mark.parametrize("over", [dict(xbc=None), dict(dt=None), dict(w=None), dict(A_log=None), dict(y=None), dict(state_out=None),
+                                  dict(conv_out=None), dict(ws=None), dict(ws_bytes=100), dict(ws=off(14, 8)), dict(xbc=off(0, 1)),
+                                  dict(A_log=off(7, 2)), dict(state_in=off(10, 4)), dict(state_out=off(13, 8)),
+                                  dict(y=P64[0]), dict(y=P64[2]), dict(conv_out=P64[5]), dict(state_out=off(10, 16))])
+def test_bad_prefill_pointers_are_refused(over):
+    assert call_prefill(_ssm(), _params(), **over) == gdn.GDN_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [dict(xbc=None), dict(dt=None), dict(w=None), dict(A_log=None), dict(y=None), dict(state=None),
+                                  dict(conv=None), dict(state=off(9, 4)), dict(slots=P64[14], pool=0), dict(slots=off(14, 2)),
+                                  dict(y=P64[0]), dict(z=off(2, 1))])
+def test_bad_decode_pointers_are_refused(over):
+    assert call_decode(_ssm(seqlen=1), _params(), **over) == gdn.GDN_ERR_INVALID_ARG
+    assert call_decode(_ssm(seqlen=2), _params()) == gdn.GDN_ERR_INVALID_ARG
+    assert call_prefill(None, _params()) == call_prefill(_ssm(), None) == gdn.GDN_ERR_INVALID_ARG
+
+
+def test_nothing_to_do_is_no_error():
+    assert call_prefill(_ssm(batch=0, num_seqs=0), _params()) == gdn.GDN_OK
+    assert call_decode(_ssm(batch=0, num_seqs=0, seqlen=1), _params()) == gdn.GDN_OK
+
+
+def test_binding_refuses_cpu_tensors():
+    m = draw("f32", [4], 2, 32, 1, 16, 2, device="cpu")
+    for call in (lambda: lib.gdn_ssm_prefill(m["xbc"], m["dt"], m["A_log"], state_in=m["state"], conv_state_in=m["conv"], **kwargs(m)),
+                 lambda: lib.gdn_ssm_decode(m["xbc"][:, :1], m["dt"][:, :1], m["A_log"], m["state"], conv_state=m["conv"],
+                                            **dict(kwargs(m), z=None))):
+        with pytest.raises(lib.GdnError):
+            call()
