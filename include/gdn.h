@@ -530,11 +530,20 @@ typedef struct gdn_ssm_params {
  *   y            [rows, heads, head_dim], contiguous; must not overlap xbc or z.
  *   workspace    gdn_ssm_prefill_workspace_bytes(shape, params) bytes, 16-byte aligned; its
  *                contents need no initialisation and are not preserved.
- * Inputs are finite, but dt may be -infinity: with dt_min 0 such a token's step is 0, and it
- * leaves the state as it was.  Errors are found before anything is launched, but for malformed
- * cu_seqlens (gdn_last_device_status), whose sequences are skipped.
+ * Inputs are finite (an infinity or NaN can reach the whole chunk of 64 tokens that holds it,
+ * and what follows in its sequence, but no other sequence), but dt may be -infinity: with
+ * dt_min 0 such a token's step is 0, and it leaves the state as it was.  Errors are found before
+ * anything is launched, but for malformed cu_seqlens (gdn_last_device_status), whose sequences
+ * are skipped.
  */
 size_t gdn_ssm_prefill_workspace_bytes(const gdn_ssm_shape *shape, const gdn_ssm_params *params);
+
+/*
+ * gdn_ssm_prefill_plan -- gdn_prefill_plan for gdn_ssm_prefill: *path 1 = token-sequential on
+ * the FP32 cores, 2 = chunked on the tensor cores (bf16, head_dim a multiple of 8, d_state up
+ * to 128, xbc and y 16-byte aligned), 3 = that in time segments.  Launches nothing.
+ */
+gdn_status gdn_ssm_prefill_plan(const gdn_ssm_shape *shape, const gdn_ssm_params *params, int32_t *path, int32_t *launches);
 
 gdn_status gdn_ssm_prefill(const gdn_ssm_shape *shape, const gdn_ssm_params *params, const void *xbc, const void *dt,
                            const void *z, const void *conv_weight, const void *conv_bias, const void *conv_state_in,

@@ -11,4 +11,4 @@ from .gdn import (GdnError, GdnShape, gdn_causal_conv, gdn_causal_conv_slots,  #
                   gdn_prefill_workspace_bytes,
                   gdn_rotary, gdn_rotary_frequencies,
                   gdn_scan_variant, gdn_scan_window, gdn_ssm_decode, gdn_ssm_prefill,
-                  gdn_ssm_prefill_workspace_bytes, gdn_status_string, load)
+                  gdn_ssm_prefill_plan, gdn_ssm_prefill_workspace_bytes, gdn_status_string, load)

@@ -188,10 +188,11 @@ cudaError_t launch_prefill_tc(const ScanParams &p, gdn_dtype io, int64_t total_t
 extern long long g_wait_budget;
 
 // A TMA tensor map over a 3-D tensor of 16-bit values (dims innermost first, the two outer
-// strides in bytes, multiples of 16), no swizzle, out-of-range elements read as zero.
+// strides in bytes, multiples of 16), no swizzle or the 128-byte one, out-of-range elements
+// read as zero.
 // False when the driver's encoder is missing or rejects the arguments.
 bool encode_map_3d(CUtensorMap *m, const void *base, gdn_dtype io, const uint64_t dims[3],
-                   const uint64_t strides[2], const uint32_t box[3]);
+                   const uint64_t strides[2], const uint32_t box[3], bool swizzle128 = false);
 
 // The gated RMS norm applied to o after the scan (gdn_prefill_norm).
 // The causal convolution before the prefill (gdn_prefill_layer): x [tokens][C], C =

@@ -3181,7 +3181,7 @@ cudaError_t launch_tp(TcParams tp, int64_t n_slots, int nseg, uint8_t *extra, cu
 long long g_wait_budget = 0;   // 0: the kernels' default budget
 
 bool encode_map_3d(CUtensorMap *m, const void *base, gdn_dtype io, const uint64_t dims[3],
-                   const uint64_t strides[2], const uint32_t box[3]) {
+                   const uint64_t strides[2], const uint32_t box[3], bool swizzle128) {
     auto fn = encode_fn();
     if (fn == nullptr || io == GDN_F32) return false;
     const cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
@@ -3190,7 +3190,7 @@ bool encode_map_3d(CUtensorMap *m, const void *base, gdn_dtype io, const uint64_
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = fn(m, io == GDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                           3, const_cast<void *>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                          swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }

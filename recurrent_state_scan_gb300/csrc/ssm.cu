@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(const SsmParams 
 #pragma unroll
                 for (int i = 0; i < NS; i += V) {
                     const int at = (i / V) * (8 * V) + slice * V;
-                    float b[V], c[V];
+                    alignas(16) float b[V], c[V];
                     if constexpr (V == 4) {
                         *reinterpret_cast<float4 *>(b) = *reinterpret_cast<const float4 *>(&sb[buf][k][0][at]);
                         *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(&sb[buf][k][1][at]);

@@ -86,8 +86,27 @@ gdn_status check_rows(const gdn_ssm_params *q, const Geometry &g, const void *xb
 
 int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
 
-// The convolved rows in the workspace: heads and groups on 8-element boundaries.
+// The convolved (or re-laid) rows in the workspace: heads and groups on 8-element boundaries.
 int64_t u_stride(const gdn_ssm_shape *s) { return s->heads * round8(s->head_dim) + 2 * s->groups * round8(s->d_state); }
+
+bool tc_shape(const gdn_ssm_shape *s, const Geometry &g) {
+    return g.rows > 0 && s->num_seqs > 0 && ssm_tc_shape_ok((gdn_dtype)s->io_dtype, s->head_dim, s->d_state);
+}
+
+// Workspace bytes: first the rows the scan reads, where it cannot read xbc itself (behind the
+// convolution; on the tensor cores also where TMA cannot take xbc's strides, whose rows are then
+// copied), then the tensor-core scan's segments.
+struct Layout {
+    size_t u, total;
+};
+Layout layout(const gdn_ssm_shape *s, const gdn_ssm_params *q, const Geometry &g, bool varlen) {
+    const bool tc = tc_shape(s, g);
+    const bool relay = tc && (g.ld_x % 8 != 0 || s->d_state % 8 != 0);
+    Layout l{};
+    if (q->conv_kernel || relay) l.u = ((size_t)g.rows * u_stride(s) * g.es + 255) / 256 * 256;
+    l.total = l.u + (tc ? ssm_tc_workspace(varlen, s->seqlen, g.rows, s->num_seqs, s->heads, s->groups, s->head_dim, s->d_state) : 0);
+    return l;
+}
 
 }  // namespace
 }  // namespace gdn
@@ -99,7 +118,19 @@ extern "C" {
 size_t gdn_ssm_prefill_workspace_bytes(const gdn_ssm_shape *shape, const gdn_ssm_params *params) {
     Geometry g;
     if (shape == nullptr || params == nullptr || check(shape, params, shape->batch == 1, g) != GDN_OK) return 0;
-    return params->conv_kernel ? ((size_t)g.rows * u_stride(shape) * g.es + 255) / 256 * 256 : 0;
+    return layout(shape, params, g, shape->batch == 1).total;
+}
+
+gdn_status gdn_ssm_prefill_plan(const gdn_ssm_shape *shape, const gdn_ssm_params *params, int32_t *path, int32_t *launches) {
+    Geometry g;
+    const bool varlen = shape != nullptr && shape->batch == 1 && shape->num_seqs != 1;
+    const gdn_status st = check(shape, params, varlen, g);
+    if (st != GDN_OK) return st;
+    const bool tc = tc_shape(shape, g);
+    const bool seg = tc && ssm_tc_segments(varlen, shape->seqlen, g.rows, shape->num_seqs, shape->heads, shape->groups, shape->head_dim);
+    if (path) *path = tc ? (seg ? 3 : 2) : 1;
+    if (launches) *launches = shape->num_seqs > 0 ? (layout(shape, params, g, varlen).u > 0 ? 1 : 0) + (seg ? 3 : 1) : 0;
+    return GDN_OK;
 }
 
 gdn_status gdn_ssm_prefill(const gdn_ssm_shape *shape, const gdn_ssm_params *params, const void *xbc, const void *dt,
@@ -127,11 +158,11 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_shape *shape, const gdn_ssm_params *par
         if (overlaps(conv_state_in, cb, conv_state_out, cb))
             return fail(GDN_ERR_INVALID_ARG, "conv_state_out overlaps conv_state_in (the update cannot be in place)");
     }
-    const size_t need = params->conv_kernel ? (size_t)g.rows * u_stride(shape) * g.es : 0;
-    if (need > 0) {
-        if (workspace == nullptr || workspace_bytes < need)
+    const Layout ws = layout(shape, params, g, cu_seqlens != nullptr);
+    if (ws.total > 0) {
+        if (workspace == nullptr || workspace_bytes < ws.total)
             return fail(GDN_ERR_INVALID_ARG, "workspace of %zu bytes is below the %zu this call needs",
-                        workspace == nullptr ? (size_t)0 : workspace_bytes, need);
+                        workspace == nullptr ? (size_t)0 : workspace_bytes, ws.total);
         if (!aligned(workspace, 16)) return fail(GDN_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
     }
     int *word = nullptr;
@@ -148,21 +179,24 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_shape *shape, const gdn_ssm_params *par
     p.state_in = state_in; p.state_out = state_out; p.y = y; p.cu_seqlens = cu_seqlens;
     p.seqlen = shape->seqlen; p.rows = g.rows; p.num_seqs = shape->num_seqs; p.heads = shape->heads;
     p.groups = shape->groups; p.head_dim = shape->head_dim; p.d_state = shape->d_state; p.status = word;
-    if (params->conv_kernel) {
+    if (params->conv_kernel || ws.u > 0) {
         SsmConvParams c{};
-        c.x = xbc; c.ld_x = g.ld_x; c.w = conv_weight; c.bias = conv_bias;
+        c.x = xbc; c.ld_x = g.ld_x; c.w = params->conv_kernel ? conv_weight : nullptr; c.bias = conv_bias;
         c.conv_in = params->conv_kernel > 1 ? conv_state_in : nullptr; c.conv_out = conv_state_out;
         c.u = workspace; c.ld_u = u_stride(shape); c.x_head = (int32_t)round8(shape->head_dim);
         c.bc_group = (int32_t)round8(shape->d_state);
         c.off_b = shape->heads * c.x_head; c.off_c = c.off_b + shape->groups * c.bc_group;
         c.cu_seqlens = cu_seqlens; c.seqlen = p.seqlen; c.rows = p.rows; c.num_seqs = p.num_seqs; c.heads = p.heads;
-        c.groups = p.groups; c.head_dim = p.head_dim; c.d_state = p.d_state; c.C = (int32_t)g.C; c.K = params->conv_kernel;
+        c.groups = p.groups; c.head_dim = p.head_dim; c.d_state = p.d_state; c.C = (int32_t)g.C;
+        c.K = params->conv_kernel ? params->conv_kernel : 1;
         c.silu = params->conv_activation == GDN_ACT_SILU; c.status = word;
         const cudaError_t e = launch_ssm_conv(c, io, cs);
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "state-space convolution launch: %s", cudaGetErrorString(e));
         p.xs = c.u; p.ldx = c.ld_u; p.x_head = c.x_head; p.off_b = c.off_b; p.off_c = c.off_c; p.bc_group = c.bc_group;
     }
-    const cudaError_t e = launch_ssm_scan_simt(p, io, cs);
+    // An xbc or y off 16 bytes (which no shape tells) leaves the tensor cores.
+    const bool tc = tc_shape(shape, g) && ssm_tc_rows_ok(p);
+    const cudaError_t e = tc ? launch_ssm_tc(p, static_cast<uint8_t *>(workspace) + ws.u, cs) : launch_ssm_scan_simt(p, io, cs);
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "state-space scan launch: %s", cudaGetErrorString(e));
     return GDN_OK;
 }

@@ -1,0 +1,672 @@
+// ssm_tc.cu -- the selective state-space scan of prompts on the tcgen05 tensor cores (bf16
+// I/O, head_dim a multiple of 8, d_state up to 128).
+//
+// The recurrence S = a_t S + d_t B_t (x) x_t, y_t = S^T C_t over chunks of L = 64 tokens, with
+// g_t = ln a_t, G_i = g_1 + .. + g_i and S0 the state entering the chunk, is
+//   y_i = e^{G_i} C_i S0 + sum_{j <= i} M_ij x_j,   M_ij = (C_i . B_j) e^{G_i - G_j} d_j
+//   S   = e^{G_L} S0 + sum_j B_j (x) w_j x_j,       w_j = d_j e^{G_L - G_j}
+// Every exponent is a difference that is never positive, so nothing overflows.
+//
+// A CTA takes two units -- a unit is 64 columns of one head's state -- of one B / C group and
+// walks the chunks of a sequence (or of one time segment of it).  Two, because the group's
+// scores C B^T then serve both and every MMA is 128 x 128 but the scores' 128 x 64: C stands
+// twice in shared memory, so that accumulator rows 0-63 are unit 0's tokens and rows 64-127
+// unit 1's, and all 16 warps (and all four lane quarters of tensor memory) share the work.
+// Per chunk, the MMA group on the left runs under the thread work on the right:
+//   scores C B^T, readout C [S0 | S1]    y of the chunk before; w x split into bf16 hi + lo
+//   B^T [w x hi] + B^T [w x lo]          M from the scores (fp32), rounded to bf16
+//   [M0; M1] [x0 | x1]                   S = e^{G_L} S + .. in fp32 registers; bf16(S) for the next C S
+// Precision: the state is fp32 and its update's operands are exact (B) or a two-term bf16 split
+// (w x: 2^-17 of each product), because the state is returned in fp32 and carried on; M and
+// the S that C reads are rounded once to bf16, half a step (2^-9 of each term's size at random
+// signs), under the one rounding that y meets itself.  f16 stays on the FP32 cores: w x and M
+// leave its range.
+//
+// Where sequences x units leave most SMs idle, each sequence is cut along time: a state-only
+// pass of every segment but the last from zero, a short pass that turns the segments' ends into
+// the states entering them, and then all segments at once.
+#include <cudaTypedefs.h>
+#include <stddef.h>
+#include <string.h>
+
+#include "ssm_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace tc;
+
+constexpr int kL = 64;                       // tokens per chunk
+constexpr int kThreads = 512;
+constexpr long long kBudget = 4000000000LL;  // cycles (~2 s) before a wait gives up
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Shared memory (1024-byte aligned): two stages of what TMA brings, then the operands the
+// threads make.  All tiles are stacks of 128-byte-swizzled rows of 64 bf16.
+constexpr int ST_C = 0;                      // 2 regions of 64 state columns x 128 rows: C twice
+constexpr int ST_B = 32768;                  // 2 regions x 64 rows
+constexpr int ST_X = 49152;                  // 2 units x 64 rows
+constexpr int kStage = 65536;
+constexpr int O_M = 2 * kStage;              // 128 rows: unit 0's M, unit 1's
+constexpr int O_XH = O_M + 16384;            // w x, high part: 2 units x 64 rows
+constexpr int O_XL = O_XH + 16384;           // low part
+constexpr int O_S = O_XL + 16384;            // bf16(S): 2 units x 128 state rows
+constexpr int kSmem = O_S + 32768 + 1024;
+
+// Tensor memory columns.
+constexpr uint32_t T_CB = 0, T_CS = 64, T_DS = 192, T_MX = 320, kCols = 512;
+
+struct TcParams {
+    CUtensorMap tm_x, tm_b, tm_c;
+    const __nv_bfloat16 *dt, *z;
+    __nv_bfloat16 *y;
+    int64_t ld_dt, ld_z;
+    const float *A_log, *dt_bias, *D;
+    float dt_min, dt_max;
+    const float *state_in;
+    float *state_out;
+    const int32_t *cu_seqlens;
+    int64_t seqlen, rows;
+    int32_t num_seqs, heads, groups, P, N;
+    int32_t ptiles, units, pairs_per_group;      // units of one group
+    int32_t z_wide;                              // z rows on 16-byte boundaries
+    int32_t seg_chunks;                          // chunks per time segment (0: no segments)
+    float *seg_state, *seg_decay;                // [slot][unit][N][64], [slot][unit]
+    int *status;
+    long long budget;
+};
+
+struct alignas(16) Gates {       // read in float2 and float4
+    float ci[kL];    // log2 e^{G_i}
+    float cj[kL];    // the same less log2 d_j
+    float ec[kL];    // e^{G_i}
+    float w[kL];     // d_j e^{G_L - G_j}
+    float decay;     // e^{G_L}
+    float total;     // its log2
+};
+
+struct Ctl {
+    uint64_t full[2], cb, cs, ds, mx, drain;
+    uint32_t tmem;
+    Gates g[2][2];   // [chunk parity][unit]
+};
+static_assert(sizeof(Gates) % 16 == 0 && offsetof(Ctl, g) % 16 == 0, "vector accesses of the gates");
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+__device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// mbar_wait, but under a short budget (gdn_set_wait_budget) a wait that took longer has run
+// out even where the one blocking try saw it end.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, long long budget) {
+    if (budget >= 100000) return mbar_wait(bar, parity, budget);
+    const long long t0 = clock64();
+    return mbar_wait(bar, parity, budget) && clock64() - t0 <= budget;
+}
+
+// One work item: the chunks [t0, t1) of segment k of sequence n.
+struct Item {
+    int64_t n, slot, t0, t1;
+    int k, nseg;
+    bool valid;
+};
+
+__device__ __forceinline__ int64_t slot_base(const TcParams &p, int64_t n, int64_t ls, int64_t per) {
+    return p.cu_seqlens ? p.cu_seqlens[n] / ls + n : n * per;
+}
+
+// Slot s of a call: without segments the sequence s.  With segments of ls tokens, batched
+// sequences take equal runs of slots, and packed ones start at floor(cu[n] / ls) + n, which
+// leaves room for each one's ceil(len / ls) segments.
+__device__ __forceinline__ Item item_of(const TcParams &p, int64_t s) {
+    Item it;
+    it.slot = s;
+    it.k = 0;
+    it.nseg = 1;
+    if (p.seg_chunks == 0) {
+        it.n = s;
+        it.valid = seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, s, it.t0, it.t1);
+        return it;
+    }
+    const int64_t ls = (int64_t)p.seg_chunks * kL, per = (p.seqlen + ls - 1) / ls;
+    int64_t lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) >> 1;
+        if (slot_base(p, mid, ls, per) <= s) lo = mid;
+        else hi = mid - 1;
+    }
+    it.n = lo;
+    int64_t t0, t1;
+    it.valid = seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, lo, t0, t1);
+    const int64_t k = s - slot_base(p, lo, ls, per), segs = (t1 - t0 + ls - 1) / ls;
+    it.nseg = segs > 1 ? (int)segs : 1;
+    it.valid = it.valid && k >= 0 && k < it.nseg;
+    it.k = (int)k;
+    it.t0 = t0 + k * ls;
+    it.t1 = it.t0 + ls < t1 ? it.t0 + ls : t1;
+    return it;
+}
+
+// kState: the state-only pass of a segment (no scores, no y).
+template <bool kState>
+__global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_constant__ TcParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    __shared__ Ctl ctl;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int pairs = p.groups * p.pairs_per_group;
+    const int pair = blockIdx.x % pairs;
+    const Item it = item_of(p, blockIdx.x / pairs);
+    // Each sequence's offsets are checked once, whether or not a slot leads to it.
+    if (!kState && p.seg_chunks != 0 && tid == 0 && (int64_t)blockIdx.x < p.num_seqs) {
+        int64_t a, b;
+        seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, blockIdx.x, a, b);
+    }
+    if (!it.valid || (kState && it.k + 1 >= it.nseg)) return;
+
+    // The two units.  An odd last unit is computed twice and stored once.
+    const int g = pair / p.pairs_per_group, u0 = 2 * (pair % p.pairs_per_group);
+    const int hpg = p.heads / p.groups;
+    const bool two = u0 + 1 < p.units;
+    auto unit_head = [&](int u) { return g * hpg + (u0 + (two ? u : 0)) / p.ptiles; };
+    auto unit_tile = [&](int u) { return (u0 + (two ? u : 0)) % p.ptiles; };
+
+    const long long budget = p.budget > 0 ? p.budget : kBudget;
+    if (warp == 0) {
+        tmem_alloc(&ctl.tmem, kCols);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        mbar_init(&ctl.full[0], 1);
+        mbar_init(&ctl.full[1], 1);
+        mbar_init(&ctl.cb, 1);
+        mbar_init(&ctl.cs, 1);
+        mbar_init(&ctl.ds, 1);
+        mbar_init(&ctl.mx, 1);
+        mbar_init(&ctl.drain, 1);
+        fence_mbar_init();
+    }
+
+    // This thread's part of S: state row n, 32 columns of unit su.
+    const int q = warp & 3, cg = warp >> 2;           // TMEM lane quarter, column group
+    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+    const int sn = 32 * q + lane, su = cg >> 1, sc = 32 * (cg & 1);
+    const int shead = unit_head(su), scol = unit_tile(su) * 64 + sc;
+    const int ucols = p.P - unit_tile(su) * 64;       // columns of this unit that exist
+    const int64_t nunits = (int64_t)p.groups * p.units;
+    const int64_t sunit = (int64_t)g * p.units + u0 + (two ? su : 0);
+    const size_t sglob = (((size_t)it.n * p.heads + shead) * p.N + sn) * p.P + scol;
+    const size_t sseg = ((size_t)it.slot * nunits + sunit) * p.N * 64 + (size_t)sn * 64 + sc;
+    alignas(16) float S[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) S[i] = 0.f;
+    if (!kState && sn < p.N) {
+        if (it.nseg > 1) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4 *>(S + i) = *reinterpret_cast<const float4 *>(p.seg_state + sseg + i);
+        } else if (p.state_in) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+                if (sc + i < ucols) *reinterpret_cast<float4 *>(S + i) = *reinterpret_cast<const float4 *>(p.state_in + sglob + i);
+        }
+    }
+    auto put_S = [&]() {     // bf16(S) as the next readout's operand
+        uint8_t *row = sm + O_S + su * 16384;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4 *>(row + sw128_offset(sn, (sc >> 3) + c)) =
+                make_uint4(pack2(S[8 * c], S[8 * c + 1]), pack2(S[8 * c + 2], S[8 * c + 3]), pack2(S[8 * c + 4], S[8 * c + 5]),
+                           pack2(S[8 * c + 6], S[8 * c + 7]));
+    };
+    if (!kState) put_S();
+
+    // This thread's part of M and y: token `ri` of unit ru, 16 columns.
+    const int row = 32 * q + lane, ru = q >> 1, ri = row & 63;
+    const int rhead = unit_head(ru), rtile = unit_tile(ru);
+    const int ycol = rtile * 64 + 16 * cg;            // first of its columns in the head
+    const bool ylive = (ru == 0 || two) && ycol < p.P;
+    const float Dh = p.D ? p.D[rhead] : 0.f;
+
+    const int nchunks = (int)((it.t1 - it.t0 + kL - 1) / kL);
+    const int regions = p.N > 64 ? 2 : 1, ksteps = (p.N + 15) / 16;
+    auto load = [&](int c) {          // chunk c into its stage (one thread)
+        uint8_t *st = sm + (c & 1) * kStage;
+        uint64_t *bar = &ctl.full[c & 1];
+        const int t = (int)(it.t0 + (int64_t)c * kL);
+        mbar_arrive_expect_tx(bar, 8192u * (regions * (kState ? 1 : 3) + 2));
+        for (int r = 0; r < regions; ++r) {
+            tma_load_3d(st + ST_B + r * 8192, &p.tm_b, 64 * r, g, t, bar);
+            if (!kState) {
+                tma_load_3d(st + ST_C + r * 16384, &p.tm_c, 64 * r, g, t, bar);
+                tma_load_3d(st + ST_C + r * 16384 + 8192, &p.tm_c, 64 * r, g, t, bar);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) tma_load_3d(st + ST_X + u * 8192, &p.tm_x, 64 * unit_tile(u), unit_head(u), t, bar);
+    };
+    // Gates of chunk c, by warp u for unit u: two tokens to a lane.  A decay of e^-111 is
+    // already nothing in fp32, so g is held above that: a reset then leaves the running sum
+    // small enough to keep the differences of the tokens behind it.
+    float dt0 = 0.f, dt1 = 0.f;
+    const int gw = warp & 1;
+    const float gA = -expf(p.A_log[unit_head(gw)]) * kLog2e, gbias = p.dt_bias ? p.dt_bias[unit_head(gw)] : 0.f;
+    auto load_dt = [&](int c) {
+        const int64_t t = it.t0 + (int64_t)c * kL + 2 * lane;
+        const __nv_bfloat16 *at = p.dt + t * p.ld_dt + unit_head(gw);
+        dt0 = t < it.t1 ? __bfloat162float(at[0]) : 0.f;
+        dt1 = t + 1 < it.t1 ? __bfloat162float(at[p.ld_dt]) : 0.f;
+    };
+    auto gates = [&](int c) {
+        const int64_t t = it.t0 + (int64_t)c * kL + 2 * lane;
+        const float d0 = t < it.t1 ? ssm_step(dt0, gbias, p.dt_min, p.dt_max) : 0.f;
+        const float d1 = t + 1 < it.t1 ? ssm_step(dt1, gbias, p.dt_min, p.dt_max) : 0.f;
+        float g0 = gA * d0, g1 = gA * d1;
+        g0 = g0 < -160.f ? -160.f : g0;
+        g1 = g1 < -160.f ? -160.f : g1;
+        float pre = g0 + g1, suf = pre;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float a = __shfl_up_sync(0xffffffffu, pre, o), b = __shfl_down_sync(0xffffffffu, suf, o);
+            if (lane >= o) pre += a;
+            if (lane + o < 32) suf += b;
+        }
+        float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
+        if (lane == 0) before = 0.f;
+        if (lane == 31) after = 0.f;
+        Gates &G = ctl.g[c & 1][gw];
+        const float c0 = before + g0, c1 = pre;
+        const float l0 = __log2f(d0), l1 = __log2f(d1);   // -inf where the step is zero: no weight
+        *reinterpret_cast<float2 *>(&G.ci[2 * lane]) = make_float2(c0, c1);
+        *reinterpret_cast<float2 *>(&G.cj[2 * lane]) = make_float2(c0 - l0, c1 - l1);
+        *reinterpret_cast<float2 *>(&G.ec[2 * lane]) = make_float2(ex2(c0), ex2(c1));
+        *reinterpret_cast<float2 *>(&G.w[2 * lane]) = make_float2(d0 * ex2(after + g1), d1 * ex2(after));
+        if (lane == 0) {
+            G.total = suf;
+            G.decay = ex2(suf);
+        }
+    };
+    if (nchunks > 0) {
+        if (warp < 2) {
+            load_dt(0);
+            gates(0);
+            if (nchunks > 1) load_dt(1);
+        }
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    const uint32_t base = smem_u32(sm);
+    constexpr uint32_t kIdCB = idesc_f16(true, 128, 64, false, false), kIdCS = idesc_f16(true, 128, 128, false, true),
+                       kIdDS = idesc_f16(true, 128, 128, true, true);
+
+    int loaded = 0;                   // chunks whose loads are issued (thread 0)
+    if (tid == 0 && nchunks > 0) {
+        load(0);
+        loaded = 1;
+    }
+    bool ok = true;
+    float seg_total = 0.f;
+    // y of the chunk before: what its accumulators held, and its z.
+    float acc[16], accs[16];
+    uint4 zr[2];
+    auto load_z = [&](int c) {
+        const int64_t t = it.t0 + (int64_t)c * kL + ri;
+        if (p.z == nullptr || !ylive || t >= it.t1) return;
+        const __nv_bfloat16 *src = p.z + t * p.ld_z + (int64_t)rhead * p.P + ycol;
+        if (p.z_wide) {
+            zr[0] = *reinterpret_cast<const uint4 *>(src);
+            if (ycol + 8 < p.P) zr[1] = *reinterpret_cast<const uint4 *>(src + 8);
+        } else {
+            __nv_bfloat16 *h = reinterpret_cast<__nv_bfloat16 *>(zr);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (ycol + i < p.P) h[i] = src[i];
+        }
+    };
+    auto readout = [&](int c) {
+        const int64_t t = it.t0 + (int64_t)c * kL + ri;
+        if (!ylive || t >= it.t1) return;
+        const float e = ctl.g[c & 1][ru].ec[ri];
+        const uint8_t *xt = sm + (c & 1) * kStage + ST_X + ru * 8192;
+        __nv_bfloat16 *dst = p.y + (t * p.heads + rhead) * (int64_t)p.P + ycol;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            if (ycol + 8 * v >= p.P) break;
+            const uint4 xv = *reinterpret_cast<const uint4 *>(xt + sw128_offset(ri, 2 * cg + v));
+            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, zw[4] = {zr[v].x, zr[v].y, zr[v].z, zr[v].w};
+            uint32_t out[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = 8 * v + 2 * i;
+                float a = fmaf(Dh, lo_f(xw[i]), fmaf(e, accs[k], acc[k]));
+                float b = fmaf(Dh, hi_f(xw[i]), fmaf(e, accs[k + 1], acc[k + 1]));
+                if (p.z) {
+                    a *= silu_gate(lo_f(zw[i]));
+                    b *= silu_gate(hi_f(zw[i]));
+                }
+                out[i] = pack2(a, b);
+            }
+            *reinterpret_cast<uint4 *>(dst + 8 * v) = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+    };
+
+    for (int c = 0; c < nchunks; ++c) {
+        const int s = c & 1;
+        uint8_t *st = sm + s * kStage;
+        const uint32_t aC = base + s * kStage + ST_C, aB = base + s * kStage + ST_B, aX = base + s * kStage + ST_X;
+        const uint32_t ph = c & 1;
+        const int len = (int)(it.t1 - it.t0 - (int64_t)c * kL < kL ? it.t1 - it.t0 - (int64_t)c * kL : kL);
+        ok = wait_for(&ctl.full[s], (c >> 1) & 1, budget);
+        if (len < kL) {
+            // The rows behind the sequence are another's: as operands they have to be zero.
+            if (ok)
+                for (int e = tid; e < (kL - len) * 32; e += kThreads) {
+                    const int r = len + (e >> 5), k = e & 31, tile = k >> 3;   // B regions 0, 1, units 0, 1
+                    *reinterpret_cast<uint4 *>(st + (tile < 2 ? ST_B + tile * 8192 : ST_X + (tile - 2) * 8192) +
+                                               sw128_offset(r, k & 7)) = make_uint4(0, 0, 0, 0);
+                }
+            fence_async_smem();
+            if (!(ok = __syncthreads_and(ok))) break;
+        }
+        if (!kState && tid == 0 && ok) {
+            tc_fence_after();
+            for (int k = 0; k < ksteps; ++k) {
+                const uint32_t col = (k & 3) * 32;
+                mma_f16(tmem + T_CB, sw128_desc(aC + (k >> 2) * 16384 + col, 16, 1024),
+                        sw128_desc(aB + (k >> 2) * 8192 + col, 16, 1024), kIdCB, k > 0);
+            }
+            mma_commit(&ctl.cb);
+            for (int k = 0; k < ksteps; ++k)
+                mma_f16(tmem + T_CS, sw128_desc(aC + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
+                        sw128_desc(base + O_S + k * 2048, 16384, 1024), kIdCS, k > 0);
+            mma_commit(&ctl.cs);
+        }
+        __syncwarp();
+        if (!kState && c > 0) readout(c - 1);
+
+        // w x of both units, split: unit tid / 256, token, two 16-byte pieces.
+        if (ok) {
+            const int u = tid >> 8, j = (tid & 255) >> 2, piece = 2 * (tid & 3);
+            const float w = ctl.g[s][u].w[j];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const uint32_t at = u * 8192 + sw128_offset(j, piece + v);
+                const uint4 xv = *reinterpret_cast<const uint4 *>(st + ST_X + at);
+                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a = w * lo_f(xw[i]), b = w * hi_f(xw[i]);
+                    hi[i] = pack2(a, b);
+                    lo[i] = pack2(a - lo_f(hi[i]), b - hi_f(hi[i]));
+                }
+                *reinterpret_cast<uint4 *>(sm + O_XH + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(sm + O_XL + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        }
+        fence_async_smem();
+        if (!(ok = __syncthreads_and(ok))) break;
+        if (tid == 0) {
+            tc_fence_after();
+            for (int k = 0; k < 4; ++k)
+                mma_f16(tmem + T_DS, sw128_desc(aB + k * 2048, 8192, 1024), sw128_desc(base + O_XH + k * 2048, 8192, 1024), kIdDS, k > 0);
+            for (int k = 0; k < 4; ++k)
+                mma_f16(tmem + T_DS, sw128_desc(aB + k * 2048, 8192, 1024), sw128_desc(base + O_XL + k * 2048, 8192, 1024), kIdDS, 1);
+            mma_commit(&ctl.ds);
+            if (c + 1 < nchunks) {      // the other stage: its last reader was the readout above
+                load(c + 1);
+                loaded = c + 2;
+            }
+        }
+        __syncwarp();
+        if (warp < 2 && c + 1 < nchunks) {
+            gates(c + 1);
+            if (c + 2 < nchunks) load_dt(c + 2);
+        }
+        if (!kState) {
+            load_z(c);
+            // M: scores of this thread's row and 16 columns, weighted.
+            ok = __all_sync(0xffffffffu, wait_for(&ctl.cb, ph, budget));
+            if (ok) {
+                tc_fence_after();
+                uint32_t r[16];
+                tmem_ld16(tmem + T_CB + lanes + 16 * cg, r);
+                tmem_ld_wait();
+                const Gates &G = ctl.g[s][ru];
+                const float ci = G.ci[ri];
+                uint32_t m[8];
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 cj = *reinterpret_cast<const float4 *>(&G.cj[16 * cg + i]);
+                    const int j = 16 * cg + i;
+                    const float v0 = j <= ri ? __uint_as_float(r[i]) * ex2(ci - cj.x) : 0.f;
+                    const float v1 = j + 1 <= ri ? __uint_as_float(r[i + 1]) * ex2(ci - cj.y) : 0.f;
+                    const float v2 = j + 2 <= ri ? __uint_as_float(r[i + 2]) * ex2(ci - cj.z) : 0.f;
+                    const float v3 = j + 3 <= ri ? __uint_as_float(r[i + 3]) * ex2(ci - cj.w) : 0.f;
+                    m[i / 2] = pack2(v0, v1);
+                    m[i / 2 + 1] = pack2(v2, v3);
+                }
+                *reinterpret_cast<uint4 *>(sm + O_M + sw128_offset(row, 2 * cg)) = make_uint4(m[0], m[1], m[2], m[3]);
+                *reinterpret_cast<uint4 *>(sm + O_M + sw128_offset(row, 2 * cg + 1)) = make_uint4(m[4], m[5], m[6], m[7]);
+            }
+            fence_async_smem();
+            tc_fence_before();
+            if (!(ok = __syncthreads_and(ok))) break;
+            if (tid == 0) {
+                tc_fence_after();
+                for (int k = 0; k < 4; ++k)
+                    mma_f16(tmem + T_MX, sw128_desc(base + O_M + k * 32, 16, 1024), sw128_desc(aX + k * 2048, 8192, 1024), kIdCS, k > 0);
+                mma_commit(&ctl.mx);
+            }
+            __syncwarp();
+        }
+
+        // S of this thread's row and columns; the readout of this chunk has read the old one.
+        ok = wait_for(&ctl.ds, ph, budget);
+        if (!kState) ok = wait_for(&ctl.cs, ph, budget) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            tc_fence_after();
+            const float dec = ctl.g[s][su].decay;
+            if (kState) seg_total += ctl.g[s][su].total;
+            uint32_t r[32];
+            tmem_ld32(tmem + T_DS + lanes + 32 * cg, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[i] = fmaf(dec, S[i], __uint_as_float(r[i]));
+            if (!kState) put_S();
+        }
+        fence_async_smem();
+        if (!kState) {
+            ok = __all_sync(0xffffffffu, wait_for(&ctl.mx, ph, budget) && ok);
+            if (ok) {
+                uint32_t a[16], b[16];
+                tmem_ld16(tmem + T_MX + lanes + 64 * ru + 16 * cg, a);
+                tmem_ld16(tmem + T_CS + lanes + 64 * ru + 16 * cg, b);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    acc[i] = __uint_as_float(a[i]);
+                    accs[i] = __uint_as_float(b[i]);
+                }
+            }
+        }
+        tc_fence_before();
+        if (!(ok = __syncthreads_and(ok))) break;
+    }
+    if (ok && !kState && nchunks > 0) readout(nchunks - 1);
+
+    if (ok) {
+        if (kState) {
+            if (sn < p.N && (su == 0 || two)) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<float4 *>(p.seg_state + sseg + i) = *reinterpret_cast<const float4 *>(S + i);
+                if (sn == 0 && sc == 0) p.seg_decay[it.slot * nunits + sunit] = ex2(seg_total);
+            }
+        } else if (it.k + 1 == it.nseg && sn < p.N && (su == 0 || two)) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+                if (sc + i < ucols) *reinterpret_cast<float4 *>(p.state_out + sglob + i) = *reinterpret_cast<const float4 *>(S + i);
+        }
+    } else {
+        // A wait ran out: the loads and MMAs in flight finish first (bounded), then the CTA leaves.
+        if (tid == 0) {
+            for (int c = loaded - 2 < 0 ? 0 : loaded - 2; c < loaded; ++c) mbar_wait(&ctl.full[c & 1], (c >> 1) & 1, kBudget);
+            mma_commit(&ctl.drain);
+            mbar_wait(&ctl.drain, 0, kBudget);
+            atomicOr(p.status, kDevTimeout);
+        }
+    }
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, kCols);
+}
+
+// The state entering each segment, in the place of the segment's own end state.
+__global__ void __launch_bounds__(256) ssm_segment_states(const __grid_constant__ TcParams p) {
+    const int64_t n = blockIdx.x, unit = blockIdx.y, nunits = (int64_t)p.groups * p.units;
+    const int64_t ls = (int64_t)p.seg_chunks * kL, per = (p.seqlen + ls - 1) / ls;
+    int64_t t0, t1;
+    if (!seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, n, t0, t1)) return;
+    const int nseg = (int)((t1 - t0 + ls - 1) / ls);
+    if (nseg <= 1) return;
+    const int64_t first = slot_base(p, n, ls, per);
+    const int head = (int)(unit / p.units) * (p.heads / p.groups) + (int)(unit % p.units) / p.ptiles;
+    const int tile = (int)(unit % p.units) % p.ptiles;
+    for (int e = blockIdx.z * 256 + threadIdx.x; e < p.N * 16; e += gridDim.z * 256) {
+        const int r = e >> 4, col = 4 * (e & 15);
+        float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.state_in && tile * 64 + col < p.P)
+            S = *reinterpret_cast<const float4 *>(p.state_in + (((size_t)n * p.heads + head) * p.N + r) * p.P + tile * 64 + col);
+        for (int k = 0; k < nseg; ++k) {
+            const int64_t at = (first + k) * nunits + unit;
+            float4 *place = reinterpret_cast<float4 *>(p.seg_state + (size_t)at * p.N * 64 + 4 * (size_t)e);
+            const float4 own = *place;
+            *place = S;
+            if (k + 1 == nseg) break;
+            const float d = p.seg_decay[at];
+            S.x = fmaf(d, S.x, own.x); S.y = fmaf(d, S.y, own.y);
+            S.z = fmaf(d, S.z, own.z); S.w = fmaf(d, S.w, own.w);
+        }
+    }
+}
+
+int unit_pairs(int heads, int groups, int head_dim) {
+    const int units = heads / groups * ((head_dim + 63) / 64);
+    return groups * ((units + 1) / 2);
+}
+
+constexpr int kSms = 152, kMinSegChunks = 8;
+
+// Chunks per segment (0: no segments).  Sequences are cut where sequences x pairs of units
+// fill less than half of the SMs; the segments then fill them once.
+int segment_chunks(bool varlen, int64_t seqlen, int64_t rows, int64_t num_seqs, int pairs) {
+    if (num_seqs <= 0 || pairs <= 0) return 0;
+    const int64_t chunks = varlen ? (rows + kL - 1) / kL : (seqlen + kL - 1) / kL;
+    const int64_t wanted = kSms / (varlen ? pairs : pairs * num_seqs);   // packed: of the whole row
+    if (wanted < 2) return 0;
+    int64_t seg = (chunks + wanted - 1) / wanted;
+    if (seg < kMinSegChunks) seg = kMinSegChunks;
+    return seg >= chunks ? 0 : (int)seg;
+}
+
+int64_t segment_slots(bool varlen, int64_t seqlen, int64_t rows, int64_t num_seqs, int seg) {
+    if (seg == 0) return num_seqs;
+    const int64_t ls = (int64_t)seg * kL;
+    return varlen ? rows / ls + num_seqs : num_seqs * ((seqlen + ls - 1) / ls);
+}
+
+struct SegBytes {
+    int seg;
+    int64_t slots;
+    size_t state, total;
+};
+SegBytes segment_bytes(bool varlen, int64_t seqlen, int64_t rows, int64_t num_seqs, int heads, int groups, int head_dim,
+                       int d_state) {
+    SegBytes b{};
+    b.seg = segment_chunks(varlen, seqlen, rows, num_seqs, unit_pairs(heads, groups, head_dim));
+    b.slots = segment_slots(varlen, seqlen, rows, num_seqs, b.seg);
+    if (b.seg == 0) return b;
+    const size_t units = (size_t)heads * ((head_dim + 63) / 64);
+    b.state = (size_t)b.slots * units * d_state * 64 * 4;
+    b.total = b.state + ((size_t)b.slots * units * 4 + 255) / 256 * 256;
+    return b;
+}
+
+}  // namespace
+
+bool ssm_tc_shape_ok(gdn_dtype io, int head_dim, int d_state) {
+    return io == GDN_BF16 && head_dim % 8 == 0 && d_state <= 128;
+}
+
+bool ssm_tc_rows_ok(const SsmParams &p) {
+    return reinterpret_cast<uintptr_t>(p.xs) % 16 == 0 && p.ldx % 8 == 0 && p.x_head % 8 == 0 && p.off_b % 8 == 0 &&
+           p.off_c % 8 == 0 && p.bc_group % 8 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
+}
+
+bool ssm_tc_segments(bool varlen, int64_t seqlen, int64_t rows, int64_t num_seqs, int heads, int groups, int head_dim) {
+    return segment_chunks(varlen, seqlen, rows, num_seqs, unit_pairs(heads, groups, head_dim)) > 0;
+}
+
+size_t ssm_tc_workspace(bool varlen, int64_t seqlen, int64_t rows, int64_t num_seqs, int heads, int groups, int head_dim,
+                        int d_state) {
+    return segment_bytes(varlen, seqlen, rows, num_seqs, heads, groups, head_dim, d_state).total;
+}
+
+cudaError_t launch_ssm_tc(const SsmParams &s, void *workspace, cudaStream_t stream) {
+    TcParams p;
+    memset(&p, 0, sizeof(p));
+    const bool varlen = s.cu_seqlens != nullptr;
+    const uint64_t row = (uint64_t)s.ldx * 2;
+    const __nv_bfloat16 *xs = static_cast<const __nv_bfloat16 *>(s.xs);
+    const uint32_t box[3] = {64, 1, kL};
+    const uint64_t dx[3] = {(uint64_t)s.head_dim, (uint64_t)s.heads, (uint64_t)s.rows}, sx[2] = {(uint64_t)s.x_head * 2, row};
+    const uint64_t db[3] = {(uint64_t)s.d_state, (uint64_t)s.groups, (uint64_t)s.rows}, sb[2] = {(uint64_t)s.bc_group * 2, row};
+    if (!encode_map_3d(&p.tm_x, xs, GDN_BF16, dx, sx, box, true) || !encode_map_3d(&p.tm_b, xs + s.off_b, GDN_BF16, db, sb, box, true) ||
+        !encode_map_3d(&p.tm_c, xs + s.off_c, GDN_BF16, db, sb, box, true))
+        return cudaErrorInvalidValue;
+    p.dt = static_cast<const __nv_bfloat16 *>(s.dt);
+    p.z = static_cast<const __nv_bfloat16 *>(s.z);
+    p.y = static_cast<__nv_bfloat16 *>(s.y);
+    p.ld_dt = s.ld_dt; p.ld_z = s.ld_z; p.A_log = s.A_log; p.dt_bias = s.dt_bias; p.D = s.D;
+    p.dt_min = s.dt_min; p.dt_max = s.dt_max; p.state_in = s.state_in; p.state_out = s.state_out;
+    p.cu_seqlens = s.cu_seqlens; p.seqlen = s.seqlen; p.rows = s.rows; p.num_seqs = s.num_seqs;
+    p.heads = s.heads; p.groups = s.groups; p.P = s.head_dim; p.N = s.d_state;
+    p.ptiles = (s.head_dim + 63) / 64;
+    p.units = s.heads / s.groups * p.ptiles;
+    p.pairs_per_group = (p.units + 1) / 2;
+    p.z_wide = reinterpret_cast<uintptr_t>(s.z) % 16 == 0 && s.ld_z % 8 == 0;
+    p.status = s.status;
+    p.budget = __atomic_load_n(&g_wait_budget, __ATOMIC_RELAXED);
+    const SegBytes b = segment_bytes(varlen, s.seqlen, s.rows, s.num_seqs, s.heads, s.groups, s.head_dim, s.d_state);
+    p.seg_chunks = b.seg;
+    p.seg_state = static_cast<float *>(workspace);
+    p.seg_decay = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + b.state);
+
+    const int64_t grid = b.slots * (int64_t)s.groups * p.pairs_per_group;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(ssm_chunk_scan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_chunk_scan<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (b.seg > 0) {
+        ssm_chunk_scan<true><<<(unsigned)grid, kThreads, kSmem, stream>>>(p);
+        ssm_segment_states<<<dim3((unsigned)s.num_seqs, (unsigned)(s.groups * p.units), 2), 256, 0, stream>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    ssm_chunk_scan<false><<<(unsigned)grid, kThreads, kSmem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

@@ -30,7 +30,7 @@ EXPORTS = ("gdn_prefill_workspace_bytes", "gdn_prefill", "gdn_decode_step",
            "gdn_gated_rmsnorm", "gdn_set_wait_budget", "gdn_decode_layer", "gdn_prefill_variant",
            "gdn_prefill_norm", "gdn_prefill_variant_workspace_bytes", "gdn_prefill_variant_plan",
            "gdn_prefill_layer", "gdn_prefill_layer_workspace_bytes", "gdn_ssm_prefill_workspace_bytes",
-           "gdn_ssm_prefill", "gdn_ssm_decode", "gdn_rotary", "gdn_rotary_frequencies")
+           "gdn_ssm_prefill", "gdn_ssm_prefill_plan", "gdn_ssm_decode", "gdn_rotary", "gdn_rotary_frequencies")
 PATH_SIMT, PATH_TC, PATH_TC_TP = 1, 2, 3
 # gdn_rule codes.
 RULES = {"gated_delta": 0, "delta": 1, "gated": 2, "linear": 3}
@@ -175,6 +175,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.gdn_ssm_prefill_workspace_bytes.argtypes = [SS, SP]
     lib.gdn_ssm_prefill.restype = ctypes.c_int
     lib.gdn_ssm_prefill.argtypes = [SS, SP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.gdn_ssm_prefill_plan.restype = ctypes.c_int
+    lib.gdn_ssm_prefill_plan.argtypes = [SS, SP, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]
     lib.gdn_ssm_decode.restype = ctypes.c_int
     lib.gdn_ssm_decode.argtypes = [SS, SP, P, P, P, P, P, P, P, P, P, P, ctypes.c_int64, P, P, P]
     lib.gdn_rotary.restype = ctypes.c_int
@@ -914,6 +916,13 @@ def _ssm_geometry(xbc, dt, z, heads, head_dim, groups, d_state, cu_seqlens, conv
 
 def gdn_ssm_prefill_workspace_bytes(shape: GdnSsmShape, params: GdnSsmParams) -> int:
     return int(load().gdn_ssm_prefill_workspace_bytes(ctypes.byref(shape), ctypes.byref(params)))
+
+
+def gdn_ssm_prefill_plan(shape: GdnSsmShape, params: GdnSsmParams):
+    """(path, launches) of a gdn_ssm_prefill call: PATH_SIMT, PATH_TC or PATH_TC_TP (time segments)."""
+    path, launches = ctypes.c_int32(), ctypes.c_int32()
+    _check(load().gdn_ssm_prefill_plan(ctypes.byref(shape), ctypes.byref(params), ctypes.byref(path), ctypes.byref(launches)))
+    return path.value, launches.value
 
 
 def gdn_ssm_prefill(xbc, dt, A_log, *, heads: int, head_dim: int, d_state: int, groups: int = 1, D=None, dt_bias=None,

@@ -222,6 +222,32 @@ def test_bad_offsets_are_reported_and_skipped():
     assert torch.equal(y[:, :90], good[0][:, :90])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,P,G,N", [(2, 64, 1, 128), (3, 64, 1, 100), (6, 128, 2, 64), (5, 80, 1, 16)])
+@pytest.mark.parametrize("lens,packed", [([3000], False), ([1500, 1500], False), ([2100, 5, 0, 1400, 513], True)])
+def test_long_prompts_in_time_segments(H, P, G, N, lens, packed):
+    """Odd unit counts and lengths over several segments, against the fp32 cores' scan of the same values."""
+    m = draw("bf16", lens, H, P, G, N, 0, packed=packed, seed=N + len(lens), gap=(-(2 * H * P + 2 * G * N + H)) % 8)
+    shape = gdn.GdnSsmShape(1, len(lens) if not packed else 1, sum(lens) if packed else lens[0], len(lens), H, P, G, N, 0, 0, 0)
+    assert gdn.gdn_ssm_prefill_plan(shape, gdn.GdnSsmParams(0, 0, 0.0, 1.0))[0] == gdn.PATH_TC_TP
+    wide = dict(m, io=torch.float32, **{k: m[k].float() for k in ("xbc", "dt", "z")})
+    check(m, prefill(m), prefill(wide))
+
+
+@pytest.mark.gpu
+def test_a_wait_that_runs_out_is_reported():
+    m = draw("bf16", [300, 1400], 4, 64, 1, 128, 0, seed=14)
+    want = prefill(m)
+    gdn.gdn_set_wait_budget(50)          # far below one tile load
+    try:
+        lib.gdn_ssm_prefill(m["xbc"], m["dt"], m["A_log"], state_in=m["state"], cu_seqlens=m["cu"], **kwargs(m))
+        torch.cuda.synchronize()
+        assert lib.gdn_last_device_status() == gdn.GDN_ERR_TIMEOUT
+    finally:
+        gdn.gdn_set_wait_budget(0)
+    assert all(torch.equal(a, b) for a, b in zip(prefill(m)[:2], want[:2]))
+
+
 # ------------------------------------------------------------------ single tokens
 @pytest.mark.gpu
 @pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
@@ -378,6 +404,17 @@ def test_bad_decode_pointers_are_refused(over):
     assert call_decode(_ssm(seqlen=1), _params(), **over) == gdn.GDN_ERR_INVALID_ARG
     assert call_decode(_ssm(seqlen=2), _params()) == gdn.GDN_ERR_INVALID_ARG
     assert call_prefill(None, _params()) == call_prefill(_ssm(), None) == gdn.GDN_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("shape,params,want", [
+    (dict(seqlen=8192, heads=64, groups=1, d_state=128), {}, (gdn.PATH_TC_TP, 4)),
+    (dict(seqlen=8192, heads=64, groups=1, d_state=128), dict(conv_kernel=0), (gdn.PATH_TC_TP, 3)),
+    (dict(seqlen=8192, heads=64, groups=1, d_state=100), dict(conv_kernel=0), (gdn.PATH_TC_TP, 4)),
+    (dict(seqlen=100, heads=64, groups=8), {}, (gdn.PATH_TC, 2)), (dict(seqlen=100, batch=64, num_seqs=64), dict(conv_kernel=0), (gdn.PATH_TC, 1)),
+    (dict(io_dtype=0), {}, (gdn.PATH_SIMT, 2)), (dict(io_dtype=2), dict(conv_kernel=0), (gdn.PATH_SIMT, 1)),
+    (dict(d_state=129), {}, (gdn.PATH_SIMT, 2)), (dict(head_dim=52), {}, (gdn.PATH_SIMT, 2)), (dict(batch=0, num_seqs=0), {}, (gdn.PATH_SIMT, 0))])
+def test_plans(shape, params, want):
+    assert gdn.gdn_ssm_prefill_plan(_ssm(**shape), _params(**params)) == want
 
 
 def test_nothing_to_do_is_no_error():
