@@ -11,11 +11,11 @@
 // walks the chunks of a sequence (or of one time segment of it).  Two, because the group's
 // scores C B^T then serve both and every MMA is 128 x 128 but the scores' 128 x 64: C stands
 // twice in shared memory, so that accumulator rows 0-63 are unit 0's tokens and rows 64-127
-// unit 1's, and all 16 warps (and all four lane quarters of tensor memory) share the work.
-// Per chunk, the MMA group on the left runs under the thread work on the right:
-//   scores C B^T, readout C [S0 | S1]    y of the chunk before; w x split into bf16 hi + lo
-//   B^T [w x hi] + B^T [w x lo]          M from the scores (fp32), rounded to bf16
-//   [M0; M1] [x0 | x1]                   S = e^{G_L} S + .. in fp32 registers; bf16(S) for the next C S
+// unit 1's, and every lane quarter of tensor memory has work.  Per chunk:
+//   scores C B^T -> M (fp32 weights, rounded to bf16) -> [M0; M1] [x0 | x1]     \ y, by the y warps
+//   C [S0 | S1]                                                                  /
+//   w x split into bf16 hi + lo -> B^T [w x hi] + B^T [w x lo] -> S = e^{G_L} S + ..   by the S warps
+// The warps' roles run side by side, a chunk apart where the data allows it.
 // Precision: the state is fp32 and its update's operands are exact (B) or a two-term bf16 split
 // (w x: 2^-17 of each product), because the state is returned in fp32 and carried on; M and
 // the S that C reads are rounded once to bf16, half a step (2^-9 of each term's size at random
@@ -38,7 +38,7 @@ namespace {
 using namespace tc;
 
 constexpr int kL = 64;                       // tokens per chunk
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr long long kBudget = 4000000000LL;  // cycles (~2 s) before a wait gives up
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -87,8 +87,11 @@ struct alignas(16) Gates {       // read in float2 and float4
 };
 
 struct Ctl {
-    uint64_t full[2], cb, cs, ds, mx, drain;
+    // Barriers: pairs by chunk parity where a waiter can be a chunk behind.
+    uint64_t full[2], gates[2], y_read[2], s_ready[2], wx_ready[2], ds[2];
+    uint64_t cb, cs, mx, m_ready, s_first, drain;
     uint32_t tmem;
+    int32_t abort;   // a wait ran out
     Gates g[2][2];   // [chunk parity][unit]
 };
 static_assert(sizeof(Gates) % 16 == 0 && offsetof(Ctl, g) % 16 == 0, "vector accesses of the gates");
@@ -105,12 +108,31 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// mbar_wait, but under a short budget (gdn_set_wait_budget) a wait that took longer has run
-// out even where the one blocking try saw it end.
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, long long budget) {
-    if (budget >= 100000) return mbar_wait(bar, parity, budget);
+// Tensor-memory loads have landed.  The values pass through it, so that no arithmetic on them
+// can be scheduled ahead of the wait (which does not name them itself).
+template <int N> __device__ __forceinline__ void landed(uint32_t (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// A bounded wait that gives up when another thread has.  Under a short budget
+// (gdn_set_wait_budget) a wait that took longer has run out even where a blocking try saw it end.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int32_t *abort, long long budget) {
+    const bool brief = budget < 100000;
+    if (!brief && mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
-    return mbar_wait(bar, parity, budget) && clock64() - t0 <= budget;
+    while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+        if (*abort) return false;
+        if (clock64() - t0 > budget) {
+            *abort = 1;
+            return false;
+        }
+    }
+    if (brief && clock64() - t0 > budget) {
+        *abort = 1;
+        return false;
+    }
+    return true;
 }
 
 // One work item: the chunks [t0, t1) of segment k of sequence n.
@@ -156,7 +178,13 @@ __device__ __forceinline__ Item item_of(const TcParams &p, int64_t s) {
     return it;
 }
 
-// kState: the state-only pass of a segment (no scores, no y).
+// The roles of a CTA's warps, each with its own pace; mbarriers carry the order.
+//   0-7    y: M from the scores, and the readout (row 32 (warp & 3) + lane, 32 columns of it)
+//   8-15   S: w x, and the state (its row n, the 64 columns of one unit, in registers)
+//   16     issues the MMAs     17  issues the TMA loads     18, 19  the gates of unit 0, 1
+constexpr int kIssueWarp = 16, kLoadWarp = 17, kGateWarp = 18;
+
+// kState: the state-only pass of a segment (no scores, no y; warps 0-7 make w x there).
 template <bool kState>
 __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_constant__ TcParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -181,356 +209,415 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
     auto unit_tile = [&](int u) { return (u0 + (two ? u : 0)) % p.ptiles; };
 
     const long long budget = p.budget > 0 ? p.budget : kBudget;
-    if (warp == 0) {
+    if (warp == kIssueWarp) {
         tmem_alloc(&ctl.tmem, kCols);
         tmem_relinquish();
     }
     if (tid == 0) {
-        mbar_init(&ctl.full[0], 1);
-        mbar_init(&ctl.full[1], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl.full[i], 1);
+            mbar_init(&ctl.gates[i], 2);
+            mbar_init(&ctl.y_read[i], 8);
+            mbar_init(&ctl.s_ready[i], 8);
+            mbar_init(&ctl.wx_ready[i], 8);
+            mbar_init(&ctl.ds[i], 1);
+        }
         mbar_init(&ctl.cb, 1);
         mbar_init(&ctl.cs, 1);
-        mbar_init(&ctl.ds, 1);
         mbar_init(&ctl.mx, 1);
+        mbar_init(&ctl.m_ready, 8);
+        mbar_init(&ctl.s_first, 8);
         mbar_init(&ctl.drain, 1);
         fence_mbar_init();
+        ctl.abort = 0;
     }
-
-    // This thread's part of S: state row n, 32 columns of unit su.
-    const int q = warp & 3, cg = warp >> 2;           // TMEM lane quarter, column group
-    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-    const int sn = 32 * q + lane, su = cg >> 1, sc = 32 * (cg & 1);
-    const int shead = unit_head(su), scol = unit_tile(su) * 64 + sc;
-    const int ucols = p.P - unit_tile(su) * 64;       // columns of this unit that exist
-    const int64_t nunits = (int64_t)p.groups * p.units;
-    const int64_t sunit = (int64_t)g * p.units + u0 + (two ? su : 0);
-    const size_t sglob = (((size_t)it.n * p.heads + shead) * p.N + sn) * p.P + scol;
-    const size_t sseg = ((size_t)it.slot * nunits + sunit) * p.N * 64 + (size_t)sn * 64 + sc;
-    alignas(16) float S[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) S[i] = 0.f;
-    if (!kState && sn < p.N) {
-        if (it.nseg > 1) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4 *>(S + i) = *reinterpret_cast<const float4 *>(p.seg_state + sseg + i);
-        } else if (p.state_in) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-                if (sc + i < ucols) *reinterpret_cast<float4 *>(S + i) = *reinterpret_cast<const float4 *>(p.state_in + sglob + i);
-        }
-    }
-    auto put_S = [&]() {     // bf16(S) as the next readout's operand
-        uint8_t *row = sm + O_S + su * 16384;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4 *>(row + sw128_offset(sn, (sc >> 3) + c)) =
-                make_uint4(pack2(S[8 * c], S[8 * c + 1]), pack2(S[8 * c + 2], S[8 * c + 3]), pack2(S[8 * c + 4], S[8 * c + 5]),
-                           pack2(S[8 * c + 6], S[8 * c + 7]));
-    };
-    if (!kState) put_S();
-
-    // This thread's part of M and y: token `ri` of unit ru, 16 columns.
-    const int row = 32 * q + lane, ru = q >> 1, ri = row & 63;
-    const int rhead = unit_head(ru), rtile = unit_tile(ru);
-    const int ycol = rtile * 64 + 16 * cg;            // first of its columns in the head
-    const bool ylive = (ru == 0 || two) && ycol < p.P;
-    const float Dh = p.D ? p.D[rhead] : 0.f;
-
+    volatile int32_t *abort = &ctl.abort;
     const int nchunks = (int)((it.t1 - it.t0 + kL - 1) / kL);
-    const int regions = p.N > 64 ? 2 : 1, ksteps = (p.N + 15) / 16;
-    auto load = [&](int c) {          // chunk c into its stage (one thread)
+    auto chunk_len = [&](int c) {
+        const int64_t left = it.t1 - it.t0 - (int64_t)c * kL;
+        return left < kL ? (int)left : kL;
+    };
+    // A phase of a barrier that completes once per chunk, and of one of a pair by chunk parity.
+    auto wait = [&](uint64_t *bar, int c) { return wait_for(bar, c & 1, abort, budget); };
+    auto wait2 = [&](uint64_t *bar, int c) { return wait_for(bar + (c & 1), (c >> 1) & 1, abort, budget); };
+    auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
+    // This warp's shared-memory writes are done (for the tensor cores too): one arrival.
+    auto arrive = [&](uint64_t *bar) {
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    // w x of chunk c by 256 threads (`who` 0-255), split into two bf16 terms, at buffer `xh`.
+    // Rows behind the sequence are another's: as operands they have to be zero.
+    auto make_wx = [&](int c, int who, uint8_t *xh) {
         uint8_t *st = sm + (c & 1) * kStage;
-        uint64_t *bar = &ctl.full[c & 1];
-        const int t = (int)(it.t0 + (int64_t)c * kL);
-        mbar_arrive_expect_tx(bar, 8192u * (regions * (kState ? 1 : 3) + 2));
-        for (int r = 0; r < regions; ++r) {
-            tma_load_3d(st + ST_B + r * 8192, &p.tm_b, 64 * r, g, t, bar);
-            if (!kState) {
-                tma_load_3d(st + ST_C + r * 16384, &p.tm_c, 64 * r, g, t, bar);
-                tma_load_3d(st + ST_C + r * 16384 + 8192, &p.tm_c, 64 * r, g, t, bar);
+        const int len = chunk_len(c);
+        if (len < kL)
+            for (int e = who; e < (kL - len) * 32; e += 256) {
+                const int r = len + (e >> 5), k = e & 31, tile = k >> 3;   // B regions 0, 1, units 0, 1
+                *reinterpret_cast<uint4 *>(st + (tile < 2 ? ST_B + tile * 8192 : ST_X + (tile - 2) * 8192) + sw128_offset(r, k & 7)) =
+                    make_uint4(0, 0, 0, 0);
             }
-        }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) tma_load_3d(st + ST_X + u * 8192, &p.tm_x, 64 * unit_tile(u), unit_head(u), t, bar);
-    };
-    // Gates of chunk c, by warp u for unit u: two tokens to a lane.  A decay of e^-111 is
-    // already nothing in fp32, so g is held above that: a reset then leaves the running sum
-    // small enough to keep the differences of the tokens behind it.
-    float dt0 = 0.f, dt1 = 0.f;
-    const int gw = warp & 1;
-    const float gA = -expf(p.A_log[unit_head(gw)]) * kLog2e, gbias = p.dt_bias ? p.dt_bias[unit_head(gw)] : 0.f;
-    auto load_dt = [&](int c) {
-        const int64_t t = it.t0 + (int64_t)c * kL + 2 * lane;
-        const __nv_bfloat16 *at = p.dt + t * p.ld_dt + unit_head(gw);
-        dt0 = t < it.t1 ? __bfloat162float(at[0]) : 0.f;
-        dt1 = t + 1 < it.t1 ? __bfloat162float(at[p.ld_dt]) : 0.f;
-    };
-    auto gates = [&](int c) {
-        const int64_t t = it.t0 + (int64_t)c * kL + 2 * lane;
-        const float d0 = t < it.t1 ? ssm_step(dt0, gbias, p.dt_min, p.dt_max) : 0.f;
-        const float d1 = t + 1 < it.t1 ? ssm_step(dt1, gbias, p.dt_min, p.dt_max) : 0.f;
-        float g0 = gA * d0, g1 = gA * d1;
-        g0 = g0 < -160.f ? -160.f : g0;
-        g1 = g1 < -160.f ? -160.f : g1;
-        float pre = g0 + g1, suf = pre;
+        for (int v = 0; v < 4; ++v) {
+            const int u = v >> 1, j = (who >> 3) + 32 * (v & 1);
+            const uint32_t at = u * 8192 + sw128_offset(j, who & 7);
+            const float w = j < len ? ctl.g[c & 1][u].w[j] : 0.f;
+            const uint4 xv = j < len ? *reinterpret_cast<const uint4 *>(st + ST_X + at) : make_uint4(0, 0, 0, 0);
+            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+            uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float a = __shfl_up_sync(0xffffffffu, pre, o), b = __shfl_down_sync(0xffffffffu, suf, o);
-            if (lane >= o) pre += a;
-            if (lane + o < 32) suf += b;
-        }
-        float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
-        if (lane == 0) before = 0.f;
-        if (lane == 31) after = 0.f;
-        Gates &G = ctl.g[c & 1][gw];
-        const float c0 = before + g0, c1 = pre;
-        const float l0 = __log2f(d0), l1 = __log2f(d1);   // -inf where the step is zero: no weight
-        *reinterpret_cast<float2 *>(&G.ci[2 * lane]) = make_float2(c0, c1);
-        *reinterpret_cast<float2 *>(&G.cj[2 * lane]) = make_float2(c0 - l0, c1 - l1);
-        *reinterpret_cast<float2 *>(&G.ec[2 * lane]) = make_float2(ex2(c0), ex2(c1));
-        *reinterpret_cast<float2 *>(&G.w[2 * lane]) = make_float2(d0 * ex2(after + g1), d1 * ex2(after));
-        if (lane == 0) {
-            G.total = suf;
-            G.decay = ex2(suf);
+            for (int i = 0; i < 4; ++i) {
+                const float a = w * lo_f(xw[i]), b = w * hi_f(xw[i]);
+                hi[i] = pack2(a, b);
+                lo[i] = pack2(a - lo_f(hi[i]), b - hi_f(hi[i]));
+            }
+            *reinterpret_cast<uint4 *>(xh + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(xh + 16384 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     };
-    if (nchunks > 0) {
-        if (warp < 2) {
-            load_dt(0);
-            gates(0);
-            if (nchunks > 1) load_dt(1);
-        }
-    }
-    fence_async_smem();
+
+    const int q = warp & 3, half = (warp >> 2) & 1;   // TMEM lane quarter; column half
+    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
-    const uint32_t base = smem_u32(sm);
-    constexpr uint32_t kIdCB = idesc_f16(true, 128, 64, false, false), kIdCS = idesc_f16(true, 128, 128, false, true),
-                       kIdDS = idesc_f16(true, 128, 128, true, true);
-
-    int loaded = 0;                   // chunks whose loads are issued (thread 0)
-    if (tid == 0 && nchunks > 0) {
-        load(0);
-        loaded = 1;
-    }
     bool ok = true;
-    float seg_total = 0.f;
-    // y of the chunk before: what its accumulators held, and its z.
-    float acc[16], accs[16];
-    uint4 zr[2];
-    auto load_z = [&](int c) {
-        const int64_t t = it.t0 + (int64_t)c * kL + ri;
-        if (p.z == nullptr || !ylive || t >= it.t1) return;
-        const __nv_bfloat16 *src = p.z + t * p.ld_z + (int64_t)rhead * p.P + ycol;
-        if (p.z_wide) {
-            zr[0] = *reinterpret_cast<const uint4 *>(src);
-            if (ycol + 8 < p.P) zr[1] = *reinterpret_cast<const uint4 *>(src + 8);
-        } else {
-            __nv_bfloat16 *h = reinterpret_cast<__nv_bfloat16 *>(zr);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (ycol + i < p.P) h[i] = src[i];
-        }
-    };
-    auto readout = [&](int c) {
-        const int64_t t = it.t0 + (int64_t)c * kL + ri;
-        if (!ylive || t >= it.t1) return;
-        const float e = ctl.g[c & 1][ru].ec[ri];
-        const uint8_t *xt = sm + (c & 1) * kStage + ST_X + ru * 8192;
-        __nv_bfloat16 *dst = p.y + (t * p.heads + rhead) * (int64_t)p.P + ycol;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            if (ycol + 8 * v >= p.P) break;
-            const uint4 xv = *reinterpret_cast<const uint4 *>(xt + sw128_offset(ri, 2 * cg + v));
-            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, zw[4] = {zr[v].x, zr[v].y, zr[v].z, zr[v].w};
-            uint32_t out[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = 8 * v + 2 * i;
-                float a = fmaf(Dh, lo_f(xw[i]), fmaf(e, accs[k], acc[k]));
-                float b = fmaf(Dh, hi_f(xw[i]), fmaf(e, accs[k + 1], acc[k + 1]));
-                if (p.z) {
-                    a *= silu_gate(lo_f(zw[i]));
-                    b *= silu_gate(hi_f(zw[i]));
-                }
-                out[i] = pack2(a, b);
-            }
-            *reinterpret_cast<uint4 *>(dst + 8 * v) = make_uint4(out[0], out[1], out[2], out[3]);
-        }
-    };
 
-    for (int c = 0; c < nchunks; ++c) {
-        const int s = c & 1;
-        uint8_t *st = sm + s * kStage;
-        const uint32_t aC = base + s * kStage + ST_C, aB = base + s * kStage + ST_B, aX = base + s * kStage + ST_X;
-        const uint32_t ph = c & 1;
-        const int len = (int)(it.t1 - it.t0 - (int64_t)c * kL < kL ? it.t1 - it.t0 - (int64_t)c * kL : kL);
-        ok = wait_for(&ctl.full[s], (c >> 1) & 1, budget);
-        if (len < kL) {
-            // The rows behind the sequence are another's: as operands they have to be zero.
-            if (ok)
-                for (int e = tid; e < (kL - len) * 32; e += kThreads) {
-                    const int r = len + (e >> 5), k = e & 31, tile = k >> 3;   // B regions 0, 1, units 0, 1
-                    *reinterpret_cast<uint4 *>(st + (tile < 2 ? ST_B + tile * 8192 : ST_X + (tile - 2) * 8192) +
-                                               sw128_offset(r, k & 7)) = make_uint4(0, 0, 0, 0);
-                }
-            fence_async_smem();
-            if (!(ok = __syncthreads_and(ok))) break;
-        }
-        if (!kState && tid == 0 && ok) {
-            tc_fence_after();
-            for (int k = 0; k < ksteps; ++k) {
-                const uint32_t col = (k & 3) * 32;
-                mma_f16(tmem + T_CB, sw128_desc(aC + (k >> 2) * 16384 + col, 16, 1024),
-                        sw128_desc(aB + (k >> 2) * 8192 + col, 16, 1024), kIdCB, k > 0);
-            }
-            mma_commit(&ctl.cb);
-            for (int k = 0; k < ksteps; ++k)
-                mma_f16(tmem + T_CS, sw128_desc(aC + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
-                        sw128_desc(base + O_S + k * 2048, 16384, 1024), kIdCS, k > 0);
-            mma_commit(&ctl.cs);
-        }
-        __syncwarp();
-        if (!kState && c > 0) readout(c - 1);
-
-        // w x of both units, split: unit tid / 256, token, two 16-byte pieces.
-        if (ok) {
-            const int u = tid >> 8, j = (tid & 255) >> 2, piece = 2 * (tid & 3);
-            const float w = ctl.g[s][u].w[j];
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const uint32_t at = u * 8192 + sw128_offset(j, piece + v);
-                const uint4 xv = *reinterpret_cast<const uint4 *>(st + ST_X + at);
-                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = w * lo_f(xw[i]), b = w * hi_f(xw[i]);
-                    hi[i] = pack2(a, b);
-                    lo[i] = pack2(a - lo_f(hi[i]), b - hi_f(hi[i]));
-                }
-                *reinterpret_cast<uint4 *>(sm + O_XH + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(sm + O_XL + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
-        }
-        fence_async_smem();
-        if (!(ok = __syncthreads_and(ok))) break;
-        if (tid == 0) {
-            tc_fence_after();
-            for (int k = 0; k < 4; ++k)
-                mma_f16(tmem + T_DS, sw128_desc(aB + k * 2048, 8192, 1024), sw128_desc(base + O_XH + k * 2048, 8192, 1024), kIdDS, k > 0);
-            for (int k = 0; k < 4; ++k)
-                mma_f16(tmem + T_DS, sw128_desc(aB + k * 2048, 8192, 1024), sw128_desc(base + O_XL + k * 2048, 8192, 1024), kIdDS, 1);
-            mma_commit(&ctl.ds);
-            if (c + 1 < nchunks) {      // the other stage: its last reader was the readout above
-                load(c + 1);
-                loaded = c + 2;
-            }
-        }
-        __syncwarp();
-        if (warp < 2 && c + 1 < nchunks) {
-            gates(c + 1);
-            if (c + 2 < nchunks) load_dt(c + 2);
-        }
-        if (!kState) {
-            load_z(c);
-            // M: scores of this thread's row and 16 columns, weighted.
-            ok = __all_sync(0xffffffffu, wait_for(&ctl.cb, ph, budget));
-            if (ok) {
+    if (warp == kIssueWarp) {
+        // ------------------------------------------------------------ MMAs
+        if (lane == 0) {
+            const uint32_t base = smem_u32(sm);
+            constexpr uint32_t kIdCB = idesc_f16(true, 128, 64, false, false), kIdCS = idesc_f16(true, 128, 128, false, true),
+                               kIdDS = idesc_f16(true, 128, 128, true, true);
+            const int ksteps = (p.N + 15) / 16;
+            // Descriptors; their low field counts 16 bytes, so a K step adds 2 (K-major) or 128.
+            // (The loops over ksteps stay loops: unrolled, with each MMA under its own
+            // condition, nvcc 13.0 gave one of them another's operand.)
+            const uint64_t dC = sw128_desc(base + ST_C, 16, 1024), dBk = sw128_desc(base + ST_B, 16, 1024),
+                           dS = sw128_desc(base + O_S, 16384, 1024), dBm = sw128_desc(base + ST_B, 8192, 1024),
+                           dXH = sw128_desc(base + O_XH, 8192, 1024), dX = sw128_desc(base + ST_X, 8192, 1024),
+                           dM = sw128_desc(base + O_M, 16, 1024), dXH1 = sw128_desc(base + O_S, 8192, 1024);
+            auto issue_cb = [&](int c) {
+                const uint64_t st = (uint64_t)(c & 1) * (kStage >> 4);
+                for (int k = 0; k < ksteps; ++k)
+                    mma_f16(tmem + T_CB, dC + st + (k >> 2) * 1024 + (k & 3) * 2, dBk + st + (k >> 2) * 512 + (k & 3) * 2, kIdCB, k > 0);
+                mma_commit(&ctl.cb);
+            };
+            if (!kState && nchunks > 0 && (ok = wait2(ctl.full, 0))) issue_cb(0);
+            for (int c = 0; ok && c < nchunks; ++c) {
+                const uint64_t st = (uint64_t)(c & 1) * (kStage >> 4);
+                if (!(ok = wait2(ctl.wx_ready, c) && wait2(ctl.full, c) && (!kState || c < 2 || wait2(ctl.s_ready, c - 2)))) break;
                 tc_fence_after();
-                uint32_t r[16];
-                tmem_ld16(tmem + T_CB + lanes + 16 * cg, r);
-                tmem_ld_wait();
-                const Gates &G = ctl.g[s][ru];
-                const float ci = G.ci[ri];
-                uint32_t m[8];
+                const uint64_t xh = kState && (c & 1) ? dXH1 : dXH;
+                const uint32_t dst = tmem + (kState && (c & 1) ? T_CS : T_DS);
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 cj = *reinterpret_cast<const float4 *>(&G.cj[16 * cg + i]);
-                    const int j = 16 * cg + i;
-                    const float v0 = j <= ri ? __uint_as_float(r[i]) * ex2(ci - cj.x) : 0.f;
-                    const float v1 = j + 1 <= ri ? __uint_as_float(r[i + 1]) * ex2(ci - cj.y) : 0.f;
-                    const float v2 = j + 2 <= ri ? __uint_as_float(r[i + 2]) * ex2(ci - cj.z) : 0.f;
-                    const float v3 = j + 3 <= ri ? __uint_as_float(r[i + 3]) * ex2(ci - cj.w) : 0.f;
-                    m[i / 2] = pack2(v0, v1);
-                    m[i / 2 + 1] = pack2(v2, v3);
-                }
-                *reinterpret_cast<uint4 *>(sm + O_M + sw128_offset(row, 2 * cg)) = make_uint4(m[0], m[1], m[2], m[3]);
-                *reinterpret_cast<uint4 *>(sm + O_M + sw128_offset(row, 2 * cg + 1)) = make_uint4(m[4], m[5], m[6], m[7]);
-            }
-            fence_async_smem();
-            tc_fence_before();
-            if (!(ok = __syncthreads_and(ok))) break;
-            if (tid == 0) {
+                for (int k = 0; k < 8; ++k)
+                    mma_f16(dst, dBm + st + (k & 3) * 128, xh + (k >> 2) * 1024 + (k & 3) * 128, kIdDS, k > 0);
+                mma_commit(&ctl.ds[kState ? c & 1 : 0]);
+                if (kState) continue;
+                // C S, once S is in place and the accumulators of the chunk before are read.
+                if (!(ok = c == 0 ? wait(&ctl.s_first, 0) : wait2(ctl.s_ready, c - 1) && wait2(ctl.y_read, c - 1))) break;
                 tc_fence_after();
-                for (int k = 0; k < 4; ++k)
-                    mma_f16(tmem + T_MX, sw128_desc(base + O_M + k * 32, 16, 1024), sw128_desc(aX + k * 2048, 8192, 1024), kIdCS, k > 0);
+                for (int k = 0; k < ksteps; ++k)
+                    mma_f16(tmem + T_CS, dC + st + (k >> 2) * 1024 + (k & 3) * 2, dS + k * 128, kIdCS, k > 0);
+                mma_commit(&ctl.cs);
+                if (!(ok = wait(&ctl.m_ready, c))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma_f16(tmem + T_MX, dM + k * 2, dX + st + k * 128, kIdCS, k > 0);
                 mma_commit(&ctl.mx);
-            }
-            __syncwarp();
-        }
-
-        // S of this thread's row and columns; the readout of this chunk has read the old one.
-        ok = wait_for(&ctl.ds, ph, budget);
-        if (!kState) ok = wait_for(&ctl.cs, ph, budget) && ok;
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-            tc_fence_after();
-            const float dec = ctl.g[s][su].decay;
-            if (kState) seg_total += ctl.g[s][su].total;
-            uint32_t r[32];
-            tmem_ld32(tmem + T_DS + lanes + 32 * cg, r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) S[i] = fmaf(dec, S[i], __uint_as_float(r[i]));
-            if (!kState) put_S();
-        }
-        fence_async_smem();
-        if (!kState) {
-            ok = __all_sync(0xffffffffu, wait_for(&ctl.mx, ph, budget) && ok);
-            if (ok) {
-                uint32_t a[16], b[16];
-                tmem_ld16(tmem + T_MX + lanes + 64 * ru + 16 * cg, a);
-                tmem_ld16(tmem + T_CS + lanes + 64 * ru + 16 * cg, b);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    acc[i] = __uint_as_float(a[i]);
-                    accs[i] = __uint_as_float(b[i]);
+                if (c + 1 < nchunks) {
+                    if (!(ok = wait2(ctl.full, c + 1))) break;
+                    issue_cb(c + 1);
                 }
             }
-        }
-        tc_fence_before();
-        if (!(ok = __syncthreads_and(ok))) break;
-    }
-    if (ok && !kState && nchunks > 0) readout(nchunks - 1);
-
-    if (ok) {
-        if (kState) {
-            if (sn < p.N && (su == 0 || two)) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<float4 *>(p.seg_state + sseg + i) = *reinterpret_cast<const float4 *>(S + i);
-                if (sn == 0 && sc == 0) p.seg_decay[it.slot * nunits + sunit] = ex2(seg_total);
-            }
-        } else if (it.k + 1 == it.nseg && sn < p.N && (su == 0 || two)) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-                if (sc + i < ucols) *reinterpret_cast<float4 *>(p.state_out + sglob + i) = *reinterpret_cast<const float4 *>(S + i);
-        }
-    } else {
-        // A wait ran out: the loads and MMAs in flight finish first (bounded), then the CTA leaves.
-        if (tid == 0) {
-            for (int c = loaded - 2 < 0 ? 0 : loaded - 2; c < loaded; ++c) mbar_wait(&ctl.full[c & 1], (c >> 1) & 1, kBudget);
+            if (!ok) *abort = 1;
+            // What is in flight finishes before the CTA leaves (bounded).
             mma_commit(&ctl.drain);
             mbar_wait(&ctl.drain, 0, kBudget);
-            atomicOr(p.status, kDevTimeout);
         }
+        __syncwarp();
+    } else if (warp == kLoadWarp) {
+        // ------------------------------------------------------------ TMA loads
+        if (lane == 0) {
+            const int regions = p.N > 64 ? 2 : 1;
+            int loaded = 0;
+            for (int c = 0; c < nchunks; ++c) {
+                // The stage is free when chunk c - 2 has been read out: its last MMA is then done.
+                if (c >= 2 && !(ok = wait2(kState ? ctl.s_ready : ctl.y_read, c - 2))) break;
+                uint8_t *st = sm + (c & 1) * kStage;
+                uint64_t *bar = &ctl.full[c & 1];
+                const int t = (int)(it.t0 + (int64_t)c * kL);
+                mbar_arrive_expect_tx(bar, 8192u * (regions * (kState ? 1 : 3) + 2));
+                for (int r = 0; r < regions; ++r) {
+                    tma_load_3d(st + ST_B + r * 8192, &p.tm_b, 64 * r, g, t, bar);
+                    if (!kState) {
+                        tma_load_3d(st + ST_C + r * 16384, &p.tm_c, 64 * r, g, t, bar);
+                        tma_load_3d(st + ST_C + r * 16384 + 8192, &p.tm_c, 64 * r, g, t, bar);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) tma_load_3d(st + ST_X + u * 8192, &p.tm_x, 64 * unit_tile(u), unit_head(u), t, bar);
+                loaded = c + 1;
+            }
+            // Loads still in flight land before the CTA leaves (bounded).
+            for (int c = loaded - 2 < 0 ? 0 : loaded - 2; c < loaded; ++c) mbar_wait(&ctl.full[c & 1], (c >> 1) & 1, kBudget);
+            if (!ok) *abort = 1;
+        }
+        __syncwarp();
+    } else if (warp >= kGateWarp) {
+        // ------------------------------------------------------------ gates: two tokens to a lane
+        // A decay of e^-111 is already nothing in fp32, so g is held above that: a reset then
+        // leaves the running sum small enough to keep the differences of the tokens behind it.
+        const int u = warp - kGateWarp, head = unit_head(u);
+        const float A = -expf(p.A_log[head]) * kLog2e, bias = p.dt_bias ? p.dt_bias[head] : 0.f;
+        float n0 = 0.f, n1 = 0.f;
+        auto load_dt = [&](int c) {
+            const int64_t t = it.t0 + (int64_t)c * kL + 2 * lane;
+            const __nv_bfloat16 *at = p.dt + t * p.ld_dt + head;
+            n0 = t < it.t1 ? __bfloat162float(at[0]) : 0.f;
+            n1 = t + 1 < it.t1 ? __bfloat162float(at[p.ld_dt]) : 0.f;
+        };
+        if (nchunks > 0) load_dt(0);
+        for (int c = 0; c < nchunks; ++c) {
+            const float r0 = n0, r1 = n1;
+            if (c + 1 < nchunks) load_dt(c + 1);
+            const int len = chunk_len(c);
+            const float d0 = 2 * lane < len ? ssm_step(r0, bias, p.dt_min, p.dt_max) : 0.f;
+            const float d1 = 2 * lane + 1 < len ? ssm_step(r1, bias, p.dt_min, p.dt_max) : 0.f;
+            float g0 = A * d0, g1 = A * d1;
+            g0 = g0 < -160.f ? -160.f : g0;
+            g1 = g1 < -160.f ? -160.f : g1;
+            float pre = g0 + g1, suf = pre;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float a = __shfl_up_sync(0xffffffffu, pre, o), b = __shfl_down_sync(0xffffffffu, suf, o);
+                if (lane >= o) pre += a;
+                if (lane + o < 32) suf += b;
+            }
+            float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
+            if (lane == 0) before = 0.f;
+            if (lane == 31) after = 0.f;
+            if (c >= 2 && !(ok = all(wait2(ctl.s_ready, c - 2) && (kState || wait2(ctl.y_read, c - 2))))) break;
+            Gates &G = ctl.g[c & 1][u];
+            const float c0 = before + g0, c1 = pre;
+            const float l0 = __log2f(d0), l1 = __log2f(d1);   // -inf where the step is zero: no weight
+            *reinterpret_cast<float2 *>(&G.ci[2 * lane]) = make_float2(c0, c1);
+            *reinterpret_cast<float2 *>(&G.cj[2 * lane]) = make_float2(c0 - l0, c1 - l1);
+            *reinterpret_cast<float2 *>(&G.ec[2 * lane]) = make_float2(ex2(c0), ex2(c1));
+            *reinterpret_cast<float2 *>(&G.w[2 * lane]) = make_float2(d0 * ex2(after + g1), d1 * ex2(after));
+            if (lane == 0) {
+                G.total = suf;
+                G.decay = ex2(suf);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.gates[c & 1]);
+        }
+        if (!ok) *abort = 1;
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------ S: state row sn, the 64 columns of unit su
+        const int sn = 32 * q + lane, su = half;
+        const int ucols = p.P - unit_tile(su) * 64;       // columns of this unit that exist
+        const int64_t nunits = (int64_t)p.groups * p.units;
+        const int64_t sunit = (int64_t)g * p.units + u0 + (two ? su : 0);
+        const size_t sglob = (((size_t)it.n * p.heads + unit_head(su)) * p.N + sn) * p.P + unit_tile(su) * 64;
+        const size_t sseg = ((size_t)it.slot * nunits + sunit) * p.N * 64 + (size_t)sn * 64;
+        const float *from = nullptr;
+        if (!kState && sn < p.N) from = it.nseg > 1 ? p.seg_state + sseg : p.state_in ? p.state_in + sglob : nullptr;
+        const int have = from == nullptr ? 0 : it.nseg > 1 ? 64 : ucols;
+        float S[64];
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < have) v = *reinterpret_cast<const float4 *>(from + i);
+            S[i] = v.x; S[i + 1] = v.y; S[i + 2] = v.z; S[i + 3] = v.w;
+        }
+        auto put_S = [&]() {     // bf16(S) as the next readout's operand
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4 *>(sm + O_S + su * 16384 + sw128_offset(sn, c)) =
+                    make_uint4(pack2(S[8 * c], S[8 * c + 1]), pack2(S[8 * c + 2], S[8 * c + 3]), pack2(S[8 * c + 4], S[8 * c + 5]),
+                               pack2(S[8 * c + 6], S[8 * c + 7]));
+        };
+        if (!kState) {
+            put_S();
+            arrive(&ctl.s_first);
+        }
+        float seg_total = 0.f;
+        for (int c = 0; c < nchunks; ++c) {
+            if (!kState) {
+                // (w x of the chunk before has been read: S waited for that MMA.)
+                if (!(ok = all(wait2(ctl.full, c) && wait2(ctl.gates, c)))) break;
+                make_wx(c, tid - 256, sm + O_XH);
+                arrive(&ctl.wx_ready[c & 1]);
+            }
+            if (!(ok = all(kState ? wait2(ctl.ds, c) && wait2(ctl.gates, c) : wait(&ctl.ds[0], c)))) break;
+            tc_fence_after();
+            const float dec = ctl.g[c & 1][su].decay;
+            seg_total += ctl.g[c & 1][su].total;
+            const uint32_t src = tmem + lanes + (kState && (c & 1) ? T_CS : T_DS) + 64 * su;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t r[16];
+                tmem_ld16(src + 16 * b, r);
+                tmem_ld_wait();
+                landed(r);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[16 * b + i] = fmaf(dec, S[16 * b + i], __uint_as_float(r[i]));
+            }
+            if (!kState) {
+                if (!(ok = all(wait(&ctl.cs, c)))) break;      // the readout has read the old S
+                put_S();
+            }
+            arrive(&ctl.s_ready[c & 1]);
+        }
+        if (!ok) {
+            *abort = 1;
+        } else if (sn < p.N && (su == 0 || two)) {
+            if (kState) {
+#pragma unroll
+                for (int i = 0; i < 64; i += 4)
+                    *reinterpret_cast<float4 *>(p.seg_state + sseg + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+                if (sn == 0) p.seg_decay[it.slot * nunits + sunit] = ex2(seg_total);
+            } else if (it.k + 1 == it.nseg) {
+#pragma unroll
+                for (int i = 0; i < 64; i += 4)
+                    if (i < ucols) *reinterpret_cast<float4 *>(p.state_out + sglob + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+            }
+        }
+    } else if (kState) {
+        // ------------------------------------------------------------ w x of the state-only pass, two buffers
+        for (int c = 0; c < nchunks; ++c) {
+            if (!(ok = all(wait2(ctl.full, c) && wait2(ctl.gates, c) && (c < 2 || wait2(ctl.ds, c - 2))))) break;
+            make_wx(c, tid, sm + (c & 1 ? O_S : O_XH));
+            arrive(&ctl.wx_ready[c & 1]);
+        }
+        if (!ok) *abort = 1;
+    } else {
+        // ------------------------------------------------------------ M and y
+        // Token ri of unit ru; columns 32 half .. of the scores and of the unit.
+        const int row = 32 * q + lane, ru = q >> 1, ri = row & 63;
+        const int head = unit_head(ru), col = unit_tile(ru) * 64 + 32 * half;
+        const bool live = (ru == 0 || two) && col < p.P;
+        const float D = p.D ? p.D[head] : 0.f;
+        uint4 zr[4];
+        auto load_z = [&](int c) {
+            if (p.z == nullptr || !live || ri >= chunk_len(c)) return;
+            const __nv_bfloat16 *src = p.z + (it.t0 + (int64_t)c * kL + ri) * p.ld_z + (int64_t)head * p.P + col;
+            if (p.z_wide) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (col + 8 * v < p.P) zr[v] = *reinterpret_cast<const uint4 *>(src + 8 * v);
+            } else {
+                const unsigned short *h = reinterpret_cast<const unsigned short *>(src);
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (col + 8 * v < p.P)
+                        zr[v] = make_uint4(h[8 * v] | (uint32_t)h[8 * v + 1] << 16, h[8 * v + 2] | (uint32_t)h[8 * v + 3] << 16,
+                                           h[8 * v + 4] | (uint32_t)h[8 * v + 5] << 16, h[8 * v + 6] | (uint32_t)h[8 * v + 7] << 16);
+            }
+        };
+        // Scores of chunk c, weighted: 0 above the diagonal (all of this warp's where its
+        // columns are behind its rows).
+        auto make_m = [&](int c) {
+            uint8_t *dst = sm + O_M;
+            if ((q & 1) < half) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 4 * half + v)) = make_uint4(0, 0, 0, 0);
+                return;
+            }
+            tc_fence_after();
+            const Gates &G = ctl.g[c & 1][ru];
+            const float ci = G.ci[ri];
+            uint32_t r[32];
+            tmem_ld32(tmem + T_CB + lanes + 32 * half, r);
+            tmem_ld_wait();
+            landed(r);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                uint32_t m[4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = 32 * half + 8 * v + 4 * i;
+                    const float4 cj = *reinterpret_cast<const float4 *>(&G.cj[j]);
+                    const float v0 = j <= ri ? __uint_as_float(r[8 * v + 4 * i]) * ex2(ci - cj.x) : 0.f;
+                    const float v1 = j + 1 <= ri ? __uint_as_float(r[8 * v + 4 * i + 1]) * ex2(ci - cj.y) : 0.f;
+                    const float v2 = j + 2 <= ri ? __uint_as_float(r[8 * v + 4 * i + 2]) * ex2(ci - cj.z) : 0.f;
+                    const float v3 = j + 3 <= ri ? __uint_as_float(r[8 * v + 4 * i + 3]) * ex2(ci - cj.w) : 0.f;
+                    m[2 * i] = pack2(v0, v1);
+                    m[2 * i + 1] = pack2(v2, v3);
+                }
+                *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 4 * half + v)) = make_uint4(m[0], m[1], m[2], m[3]);
+            }
+        };
+        if (nchunks > 0 && (ok = all(wait2(ctl.gates, 0) && wait(&ctl.cb, 0)))) {
+            make_m(0);
+            arrive(&ctl.m_ready);
+            load_z(0);
+        }
+        for (int c = 0; ok && c < nchunks; ++c) {
+            // (The last MMA of the chunk: what was issued before it, C S among it, is done too.)
+            if (!(ok = all(wait(&ctl.mx, c) && wait2(ctl.full, c)))) break;
+            tc_fence_after();
+            const float e = ctl.g[c & 1][ru].ec[ri];
+            const uint8_t *xt = sm + (c & 1) * kStage + ST_X + ru * 8192;
+            float acc[32];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t m[16], s[16];
+                tmem_ld16(tmem + T_MX + lanes + 64 * ru + 32 * half + 16 * b, m);
+                tmem_ld16(tmem + T_CS + lanes + 64 * ru + 32 * half + 16 * b, s);
+                tmem_ld_wait();
+                landed(m);
+                landed(s);
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const uint4 xv = *reinterpret_cast<const uint4 *>(xt + sw128_offset(ri, 4 * half + 2 * b + v));
+                    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = 8 * v + 2 * i;
+                        acc[16 * b + k] = fmaf(D, lo_f(xw[i]), fmaf(e, __uint_as_float(s[k]), __uint_as_float(m[k])));
+                        acc[16 * b + k + 1] = fmaf(D, hi_f(xw[i]), fmaf(e, __uint_as_float(s[k + 1]), __uint_as_float(m[k + 1])));
+                    }
+                }
+            }
+            arrive(&ctl.y_read[c & 1]);
+            if (c + 1 < nchunks) {
+                if (!(ok = all(wait2(ctl.gates, c + 1) && wait(&ctl.cb, c + 1)))) break;
+                make_m(c + 1);
+                arrive(&ctl.m_ready);
+            }
+            if (live && ri < chunk_len(c)) {
+                __nv_bfloat16 *dst = p.y + ((it.t0 + (int64_t)c * kL + ri) * p.heads + head) * (int64_t)p.P + col;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    if (col + 8 * v >= p.P) break;
+                    const uint32_t zw[4] = {zr[v].x, zr[v].y, zr[v].z, zr[v].w};
+                    uint32_t out[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float a = acc[8 * v + 2 * i], b = acc[8 * v + 2 * i + 1];
+                        if (p.z) {
+                            a *= silu_gate(lo_f(zw[i]));
+                            b *= silu_gate(hi_f(zw[i]));
+                        }
+                        out[i] = pack2(a, b);
+                    }
+                    *reinterpret_cast<uint4 *>(dst + 8 * v) = make_uint4(out[0], out[1], out[2], out[3]);
+                }
+            }
+            if (c + 1 < nchunks) load_z(c + 1);
+        }
+        if (!ok) *abort = 1;
     }
+    tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, kCols);
+    if (tid == 0 && ctl.abort) atomicOr(p.status, kDevTimeout);
+    if (warp == kIssueWarp) tmem_dealloc(tmem, kCols);
 }
 
 // The state entering each segment, in the place of the segment's own end state.
