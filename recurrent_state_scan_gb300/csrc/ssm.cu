@@ -5,6 +5,8 @@
 //   S   = a_t S + d_t B_t (x) x_t           S [d_state][head_dim] per (sequence, head), fp32
 //   y_t = (S^T C_t + D x_t) silu(z_t)
 // Head h reads B and C of group h / (heads / groups).
+#include <type_traits>
+
 #include "ssm_internal.cuh"
 
 namespace gdn {
@@ -20,6 +22,19 @@ constexpr int kRun = 32, kAhead = 8;
 template <typename IO, int V> struct alignas(sizeof(IO) * V) Pack {
     IO v[V];
 };
+
+// silu whose rounding to IO is silu_exact's.  For 16-bit types the fast form serves unless it is
+// within 32 fp32 steps of the border between two values (below |v| = 8 it is within 16 of the exact
+// form: 2 in the exponential, 1 in the reciprocal, 12 from the argument's rounding).
+template <typename IO> __device__ __forceinline__ float silu_for(float v) {
+    if constexpr (sizeof(IO) == 4) return silu_exact(v);
+    const float fast = silu_gate(v);
+    constexpr uint32_t kCut = std::is_same<IO, __half>::value ? 0x1fffu : 0xffffu;    // bits that the rounding drops
+    const uint32_t off = (__float_as_uint(fast) + 32u + (kCut + 1) / 2) & kCut;
+    // (f16's subnormal results round elsewhere.)
+    const bool sure = fabsf(v) < 8.f && off >= 64u && (!std::is_same<IO, __half>::value || fabsf(fast) > 0x1p-13f);
+    return sure ? fast : silu_exact(v);
+}
 
 template <typename IO, int V, int K>
 __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, int64_t run_blocks) {
@@ -131,7 +146,7 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
 #pragma unroll
                     for (int j = 0; j < K - 1; ++j) acc = fmaf(w[v][j], IoType<IO>::ld(&past[j].v[v]), acc);
                     acc = fmaf(w[v][K - 1], IoType<IO>::ld(&in[i].v[v]), acc);
-                    IoType<IO>::st(&out.v[v], p.silu ? silu_exact(acc) : acc);
+                    IoType<IO>::st(&out.v[v], p.silu ? silu_for<IO>(acc) : acc);
                 }
             }
             *reinterpret_cast<Vec *>(u + r * p.ld_u) = out;

@@ -70,7 +70,7 @@ struct TcParams {
     int64_t seqlen, rows;
     int32_t num_seqs, heads, groups, P, N;
     int32_t ptiles, units, pairs_per_group;      // units of one group
-    int32_t z_wide;                              // z rows on 16-byte boundaries
+    int32_t z_wide, y_wide;                      // z pieces on 16-byte (1) or 32-byte (2) boundaries; y on 32-byte ones
     int32_t seg_chunks;                          // chunks per time segment (0: no segments)
     float *seg_state, *seg_decay;                // [slot][unit][N][64], [slot][unit]
     int *status;
@@ -107,6 +107,56 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 __device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// Two fp32 operations in one instruction.
+struct F2 {
+    float x, y;
+};
+__device__ __forceinline__ uint64_t bits(F2 a) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ F2 pair(uint64_t v) {
+    F2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 both(float a) { return {a, a}; }
+__device__ __forceinline__ F2 words(uint32_t a, uint32_t b) { return {__uint_as_float(a), __uint_as_float(b)}; }
+__device__ __forceinline__ F2 widen(uint32_t v) { return {lo_f(v), hi_f(v)}; }
+__device__ __forceinline__ uint32_t pack2(F2 a) { return pack2(a.x, a.y); }
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// a silu(z): e^-z overflows to infinity for very negative z, whose reciprocal is the limit 0.
+__device__ __forceinline__ F2 gated(F2 a, F2 z) {
+    const F2 t = mul2(z, both(-kLog2e));
+    const F2 d = add2({ex2(t.x), ex2(t.y)}, both(1.f));
+    return mul2(mul2(a, z), {rcp(d.x), rcp(d.y)});
+}
+__device__ __forceinline__ void ld_global_v8(uint4 &lo, uint4 &hi, const void *src) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w), "=r"(hi.x), "=r"(hi.y), "=r"(hi.z), "=r"(hi.w)
+                 : "l"(src));
+}
 
 // Tensor-memory loads have landed.  The values pass through it, so that no arithmetic on them
 // can be scheduled ahead of the wait (which does not name them itself).
@@ -269,9 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float a = w * lo_f(xw[i]), b = w * hi_f(xw[i]);
-                hi[i] = pack2(a, b);
-                lo[i] = pack2(a - lo_f(hi[i]), b - hi_f(hi[i]));
+                const F2 a = mul2(both(w), widen(xw[i]));
+                hi[i] = pack2(a);
+                lo[i] = pack2(fma2(both(-1.f), widen(hi[i]), a));
             }
             *reinterpret_cast<uint4 *>(xh + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(xh + 16384 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -374,16 +424,16 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         // leaves the running sum small enough to keep the differences of the tokens behind it.
         const int u = warp - kGateWarp, head = unit_head(u);
         const float A = -expf(p.A_log[head]) * kLog2e, bias = p.dt_bias ? p.dt_bias[head] : 0.f;
-        float n0 = 0.f, n1 = 0.f;
+        unsigned short n0 = 0, n1 = 0;      // bits, widened a chunk later: nothing waits for the load here
         auto load_dt = [&](int c) {
             const int64_t t = it.t0 + (int64_t)c * kL + 2 * lane;
-            const __nv_bfloat16 *at = p.dt + t * p.ld_dt + head;
-            n0 = t < it.t1 ? __bfloat162float(at[0]) : 0.f;
-            n1 = t + 1 < it.t1 ? __bfloat162float(at[p.ld_dt]) : 0.f;
+            const unsigned short *at = reinterpret_cast<const unsigned short *>(p.dt + t * p.ld_dt + head);
+            if (t < it.t1) n0 = at[0];
+            if (t + 1 < it.t1) n1 = at[p.ld_dt];
         };
         if (nchunks > 0) load_dt(0);
         for (int c = 0; c < nchunks; ++c) {
-            const float r0 = n0, r1 = n1;
+            const float r0 = __uint_as_float((uint32_t)n0 << 16), r1 = __uint_as_float((uint32_t)n1 << 16);
             if (c + 1 < nchunks) load_dt(c + 1);
             const int len = chunk_len(c);
             const float d0 = 2 * lane < len ? ssm_step(r0, bias, p.dt_min, p.dt_max) : 0.f;
@@ -466,7 +516,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
                 tmem_ld_wait();
                 landed(r);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[16 * b + i] = fmaf(dec, S[16 * b + i], __uint_as_float(r[i]));
+                for (int i = 0; i < 16; i += 2) {
+                    const F2 v = fma2(both(dec), {S[16 * b + i], S[16 * b + i + 1]}, words(r[i], r[i + 1]));
+                    S[16 * b + i] = v.x;
+                    S[16 * b + i + 1] = v.y;
+                }
             }
             if (!kState) {
                 if (!(ok = all(wait(&ctl.cs, c)))) break;      // the readout has read the old S
@@ -507,7 +561,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         auto load_z = [&](int c) {
             if (p.z == nullptr || !live || ri >= chunk_len(c)) return;
             const __nv_bfloat16 *src = p.z + (it.t0 + (int64_t)c * kL + ri) * p.ld_z + (int64_t)head * p.P + col;
-            if (p.z_wide) {
+            if (p.z_wide == 2) {
+#pragma unroll
+                for (int v = 0; v < 4; v += 2)
+                    if (col + 8 * v < p.P) ld_global_v8(zr[v], zr[v + 1], src + 8 * v);
+            } else if (p.z_wide) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
                     if (col + 8 * v < p.P) zr[v] = *reinterpret_cast<const uint4 *>(src + 8 * v);
@@ -536,19 +594,23 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             tmem_ld32(tmem + T_CB + lanes + 32 * half, r);
             tmem_ld_wait();
             landed(r);
+            const bool diagonal = (q & 1) == half;
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 uint32_t m[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = 32 * half + 8 * v + 4 * i;
+                for (int i = 0; i < 4; i += 2) {
+                    const int at = 8 * v + 2 * i, j = 32 * half + at;
                     const float4 cj = *reinterpret_cast<const float4 *>(&G.cj[j]);
-                    const float v0 = j <= ri ? __uint_as_float(r[8 * v + 4 * i]) * ex2(ci - cj.x) : 0.f;
-                    const float v1 = j + 1 <= ri ? __uint_as_float(r[8 * v + 4 * i + 1]) * ex2(ci - cj.y) : 0.f;
-                    const float v2 = j + 2 <= ri ? __uint_as_float(r[8 * v + 4 * i + 2]) * ex2(ci - cj.z) : 0.f;
-                    const float v3 = j + 3 <= ri ? __uint_as_float(r[8 * v + 4 * i + 3]) * ex2(ci - cj.w) : 0.f;
-                    m[2 * i] = pack2(v0, v1);
-                    m[2 * i + 1] = pack2(v2, v3);
+                    const F2 e0 = fma2(both(-1.f), {cj.x, cj.y}, both(ci)), e1 = fma2(both(-1.f), {cj.z, cj.w}, both(ci));
+                    F2 v0 = mul2(words(r[at], r[at + 1]), {ex2(e0.x), ex2(e0.y)});
+                    F2 v1 = mul2(words(r[at + 2], r[at + 3]), {ex2(e1.x), ex2(e1.y)});
+                    if (diagonal) {
+                        v0 = {at <= lane ? v0.x : 0.f, at + 1 <= lane ? v0.y : 0.f};
+                        v1 = {at + 2 <= lane ? v1.x : 0.f, at + 3 <= lane ? v1.y : 0.f};
+                    }
+                    m[i] = pack2(v0);
+                    m[i + 1] = pack2(v1);
                 }
                 *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 4 * half + v)) = make_uint4(m[0], m[1], m[2], m[3]);
             }
@@ -564,15 +626,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             tc_fence_after();
             const float e = ctl.g[c & 1][ru].ec[ri];
             const uint8_t *xt = sm + (c & 1) * kStage + ST_X + ru * 8192;
-            float acc[32];
+            F2 acc[16];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                uint32_t m[16], s[16];
+                uint32_t m[16], cs[16];
                 tmem_ld16(tmem + T_MX + lanes + 64 * ru + 32 * half + 16 * b, m);
-                tmem_ld16(tmem + T_CS + lanes + 64 * ru + 32 * half + 16 * b, s);
+                tmem_ld16(tmem + T_CS + lanes + 64 * ru + 32 * half + 16 * b, cs);
                 tmem_ld_wait();
                 landed(m);
-                landed(s);
+                landed(cs);
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                     const uint4 xv = *reinterpret_cast<const uint4 *>(xt + sw128_offset(ri, 4 * half + 2 * b + v));
@@ -580,8 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int k = 8 * v + 2 * i;
-                        acc[16 * b + k] = fmaf(D, lo_f(xw[i]), fmaf(e, __uint_as_float(s[k]), __uint_as_float(m[k])));
-                        acc[16 * b + k + 1] = fmaf(D, hi_f(xw[i]), fmaf(e, __uint_as_float(s[k + 1]), __uint_as_float(m[k + 1])));
+                        acc[8 * b + 4 * v + i] =
+                            fma2(both(D), widen(xw[i]), fma2(both(e), words(cs[k], cs[k + 1]), words(m[k], m[k + 1])));
                     }
                 }
             }
@@ -595,19 +657,21 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
                 __nv_bfloat16 *dst = p.y + ((it.t0 + (int64_t)c * kL + ri) * p.heads + head) * (int64_t)p.P + col;
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    if (col + 8 * v >= p.P) break;
                     const uint32_t zw[4] = {zr[v].x, zr[v].y, zr[v].z, zr[v].w};
                     uint32_t out[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float a = acc[8 * v + 2 * i], b = acc[8 * v + 2 * i + 1];
-                        if (p.z) {
-                            a *= silu_gate(lo_f(zw[i]));
-                            b *= silu_gate(hi_f(zw[i]));
-                        }
-                        out[i] = pack2(a, b);
+                    for (int i = 0; i < 4; ++i)
+                        out[i] = pack2(p.z ? gated(acc[4 * v + i], widen(zw[i])) : acc[4 * v + i]);
+                    zr[v] = make_uint4(out[0], out[1], out[2], out[3]);
+                }
+#pragma unroll
+                for (int v = 0; v < 4; v += 2) {
+                    if (p.y_wide) {
+                        if (col + 8 * v < p.P) st_global_v8(dst + 8 * v, zr[v], zr[v + 1]);
+                    } else {
+                        if (col + 8 * v < p.P) *reinterpret_cast<uint4 *>(dst + 8 * v) = zr[v];
+                        if (col + 8 * v + 8 < p.P) *reinterpret_cast<uint4 *>(dst + 8 * v + 8) = zr[v + 1];
                     }
-                    *reinterpret_cast<uint4 *>(dst + 8 * v) = make_uint4(out[0], out[1], out[2], out[3]);
                 }
             }
             if (c + 1 < nchunks) load_z(c + 1);
@@ -631,20 +695,31 @@ __global__ void __launch_bounds__(256) ssm_segment_states(const __grid_constant_
     const int64_t first = slot_base(p, n, ls, per);
     const int head = (int)(unit / p.units) * (p.heads / p.groups) + (int)(unit % p.units) / p.ptiles;
     const int tile = (int)(unit % p.units) % p.ptiles;
-    for (int e = blockIdx.z * 256 + threadIdx.x; e < p.N * 16; e += gridDim.z * 256) {
-        const int r = e >> 4, col = 4 * (e & 15);
-        float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.state_in && tile * 64 + col < p.P)
-            S = *reinterpret_cast<const float4 *>(p.state_in + (((size_t)n * p.heads + head) * p.N + r) * p.P + tile * 64 + col);
-        for (int k = 0; k < nseg; ++k) {
-            const int64_t at = (first + k) * nunits + unit;
-            float4 *place = reinterpret_cast<float4 *>(p.seg_state + (size_t)at * p.N * 64 + 4 * (size_t)e);
-            const float4 own = *place;
-            *place = S;
-            if (k + 1 == nseg) break;
-            const float d = p.seg_decay[at];
-            S.x = fmaf(d, S.x, own.x); S.y = fmaf(d, S.y, own.y);
-            S.z = fmaf(d, S.z, own.z); S.w = fmaf(d, S.w, own.w);
+    const int e = blockIdx.z * 256 + threadIdx.x, r = e >> 4, col = 4 * (e & 15);
+    if (e >= p.N * 16) return;
+    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.state_in && tile * 64 + col < p.P)
+        S = *reinterpret_cast<const float4 *>(p.state_in + (((size_t)n * p.heads + head) * p.N + r) * p.P + tile * 64 + col);
+    const size_t step = (size_t)nunits * p.N * 64;
+    float4 *place = reinterpret_cast<float4 *>(p.seg_state + (size_t)(first * nunits + unit) * p.N * 64 + 4 * (size_t)e);
+    const float *decay = p.seg_decay + first * nunits + unit;
+    constexpr int kAhead = 8;         // segments loaded at once: the chain itself is one FMA each
+    for (int k0 = 0; k0 < nseg; k0 += kAhead) {
+        float4 own[kAhead];
+        float d[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (k0 + i + 1 < nseg) {
+                own[i] = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(place) + (size_t)(k0 + i) * step);
+                d[i] = decay[(int64_t)(k0 + i) * nunits];
+            }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (k0 + i >= nseg) break;
+            *reinterpret_cast<float4 *>(reinterpret_cast<float *>(place) + (size_t)(k0 + i) * step) = S;
+            if (k0 + i + 1 == nseg) break;
+            S.x = fmaf(d[i], S.x, own[i].x); S.y = fmaf(d[i], S.y, own[i].y);
+            S.z = fmaf(d[i], S.z, own[i].z); S.w = fmaf(d[i], S.w, own[i].w);
         }
     }
 }
@@ -733,7 +808,10 @@ cudaError_t launch_ssm_tc(const SsmParams &s, void *workspace, cudaStream_t stre
     p.ptiles = (s.head_dim + 63) / 64;
     p.units = s.heads / s.groups * p.ptiles;
     p.pairs_per_group = (p.units + 1) / 2;
-    p.z_wide = reinterpret_cast<uintptr_t>(s.z) % 16 == 0 && s.ld_z % 8 == 0;
+    const bool by16 = s.head_dim % 16 == 0;
+    p.z_wide = reinterpret_cast<uintptr_t>(s.z) % 16 != 0 || s.ld_z % 8 != 0 ? 0
+               : by16 && reinterpret_cast<uintptr_t>(s.z) % 32 == 0 && s.ld_z % 16 == 0 ? 2 : 1;
+    p.y_wide = by16 && reinterpret_cast<uintptr_t>(s.y) % 32 == 0;
     p.status = s.status;
     p.budget = __atomic_load_n(&g_wait_budget, __ATOMIC_RELAXED);
     const SegBytes b = segment_bytes(varlen, s.seqlen, s.rows, s.num_seqs, s.heads, s.groups, s.head_dim, s.d_state);
@@ -748,7 +826,7 @@ cudaError_t launch_ssm_tc(const SsmParams &s, void *workspace, cudaStream_t stre
     if (e != cudaSuccess) return e;
     if (b.seg > 0) {
         ssm_chunk_scan<true><<<(unsigned)grid, kThreads, kSmem, stream>>>(p);
-        ssm_segment_states<<<dim3((unsigned)s.num_seqs, (unsigned)(s.groups * p.units), 2), 256, 0, stream>>>(p);
+        ssm_segment_states<<<dim3((unsigned)s.num_seqs, (unsigned)(s.groups * p.units), (unsigned)((s.d_state + 15) / 16)), 256, 0, stream>>>(p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
