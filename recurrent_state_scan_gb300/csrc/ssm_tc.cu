@@ -42,23 +42,25 @@ constexpr int kThreads = 640;
 constexpr long long kBudget = 4000000000LL;  // cycles (~2 s) before a wait gives up
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Shared memory (1024-byte aligned): two stages of what TMA brings, then the operands the
-// threads make.  All tiles are stacks of 128-byte-swizzled rows of 64 bf16.
-constexpr int ST_C = 0;                      // 2 regions of 64 state columns x 128 rows: C twice
-constexpr int ST_B = 32768;                  // 2 regions x 64 rows
-constexpr int ST_X = 49152;                  // 2 units x 64 rows
-constexpr int kStage = 65536;
-constexpr int O_M = 2 * kStage;              // 128 rows: unit 0's M, unit 1's
-constexpr int O_XH = O_M + 16384;            // w x, high part: 2 units x 64 rows
+// Shared memory (1024-byte aligned): stages of what TMA brings, then the operands the threads
+// make.  All tiles are stacks of 128-byte-swizzled rows of 64 bf16.  y takes z's place, for a
+// TMA store.  The state-only pass has no C and twice the stages.
+constexpr int ST_B = 0;                      // 2 regions of 64 state columns x 64 rows
+constexpr int ST_X = 16384;                  // 2 units x 64 rows
+constexpr int ST_C = 32768;                  // 2 regions x 128 rows: C twice
+template <bool kState> constexpr int kStageBytes = kState ? 32768 : 65536;
+template <bool kState> constexpr int kStages = kState ? 4 : 2;
+constexpr int O_Z = 131072;                  // z, then y: 2 units x 64 rows
+constexpr int O_XH = O_Z + 16384;            // w x, high part: 2 units x 64 rows
 constexpr int O_XL = O_XH + 16384;           // low part
 constexpr int O_S = O_XL + 16384;            // bf16(S): 2 units x 128 state rows
 constexpr int kSmem = O_S + 32768 + 1024;
 
-// Tensor memory columns.
-constexpr uint32_t T_CB = 0, T_CS = 64, T_DS = 192, T_MX = 320, kCols = 512;
+// Tensor memory columns; M is the A operand of the last MMA, bf16 pairs.
+constexpr uint32_t T_CB = 0, T_CS = 64, T_DS = 192, T_MX = 320, T_M = 448, kCols = 512;
 
 struct TcParams {
-    CUtensorMap tm_x, tm_b, tm_c;
+    CUtensorMap tm_x, tm_b, tm_c, tm_z, tm_y;
     const __nv_bfloat16 *dt, *z;
     __nv_bfloat16 *y;
     int64_t ld_dt, ld_z;
@@ -70,7 +72,7 @@ struct TcParams {
     int64_t seqlen, rows;
     int32_t num_seqs, heads, groups, P, N;
     int32_t ptiles, units, pairs_per_group;      // units of one group
-    int32_t z_wide, y_wide;                      // z pieces on 16-byte (1) or 32-byte (2) boundaries; y on 32-byte ones
+    int32_t z_tma;                               // z comes by TMA (its rows are on 16-byte boundaries)
     int32_t seg_chunks;                          // chunks per time segment (0: no segments)
     float *seg_state, *seg_decay;                // [slot][unit][N][64], [slot][unit]
     int *status;
@@ -87,9 +89,10 @@ struct alignas(16) Gates {       // read in float2 and float4
 };
 
 struct Ctl {
-    // Barriers: pairs by chunk parity where a waiter can be a chunk behind.
-    uint64_t full[2], gates[2], y_read[2], s_ready[2], wx_ready[2], ds[2];
-    uint64_t cb, cs, mx, m_ready, s_first, drain;
+    // Barriers: pairs by chunk parity where a waiter can be a chunk behind (`full` and s_ready
+    // by stage).
+    uint64_t full[4], gates[2], y_read[2], s_ready[4], wx_ready[2], ds[2];
+    uint64_t y_done, full_z, cb, cs, mx, m_ready, s_first, drain;
     uint32_t tmem;
     int32_t abort;   // a wait ran out
     Gates g[2][2];   // [chunk parity][unit]
@@ -146,16 +149,12 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// a silu(z): e^-z overflows to infinity for very negative z, whose reciprocal is the limit 0.
+// a silu(z) for two values with one reciprocal: 1 / d0 = d1 / (d0 d1).  e^-z stops at 2^60, so that
+// the product stays finite (silu is then 2^-60 z, where it is smaller still).
 __device__ __forceinline__ F2 gated(F2 a, F2 z) {
     const F2 t = mul2(z, both(-kLog2e));
-    const F2 d = add2({ex2(t.x), ex2(t.y)}, both(1.f));
-    return mul2(mul2(a, z), {rcp(d.x), rcp(d.y)});
-}
-__device__ __forceinline__ void ld_global_v8(uint4 &lo, uint4 &hi, const void *src) {
-    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w), "=r"(hi.x), "=r"(hi.y), "=r"(hi.z), "=r"(hi.w)
-                 : "l"(src));
+    const F2 d = add2({ex2(fminf(t.x, 60.f)), ex2(fminf(t.y, 60.f))}, both(1.f));
+    return mul2(mul2(mul2(a, z), both(rcp(d.x * d.y))), {d.y, d.x});
 }
 
 // Tensor-memory loads have landed.  The values pass through it, so that no arithmetic on them
@@ -167,22 +166,38 @@ template <int N> __device__ __forceinline__ void landed(uint32_t (&r)[N]) {
 
 // A bounded wait that gives up when another thread has.  Under a short budget
 // (gdn_set_wait_budget) a wait that took longer has run out even where a blocking try saw it end.
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int32_t *abort, long long budget) {
-    const bool brief = budget < 100000;
-    if (!brief && mbar_try_wait(bar, parity)) return true;
+// (Out of line: with it inlined at every wait the roles' loops together outgrew the instruction
+// cache, and a chunk took 7,700 cycles instead of SPEED.)
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int32_t *abort, long long budget) {
     const long long t0 = clock64();
-    while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+    while (!mbar_try_wait(bar, parity)) {
         if (*abort) return false;
         if (clock64() - t0 > budget) {
             *abort = 1;
             return false;
         }
     }
-    if (brief && clock64() - t0 > budget) {
+    if (budget < 100000 && clock64() - t0 > budget) {
         *abort = 1;
         return false;
     }
     return true;
+}
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int32_t *abort, long long budget) {
+    if (budget >= 100000 && mbar_try_wait(bar, parity)) return true;
+    return wait_long(bar, parity, abort, budget);
+}
+
+// Eight z values off 16 bytes (which TMA cannot take).
+__device__ __noinline__ uint4 load_unaligned(const __nv_bfloat16 *src) {
+    const unsigned short *h = reinterpret_cast<const unsigned short *>(src);
+    return make_uint4(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16, h[4] | (uint32_t)h[5] << 16,
+                      h[6] | (uint32_t)h[7] << 16);
+}
+
+// ssm_step of a bf16 value, out of line as well.
+__device__ __noinline__ float step_of(uint32_t bits, float bias, float lo, float hi) {
+    return ssm_step(__uint_as_float(bits << 16), bias, lo, hi);
 }
 
 // One work item: the chunks [t0, t1) of segment k of sequence n.
@@ -229,10 +244,10 @@ __device__ __forceinline__ Item item_of(const TcParams &p, int64_t s) {
 }
 
 // The roles of a CTA's warps, each with its own pace; mbarriers carry the order.
-//   0-7    y: M from the scores, and the readout (row 32 (warp & 3) + lane, 32 columns of it)
-//   8-15   S: w x, and the state (its row n, the 64 columns of one unit, in registers)
-//   16     issues the MMAs     17  issues the TMA loads     18, 19  the gates of unit 0, 1
-constexpr int kIssueWarp = 16, kLoadWarp = 17, kGateWarp = 18;
+//   0-7    y: M from the scores, and the readout (row 32 (warp % 4) + lane, 32 columns of it)
+//   8-15   S: the state (its row n, the 64 columns of one unit, in registers), and w x
+//   16     issues the MMAs     17  issues the TMA copies     18, 19  the gates of unit 0, 1
+constexpr int kSWarp = 8, kIssueWarp = 16, kLoadWarp = 17, kGateWarp = 18;
 
 // kState: the state-only pass of a segment (no scores, no y; warps 0-7 make w x there).
 template <bool kState>
@@ -264,14 +279,18 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         tmem_relinquish();
     }
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&ctl.full[i], 1);
+            mbar_init(&ctl.s_ready[i], 8);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl.gates[i], 2);
             mbar_init(&ctl.y_read[i], 8);
-            mbar_init(&ctl.s_ready[i], 8);
             mbar_init(&ctl.wx_ready[i], 8);
             mbar_init(&ctl.ds[i], 1);
         }
+        mbar_init(&ctl.y_done, 8);
+        mbar_init(&ctl.full_z, 1);
         mbar_init(&ctl.cb, 1);
         mbar_init(&ctl.cs, 1);
         mbar_init(&ctl.mx, 1);
@@ -290,31 +309,38 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
     // A phase of a barrier that completes once per chunk, and of one of a pair by chunk parity.
     auto wait = [&](uint64_t *bar, int c) { return wait_for(bar, c & 1, abort, budget); };
     auto wait2 = [&](uint64_t *bar, int c) { return wait_for(bar + (c & 1), (c >> 1) & 1, abort, budget); };
+    constexpr int NS = kStages<kState>;
+    auto wait_st = [&](uint64_t *bar, int c) { return wait_for(bar + (c & (NS - 1)), (c / NS) & 1, abort, budget); };
+    auto stage = [&](int c) { return sm + (c & (NS - 1)) * kStageBytes<kState>; };
     auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
-    // This warp's shared-memory writes are done (for the tensor cores too): one arrival.
-    auto arrive = [&](uint64_t *bar) {
-        fence_async_smem();
+    // This warp's tensor-memory accesses are done (and, with `smem`, its shared-memory writes, for
+    // the tensor cores and TMA too): one arrival.
+    auto arrive = [&](uint64_t *bar, bool smem) {
+        if (smem) fence_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
-    // w x of chunk c by 256 threads (`who` 0-255), split into two bf16 terms, at buffer `xh`.
     // Rows behind the sequence are another's: as operands they have to be zero.
-    auto make_wx = [&](int c, int who, uint8_t *xh) {
-        uint8_t *st = sm + (c & 1) * kStage;
+    auto clear_rows = [&](int c, int who) {
+        uint8_t *st = stage(c);
         const int len = chunk_len(c);
-        if (len < kL)
-            for (int e = who; e < (kL - len) * 32; e += 256) {
-                const int r = len + (e >> 5), k = e & 31, tile = k >> 3;   // B regions 0, 1, units 0, 1
-                *reinterpret_cast<uint4 *>(st + (tile < 2 ? ST_B + tile * 8192 : ST_X + (tile - 2) * 8192) + sw128_offset(r, k & 7)) =
-                    make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
+        for (int e = who; e < (kL - len) * 32; e += 256) {
+            const int r = len + (e >> 5), k = e & 31;       // B regions 0, 1, units 0, 1
+            *reinterpret_cast<uint4 *>(st + (k >> 3) * 8192 + sw128_offset(r, k & 7)) = make_uint4(0, 0, 0, 0);
+        }
+    };
+    // w x of chunk c by 256 threads, split into two bf16 terms, at buffer `xh`.
+    auto make_wx = [&](int c, int who, uint8_t *xh) {
+        const uint8_t *xt = stage(c) + ST_X;
+        const int len = chunk_len(c);
+        if (len < kL) clear_rows(c, who);
+#pragma unroll 1
         for (int v = 0; v < 4; ++v) {
             const int u = v >> 1, j = (who >> 3) + 32 * (v & 1);
             const uint32_t at = u * 8192 + sw128_offset(j, who & 7);
             const float w = j < len ? ctl.g[c & 1][u].w[j] : 0.f;
-            const uint4 xv = j < len ? *reinterpret_cast<const uint4 *>(st + ST_X + at) : make_uint4(0, 0, 0, 0);
+            const uint4 xv = j < len ? *reinterpret_cast<const uint4 *>(xt + at) : make_uint4(0, 0, 0, 0);
             const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -328,13 +354,14 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         }
     };
 
-    const int q = warp & 3, half = (warp >> 2) & 1;   // TMEM lane quarter; column half
+    const int q = warp & 3, half = (warp >> 2) & 1;   // TMEM lane quarter, column half
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
     bool ok = true;
+
 
     if (warp == kIssueWarp) {
         // ------------------------------------------------------------ MMAs
@@ -349,17 +376,18 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             const uint64_t dC = sw128_desc(base + ST_C, 16, 1024), dBk = sw128_desc(base + ST_B, 16, 1024),
                            dS = sw128_desc(base + O_S, 16384, 1024), dBm = sw128_desc(base + ST_B, 8192, 1024),
                            dXH = sw128_desc(base + O_XH, 8192, 1024), dX = sw128_desc(base + ST_X, 8192, 1024),
-                           dM = sw128_desc(base + O_M, 16, 1024), dXH1 = sw128_desc(base + O_S, 8192, 1024);
+                           dXH1 = sw128_desc(base + O_S, 8192, 1024);
             auto issue_cb = [&](int c) {
-                const uint64_t st = (uint64_t)(c & 1) * (kStage >> 4);
+                const uint64_t st = (uint64_t)(c & (NS - 1)) * (kStageBytes<kState> >> 4);
                 for (int k = 0; k < ksteps; ++k)
                     mma_f16(tmem + T_CB, dC + st + (k >> 2) * 1024 + (k & 3) * 2, dBk + st + (k >> 2) * 512 + (k & 3) * 2, kIdCB, k > 0);
                 mma_commit(&ctl.cb);
             };
-            if (!kState && nchunks > 0 && (ok = wait2(ctl.full, 0))) issue_cb(0);
+            if (!kState && nchunks > 0 && (ok = wait_st(ctl.full, 0))) issue_cb(0);
             for (int c = 0; ok && c < nchunks; ++c) {
-                const uint64_t st = (uint64_t)(c & 1) * (kStage >> 4);
-                if (!(ok = wait2(ctl.wx_ready, c) && wait2(ctl.full, c) && (!kState || c < 2 || wait2(ctl.s_ready, c - 2)))) break;
+                const uint64_t st = (uint64_t)(c & (NS - 1)) * (kStageBytes<kState> >> 4);
+                // (w x ready: the S warps have also read the accumulators of the chunk before.)
+                if (!(ok = wait2(ctl.wx_ready, c) && wait_st(ctl.full, c) && (!kState || c < 2 || wait_st(ctl.s_ready, c - 2)))) break;
                 tc_fence_after();
                 const uint64_t xh = kState && (c & 1) ? dXH1 : dXH;
                 const uint32_t dst = tmem + (kState && (c & 1) ? T_CS : T_DS);
@@ -369,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
                 mma_commit(&ctl.ds[kState ? c & 1 : 0]);
                 if (kState) continue;
                 // C S, once S is in place and the accumulators of the chunk before are read.
-                if (!(ok = c == 0 ? wait(&ctl.s_first, 0) : wait2(ctl.s_ready, c - 1) && wait2(ctl.y_read, c - 1))) break;
+                if (!(ok = c == 0 ? wait(&ctl.s_first, 0) : wait_st(ctl.s_ready, c - 1) && wait2(ctl.y_read, c - 1))) break;
                 tc_fence_after();
                 for (int k = 0; k < ksteps; ++k)
                     mma_f16(tmem + T_CS, dC + st + (k >> 2) * 1024 + (k & 3) * 2, dS + k * 128, kIdCS, k > 0);
@@ -377,10 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
                 if (!(ok = wait(&ctl.m_ready, c))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_f16(tmem + T_MX, dM + k * 2, dX + st + k * 128, kIdCS, k > 0);
+                for (int k = 0; k < 4; ++k) mma_f16_ts(tmem + T_MX, tmem + T_M + 8 * k, dX + st + k * 128, kIdCS, k > 0);
                 mma_commit(&ctl.mx);
                 if (c + 1 < nchunks) {
-                    if (!(ok = wait2(ctl.full, c + 1))) break;
+                    if (!(ok = wait_st(ctl.full, c + 1))) break;
                     issue_cb(c + 1);
                 }
             }
@@ -394,27 +422,59 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         // ------------------------------------------------------------ TMA loads
         if (lane == 0) {
             const int regions = p.N > 64 ? 2 : 1;
-            int loaded = 0;
-            for (int c = 0; c < nchunks; ++c) {
-                // The stage is free when chunk c - 2 has been read out: its last MMA is then done.
-                if (c >= 2 && !(ok = wait2(kState ? ctl.s_ready : ctl.y_read, c - 2))) break;
-                uint8_t *st = sm + (c & 1) * kStage;
-                uint64_t *bar = &ctl.full[c & 1];
-                const int t = (int)(it.t0 + (int64_t)c * kL);
-                mbar_arrive_expect_tx(bar, 8192u * (regions * (kState ? 1 : 3) + 2));
-                for (int r = 0; r < regions; ++r) {
-                    tma_load_3d(st + ST_B + r * 8192, &p.tm_b, 64 * r, g, t, bar);
-                    if (!kState) {
-                        tma_load_3d(st + ST_C + r * 16384, &p.tm_c, 64 * r, g, t, bar);
-                        tma_load_3d(st + ST_C + r * 16384 + 8192, &p.tm_c, 64 * r, g, t, bar);
-                    }
+            int loaded = 0, loaded_z = 0;
+            const int tile_u[2] = {64 * unit_tile(0), 64 * unit_tile(1)}, head_u[2] = {unit_head(0), unit_head(1)};
+            auto load_z = [&](int c) {
+                mbar_arrive_expect_tx(&ctl.full_z, 16384);
+                for (int u = 0; u < 2; ++u)
+                    tma_load_3d(sm + O_Z + u * 8192, &p.tm_z, tile_u[u], head_u[u], (int)(it.t0 + (int64_t)c * kL), &ctl.full_z);
+                loaded_z = c + 1;
+            };
+            // y of chunk c has taken z's place: out with it, then the next z in.  (A sequence's last
+            // rows, where they do not fill the chunk, are stored by their threads.)
+            auto store_y = [&](int c) {
+                if (!(ok = wait(&ctl.y_done, c))) return;
+                if (chunk_len(c) == kL) {
+                    for (int u = 0; u < 1 + two; ++u)
+                        tma_store_3d(&p.tm_y, sm + O_Z + u * 8192, tile_u[u], head_u[u], (int)(it.t0 + (int64_t)c * kL));
+                    bulk_commit();
+                    bulk_wait_read();
                 }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) tma_load_3d(st + ST_X + u * 8192, &p.tm_x, 64 * unit_tile(u), unit_head(u), t, bar);
-                loaded = c + 1;
+                if (c + 1 < nchunks) {
+                    if (p.z_tma) load_z(c + 1);
+                    else mbar_arrive(&ctl.full_z);     // its place is free
+                }
+            };
+            if (!kState && nchunks > 0) {
+                if (p.z_tma) load_z(0);
+                else mbar_arrive(&ctl.full_z);
             }
-            // Loads still in flight land before the CTA leaves (bounded).
-            for (int c = loaded - 2 < 0 ? 0 : loaded - 2; c < loaded; ++c) mbar_wait(&ctl.full[c & 1], (c >> 1) & 1, kBudget);
+            for (int c = 0; ok && c < nchunks + (kState ? 0 : NS); ++c) {
+                if (c < nchunks) {
+                    // The stage is free when the last MMAs of the chunk in it are done: its S has been
+                    // taken, and its y read out.
+                    if (c >= NS && !(ok = wait_st(ctl.s_ready, c - NS) && (kState || wait2(ctl.y_read, c - NS)))) break;
+                    uint8_t *st = stage(c);
+                    uint64_t *bar = &ctl.full[c & (NS - 1)];
+                    const int t = (int)(it.t0 + (int64_t)c * kL);
+                    mbar_arrive_expect_tx(bar, 8192u * (kState ? regions + 2 : 3 * regions + 2));
+#pragma unroll 1
+                    for (int r = 0; r < regions; ++r) {
+                        tma_load_3d(st + ST_B + r * 8192, &p.tm_b, 64 * r, g, t, bar);
+                        if (!kState) {
+                            tma_load_3d(st + ST_C + r * 16384, &p.tm_c, 64 * r, g, t, bar);
+                            tma_load_3d(st + ST_C + r * 16384 + 8192, &p.tm_c, 64 * r, g, t, bar);
+                        }
+                    }
+                    for (int u = 0; u < 2; ++u) tma_load_3d(st + ST_X + u * 8192, &p.tm_x, tile_u[u], head_u[u], t, bar);
+                    loaded = c + 1;
+                }
+                if (!kState && c >= NS) store_y(c - NS);
+            }
+            // Copies still in flight finish before the CTA leaves (bounded).
+            for (int c = loaded - NS < 0 ? 0 : loaded - NS; c < loaded; ++c) mbar_wait(&ctl.full[c & (NS - 1)], (c / NS) & 1, kBudget);
+            if (loaded_z > 0) mbar_wait(&ctl.full_z, (loaded_z - 1) & 1, kBudget);
+            bulk_wait_all();
             if (!ok) *abort = 1;
         }
         __syncwarp();
@@ -433,11 +493,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         };
         if (nchunks > 0) load_dt(0);
         for (int c = 0; c < nchunks; ++c) {
-            const float r0 = __uint_as_float((uint32_t)n0 << 16), r1 = __uint_as_float((uint32_t)n1 << 16);
+            const uint32_t r0 = n0, r1 = n1;
             if (c + 1 < nchunks) load_dt(c + 1);
             const int len = chunk_len(c);
-            const float d0 = 2 * lane < len ? ssm_step(r0, bias, p.dt_min, p.dt_max) : 0.f;
-            const float d1 = 2 * lane + 1 < len ? ssm_step(r1, bias, p.dt_min, p.dt_max) : 0.f;
+            const float d0 = 2 * lane < len ? step_of(r0, bias, p.dt_min, p.dt_max) : 0.f;
+            const float d1 = 2 * lane + 1 < len ? step_of(r1, bias, p.dt_min, p.dt_max) : 0.f;
             float g0 = A * d0, g1 = A * d1;
             g0 = g0 < -160.f ? -160.f : g0;
             g1 = g1 < -160.f ? -160.f : g1;
@@ -451,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
             if (lane == 0) before = 0.f;
             if (lane == 31) after = 0.f;
-            if (c >= 2 && !(ok = all(wait2(ctl.s_ready, c - 2) && (kState || wait2(ctl.y_read, c - 2))))) break;
+            if (c >= 2 && !(ok = all(wait_st(ctl.s_ready, c - 2) && (kState || wait2(ctl.y_read, c - 2))))) break;
             Gates &G = ctl.g[c & 1][u];
             const float c0 = before + g0, c1 = pre;
             const float l0 = __log2f(d0), l1 = __log2f(d1);   // -inf where the step is zero: no weight
@@ -467,9 +527,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             if (lane == 0) mbar_arrive(&ctl.gates[c & 1]);
         }
         if (!ok) *abort = 1;
-    } else if (warp >= 8) {
+    } else if (warp >= kSWarp) {
+
         // ------------------------------------------------------------ S: state row sn, the 64 columns of unit su
-        const int sn = 32 * q + lane, su = half;
+        const int sn = 32 * q + lane, su = (warp >> 2) & 1;
         const int ucols = p.P - unit_tile(su) * 64;       // columns of this unit that exist
         const int64_t nunits = (int64_t)p.groups * p.units;
         const int64_t sunit = (int64_t)g * p.units + u0 + (two ? su : 0);
@@ -494,17 +555,17 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         };
         if (!kState) {
             put_S();
-            arrive(&ctl.s_first);
+            arrive(&ctl.s_first, true);
         }
         float seg_total = 0.f;
-        for (int c = 0; c < nchunks; ++c) {
-            if (!kState) {
-                // (w x of the chunk before has been read: S waited for that MMA.)
-                if (!(ok = all(wait2(ctl.full, c) && wait2(ctl.gates, c)))) break;
-                make_wx(c, tid - 256, sm + O_XH);
-                arrive(&ctl.wx_ready[c & 1]);
-            }
-            if (!(ok = all(kState ? wait2(ctl.ds, c) && wait2(ctl.gates, c) : wait(&ctl.ds[0], c)))) break;
+        auto next_wx = [&](int c) {      // (the state's MMA of the chunk before has left its buffer)
+            if (!(ok = all(wait_st(ctl.full, c) && wait2(ctl.gates, c)))) return;
+            make_wx(c, tid - 32 * kSWarp, sm + O_XH);
+            arrive(&ctl.wx_ready[c & 1], true);
+        };
+        if (!kState && nchunks > 0) next_wx(0);
+        for (int c = 0; ok && c < nchunks; ++c) {
+            if (!(ok = all((kState ? wait2(ctl.ds, c) : wait(&ctl.ds[0], c)) && wait2(ctl.gates, c)))) break;
             tc_fence_after();
             const float dec = ctl.g[c & 1][su].decay;
             seg_total += ctl.g[c & 1][su].total;
@@ -523,10 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
                 }
             }
             if (!kState) {
-                if (!(ok = all(wait(&ctl.cs, c)))) break;      // the readout has read the old S
+                if (c + 1 < nchunks) next_wx(c + 1);
+                if (!ok || !(ok = all(wait(&ctl.cs, c)))) break;      // the readout has read the old S
                 put_S();
             }
-            arrive(&ctl.s_ready[c & 1]);
+            arrive(&ctl.s_ready[c & (NS - 1)], !kState);
         }
         if (!ok) {
             *abort = 1;
@@ -544,10 +606,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         }
     } else if (kState) {
         // ------------------------------------------------------------ w x of the state-only pass, two buffers
+
         for (int c = 0; c < nchunks; ++c) {
-            if (!(ok = all(wait2(ctl.full, c) && wait2(ctl.gates, c) && (c < 2 || wait2(ctl.ds, c - 2))))) break;
+            if (!(ok = all(wait_st(ctl.full, c) && wait2(ctl.gates, c) && (c < 2 || wait2(ctl.ds, c - 2))))) break;
             make_wx(c, tid, sm + (c & 1 ? O_S : O_XH));
-            arrive(&ctl.wx_ready[c & 1]);
+            arrive(&ctl.wx_ready[c & 1], true);
         }
         if (!ok) *abort = 1;
     } else {
@@ -557,124 +620,95 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         const int head = unit_head(ru), col = unit_tile(ru) * 64 + 32 * half;
         const bool live = (ru == 0 || two) && col < p.P;
         const float D = p.D ? p.D[head] : 0.f;
-        uint4 zr[4];
-        auto load_z = [&](int c) {
-            if (p.z == nullptr || !live || ri >= chunk_len(c)) return;
-            const __nv_bfloat16 *src = p.z + (it.t0 + (int64_t)c * kL + ri) * p.ld_z + (int64_t)head * p.P + col;
-            if (p.z_wide == 2) {
-#pragma unroll
-                for (int v = 0; v < 4; v += 2)
-                    if (col + 8 * v < p.P) ld_global_v8(zr[v], zr[v + 1], src + 8 * v);
-            } else if (p.z_wide) {
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    if (col + 8 * v < p.P) zr[v] = *reinterpret_cast<const uint4 *>(src + 8 * v);
-            } else {
-                const unsigned short *h = reinterpret_cast<const unsigned short *>(src);
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    if (col + 8 * v < p.P)
-                        zr[v] = make_uint4(h[8 * v] | (uint32_t)h[8 * v + 1] << 16, h[8 * v + 2] | (uint32_t)h[8 * v + 3] << 16,
-                                           h[8 * v + 4] | (uint32_t)h[8 * v + 5] << 16, h[8 * v + 6] | (uint32_t)h[8 * v + 7] << 16);
-            }
-        };
         // Scores of chunk c, weighted: 0 above the diagonal (all of this warp's where its
         // columns are behind its rows).
         auto make_m = [&](int c) {
-            uint8_t *dst = sm + O_M;
-            if ((q & 1) < half) {
-#pragma unroll
-                for (int v = 0; v < 4; ++v) *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 4 * half + v)) = make_uint4(0, 0, 0, 0);
-                return;
-            }
-            tc_fence_after();
             const Gates &G = ctl.g[c & 1][ru];
             const float ci = G.ci[ri];
-            uint32_t r[32];
-            tmem_ld32(tmem + T_CB + lanes + 32 * half, r);
-            tmem_ld_wait();
-            landed(r);
-            const bool diagonal = (q & 1) == half;
+            tc_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                const int j0 = 32 * half + 16 * b;
+                uint32_t m[8];
+                if (j0 > 32 * (q & 1) + 31) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                uint32_t m[4];
+                    for (int i = 0; i < 8; ++i) m[i] = 0;
+                } else {
+                    uint32_t r[16];
+                    tmem_ld16(tmem + T_CB + lanes + j0, r);
+                    tmem_ld_wait();
+                    landed(r);
 #pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const int at = 8 * v + 2 * i, j = 32 * half + at;
-                    const float4 cj = *reinterpret_cast<const float4 *>(&G.cj[j]);
-                    const F2 e0 = fma2(both(-1.f), {cj.x, cj.y}, both(ci)), e1 = fma2(both(-1.f), {cj.z, cj.w}, both(ci));
-                    F2 v0 = mul2(words(r[at], r[at + 1]), {ex2(e0.x), ex2(e0.y)});
-                    F2 v1 = mul2(words(r[at + 2], r[at + 3]), {ex2(e1.x), ex2(e1.y)});
-                    if (diagonal) {
-                        v0 = {at <= lane ? v0.x : 0.f, at + 1 <= lane ? v0.y : 0.f};
-                        v1 = {at + 2 <= lane ? v1.x : 0.f, at + 3 <= lane ? v1.y : 0.f};
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 cj = *reinterpret_cast<const float4 *>(&G.cj[j0 + i]);
+                        const F2 e0 = fma2(both(-1.f), {cj.x, cj.y}, both(ci)), e1 = fma2(both(-1.f), {cj.z, cj.w}, both(ci));
+                        F2 v0 = mul2(words(r[i], r[i + 1]), {ex2(e0.x), ex2(e0.y)});
+                        F2 v1 = mul2(words(r[i + 2], r[i + 3]), {ex2(e1.x), ex2(e1.y)});
+                        const int past = j0 + i - ri;
+                        v0 = {past <= 0 ? v0.x : 0.f, past + 1 <= 0 ? v0.y : 0.f};
+                        v1 = {past + 2 <= 0 ? v1.x : 0.f, past + 3 <= 0 ? v1.y : 0.f};
+                        m[i / 2] = pack2(v0);
+                        m[i / 2 + 1] = pack2(v1);
                     }
-                    m[i] = pack2(v0);
-                    m[i + 1] = pack2(v1);
                 }
-                *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 4 * half + v)) = make_uint4(m[0], m[1], m[2], m[3]);
+                tmem_st8(tmem + T_M + lanes + j0 / 2, m);
             }
+            tmem_st_wait();
         };
-        if (nchunks > 0 && (ok = all(wait2(ctl.gates, 0) && wait(&ctl.cb, 0)))) {
-            make_m(0);
-            arrive(&ctl.m_ready);
-            load_z(0);
-        }
+        auto next_m = [&](int c) {
+            if (!(ok = all(wait2(ctl.gates, c) && wait(&ctl.cb, c)))) return;
+            make_m(c);
+            arrive(&ctl.m_ready, false);
+        };
+        if (nchunks > 0) next_m(0);
         for (int c = 0; ok && c < nchunks; ++c) {
             // (The last MMA of the chunk: what was issued before it, C S among it, is done too.)
-            if (!(ok = all(wait(&ctl.mx, c) && wait2(ctl.full, c)))) break;
+            if (!(ok = all(wait(&ctl.mx, c) && wait_st(ctl.full, c) && wait(&ctl.full_z, c)))) break;
             tc_fence_after();
+            const uint8_t *xt = stage(c) + ST_X + ru * 8192;
+            uint8_t *zt = sm + O_Z + ru * 8192;
             const float e = ctl.g[c & 1][ru].ec[ri];
-            const uint8_t *xt = sm + (c & 1) * kStage + ST_X + ru * 8192;
-            F2 acc[16];
-#pragma unroll
+            const int len = chunk_len(c);
+            __nv_bfloat16 *dst = p.y + ((it.t0 + (int64_t)c * kL + ri) * p.heads + head) * (int64_t)p.P + col;
+#pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 uint32_t m[16], cs[16];
-                tmem_ld16(tmem + T_MX + lanes + 64 * ru + 32 * half + 16 * b, m);
-                tmem_ld16(tmem + T_CS + lanes + 64 * ru + 32 * half + 16 * b, cs);
+                const uint32_t at = lanes + 64 * ru + 32 * half + 16 * b;
+                tmem_ld16(tmem + T_MX + at, m);
+                tmem_ld16(tmem + T_CS + at, cs);
                 tmem_ld_wait();
                 landed(m);
                 landed(cs);
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
-                    const uint4 xv = *reinterpret_cast<const uint4 *>(xt + sw128_offset(ri, 4 * half + 2 * b + v));
-                    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                    const uint32_t piece = sw128_offset(ri, 4 * half + 2 * b + v);
+                    const uint4 xv = *reinterpret_cast<const uint4 *>(xt + piece);
+                    uint4 *place = reinterpret_cast<uint4 *>(zt + piece);
+                    const int pc = 16 * b + 8 * v;
+                    uint4 zv = make_uint4(0, 0, 0, 0);
+                    if (p.z != nullptr) {
+                        if (p.z_tma) zv = *place;
+                        else if (live && ri < len && col + pc < p.P)
+                            zv = load_unaligned(p.z + (it.t0 + (int64_t)c * kL + ri) * p.ld_z + (int64_t)head * p.P + col + pc);
+                    }
+                    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, zw[4] = {zv.x, zv.y, zv.z, zv.w};
+                    uint32_t out[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int k = 8 * v + 2 * i;
-                        acc[8 * b + 4 * v + i] =
-                            fma2(both(D), widen(xw[i]), fma2(both(e), words(cs[k], cs[k + 1]), words(m[k], m[k + 1])));
+                        F2 a = fma2(both(D), widen(xw[i]), fma2(both(e), words(cs[k], cs[k + 1]), words(m[k], m[k + 1])));
+                        if (p.z != nullptr) a = gated(a, widen(zw[i]));
+                        out[i] = pack2(a);
                     }
+                    const uint4 o = make_uint4(out[0], out[1], out[2], out[3]);
+                    // A whole chunk's y goes out by TMA, from z's place.
+                    if (len == kL) *place = o;
+                    else if (live && ri < len && col + pc < p.P) *reinterpret_cast<uint4 *>(dst + pc) = o;
                 }
             }
-            arrive(&ctl.y_read[c & 1]);
-            if (c + 1 < nchunks) {
-                if (!(ok = all(wait2(ctl.gates, c + 1) && wait(&ctl.cb, c + 1)))) break;
-                make_m(c + 1);
-                arrive(&ctl.m_ready);
-            }
-            if (live && ri < chunk_len(c)) {
-                __nv_bfloat16 *dst = p.y + ((it.t0 + (int64_t)c * kL + ri) * p.heads + head) * (int64_t)p.P + col;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const uint32_t zw[4] = {zr[v].x, zr[v].y, zr[v].z, zr[v].w};
-                    uint32_t out[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        out[i] = pack2(p.z ? gated(acc[4 * v + i], widen(zw[i])) : acc[4 * v + i]);
-                    zr[v] = make_uint4(out[0], out[1], out[2], out[3]);
-                }
-#pragma unroll
-                for (int v = 0; v < 4; v += 2) {
-                    if (p.y_wide) {
-                        if (col + 8 * v < p.P) st_global_v8(dst + 8 * v, zr[v], zr[v + 1]);
-                    } else {
-                        if (col + 8 * v < p.P) *reinterpret_cast<uint4 *>(dst + 8 * v) = zr[v];
-                        if (col + 8 * v + 8 < p.P) *reinterpret_cast<uint4 *>(dst + 8 * v + 8) = zr[v + 1];
-                    }
-                }
-            }
-            if (c + 1 < nchunks) load_z(c + 1);
+            arrive(&ctl.y_read[c & 1], false);
+            arrive(&ctl.y_done, true);
+            if (c + 1 < nchunks) next_m(c + 1);
         }
         if (!ok) *abort = 1;
     }
@@ -808,10 +842,11 @@ cudaError_t launch_ssm_tc(const SsmParams &s, void *workspace, cudaStream_t stre
     p.ptiles = (s.head_dim + 63) / 64;
     p.units = s.heads / s.groups * p.ptiles;
     p.pairs_per_group = (p.units + 1) / 2;
-    const bool by16 = s.head_dim % 16 == 0;
-    p.z_wide = reinterpret_cast<uintptr_t>(s.z) % 16 != 0 || s.ld_z % 8 != 0 ? 0
-               : by16 && reinterpret_cast<uintptr_t>(s.z) % 32 == 0 && s.ld_z % 16 == 0 ? 2 : 1;
-    p.y_wide = by16 && reinterpret_cast<uintptr_t>(s.y) % 32 == 0;
+    p.z_tma = s.z != nullptr && reinterpret_cast<uintptr_t>(s.z) % 16 == 0 && s.ld_z % 8 == 0;
+    const uint64_t sy[2] = {(uint64_t)s.head_dim * 2, (uint64_t)s.head_dim * s.heads * 2}, sz[2] = {sy[0], (uint64_t)s.ld_z * 2};
+    if (!encode_map_3d(&p.tm_y, s.y, GDN_BF16, dx, sy, box, true) ||
+        (p.z_tma && !encode_map_3d(&p.tm_z, s.z, GDN_BF16, dx, sz, box, true)))
+        return cudaErrorInvalidValue;
     p.status = s.status;
     p.budget = __atomic_load_n(&g_wait_budget, __ATOMIC_RELAXED);
     const SegBytes b = segment_bytes(varlen, s.seqlen, s.rows, s.num_seqs, s.heads, s.groups, s.head_dim, s.d_state);
