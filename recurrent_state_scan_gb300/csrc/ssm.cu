@@ -16,24 +16,43 @@ namespace {
 // A thread takes V channels and a run of kRun token rows, the last K - 1 rows kept in
 // registers; the rows are loaded kAhead at a time, so that enough of them are in flight.
 // Products of two 16-bit values are exact in fp32, so the sum's order alone decides its
-// value: bias first, then the taps in order.
-constexpr int kRun = 32, kAhead = 8;
+// value: bias first, then the taps in order.  Bound by reading and writing the rows; the
+// arithmetic (13 instructions a value) takes nearly as long.
+constexpr int kRun = 32, kAhead = 4;
 
 template <typename IO, int V> struct alignas(sizeof(IO) * V) Pack {
     IO v[V];
 };
 
-// silu whose rounding to IO is silu_exact's.  For 16-bit types the fast form serves unless it is
-// within 32 fp32 steps of the border between two values (below |v| = 8 it is within 16 of the exact
-// form: 2 in the exponential, 1 in the reciprocal, 12 from the argument's rounding).
-template <typename IO> __device__ __forceinline__ float silu_for(float v) {
-    if constexpr (sizeof(IO) == 4) return silu_exact(v);
-    const float fast = silu_gate(v);
-    constexpr uint32_t kCut = std::is_same<IO, __half>::value ? 0x1fffu : 0xffffu;    // bits that the rounding drops
-    const uint32_t off = (__float_as_uint(fast) + 32u + (kCut + 1) / 2) & kCut;
-    // (f16's subnormal results round elsewhere.)
-    const bool sure = fabsf(v) < 8.f && off >= 64u && (!std::is_same<IO, __half>::value || fabsf(fast) > 0x1p-13f);
-    return sure ? fast : silu_exact(v);
+// silu of V values, each rounded to IO as silu_exact rounds.  For 16-bit types the fast form
+// serves unless one of them is within 32 fp32 steps of the border between two 16-bit values: below
+// |v| = 8 it is within 12 of the exact form (6 from the exponent's rounding, 2 in the exponential,
+// 1 in the reciprocal, the rest in the roundings between).
+template <typename IO, int V> __device__ __forceinline__ void silu_rounded(float (&v)[V]) {
+    if constexpr (sizeof(IO) == 2) {
+        constexpr uint32_t kCut = std::is_same<IO, __half>::value ? 0x1fffu : 0xffffu;    // bits that the rounding drops
+        float f[V];
+        uint32_t near = 0;
+        float top = 0.f, least = 1.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            f[i] = v[i] * rcp(1.f + ex2(-kLog2e * v[i]));
+            near |= ((__float_as_uint(f[i]) + 32u + (kCut + 1) / 2) & kCut) < 64u;
+            top = fmaxf(top, fabsf(v[i]));
+            if (kCut == 0x1fffu) least = fminf(least, fabsf(f[i]));    // (f16's subnormals round elsewhere)
+        }
+        if (!near && top < 8.f && (kCut != 0x1fffu || least > 0x1p-13f)) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = f[i];
+            return;
+        }
+    }
+    for (int i = 0; i < V; ++i) v[i] = silu_exact(v[i]);
+}
+
+template <typename IO, int V> __device__ __forceinline__ void widen(const Pack<IO, V> &a, float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = IoType<IO>::ld(&a.v[i]);
 }
 
 template <typename IO, int V, int K>
@@ -75,12 +94,12 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
         uc = (b < gn ? p.off_b : p.off_c) + (int64_t)(in / p.d_state) * p.bc_group + in % p.d_state;
     }
     IO *u = static_cast<IO *>(p.u) + uc;
-    float w[V][K], bias[V];
+    float w[K][V], bias[V];
     if (p.w != nullptr) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
 #pragma unroll
-            for (int j = 0; j < K; ++j) w[i][j] = IoType<IO>::ld(static_cast<const IO *>(p.w) + (int64_t)(c0 + i) * K + j);
+            for (int j = 0; j < K; ++j) w[j][i] = IoType<IO>::ld(static_cast<const IO *>(p.w) + (int64_t)(c0 + i) * K + j);
             bias[i] = p.bias ? IoType<IO>::ld(static_cast<const IO *>(p.bias) + c0 + i) : 0.f;
         }
     }
@@ -106,19 +125,21 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
         if (t0 < 0 || t0 > r0) t0 = r0;     // malformed offsets: stay inside the rows (the scan reports them)
         if (t1 <= r0) t1 = r0 + 1;
     }
-    Vec past[K > 1 ? K - 1 : 1];
+    float past[K > 1 ? K - 1 : 1][V];
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
         const int64_t at = r0 - (K - 1) + j;
-        past[j] = zero;
-        if (at >= t0) past[j] = *reinterpret_cast<const Vec *>(x + at * p.ld_x);
-        else if (cin) past[j] = *reinterpret_cast<const Vec *>(cin + (n * (K - 1) + (K - 1) + (at - t0)) * p.C);
+        Vec v = zero;
+        if (at >= t0) v = *reinterpret_cast<const Vec *>(x + at * p.ld_x);
+        else if (cin) v = *reinterpret_cast<const Vec *>(cin + (n * (K - 1) + (K - 1) + (at - t0)) * p.C);
+        widen<IO, V>(v, past[j]);
     }
-    for (int64_t rb = r0; rb < r1; rb += kAhead) {
-        Vec in[kAhead];
+    Vec in[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (rb + i < r1) in[i] = *reinterpret_cast<const Vec *>(x + (rb + i) * p.ld_x);
+    for (int i = 0; i < kAhead; ++i)
+        if (r0 + i < r1) in[i] = *reinterpret_cast<const Vec *>(x + (r0 + i) * p.ld_x);
+#pragma unroll 1
+    for (int64_t rb = r0; rb < r1; rb += kAhead) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int64_t r = rb + i;
@@ -136,23 +157,41 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
                 }
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j)
-                    past[j] = cin ? *reinterpret_cast<const Vec *>(cin + (n * (K - 1) + j) * p.C) : zero;
+                    widen<IO, V>(cin ? *reinterpret_cast<const Vec *>(cin + (n * (K - 1) + j) * p.C) : zero, past[j]);
             }
             Vec out = in[i];
+            float now[V];
+            widen<IO, V>(in[i], now);
+            if (r + kAhead < r1) in[i] = *reinterpret_cast<const Vec *>(x + (r + kAhead) * p.ld_x);
             if (p.w != nullptr) {
+                float acc[V];
+                if constexpr (V % 2 == 0) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float acc = bias[v];
+                    for (int v = 0; v < V; v += 2) {
+                        F2 a = {bias[v], bias[v + 1]};
 #pragma unroll
-                    for (int j = 0; j < K - 1; ++j) acc = fmaf(w[v][j], IoType<IO>::ld(&past[j].v[v]), acc);
-                    acc = fmaf(w[v][K - 1], IoType<IO>::ld(&in[i].v[v]), acc);
-                    IoType<IO>::st(&out.v[v], p.silu ? silu_for<IO>(acc) : acc);
+                        for (int j = 0; j < K - 1; ++j) a = fma2({w[j][v], w[j][v + 1]}, {past[j][v], past[j][v + 1]}, a);
+                        a = fma2({w[K - 1][v], w[K - 1][v + 1]}, {now[v], now[v + 1]}, a);
+                        acc[v] = a.x;
+                        acc[v + 1] = a.y;
+                    }
+                } else {
+                    acc[0] = bias[0];
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) acc[0] = fmaf(w[j][0], past[j][0], acc[0]);
+                    acc[0] = fmaf(w[K - 1][0], now[0], acc[0]);
                 }
+                if (p.silu) silu_rounded<IO, V>(acc);
+#pragma unroll
+                for (int v = 0; v < V; ++v) IoType<IO>::st(&out.v[v], acc[v]);
             }
             *reinterpret_cast<Vec *>(u + r * p.ld_u) = out;
 #pragma unroll
-            for (int j = 0; j + 1 < K - 1; ++j) past[j] = past[j + 1];
-            if (K > 1) past[K > 1 ? K - 2 : 0] = in[i];
+            for (int v = 0; v < V; ++v) {
+#pragma unroll
+                for (int j = 0; j + 1 < K - 1; ++j) past[j][v] = past[j + 1][v];
+                if (K > 1) past[K > 1 ? K - 2 : 0][v] = now[v];
+            }
         }
     }
 }

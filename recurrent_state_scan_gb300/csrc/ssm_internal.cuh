@@ -71,6 +71,48 @@ size_t ssm_tc_workspace(bool varlen, int64_t seqlen, int64_t rows, int64_t num_s
 cudaError_t launch_ssm_tc(const SsmParams &p, void *workspace, cudaStream_t stream);
 cudaError_t launch_ssm_decode(const SsmDecodeParams &p, gdn_dtype io, cudaStream_t stream);
 
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Two fp32 operations in one instruction.
+struct F2 {
+    float x, y;
+};
+__device__ __forceinline__ uint64_t bits(F2 a) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ F2 pair(uint64_t v) {
+    F2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 both(float a) { return {a, a}; }
+
 // silu as the convolution stores it: the correctly scaled exponential and a true divide,
 // so that its rounding to a 16-bit type does not hang on an approximation's last bits.
 __device__ __forceinline__ float silu_exact(float v) { return v / (1.0f + expf(-v)); }

@@ -40,7 +40,6 @@ using namespace tc;
 constexpr int kL = 64;                       // tokens per chunk
 constexpr int kThreads = 640;
 constexpr long long kBudget = 4000000000LL;  // cycles (~2 s) before a wait gives up
-constexpr float kLog2e = 1.4426950408889634f;
 
 // Shared memory (1024-byte aligned): stages of what TMA brings, then the operands the threads
 // make.  All tiles are stacks of 128-byte-swizzled rows of 64 bf16.  y takes z's place, for a
@@ -50,11 +49,11 @@ constexpr int ST_X = 16384;                  // 2 units x 64 rows
 constexpr int ST_C = 32768;                  // 2 regions x 128 rows: C twice
 template <bool kState> constexpr int kStageBytes = kState ? 32768 : 65536;
 template <bool kState> constexpr int kStages = kState ? 4 : 2;
-constexpr int O_Z = 131072;                  // z, then y: 2 units x 64 rows
-constexpr int O_XH = O_Z + 16384;            // w x, high part: 2 units x 64 rows
+constexpr int O_Z = 131072;                  // z, then y, by chunk parity: 2 units x 64 rows each
+constexpr int O_XH = O_Z + 32768;            // w x, high part: 2 units x 64 rows
 constexpr int O_XL = O_XH + 16384;           // low part
 constexpr int O_S = O_XL + 16384;            // bf16(S): 2 units x 128 state rows
-constexpr int kSmem = O_S + 32768 + 1024;
+constexpr int O_CTL = O_S + 32768;           // Ctl
 
 // Tensor memory columns; M is the A operand of the last MMA, bf16 pairs.
 constexpr uint32_t T_CB = 0, T_CS = 64, T_DS = 192, T_MX = 320, T_M = 448, kCols = 512;
@@ -79,31 +78,27 @@ struct TcParams {
     long long budget;
 };
 
+// Of the chunk's tokens, in log2: s_i = log2 e^{G_L - G_i}, what the state loses behind token i,
+// and lw_j = s_j + log2 d_j.  All that is needed follows: w_j = 2^{lw_j}, the scores' weights
+// 2^{lw_j - s_i}, and e^{G_i} = 2^{total - s_i}.
 struct alignas(16) Gates {       // read in float2 and float4
-    float ci[kL];    // log2 e^{G_i}
-    float cj[kL];    // the same less log2 d_j
-    float ec[kL];    // e^{G_i}
-    float w[kL];     // d_j e^{G_L - G_j}
-    float decay;     // e^{G_L}
-    float total;     // its log2
+    float lw[kL], s[kL];
+    float total, decay;          // log2 e^{G_L}, e^{G_L}
 };
 
 struct Ctl {
     // Barriers: pairs by chunk parity where a waiter can be a chunk behind (`full` and s_ready
     // by stage).
-    uint64_t full[4], gates[2], y_read[2], s_ready[4], wx_ready[2], ds[2];
-    uint64_t y_done, full_z, cb, cs, mx, m_ready, s_first, drain;
+    uint64_t full[4], gates[2], y_read[2], s_ready[4], wx_ready[2], ds[2], full_x[2], full_z[2];
+    uint64_t y_done[2], cb, cs, mx, m_ready, s_first, drain;
     uint32_t tmem;
     int32_t abort;   // a wait ran out
     Gates g[2][2];   // [chunk parity][unit]
 };
-static_assert(sizeof(Gates) % 16 == 0 && offsetof(Ctl, g) % 16 == 0, "vector accesses of the gates");
+static_assert(sizeof(Gates) % 16 == 0 && offsetof(Ctl, g) % 16 == 0 && O_CTL % 16 == 0, "vector accesses of the gates");
+constexpr int kSmem = O_CTL + sizeof(Ctl);
+static_assert(kSmem <= 232448, "shared memory of a CTA");
 
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&v);
@@ -111,44 +106,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// Two fp32 operations in one instruction.
-struct F2 {
-    float x, y;
-};
-__device__ __forceinline__ uint64_t bits(F2 a) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
-    return r;
-}
-__device__ __forceinline__ F2 pair(uint64_t v) {
-    F2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-    return pair(r);
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-    return pair(r);
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-    return pair(r);
-}
-__device__ __forceinline__ F2 both(float a) { return {a, a}; }
 __device__ __forceinline__ F2 words(uint32_t a, uint32_t b) { return {__uint_as_float(a), __uint_as_float(b)}; }
 __device__ __forceinline__ F2 widen(uint32_t v) { return {lo_f(v), hi_f(v)}; }
 __device__ __forceinline__ uint32_t pack2(F2 a) { return pack2(a.x, a.y); }
-__device__ __forceinline__ float rcp(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 // a silu(z) for two values with one reciprocal: 1 / d0 = d1 / (d0 d1).  e^-z stops at 2^60, so that
 // the product stays finite (silu is then 2^-60 z, where it is smaller still).
 __device__ __forceinline__ F2 gated(F2 a, F2 z) {
@@ -252,9 +212,10 @@ constexpr int kSWarp = 8, kIssueWarp = 16, kLoadWarp = 17, kGateWarp = 18;
 // kState: the state-only pass of a segment (no scores, no y; warps 0-7 make w x there).
 template <bool kState>
 __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_constant__ TcParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    __shared__ Ctl ctl;
+    // (Nothing static stands before it, so dynamic shared memory begins on a 1024-byte boundary, as
+    // the swizzled tiles need; there is no room to align it here.)
+    extern __shared__ __align__(1024) uint8_t sm[];
+    Ctl &ctl = *reinterpret_cast<Ctl *>(sm + O_CTL);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pairs = p.groups * p.pairs_per_group;
     const int pair = blockIdx.x % pairs;
@@ -265,6 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, blockIdx.x, a, b);
     }
     if (!it.valid || (kState && it.k + 1 >= it.nseg)) return;
+    if (smem_u32(sm) % 1024 != 0) {
+        if (tid == 0) atomicOr(p.status, kDevTimeout);
+        return;
+    }
 
     // The two units.  An odd last unit is computed twice and stored once.
     const int g = pair / p.pairs_per_group, u0 = 2 * (pair % p.pairs_per_group);
@@ -288,9 +253,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             mbar_init(&ctl.y_read[i], 8);
             mbar_init(&ctl.wx_ready[i], 8);
             mbar_init(&ctl.ds[i], 1);
+            mbar_init(&ctl.full_x[i], 1);
+            mbar_init(&ctl.full_z[i], 1);
+            mbar_init(&ctl.y_done[i], 8);
         }
-        mbar_init(&ctl.y_done, 8);
-        mbar_init(&ctl.full_z, 1);
         mbar_init(&ctl.cb, 1);
         mbar_init(&ctl.cs, 1);
         mbar_init(&ctl.mx, 1);
@@ -339,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         for (int v = 0; v < 4; ++v) {
             const int u = v >> 1, j = (who >> 3) + 32 * (v & 1);
             const uint32_t at = u * 8192 + sw128_offset(j, who & 7);
-            const float w = j < len ? ctl.g[c & 1][u].w[j] : 0.f;
+            const float w = j < len ? ex2(ctl.g[c & 1][u].lw[j]) : 0.f;
             const uint4 xv = j < len ? *reinterpret_cast<const uint4 *>(xt + at) : make_uint4(0, 0, 0, 0);
             const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
             uint32_t hi[4], lo[4];
@@ -387,7 +353,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             for (int c = 0; ok && c < nchunks; ++c) {
                 const uint64_t st = (uint64_t)(c & (NS - 1)) * (kStageBytes<kState> >> 4);
                 // (w x ready: the S warps have also read the accumulators of the chunk before.)
-                if (!(ok = wait2(ctl.wx_ready, c) && wait_st(ctl.full, c) && (!kState || c < 2 || wait_st(ctl.s_ready, c - 2)))) break;
+                if (!(ok = wait2(ctl.wx_ready, c) && wait_st(ctl.full, c) &&
+                           (kState ? c < 2 || wait_st(ctl.s_ready, c - 2) : wait2(ctl.full_x, c))))
+                    break;
                 tc_fence_after();
                 const uint64_t xh = kState && (c & 1) ? dXH1 : dXH;
                 const uint32_t dst = tmem + (kState && (c & 1) ? T_CS : T_DS);
@@ -424,64 +392,66 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             const int regions = p.N > 64 ? 2 : 1;
             int loaded = 0, loaded_z = 0;
             const int tile_u[2] = {64 * unit_tile(0), 64 * unit_tile(1)}, head_u[2] = {unit_head(0), unit_head(1)};
-            auto load_z = [&](int c) {
-                mbar_arrive_expect_tx(&ctl.full_z, 16384);
-                for (int u = 0; u < 2; ++u)
-                    tma_load_3d(sm + O_Z + u * 8192, &p.tm_z, tile_u[u], head_u[u], (int)(it.t0 + (int64_t)c * kL), &ctl.full_z);
+            auto row_of = [&](int c) { return (int)(it.t0 + (int64_t)c * kL); };
+            auto load_z = [&](int c) {      // (without a z that TMA can take: its place is free)
+                uint64_t *bar = &ctl.full_z[c & 1];
                 loaded_z = c + 1;
-            };
-            // y of chunk c has taken z's place: out with it, then the next z in.  (A sequence's last
-            // rows, where they do not fill the chunk, are stored by their threads.)
-            auto store_y = [&](int c) {
-                if (!(ok = wait(&ctl.y_done, c))) return;
-                if (chunk_len(c) == kL) {
-                    for (int u = 0; u < 1 + two; ++u)
-                        tma_store_3d(&p.tm_y, sm + O_Z + u * 8192, tile_u[u], head_u[u], (int)(it.t0 + (int64_t)c * kL));
-                    bulk_commit();
-                    bulk_wait_read();
+                if (!p.z_tma) {
+                    mbar_arrive(bar);
+                    return;
                 }
-                if (c + 1 < nchunks) {
-                    if (p.z_tma) load_z(c + 1);
-                    else mbar_arrive(&ctl.full_z);     // its place is free
-                }
+                mbar_arrive_expect_tx(bar, 16384);
+                for (int u = 0; u < 2; ++u) tma_load_3d(sm + O_Z + (c & 1) * 16384 + u * 8192, &p.tm_z, tile_u[u], head_u[u], row_of(c), bar);
             };
-            if (!kState && nchunks > 0) {
-                if (p.z_tma) load_z(0);
-                else mbar_arrive(&ctl.full_z);
-            }
-            for (int c = 0; ok && c < nchunks + (kState ? 0 : NS); ++c) {
-                if (c < nchunks) {
-                    // The stage is free when the last MMAs of the chunk in it are done: its S has been
-                    // taken, and its y read out.
-                    if (c >= NS && !(ok = wait_st(ctl.s_ready, c - NS) && (kState || wait2(ctl.y_read, c - NS)))) break;
-                    uint8_t *st = stage(c);
-                    uint64_t *bar = &ctl.full[c & (NS - 1)];
-                    const int t = (int)(it.t0 + (int64_t)c * kL);
-                    mbar_arrive_expect_tx(bar, 8192u * (kState ? regions + 2 : 3 * regions + 2));
-#pragma unroll 1
-                    for (int r = 0; r < regions; ++r) {
-                        tma_load_3d(st + ST_B + r * 8192, &p.tm_b, 64 * r, g, t, bar);
-                        if (!kState) {
-                            tma_load_3d(st + ST_C + r * 16384, &p.tm_c, 64 * r, g, t, bar);
-                            tma_load_3d(st + ST_C + r * 16384 + 8192, &p.tm_c, 64 * r, g, t, bar);
-                        }
+            for (int c = 0; ok && c < nchunks + (kState ? 0 : 2); ++c) {
+                // y of chunk c - 2 has taken z's place: out with it, ahead of the next loads.  (A
+                // sequence's last rows, where they do not fill the chunk, are stored by their threads.)
+                if (!kState && c >= 2) {
+                    if (!(ok = wait2(ctl.y_done, c - 2))) break;
+                    if (chunk_len(c - 2) == kL) {
+                        for (int u = 0; u < 1 + two; ++u)
+                            tma_store_3d(&p.tm_y, sm + O_Z + (c & 1) * 16384 + u * 8192, tile_u[u], head_u[u], row_of(c - 2));
+                        bulk_commit();
                     }
-                    for (int u = 0; u < 2; ++u) tma_load_3d(st + ST_X + u * 8192, &p.tm_x, tile_u[u], head_u[u], t, bar);
-                    loaded = c + 1;
                 }
-                if (!kState && c >= NS) store_y(c - NS);
+                if (c >= nchunks) continue;
+                // The stage is free when the last MMA of the chunk in it is done: its S has been taken,
+                // or its y read out (x with it).
+                if (c >= NS && !(ok = kState ? wait_st(ctl.s_ready, c - NS) : wait2(ctl.y_read, c - NS))) break;
+                uint8_t *st = stage(c);
+                uint64_t *bar = &ctl.full[c & (NS - 1)], *bar_x = kState ? bar : &ctl.full_x[c & 1];
+                const int t = row_of(c);
+                if (!kState) mbar_arrive_expect_tx(bar_x, 16384);
+                mbar_arrive_expect_tx(bar, 8192u * (kState ? regions + 2 : 3 * regions));
+                for (int u = 0; u < 2; ++u) tma_load_3d(st + ST_X + u * 8192, &p.tm_x, tile_u[u], head_u[u], t, bar_x);
+#pragma unroll 1
+                for (int r = 0; r < regions; ++r) {
+                    tma_load_3d(st + ST_B + r * 8192, &p.tm_b, 64 * r, g, t, bar);
+                    if (!kState) {
+                        tma_load_3d(st + ST_C + r * 16384, &p.tm_c, 64 * r, g, t, bar);
+                        tma_load_3d(st + ST_C + r * 16384 + 8192, &p.tm_c, 64 * r, g, t, bar);
+                    }
+                }
+                loaded = c + 1;
+                if (!kState) {
+                    bulk_wait_read();
+                    load_z(c);
+                }
             }
             // Copies still in flight finish before the CTA leaves (bounded).
             for (int c = loaded - NS < 0 ? 0 : loaded - NS; c < loaded; ++c) mbar_wait(&ctl.full[c & (NS - 1)], (c / NS) & 1, kBudget);
-            if (loaded_z > 0) mbar_wait(&ctl.full_z, (loaded_z - 1) & 1, kBudget);
+            if (!kState) {
+                for (int c = loaded - 2 < 0 ? 0 : loaded - 2; c < loaded; ++c) mbar_wait(&ctl.full_x[c & 1], (c >> 1) & 1, kBudget);
+                for (int c = loaded_z - 2 < 0 ? 0 : loaded_z - 2; c < loaded_z; ++c) mbar_wait(&ctl.full_z[c & 1], (c >> 1) & 1, kBudget);
+            }
             bulk_wait_all();
             if (!ok) *abort = 1;
         }
         __syncwarp();
     } else if (warp >= kGateWarp) {
         // ------------------------------------------------------------ gates: two tokens to a lane
-        // A decay of e^-111 is already nothing in fp32, so g is held above that: a reset then
-        // leaves the running sum small enough to keep the differences of the tokens behind it.
+        // A decay of e^-111 is already nothing in fp32, so g is held above that: a reset then leaves
+        // the sums over it small enough to keep the differences of the tokens before it.
         const int u = warp - kGateWarp, head = unit_head(u);
         const float A = -expf(p.A_log[head]) * kLog2e, bias = p.dt_bias ? p.dt_bias[head] : 0.f;
         unsigned short n0 = 0, n1 = 0;      // bits, widened a chunk later: nothing waits for the load here
@@ -501,24 +471,19 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             float g0 = A * d0, g1 = A * d1;
             g0 = g0 < -160.f ? -160.f : g0;
             g1 = g1 < -160.f ? -160.f : g1;
-            float pre = g0 + g1, suf = pre;
+            float suf = g0 + g1;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const float a = __shfl_up_sync(0xffffffffu, pre, o), b = __shfl_down_sync(0xffffffffu, suf, o);
-                if (lane >= o) pre += a;
-                if (lane + o < 32) suf += b;
+                const float v = __shfl_down_sync(0xffffffffu, suf, o);
+                if (lane + o < 32) suf += v;
             }
-            float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
-            if (lane == 0) before = 0.f;
+            float after = __shfl_down_sync(0xffffffffu, suf, 1);
             if (lane == 31) after = 0.f;
+            const float l0 = __log2f(d0), l1 = __log2f(d1);   // -inf where the step is zero: no weight
             if (c >= 2 && !(ok = all(wait_st(ctl.s_ready, c - 2) && (kState || wait2(ctl.y_read, c - 2))))) break;
             Gates &G = ctl.g[c & 1][u];
-            const float c0 = before + g0, c1 = pre;
-            const float l0 = __log2f(d0), l1 = __log2f(d1);   // -inf where the step is zero: no weight
-            *reinterpret_cast<float2 *>(&G.ci[2 * lane]) = make_float2(c0, c1);
-            *reinterpret_cast<float2 *>(&G.cj[2 * lane]) = make_float2(c0 - l0, c1 - l1);
-            *reinterpret_cast<float2 *>(&G.ec[2 * lane]) = make_float2(ex2(c0), ex2(c1));
-            *reinterpret_cast<float2 *>(&G.w[2 * lane]) = make_float2(d0 * ex2(after + g1), d1 * ex2(after));
+            *reinterpret_cast<float2 *>(&G.s[2 * lane]) = make_float2(after + g1, after);
+            *reinterpret_cast<float2 *>(&G.lw[2 * lane]) = make_float2(after + g1 + l0, after + l1);
             if (lane == 0) {
                 G.total = suf;
                 G.decay = ex2(suf);
@@ -559,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         }
         float seg_total = 0.f;
         auto next_wx = [&](int c) {      // (the state's MMA of the chunk before has left its buffer)
-            if (!(ok = all(wait_st(ctl.full, c) && wait2(ctl.gates, c)))) return;
+            if (!(ok = all(wait2(ctl.full_x, c) && (chunk_len(c) == kL || wait_st(ctl.full, c)) && wait2(ctl.gates, c)))) return;
             make_wx(c, tid - 32 * kSWarp, sm + O_XH);
             arrive(&ctl.wx_ready[c & 1], true);
         };
@@ -624,24 +589,20 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         // columns are behind its rows).
         auto make_m = [&](int c) {
             const Gates &G = ctl.g[c & 1][ru];
-            const float ci = G.ci[ri];
+            const float si = G.s[ri];
             tc_fence_after();
 #pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
-                const int j0 = 32 * half + 16 * b;
-                uint32_t m[8];
-                if (j0 > 32 * (q & 1) + 31) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) m[i] = 0;
-                } else {
-                    uint32_t r[16];
-                    tmem_ld16(tmem + T_CB + lanes + j0, r);
+            for (int j0 = 32 * half; j0 < 32 * half + 32; j0 += 8) {
+                uint32_t m[4] = {0, 0, 0, 0};
+                if (j0 <= 32 * (q & 1) + 31) {
+                    uint32_t r[8];
+                    tmem_ld8(tmem + T_CB + lanes + j0, r);
                     tmem_ld_wait();
                     landed(r);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 cj = *reinterpret_cast<const float4 *>(&G.cj[j0 + i]);
-                        const F2 e0 = fma2(both(-1.f), {cj.x, cj.y}, both(ci)), e1 = fma2(both(-1.f), {cj.z, cj.w}, both(ci));
+                    for (int i = 0; i < 8; i += 4) {
+                        const float4 lw = *reinterpret_cast<const float4 *>(&G.lw[j0 + i]);
+                        const F2 e0 = add2({lw.x, lw.y}, both(-si)), e1 = add2({lw.z, lw.w}, both(-si));
                         F2 v0 = mul2(words(r[i], r[i + 1]), {ex2(e0.x), ex2(e0.y)});
                         F2 v1 = mul2(words(r[i + 2], r[i + 3]), {ex2(e1.x), ex2(e1.y)});
                         const int past = j0 + i - ri;
@@ -651,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
                         m[i / 2 + 1] = pack2(v1);
                     }
                 }
-                tmem_st8(tmem + T_M + lanes + j0 / 2, m);
+                tmem_st4(tmem + T_M + lanes + j0 / 2, m);
             }
             tmem_st_wait();
         };
@@ -663,51 +624,47 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         if (nchunks > 0) next_m(0);
         for (int c = 0; ok && c < nchunks; ++c) {
             // (The last MMA of the chunk: what was issued before it, C S among it, is done too.)
-            if (!(ok = all(wait(&ctl.mx, c) && wait_st(ctl.full, c) && wait(&ctl.full_z, c)))) break;
+            if (!(ok = all(wait(&ctl.mx, c) && wait2(ctl.full_x, c) && wait2(ctl.full_z, c)))) break;
             tc_fence_after();
             const uint8_t *xt = stage(c) + ST_X + ru * 8192;
-            uint8_t *zt = sm + O_Z + ru * 8192;
-            const float e = ctl.g[c & 1][ru].ec[ri];
+            uint8_t *zt = sm + O_Z + (c & 1) * 16384 + ru * 8192;
+            const float e = ex2(ctl.g[c & 1][ru].total - ctl.g[c & 1][ru].s[ri]);
             const int len = chunk_len(c);
             __nv_bfloat16 *dst = p.y + ((it.t0 + (int64_t)c * kL + ri) * p.heads + head) * (int64_t)p.P + col;
 #pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
-                uint32_t m[16], cs[16];
-                const uint32_t at = lanes + 64 * ru + 32 * half + 16 * b;
-                tmem_ld16(tmem + T_MX + at, m);
-                tmem_ld16(tmem + T_CS + at, cs);
+            for (int b = 0; b < 4; ++b) {
+                uint32_t m[8], cs[8];
+                const uint32_t at = lanes + 64 * ru + 32 * half + 8 * b;
+                tmem_ld8(tmem + T_MX + at, m);
+                tmem_ld8(tmem + T_CS + at, cs);
+                const uint32_t piece = sw128_offset(ri, 4 * half + b);
+                const uint4 xv = *reinterpret_cast<const uint4 *>(xt + piece);
+                uint4 *place = reinterpret_cast<uint4 *>(zt + piece);
+                const int pc = 8 * b;
+                uint4 zv = make_uint4(0, 0, 0, 0);
+                if (p.z != nullptr) {
+                    if (p.z_tma) zv = *place;
+                    else if (live && ri < len && col + pc < p.P)
+                        zv = load_unaligned(p.z + (it.t0 + (int64_t)c * kL + ri) * p.ld_z + (int64_t)head * p.P + col + pc);
+                }
                 tmem_ld_wait();
                 landed(m);
                 landed(cs);
+                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, zw[4] = {zv.x, zv.y, zv.z, zv.w};
+                uint32_t out[4];
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const uint32_t piece = sw128_offset(ri, 4 * half + 2 * b + v);
-                    const uint4 xv = *reinterpret_cast<const uint4 *>(xt + piece);
-                    uint4 *place = reinterpret_cast<uint4 *>(zt + piece);
-                    const int pc = 16 * b + 8 * v;
-                    uint4 zv = make_uint4(0, 0, 0, 0);
-                    if (p.z != nullptr) {
-                        if (p.z_tma) zv = *place;
-                        else if (live && ri < len && col + pc < p.P)
-                            zv = load_unaligned(p.z + (it.t0 + (int64_t)c * kL + ri) * p.ld_z + (int64_t)head * p.P + col + pc);
-                    }
-                    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, zw[4] = {zv.x, zv.y, zv.z, zv.w};
-                    uint32_t out[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int k = 8 * v + 2 * i;
-                        F2 a = fma2(both(D), widen(xw[i]), fma2(both(e), words(cs[k], cs[k + 1]), words(m[k], m[k + 1])));
-                        if (p.z != nullptr) a = gated(a, widen(zw[i]));
-                        out[i] = pack2(a);
-                    }
-                    const uint4 o = make_uint4(out[0], out[1], out[2], out[3]);
-                    // A whole chunk's y goes out by TMA, from z's place.
-                    if (len == kL) *place = o;
-                    else if (live && ri < len && col + pc < p.P) *reinterpret_cast<uint4 *>(dst + pc) = o;
+                for (int i = 0; i < 4; ++i) {
+                    F2 a = fma2(both(D), widen(xw[i]), fma2(both(e), words(cs[2 * i], cs[2 * i + 1]), words(m[2 * i], m[2 * i + 1])));
+                    if (p.z != nullptr) a = gated(a, widen(zw[i]));
+                    out[i] = pack2(a);
                 }
+                const uint4 o = make_uint4(out[0], out[1], out[2], out[3]);
+                // A whole chunk's y goes out by TMA, from z's place.
+                if (len == kL) *place = o;
+                else if (live && ri < len && col + pc < p.P) *reinterpret_cast<uint4 *>(dst + pc) = o;
             }
             arrive(&ctl.y_read[c & 1], false);
-            arrive(&ctl.y_done, true);
+            arrive(&ctl.y_done[c & 1], true);
             if (c + 1 < nchunks) next_m(c + 1);
         }
         if (!ok) *abort = 1;

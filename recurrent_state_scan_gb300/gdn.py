@@ -846,72 +846,84 @@ def gdn_prefill_layer(x, conv_weight, conv_bias, conv_state_in, a, b, A_log, dt_
 
 
 # ------------------------------------------------------------------ the state-space layer
-def _on(device, stream):
-    """The context a call allocates and launches in: its tensors' device, and the stream's own
-    memory pool when it names one (a workspace freed on return is then reused in its order)."""
-    ctx = contextlib.ExitStack()
-    ctx.enter_context(torch.cuda.device(device))
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        ctx.enter_context(torch.cuda.stream(stream))
-    return ctx
-
-
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be on {device}, as the call's first tensor is")
-
-
-def _need_shape(name: str, t, shape, dtype):
-    """A contiguous CUDA tensor of this shape and type; None passes."""
-    if t is None:
-        return
-    _need_cuda(name, t, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _row_stride(name: str, t, B: int, T: int, row: tuple, dtype) -> int:
-    """Elements between the token rows of t [B, T, *row], whose rows are contiguous and evenly spaced."""
+def _bad(name: str, t, shape, dtype, device: int):
+    """Say what _arg found wrong with a tensor."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != (B, T) + row:
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be {(B, T) + row}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be on cuda:{device}, as the call's first tensor is")
     if t.dtype != dtype:
         raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be {dtype}, got {t.dtype}")
-    step = 1
-    for n, s in zip(reversed(row), reversed(t.stride()[2:])):
+    if shape is not None and t.shape != shape:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be contiguous")
+
+
+def _arg(name: str, t, shape, dtype, device: int):
+    """Address of a contiguous tensor of this shape (None: any), type and device; None passes."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype != dtype or not t.is_contiguous() or \
+            (shape is not None and t.shape != shape):
+        _bad(name, t, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _rows(name: str, t, B: int, T: int, row: tuple, dtype, device: int):
+    """(address, elements between token rows) of t [B, T, *row], whose token rows are contiguous in
+    themselves and evenly spaced."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype != dtype or t.shape != (B, T) + row:
+        _bad(name, t, (B, T) + row, dtype, device)
+    stride, step = t.stride(), 1
+    for n, s in zip(reversed(row), reversed(stride[2:])):
         if n > 1 and s != step:
             raise GdnError(GDN_ERR_INVALID_ARG, f"{name}'s token rows must be contiguous")
         step *= n
     if T > 1:
-        if B > 1 and t.stride(0) != T * t.stride(1):
+        if B > 1 and stride[0] != T * stride[1]:
             raise GdnError(GDN_ERR_INVALID_ARG, f"{name}'s token rows must be evenly spaced over the batch")
-        return t.stride(1)
-    return t.stride(0) if B > 1 else step
+        return t.data_ptr(), stride[1]
+    return t.data_ptr(), stride[0] if B > 1 else step
 
 
-def _ssm_geometry(xbc, dt, z, heads, head_dim, groups, d_state, cu_seqlens, conv_weight, conv_activation, dt_min, dt_max):
-    """(shape, params) of the call; the rows are checked."""
-    if not isinstance(xbc, torch.Tensor) or xbc.dim() != 3 or xbc.dtype not in _DTYPE_CODE:
-        raise GdnError(GDN_ERR_INVALID_ARG, "xbc must be [B, T, C] in float32, bfloat16 or float16")
-    if conv_activation not in ("none", "silu"):
-        raise GdnError(GDN_ERR_INVALID_ARG, "the convolution's activation is 'none' or 'silu'")
-    B, T = xbc.shape[:2]
-    C = heads * head_dim + 2 * groups * d_state
-    n = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    K = 0
-    if conv_weight is not None:
-        if C <= 0 or conv_weight.dim() == 0 or conv_weight.shape[0] != C or conv_weight.numel() == 0:
-            raise GdnError(GDN_ERR_INVALID_ARG, f"conv_weight must be [{C}, 1, K]")
-        K = conv_weight.numel() // C
-    shape = GdnSsmShape(_DTYPE_CODE[xbc.dtype], B, T, n, heads, head_dim, groups, d_state,
-                        _row_stride("xbc", xbc, B, T, (C,), xbc.dtype),
-                        _row_stride("dt", dt, B, T, (heads,), xbc.dtype),
-                        0 if z is None else _row_stride("z", z, B, T, (heads, head_dim), xbc.dtype))
-    return shape, GdnSsmParams(K, ACTIVATIONS[conv_activation], float(dt_min), float(dt_max))
+@contextlib.contextmanager
+def _elsewhere(device: int, stream):
+    with torch.cuda.device(device):
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            yield
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: int, stream):
+    """The context a call allocates and launches in: its tensors' device, and the stream's own
+    memory pool when it names one (a workspace freed on return is then reused in its order)."""
+    return _HERE if stream is None and torch.cuda.current_device() == device else _elsewhere(device, stream)
+
+
+def _raw_stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _first(name: str, t, dims: int) -> int:
+    """Device of the call's first tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dims or t.dtype not in _DTYPE_CODE:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must have {dims} axes, in float32, bfloat16 or float16")
+    if not t.is_cuda:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _conv_taps(conv_weight, C: int) -> int:
+    if conv_weight is None:
+        return 0
+    if C <= 0 or not isinstance(conv_weight, torch.Tensor) or conv_weight.dim() == 0 or conv_weight.shape[0] != C or \
+            conv_weight.numel() == 0:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"conv_weight must be [{C}, 1, K]")
+    return conv_weight.numel() // C
 
 
 def gdn_ssm_prefill_workspace_bytes(shape: GdnSsmShape, params: GdnSsmParams) -> int:
@@ -923,6 +935,9 @@ def gdn_ssm_prefill_plan(shape: GdnSsmShape, params: GdnSsmParams):
     path, launches = ctypes.c_int32(), ctypes.c_int32()
     _check(load().gdn_ssm_prefill_plan(ctypes.byref(shape), ctypes.byref(params), ctypes.byref(path), ctypes.byref(launches)))
     return path.value, launches.value
+
+
+_CONV_ACT = {"none": 0, "silu": 1}
 
 
 def gdn_ssm_prefill(xbc, dt, A_log, *, heads: int, head_dim: int, d_state: int, groups: int = 1, D=None, dt_bias=None,
@@ -938,42 +953,43 @@ def gdn_ssm_prefill(xbc, dt, A_log, *, heads: int, head_dim: int, d_state: int, 
     conv_state_in [N, K - 1, C], state_in [N, heads, d_state, head_dim] fp32: zeros when None.
     A_log, dt_bias, D [heads] fp32.  Returns (y [B, T, heads, head_dim], state_out,
     conv_state_out or None)."""
-    lib = load()
-    shape, params = _ssm_geometry(xbc, dt, z, heads, head_dim, groups, d_state, cu_seqlens, conv_weight, conv_activation,
-                                  dt_min, dt_max)
-    io, dev, (B, T, C), n, K = xbc.dtype, xbc.device, xbc.shape, shape.num_seqs, params.conv_kernel
-    states, convs = (max(n, 0), heads, d_state, head_dim), (max(n, 0), max(K - 1, 0), C)
-    if cu_seqlens is not None:
-        _need_shape("cu_seqlens", cu_seqlens, (n + 1,), torch.int32)
-    for name, t in (("A_log", A_log), ("dt_bias", dt_bias), ("D", D)):
-        _need_shape(name, t, (heads,), torch.float32)
-    for name, t in (("conv_weight", conv_weight), ("workspace", workspace)):
-        if t is not None:
-            _need_cuda(name, t, io if name == "conv_weight" else None)
-    _need_shape("conv_bias", conv_bias, (C,), io)
-    _need_shape("state_in", state_in, states, torch.float32)
-    _need_shape("state_out", state_out, states, torch.float32)
-    _need_shape("y", y, (B, T, heads, head_dim), io)
-    _need_shape("conv_state_in", conv_state_in, convs, io)
-    _need_shape("conv_state_out", conv_state_out, convs, io)
-    _same_device(dev, dt=dt, z=z, A_log=A_log, dt_bias=dt_bias, D=D, conv_weight=conv_weight, conv_bias=conv_bias,
-                 conv_state_in=conv_state_in, conv_state_out=conv_state_out, state_in=state_in, state_out=state_out,
-                 cu_seqlens=cu_seqlens, y=y, workspace=workspace)
+    lib = _lib or load()
+    dev = _first("xbc", xbc, 3)
+    if conv_activation not in _CONV_ACT:
+        raise GdnError(GDN_ERR_INVALID_ARG, "the convolution's activation is 'none' or 'silu'")
+    io, (B, T, _) = xbc.dtype, xbc.shape
+    C = heads * head_dim + 2 * groups * d_state
+    K = _conv_taps(conv_weight, C)
+    n = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    f32, states, convs = torch.float32, (max(n, 0), heads, d_state, head_dim), (max(n, 0), max(K - 1, 0), C)
+    px, ldx = _rows("xbc", xbc, B, T, (C,), io, dev)
+    pdt, lddt = _rows("dt", dt, B, T, (heads,), io, dev)
+    pz, ldz = (None, 0) if z is None else _rows("z", z, B, T, (heads, head_dim), io, dev)
+    per_head, chan = (heads,), (C,)
+    pcu = _arg("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, dev)
+    pA, pb, pD = (_arg("A_log", A_log, per_head, f32, dev), _arg("dt_bias", dt_bias, per_head, f32, dev),
+                  _arg("D", D, per_head, f32, dev))
+    pw, pcb = _arg("conv_weight", conv_weight, None, io, dev), _arg("conv_bias", conv_bias, chan, io, dev)
+    psi, pci = _arg("state_in", state_in, states, f32, dev), _arg("conv_state_in", conv_state_in, convs, io, dev)
+    shape = GdnSsmShape(_DTYPE_CODE[io], B, T, n, heads, head_dim, groups, d_state, ldx, lddt, ldz)
+    params = GdnSsmParams(K, _CONV_ACT[conv_activation], dt_min, dt_max)
+    rs, rp = ctypes.byref(shape), ctypes.byref(params)
     with _on(dev, stream):
         if y is None:
-            y = torch.empty((B, T, heads, head_dim), dtype=io, device=dev)
+            y = torch.empty((B, T, heads, head_dim), dtype=io, device=xbc.device)
         if state_out is None:
-            state_out = torch.empty(states, dtype=torch.float32, device=dev)
+            state_out = torch.empty(states, dtype=f32, device=xbc.device)
         if conv_state_out is None and K:
-            conv_state_out = torch.empty(convs, dtype=io, device=dev)
-        need = gdn_ssm_prefill_workspace_bytes(shape, params)
+            conv_state_out = torch.empty(convs, dtype=io, device=xbc.device)
+        need = lib.gdn_ssm_prefill_workspace_bytes(rs, rp)
         if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=xbc.device)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib.gdn_ssm_prefill(ctypes.byref(shape), ctypes.byref(params), _ptr(xbc), _ptr(dt), _ptr(z), _ptr(conv_weight),
-                                   _ptr(conv_bias), _ptr(conv_state_in), _ptr(conv_state_out), _ptr(A_log), _ptr(dt_bias),
-                                   _ptr(D), _ptr(state_in), _ptr(cu_seqlens), _ptr(y), _ptr(state_out), _ptr(workspace),
-                                   ws_bytes, _stream(stream)))
+        _check(lib.gdn_ssm_prefill(rs, rp, px, pdt, pz, pw, pcb, pci, _arg("conv_state_out", conv_state_out, convs, io, dev),
+                                   pA, pb, pD, psi, pcu, _arg("y", y, (B, T, heads, head_dim), io, dev),
+                                   _arg("state_out", state_out, states, f32, dev),
+                                   None if workspace is None else _arg("workspace", workspace, None, workspace.dtype, dev),
+                                   ws_bytes, _raw_stream(dev)))
     return y, state_out, conv_state_out
 
 
@@ -984,32 +1000,35 @@ def gdn_ssm_decode(xbc, dt, A_log, state, *, heads: int, head_dim: int, d_state:
     ``state`` [E, heads, d_state, head_dim] fp32 and ``conv_state`` [E, K - 1, C] advanced in
     place.  With slots (int32 [B], distinct) row b uses entry slots[b], else entry b (E = B).
     Returns y [B, 1, heads, head_dim]."""
-    lib = load()
-    shape, params = _ssm_geometry(xbc, dt, z, heads, head_dim, groups, d_state, None, conv_weight, conv_activation, dt_min,
-                                  dt_max)
-    io, dev, (B, T, C), K = xbc.dtype, xbc.device, xbc.shape, params.conv_kernel
-    _need_cuda("state", state, torch.float32)
-    E = state.shape[0] if slots is not None and state.dim() == 4 else B
-    _need_shape("state", state, (E, heads, d_state, head_dim), torch.float32)
-    for name, t in (("A_log", A_log), ("dt_bias", dt_bias), ("D", D)):
-        _need_shape(name, t, (heads,), torch.float32)
-    if conv_weight is not None:
-        _need_cuda("conv_weight", conv_weight, io)
-    _need_shape("conv_bias", conv_bias, (C,), io)
-    _need_shape("slots", slots, (B,), torch.int32)
-    _need_shape("y", y, (B, T, heads, head_dim), io)
+    lib = _lib or load()
+    dev = _first("xbc", xbc, 3)
+    if conv_activation not in _CONV_ACT:
+        raise GdnError(GDN_ERR_INVALID_ARG, "the convolution's activation is 'none' or 'silu'")
+    io, (B, T, _) = xbc.dtype, xbc.shape
+    C = heads * head_dim + 2 * groups * d_state
+    K = _conv_taps(conv_weight, C)
     if K > 1 and conv_state is None:
         raise GdnError(GDN_ERR_INVALID_ARG, "conv_state is needed with conv_weight")
-    if K:
-        _need_shape("conv_state", conv_state, (E, K - 1, C), io)
-    _same_device(dev, dt=dt, z=z, A_log=A_log, dt_bias=dt_bias, D=D, conv_weight=conv_weight, conv_bias=conv_bias,
-                 conv_state=conv_state, state=state, slots=slots, y=y)
+    E = state.shape[0] if slots is not None and isinstance(state, torch.Tensor) and state.dim() == 4 else B
+    f32, per_head = torch.float32, (heads,)
+    px, ldx = _rows("xbc", xbc, B, T, (C,), io, dev)
+    pdt, lddt = _rows("dt", dt, B, T, (heads,), io, dev)
+    pz, ldz = (None, 0) if z is None else _rows("z", z, B, T, (heads, head_dim), io, dev)
+    shape = GdnSsmShape(_DTYPE_CODE[io], B, T, B, heads, head_dim, groups, d_state, ldx, lddt, ldz)
+    params = GdnSsmParams(K, _CONV_ACT[conv_activation], dt_min, dt_max)
     with _on(dev, stream):
         if y is None:
-            y = torch.empty((B, T, heads, head_dim), dtype=io, device=dev)
-        _check(lib.gdn_ssm_decode(ctypes.byref(shape), ctypes.byref(params), _ptr(xbc), _ptr(dt), _ptr(z), _ptr(conv_weight),
-                                  _ptr(conv_bias), _ptr(conv_state), _ptr(A_log), _ptr(dt_bias), _ptr(D), _ptr(state), E,
-                                  _ptr(slots), _ptr(y), _stream(stream)))
+            y = torch.empty((B, T, heads, head_dim), dtype=io, device=xbc.device)
+        if state is None:
+            raise GdnError(GDN_ERR_INVALID_ARG, "state is needed")
+        _check(lib.gdn_ssm_decode(ctypes.byref(shape), ctypes.byref(params), px, pdt, pz,
+                                  _arg("conv_weight", conv_weight, None, io, dev), _arg("conv_bias", conv_bias, (C,), io, dev),
+                                  _arg("conv_state", conv_state, (E, K - 1, C), io, dev) if K else None,
+                                  _arg("A_log", A_log, per_head, f32, dev), _arg("dt_bias", dt_bias, per_head, f32, dev),
+                                  _arg("D", D, per_head, f32, dev),
+                                  _arg("state", state, (E, heads, d_state, head_dim), f32, dev), E,
+                                  _arg("slots", slots, (B,), torch.int32, dev),
+                                  _arg("y", y, (B, T, heads, head_dim), io, dev), _raw_stream(dev)))
     return y
 
 
@@ -1029,21 +1048,18 @@ def gdn_rotary_frequencies(rot_dim: int, base: float = 10000.0, kind: str = "pla
     return inv_freq.to(device) if device is not None else inv_freq, scale.value
 
 
-def _head_strides(name: str, t, B: int, T: int, dtype):
-    """(row, head) element strides of t [B, T, H, D], whose rows are evenly spaced."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
-    if t.dim() != 4 or tuple(t.shape[:2]) != (B, T):
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be [{B}, {T}, H, D]")
-    if t.dtype != dtype:
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be {dtype}, got {t.dtype}")
-    H, D = t.shape[2:]
-    if D > 1 and t.stride(3) != 1:
+def _heads(name: str, t, shape, dtype, device: int):
+    """(address, row stride, head stride) of t [B, T, H, D], whose rows are evenly spaced."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype != dtype or t.shape != shape:
+        _bad(name, t, shape, dtype, device)
+    B, T, H, D = shape
+    s0, s1, s2, s3 = t.stride()
+    if D > 1 and s3 != 1:
         raise GdnError(GDN_ERR_INVALID_ARG, f"{name}'s heads must be contiguous")
-    head = t.stride(2) if H > 1 else D
-    if T > 1 and B > 1 and t.stride(0) != T * t.stride(1):
+    head = s2 if H > 1 else D
+    if T > 1 and B > 1 and s0 != T * s1:
         raise GdnError(GDN_ERR_INVALID_ARG, f"{name}'s token rows must be evenly spaced over the batch")
-    return (t.stride(1) if T > 1 else t.stride(0) if B > 1 else max(H * head, D)), head
+    return t.data_ptr(), s1 if T > 1 else s0 if B > 1 else max(H * head, D), head
 
 
 def gdn_rotary(q, k, inv_freq, *, positions=None, cu_seqlens=None, rot_offset: int = 0, interleaved: bool = False,
@@ -1054,36 +1070,28 @@ def gdn_rotary(q, k, inv_freq, *, positions=None, cu_seqlens=None, rot_offset: i
     (2i, 2i + 1) when interleaved, else (i, i + rot_dim / 2); the rest is copied.  positions
     int32 [B, T], or None: a token's place in its sequence (cu_seqlens int32 [N + 1] when packed).
     Heads may be slices of wider rows.  q_out / k_out may be q / k.  Returns (q_out, k_out)."""
-    lib = load()
-    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.dtype not in _DTYPE_CODE:
-        raise GdnError(GDN_ERR_INVALID_ARG, "q must be [B, T, H, D] in float32, bfloat16 or float16")
-    B, T, hq, D = q.shape
-    if k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 4 or k.shape[3] != D):
-        raise GdnError(GDN_ERR_INVALID_ARG, f"k must be [{B}, {T}, H, {D}]")
-    hk = 0 if k is None else k.shape[2]
-    _need_cuda("inv_freq", inv_freq, torch.float32)
-    if inv_freq.dim() != 1:
+    lib = _lib or load()
+    dev = _first("q", q, 4)
+    io, (B, T, hq, D) = q.dtype, q.shape
+    pq, qr, qh = _heads("q", q, q.shape, io, dev)
+    pk, kr, kh, hk = None, 0, 0, 0
+    if k is not None:
+        hk = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+        pk, kr, kh = _heads("k", k, (B, T, hk, D), io, dev)
+    n = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
         raise GdnError(GDN_ERR_INVALID_ARG, "inv_freq must be [rot_dim / 2]")
-    _need_shape("positions", positions, (B, T), torch.int32)
-    if cu_seqlens is not None:
-        _need_shape("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), torch.int32)
-    strides = [*_head_strides("q", q, B, T, q.dtype), *((0, 0) if k is None else _head_strides("k", k, B, T, q.dtype))]
-    _same_device(q.device, k=k, inv_freq=inv_freq, positions=positions, cu_seqlens=cu_seqlens, q_out=q_out, k_out=k_out)
-    with _on(q.device, stream):
+    pf = _arg("inv_freq", inv_freq, None, torch.float32, dev)
+    pp = _arg("positions", positions, (B, T), torch.int32, dev)
+    pc = _arg("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, dev)
+    with _on(dev, stream):
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty(q.shape, dtype=io, device=q.device)
         if k_out is None and k is not None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
-            if like is None:
-                strides += [0, 0]
-                continue
-            strides += _head_strides(name, t, B, T, q.dtype)
-            if t.shape != like.shape:
-                raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be {tuple(like.shape)}")
-        n = B if cu_seqlens is None else cu_seqlens.numel() - 1
-        shape = GdnRotaryShape(_DTYPE_CODE[q.dtype], B, T, n, hq, hk, D, 2 * inv_freq.numel(), rot_offset,
-                               int(bool(interleaved)), int(bool(inverse)), float(scale), *strides)
-        _check(lib.gdn_rotary(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(inv_freq), _ptr(positions), _ptr(cu_seqlens),
-                              _ptr(q_out), _ptr(k_out), _stream(stream)))
+            k_out = torch.empty(k.shape, dtype=io, device=q.device)
+        pqo, qor, qoh = _heads("q_out", q_out, q.shape, io, dev)
+        pko, kor, koh = (None, 0, 0) if k is None else _heads("k_out", k_out, k.shape, io, dev)
+        shape = GdnRotaryShape(_DTYPE_CODE[io], B, T, n, hq, hk, D, 2 * inv_freq.shape[0], rot_offset, bool(interleaved),
+                               bool(inverse), scale, qr, qh, kr, kh, qor, qoh, kor, koh)
+        _check(lib.gdn_rotary(ctypes.byref(shape), pq, pk, pf, pp, pc, pqo, pko, _raw_stream(dev)))
     return q_out, k_out
