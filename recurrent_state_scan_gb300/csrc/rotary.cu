@@ -19,9 +19,10 @@ namespace {
 // is position * 2^-54 turns.  sincospif then takes the nearest 32 bits.
 //
 // A CTA takes `tile` token rows: it fills a table of their cosines and sines, then streams the
-// rows' heads in vectors of V values, two vectors (the V pairs) or one of the copied rest to
-// an item, kItems items in flight to a thread.  Bound by reading and writing the heads.
-constexpr int kThreads = 256, kItems = 4, kMaxPairs = 128, kMaxTile = 8;
+// heads.  A thread's item is a place in the row -- two vectors of V values (the V pairs) or one of
+// the copied rest -- that it follows down the rows, kRows of them in flight.  Bound by reading and
+// writing the heads.
+constexpr int kThreads = 256, kRows = 4, kMaxPairs = 128, kMaxTile = 32;
 
 struct RotaryParams {
     const void *in[2];
@@ -32,6 +33,7 @@ struct RotaryParams {
     const int32_t *positions, *cu_seqlens;   // either may be null
     int64_t rows, seqlen;
     int32_t num_seqs, dim, rot, offset, inverse, tile;
+    int32_t across, down;                    // the CTA's threads: items of a row x rows
     float scale;
     int *status;
 };
@@ -57,91 +59,99 @@ __device__ __forceinline__ int64_t row_position(const RotaryParams &p, int64_t r
 template <typename IO, int V, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) {
     __shared__ uint64_t turns[kMaxPairs];
-    __shared__ float2 cs[kMaxTile * kMaxPairs];
+    extern __shared__ __align__(16) float2 cs[];     // [tile][V][pairs / V]: lanes side by side read side by side
     __shared__ int64_t pos[kMaxTile];
     const int tid = threadIdx.x, half = p.rot / 2;
     const int64_t r0 = (int64_t)blockIdx.x * p.tile;
     const int rows = (int)(p.rows - r0 < p.tile ? p.rows - r0 : p.tile);
-    for (int i = tid; i < half; i += kThreads) {
+    for (int i = tid; i < half; i += blockDim.x) {
         const double t = (double)p.inv_freq[i] * 0.15915494309189533577;   // 1 / 2 pi
         turns[i] = (uint64_t)((t - floor(t)) * 18446744073709551616.0);
     }
-    if (tid < rows) pos[tid] = row_position(p, r0 + tid);
+    for (int i = tid; i < rows; i += blockDim.x) pos[i] = row_position(p, r0 + i);
     __syncthreads();
-    for (int e = tid; e < rows * half; e += kThreads) {
-        const int64_t angle = (int64_t)((uint64_t)pos[e / half] * turns[e % half]);   // 2^-64 turns, in [-1/2, 1/2)
+    const int pairs = half / V;
+    for (int e = tid; e < rows * half; e += blockDim.x) {
+        const int r = e / half, f = e - r * half;
+        const int64_t angle = (int64_t)((uint64_t)pos[r] * turns[f]);      // 2^-64 turns, in [-1/2, 1/2)
         float s, c;
         sincospif((float)(angle >> 32) * 0x1p-31f, &s, &c);
-        cs[e] = make_float2(c * p.scale, p.inverse ? -s * p.scale : s * p.scale);
+        cs[r * half + (f % V) * pairs + f / V] = make_float2(c * p.scale, p.inverse ? -s * p.scale : s * p.scale);
     }
     __syncthreads();
 
-    const int pairs = half / V, items = pairs + (p.dim - p.rot) / V;
-    const int heads = p.heads[0] + p.heads[1], per_row = heads * items, total = rows * per_row;
-    for (int base = tid; base < total; base += kThreads * kItems) {
-        Vec<IO, V> a[kItems], b[kItems];
-        IO *to[kItems];
-        int at[kItems];     // index of the item's first pair in cs, or -1: a copied vector
+    const int items = pairs + (p.dim - p.rot) / V, per_row = (p.heads[0] + p.heads[1]) * items;
+    const int down = tid / p.across;
+    if (down >= p.down) return;
+    for (int it = tid - down * p.across; it < per_row; it += p.across) {
+        const int hd = it / items, j = it - hd * items;
+        const int which = hd >= p.heads[0], h = hd - (which ? p.heads[0] : 0);
+        const bool turn = j < pairs;
+        const int e = (j - pairs) * V;
+        const int d = turn ? p.offset + (kInterleaved ? 2 : 1) * V * j : e < p.offset ? e : e + p.rot;
+        const IO *src = static_cast<const IO *>(p.in[which]) + r0 * p.in_row[which] + h * p.in_head[which] + d;
+        IO *dst = static_cast<IO *>(p.out[which]) + r0 * p.out_row[which] + h * p.out_head[which] + d;
+        const int next = kInterleaved ? V : half;
+        for (int rb = down; rb < rows; rb += kRows * p.down) {
+            Vec<IO, V> a[kRows], b[kRows];
 #pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-            const int it = base + k * kThreads;
-            if (it >= total) break;
-            const int row = it / per_row, in_row = it - row * per_row;
-            const int hd = in_row / items, j = in_row - hd * items;
-            const int which = hd >= p.heads[0], h = hd - (which ? p.heads[0] : 0);
-            const IO *src = static_cast<const IO *>(p.in[which]) + (r0 + row) * p.in_row[which] + h * p.in_head[which];
-            IO *dst = static_cast<IO *>(p.out[which]) + (r0 + row) * p.out_row[which] + h * p.out_head[which];
-            if (j < pairs) {
-                const int d = p.offset + (kInterleaved ? 2 : 1) * V * j;
-                a[k] = *reinterpret_cast<const Vec<IO, V> *>(src + d);
-                b[k] = *reinterpret_cast<const Vec<IO, V> *>(src + d + (kInterleaved ? V : half));
-                to[k] = dst + d;
-                at[k] = row * half + V * j;
-            } else {
-                const int e = (j - pairs) * V, d = e < p.offset ? e : e + p.rot;
-                a[k] = *reinterpret_cast<const Vec<IO, V> *>(src + d);
-                to[k] = dst + d;
-                at[k] = -1;
+            for (int k = 0; k < kRows; ++k) {
+                const int r = rb + k * p.down;
+                if (r < rows) {
+                    a[k] = *reinterpret_cast<const Vec<IO, V> *>(src + r * p.in_row[which]);
+                    if (turn) b[k] = *reinterpret_cast<const Vec<IO, V> *>(src + r * p.in_row[which] + next);
+                }
             }
-        }
 #pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-            if (base + k * kThreads >= total) break;
-            if (at[k] >= 0) {
-                float x[2 * V];
+            for (int k = 0; k < kRows; ++k) {
+                const int r = rb + k * p.down;
+                if (r >= rows) break;
+                if (turn) {
+                    float x[2 * V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    x[i] = IoType<IO>::ld(&a[k].v[i]);
-                    x[V + i] = IoType<IO>::ld(&b[k].v[i]);
+                    for (int i = 0; i < V; ++i) {
+                        x[i] = IoType<IO>::ld(&a[k].v[i]);
+                        x[V + i] = IoType<IO>::ld(&b[k].v[i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float2 t = cs[r * half + i * pairs + j];
+                        float &u = x[kInterleaved ? 2 * i : i], &v = x[kInterleaved ? 2 * i + 1 : V + i];
+                        const float w = u * t.x - v * t.y;
+                        v = v * t.x + u * t.y;
+                        u = w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        IoType<IO>::st(&a[k].v[i], x[i]);
+                        IoType<IO>::st(&b[k].v[i], x[V + i]);
+                    }
+                    *reinterpret_cast<Vec<IO, V> *>(dst + r * p.out_row[which] + next) = b[k];
                 }
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float2 t = cs[at[k] + i];
-                    float &u = x[kInterleaved ? 2 * i : i], &v = x[kInterleaved ? 2 * i + 1 : V + i];
-                    const float w = u * t.x - v * t.y;
-                    v = v * t.x + u * t.y;
-                    u = w;
-                }
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    IoType<IO>::st(&a[k].v[i], x[i]);
-                    IoType<IO>::st(&b[k].v[i], x[V + i]);
-                }
-                *reinterpret_cast<Vec<IO, V> *>(to[k] + (kInterleaved ? V : half)) = b[k];
+                *reinterpret_cast<Vec<IO, V> *>(dst + r * p.out_row[which]) = a[k];
             }
-            *reinterpret_cast<Vec<IO, V> *>(to[k]) = a[k];
         }
     }
 }
 
 template <typename IO>
-cudaError_t rotary_launch(const RotaryParams &p, bool interleaved, bool wide, cudaStream_t stream) {
-    constexpr int W = 16 / sizeof(IO);
-    const unsigned grid = (unsigned)((p.rows + p.tile - 1) / p.tile);
-    if (wide && interleaved) rotary_kernel<IO, W, true><<<grid, kThreads, 0, stream>>>(p);
-    else if (wide) rotary_kernel<IO, W, false><<<grid, kThreads, 0, stream>>>(p);
-    else if (interleaved) rotary_kernel<IO, 1, true><<<grid, kThreads, 0, stream>>>(p);
-    else rotary_kernel<IO, 1, false><<<grid, kThreads, 0, stream>>>(p);
+cudaError_t rotary_launch(RotaryParams p, bool interleaved, bool wide, cudaStream_t stream) {
+    const int V = wide ? 16 / (int)sizeof(IO) : 1;
+    // Threads: a row's items in as few equal turns as fit the CTA, rows side by side where they are few.
+    const int per_row = (p.heads[0] + p.heads[1]) * (p.rot / 2 / V + (p.dim - p.rot) / V);
+    const int turns = (per_row + kThreads - 1) / kThreads;
+    p.across = (per_row + turns - 1) / turns;
+    // Rows to a CTA: enough CTAs for eight to an SM, up to kMaxTile rows each.
+    p.tile = (int32_t)(p.rows / 1216);
+    p.tile = p.tile < 1 ? 1 : p.tile > kMaxTile ? kMaxTile : p.tile;
+    p.down = kThreads / p.across;
+    if (p.down > p.tile) p.down = p.tile;
+    const unsigned grid = (unsigned)((p.rows + p.tile - 1) / p.tile), threads = (unsigned)((p.across * p.down + 31) / 32 * 32);
+    const size_t smem = (size_t)p.tile * (p.rot / 2) * sizeof(float2);
+    if (wide && interleaved) rotary_kernel<IO, 16 / sizeof(IO), true><<<grid, threads, smem, stream>>>(p);
+    else if (wide) rotary_kernel<IO, 16 / sizeof(IO), false><<<grid, threads, smem, stream>>>(p);
+    else if (interleaved) rotary_kernel<IO, 1, true><<<grid, threads, smem, stream>>>(p);
+    else rotary_kernel<IO, 1, false><<<grid, threads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -214,7 +224,6 @@ extern "C" gdn_status gdn_rotary(const gdn_rotary_shape *s, const void *q, const
     p.rows = rows; p.seqlen = s->seqlen; p.num_seqs = s->num_seqs;
     p.dim = s->head_dim; p.rot = s->rot_dim; p.offset = s->rot_offset; p.inverse = s->inverse != 0;
     p.scale = s->scale; p.status = word;
-    p.tile = rows >= 4096 ? 4 : 1;
     cudaError_t e;
     const bool il = s->interleaved != 0;
     if (s->io_dtype == GDN_F32) e = rotary_launch<float>(p, il, wide, (cudaStream_t)stream);

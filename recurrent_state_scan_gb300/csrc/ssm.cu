@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "ssm_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace gdn {
 namespace {
@@ -18,35 +19,47 @@ namespace {
 // Products of two 16-bit values are exact in fp32, so the sum's order alone decides its
 // value: bias first, then the taps in order.  Bound by reading and writing the rows; the
 // arithmetic (13 instructions a value) takes nearly as long.
-constexpr int kRun = 32, kAhead = 4;
+constexpr int kRun = 33, kAhead = 3;
 
 template <typename IO, int V> struct alignas(sizeof(IO) * V) Pack {
     IO v[V];
 };
 
-// silu of V values, each rounded to IO as silu_exact rounds.  For 16-bit types the fast form
-// serves unless one of them is within 32 fp32 steps of the border between two 16-bit values: below
-// |v| = 8 it is within 12 of the exact form (6 from the exponent's rounding, 2 in the exponential,
-// 1 in the reciprocal, the rest in the roundings between).
+// silu of V values, each rounded to IO as silu_exact rounds.  For 16-bit types a fast form serves
+// where it is not within 8 fp32 steps of the border between two 16-bit values: with its exponent
+// carried in two terms it is within 6 of silu_exact (2 in the exponential, 1 in the reciprocal,
+// half a step in each of the operations between, and silu_exact's own 1), below |v| = 64.
+__device__ __noinline__ float silu_apart(float v) { return silu_exact(v); }
+
 template <typename IO, int V> __device__ __forceinline__ void silu_rounded(float (&v)[V]) {
-    if constexpr (sizeof(IO) == 2) {
-        constexpr uint32_t kCut = std::is_same<IO, __half>::value ? 0x1fffu : 0xffffu;    // bits that the rounding drops
-        float f[V];
-        uint32_t near = 0;
-        float top = 0.f, least = 1.f;
+    if constexpr (sizeof(IO) == 2 && V % 2 == 0) {
+        constexpr bool kHalf = std::is_same<IO, __half>::value;
+        constexpr uint32_t kCut = kHalf ? 0x1fffu : 0xffffu;    // bits that the rounding drops
+        constexpr float kHi = -kLog2e, kLo = -1.925963033e-8f;  // -log2 e in two terms
+        float f[V], top = 0.f, low = 1.f;
+        uint32_t off = ~0u;
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const F2 x = {v[i], v[i + 1]}, t = mul2(x, both(kHi));
+            const F2 rest = fma2(x, both(kLo), fma2(x, both(kHi), {-t.x, -t.y}));
+            F2 e = {ex2(t.x), ex2(t.y)};
+            e = fma2(e, mul2(rest, both(0.69314718f)), e);
+            const F2 d = add2(e, both(1.f)), y = mul2(x, {rcp(d.x), rcp(d.y)});
+            f[i] = y.x;
+            f[i + 1] = y.y;
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            f[i] = v[i] * rcp(1.f + ex2(-kLog2e * v[i]));
-            near |= ((__float_as_uint(f[i]) + 32u + (kCut + 1) / 2) & kCut) < 64u;
+            off = min(off, (__float_as_uint(f[i]) + 8u + (kCut + 1) / 2) & (kCut & ~15u));   // 0: near a border
             top = fmaxf(top, fabsf(v[i]));
-            if (kCut == 0x1fffu) least = fminf(least, fabsf(f[i]));    // (f16's subnormals round elsewhere)
+            if (kHalf) low = fminf(low, fabsf(f[i]));    // (f16's subnormals round elsewhere)
         }
-        if (!near && top < 8.f && (kCut != 0x1fffu || least > 0x1p-13f)) {
+        const bool sure = off != 0 && top < 64.f && (!kHalf || low > 0x1p-13f);
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = f[i];
-            return;
-        }
+        for (int i = 0; i < V; ++i) v[i] = sure ? f[i] : silu_apart(v[i]);
+        return;
     }
+#pragma unroll
     for (int i = 0; i < V; ++i) v[i] = silu_exact(v[i]);
 }
 
@@ -134,17 +147,21 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
         else if (cin) v = *reinterpret_cast<const Vec *>(cin + (n * (K - 1) + (K - 1) + (at - t0)) * p.C);
         widen<IO, V>(v, past[j]);
     }
+    const int left = (int)(r1 - r0);            // rows of this run, and of its first sequence
+    int turn = t1 - r0 < left ? (int)(t1 - r0) : left;
+    const IO *px = x + r0 * p.ld_x;
+    u += r0 * p.ld_u;
     Vec in[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-        if (r0 + i < r1) in[i] = *reinterpret_cast<const Vec *>(x + (r0 + i) * p.ld_x);
+    for (int i = 0; i < kAhead; ++i, px += p.ld_x)
+        if (i < left) in[i] = *reinterpret_cast<const Vec *>(px);
 #pragma unroll 1
-    for (int64_t rb = r0; rb < r1; rb += kAhead) {
+    for (int done = 0; done < left; done += kAhead) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int64_t r = rb + i;
-            if (r >= r1) break;
-            if (r >= t1) {                  // the next sequence that has a row
+        for (int i = 0; i < kAhead; ++i, px += p.ld_x, u += p.ld_u) {
+            if (done + i >= left) break;
+            if (done + i >= turn) {             // the next sequence that has a row
+                const int64_t r = r0 + done + i;
                 if (p.cu_seqlens == nullptr) {
                     ++n;
                     t1 += p.seqlen;
@@ -155,6 +172,7 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
                     t1 = p.cu_seqlens[n + 1];
                     if (t1 <= r) t1 = p.rows;
                 }
+                turn = t1 - r0 < left ? (int)(t1 - r0) : left;
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j)
                     widen<IO, V>(cin ? *reinterpret_cast<const Vec *>(cin + (n * (K - 1) + j) * p.C) : zero, past[j]);
@@ -162,7 +180,7 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
             Vec out = in[i];
             float now[V];
             widen<IO, V>(in[i], now);
-            if (r + kAhead < r1) in[i] = *reinterpret_cast<const Vec *>(x + (r + kAhead) * p.ld_x);
+            if (done + i + kAhead < left) in[i] = *reinterpret_cast<const Vec *>(px);
             if (p.w != nullptr) {
                 float acc[V];
                 if constexpr (V % 2 == 0) {
@@ -185,7 +203,7 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
 #pragma unroll
                 for (int v = 0; v < V; ++v) IoType<IO>::st(&out.v[v], acc[v]);
             }
-            *reinterpret_cast<Vec *>(u + r * p.ld_u) = out;
+            *reinterpret_cast<Vec *>(u) = out;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
 #pragma unroll
@@ -213,8 +231,10 @@ cudaError_t conv_launch(const SsmConvParams &p, cudaStream_t stream) {
 
 template <typename IO>
 cudaError_t conv_dispatch(const SsmConvParams &p, cudaStream_t stream) {
-    constexpr int V = 16 / sizeof(IO);
-    auto ok = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+    // Four channels: eight of a 16-bit type took 144 registers, and with 12 warps to an SM 91 us for
+    // 8,192 rows of 4,352 channels where four take CONV4 us.
+    constexpr int V = 4;
+    auto ok = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & (V * sizeof(IO) - 1)) == 0; };
     const bool wide = p.head_dim % V == 0 && p.d_state % V == 0 && p.ld_x % V == 0 && p.ld_u % V == 0 && ok(p.x) && ok(p.u) &&
                       ok(p.conv_in) && ok(p.conv_out) && p.x_head % V == 0 && p.off_b % V == 0 && p.off_c % V == 0 &&
                       p.bc_group % V == 0;
@@ -357,7 +377,7 @@ cudaError_t scan_dispatch(const SsmParams &p, cudaStream_t stream) {
 // A CTA takes one (row, head): its state [N][P] as float4 quads, a thread's quads all of one
 // column quad, kDecQuads of them in flight while the row's convolution and gates are
 // computed.  Bound by reading and writing the state.
-constexpr int kDecThreads = 256, kDecQuads = 8;
+constexpr int kDecThreads = 256, kDecQuads = 8, kSms = 152;
 
 template <typename IO>
 __device__ __forceinline__ float conv_token(const SsmDecodeParams &p, const IO *x, const IO *conv, int c) {
@@ -449,6 +469,164 @@ __global__ void __launch_bounds__(kDecThreads, 4) ssm_decode_kernel(const SsmDec
     }
 }
 
+// The same for states of up to kStreamState values, by a persistent CTA: a contiguous run of
+// (row, head) units, whose states pass through a ring of kRing stages in shared memory by bulk
+// copies in both directions.  The convolved B and C of a (row, group) are kept for all of its
+// heads, and the next unit's inputs are loaded while this one is computed.  Two CTAs to an SM
+// keep 128 KB of loads in flight.
+constexpr int kStreamState = 8192, kRing = 3, kSlots = 3;
+
+template <typename IO>
+__global__ void __launch_bounds__(kDecThreads, 2) ssm_decode_stream_kernel(const SsmDecodeParams p, int64_t units) {
+    using namespace tc;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float sB[256], sC[256], sx[256];
+    __shared__ __align__(16) float red[kDecThreads * 4];
+    __shared__ uint64_t full[kRing];
+    const int tid = threadIdx.x;
+    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+    const int count = (int)(u1 - u0);
+    const int N = p.d_state, P = p.head_dim, Q = P / 4, RP = kDecThreads / Q, hpg = p.heads / p.groups;
+    const int hp = p.heads * P, gn = p.groups * N, quad = tid % Q, r0 = tid / Q;
+    const uint32_t bytes = (uint32_t)N * P * 4;
+    if (tid == 0) {
+        for (int i = 0; i < kRing; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    auto state_of = [&](int64_t u) -> float * {      // null: a slot outside the pool
+        const int64_t b = u / p.heads, e = p.slots ? (int64_t)p.slots[b] : b;
+        return e < 0 || e >= p.pool_size ? nullptr : p.state + (e * p.heads + u % p.heads) * (int64_t)N * P;
+    };
+    auto fetch = [&](int i) {                        // (one thread) unit i's state into its stage
+        const float *from = state_of(u0 + i);
+        if (from == nullptr) {
+            mbar_arrive(&full[i % kRing]);
+            return;
+        }
+        mbar_arrive_expect_tx(&full[i % kRing], bytes);
+        bulk_load(ring + (size_t)(i % kRing) * bytes, from, bytes, &full[i % kRing]);
+    };
+
+    // Inputs of the next unit, as they come: up to kSlots channels of [x | B | C] to a thread.
+    IO raw[kSlots][4], w[kSlots][4], bias[kSlots], raw_dt;
+    float A = 0.f, db = 0.f, D = 0.f;
+    IoType<IO>::st(&raw_dt, 0.f);
+    int have = 0;                                    // channels of this thread among them
+    bool fresh = false;                              // the unit begins another (row, group)
+    auto gather = [&](int64_t u) {
+        const int64_t b = u / p.heads;
+        const int h = (int)(u % p.heads), g = h / hpg;
+        fresh = u == u0 || h % hpg == 0;
+        const int64_t e = p.slots ? (int64_t)p.slots[b] : b;
+        have = 0;
+        raw_dt = static_cast<const IO *>(p.dt)[b * p.ld_dt + h];
+        A = p.A_log[h];
+        db = p.dt_bias ? p.dt_bias[h] : 0.f;
+        D = p.D ? p.D[h] : 0.f;
+        if (e < 0 || e >= p.pool_size) return;
+        const IO *x = static_cast<const IO *>(p.x) + b * p.ld_x;
+        const IO *conv = p.conv ? static_cast<const IO *>(p.conv) + e * (int64_t)(p.K - 1) * p.C : nullptr;
+        const int n = fresh ? P + 2 * N : P;
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+            const int i = tid + j * kDecThreads;
+            if (i >= n) break;
+            const int c = i < P ? h * P + i : i < P + N ? hp + g * N + i - P : hp + gn + g * N + i - P - N;
+            raw[j][3] = x[c];
+            if (p.w != nullptr) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {        // (the last tap stands last)
+                    const int tap = k - (4 - p.K);
+                    if (tap >= 0) w[j][k] = static_cast<const IO *>(p.w)[(int64_t)c * p.K + tap];
+                    if (tap >= 0 && k < 3) raw[j][k] = conv[(int64_t)tap * p.C + c];
+                }
+                if (p.bias) bias[j] = static_cast<const IO *>(p.bias)[c];
+            }
+            have = j + 1;
+        }
+    };
+    float d = 0.f, a = 0.f, skip = 0.f;
+    auto settle = [&]() {                            // the gathered inputs into place
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+            if (j >= have) break;
+            const int i = tid + j * kDecThreads;
+            float v = IoType<IO>::ld(&raw[j][3]);
+            if (p.w != nullptr) {
+                float acc = p.bias ? IoType<IO>::ld(&bias[j]) : 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k >= 4 - p.K) acc = fmaf(IoType<IO>::ld(&w[j][k]), IoType<IO>::ld(&raw[j][k]), acc);
+                IO out;
+                IoType<IO>::st(&out, p.silu ? silu_exact(acc) : acc);
+                v = IoType<IO>::ld(&out);
+            }
+            (i < P ? sx[i] : i < P + N ? sB[i - P] : sC[i - P - N]) = v;
+        }
+        d = ssm_step(IoType<IO>::ld(&raw_dt), db, p.dt_min, p.dt_max);
+        a = expf(-expf(A) * d);
+        skip = D;
+    };
+
+    __syncthreads();
+    if (tid == 0)
+        for (int i = 0; i < kRing - 1 && i < count; ++i) fetch(i);
+    if (count > 0) {
+        gather(u0);
+        settle();
+    }
+    __syncthreads();
+    for (int i = 0; i < count; ++i) {
+        const int64_t u = u0 + i, b = u / p.heads;
+        const int h = (int)(u % p.heads);
+        float *state = state_of(u);
+        const bool live = state != nullptr;
+        if (tid == 0 && i + kRing - 1 < count) {
+            bulk_wait_read();                        // the stage's state has gone out
+            fetch(i + kRing - 1);
+        }
+        if (i + 1 < count) gather(u + 1);
+        const int64_t yc = (int64_t)h * P + tid;
+        float gate = 1.f;
+        if (p.z && tid < P) gate = silu_gate(IoType<IO>::ld(static_cast<const IO *>(p.z) + b * p.ld_z + yc));
+        const bool ok = mbar_wait(&full[i % kRing], (i / kRing) & 1, 4000000000LL);
+        if (!ok) atomicOr(p.status, kDevTimeout);
+        float4 *S = reinterpret_cast<float4 *>(ring + (size_t)(i % kRing) * bytes) + quad;
+        if (live && ok && r0 < RP) {
+            const float4 dx = make_float4(d * sx[4 * quad], d * sx[4 * quad + 1], d * sx[4 * quad + 2], d * sx[4 * quad + 3]);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int n = r0; n < N; n += RP) {
+                const float bn = sB[n], cn = sC[n];
+                float4 v = S[(size_t)n * Q];
+                v.x = fmaf(a, v.x, bn * dx.x); v.y = fmaf(a, v.y, bn * dx.y);
+                v.z = fmaf(a, v.z, bn * dx.z); v.w = fmaf(a, v.w, bn * dx.w);
+                acc.x = fmaf(cn, v.x, acc.x); acc.y = fmaf(cn, v.y, acc.y);
+                acc.z = fmaf(cn, v.z, acc.z); acc.w = fmaf(cn, v.w, acc.w);
+                S[(size_t)n * Q] = v;
+            }
+            reinterpret_cast<float4 *>(red)[tid] = acc;
+        }
+        fence_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+            if (live && ok) bulk_store(state, ring + (size_t)(i % kRing) * bytes, bytes);
+            else if (!live) atomicOr(p.status, kDevBadSlot);
+            bulk_commit();
+        }
+        if (live && tid < P) {
+            float out = 0.f;
+            for (int r = 0; r < RP; ++r) out += red[r * P + tid];
+            out = fmaf(skip, sx[tid], out) * gate;
+            IoType<IO>::st(static_cast<IO *>(p.y) + b * (int64_t)hp + yc, out);
+        }
+        __syncthreads();                             // sx, sB, sC and red are free
+        if (i + 1 < count) settle();
+        __syncthreads();
+    }
+    if (tid == 0) bulk_wait_all();
+}
+
 // The conv states one token on, after the step has read them: rows move up, x comes last.
 // (The step's CTAs all read their group's B and C taps, so it cannot move them itself.)
 template <typename IO>
@@ -465,7 +643,17 @@ __global__ void __launch_bounds__(256) ssm_conv_shift_kernel(const SsmDecodePara
 
 template <typename IO>
 cudaError_t decode_dispatch(const SsmDecodeParams &p, cudaStream_t stream) {
-    ssm_decode_kernel<IO><<<(unsigned)(p.heads * p.batch), kDecThreads, 0, stream>>>(p);
+    const int64_t units = (int64_t)p.heads * p.batch;
+    if (p.d_state * p.head_dim <= kStreamState) {
+        const int smem = kRing * p.d_state * p.head_dim * 4;
+        const cudaError_t e = cudaFuncSetAttribute(ssm_decode_stream_kernel<IO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kRing * kStreamState * 4);
+        if (e != cudaSuccess) return e;
+        const unsigned grid = (unsigned)(units < 2 * kSms ? units : 2 * kSms);
+        ssm_decode_stream_kernel<IO><<<grid, kDecThreads, smem, stream>>>(p, units);
+    } else {
+        ssm_decode_kernel<IO><<<(unsigned)units, kDecThreads, 0, stream>>>(p);
+    }
     if (p.w != nullptr && p.K > 1)
         ssm_conv_shift_kernel<IO><<<dim3((unsigned)p.batch, (unsigned)((p.C + 255) / 256)), 256, 0, stream>>>(p);
     return cudaGetLastError();
