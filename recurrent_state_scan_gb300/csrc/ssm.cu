@@ -29,10 +29,12 @@ template <typename IO, int V> struct alignas(sizeof(IO) * V) Pack {
 // where it is not within 8 fp32 steps of the border between two 16-bit values: with its exponent
 // carried in two terms it is within 6 of silu_exact (2 in the exponential, 1 in the reciprocal,
 // half a step in each of the operations between, and silu_exact's own 1), below |v| = 64.
-__device__ __noinline__ float silu_apart(float v) { return silu_exact(v); }
+__device__ __noinline__ float4 silu_apart(float4 v) {
+    return make_float4(silu_exact(v.x), silu_exact(v.y), silu_exact(v.z), silu_exact(v.w));
+}
 
 template <typename IO, int V> __device__ __forceinline__ void silu_rounded(float (&v)[V]) {
-    if constexpr (sizeof(IO) == 2 && V % 2 == 0) {
+    if constexpr (sizeof(IO) == 2 && V == 4) {
         constexpr bool kHalf = std::is_same<IO, __half>::value;
         constexpr uint32_t kCut = kHalf ? 0x1fffu : 0xffffu;    // bits that the rounding drops
         constexpr float kHi = -kLog2e, kLo = -1.925963033e-8f;  // -log2 e in two terms
@@ -55,17 +57,88 @@ template <typename IO, int V> __device__ __forceinline__ void silu_rounded(float
             if (kHalf) low = fminf(low, fabsf(f[i]));    // (f16's subnormals round elsewhere)
         }
         const bool sure = off != 0 && top < 64.f && (!kHalf || low > 0x1p-13f);
+        if (!sure) {
+            const float4 s = silu_apart(make_float4(v[0], v[1], v[2], v[3]));
+            f[0] = s.x; f[1] = s.y; f[2] = s.z; f[3] = s.w;
+        }
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = sure ? f[i] : silu_apart(v[i]);
-        return;
+        for (int i = 0; i < V; ++i) v[i] = f[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = silu_exact(v[i]);
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = silu_exact(v[i]);
 }
 
 template <typename IO, int V> __device__ __forceinline__ void widen(const Pack<IO, V> &a, float (&f)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = IoType<IO>::ld(&a.v[i]);
+}
+
+// The last K - 1 inputs of sequence n: its own rows, or past ones where it is short.
+template <typename IO, int V, int K>
+__device__ __forceinline__ void conv_states(const SsmConvParams &p, int64_t n, int c0) {
+    using Vec = Pack<IO, V>;
+    int64_t t0, t1;
+    if (!seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, n, t0, t1)) return;
+    const IO *x = static_cast<const IO *>(p.x) + c0, *cin = p.conv_in ? static_cast<const IO *>(p.conv_in) + c0 : nullptr;
+    IO *out = static_cast<IO *>(p.conv_out) + (n * (K - 1)) * p.C + c0;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+        const int64_t at = t1 - (K - 1) + j;
+        Vec v;
+#pragma unroll
+        for (int i = 0; i < V; ++i) IoType<IO>::st(&v.v[i], 0.f);
+        if (at >= t0) v = *reinterpret_cast<const Vec *>(x + at * p.ld_x);
+        else if (cin) v = *reinterpret_cast<const Vec *>(cin + (n * (K - 1) + (t1 - t0) + j) * p.C);
+        *reinterpret_cast<Vec *>(out + (int64_t)j * p.C) = v;
+    }
+}
+
+// The sequence of a run of rows and the walk along it, for both convolution kernels.
+struct Walk {
+    int64_t n, t0, t1;      // sequence, its first row, the row behind it
+};
+__device__ __forceinline__ Walk walk_from(const SsmConvParams &p, int64_t r0) {
+    Walk w{0, 0, p.rows};
+    if (p.cu_seqlens == nullptr) {
+        w.n = r0 / p.seqlen;
+        w.t0 = w.n * p.seqlen;
+        w.t1 = w.t0 + p.seqlen;
+        return w;
+    }
+    int64_t lo = 0, hi = p.num_seqs - 1;         // the last sequence whose first row is not behind r0
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) >> 1;
+        if (p.cu_seqlens[mid] <= r0) lo = mid;
+        else hi = mid - 1;
+    }
+    w.n = lo;
+    w.t0 = p.cu_seqlens[lo];
+    w.t1 = p.cu_seqlens[lo + 1];
+    if (w.t0 < 0 || w.t0 > r0) w.t0 = r0;        // malformed offsets: stay inside the rows (the scan reports them)
+    if (w.t1 <= r0) w.t1 = r0 + 1;
+    return w;
+}
+// The next sequence that has row r; false: none.
+__device__ __forceinline__ bool walk_on(const SsmConvParams &p, Walk &w, int64_t r) {
+    if (p.cu_seqlens == nullptr) {
+        ++w.n;
+        w.t1 += p.seqlen;
+        return true;
+    }
+    do ++w.n;
+    while (w.n + 1 < p.num_seqs && p.cu_seqlens[w.n + 1] <= r);
+    if (w.n >= p.num_seqs) return false;
+    w.t1 = p.cu_seqlens[w.n + 1];
+    if (w.t1 <= r) w.t1 = p.rows;
+    return true;
+}
+// Where channel c0 of a row of x stands in a row of u.
+__device__ __forceinline__ int64_t u_channel(const SsmConvParams &p, int c0) {
+    const int hp = p.heads * p.head_dim, gn = p.groups * p.d_state;
+    if (c0 < hp) return (int64_t)(c0 / p.head_dim) * p.x_head + c0 % p.head_dim;
+    const int b = c0 - hp, in = b % gn;
+    return (b < gn ? p.off_b : p.off_c) + (int64_t)(in / p.d_state) * p.bc_group + in % p.d_state;
 }
 
 template <typename IO, int V, int K>
@@ -74,39 +147,16 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
     const int64_t cv = (int64_t)blockIdx.y * 128 + threadIdx.x;      // channel vector
     if (cv * V >= p.C) return;
     const int c0 = (int)cv * V;
+    if ((int64_t)blockIdx.x >= run_blocks) {
+        conv_states<IO, V, K>(p, (int64_t)blockIdx.x - run_blocks, c0);
+        return;
+    }
     const IO *x = static_cast<const IO *>(p.x) + c0;
     const IO *cin = p.conv_in ? static_cast<const IO *>(p.conv_in) + c0 : nullptr;
     Vec zero;
 #pragma unroll
     for (int i = 0; i < V; ++i) IoType<IO>::st(&zero.v[i], 0.f);
-
-    if ((int64_t)blockIdx.x >= run_blocks) {
-        // The last K - 1 inputs of one sequence: its own rows, or past ones where it is short.
-        const int64_t n = (int64_t)blockIdx.x - run_blocks;
-        int64_t t0, t1;
-        if (!seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, n, t0, t1)) return;
-        IO *out = static_cast<IO *>(p.conv_out) + (n * (K - 1)) * p.C + c0;
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j) {
-            const int64_t at = t1 - (K - 1) + j;
-            Vec v = zero;
-            if (at >= t0) v = *reinterpret_cast<const Vec *>(x + at * p.ld_x);
-            else if (cin) v = *reinterpret_cast<const Vec *>(cin + (n * (K - 1) + (t1 - t0) + j) * p.C);
-            *reinterpret_cast<Vec *>(out + (int64_t)j * p.C) = v;
-        }
-        return;
-    }
-
-    // Where this thread's channels stand in a row of u.
-    int64_t uc;
-    const int hp = p.heads * p.head_dim, gn = p.groups * p.d_state;
-    if (c0 < hp) {
-        uc = (int64_t)(c0 / p.head_dim) * p.x_head + c0 % p.head_dim;
-    } else {
-        const int b = c0 - hp, in = b % gn;
-        uc = (b < gn ? p.off_b : p.off_c) + (int64_t)(in / p.d_state) * p.bc_group + in % p.d_state;
-    }
-    IO *u = static_cast<IO *>(p.u) + uc;
+    IO *u = static_cast<IO *>(p.u) + u_channel(p, c0);
     float w[K][V], bias[V];
     if (p.w != nullptr) {
 #pragma unroll
@@ -119,36 +169,18 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
 
     const int64_t r0 = (int64_t)blockIdx.x * kRun;
     const int64_t r1 = r0 + kRun < p.rows ? r0 + kRun : p.rows;
-    // The sequence of row r0: the last whose first row is not behind it.
-    int64_t n = 0, t0 = 0, t1 = p.rows;
-    if (p.cu_seqlens == nullptr) {
-        n = r0 / p.seqlen;
-        t0 = n * p.seqlen;
-        t1 = t0 + p.seqlen;
-    } else {
-        int64_t lo = 0, hi = p.num_seqs - 1;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi + 1) >> 1;
-            if (p.cu_seqlens[mid] <= r0) lo = mid;
-            else hi = mid - 1;
-        }
-        n = lo;
-        t0 = p.cu_seqlens[n];
-        t1 = p.cu_seqlens[n + 1];
-        if (t0 < 0 || t0 > r0) t0 = r0;     // malformed offsets: stay inside the rows (the scan reports them)
-        if (t1 <= r0) t1 = r0 + 1;
-    }
+    Walk seq = walk_from(p, r0);
     float past[K > 1 ? K - 1 : 1][V];
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
         const int64_t at = r0 - (K - 1) + j;
         Vec v = zero;
-        if (at >= t0) v = *reinterpret_cast<const Vec *>(x + at * p.ld_x);
-        else if (cin) v = *reinterpret_cast<const Vec *>(cin + (n * (K - 1) + (K - 1) + (at - t0)) * p.C);
+        if (at >= seq.t0) v = *reinterpret_cast<const Vec *>(x + at * p.ld_x);
+        else if (cin) v = *reinterpret_cast<const Vec *>(cin + (seq.n * (K - 1) + (K - 1) + (at - seq.t0)) * p.C);
         widen<IO, V>(v, past[j]);
     }
     const int left = (int)(r1 - r0);            // rows of this run, and of its first sequence
-    int turn = t1 - r0 < left ? (int)(t1 - r0) : left;
+    int turn = seq.t1 - r0 < left ? (int)(seq.t1 - r0) : left;
     const IO *px = x + r0 * p.ld_x;
     u += r0 * p.ld_u;
     Vec in[kAhead];
@@ -161,21 +193,11 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
         for (int i = 0; i < kAhead; ++i, px += p.ld_x, u += p.ld_u) {
             if (done + i >= left) break;
             if (done + i >= turn) {             // the next sequence that has a row
-                const int64_t r = r0 + done + i;
-                if (p.cu_seqlens == nullptr) {
-                    ++n;
-                    t1 += p.seqlen;
-                } else {
-                    do ++n;
-                    while (n + 1 < p.num_seqs && p.cu_seqlens[n + 1] <= r);
-                    if (n >= p.num_seqs) return;
-                    t1 = p.cu_seqlens[n + 1];
-                    if (t1 <= r) t1 = p.rows;
-                }
-                turn = t1 - r0 < left ? (int)(t1 - r0) : left;
+                if (!walk_on(p, seq, r0 + done + i)) return;
+                turn = seq.t1 - r0 < left ? (int)(seq.t1 - r0) : left;
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j)
-                    widen<IO, V>(cin ? *reinterpret_cast<const Vec *>(cin + (n * (K - 1) + j) * p.C) : zero, past[j]);
+                    widen<IO, V>(cin ? *reinterpret_cast<const Vec *>(cin + (seq.n * (K - 1) + j) * p.C) : zero, past[j]);
             }
             Vec out = in[i];
             float now[V];
@@ -214,6 +236,114 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
     }
 }
 
+// The convolution of 16-bit rows that bulk copies can take (16-byte rows and channel runs): a CTA
+// takes 512 channels of a run of kBulkRun rows, which arrive kStageRows at a time in a ring of
+// kBulkRing stages; a thread reads its four channels of each row once, the last K - 1 rows kept in
+// registers, and writes them straight out.  (The kernel above, with its loads in registers, holds
+// 18 KB in flight to an SM, and took 91 us for 8,192 rows of 4,352 channels; this one 150 KB: 46 us.)
+constexpr int kStageRows = 6, kBulkRing = 4, kBulkRun = 72, kBulkChannels = 512;
+
+template <typename IO, int K>
+__global__ void __launch_bounds__(128) ssm_conv_bulk_kernel(const SsmConvParams p, int64_t run_blocks) {
+    using namespace tc;
+    constexpr int V = 4;
+    using Vec = Pack<IO, V>;
+    __shared__ __align__(128) IO ring[kBulkRing][kStageRows][kBulkChannels];
+    __shared__ uint64_t full[kBulkRing];
+    const int tid = threadIdx.x, cta0 = blockIdx.y * kBulkChannels, c0 = cta0 + V * tid;
+    if ((int64_t)blockIdx.x >= run_blocks) {
+        if (c0 < p.C) conv_states<IO, V, K>(p, (int64_t)blockIdx.x - run_blocks, c0);
+        return;
+    }
+    const int64_t r0 = (int64_t)blockIdx.x * kBulkRun;
+    const int left = (int)(p.rows - r0 < kBulkRun ? p.rows - r0 : kBulkRun), stages = (left + kStageRows - 1) / kStageRows;
+    const uint32_t bytes = 2u * (uint32_t)(p.C - cta0 < kBulkChannels ? p.C - cta0 : kBulkChannels);
+    if (tid == 0) {
+        for (int i = 0; i < kBulkRing; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    auto fetch = [&](int s) {
+        const int rows = left - s * kStageRows < kStageRows ? left - s * kStageRows : kStageRows;
+        const IO *from = static_cast<const IO *>(p.x) + (r0 + s * kStageRows) * p.ld_x + cta0;
+        mbar_arrive_expect_tx(&full[s % kBulkRing], rows * bytes);
+        for (int i = 0; i < rows; ++i) bulk_load(ring[s % kBulkRing][i], from + i * p.ld_x, bytes, &full[s % kBulkRing]);
+    };
+    if (tid == 0)
+        for (int s = 0; s < kBulkRing && s < stages; ++s) fetch(s);
+
+    const bool live = c0 < p.C;
+    const IO *x = static_cast<const IO *>(p.x) + c0, *cin = p.conv_in ? static_cast<const IO *>(p.conv_in) + c0 : nullptr;
+    Walk at = walk_from(p, r0);
+    float w[K][V], bias[V], past[K > 1 ? K - 1 : 1][V];
+    IO *u = static_cast<IO *>(p.u) + r0 * p.ld_u;
+    if (live) {
+        u += u_channel(p, c0);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[j][i] = IoType<IO>::ld(static_cast<const IO *>(p.w) + (int64_t)(c0 + i) * K + j);
+            bias[i] = p.bias ? IoType<IO>::ld(static_cast<const IO *>(p.bias) + c0 + i) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            const int64_t r = r0 - (K - 1) + j;
+#pragma unroll
+            for (int v = 0; v < V; ++v) past[j][v] = 0.f;
+            if (r >= at.t0) widen<IO, V>(*reinterpret_cast<const Vec *>(x + r * p.ld_x), past[j]);
+            else if (cin) widen<IO, V>(*reinterpret_cast<const Vec *>(cin + (at.n * (K - 1) + (K - 1) + (r - at.t0)) * p.C), past[j]);
+        }
+    }
+    int turn = at.t1 - r0 < left ? (int)(at.t1 - r0) : left;
+    bool ok = true, more = true;       // more: the offsets lead to a sequence for the next row
+#pragma unroll 1
+    for (int s = 0; s < stages; ++s) {
+        ok = mbar_wait(&full[s % kBulkRing], (s / kBulkRing) & 1, 4000000000LL) && ok;
+        if (live && ok && more) {
+#pragma unroll
+            for (int i = 0; i < kStageRows; ++i, u += p.ld_u) {
+                const int r = s * kStageRows + i;
+                if (r >= left) break;
+                if (r >= turn) {
+                    if (!(more = walk_on(p, at, r0 + r))) break;
+                    turn = at.t1 - r0 < left ? (int)(at.t1 - r0) : left;
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) past[j][v] = 0.f;
+                        if (cin) widen<IO, V>(*reinterpret_cast<const Vec *>(cin + (at.n * (K - 1) + j) * p.C), past[j]);
+                    }
+                }
+                float now[V], acc[V];
+                widen<IO, V>(*reinterpret_cast<const Vec *>(&ring[s % kBulkRing][i][V * tid]), now);
+#pragma unroll
+                for (int v = 0; v < V; v += 2) {
+                    F2 a = {bias[v], bias[v + 1]};
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) a = fma2({w[j][v], w[j][v + 1]}, {past[j][v], past[j][v + 1]}, a);
+                    a = fma2({w[K - 1][v], w[K - 1][v + 1]}, {now[v], now[v + 1]}, a);
+                    acc[v] = a.x;
+                    acc[v + 1] = a.y;
+                }
+                if (p.silu) silu_rounded<IO, V>(acc);
+                Vec out;
+#pragma unroll
+                for (int v = 0; v < V; ++v) IoType<IO>::st(&out.v[v], acc[v]);
+                *reinterpret_cast<Vec *>(u) = out;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+#pragma unroll
+                    for (int j = 0; j + 1 < K - 1; ++j) past[j][v] = past[j + 1][v];
+                    if (K > 1) past[K > 1 ? K - 2 : 0][v] = now[v];
+                }
+            }
+        }
+        __syncthreads();        // the stage has been read
+        if (tid == 0 && s + kBulkRing < stages) fetch(s + kBulkRing);
+    }
+    if (!ok && tid == 0) atomicOr(p.status, kDevTimeout);
+}
+
 template <typename IO, int V>
 cudaError_t conv_launch(const SsmConvParams &p, cudaStream_t stream) {
     const int64_t runs = (p.rows + kRun - 1) / kRun;
@@ -231,13 +361,25 @@ cudaError_t conv_launch(const SsmConvParams &p, cudaStream_t stream) {
 
 template <typename IO>
 cudaError_t conv_dispatch(const SsmConvParams &p, cudaStream_t stream) {
-    // Four channels: eight of a 16-bit type took 144 registers, and with 12 warps to an SM 91 us for
-    // 8,192 rows of 4,352 channels where four take CONV4 us.
     constexpr int V = 4;
     auto ok = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & (V * sizeof(IO) - 1)) == 0; };
     const bool wide = p.head_dim % V == 0 && p.d_state % V == 0 && p.ld_x % V == 0 && p.ld_u % V == 0 && ok(p.x) && ok(p.u) &&
                       ok(p.conv_in) && ok(p.conv_out) && p.x_head % V == 0 && p.off_b % V == 0 && p.off_c % V == 0 &&
                       p.bc_group % V == 0;
+    if constexpr (sizeof(IO) == 2) {
+        auto by16 = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+        if (wide && p.w != nullptr && p.rows > 0 && p.C % 8 == 0 && p.ld_x % 8 == 0 && by16(p.x)) {
+            const int64_t runs = (p.rows + kBulkRun - 1) / kBulkRun;
+            const dim3 grid((unsigned)(runs + (p.K > 1 ? p.num_seqs : 0)), (unsigned)((p.C + kBulkChannels - 1) / kBulkChannels));
+            switch (p.K) {
+                case 1: ssm_conv_bulk_kernel<IO, 1><<<grid, 128, 0, stream>>>(p, runs); break;
+                case 2: ssm_conv_bulk_kernel<IO, 2><<<grid, 128, 0, stream>>>(p, runs); break;
+                case 3: ssm_conv_bulk_kernel<IO, 3><<<grid, 128, 0, stream>>>(p, runs); break;
+                default: ssm_conv_bulk_kernel<IO, 4><<<grid, 128, 0, stream>>>(p, runs); break;
+            }
+            return cudaGetLastError();
+        }
+    }
     return wide ? conv_launch<IO, V>(p, stream) : conv_launch<IO, 1>(p, stream);
 }
 

@@ -89,11 +89,11 @@ struct alignas(16) Gates {       // read in float2 and float4
 struct Ctl {
     // Barriers: pairs by chunk parity where a waiter can be a chunk behind (`full` and s_ready
     // by stage).
-    uint64_t full[4], gates[2], y_read[2], s_ready[4], wx_ready[2], ds[2], full_x[2], full_z[2];
+    uint64_t full[4], gates[4], y_read[2], s_ready[4], wx_ready[2], ds[2], full_x[2], full_z[2];
     uint64_t y_done[2], cb, cs, mx, m_ready, s_first, drain;
     uint32_t tmem;
     int32_t abort;   // a wait ran out
-    Gates g[2][2];   // [chunk parity][unit]
+    Gates g[2][2];   // [stage][unit] (the state-only pass, with room behind, has four stages)
 };
 static_assert(sizeof(Gates) % 16 == 0 && offsetof(Ctl, g) % 16 == 0 && O_CTL % 16 == 0, "vector accesses of the gates");
 constexpr int kSmem = O_CTL + sizeof(Ctl);
@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
     // (Nothing static stands before it, so dynamic shared memory begins on a 1024-byte boundary, as
     // the swizzled tiles need; there is no room to align it here.)
     extern __shared__ __align__(1024) uint8_t sm[];
-    Ctl &ctl = *reinterpret_cast<Ctl *>(sm + O_CTL);
+    Ctl &ctl = *reinterpret_cast<Ctl *>(sm + (kState ? O_Z : O_CTL));
+    Gates(*const gate)[2] = reinterpret_cast<Gates(*)[2]>(reinterpret_cast<uint8_t *>(&ctl) + offsetof(Ctl, g));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pairs = p.groups * p.pairs_per_group;
     const int pair = blockIdx.x % pairs;
@@ -247,9 +248,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         for (int i = 0; i < 4; ++i) {
             mbar_init(&ctl.full[i], 1);
             mbar_init(&ctl.s_ready[i], 8);
+            mbar_init(&ctl.gates[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ctl.gates[i], 2);
             mbar_init(&ctl.y_read[i], 8);
             mbar_init(&ctl.wx_ready[i], 8);
             mbar_init(&ctl.ds[i], 1);
@@ -267,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         ctl.abort = 0;
     }
     volatile int32_t *abort = &ctl.abort;
+    constexpr int NS = kStages<kState>;
     const int nchunks = (int)((it.t1 - it.t0 + kL - 1) / kL);
     auto chunk_len = [&](int c) {
         const int64_t left = it.t1 - it.t0 - (int64_t)c * kL;
@@ -275,7 +277,6 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
     // A phase of a barrier that completes once per chunk, and of one of a pair by chunk parity.
     auto wait = [&](uint64_t *bar, int c) { return wait_for(bar, c & 1, abort, budget); };
     auto wait2 = [&](uint64_t *bar, int c) { return wait_for(bar + (c & 1), (c >> 1) & 1, abort, budget); };
-    constexpr int NS = kStages<kState>;
     auto wait_st = [&](uint64_t *bar, int c) { return wait_for(bar + (c & (NS - 1)), (c / NS) & 1, abort, budget); };
     auto stage = [&](int c) { return sm + (c & (NS - 1)) * kStageBytes<kState>; };
     auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         for (int v = 0; v < 4; ++v) {
             const int u = v >> 1, j = (who >> 3) + 32 * (v & 1);
             const uint32_t at = u * 8192 + sw128_offset(j, who & 7);
-            const float w = j < len ? ex2(ctl.g[c & 1][u].lw[j]) : 0.f;
+            const float w = j < len ? ex2(gate[c & (NS - 1)][u].lw[j]) : 0.f;
             const uint4 xv = j < len ? *reinterpret_cast<const uint4 *>(xt + at) : make_uint4(0, 0, 0, 0);
             const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
             uint32_t hi[4], lo[4];
@@ -480,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             float after = __shfl_down_sync(0xffffffffu, suf, 1);
             if (lane == 31) after = 0.f;
             const float l0 = __log2f(d0), l1 = __log2f(d1);   // -inf where the step is zero: no weight
-            if (c >= 2 && !(ok = all(wait_st(ctl.s_ready, c - 2) && (kState || wait2(ctl.y_read, c - 2))))) break;
-            Gates &G = ctl.g[c & 1][u];
+            if (c >= NS && !(ok = all(wait_st(ctl.s_ready, c - NS) && (kState || wait2(ctl.y_read, c - NS))))) break;
+            Gates &G = gate[c & (NS - 1)][u];
             *reinterpret_cast<float2 *>(&G.s[2 * lane]) = make_float2(after + g1, after);
             *reinterpret_cast<float2 *>(&G.lw[2 * lane]) = make_float2(after + g1 + l0, after + l1);
             if (lane == 0) {
@@ -489,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
                 G.decay = ex2(suf);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.gates[c & 1]);
+            if (lane == 0) mbar_arrive(&ctl.gates[c & (NS - 1)]);
         }
         if (!ok) *abort = 1;
     } else if (warp >= kSWarp) {
@@ -524,16 +525,16 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         }
         float seg_total = 0.f;
         auto next_wx = [&](int c) {      // (the state's MMA of the chunk before has left its buffer)
-            if (!(ok = all(wait2(ctl.full_x, c) && (chunk_len(c) == kL || wait_st(ctl.full, c)) && wait2(ctl.gates, c)))) return;
+            if (!(ok = all(wait2(ctl.full_x, c) && (chunk_len(c) == kL || wait_st(ctl.full, c)) && wait_st(ctl.gates, c)))) return;
             make_wx(c, tid - 32 * kSWarp, sm + O_XH);
             arrive(&ctl.wx_ready[c & 1], true);
         };
         if (!kState && nchunks > 0) next_wx(0);
         for (int c = 0; ok && c < nchunks; ++c) {
-            if (!(ok = all((kState ? wait2(ctl.ds, c) : wait(&ctl.ds[0], c)) && wait2(ctl.gates, c)))) break;
+            if (!(ok = all((kState ? wait2(ctl.ds, c) : wait(&ctl.ds[0], c)) && wait_st(ctl.gates, c)))) break;
             tc_fence_after();
-            const float dec = ctl.g[c & 1][su].decay;
-            seg_total += ctl.g[c & 1][su].total;
+            const float dec = gate[c & (NS - 1)][su].decay;
+            seg_total += gate[c & (NS - 1)][su].total;
             const uint32_t src = tmem + lanes + (kState && (c & 1) ? T_CS : T_DS) + 64 * su;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         // ------------------------------------------------------------ w x of the state-only pass, two buffers
 
         for (int c = 0; c < nchunks; ++c) {
-            if (!(ok = all(wait_st(ctl.full, c) && wait2(ctl.gates, c) && (c < 2 || wait2(ctl.ds, c - 2))))) break;
+            if (!(ok = all(wait_st(ctl.full, c) && wait_st(ctl.gates, c) && (c < 2 || wait2(ctl.ds, c - 2))))) break;
             make_wx(c, tid, sm + (c & 1 ? O_S : O_XH));
             arrive(&ctl.wx_ready[c & 1], true);
         }
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         // Scores of chunk c, weighted: 0 above the diagonal (all of this warp's where its
         // columns are behind its rows).
         auto make_m = [&](int c) {
-            const Gates &G = ctl.g[c & 1][ru];
+            const Gates &G = gate[c & (NS - 1)][ru];
             const float si = G.s[ri];
             tc_fence_after();
 #pragma unroll 1
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             tmem_st_wait();
         };
         auto next_m = [&](int c) {
-            if (!(ok = all(wait2(ctl.gates, c) && wait(&ctl.cb, c)))) return;
+            if (!(ok = all(wait_st(ctl.gates, c) && wait(&ctl.cb, c)))) return;
             make_m(c);
             arrive(&ctl.m_ready, false);
         };
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             tc_fence_after();
             const uint8_t *xt = stage(c) + ST_X + ru * 8192;
             uint8_t *zt = sm + O_Z + (c & 1) * 16384 + ru * 8192;
-            const float e = ex2(ctl.g[c & 1][ru].total - ctl.g[c & 1][ru].s[ri]);
+            const float e = ex2(gate[c & (NS - 1)][ru].total - gate[c & (NS - 1)][ru].s[ri]);
             const int len = chunk_len(c);
             __nv_bfloat16 *dst = p.y + ((it.t0 + (int64_t)c * kL + ri) * p.heads + head) * (int64_t)p.P + col;
 #pragma unroll 1
