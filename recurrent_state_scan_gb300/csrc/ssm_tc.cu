@@ -155,7 +155,7 @@ __device__ __noinline__ uint4 load_unaligned(const __nv_bfloat16 *src) {
                       h[6] | (uint32_t)h[7] << 16);
 }
 
-// ssm_step of a bf16 value, out of line as well.
+// ssm_step of a bf16 value, out of line as well (90 instructions).
 __device__ __noinline__ float step_of(uint32_t bits, float bias, float lo, float hi) {
     return ssm_step(__uint_as_float(bits << 16), bias, lo, hi);
 }
@@ -464,11 +464,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         };
         if (nchunks > 0) load_dt(0);
         for (int c = 0; c < nchunks; ++c) {
-            const uint32_t r0 = n0, r1 = n1;
-            if (c + 1 < nchunks) load_dt(c + 1);
             const int len = chunk_len(c);
-            const float d0 = 2 * lane < len ? step_of(r0, bias, p.dt_min, p.dt_max) : 0.f;
-            const float d1 = 2 * lane + 1 < len ? step_of(r1, bias, p.dt_min, p.dt_max) : 0.f;
+            const float d0 = 2 * lane < len ? step_of(n0, bias, p.dt_min, p.dt_max) : 0.f;
+            const float d1 = 2 * lane + 1 < len ? step_of(n1, bias, p.dt_min, p.dt_max) : 0.f;
+            if (c + 1 < nchunks) load_dt(c + 1);      // (behind the calls, which would wait for it)
             float g0 = A * d0, g1 = A * d1;
             g0 = g0 < -160.f ? -160.f : g0;
             g1 = g1 < -160.f ? -160.f : g1;
