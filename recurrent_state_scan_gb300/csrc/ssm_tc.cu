@@ -73,6 +73,8 @@ struct TcParams {
     int32_t ptiles, units, pairs_per_group;      // units of one group
     int32_t z_tma;                               // z comes by TMA (its rows are on 16-byte boundaries)
     int32_t seg_chunks;                          // chunks per time segment (0: no segments)
+    int32_t cut_over;                            // packed sequences are cut if one has more chunks than this
+    int32_t by_length;                           // items are taken the long ones first
     float *seg_state, *seg_decay;                // [slot][unit][N][64], [slot][unit]
     int *status;
     long long budget;
@@ -127,7 +129,7 @@ template <int N> __device__ __forceinline__ void landed(uint32_t (&r)[N]) {
 // A bounded wait that gives up when another thread has.  Under a short budget
 // (gdn_set_wait_budget) a wait that took longer has run out even where a blocking try saw it end.
 // (Out of line: with it inlined at every wait the roles' loops together outgrew the instruction
-// cache, and a chunk took 7,700 cycles instead of SPEED.)
+// cache, whose hits went from 90% to 54%.)
 __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int32_t *abort, long long budget) {
     const long long t0 = clock64();
     while (!mbar_try_wait(bar, parity)) {
@@ -171,35 +173,123 @@ __device__ __forceinline__ int64_t slot_base(const TcParams &p, int64_t n, int64
     return p.cu_seqlens ? p.cu_seqlens[n] / ls + n : n * per;
 }
 
-// Slot s of a call: without segments the sequence s.  With segments of ls tokens, batched
-// sequences take equal runs of slots, and packed ones start at floor(cu[n] / ls) + n, which
-// leaves room for each one's ceil(len / ls) segments.
-__device__ __forceinline__ Item item_of(const TcParams &p, int64_t s) {
+// Item `place` where every sequence has equally many, or there is one sequence.
+__device__ __forceinline__ Item item_at(const TcParams &p, int64_t place) {
     Item it;
-    it.slot = s;
-    it.k = 0;
-    it.nseg = 1;
-    if (p.seg_chunks == 0) {
-        it.n = s;
-        it.valid = seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, s, it.t0, it.t1);
-        return it;
-    }
-    const int64_t ls = (int64_t)p.seg_chunks * kL, per = (p.seqlen + ls - 1) / ls;
-    int64_t lo = 0, hi = p.num_seqs - 1;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) >> 1;
-        if (slot_base(p, mid, ls, per) <= s) lo = mid;
-        else hi = mid - 1;
-    }
-    it.n = lo;
     int64_t t0, t1;
-    it.valid = seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, lo, t0, t1);
-    const int64_t k = s - slot_base(p, lo, ls, per), segs = (t1 - t0 + ls - 1) / ls;
-    it.nseg = segs > 1 ? (int)segs : 1;
-    it.valid = it.valid && k >= 0 && k < it.nseg;
-    it.k = (int)k;
-    it.t0 = t0 + k * ls;
-    it.t1 = it.t0 + ls < t1 ? it.t0 + ls : t1;
+    const int64_t ls = (int64_t)p.seg_chunks * kL, per = ls == 0 ? 1 : (p.seqlen + ls - 1) / ls;
+    it.slot = place;
+    it.n = per <= 1 ? place : place / per;
+    it.k = per <= 1 ? 0 : (int)(place % per);
+    it.nseg = per <= 1 ? 1 : (int)per;
+    it.valid = it.n < p.num_seqs && seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, it.n, t0, t1);
+    if (!it.valid) return it;
+    it.t0 = ls == 0 ? t0 : t0 + it.k * ls;
+    it.t1 = ls == 0 || it.t0 + ls > t1 ? t1 : it.t0 + ls;
+    return it;
+}
+
+__device__ __forceinline__ int chunks_of(const TcParams &p, int64_t n) {   // -1: bad offsets
+    int64_t t0, t1;
+    return seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, n, t0, t1) ? (int)((t1 - t0 + kL - 1) / kL) : -1;
+}
+
+// Segments of packed sequences are cut only where one is long enough to be worth the state-only
+// pass; by all threads of a block, which have to pass a barrier before the next use of `longest`.
+__device__ __forceinline__ int cut_of(const TcParams &p, int *longest) {
+    if (p.seg_chunks == 0 || p.cut_over == 0) return p.seg_chunks;
+    if (threadIdx.x == 0) *longest = 0;
+    __syncthreads();
+    int most = 0;
+    for (int64_t n = threadIdx.x; n < p.num_seqs; n += blockDim.x) most = max(most, chunks_of(p, n));
+    if (most > 0) atomicMax(longest, most);
+    __syncthreads();
+    return *longest > p.cut_over ? p.seg_chunks : 0;
+}
+
+// Items of packed sequences, the long ones first: more of them than SMs are then done soonest
+// (six sequences of 4,096 to 20,480 tokens on 32 unit pairs: 1,179 us in their own order and cut
+// at a fair share, 892 us by length and uncut).  They stand by quarters of an octave of their
+// chunks; each block counts them and takes the one at its place.
+struct Order {
+    int count[128], warp[kThreads / 32];
+    int longest, bin, rank;
+    int n, k;
+};
+__device__ __forceinline__ int bin_of(int chunks) {            // 0 for the longest
+    return chunks <= 0 ? 127 : 126 - min(126, (int)(__float_as_uint((float)chunks) >> 21) - (127 << 2));
+}
+__device__ __noinline__ Item item_by_length(const TcParams &p, int place, Order &o) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid < 128) o.count[tid] = 0;
+    if (tid == 0) o.n = -1;
+    __syncthreads();
+    const int seg = cut_of(p, &o.longest);
+    // Of sequence n: whole segments (in bin_of(seg)) and one rest, which an empty sequence has too.
+    auto parts = [&](int chunks, int &whole, int &rest) {
+        whole = seg == 0 || chunks < 0 ? 0 : chunks / seg;
+        rest = chunks < 0 ? -1 : chunks - whole * seg;
+        if (rest == 0 && whole > 0) rest = -1;
+    };
+    int whole, rest;
+    for (int64_t n = tid; n < p.num_seqs; n += kThreads) {
+        parts(chunks_of(p, n), whole, rest);
+        if (whole > 0) atomicAdd(&o.count[bin_of(seg)], whole);
+        if (rest >= 0) atomicAdd(&o.count[bin_of(rest)], 1);
+    }
+    __syncthreads();
+    if (tid < 32) {                                            // the bin of the place, and the place in it
+        int c[4], sum = 0;
+        for (int i = 0; i < 4; ++i) sum += c[i] = o.count[4 * lane + i];
+        int upto = sum;
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += v;
+        }
+        int at = place - (upto - sum);
+        for (int i = 0; i < 4; ++i) {
+            if (at >= 0 && at < c[i]) { o.bin = 4 * lane + i; o.rank = at; o.n = -2; }
+            at -= c[i];
+        }
+    }
+    __syncthreads();
+    Item it;
+    it.valid = o.n == -2;
+    if (!it.valid) return it;                                  // fewer items than places
+    const int bin = o.bin;
+    int before = o.rank;                                       // items of the bin still to pass
+    for (int64_t base = 0; base < p.num_seqs; base += kThreads) {
+        const int64_t n = base + tid;
+        whole = 0, rest = -1;
+        if (n < p.num_seqs) parts(chunks_of(p, n), whole, rest);
+        const int w = bin == bin_of(seg) ? whole : 0, own = w + (rest >= 0 && bin_of(rest) == bin);
+        int upto = own;
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += v;
+        }
+        if (lane == 31) o.warp[tid >> 5] = upto;
+        __syncthreads();
+        int all = 0, at = before - (upto - own);
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < tid >> 5) at -= o.warp[i];
+            all += o.warp[i];
+        }
+        if (at >= 0 && at < own) { o.n = (int)n; o.k = at < w ? at : whole; }
+        before -= all;
+        __syncthreads();
+        if (before < 0) break;
+    }
+    int64_t t0, t1;
+    it.n = o.n;
+    it.valid = it.n >= 0 && seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, it.n, t0, t1);
+    if (!it.valid) return it;
+    const int64_t ls = (int64_t)seg * kL;
+    it.k = o.k;
+    it.nseg = seg == 0 || t1 == t0 ? 1 : (int)((t1 - t0 + ls - 1) / ls);
+    it.slot = seg == 0 ? it.n : slot_base(p, it.n, ls, 0) + it.k;
+    it.t0 = t0 + it.k * ls;
+    it.t1 = seg == 0 || it.t0 + ls > t1 ? t1 : it.t0 + ls;
     return it;
 }
 
@@ -220,12 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pairs = p.groups * p.pairs_per_group;
     const int pair = blockIdx.x % pairs;
-    const Item it = item_of(p, blockIdx.x / pairs);
-    // Each sequence's offsets are checked once, whether or not a slot leads to it.
-    if (!kState && p.seg_chunks != 0 && tid == 0 && (int64_t)blockIdx.x < p.num_seqs) {
-        int64_t a, b;
-        seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, blockIdx.x, a, b);
-    }
+    const Item it = p.by_length ? item_by_length(p, blockIdx.x / pairs, *reinterpret_cast<Order *>(sm + O_S))
+                                : item_at(p, blockIdx.x / pairs);
     if (!it.valid || (kState && it.k + 1 >= it.nseg)) return;
     if (smem_u32(sm) % 1024 != 0) {
         if (tid == 0) atomicOr(p.status, kDevTimeout);
@@ -678,6 +764,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
 // The state entering each segment, in the place of the segment's own end state.
 __global__ void __launch_bounds__(256) ssm_segment_states(const __grid_constant__ TcParams p) {
     const int64_t n = blockIdx.x, unit = blockIdx.y, nunits = (int64_t)p.groups * p.units;
+    __shared__ int longest;
+    if (cut_of(p, &longest) == 0) return;
     const int64_t ls = (int64_t)p.seg_chunks * kL, per = (p.seqlen + ls - 1) / ls;
     int64_t t0, t1;
     if (!seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, n, t0, t1)) return;
@@ -720,7 +808,10 @@ int unit_pairs(int heads, int groups, int head_dim) {
     return groups * ((units + 1) / 2);
 }
 
+// A state-only chunk takes 0.45 of a whole one, so cutting into the SMs' fair shares costs 1.45 of
+// one at least, and up to 1.9 with rests: uncut sequences of up to kCutOver shares are as good.
 constexpr int kSms = 152, kMinSegChunks = 8;
+constexpr double kCutOver = 1.6;
 
 // Chunks per segment (0: no segments).  Sequences are cut where sequences x pairs of units
 // fill less than half of the SMs; the segments then fill them once.
@@ -808,10 +899,13 @@ cudaError_t launch_ssm_tc(const SsmParams &s, void *workspace, cudaStream_t stre
     p.budget = __atomic_load_n(&g_wait_budget, __ATOMIC_RELAXED);
     const SegBytes b = segment_bytes(varlen, s.seqlen, s.rows, s.num_seqs, s.heads, s.groups, s.head_dim, s.d_state);
     p.seg_chunks = b.seg;
+    const int pairs = s.groups * p.pairs_per_group;
+    p.by_length = varlen && s.num_seqs > 1 && (b.seg > 0 || b.slots * pairs > kSms);
+    if (varlen && s.num_seqs > 1 && b.seg > 0) p.cut_over = (int32_t)(kCutOver * ((s.rows + kL - 1) / kL) * pairs / kSms);
     p.seg_state = static_cast<float *>(workspace);
     p.seg_decay = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + b.state);
 
-    const int64_t grid = b.slots * (int64_t)s.groups * p.pairs_per_group;
+    const int64_t grid = b.slots * pairs;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(ssm_chunk_scan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_chunk_scan<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);

@@ -235,6 +235,34 @@ def test_long_prompts_in_time_segments(H, P, G, N, lens, packed):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,lens", [
+    (64, [700, 3, 650, 0, 690, 64, 65, 2]),                              # long enough to cut, but none worth it
+    (64, [1800, 3, 650, 0, 90, 64, 65, 2]),                              # one that is
+    (2, [(37 * i * i) % 150 for i in range(1300)]),                      # more sequences than threads, some empty
+    (4, [64] * 700 + [0] * 5 + [1] * 40),
+])
+def test_packed_prompts_by_length(H, lens):
+    """The long ones are taken first: each sequence is still computed, once, wherever it stands."""
+    m = draw("bf16", lens, H, 64, 1, 32, 0, seed=len(lens), gap=(-(2 * H * 64 + 64 + H)) % 8)
+    wide = dict(m, io=torch.float32, **{k: m[k].float() for k in ("xbc", "dt", "z")})
+    check(m, prefill(m), prefill(wide))
+
+
+@pytest.mark.gpu
+def test_bad_offsets_among_many_sequences():
+    """Sequences of bad offsets are left alone, the others computed."""
+    lens = [70] * 400
+    m = draw("bf16", lens, 4, 64, 1, 16, 0, seed=5)
+    good = prefill(m)
+    m["cu"][200] = 20000
+    y, state = (torch.full_like(t, 7.0) for t in good[:2])
+    lib.gdn_ssm_prefill(m["xbc"], m["dt"], m["A_log"], state_in=m["state"], cu_seqlens=m["cu"], y=y, state_out=state, **kwargs(m))
+    assert lib.gdn_last_device_status() == gdn.GDN_ERR_DEVICE_CHECK
+    assert torch.equal(state[:199], good[1][:199]) and torch.equal(state[201:], good[1][201:]) and (state[200] == 7).all()
+    assert torch.equal(y[:, :199 * 70], good[0][:, :199 * 70])
+
+
+@pytest.mark.gpu
 def test_a_wait_that_runs_out_is_reported():
     m = draw("bf16", [300, 1400], 4, 64, 1, 128, 0, seed=14)
     want = prefill(m)
