@@ -386,15 +386,19 @@ cudaError_t conv_dispatch(const SsmConvParams &p, cudaStream_t stream) {
 // ------------------------------------------------------------------ token-sequential scan
 // A CTA of four warps takes 16 columns of one head's state and walks the sequence.  A warp
 // holds four columns; a column's d_state rows are dealt to eight lanes, NS to each, in
-// registers.  B, C, x and the gates of kTile tokens are staged in shared memory as fp32,
-// the next tile's values loaded while this one is computed.  The eight lanes' partial
-// readouts of eight tokens are summed by a reduce-scatter (seven shuffles for eight
-// tokens), after which lane slice s owns token s.
-constexpr int kTile = 8, kCols = 16, kScanThreads = 128;
+// registers, two rows to a packed instruction.  B, C, x, z and the gates of two batches of eight
+// tokens (one, where d_state > 128 leaves no room) are fetched while the two before them are
+// computed, as raw bits: widened at the load they were waited for there (133 us, then 207).  The
+// eight lanes' partial readouts of a batch are summed by a reduce-scatter (seven shuffles for
+// eight tokens), after which lane slice s owns token s.
+// Bound by issue and latency: 2 x 1,001 f16 tokens of 24 heads of 64 columns x 128 rows take
+// 133 us, 250 cycles a token, on SMs with four or eight warps each; there is no more parallelism
+// than columns without cutting time.
+constexpr int kBatch = 8, kCols = 16, kScanThreads = 128;
 
 template <typename IO, int NS>
 __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(const SsmParams p) {
-    constexpr int NP = 8 * NS, V = NS < 4 ? NS : 4;
+    constexpr int NP = 8 * NS, V = NS < 4 ? NS : 4, kTile = NS > 16 ? kBatch : 2 * kBatch, kXs = kTile * kCols / kScanThreads;
     constexpr int LOADS = 2 * NP * kTile / kScanThreads;   // B and C values a thread stages
     __shared__ __align__(16) float sb[2][kTile][2][NP];
     __shared__ float sx[2][kTile][kCols], sg[2][kTile][2];
@@ -411,97 +415,121 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(const SsmParams 
     auto state_at = [&](int i) { return (i / V) * (8 * V) + slice * V + i % V; };
     const size_t sbase = ((size_t)n * p.heads + h) * (size_t)N * P + c0 + col;
 
-    float S[NS];
+    F2 S[NS / 2];
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
-        S[i] = (p.state_in && live && state_at(i) < N) ? p.state_in[sbase + (size_t)state_at(i) * P] : 0.f;
+    for (int i = 0; i < NS; i += 2) {
+        auto at = [&](int j) { return p.state_in && live && state_at(j) < N ? p.state_in[sbase + (size_t)state_at(j) * P] : 0.f; };
+        S[i / 2] = {at(i), at(i + 1)};
+    }
 
     const IO *xs = static_cast<const IO *>(p.xs), *dt = static_cast<const IO *>(p.dt);
     const IO *z = static_cast<const IO *>(p.z);
     const float A = -expf(p.A_log[h]), bias = p.dt_bias ? p.dt_bias[h] : 0.f, D = p.D ? p.D[h] : 0.f;
-    float rb[LOADS], rx, rd;
+    IO rb[LOADS], rx[kXs], rd, rz[kTile / kBatch];      // (widened where they are used: nothing waits for them in load)
+    const IO none = IO(0.f);
+    const int64_t yc = (int64_t)h * P + c0 + col;
     // Tile loads: value e of a thread is (token, B or C, row), x one (token, column), dt one token.
     auto load = [&](int64_t tb) {
 #pragma unroll
         for (int e = 0; e < LOADS; ++e) {
             const int at = tid + e * kScanThreads, tk = at / (2 * NP), bc = (at / NP) & 1, i = at % NP;
             rb[e] = (tb + tk < t1 && i < N)
-                        ? IoType<IO>::ld(xs + (tb + tk) * p.ldx + (bc ? p.off_c : p.off_b) + (int64_t)g * p.bc_group + i)
-                        : 0.f;
+                        ? xs[(tb + tk) * p.ldx + (bc ? p.off_c : p.off_b) + (int64_t)g * p.bc_group + i]
+                        : none;
         }
-        const int tk = tid / kCols, c = tid % kCols;
-        rx = (tb + tk < t1 && c0 + c < P) ? IoType<IO>::ld(xs + (tb + tk) * p.ldx + (int64_t)h * p.x_head + c0 + c) : 0.f;
-        rd = (tid < kTile && tb + tid < t1) ? IoType<IO>::ld(dt + (tb + tid) * p.ld_dt + h) : 0.f;
+#pragma unroll
+        for (int e = 0; e < kXs; ++e) {
+            const int tk = (tid + e * kScanThreads) / kCols, c = tid % kCols;
+            rx[e] = (tb + tk < t1 && c0 + c < P) ? xs[(tb + tk) * p.ldx + (int64_t)h * p.x_head + c0 + c] : none;
+        }
+        rd = (tid < kTile && tb + tid < t1) ? dt[(tb + tid) * p.ld_dt + h] : none;
+#pragma unroll
+        for (int e = 0; e < kTile / kBatch; ++e) {
+            const int64_t t = tb + e * kBatch + slice;
+            rz[e] = z && live && t < t1 ? z[t * p.ld_z + yc] : none;
+        }
     };
-    auto put = [&](int buf) {
+    auto put = [&](int64_t tb, int buf) {      // tokens behind the sequence change nothing: d = 0, decay 1
 #pragma unroll
         for (int e = 0; e < LOADS; ++e) {
             const int at = tid + e * kScanThreads;
-            sb[buf][at / (2 * NP)][(at / NP) & 1][at % NP] = rb[e];
+            sb[buf][at / (2 * NP)][(at / NP) & 1][at % NP] = IoType<IO>::ld(&rb[e]);
         }
-        sx[buf][tid / kCols][tid % kCols] = rx;
+#pragma unroll
+        for (int e = 0; e < kXs; ++e) sx[buf][(tid + e * kScanThreads) / kCols][tid % kCols] = IoType<IO>::ld(&rx[e]);
         if (tid < kTile) {
-            const float d = ssm_step(rd, bias, p.dt_min, p.dt_max);
+            const float d = tb + tid < t1 ? ssm_step(IoType<IO>::ld(&rd), bias, p.dt_min, p.dt_max) : 0.f;
             sg[buf][tid][0] = d;
             sg[buf][tid][1] = expf(A * d);
         }
     };
     load(t0);
-    put(0);
+    put(t0, 0);
     __syncthreads();
     int buf = 0;
     for (int64_t tb = t0; tb < t1; tb += kTile, buf ^= 1) {
         const bool more = tb + kTile < t1;
-        if (more) load(tb + kTile);
-        float y[kTile];
+        IO zv[kTile / kBatch];
 #pragma unroll
-        for (int k = 0; k < kTile; ++k) {
-            y[k] = 0.f;
-            if (tb + k < t1) {
-                const float a = sg[buf][k][1], dx = sg[buf][k][0] * sx[buf][k][col];
+        for (int e = 0; e < kTile / kBatch; ++e) zv[e] = rz[e];
+        if (more) load(tb + kTile);
+#pragma unroll
+        for (int e = 0; e < kTile / kBatch; ++e) {
+            if (e > 0 && tb + e * kBatch >= t1) break;
+            float y[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int tk = e * kBatch + k;
+                const F2 a = both(sg[buf][tk][1]), dx = both(sg[buf][tk][0] * sx[buf][tk][col]);
+                F2 sum = both(0.f);
 #pragma unroll
                 for (int i = 0; i < NS; i += V) {
                     const int at = (i / V) * (8 * V) + slice * V;
-                    alignas(16) float b[V], c[V];
+                    F2 b[V / 2], c[V / 2];
                     if constexpr (V == 4) {
-                        *reinterpret_cast<float4 *>(b) = *reinterpret_cast<const float4 *>(&sb[buf][k][0][at]);
-                        *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(&sb[buf][k][1][at]);
+                        const float4 bv = *reinterpret_cast<const float4 *>(&sb[buf][tk][0][at]);
+                        const float4 cv = *reinterpret_cast<const float4 *>(&sb[buf][tk][1][at]);
+                        b[0] = {bv.x, bv.y}; b[1] = {bv.z, bv.w}; c[0] = {cv.x, cv.y}; c[1] = {cv.z, cv.w};
                     } else {
-                        *reinterpret_cast<float2 *>(b) = *reinterpret_cast<const float2 *>(&sb[buf][k][0][at]);
-                        *reinterpret_cast<float2 *>(c) = *reinterpret_cast<const float2 *>(&sb[buf][k][1][at]);
+                        const float2 bv = *reinterpret_cast<const float2 *>(&sb[buf][tk][0][at]);
+                        const float2 cv = *reinterpret_cast<const float2 *>(&sb[buf][tk][1][at]);
+                        b[0] = {bv.x, bv.y}; c[0] = {cv.x, cv.y};
                     }
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        S[i + v] = fmaf(a, S[i + v], dx * b[v]);
-                        y[k] = fmaf(c[v], S[i + v], y[k]);
+                    for (int v = 0; v < V / 2; ++v) {
+                        F2 &s = S[i / 2 + v];
+                        s = fma2(a, s, mul2(dx, b[v]));
+                        sum = fma2(c[v], s, sum);
                     }
                 }
+                y[k] = sum.x + sum.y;
+            }
+            // Reduce-scatter over the eight slices (lane bits 2..4): slice s ends with token s.
+#pragma unroll
+            for (int bit = 2, half = 4; bit >= 0; --bit, half >>= 1) {
+                const bool up = (slice >> bit) & 1;
+#pragma unroll
+                for (int k = 0; k < half; ++k) {
+                    const float keep = up ? y[k + half] : y[k], give = up ? y[k] : y[k + half];
+                    y[k] = keep + __shfl_xor_sync(0xffffffffu, give, 4 << bit);
+                }
+            }
+            const int64_t t = tb + e * kBatch + slice;
+            if (live && t < t1) {
+                float out = fmaf(D, sx[buf][e * kBatch + slice][col], y[0]);
+                if (z) out *= silu_gate(IoType<IO>::ld(&zv[e]));
+                IoType<IO>::st(static_cast<IO *>(p.y) + t * (int64_t)p.heads * P + yc, out);
             }
         }
-        // Reduce-scatter over the eight slices (lane bits 2..4): slice s ends with token s.
-#pragma unroll
-        for (int bit = 2, half = 4; bit >= 0; --bit, half >>= 1) {
-            const bool up = (slice >> bit) & 1;
-#pragma unroll
-            for (int k = 0; k < half; ++k) {
-                const float keep = up ? y[k + half] : y[k], give = up ? y[k] : y[k + half];
-                y[k] = keep + __shfl_xor_sync(0xffffffffu, give, 4 << bit);
-            }
-        }
-        const int64_t t = tb + slice;
-        if (live && t < t1) {
-            float out = fmaf(D, sx[buf][slice][col], y[0]);
-            const int64_t yc = (int64_t)h * P + c0 + col;
-            if (z) out *= silu_gate(IoType<IO>::ld(z + t * p.ld_z + yc));
-            IoType<IO>::st(static_cast<IO *>(p.y) + t * (int64_t)p.heads * P + yc, out);
-        }
-        if (more) put(buf ^ 1);
+        if (more) put(tb + kTile, buf ^ 1);
         __syncthreads();
     }
     if (!live) return;
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
-        if (state_at(i) < N) p.state_out[sbase + (size_t)state_at(i) * P] = S[i];
+    for (int i = 0; i < NS; i += 2) {
+        if (state_at(i) < N) p.state_out[sbase + (size_t)state_at(i) * P] = S[i / 2].x;
+        if (state_at(i + 1) < N) p.state_out[sbase + (size_t)state_at(i + 1) * P] = S[i / 2].y;
+    }
 }
 
 template <typename IO>
