@@ -127,9 +127,10 @@ gdn_status gdn_ssm_prefill_plan(const gdn_ssm_shape *shape, const gdn_ssm_params
     const gdn_status st = check(shape, params, varlen, g);
     if (st != GDN_OK) return st;
     const bool tc = tc_shape(shape, g);
-    const bool seg = tc && ssm_tc_segments(varlen, shape->seqlen, g.rows, shape->num_seqs, shape->heads, shape->groups, shape->head_dim);
+    bool seg = false;
+    const int scans = tc ? ssm_tc_launches(varlen, shape->seqlen, g.rows, shape->num_seqs, shape->heads, shape->groups, shape->head_dim, &seg) : 1;
     if (path) *path = tc ? (seg ? 3 : 2) : 1;
-    if (launches) *launches = shape->num_seqs > 0 ? (layout(shape, params, g, varlen).u > 0 ? 1 : 0) + (seg ? 3 : 1) : 0;
+    if (launches) *launches = shape->num_seqs > 0 ? (layout(shape, params, g, varlen).u > 0 ? 1 : 0) + scans : 0;
     return GDN_OK;
 }
 

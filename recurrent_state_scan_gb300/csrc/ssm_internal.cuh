@@ -61,11 +61,12 @@ struct SsmDecodeParams {
 
 cudaError_t launch_ssm_conv(const SsmConvParams &p, gdn_dtype io, cudaStream_t stream);
 cudaError_t launch_ssm_scan_simt(const SsmParams &p, gdn_dtype io, cudaStream_t stream);
-// The tensor-core scan: its types and sizes, the rows it can read by TMA, the bytes of its time
-// segments' states (16-byte aligned; 0: none), whether it runs in segments, and the launch.
+// The tensor-core scan: its types and sizes, the rows it can read by TMA, its launches (and whether
+// it runs in time segments), the bytes of its segments' states and items (16-byte aligned; 0:
+// none), and the launch.
 bool ssm_tc_shape_ok(gdn_dtype io, int head_dim, int d_state);
 bool ssm_tc_rows_ok(const SsmParams &p);
-bool ssm_tc_segments(bool varlen, int64_t seqlen, int64_t rows, int64_t num_seqs, int heads, int groups, int head_dim);
+int ssm_tc_launches(bool varlen, int64_t seqlen, int64_t rows, int64_t num_seqs, int heads, int groups, int head_dim, bool *segments);
 size_t ssm_tc_workspace(bool varlen, int64_t seqlen, int64_t rows, int64_t num_seqs, int heads, int groups, int head_dim,
                         int d_state);
 cudaError_t launch_ssm_tc(const SsmParams &p, void *workspace, cudaStream_t stream);

@@ -73,8 +73,8 @@ struct TcParams {
     int32_t ptiles, units, pairs_per_group;      // units of one group
     int32_t z_tma;                               // z comes by TMA (its rows are on 16-byte boundaries)
     int32_t seg_chunks;                          // chunks per time segment (0: no segments)
-    int32_t cut_over;                            // packed sequences are cut if one has more chunks than this
-    int32_t by_length;                           // items are taken the long ones first
+    int32_t cut_over;                            // ssm_order cuts if a sequence has more chunks than this
+    int4 *items;                                 // [slot] its sequence, segment and seg_chunks, or null: not ordered
     float *seg_state, *seg_decay;                // [slot][unit][N][64], [slot][unit]
     int *status;
     long long budget;
@@ -173,124 +173,97 @@ __device__ __forceinline__ int64_t slot_base(const TcParams &p, int64_t n, int64
     return p.cu_seqlens ? p.cu_seqlens[n] / ls + n : n * per;
 }
 
-// Item `place` where every sequence has equally many, or there is one sequence.
+// Item `place` of a call: of an ordered one as ssm_order put it, else every sequence has equally
+// many (or there is one sequence).
 __device__ __forceinline__ Item item_at(const TcParams &p, int64_t place) {
     Item it;
-    int64_t t0, t1;
-    const int64_t ls = (int64_t)p.seg_chunks * kL, per = ls == 0 ? 1 : (p.seqlen + ls - 1) / ls;
-    it.slot = place;
-    it.n = per <= 1 ? place : place / per;
-    it.k = per <= 1 ? 0 : (int)(place % per);
-    it.nseg = per <= 1 ? 1 : (int)per;
-    it.valid = it.n < p.num_seqs && seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, it.n, t0, t1);
+    int64_t t0, t1, ls = (int64_t)p.seg_chunks * kL;
+    if (p.items != nullptr) {
+        const int4 v = p.items[place];
+        it.n = v.x;
+        it.k = v.y;
+        ls = (int64_t)v.z * kL;
+        it.valid = v.x >= 0;
+    } else {
+        const int64_t per = ls == 0 ? 1 : (p.seqlen + ls - 1) / ls;
+        it.n = per <= 1 ? place : place / per;
+        it.k = per <= 1 ? 0 : (int)(place % per);
+        it.valid = it.n < p.num_seqs;
+    }
+    it.valid = it.valid && seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, it.n, t0, t1);
     if (!it.valid) return it;
-    it.t0 = ls == 0 ? t0 : t0 + it.k * ls;
+    it.nseg = ls == 0 || t1 == t0 ? 1 : (int)((t1 - t0 + ls - 1) / ls);
+    it.slot = ls == 0 ? it.n : slot_base(p, it.n, ls, (p.seqlen + ls - 1) / ls) + it.k;
+    it.t0 = t0 + it.k * ls;
     it.t1 = ls == 0 || it.t0 + ls > t1 ? t1 : it.t0 + ls;
     return it;
 }
 
-__device__ __forceinline__ int chunks_of(const TcParams &p, int64_t n) {   // -1: bad offsets
-    int64_t t0, t1;
-    return seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, n, t0, t1) ? (int)((t1 - t0 + kL - 1) / kL) : -1;
-}
-
-// Segments of packed sequences are cut only where one is long enough to be worth the state-only
-// pass; by all threads of a block, which have to pass a barrier before the next use of `longest`.
-__device__ __forceinline__ int cut_of(const TcParams &p, int *longest) {
-    if (p.seg_chunks == 0 || p.cut_over == 0) return p.seg_chunks;
-    if (threadIdx.x == 0) *longest = 0;
-    __syncthreads();
-    int most = 0;
-    for (int64_t n = threadIdx.x; n < p.num_seqs; n += blockDim.x) most = max(most, chunks_of(p, n));
-    if (most > 0) atomicMax(longest, most);
-    __syncthreads();
-    return *longest > p.cut_over ? p.seg_chunks : 0;
-}
-
-// Items of packed sequences, the long ones first: more of them than SMs are then done soonest
-// (six sequences of 4,096 to 20,480 tokens on 32 unit pairs: 1,179 us in their own order and cut
-// at a fair share, 892 us by length and uncut).  They stand by quarters of an octave of their
-// chunks; each block counts them and takes the one at its place.
-struct Order {
-    int count[128], warp[kThreads / 32];
-    int longest, bin, rank;
-    int n, k;
-};
+// The items of packed sequences in order, the long ones first: more of them than SMs are then
+// done soonest.  Six sequences of 4,096 to 20,480 tokens on 32 unit pairs took 1,180 us in their
+// own order and cut at a fair share, and take 892 us like this.  Sequences are cut along time
+// only where one is long enough to be worth the state-only pass.  By one block, in bins of a
+// quarter of an octave of their chunks: atomics place the items of a bin, in any order (which no
+// result depends on); places without an item hold sequence -1.  Bound by latency and the launch.
+constexpr int kOrderThreads = 512, kBins = 128;
 __device__ __forceinline__ int bin_of(int chunks) {            // 0 for the longest
-    return chunks <= 0 ? 127 : 126 - min(126, (int)(__float_as_uint((float)chunks) >> 21) - (127 << 2));
+    return chunks <= 0 ? kBins - 1 : kBins - 2 - min(kBins - 2, (int)(__float_as_uint((float)chunks) >> 21) - (127 << 2));
 }
-__device__ __noinline__ Item item_by_length(const TcParams &p, int place, Order &o) {
-    const int tid = threadIdx.x, lane = tid & 31;
-    if (tid < 128) o.count[tid] = 0;
-    if (tid == 0) o.n = -1;
+__global__ void __launch_bounds__(kOrderThreads) ssm_order(const __grid_constant__ TcParams p, int64_t places) {
+    __shared__ int at[kBins], longest, items;
+    const int tid = threadIdx.x;
+    if (tid < kBins) at[tid] = 0;
+    if (tid == 0) longest = 0;
     __syncthreads();
-    const int seg = cut_of(p, &o.longest);
-    // Of sequence n: whole segments (in bin_of(seg)) and one rest, which an empty sequence has too.
-    auto parts = [&](int chunks, int &whole, int &rest) {
+    auto chunks_of = [&](int64_t n) {                          // -1: bad offsets
+        int64_t t0, t1;
+        return seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, n, t0, t1) ? (int)((t1 - t0 + kL - 1) / kL) : -1;
+    };
+    int most = 0;
+    for (int64_t n = tid; n < p.num_seqs; n += kOrderThreads) most = max(most, chunks_of(n));
+    if (most > 0) atomicMax(&longest, most);
+    __syncthreads();
+    const int seg = longest > p.cut_over ? p.seg_chunks : 0;
+    // Of sequence n: `whole` segments of seg chunks, and one rest (an empty sequence's only item) or none (-1).
+    auto parts = [&](int64_t n, int &whole, int &rest) {
+        const int chunks = chunks_of(n);
         whole = seg == 0 || chunks < 0 ? 0 : chunks / seg;
-        rest = chunks < 0 ? -1 : chunks - whole * seg;
-        if (rest == 0 && whole > 0) rest = -1;
+        rest = chunks < 0 || (whole > 0 && chunks == whole * seg) ? -1 : chunks - whole * seg;
     };
     int whole, rest;
-    for (int64_t n = tid; n < p.num_seqs; n += kThreads) {
-        parts(chunks_of(p, n), whole, rest);
-        if (whole > 0) atomicAdd(&o.count[bin_of(seg)], whole);
-        if (rest >= 0) atomicAdd(&o.count[bin_of(rest)], 1);
+    for (int64_t n = tid; n < p.num_seqs; n += kOrderThreads) {
+        parts(n, whole, rest);
+        if (whole > 0) atomicAdd(&at[bin_of(seg)], whole);
+        if (rest >= 0) atomicAdd(&at[bin_of(rest)], 1);
     }
     __syncthreads();
-    if (tid < 32) {                                            // the bin of the place, and the place in it
-        int c[4], sum = 0;
-        for (int i = 0; i < 4; ++i) sum += c[i] = o.count[4 * lane + i];
+    if (tid < 32) {                                            // counts to first places
+        int c[kBins / 32], sum = 0;
+        for (int i = 0; i < kBins / 32; ++i) sum += c[i] = at[kBins / 32 * tid + i];
         int upto = sum;
         for (int d = 1; d < 32; d *= 2) {
             const int v = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += v;
+            if (tid >= d) upto += v;
         }
-        int at = place - (upto - sum);
-        for (int i = 0; i < 4; ++i) {
-            if (at >= 0 && at < c[i]) { o.bin = 4 * lane + i; o.rank = at; o.n = -2; }
-            at -= c[i];
+        if (tid == 31) items = upto;
+        upto -= sum;
+        for (int i = 0; i < kBins / 32; ++i) {
+            at[kBins / 32 * tid + i] = upto;
+            upto += c[i];
         }
     }
     __syncthreads();
-    Item it;
-    it.valid = o.n == -2;
-    if (!it.valid) return it;                                  // fewer items than places
-    const int bin = o.bin;
-    int before = o.rank;                                       // items of the bin still to pass
-    for (int64_t base = 0; base < p.num_seqs; base += kThreads) {
-        const int64_t n = base + tid;
-        whole = 0, rest = -1;
-        if (n < p.num_seqs) parts(chunks_of(p, n), whole, rest);
-        const int w = bin == bin_of(seg) ? whole : 0, own = w + (rest >= 0 && bin_of(rest) == bin);
-        int upto = own;
-        for (int d = 1; d < 32; d *= 2) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += v;
-        }
-        if (lane == 31) o.warp[tid >> 5] = upto;
-        __syncthreads();
-        int all = 0, at = before - (upto - own);
-        for (int i = 0; i < kThreads / 32; ++i) {
-            if (i < tid >> 5) at -= o.warp[i];
-            all += o.warp[i];
-        }
-        if (at >= 0 && at < own) { o.n = (int)n; o.k = at < w ? at : whole; }
-        before -= all;
-        __syncthreads();
-        if (before < 0) break;
+    // (Overlapping sequences, each fine by itself beside bad ones, can be more than the places.)
+    auto put = [&](int place, int64_t n, int k) {
+        if (place < places) p.items[place] = make_int4((int)n, k, seg, 0);
+    };
+    for (int64_t n = tid; n < p.num_seqs; n += kOrderThreads) {
+        parts(n, whole, rest);
+        const int first = whole > 0 ? atomicAdd(&at[bin_of(seg)], whole) : 0;
+        for (int k = 0; k < whole; ++k) put(first + k, n, k);
+        if (rest >= 0) put(atomicAdd(&at[bin_of(rest)], 1), n, whole);
     }
-    int64_t t0, t1;
-    it.n = o.n;
-    it.valid = it.n >= 0 && seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, it.n, t0, t1);
-    if (!it.valid) return it;
-    const int64_t ls = (int64_t)seg * kL;
-    it.k = o.k;
-    it.nseg = seg == 0 || t1 == t0 ? 1 : (int)((t1 - t0 + ls - 1) / ls);
-    it.slot = seg == 0 ? it.n : slot_base(p, it.n, ls, 0) + it.k;
-    it.t0 = t0 + it.k * ls;
-    it.t1 = seg == 0 || it.t0 + ls > t1 ? t1 : it.t0 + ls;
-    return it;
+    for (int64_t i = items + (int64_t)tid; i < places; i += kOrderThreads) p.items[i] = make_int4(-1, 0, seg, 0);
 }
 
 // The roles of a CTA's warps, each with its own pace; mbarriers carry the order.
@@ -310,8 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pairs = p.groups * p.pairs_per_group;
     const int pair = blockIdx.x % pairs;
-    const Item it = p.by_length ? item_by_length(p, blockIdx.x / pairs, *reinterpret_cast<Order *>(sm + O_S))
-                                : item_at(p, blockIdx.x / pairs);
+    const Item it = item_at(p, blockIdx.x / pairs);
     if (!it.valid || (kState && it.k + 1 >= it.nseg)) return;
     if (smem_u32(sm) % 1024 != 0) {
         if (tid == 0) atomicOr(p.status, kDevTimeout);
@@ -764,8 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
 // The state entering each segment, in the place of the segment's own end state.
 __global__ void __launch_bounds__(256) ssm_segment_states(const __grid_constant__ TcParams p) {
     const int64_t n = blockIdx.x, unit = blockIdx.y, nunits = (int64_t)p.groups * p.units;
-    __shared__ int longest;
-    if (cut_of(p, &longest) == 0) return;
+    if (p.items != nullptr && p.items[0].z == 0) return;
     const int64_t ls = (int64_t)p.seg_chunks * kL, per = (p.seqlen + ls - 1) / ls;
     int64_t t0, t1;
     if (!seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, n, t0, t1)) return;
@@ -834,17 +805,21 @@ int64_t segment_slots(bool varlen, int64_t seqlen, int64_t rows, int64_t num_seq
 struct SegBytes {
     int seg;
     int64_t slots;
-    size_t state, total;
+    bool ordered;
+    size_t state, items, total;
 };
 SegBytes segment_bytes(bool varlen, int64_t seqlen, int64_t rows, int64_t num_seqs, int heads, int groups, int head_dim,
                        int d_state) {
     SegBytes b{};
     b.seg = segment_chunks(varlen, seqlen, rows, num_seqs, unit_pairs(heads, groups, head_dim));
     b.slots = segment_slots(varlen, seqlen, rows, num_seqs, b.seg);
-    if (b.seg == 0) return b;
-    const size_t units = (size_t)heads * ((head_dim + 63) / 64);
-    b.state = (size_t)b.slots * units * d_state * 64 * 4;
-    b.total = b.state + ((size_t)b.slots * units * 4 + 255) / 256 * 256;
+    b.ordered = varlen && num_seqs > 1 && (b.seg > 0 || b.slots * unit_pairs(heads, groups, head_dim) > kSms);
+    if (b.seg > 0) {
+        const size_t units = (size_t)heads * ((head_dim + 63) / 64);
+        b.state = (size_t)b.slots * units * d_state * 64 * 4;
+        b.items = b.state + ((size_t)b.slots * units * 4 + 255) / 256 * 256;
+    }
+    b.total = b.items + (b.ordered ? (size_t)b.slots * 16 : 0);
     return b;
 }
 
@@ -859,8 +834,10 @@ bool ssm_tc_rows_ok(const SsmParams &p) {
            p.off_c % 8 == 0 && p.bc_group % 8 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
 }
 
-bool ssm_tc_segments(bool varlen, int64_t seqlen, int64_t rows, int64_t num_seqs, int heads, int groups, int head_dim) {
-    return segment_chunks(varlen, seqlen, rows, num_seqs, unit_pairs(heads, groups, head_dim)) > 0;
+int ssm_tc_launches(bool varlen, int64_t seqlen, int64_t rows, int64_t num_seqs, int heads, int groups, int head_dim, bool *segments) {
+    const SegBytes b = segment_bytes(varlen, seqlen, rows, num_seqs, heads, groups, head_dim, 1);
+    *segments = b.seg > 0;
+    return (b.ordered ? 1 : 0) + (b.seg > 0 ? 3 : 1);
 }
 
 size_t ssm_tc_workspace(bool varlen, int64_t seqlen, int64_t rows, int64_t num_seqs, int heads, int groups, int head_dim,
@@ -900,16 +877,21 @@ cudaError_t launch_ssm_tc(const SsmParams &s, void *workspace, cudaStream_t stre
     const SegBytes b = segment_bytes(varlen, s.seqlen, s.rows, s.num_seqs, s.heads, s.groups, s.head_dim, s.d_state);
     p.seg_chunks = b.seg;
     const int pairs = s.groups * p.pairs_per_group;
-    p.by_length = varlen && s.num_seqs > 1 && (b.seg > 0 || b.slots * pairs > kSms);
-    if (varlen && s.num_seqs > 1 && b.seg > 0) p.cut_over = (int32_t)(kCutOver * ((s.rows + kL - 1) / kL) * pairs / kSms);
+    if (b.seg > 0) p.cut_over = (int32_t)(kCutOver * ((s.rows + kL - 1) / kL) * pairs / kSms);
     p.seg_state = static_cast<float *>(workspace);
     p.seg_decay = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + b.state);
+    p.items = b.ordered ? reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) + b.items) : nullptr;
 
     const int64_t grid = b.slots * pairs;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(ssm_chunk_scan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_chunk_scan<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
+    if (b.ordered) {
+        ssm_order<<<1, kOrderThreads, 0, stream>>>(p, b.slots);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     if (b.seg > 0) {
         ssm_chunk_scan<true><<<(unsigned)grid, kThreads, kSmem, stream>>>(p);
         ssm_segment_states<<<dim3((unsigned)s.num_seqs, (unsigned)(s.groups * p.units), (unsigned)((s.d_state + 15) / 16)), 256, 0, stream>>>(p);

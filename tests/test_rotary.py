@@ -130,6 +130,36 @@ def test_turned_queries_and_keys_through_the_linear_rule():
     assert rel(outs[1], outs[0]) <= 2.0 ** -20
 
 
+@pytest.mark.gpu
+def test_rows_beyond_32_bits():
+    g = torch.Generator().manual_seed(14)
+    wide = torch.empty(1, 70, 1 << 25, dtype=torch.bfloat16, device="cuda")
+    q = wide[..., 64:64 + 3 * 64].unflatten(2, (3, 64))
+    q.copy_(torch.randn(1, 70, 3, 64, generator=g))
+    inv_freq, _ = lib.gdn_rotary_frequencies(64, device="cuda")
+    want = turn(q, torch.arange(70)[None], inv_freq, 0, False, False, 1.0)
+    lib.gdn_rotary(q, None, inv_freq, q_out=q)
+    assert rel(q, want) <= 2 ** -8
+
+
+@pytest.mark.gpu
+def test_another_stream_and_a_captured_graph():
+    g = torch.Generator().manual_seed(15)
+    q, k = torch.randn(2, 37, 4, 128, generator=g).half().cuda(), torch.randn(2, 37, 1, 128, generator=g).half().cuda()
+    inv_freq, _ = lib.gdn_rotary_frequencies(128, device="cuda")
+    want = lib.gdn_rotary(q, k, inv_freq)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = lib.gdn_rotary(q, k, inv_freq, stream=side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = lib.gdn_rotary(q, k, inv_freq)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(got, want, out))
+
+
 # ------------------------------------------------------------------ frequencies and refusals (no GPU)
 def test_frequencies():
     f = lib.gdn_rotary_frequencies

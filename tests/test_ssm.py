@@ -156,6 +156,17 @@ def test_rows_may_be_slices_at_any_stride(gap):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f16"])
+@pytest.mark.parametrize("K", [1, 2, 3, 4])
+def test_convolved_rows_on_16_bytes(io, K):
+    """Rows that bulk copies can take, in runs that hold several sequences, a sequence several runs."""
+    H, P, G, N = 9, 64, 1, 40
+    m = draw(io, [1, 2, 0, 3, 150, 70, 1, 1, 77, 5], H, P, G, N, K, seed=K, gap=(-(2 * H * P + 2 * G * N + H)) % 8)
+    assert m["xbc"].stride(1) % 8 == 0 and m["xbc"].data_ptr() % 16 == 0
+    check(m, prefill(m), define(m))
+
+
+@pytest.mark.gpu
 def test_optional_operands_and_bounds_on_the_step():
     m = draw("f32", [40, 3], 4, 32, 2, 16, 3, seed=4)
     args = dict(kwargs(m), D=None, dt_bias=None, conv_bias=None)
@@ -326,7 +337,104 @@ def test_a_slot_outside_the_pool_skips_its_row():
     assert not torch.equal(state[2], m["state"][2])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("slots", [False, True])
+def test_many_tokens(slots):
+    """More rows and heads than a launch holds blocks for."""
+    B = 150
+    m = draw("bf16", [1] * B, 8, 64, 2, 64, 4, packed=False, seed=15)
+    at = torch.randperm(B, generator=torch.Generator().manual_seed(1)).cuda() if slots else torch.arange(B, device="cuda")
+    state, conv = torch.empty_like(m["state"]), torch.empty_like(m["conv"])
+    state[at], conv[at] = m["state"], m["conv"]
+    y = lib.gdn_ssm_decode(m["xbc"], m["dt"], m["A_log"], state, conv_state=conv, slots=at.int() if slots else None, **kwargs(m))
+    check(m, (y, state[at], conv[at]), define(m))
+
+
+# ------------------------------------------------------------------ rows and entries far apart
+@pytest.mark.gpu
+@pytest.mark.parametrize("io,K", [("bf16", 0), ("bf16", 4), ("f16", 4)])
+def test_rows_beyond_32_bits(io, K):
+    """Rows 2^25 elements apart: the last ones start behind 2^31 elements and 2^32 bytes."""
+    m = draw(io, [60, 10], 4, 64, 1, 64, K, seed=16)
+    want = define(m)
+    for name in ("xbc", "dt", "z"):
+        wide = torch.empty(70, 1 << 25, dtype=DT[io], device="cuda")
+        rows = m[name].flatten(2)
+        part = wide[None, :, 64:64 + rows.shape[2]]
+        part.copy_(rows)
+        m[name] = part.unflatten(2, m[name].shape[2:])
+    check(m, prefill(m), want)
+    last = {k: m[k][:, 69:] for k in ("xbc", "dt", "z")}
+    one = dict(m, lens=[1], packed=False, state=m["state"][:1], conv=m["conv"][:1] if K else None, **last)
+    state, conv = one["state"].clone(), one["conv"].clone() if K else None
+    y = lib.gdn_ssm_decode(one["xbc"], one["dt"], one["A_log"], state, conv_state=conv, **kwargs(one))
+    check(one, (y, state, conv), define(one))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,P", [(64, 64), (32, 128)])
+def test_a_pool_beyond_32_bits(H, P):
+    m = draw("bf16", [1, 1, 1], H, P, 1, 128, 4, packed=False, seed=17)
+    E = 4400                                             # of 2^19 fp32 values each
+    state = torch.empty(E, H, 128, P, device="cuda")
+    conv = torch.empty(E, 3, m["xbc"].shape[2], dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([E - 1, 0, E - 7], device="cuda")
+    state[at], conv[at] = m["state"], m["conv"]
+    y = lib.gdn_ssm_decode(m["xbc"], m["dt"], m["A_log"], state, conv_state=conv, slots=at.int(), **kwargs(m))
+    assert lib.gdn_last_device_status() == 0
+    check(m, (y, state[at], conv[at]), define(m))
+
+
 # ------------------------------------------------------------------ streams, graphs
+@pytest.mark.gpu
+def test_two_graphs_and_an_eager_call():
+    """Two captured calls and an eager one, replayed in turn: none keeps anything from another."""
+    runs = []
+    for lens, seed in (([500, 3, 200], 21), ([1300, 900], 22)):
+        m = draw("bf16", lens, 64, 64, 2, 64, 4, seed=seed, gap=(-(2 * 4096 + 256 + 64)) % 8)
+        want = prefill(m)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = lib.gdn_ssm_prefill(m["xbc"], m["dt"], m["A_log"], state_in=m["state"], conv_state_in=m["conv"],
+                                      cu_seqlens=m["cu"], **kwargs(m))
+        runs.append((m, want, graph, out))
+    for i in (0, 1, 1, 0):
+        m, want, graph, out = runs[i]
+        for t in out:
+            t.zero_()
+        graph.replay()
+        eager = prefill(runs[1 - i][0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        assert all(torch.equal(a, b) for a, b in zip(eager, runs[1 - i][1]))
+
+
+@pytest.mark.gpu
+def test_captured_tokens_advance_the_states():
+    m = draw("bf16", [6, 6], 4, 64, 1, 128, 4, packed=False, seed=23)
+    want = define(m)
+    state, conv = m["state"].clone(), m["conv"].clone()
+    step = {k: m[k][:, :1].clone() for k in ("xbc", "dt", "z")}
+    call = lambda **kw: lib.gdn_ssm_decode(step["xbc"], step["dt"], m["A_log"], state, conv_state=conv,  # noqa: E731
+                                           **dict(kwargs(m), z=step["z"]), **kw)
+    call()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        y = call()
+    state.copy_(m["state"])
+    conv.copy_(m["conv"])
+    ys = []
+    for t in range(6):
+        for k in step:
+            step[k].copy_(m[k][:, t:t + 1])
+        graph.replay()
+        ys.append(y.clone())
+    assert rel(torch.cat(ys, 1), want[0]) <= y_tol(torch.bfloat16)
+    assert rel(state, want[1]) <= state_tol(m) and torch.equal(conv.double().cpu(), want[2])
+
+
 @pytest.mark.gpu
 def test_another_stream_and_a_captured_graph():
     m = draw("bf16", [200, 50], 4, 64, 1, 128, 4, seed=11)
@@ -439,6 +547,8 @@ def test_bad_decode_pointers_are_refused(over):
     (dict(seqlen=8192, heads=64, groups=1, d_state=128), dict(conv_kernel=0), (gdn.PATH_TC_TP, 3)),
     (dict(seqlen=8192, heads=64, groups=1, d_state=100), dict(conv_kernel=0), (gdn.PATH_TC_TP, 4)),
     (dict(seqlen=100, heads=64, groups=8), {}, (gdn.PATH_TC, 2)), (dict(seqlen=100, batch=64, num_seqs=64), dict(conv_kernel=0), (gdn.PATH_TC, 1)),
+    (dict(seqlen=16384, num_seqs=12, heads=64, groups=8, d_state=128), {}, (gdn.PATH_TC_TP, 5)),
+    (dict(seqlen=16384, num_seqs=12, heads=512, groups=8, d_state=128), dict(conv_kernel=0), (gdn.PATH_TC, 2)),
     (dict(io_dtype=0), {}, (gdn.PATH_SIMT, 2)), (dict(io_dtype=2), dict(conv_kernel=0), (gdn.PATH_SIMT, 1)),
     (dict(d_state=129), {}, (gdn.PATH_SIMT, 2)), (dict(head_dim=52), {}, (gdn.PATH_SIMT, 2)), (dict(batch=0, num_seqs=0), {}, (gdn.PATH_SIMT, 0))])
 def test_plans(shape, params, want):
