@@ -13,6 +13,8 @@
 namespace gdn {
 namespace {
 
+constexpr int kSms = 152;
+
 // ------------------------------------------------------------------ causal convolution
 // A thread takes V channels and a run of kRun token rows, the last K - 1 rows kept in
 // registers; the rows are loaded kAhead at a time, so that enough of them are in flight.
@@ -237,14 +239,16 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
 }
 
 // The convolution of 16-bit rows that bulk copies can take (16-byte rows and channel runs): a CTA
-// takes 512 channels of a run of kBulkRun rows, which arrive kStageRows at a time in a ring of
+// takes 512 channels of a run of up to kBulkRun rows, which arrive kStageRows at a time in a ring of
 // kBulkRing stages; a thread reads its four channels of each row once, the last K - 1 rows kept in
 // registers, and writes them straight out.  (The kernel above, with its loads in registers, holds
 // 18 KB in flight to an SM, and took 91 us for 8,192 rows of 4,352 channels; this one 150 KB: 46 us.)
+// Runs are shorter where whole ones would leave SMs without four CTAs: 2,002 rows of 1,792 channels
+// take 29 us in runs of 72 and 12 us in runs of 12.
 constexpr int kStageRows = 6, kBulkRing = 4, kBulkRun = 72, kBulkChannels = 512;
 
 template <typename IO, int K>
-__global__ void __launch_bounds__(128) ssm_conv_bulk_kernel(const SsmConvParams p, int64_t run_blocks) {
+__global__ void __launch_bounds__(128) ssm_conv_bulk_kernel(const SsmConvParams p, int64_t run_blocks, int run) {
     using namespace tc;
     constexpr int V = 4;
     using Vec = Pack<IO, V>;
@@ -255,8 +259,8 @@ __global__ void __launch_bounds__(128) ssm_conv_bulk_kernel(const SsmConvParams 
         if (c0 < p.C) conv_states<IO, V, K>(p, (int64_t)blockIdx.x - run_blocks, c0);
         return;
     }
-    const int64_t r0 = (int64_t)blockIdx.x * kBulkRun;
-    const int left = (int)(p.rows - r0 < kBulkRun ? p.rows - r0 : kBulkRun), stages = (left + kStageRows - 1) / kStageRows;
+    const int64_t r0 = (int64_t)blockIdx.x * run;
+    const int left = (int)(p.rows - r0 < run ? p.rows - r0 : run), stages = (left + kStageRows - 1) / kStageRows;
     const uint32_t bytes = 2u * (uint32_t)(p.C - cta0 < kBulkChannels ? p.C - cta0 : kBulkChannels);
     if (tid == 0) {
         for (int i = 0; i < kBulkRing; ++i) mbar_init(&full[i], 1);
@@ -369,13 +373,15 @@ cudaError_t conv_dispatch(const SsmConvParams &p, cudaStream_t stream) {
     if constexpr (sizeof(IO) == 2) {
         auto by16 = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
         if (wide && p.w != nullptr && p.rows > 0 && p.C % 8 == 0 && p.ld_x % 8 == 0 && by16(p.x)) {
-            const int64_t runs = (p.rows + kBulkRun - 1) / kBulkRun;
-            const dim3 grid((unsigned)(runs + (p.K > 1 ? p.num_seqs : 0)), (unsigned)((p.C + kBulkChannels - 1) / kBulkChannels));
+            const int64_t blocks = (p.C + kBulkChannels - 1) / kBulkChannels, fair = p.rows * blocks / (4 * kSms);
+            const int run = fair >= kBulkRun ? kBulkRun : fair < kStageRows ? kStageRows : (int)(fair / kStageRows * kStageRows);
+            const int64_t runs = (p.rows + run - 1) / run;
+            const dim3 grid((unsigned)(runs + (p.K > 1 ? p.num_seqs : 0)), (unsigned)blocks);
             switch (p.K) {
-                case 1: ssm_conv_bulk_kernel<IO, 1><<<grid, 128, 0, stream>>>(p, runs); break;
-                case 2: ssm_conv_bulk_kernel<IO, 2><<<grid, 128, 0, stream>>>(p, runs); break;
-                case 3: ssm_conv_bulk_kernel<IO, 3><<<grid, 128, 0, stream>>>(p, runs); break;
-                default: ssm_conv_bulk_kernel<IO, 4><<<grid, 128, 0, stream>>>(p, runs); break;
+                case 1: ssm_conv_bulk_kernel<IO, 1><<<grid, 128, 0, stream>>>(p, runs, run); break;
+                case 2: ssm_conv_bulk_kernel<IO, 2><<<grid, 128, 0, stream>>>(p, runs, run); break;
+                case 3: ssm_conv_bulk_kernel<IO, 3><<<grid, 128, 0, stream>>>(p, runs, run); break;
+                default: ssm_conv_bulk_kernel<IO, 4><<<grid, 128, 0, stream>>>(p, runs, run); break;
             }
             return cudaGetLastError();
         }
@@ -547,7 +553,7 @@ cudaError_t scan_dispatch(const SsmParams &p, cudaStream_t stream) {
 // A CTA takes one (row, head): its state [N][P] as float4 quads, a thread's quads all of one
 // column quad, kDecQuads of them in flight while the row's convolution and gates are
 // computed.  Bound by reading and writing the state.
-constexpr int kDecThreads = 256, kDecQuads = 8, kSms = 152;
+constexpr int kDecThreads = 256, kDecQuads = 8;
 
 template <typename IO>
 __device__ __forceinline__ float conv_token(const SsmDecodeParams &p, const IO *x, const IO *conv, int c) {
@@ -798,17 +804,26 @@ __global__ void __launch_bounds__(kDecThreads, 2) ssm_decode_stream_kernel(const
 }
 
 // The conv states one token on, after the step has read them: rows move up, x comes last.
-// (The step's CTAs all read their group's B and C taps, so it cannot move them itself.)
-template <typename IO>
+// (The step's CTAs all read their group's B and C taps, so it cannot move them itself.)  V channels
+// to a thread: 16 bytes where the rows allow it (256 rows of 6,144 channels: 14.8 us singly,
+// 6.6 us so).
+template <typename IO, int V>
 __global__ void __launch_bounds__(256) ssm_conv_shift_kernel(const SsmDecodeParams p) {
-    const int c = blockIdx.y * 256 + threadIdx.x;
+    using Vec = Pack<IO, V>;
+    const int c = V * (blockIdx.y * 256 + threadIdx.x);
     const int64_t b = blockIdx.x;
     if (c >= p.C) return;
     const int64_t e = p.slots ? (int64_t)p.slots[b] : b;
     if (e < 0 || e >= p.pool_size) return;
     IO *conv = static_cast<IO *>(p.conv) + e * (int64_t)(p.K - 1) * p.C + c;
-    for (int j = 0; j + 1 < p.K - 1; ++j) conv[(int64_t)j * p.C] = conv[(int64_t)(j + 1) * p.C];
-    conv[(int64_t)(p.K - 2) * p.C] = static_cast<const IO *>(p.x)[b * p.ld_x + c];
+    auto row = [&](int j) { return reinterpret_cast<Vec *>(conv + (int64_t)j * p.C); };
+    const Vec x = *reinterpret_cast<const Vec *>(static_cast<const IO *>(p.x) + b * p.ld_x + c);
+    Vec a = x, d = x;
+    if (p.K > 2) a = *row(1);
+    if (p.K > 3) d = *row(2);
+    if (p.K > 2) *row(0) = a;
+    if (p.K > 3) *row(1) = d;
+    *row(p.K - 2) = x;
 }
 
 template <typename IO>
@@ -824,8 +839,13 @@ cudaError_t decode_dispatch(const SsmDecodeParams &p, cudaStream_t stream) {
     } else {
         ssm_decode_kernel<IO><<<(unsigned)units, kDecThreads, 0, stream>>>(p);
     }
-    if (p.w != nullptr && p.K > 1)
-        ssm_conv_shift_kernel<IO><<<dim3((unsigned)p.batch, (unsigned)((p.C + 255) / 256)), 256, 0, stream>>>(p);
+    if (p.w != nullptr && p.K > 1) {
+        constexpr int V = 16 / sizeof(IO);
+        const bool wide = p.C % V == 0 && p.ld_x % V == 0 && (reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.conv)) % 16 == 0;
+        const dim3 grid((unsigned)p.batch, (unsigned)((p.C + 255) / 256)), few((unsigned)p.batch, (unsigned)((p.C / V + 255) / 256));
+        if (wide) ssm_conv_shift_kernel<IO, V><<<few, 256, 0, stream>>>(p);
+        else ssm_conv_shift_kernel<IO, 1><<<grid, 256, 0, stream>>>(p);
+    }
     return cudaGetLastError();
 }
 

@@ -338,11 +338,12 @@ def test_a_slot_outside_the_pool_skips_its_row():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("K,gap", [(2, 0), (3, 0), (4, 0), (4, 5)])
 @pytest.mark.parametrize("slots", [False, True])
-def test_many_tokens(slots):
-    """More rows and heads than a launch holds blocks for."""
+def test_many_tokens(slots, K, gap):
+    """More rows and heads than a launch holds blocks for; mixed rows on 16 bytes and off them."""
     B = 150
-    m = draw("bf16", [1] * B, 8, 64, 2, 64, 4, packed=False, seed=15)
+    m = draw("bf16", [1] * B, 8, 64, 2, 64, K, packed=False, seed=15, gap=gap)
     at = torch.randperm(B, generator=torch.Generator().manual_seed(1)).cuda() if slots else torch.arange(B, device="cuda")
     state, conv = torch.empty_like(m["state"]), torch.empty_like(m["conv"])
     state[at], conv[at] = m["state"], m["conv"]
@@ -493,7 +494,8 @@ def _params(**kw):
 
 BAD_SHAPES = [dict(io_dtype=5), dict(batch=-1, num_seqs=-1), dict(seqlen=-1), dict(num_seqs=2), dict(heads=0), dict(groups=3),
               dict(groups=0), dict(head_dim=0), dict(head_dim=6), dict(head_dim=260), dict(d_state=0), dict(d_state=257),
-              dict(xbc_stride=5), dict(dt_stride=3), dict(z_stride=1), dict(heads=65536, groups=1), dict(seqlen=2 ** 31)]
+              dict(xbc_stride=5), dict(dt_stride=3), dict(z_stride=1), dict(heads=65536, groups=1), dict(seqlen=2 ** 31),
+              dict(heads=65535, groups=65535, head_dim=64, d_state=128)]
 BAD_PARAMS = [dict(conv_kernel=5), dict(conv_kernel=-1), dict(conv_activation=2), dict(dt_min=-1.0), dict(dt_min=math.nan),
               dict(dt_max=math.nan), dict(dt_min=2.0), dict(dt_min=math.inf, dt_max=math.inf)]
 P64 = [ctypes.c_void_p(1 << 40 | i << 32) for i in range(16)]     # addresses that are never read: every call is refused
