@@ -16,12 +16,21 @@ namespace {
 constexpr int kSms = 152;
 
 // ------------------------------------------------------------------ causal convolution
-// A thread takes V channels and a run of kRun token rows, the last K - 1 rows kept in
+// A thread takes V channels and a run of up to kRun token rows, the last K - 1 rows kept in
 // registers; the rows are loaded kAhead at a time, so that enough of them are in flight.
 // Products of two 16-bit values are exact in fp32, so the sum's order alone decides its
 // value: bias first, then the taps in order.  Bound by reading and writing the rows; the
 // arithmetic (13 instructions a value) takes nearly as long.
 constexpr int kRun = 33, kAhead = 3;
+
+// Rows of a run: whole ones unless they leave SMs without four CTAs, where shorter ones, of whole
+// stages, do better although each reads K - 1 rows more (bulk copies below, 2,002 rows of 1,792 f16
+// channels: 29 us in runs of 72, 12 us in runs of 12; 1,045 f32 rows of 704 channels here: 27.5 us
+// in runs of 33, 7.6 us in runs of 3).
+int rows_of_run(int64_t rows, int64_t across, int most, int stage) {
+    const int64_t fair = rows * across / (4 * kSms);
+    return fair >= most ? most : fair < stage ? stage : (int)(fair / stage * stage);
+}
 
 template <typename IO, int V> struct alignas(sizeof(IO) * V) Pack {
     IO v[V];
@@ -144,7 +153,7 @@ __device__ __forceinline__ int64_t u_channel(const SsmConvParams &p, int c0) {
 }
 
 template <typename IO, int V, int K>
-__global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, int64_t run_blocks) {
+__global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, int64_t run_blocks, int run) {
     using Vec = Pack<IO, V>;
     const int64_t cv = (int64_t)blockIdx.y * 128 + threadIdx.x;      // channel vector
     if (cv * V >= p.C) return;
@@ -169,8 +178,8 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
         }
     }
 
-    const int64_t r0 = (int64_t)blockIdx.x * kRun;
-    const int64_t r1 = r0 + kRun < p.rows ? r0 + kRun : p.rows;
+    const int64_t r0 = (int64_t)blockIdx.x * run;
+    const int64_t r1 = r0 + run < p.rows ? r0 + run : p.rows;
     Walk seq = walk_from(p, r0);
     float past[K > 1 ? K - 1 : 1][V];
 #pragma unroll
@@ -243,8 +252,6 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
 // kBulkRing stages; a thread reads its four channels of each row once, the last K - 1 rows kept in
 // registers, and writes them straight out.  (The kernel above, with its loads in registers, holds
 // 18 KB in flight to an SM, and took 91 us for 8,192 rows of 4,352 channels; this one 150 KB: 46 us.)
-// Runs are shorter where whole ones would leave SMs without four CTAs: 2,002 rows of 1,792 channels
-// take 29 us in runs of 72 and 12 us in runs of 12.
 constexpr int kStageRows = 6, kBulkRing = 4, kBulkRun = 72, kBulkChannels = 512;
 
 template <typename IO, int K>
@@ -350,15 +357,17 @@ __global__ void __launch_bounds__(128) ssm_conv_bulk_kernel(const SsmConvParams 
 
 template <typename IO, int V>
 cudaError_t conv_launch(const SsmConvParams &p, cudaStream_t stream) {
-    const int64_t runs = (p.rows + kRun - 1) / kRun;
+    const int64_t across = (p.C / V + 127) / 128;
+    const int run = rows_of_run(p.rows, across, kRun, kAhead);
+    const int64_t runs = (p.rows + run - 1) / run;
     const int64_t blocks = runs + (p.K > 1 ? p.num_seqs : 0);
     if (blocks == 0) return cudaSuccess;
-    const dim3 grid((unsigned)blocks, (unsigned)((p.C / V + 127) / 128));
+    const dim3 grid((unsigned)blocks, (unsigned)across);
     switch (p.K) {
-        case 1: ssm_conv_kernel<IO, V, 1><<<grid, 128, 0, stream>>>(p, runs); break;
-        case 2: ssm_conv_kernel<IO, V, 2><<<grid, 128, 0, stream>>>(p, runs); break;
-        case 3: ssm_conv_kernel<IO, V, 3><<<grid, 128, 0, stream>>>(p, runs); break;
-        default: ssm_conv_kernel<IO, V, 4><<<grid, 128, 0, stream>>>(p, runs); break;
+        case 1: ssm_conv_kernel<IO, V, 1><<<grid, 128, 0, stream>>>(p, runs, run); break;
+        case 2: ssm_conv_kernel<IO, V, 2><<<grid, 128, 0, stream>>>(p, runs, run); break;
+        case 3: ssm_conv_kernel<IO, V, 3><<<grid, 128, 0, stream>>>(p, runs, run); break;
+        default: ssm_conv_kernel<IO, V, 4><<<grid, 128, 0, stream>>>(p, runs, run); break;
     }
     return cudaGetLastError();
 }
@@ -373,10 +382,10 @@ cudaError_t conv_dispatch(const SsmConvParams &p, cudaStream_t stream) {
     if constexpr (sizeof(IO) == 2) {
         auto by16 = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
         if (wide && p.w != nullptr && p.rows > 0 && p.C % 8 == 0 && p.ld_x % 8 == 0 && by16(p.x)) {
-            const int64_t blocks = (p.C + kBulkChannels - 1) / kBulkChannels, fair = p.rows * blocks / (4 * kSms);
-            const int run = fair >= kBulkRun ? kBulkRun : fair < kStageRows ? kStageRows : (int)(fair / kStageRows * kStageRows);
+            const int64_t across = (p.C + kBulkChannels - 1) / kBulkChannels;
+            const int run = rows_of_run(p.rows, across, kBulkRun, kStageRows);
             const int64_t runs = (p.rows + run - 1) / run;
-            const dim3 grid((unsigned)(runs + (p.K > 1 ? p.num_seqs : 0)), (unsigned)blocks);
+            const dim3 grid((unsigned)(runs + (p.K > 1 ? p.num_seqs : 0)), (unsigned)across);
             switch (p.K) {
                 case 1: ssm_conv_bulk_kernel<IO, 1><<<grid, 128, 0, stream>>>(p, runs, run); break;
                 case 2: ssm_conv_bulk_kernel<IO, 2><<<grid, 128, 0, stream>>>(p, runs, run); break;
