@@ -46,7 +46,8 @@
  * gdn_decode_layer (conv -> decode step -> norm in one kernel) and gdn_prefill_layer
  * (conv -> prefill -> norm, the convolution inside the chunk prep; with
  * gdn_prefill_layer_workspace_bytes), and the neighbouring state-space layer:
- * gdn_ssm_prefill (with gdn_ssm_prefill_workspace_bytes) and gdn_ssm_decode, with
+ * gdn_ssm_prefill (with gdn_ssm_prefill_workspace_bytes and gdn_ssm_prefill_plan) and
+ * gdn_ssm_decode, with
  * gdn_rotary and gdn_rotary_frequencies for positions.
  *  - gdn_last_error_message() gives a human-readable detail of the last
  *    non-OK status returned on the calling thread.

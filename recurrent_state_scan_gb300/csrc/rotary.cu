@@ -21,7 +21,7 @@ namespace {
 // A CTA takes `tile` token rows: it fills a table of their cosines and sines, then streams the
 // heads.  A thread's item is a place in the row -- two vectors of V values (the V pairs) or one of
 // the copied rest -- that it follows down the rows, kRows of them in flight.  Bound by reading and
-// writing the heads: 118 us for 32,768 rows of 40 heads of 128 (5.7 TB/s); with four rows in flight,
+// writing the heads: 117 us for 32,768 rows of 40 heads of 128 (5.7 TB/s); with four rows in flight,
 // and so half as many warps to an SM, it took 163 us.
 constexpr int kThreads = 256, kRows = 2, kMaxPairs = 128, kMaxTile = 32;
 

@@ -251,7 +251,9 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
 // takes 512 channels of a run of up to kBulkRun rows, which arrive kStageRows at a time in a ring of
 // kBulkRing stages; a thread reads its four channels of each row once, the last K - 1 rows kept in
 // registers, and writes them straight out.  (The kernel above, with its loads in registers, holds
-// 18 KB in flight to an SM, and took 91 us for 8,192 rows of 4,352 channels; this one 150 KB: 46 us.)
+// 18 KB in flight to an SM, and took 91 us for 8,192 rows of 4,352 channels; this one 150 KB: 45 us.)
+// Bound by issue (61-71% of the slots, mostly the silu's), at 3.2 TB/s there and 3.8 TB/s for 16,384
+// rows of 6,144 channels (106 us).
 constexpr int kStageRows = 6, kBulkRing = 4, kBulkRun = 72, kBulkChannels = 512;
 
 template <typename IO, int K>
@@ -658,7 +660,9 @@ __global__ void __launch_bounds__(kDecThreads, 4) ssm_decode_kernel(const SsmDec
 // (row, head) units, whose states pass through a ring of kRing stages in shared memory by bulk
 // copies in both directions.  The convolved B and C of a (row, group) are kept for all of its
 // heads, and the next unit's inputs are loaded while this one is computed.  Two CTAs to an SM
-// keep 128 KB of loads in flight.
+// keep 128 KB of loads in flight.  Bound by reading and writing the states: 256 rows of 64 heads of
+// 64 x 128 take 182 us (6.0 TB/s of a copy's 6.8); the call took 253 us with the kernel above, and
+// 200 with this one.
 constexpr int kStreamState = 8192, kRing = 3, kSlots = 3;
 
 template <typename IO>
