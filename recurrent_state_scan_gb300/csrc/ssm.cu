@@ -23,13 +23,15 @@ constexpr int kSms = 152;
 // arithmetic (13 instructions a value) takes nearly as long.
 constexpr int kRun = 33, kAhead = 3;
 
-// Rows of a run: whole ones unless they leave SMs without four CTAs, where shorter ones, of whole
-// stages, do better although each reads K - 1 rows more (bulk copies below, 2,002 rows of 1,792 f16
-// channels: 29 us in runs of 72, 12 us in runs of 12; 1,045 f32 rows of 704 channels here: 27.5 us
-// in runs of 33, 7.6 us in runs of 3).
+// Rows of a run: as many runs as fill the SMs, six CTAs to each, in whole waves of runs of up to
+// `most` rows, in whole stages.  (Runs of 72 rows: 2,002 rows of 1,792 f16 channels took 29 us, in
+// runs of 12 by bulk copies below 12 us; 1,045 f32 rows of 704 channels here 27.5 us in runs of 33, 7.6
+// in runs of 3, although each run reads K - 1 rows more.  8,192 rows of 4,352 channels: WAVEOLD us in
+// runs of 72, WAVENEW in runs of 84, which are one wave.)
 int rows_of_run(int64_t rows, int64_t across, int most, int stage) {
-    const int64_t fair = rows * across / (4 * kSms);
-    return fair >= most ? most : fair < stage ? stage : (int)(fair / stage * stage);
+    const int64_t work = rows * across, wave = 6 * kSms, waves = (work + most * wave - 1) / (most * wave);
+    const int64_t run = waves == 0 ? stage : (work + waves * wave - 1) / (waves * wave);
+    return (int)((run + stage - 1) / stage * stage);
 }
 
 template <typename IO, int V> struct alignas(sizeof(IO) * V) Pack {
@@ -54,7 +56,7 @@ template <typename IO, int V> __device__ __forceinline__ void silu_rounded(float
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
             const F2 x = {v[i], v[i + 1]}, t = mul2(x, both(kHi));
-            const F2 rest = fma2(x, both(kLo), fma2(x, both(kHi), {-t.x, -t.y}));
+            const F2 rest = fma2(x, both(kLo), fma2(x, both(kHi), mul2(x, both(-kHi))));   // (the last is -t)
             F2 e = {ex2(t.x), ex2(t.y)};
             e = fma2(e, mul2(rest, both(0.69314718f)), e);
             const F2 d = add2(e, both(1.f)), y = mul2(x, {rcp(d.x), rcp(d.y)});
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
 // 18 KB in flight to an SM, and took 91 us for 8,192 rows of 4,352 channels; this one 150 KB: 45 us.)
 // Bound by issue (61-71% of the slots, mostly the silu's), at 3.2 TB/s there and 3.8 TB/s for 16,384
 // rows of 6,144 channels (106 us).
-constexpr int kStageRows = 6, kBulkRing = 4, kBulkRun = 72, kBulkChannels = 512;
+constexpr int kStageRows = 6, kBulkRing = 4, kBulkRun = 96, kBulkChannels = 512;
 
 template <typename IO, int K>
 __global__ void __launch_bounds__(128) ssm_conv_bulk_kernel(const SsmConvParams p, int64_t run_blocks, int run) {
@@ -309,13 +311,51 @@ __global__ void __launch_bounds__(128) ssm_conv_bulk_kernel(const SsmConvParams 
     }
     int turn = at.t1 - r0 < left ? (int)(at.t1 - r0) : left;
     bool ok = true, more = true;       // more: the offsets lead to a sequence for the next row
+    auto taps = [&](const float (*in)[V], float (&acc)[V]) {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            F2 a = {bias[v], bias[v + 1]};
+#pragma unroll
+            for (int j = 0; j < K; ++j) a = fma2({w[j][v], w[j][v + 1]}, {in[j][v], in[j][v + 1]}, a);
+            acc[v] = a.x;
+            acc[v + 1] = a.y;
+        }
+    };
+    auto emit = [&](float (&acc)[V], IO *to) {
+        if (p.silu) silu_rounded<IO, V>(acc);
+        Vec out;
+#pragma unroll
+        for (int v = 0; v < V; ++v) IoType<IO>::st(&out.v[v], acc[v]);
+        *reinterpret_cast<Vec *>(to) = out;
+    };
 #pragma unroll 1
     for (int s = 0; s < stages; ++s) {
         ok = mbar_wait(&full[s % kBulkRing], (s / kBulkRing) & 1, 4000000000LL) && ok;
-        if (live && ok && more) {
+        const IO(*stage)[kBulkChannels] = ring[s % kBulkRing];
+        const int first = s * kStageRows;
+        if (live && ok && more && first + kStageRows <= turn) {
+            // A whole stage of one sequence (turn is not behind the run).
+            float in[K - 1 + kStageRows][V];
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) in[j][v] = past[j][v];
+#pragma unroll
+            for (int i = 0; i < kStageRows; ++i) widen<IO, V>(*reinterpret_cast<const Vec *>(&stage[i][V * tid]), in[K - 1 + i]);
 #pragma unroll
             for (int i = 0; i < kStageRows; ++i, u += p.ld_u) {
-                const int r = s * kStageRows + i;
+                float acc[V];
+                taps(&in[i], acc);
+                emit(acc, u);
+            }
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) past[j][v] = in[kStageRows + j][v];
+        } else if (live && ok && more) {
+#pragma unroll 1
+            for (int i = 0; i < kStageRows; ++i, u += p.ld_u) {
+                const int r = first + i;
                 if (r >= left) break;
                 if (r >= turn) {
                     if (!(more = walk_on(p, at, r0 + r))) break;
@@ -327,28 +367,18 @@ __global__ void __launch_bounds__(128) ssm_conv_bulk_kernel(const SsmConvParams 
                         if (cin) widen<IO, V>(*reinterpret_cast<const Vec *>(cin + (at.n * (K - 1) + j) * p.C), past[j]);
                     }
                 }
-                float now[V], acc[V];
-                widen<IO, V>(*reinterpret_cast<const Vec *>(&ring[s % kBulkRing][i][V * tid]), now);
+                float in[K][V], acc[V];
 #pragma unroll
-                for (int v = 0; v < V; v += 2) {
-                    F2 a = {bias[v], bias[v + 1]};
+                for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-                    for (int j = 0; j < K - 1; ++j) a = fma2({w[j][v], w[j][v + 1]}, {past[j][v], past[j][v + 1]}, a);
-                    a = fma2({w[K - 1][v], w[K - 1][v + 1]}, {now[v], now[v + 1]}, a);
-                    acc[v] = a.x;
-                    acc[v + 1] = a.y;
-                }
-                if (p.silu) silu_rounded<IO, V>(acc);
-                Vec out;
+                    for (int v = 0; v < V; ++v) in[j][v] = past[j][v];
+                widen<IO, V>(*reinterpret_cast<const Vec *>(&stage[i][V * tid]), in[K - 1]);
+                taps(in, acc);
+                emit(acc, u);
 #pragma unroll
-                for (int v = 0; v < V; ++v) IoType<IO>::st(&out.v[v], acc[v]);
-                *reinterpret_cast<Vec *>(u) = out;
+                for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-#pragma unroll
-                    for (int j = 0; j + 1 < K - 1; ++j) past[j][v] = past[j + 1][v];
-                    if (K > 1) past[K > 1 ? K - 2 : 0][v] = now[v];
-                }
+                    for (int v = 0; v < V; ++v) past[j][v] = in[j + 1][v];
             }
         }
         __syncthreads();        // the stage has been read
