@@ -26,8 +26,8 @@ constexpr int kRun = 33, kAhead = 3;
 // Rows of a run: as many runs as fill the SMs, six CTAs to each, in whole waves of runs of up to
 // `most` rows, in whole stages.  (Runs of 72 rows: 2,002 rows of 1,792 f16 channels took 29 us, in
 // runs of 12 by bulk copies below 12 us; 1,045 f32 rows of 704 channels here 27.5 us in runs of 33, 7.6
-// in runs of 3, although each run reads K - 1 rows more.  8,192 rows of 4,352 channels: WAVEOLD us in
-// runs of 72, WAVENEW in runs of 84, which are one wave.)
+// in runs of 3, although each run reads K - 1 rows more.  A prompt of 8,192 rows of 4,352 channels
+// took 213 us in runs of 72, a wave and a bit, and 205 in runs of 84, one wave.)
 int rows_of_run(int64_t rows, int64_t across, int most, int stage) {
     const int64_t work = rows * across, wave = 6 * kSms, waves = (work + most * wave - 1) / (most * wave);
     const int64_t run = waves == 0 ? stage : (work + waves * wave - 1) / (waves * wave);
@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
 // takes 512 channels of a run of up to kBulkRun rows, which arrive kStageRows at a time in a ring of
 // kBulkRing stages; a thread reads its four channels of each row once, the last K - 1 rows kept in
 // registers, and writes them straight out.  (The kernel above, with its loads in registers, holds
-// 18 KB in flight to an SM, and took 91 us for 8,192 rows of 4,352 channels; this one 150 KB: 45 us.)
-// Bound by issue (61-71% of the slots, mostly the silu's), at 3.2 TB/s there and 3.8 TB/s for 16,384
-// rows of 6,144 channels (106 us).
+// 18 KB in flight to an SM, and took 91 us for 8,192 rows of 4,352 channels; this one 150 KB: 40 us.)
+// Bound by issue (66% of the slots, mostly the silu's), at 3.6 TB/s there and 4.2 TB/s for 16,384
+// rows of 6,144 channels (95 us).  A barrier to a stage costs no more than counting its readers.
 constexpr int kStageRows = 6, kBulkRing = 4, kBulkRun = 96, kBulkChannels = 512;
 
 template <typename IO, int K>
