@@ -18,8 +18,8 @@
 // The warps' roles run side by side, a chunk apart where the data allows it.
 //
 // Bound by the chain from one chunk's y to the next (readout, M, its MMA) and by issue: a pair of
-// units takes 3.1 us a chunk (3.3 with z), of which the tensor pipe works a quarter, the issue slots
-// about half and shared memory about half.  8,192 tokens of 64 heads of 64 x 128 with z: 108 us on
+// units takes 2.9 us a chunk (3.2 with z), of which the tensor pipe works a quarter, the issue slots
+// about half and shared memory about half.  8,192 tokens of 64 heads of 64 x 128 with z: 103 us on
 // 128 CTAs, behind 46 us of state-only pass (its gates bound it) and 5 us for the segments' states.
 // Precision: the state is fp32 and its update's operands are exact (B) or a two-term bf16 split
 // (w x: 2^-17 of each product), because the state is returned in fp32 and carried on; M and
@@ -30,7 +30,7 @@
 // Where sequences x units leave most SMs idle, each sequence is cut along time: a state-only
 // pass of every segment but the last from zero, a short pass that turns the segments' ends into
 // the states entering them, and then all segments at once.  (Uncut, the 8,192 tokens above would
-// stand on 32 SMs for 128 chunks, 420 us.)  Packed sequences are taken by length.
+// stand on 32 SMs for 128 chunks, 410 us.)  Packed sequences are taken by length.
 #include <cudaTypedefs.h>
 #include <stddef.h>
 #include <string.h>
@@ -44,7 +44,6 @@ namespace {
 using namespace tc;
 
 constexpr int kL = 64;                       // tokens per chunk
-constexpr int kThreads = 640;
 constexpr long long kBudget = 4000000000LL;  // cycles (~2 s) before a wait gives up
 
 // Shared memory (1024-byte aligned): stages of what TMA brings, then the operands the threads
@@ -98,7 +97,7 @@ struct Ctl {
     // Barriers: pairs by chunk parity where a waiter can be a chunk behind (`full` and s_ready
     // by stage).
     uint64_t full[4], gates[4], y_read[2], s_ready[4], wx_ready[2], ds[2], full_x[2], full_z[2];
-    uint64_t y_done[2], cb, cs, mx, m_ready, s_first, drain;
+    uint64_t y_done[2], s_read, cb, cs, mx, m_ready, s_first, drain;
     uint32_t tmem;
     int32_t abort;   // a wait ran out
     Gates g[2][2];   // [stage][unit] (the state-only pass, with room behind, has four stages)
@@ -207,7 +206,7 @@ __device__ __forceinline__ Item item_at(const TcParams &p, int64_t place) {
 
 // The items of packed sequences in order, the long ones first: more of them than SMs are then
 // done soonest.  Six sequences of 4,096 to 20,480 tokens on 32 unit pairs took 1,180 us in their
-// own order and cut at a fair share, and take 892 us like this.  Sequences are cut along time
+// own order and cut at a fair share, 892 us like this.  Sequences are cut along time
 // only where one is long enough to be worth the state-only pass.  By one block, in bins of a
 // quarter of an octave of their chunks: atomics place the items of a bin, in any order (which no
 // result depends on); places without an item hold sequence -1.  Bound by latency and the launch.
@@ -274,13 +273,16 @@ __global__ void __launch_bounds__(kOrderThreads) ssm_order(const __grid_constant
 
 // The roles of a CTA's warps, each with its own pace; mbarriers carry the order.
 //   0-7    y: M from the scores, and the readout (row 32 (warp % 4) + lane, 32 columns of it)
-//   8-15   S: the state (its row n, the 64 columns of one unit, in registers), and w x
+//   8-15   S: the state (its row n, the 64 columns of one unit, in registers)
 //   16     issues the MMAs     17  issues the TMA copies     18, 19  the gates of unit 0, 1
-constexpr int kSWarp = 8, kIssueWarp = 16, kLoadWarp = 17, kGateWarp = 18;
+//   20-23  w x (the state-only pass leaves it to warps 0-7).  With the S warps making it, behind the
+//          state's update, they held the others up: 3.09 us a chunk, now 2.87.
+constexpr int kSWarp = 8, kIssueWarp = 16, kLoadWarp = 17, kGateWarp = 18, kWxWarp = 20;
+template <bool kState> constexpr int kThreads = 32 * (kState ? kWxWarp : kWxWarp + 4);
 
 // kState: the state-only pass of a segment (no scores, no y; warps 0-7 make w x there).
 template <bool kState>
-__global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_constant__ TcParams p) {
+__global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __grid_constant__ TcParams p) {
     // (Nothing static stands before it, so dynamic shared memory begins on a 1024-byte boundary, as
     // the swizzled tiles need; there is no room to align it here.)
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -316,12 +318,13 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl.y_read[i], 8);
-            mbar_init(&ctl.wx_ready[i], 8);
+            mbar_init(&ctl.wx_ready[i], kState ? 8 : 4);
             mbar_init(&ctl.ds[i], 1);
             mbar_init(&ctl.full_x[i], 1);
             mbar_init(&ctl.full_z[i], 1);
             mbar_init(&ctl.y_done[i], 8);
         }
+        mbar_init(&ctl.s_read, 8);
         mbar_init(&ctl.cb, 1);
         mbar_init(&ctl.cs, 1);
         mbar_init(&ctl.mx, 1);
@@ -356,19 +359,20 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
     auto clear_rows = [&](int c, int who) {
         uint8_t *st = stage(c);
         const int len = chunk_len(c);
-        for (int e = who; e < (kL - len) * 32; e += 256) {
+        for (int e = who; e < (kL - len) * 32; e += kState ? 256 : 128) {
             const int r = len + (e >> 5), k = e & 31;       // B regions 0, 1, units 0, 1
             *reinterpret_cast<uint4 *>(st + (k >> 3) * 8192 + sw128_offset(r, k & 7)) = make_uint4(0, 0, 0, 0);
         }
     };
-    // w x of chunk c by 256 threads, split into two bf16 terms, at buffer `xh`.
+    // w x of chunk c by 128 threads (256 in the state-only pass), split into two bf16 terms, at buffer `xh`.
     auto make_wx = [&](int c, int who, uint8_t *xh) {
         const uint8_t *xt = stage(c) + ST_X;
         const int len = chunk_len(c);
         if (len < kL) clear_rows(c, who);
-#pragma unroll 1
-        for (int v = 0; v < 4; ++v) {
-            const int u = v >> 1, j = (who >> 3) + 32 * (v & 1);
+        constexpr int kStep = kState ? 32 : 16;      // tokens that the threads take at once
+#pragma unroll (kState ? 1 : 2)
+        for (int v = 0; v < 128 / kStep; ++v) {
+            const int u = v / (64 / kStep), j = (who >> 3) + kStep * (v % (64 / kStep));
             const uint32_t at = u * 8192 + sw128_offset(j, who & 7);
             const float w = j < len ? ex2(gate[c & (NS - 1)][u].lw[j]) : 0.f;
             const uint4 xv = j < len ? *reinterpret_cast<const uint4 *>(xt + at) : make_uint4(0, 0, 0, 0);
@@ -417,9 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             if (!kState && nchunks > 0 && (ok = wait_st(ctl.full, 0))) issue_cb(0);
             for (int c = 0; ok && c < nchunks; ++c) {
                 const uint64_t st = (uint64_t)(c & (NS - 1)) * (kStageBytes<kState> >> 4);
-                // (w x ready: the S warps have also read the accumulators of the chunk before.)
                 if (!(ok = wait2(ctl.wx_ready, c) && wait_st(ctl.full, c) &&
-                           (kState ? c < 2 || wait_st(ctl.s_ready, c - 2) : wait2(ctl.full_x, c))))
+                           (kState ? c < 2 || wait_st(ctl.s_ready, c - 2) : wait2(ctl.full_x, c) && (c == 0 || wait(&ctl.s_read, c - 1)))))
                     break;
                 tc_fence_after();
                 const uint64_t xh = kState && (c & 1) ? dXH1 : dXH;
@@ -513,6 +516,16 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             if (!ok) *abort = 1;
         }
         __syncwarp();
+    } else if (warp >= kWxWarp) {
+        // ------------------------------------------------------------ w x (the state's MMA of the chunk before has left its buffer)
+        for (int c = 0; !kState && c < nchunks; ++c) {
+            if (!(ok = all((c == 0 || wait(&ctl.ds[0], c - 1)) && wait2(ctl.full_x, c) && (chunk_len(c) == kL || wait_st(ctl.full, c)) &&
+                           wait_st(ctl.gates, c))))
+                break;
+            make_wx(c, tid - 32 * kWxWarp, sm + O_XH);
+            arrive(&ctl.wx_ready[c & 1], true);
+        }
+        if (!ok) *abort = 1;
     } else if (warp >= kGateWarp) {
         // ------------------------------------------------------------ gates: two tokens to a lane
         // A decay of e^-111 is already nothing in fp32, so g is held above that: a reset then leaves
@@ -587,12 +600,6 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             arrive(&ctl.s_first, true);
         }
         float seg_total = 0.f;
-        auto next_wx = [&](int c) {      // (the state's MMA of the chunk before has left its buffer)
-            if (!(ok = all(wait2(ctl.full_x, c) && (chunk_len(c) == kL || wait_st(ctl.full, c)) && wait_st(ctl.gates, c)))) return;
-            make_wx(c, tid - 32 * kSWarp, sm + O_XH);
-            arrive(&ctl.wx_ready[c & 1], true);
-        };
-        if (!kState && nchunks > 0) next_wx(0);
         for (int c = 0; ok && c < nchunks; ++c) {
             if (!(ok = all((kState ? wait2(ctl.ds, c) : wait(&ctl.ds[0], c)) && wait_st(ctl.gates, c)))) break;
             tc_fence_after();
@@ -600,21 +607,21 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_scan(const __grid_const
             seg_total += gate[c & (NS - 1)][su].total;
             const uint32_t src = tmem + lanes + (kState && (c & 1) ? T_CS : T_DS) + 64 * su;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                uint32_t r[16];
-                tmem_ld16(src + 16 * b, r);
+            for (int b = 0; b < 8; ++b) {
+                uint32_t r[8];
+                tmem_ld8(src + 8 * b, r);
                 tmem_ld_wait();
                 landed(r);
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const F2 v = fma2(both(dec), {S[16 * b + i], S[16 * b + i + 1]}, words(r[i], r[i + 1]));
-                    S[16 * b + i] = v.x;
-                    S[16 * b + i + 1] = v.y;
+                for (int i = 0; i < 8; i += 2) {
+                    const F2 v = fma2(both(dec), {S[8 * b + i], S[8 * b + i + 1]}, words(r[i], r[i + 1]));
+                    S[8 * b + i] = v.x;
+                    S[8 * b + i + 1] = v.y;
                 }
             }
             if (!kState) {
-                if (c + 1 < nchunks) next_wx(c + 1);
-                if (!ok || !(ok = all(wait(&ctl.cs, c)))) break;      // the readout has read the old S
+                arrive(&ctl.s_read, false);
+                if (!(ok = all(wait(&ctl.cs, c)))) break;      // the readout has read the old S
                 put_S();
             }
             arrive(&ctl.s_ready[c & (NS - 1)], !kState);
@@ -899,12 +906,12 @@ cudaError_t launch_ssm_tc(const SsmParams &s, void *workspace, cudaStream_t stre
         if (e != cudaSuccess) return e;
     }
     if (b.seg > 0) {
-        ssm_chunk_scan<true><<<(unsigned)grid, kThreads, kSmem, stream>>>(p);
+        ssm_chunk_scan<true><<<(unsigned)grid, kThreads<true>, kSmem, stream>>>(p);
         ssm_segment_states<<<dim3((unsigned)s.num_seqs, (unsigned)(s.groups * p.units), (unsigned)((s.d_state + 15) / 16)), 256, 0, stream>>>(p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    ssm_chunk_scan<false><<<(unsigned)grid, kThreads, kSmem, stream>>>(p);
+    ssm_chunk_scan<false><<<(unsigned)grid, kThreads<false>, kSmem, stream>>>(p);
     return cudaGetLastError();
 }
 
