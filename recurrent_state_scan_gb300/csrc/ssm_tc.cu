@@ -18,8 +18,8 @@
 // The warps' roles run side by side, a chunk apart where the data allows it.
 //
 // Bound by the chain from one chunk's y to the next (readout, M, its MMA) and by issue: a pair of
-// units takes 2.9 us a chunk (3.2 with z), of which the tensor pipe works a quarter, the issue slots
-// about half and shared memory about half.  8,192 tokens of 64 heads of 64 x 128 with z: 103 us on
+// units takes 2.76 us a chunk (2.92 with z), of which the tensor pipe works a quarter, the issue slots
+// about half and shared memory about half.  8,192 tokens of 64 heads of 64 x 128 with z: 97 us on
 // 128 CTAs, behind 46 us of state-only pass (its gates bound it) and 5 us for the segments' states.
 // Precision: the state is fp32 and its update's operands are exact (B) or a two-term bf16 split
 // (w x: 2^-17 of each product), because the state is returned in fp32 and carried on; M and
@@ -30,7 +30,7 @@
 // Where sequences x units leave most SMs idle, each sequence is cut along time: a state-only
 // pass of every segment but the last from zero, a short pass that turns the segments' ends into
 // the states entering them, and then all segments at once.  (Uncut, the 8,192 tokens above would
-// stand on 32 SMs for 128 chunks, 410 us.)  Packed sequences are taken by length.
+// stand on 32 SMs for 128 chunks, 370 us.)  Packed sequences are taken by length.
 #include <cudaTypedefs.h>
 #include <stddef.h>
 #include <string.h>
@@ -276,12 +276,14 @@ __global__ void __launch_bounds__(kOrderThreads) ssm_order(const __grid_constant
 //   8-15   S: the state (its row n, the 64 columns of one unit, in registers)
 //   16     issues the MMAs     17  issues the TMA copies     18, 19  the gates of unit 0, 1
 //   20-23  w x (the state-only pass leaves it to warps 0-7).  With the S warps making it, behind the
-//          state's update, they held the others up: 3.09 us a chunk, now 2.87.
+//          state's update, they held the others up: 3.09 us a chunk, then 2.87.
 constexpr int kSWarp = 8, kIssueWarp = 16, kLoadWarp = 17, kGateWarp = 18, kWxWarp = 20;
+constexpr int kZNone = 0, kZTma = 1, kZRows = 2;   // no z, z by TMA, z off 16 bytes
 template <bool kState> constexpr int kThreads = 32 * (kState ? kWxWarp : kWxWarp + 4);
 
-// kState: the state-only pass of a segment (no scores, no y; warps 0-7 make w x there).
-template <bool kState>
+// kState: the state-only pass of a segment (no scores, no y; warps 0-7 make w x there).  kZ: where z
+// comes from, known to the compiler because the loops that do not ask are 4% faster.
+template <bool kState, int kZ>
 __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __grid_constant__ TcParams p) {
     // (Nothing static stands before it, so dynamic shared memory begins on a 1024-byte boundary, as
     // the swizzled tiles need; there is no room to align it here.)
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
             auto load_z = [&](int c) {      // (without a z that TMA can take: its place is free)
                 uint64_t *bar = &ctl.full_z[c & 1];
                 loaded_z = c + 1;
-                if (!p.z_tma) {
+                if (kZ != kZTma) {
                     mbar_arrive(bar);
                     return;
                 }
@@ -472,9 +474,31 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
                 for (int u = 0; u < 2; ++u) tma_load_3d(sm + O_Z + (c & 1) * 16384 + u * 8192, &p.tm_z, tile_u[u], head_u[u], row_of(c), bar);
             };
             for (int c = 0; ok && c < nchunks + (kState ? 0 : 2); ++c) {
-                // y of chunk c - 2 has taken z's place: out with it, ahead of the next loads.  (A
-                // sequence's last rows, where they do not fill the chunk, are stored by their threads.)
-                if (!kState && c >= 2) {
+                // The stage is free when the last MMA of the chunk in it is done: its S has been taken,
+                // or its y read out (x with it).  x first: w x waits for it.
+                if (c < nchunks) {
+                    if (c >= NS && !(ok = kState ? wait_st(ctl.s_ready, c - NS) : wait2(ctl.y_read, c - NS))) break;
+                    uint8_t *st = stage(c);
+                    uint64_t *bar = &ctl.full[c & (NS - 1)], *bar_x = kState ? bar : &ctl.full_x[c & 1];
+                    const int t = row_of(c);
+                    if (!kState) mbar_arrive_expect_tx(bar_x, 16384);
+                    else mbar_arrive_expect_tx(bar, 8192u * (regions + 2));
+                    for (int u = 0; u < 2; ++u) tma_load_3d(st + ST_X + u * 8192, &p.tm_x, tile_u[u], head_u[u], t, bar_x);
+                    if (!kState) mbar_arrive_expect_tx(bar, 8192u * 3 * regions);
+#pragma unroll 1
+                    for (int r = 0; r < regions; ++r) {
+                        tma_load_3d(st + ST_B + r * 8192, &p.tm_b, 64 * r, g, t, bar);
+                        if (!kState) {
+                            tma_load_3d(st + ST_C + r * 16384, &p.tm_c, 64 * r, g, t, bar);
+                            tma_load_3d(st + ST_C + r * 16384 + 8192, &p.tm_c, 64 * r, g, t, bar);
+                        }
+                    }
+                    loaded = c + 1;
+                }
+                if (kState) continue;
+                // y of chunk c - 2 has taken z's place: out with it, and the next z in.  (A sequence's last
+                // rows, where they do not fill the chunk, are stored by their threads.)
+                if (c >= 2) {
                     if (!(ok = wait2(ctl.y_done, c - 2))) break;
                     if (chunk_len(c - 2) == kL) {
                         for (int u = 0; u < 1 + two; ++u)
@@ -482,26 +506,7 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
                         bulk_commit();
                     }
                 }
-                if (c >= nchunks) continue;
-                // The stage is free when the last MMA of the chunk in it is done: its S has been taken,
-                // or its y read out (x with it).
-                if (c >= NS && !(ok = kState ? wait_st(ctl.s_ready, c - NS) : wait2(ctl.y_read, c - NS))) break;
-                uint8_t *st = stage(c);
-                uint64_t *bar = &ctl.full[c & (NS - 1)], *bar_x = kState ? bar : &ctl.full_x[c & 1];
-                const int t = row_of(c);
-                if (!kState) mbar_arrive_expect_tx(bar_x, 16384);
-                mbar_arrive_expect_tx(bar, 8192u * (kState ? regions + 2 : 3 * regions));
-                for (int u = 0; u < 2; ++u) tma_load_3d(st + ST_X + u * 8192, &p.tm_x, tile_u[u], head_u[u], t, bar_x);
-#pragma unroll 1
-                for (int r = 0; r < regions; ++r) {
-                    tma_load_3d(st + ST_B + r * 8192, &p.tm_b, 64 * r, g, t, bar);
-                    if (!kState) {
-                        tma_load_3d(st + ST_C + r * 16384, &p.tm_c, 64 * r, g, t, bar);
-                        tma_load_3d(st + ST_C + r * 16384 + 8192, &p.tm_c, 64 * r, g, t, bar);
-                    }
-                }
-                loaded = c + 1;
-                if (!kState) {
+                if (c < nchunks) {
                     bulk_wait_read();
                     load_z(c);
                 }
@@ -713,8 +718,8 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
                 uint4 *place = reinterpret_cast<uint4 *>(zt + piece);
                 const int pc = 8 * b;
                 uint4 zv = make_uint4(0, 0, 0, 0);
-                if (p.z != nullptr) {
-                    if (p.z_tma) zv = *place;
+                if (kZ != kZNone) {
+                    if (kZ == kZTma) zv = *place;
                     else if (live && ri < len && col + pc < p.P)
                         zv = load_unaligned(p.z + (it.t0 + (int64_t)c * kL + ri) * p.ld_z + (int64_t)head * p.P + col + pc);
                 }
@@ -726,7 +731,7 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     F2 a = fma2(both(D), widen(xw[i]), fma2(both(e), words(cs[2 * i], cs[2 * i + 1]), words(m[2 * i], m[2 * i + 1])));
-                    if (p.z != nullptr) a = gated(a, widen(zw[i]));
+                    if (kZ != kZNone) a = gated(a, widen(zw[i]));
                     out[i] = pack2(a);
                 }
                 const uint4 o = make_uint4(out[0], out[1], out[2], out[3]);
@@ -897,8 +902,9 @@ cudaError_t launch_ssm_tc(const SsmParams &s, void *workspace, cudaStream_t stre
 
     const int64_t grid = b.slots * pairs;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(ssm_chunk_scan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_chunk_scan<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    void (*const main)(TcParams) = s.z == nullptr ? ssm_chunk_scan<false, kZNone> : p.z_tma ? ssm_chunk_scan<false, kZTma> : ssm_chunk_scan<false, kZRows>;
+    cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_chunk_scan<true, kZNone>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (b.ordered) {
         ssm_order<<<1, kOrderThreads, 0, stream>>>(p, b.slots);
@@ -906,12 +912,12 @@ cudaError_t launch_ssm_tc(const SsmParams &s, void *workspace, cudaStream_t stre
         if (e != cudaSuccess) return e;
     }
     if (b.seg > 0) {
-        ssm_chunk_scan<true><<<(unsigned)grid, kThreads<true>, kSmem, stream>>>(p);
+        ssm_chunk_scan<true, kZNone><<<(unsigned)grid, kThreads<true>, kSmem, stream>>>(p);
         ssm_segment_states<<<dim3((unsigned)s.num_seqs, (unsigned)(s.groups * p.units), (unsigned)((s.d_state + 15) / 16)), 256, 0, stream>>>(p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    ssm_chunk_scan<false><<<(unsigned)grid, kThreads<false>, kSmem, stream>>>(p);
+    main<<<(unsigned)grid, kThreads<false>, kSmem, stream>>>(p);
     return cudaGetLastError();
 }
 
