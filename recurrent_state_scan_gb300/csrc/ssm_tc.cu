@@ -19,8 +19,8 @@
 //
 // Bound by the chain from one chunk's y to the next (readout, M, its MMA) and by issue: a pair of
 // units takes 2.76 us a chunk (2.92 with z), of which the tensor pipe works a quarter, the issue slots
-// about half and shared memory about half.  8,192 tokens of 64 heads of 64 x 128 with z: 97 us on
-// 128 CTAs, behind 46 us of state-only pass (its gates bound it) and 5 us for the segments' states.
+// about half and shared memory about half.  8,192 tokens of 64 heads of 64 x 128 with z: 96 us on
+// 128 CTAs, behind 41 us of state-only pass and 5 us for the segments' states.
 // Precision: the state is fp32 and its update's operands are exact (B) or a two-term bf16 split
 // (w x: 2^-17 of each product), because the state is returned in fp32 and carried on; M and
 // the S that C reads are rounded once to bf16, half a step (2^-9 of each term's size at random
@@ -274,12 +274,13 @@ __global__ void __launch_bounds__(kOrderThreads) ssm_order(const __grid_constant
 // The roles of a CTA's warps, each with its own pace; mbarriers carry the order.
 //   0-7    y: M from the scores, and the readout (row 32 (warp % 4) + lane, 32 columns of it)
 //   8-15   S: the state (its row n, the 64 columns of one unit, in registers)
-//   16     issues the MMAs     17  issues the TMA copies     18, 19  the gates of unit 0, 1
+//   16     issues the MMAs     17  issues the TMA copies     18, 19  the gates of unit 0, 1; the
+//          state-only pass, which they bound (46 us), has 20, 21 for its odd chunks (41 us)
 //   20-23  w x (the state-only pass leaves it to warps 0-7).  With the S warps making it, behind the
 //          state's update, they held the others up: 3.09 us a chunk, then 2.87.
 constexpr int kSWarp = 8, kIssueWarp = 16, kLoadWarp = 17, kGateWarp = 18, kWxWarp = 20;
 constexpr int kZNone = 0, kZTma = 1, kZRows = 2;   // no z, z by TMA, z off 16 bytes
-template <bool kState> constexpr int kThreads = 32 * (kState ? kWxWarp : kWxWarp + 4);
+template <bool kState> constexpr int kThreads = 32 * (kState ? kGateWarp + 4 : kWxWarp + 4);
 
 // kState: the state-only pass of a segment (no scores, no y; warps 0-7 make w x there).  kZ: where z
 // comes from, known to the compiler because the loops that do not ask are 4% faster.
@@ -521,9 +522,9 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
             if (!ok) *abort = 1;
         }
         __syncwarp();
-    } else if (warp >= kWxWarp) {
+    } else if (!kState && warp >= kWxWarp) {
         // ------------------------------------------------------------ w x (the state's MMA of the chunk before has left its buffer)
-        for (int c = 0; !kState && c < nchunks; ++c) {
+        for (int c = 0; c < nchunks; ++c) {
             if (!(ok = all((c == 0 || wait(&ctl.ds[0], c - 1)) && wait2(ctl.full_x, c) && (chunk_len(c) == kL || wait_st(ctl.full, c)) &&
                            wait_st(ctl.gates, c))))
                 break;
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
         // ------------------------------------------------------------ gates: two tokens to a lane
         // A decay of e^-111 is already nothing in fp32, so g is held above that: a reset then leaves
         // the sums over it small enough to keep the differences of the tokens before it.
-        const int u = warp - kGateWarp, head = unit_head(u);
+        const int u = (warp - kGateWarp) & 1, head = unit_head(u), first = (warp - kGateWarp) >> 1, step = kState ? 2 : 1;
         const float A = -expf(p.A_log[head]) * kLog2e, bias = p.dt_bias ? p.dt_bias[head] : 0.f;
         unsigned short n0 = 0, n1 = 0;      // bits, widened a chunk later: nothing waits for the load here
         auto load_dt = [&](int c) {
@@ -544,12 +545,12 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
             if (t < it.t1) n0 = at[0];
             if (t + 1 < it.t1) n1 = at[p.ld_dt];
         };
-        if (nchunks > 0) load_dt(0);
-        for (int c = 0; c < nchunks; ++c) {
+        if (first < nchunks) load_dt(first);
+        for (int c = first; c < nchunks; c += step) {
             const int len = chunk_len(c);
             const float d0 = 2 * lane < len ? step_of(n0, bias, p.dt_min, p.dt_max) : 0.f;
             const float d1 = 2 * lane + 1 < len ? step_of(n1, bias, p.dt_min, p.dt_max) : 0.f;
-            if (c + 1 < nchunks) load_dt(c + 1);      // (behind the calls, which would wait for it)
+            if (c + step < nchunks) load_dt(c + step);      // (behind the calls, which would wait for it)
             float g0 = A * d0, g1 = A * d1;
             g0 = g0 < -160.f ? -160.f : g0;
             g1 = g1 < -160.f ? -160.f : g1;
