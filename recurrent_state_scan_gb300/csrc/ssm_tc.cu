@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
         const int len = chunk_len(c);
         if (len < kL) clear_rows(c, who);
         constexpr int kStep = kState ? 32 : 16;      // tokens that the threads take at once
-#pragma unroll (kState ? 1 : 2)
+#pragma unroll 2
         for (int v = 0; v < 128 / kStep; ++v) {
             const int u = v / (64 / kStep), j = (who >> 3) + kStep * (v % (64 / kStep));
             const uint32_t at = u * 8192 + sw128_offset(j, who & 7);
