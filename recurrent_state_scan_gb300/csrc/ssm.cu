@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(const SsmParams 
         if (tid < kTile) {
             const float d = tb + tid < t1 ? ssm_step(IoType<IO>::ld(&rd), bias, p.dt_min, p.dt_max) : 0.f;
             sg[buf][tid][0] = d;
-            sg[buf][tid][1] = expf(A * d);
+            sg[buf][tid][1] = ssm_decay(A * d);
         }
     };
     load(t0);
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kDecThreads, 4) ssm_decode_kernel(const SsmDec
     const IO *conv = p.conv ? static_cast<const IO *>(p.conv) + e * (int64_t)(p.K - 1) * p.C : nullptr;
     const float d = ssm_step(IoType<IO>::ld(static_cast<const IO *>(p.dt) + b * p.ld_dt + h), p.dt_bias ? p.dt_bias[h] : 0.f,
                              p.dt_min, p.dt_max);
-    const float a = expf(-expf(p.A_log[h]) * d), D = p.D ? p.D[h] : 0.f;
+    const float a = ssm_decay(-expf(p.A_log[h]) * d), D = p.D ? p.D[h] : 0.f;
     for (int i = tid; i < P + 2 * N; i += kDecThreads) {
         if (i < P) sx[i] = conv_token(p, x, conv, h * P + i);
         else if (i < P + N) sB[i - P] = conv_token(p, x, conv, hp + g * N + i - P);
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) ssm_decode_stream_kernel(const
             (i < P ? sx[i] : i < P + N ? sB[i - P] : sC[i - P - N]) = v;
         }
         d = ssm_step(IoType<IO>::ld(&raw_dt), db, p.dt_min, p.dt_max);
-        a = expf(-expf(A) * d);
+        a = ssm_decay(-expf(A) * d);
         skip = D;
     };
 

@@ -125,5 +125,8 @@ __device__ __forceinline__ float ssm_step(float dt, float bias, float lo, float 
     const float d = softplus_f(dt + bias);
     return d < lo ? lo : d > hi ? hi : d;
 }
+// e^g.  A slow decay is multiplied in thousands of times, so its rounding has to be fair: expf alone
+// drifts (2,000 tokens of e^-0.0003: 1.4e-5 off, 1.0e-6 so).
+__device__ __forceinline__ float ssm_decay(float g) { return 1.f + expm1f(g); }
 
 }  // namespace gdn

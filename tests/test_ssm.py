@@ -194,6 +194,16 @@ def test_extreme_steps(io):
 
 
 @pytest.mark.gpu
+def test_slow_decays_do_not_drift():
+    """2,000 tokens that forget next to nothing.  Each rounds its decay (half a step below 1: 2^-25), the state's update
+    (2^-24) and its own share (twice 2^-24, of a small part): at random, so they add up to sqrt(2000) times 2 * 2^-24 at most."""
+    m = draw("f32", [2000], 4, 32, 1, 16, 0, z=False, seed=24)
+    m["A_log"] = torch.full((4,), -6.0, device="cuda")
+    _, state, _ = prefill(m)
+    assert rel(state, define(m)[1]) <= 2000 ** 0.5 * 2 * 2.0 ** -24
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_a_sequence_does_not_see_its_neighbours(io):
     """Rows of another sequence, infinities and NaN among them, leave a packed sequence's results bit for bit."""
