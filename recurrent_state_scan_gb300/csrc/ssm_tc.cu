@@ -18,7 +18,7 @@
 // The warps' roles run side by side, a chunk apart where the data allows it.
 //
 // Bound by the chain from one chunk's y to the next (readout, M, its MMA) and by issue: a pair of
-// units takes 2.76 us a chunk (2.92 with z), of which the tensor pipe works a quarter, the issue slots
+// units takes 2.79 us a chunk (2.98 with z), of which the tensor pipe works a quarter, the issue slots
 // about half and shared memory about half.  8,192 tokens of 64 heads of 64 x 128 with z: 96 us on
 // 128 CTAs, behind 41 us of state-only pass and 5 us for the segments' states.
 // Precision: the state is fp32 and its update's operands are exact (B) or a two-term bf16 split
@@ -116,11 +116,18 @@ __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0
 __device__ __forceinline__ F2 words(uint32_t a, uint32_t b) { return {__uint_as_float(a), __uint_as_float(b)}; }
 __device__ __forceinline__ F2 widen(uint32_t v) { return {lo_f(v), hi_f(v)}; }
 __device__ __forceinline__ uint32_t pack2(F2 a) { return pack2(a.x, a.y); }
-// a silu(z) for two values with one reciprocal: 1 / d0 = d1 / (d0 d1).  e^-z stops at 2^60, so that
-// the product stays finite (silu is then 2^-60 z, where it is smaller still).
+// max(z, -41), NaN where z is.
+__device__ __forceinline__ float at_least_m41(float z) {
+    asm("max.NaN.f32 %0, %0, 0fC2240000;" : "+f"(z));
+    return z;
+}
+// a silu(z) for two values with one reciprocal: 1 / d0 = d1 / (d0 d1).  z stops at -41, so that the
+// product stays finite (silu is then -6e-17, where it is nearer to zero still); a NaN stays out of
+// the reciprocal, which is its neighbour's too.
 __device__ __forceinline__ F2 gated(F2 a, F2 z) {
-    const F2 t = mul2(z, both(-kLog2e));
-    const F2 d = add2({ex2(fminf(t.x, 60.f)), ex2(fminf(t.y, 60.f))}, both(1.f));
+    const F2 t = mul2({fmaxf(z.x, -41.f), fmaxf(z.y, -41.f)}, both(-kLog2e));
+    z = {at_least_m41(z.x), at_least_m41(z.y)};
+    const F2 d = add2({ex2(t.x), ex2(t.y)}, both(1.f));
     return mul2(mul2(mul2(a, z), both(rcp(d.x * d.y))), {d.y, d.x});
 }
 
@@ -400,7 +407,6 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
     const uint32_t tmem = ctl.tmem;
     bool ok = true;
 
-
     if (warp == kIssueWarp) {
         // ------------------------------------------------------------ MMAs
         if (lane == 0) {
@@ -576,7 +582,6 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
         }
         if (!ok) *abort = 1;
     } else if (warp >= kSWarp) {
-
         // ------------------------------------------------------------ S: state row sn, the 64 columns of unit su
         const int sn = 32 * q + lane, su = (warp >> 2) & 1;
         const int ucols = p.P - unit_tile(su) * 64;       // columns of this unit that exist
@@ -648,7 +653,6 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
         }
     } else if (kState) {
         // ------------------------------------------------------------ w x of the state-only pass, two buffers
-
         for (int c = 0; c < nchunks; ++c) {
             if (!(ok = all(wait_st(ctl.full, c) && wait_st(ctl.gates, c) && (c < 2 || wait2(ctl.ds, c - 2))))) break;
             make_wx(c, tid, sm + (c & 1 ? O_S : O_XH));

@@ -194,6 +194,21 @@ def test_extreme_steps(io):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("gap", [0, 1])
+def test_gates_far_out(io, gap):
+    """A gate far below zero shuts, one far above passes, a NaN stays."""
+    m = draw(io, [70], 2, 64, 1, 64, 0, seed=25, gap=gap)
+    z = m["z"].clone() if gap == 0 else torch.empty(1, 70, 129, dtype=DT[io], device="cuda")[..., 1:].unflatten(2, (2, 64)).copy_(m["z"])
+    z[:, 10], z[:, 66], z[:, 20], z[:, 30, 0, 3] = -3e38, -100.0, 1000.0, math.nan
+    m["z"] = z
+    y, want = prefill(m)[0], define(m)[0]
+    plain = prefill(dict(m, z=None))[0]
+    assert (y[:, 10].abs() <= 2.0 ** -50 * plain[:, 10].abs()).all() and (y[:, 66].abs() <= 2.0 ** -50 * plain[:, 66].abs()).all()
+    assert rel(y[:, 20], want[:, 20]) <= y_tol(DT[io]) and y[0, 30, 0, 3].isnan() and int(y.isnan().sum()) == 1
+
+
+@pytest.mark.gpu
 def test_slow_decays_do_not_drift():
     """2,000 tokens that forget next to nothing.  Each rounds its decay (half a step below 1: 2^-25), the state's update
     (2^-24) and its own share (twice 2^-24, of a small part): at random, so they add up to sqrt(2000) times 2 * 2^-24 at most."""
