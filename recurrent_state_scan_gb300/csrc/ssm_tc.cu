@@ -214,39 +214,46 @@ __device__ __forceinline__ Item item_at(const TcParams &p, int64_t place) {
 // The items of packed sequences in order, the long ones first: more of them than SMs are then
 // done soonest.  Six sequences of 4,096 to 20,480 tokens on 32 unit pairs took 1,180 us in their
 // own order and cut at a fair share, 892 us like this.  Sequences are cut along time
-// only where one is long enough to be worth the state-only pass.  By one block, in bins of a
-// quarter of an octave of their chunks: atomics place the items of a bin, in any order (which no
-// result depends on); places without an item hold sequence -1.  Bound by latency and the launch.
+// only where one is long enough to be worth the state-only pass.  By one block: the
+// segments but each sequence's last in the first bin, which are all that the state-only pass needs,
+// the others in bins of a quarter of an octave of their chunks.  Atomics place the items of a bin,
+// in any order (which no result depends on); places without an item hold sequence -1.  Bound by latency and the launch.
 constexpr int kOrderThreads = 512, kBins = 128;
-__device__ __forceinline__ int bin_of(int chunks) {            // 0 for the longest
-    return chunks <= 0 ? kBins - 1 : kBins - 2 - min(kBins - 2, (int)(__float_as_uint((float)chunks) >> 21) - (127 << 2));
+__device__ __forceinline__ int bin_of(int chunks) {            // 1 for the longest
+    return chunks <= 0 ? kBins - 1 : kBins - 2 - min(kBins - 3, (int)(__float_as_uint((float)chunks) >> 21) - (127 << 2));
 }
 __global__ void __launch_bounds__(kOrderThreads) ssm_order(const __grid_constant__ TcParams p, int64_t places) {
-    __shared__ int at[kBins], longest, items;
+    __shared__ int at[kBins], longest, bad, items;
     const int tid = threadIdx.x;
     if (tid < kBins) at[tid] = 0;
-    if (tid == 0) longest = 0;
+    if (tid == 0) longest = bad = 0;
     __syncthreads();
     auto chunks_of = [&](int64_t n) {                          // -1: bad offsets
         int64_t t0, t1;
         return seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, n, t0, t1) ? (int)((t1 - t0 + kL - 1) / kL) : -1;
     };
     int most = 0;
-    for (int64_t n = tid; n < p.num_seqs; n += kOrderThreads) most = max(most, chunks_of(n));
+    for (int64_t n = tid; n < p.num_seqs; n += kOrderThreads) {
+        const int chunks = chunks_of(n);
+        most = max(most, chunks);
+        if (chunks < 0) bad = 1;
+    }
     if (most > 0) atomicMax(&longest, most);
     __syncthreads();
-    const int seg = longest > p.cut_over ? p.seg_chunks : 0;
-    // Of sequence n: `whole` segments of seg chunks, and one rest (an empty sequence's only item) or none (-1).
-    auto parts = [&](int64_t n, int &whole, int &rest) {
+    // (Beside bad offsets sequences that are fine by themselves may overlap, and have more segments than
+    // the rows: they are not cut.)
+    const int seg = longest > p.cut_over && bad == 0 ? p.seg_chunks : 0;
+    // Of sequence n: `lead` segments of seg chunks ahead of its last, and the last's chunks (-1: no items).
+    auto parts = [&](int64_t n, int &lead, int &last) {
         const int chunks = chunks_of(n);
-        whole = seg == 0 || chunks < 0 ? 0 : chunks / seg;
-        rest = chunks < 0 || (whole > 0 && chunks == whole * seg) ? -1 : chunks - whole * seg;
+        lead = seg == 0 || chunks <= 0 ? 0 : (chunks - 1) / seg;
+        last = chunks - lead * seg;
     };
-    int whole, rest;
+    int lead, last;
     for (int64_t n = tid; n < p.num_seqs; n += kOrderThreads) {
-        parts(n, whole, rest);
-        if (whole > 0) atomicAdd(&at[bin_of(seg)], whole);
-        if (rest >= 0) atomicAdd(&at[bin_of(rest)], 1);
+        parts(n, lead, last);
+        if (lead > 0) atomicAdd(&at[0], lead);
+        if (last >= 0) atomicAdd(&at[bin_of(last)], 1);
     }
     __syncthreads();
     if (tid < 32) {                                            // counts to first places
@@ -265,15 +272,14 @@ __global__ void __launch_bounds__(kOrderThreads) ssm_order(const __grid_constant
         }
     }
     __syncthreads();
-    // (Overlapping sequences, each fine by itself beside bad ones, can be more than the places.)
     auto put = [&](int place, int64_t n, int k) {
         if (place < places) p.items[place] = make_int4((int)n, k, seg, 0);
     };
     for (int64_t n = tid; n < p.num_seqs; n += kOrderThreads) {
-        parts(n, whole, rest);
-        const int first = whole > 0 ? atomicAdd(&at[bin_of(seg)], whole) : 0;
-        for (int k = 0; k < whole; ++k) put(first + k, n, k);
-        if (rest >= 0) put(atomicAdd(&at[bin_of(rest)], 1), n, whole);
+        parts(n, lead, last);
+        const int first = lead > 0 ? atomicAdd(&at[0], lead) : 0;
+        for (int k = 0; k < lead; ++k) put(first + k, n, k);
+        if (last >= 0) put(atomicAdd(&at[bin_of(last)], 1), n, lead);
     }
     for (int64_t i = items + (int64_t)tid; i < places; i += kOrderThreads) p.items[i] = make_int4(-1, 0, seg, 0);
 }
@@ -756,10 +762,16 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
     if (warp == kIssueWarp) tmem_dealloc(tmem, kCols);
 }
 
-// The state entering each segment, in the place of the segment's own end state.
+// The state entering each segment, in the place of the segment's own end state: of sequence
+// blockIdx.x, or of an ordered call's item there, where it is its sequence's first of several.
 __global__ void __launch_bounds__(256) ssm_segment_states(const __grid_constant__ TcParams p) {
-    const int64_t n = blockIdx.x, unit = blockIdx.y, nunits = (int64_t)p.groups * p.units;
-    if (p.items != nullptr && p.items[0].z == 0) return;
+    const int64_t unit = blockIdx.y, nunits = (int64_t)p.groups * p.units;
+    int64_t n = blockIdx.x;
+    if (p.items != nullptr) {
+        const int4 v = p.items[n];
+        if (v.x < 0 || v.y != 0 || v.z == 0) return;
+        n = v.x;
+    }
     const int64_t ls = (int64_t)p.seg_chunks * kL, per = (p.seqlen + ls - 1) / ls;
     int64_t t0, t1;
     if (!seq_range(p.cu_seqlens, p.seqlen, p.num_seqs, p.status, n, t0, t1)) return;
@@ -917,8 +929,10 @@ cudaError_t launch_ssm_tc(const SsmParams &s, void *workspace, cudaStream_t stre
         if (e != cudaSuccess) return e;
     }
     if (b.seg > 0) {
-        ssm_chunk_scan<true, kZNone><<<(unsigned)grid, kThreads<true>, kSmem, stream>>>(p);
-        ssm_segment_states<<<dim3((unsigned)s.num_seqs, (unsigned)(s.groups * p.units), (unsigned)((s.d_state + 15) / 16)), 256, 0, stream>>>(p);
+        // Of an ordered call only the first bin's items, each whole segments of its own rows.
+        const int64_t lead = s.rows / ((int64_t)b.seg * kL);
+        ssm_chunk_scan<true, kZNone><<<(unsigned)((b.ordered ? lead : b.slots) * pairs), kThreads<true>, kSmem, stream>>>(p);
+        ssm_segment_states<<<dim3((unsigned)(b.ordered ? lead : s.num_seqs), (unsigned)(s.groups * p.units), (unsigned)((s.d_state + 15) / 16)), 256, 0, stream>>>(p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }

@@ -285,6 +285,19 @@ def test_packed_prompts_by_length(H, lens):
 
 
 @pytest.mark.gpu
+def test_bad_offsets_among_long_sequences():
+    """An offset far too high makes two sequences overlap and one bad: the others are as they were (uncut, where they were cut)."""
+    lens = [1500, 40, 1500, 900]
+    m = draw("bf16", lens, 4, 64, 1, 64, 0, seed=26, gap=(-(2 * 4 * 64 + 128 + 4)) % 8)
+    good = prefill(m)
+    m["cu"][1] = 3900                                    # sequence 0 runs into the others, 1 ends before it begins
+    y, state = (torch.full_like(t, 7.0) for t in good[:2])
+    lib.gdn_ssm_prefill(m["xbc"], m["dt"], m["A_log"], state_in=m["state"], cu_seqlens=m["cu"], y=y, state_out=state, **kwargs(m))
+    assert lib.gdn_last_device_status() == gdn.GDN_ERR_DEVICE_CHECK
+    assert rel(state[2:], good[1][2:]) <= 2 * STATE_TOL and (state[1] == 7).all()
+
+
+@pytest.mark.gpu
 def test_bad_offsets_among_many_sequences():
     """Sequences of bad offsets are left alone, the others computed."""
     lens = [70] * 400
