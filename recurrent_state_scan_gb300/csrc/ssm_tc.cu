@@ -18,9 +18,9 @@
 // The warps' roles run side by side, a chunk apart where the data allows it.
 //
 // Bound by the chain from one chunk's y to the next (readout, M, its MMA) and by issue: a pair of
-// units takes 2.79 us a chunk (2.98 with z), of which the tensor pipe works a quarter, the issue slots
-// about half and shared memory about half.  8,192 tokens of 64 heads of 64 x 128 with z: 96 us on
-// 128 CTAs, behind 41 us of state-only pass and 5 us for the segments' states.
+// units takes 2.6 us a chunk (2.83 with z), of which the tensor pipe works a quarter, the issue slots
+// about half and shared memory about half.  8,192 tokens of 64 heads of 64 x 128 with z: 92 us on
+// 128 CTAs, behind 39 us of state-only pass and 5 us for the segments' states.
 // Precision: the state is fp32 and its update's operands are exact (B) or a two-term bf16 split
 // (w x: 2^-17 of each product), because the state is returned in fp32 and carried on; M and
 // the S that C reads are rounded once to bf16, half a step (2^-9 of each term's size at random
@@ -213,7 +213,7 @@ __device__ __forceinline__ Item item_at(const TcParams &p, int64_t place) {
 
 // The items of packed sequences in order, the long ones first: more of them than SMs are then
 // done soonest.  Six sequences of 4,096 to 20,480 tokens on 32 unit pairs took 1,180 us in their
-// own order and cut at a fair share, 892 us like this.  Sequences are cut along time
+// own order and cut at a fair share, 892 us like this (and 728 by now).  Sequences are cut along time
 // only where one is long enough to be worth the state-only pass.  By one block: the
 // segments but each sequence's last in the first bin, which are all that the state-only pass needs,
 // the others in bins of a quarter of an octave of their chunks.  Atomics place the items of a bin,
@@ -421,16 +421,30 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
                                kIdDS = idesc_f16(true, 128, 128, true, true);
             const int ksteps = (p.N + 15) / 16;
             // Descriptors; their low field counts 16 bytes, so a K step adds 2 (K-major) or 128.
-            // (The loops over ksteps stay loops: unrolled, with each MMA under its own
-            // condition, nvcc 13.0 gave one of them another's operand.)
+            // The products over d_state are unrolled whole for 128, else by four K steps: a rolled loop
+            // does not feed the tensor cores (C S took 1,070 cycles where the state's unrolled eight took 550).
+            // (Unrolled with each MMA under its own condition, nvcc 13.0 gave one of them another's
+            // operand.)
             const uint64_t dC = sw128_desc(base + ST_C, 16, 1024), dBk = sw128_desc(base + ST_B, 16, 1024),
                            dS = sw128_desc(base + O_S, 16384, 1024), dBm = sw128_desc(base + ST_B, 8192, 1024),
                            dXH = sw128_desc(base + O_XH, 8192, 1024), dX = sw128_desc(base + ST_X, 8192, 1024),
                            dXH1 = sw128_desc(base + O_S, 8192, 1024);
             auto issue_cb = [&](int c) {
                 const uint64_t st = (uint64_t)(c & (NS - 1)) * (kStageBytes<kState> >> 4);
-                for (int k = 0; k < ksteps; ++k)
-                    mma_f16(tmem + T_CB, dC + st + (k >> 2) * 1024 + (k & 3) * 2, dBk + st + (k >> 2) * 512 + (k & 3) * 2, kIdCB, k > 0);
+                if (ksteps == 8) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_f16(tmem + T_CB, dC + st + (k >> 2) * 1024 + (k & 3) * 2, dBk + st + (k >> 2) * 512 + (k & 3) * 2, kIdCB, k > 0);
+                } else {
+#pragma unroll 1
+                    for (int q4 = 0; q4 < ksteps / 4; ++q4) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_f16(tmem + T_CB, dC + st + q4 * 1024 + k * 2, dBk + st + q4 * 512 + k * 2, kIdCB, q4 + k > 0);
+                    }
+#pragma unroll 1
+                    for (int k = ksteps & ~3; k < ksteps; ++k)
+                        mma_f16(tmem + T_CB, dC + st + (k >> 2) * 1024 + (k & 3) * 2, dBk + st + (k >> 2) * 512 + (k & 3) * 2, kIdCB, k > 0);
+                }
                 mma_commit(&ctl.cb);
             };
             if (!kState && nchunks > 0 && (ok = wait_st(ctl.full, 0))) issue_cb(0);
@@ -450,8 +464,20 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
                 // C S, once S is in place and the accumulators of the chunk before are read.
                 if (!(ok = c == 0 ? wait(&ctl.s_first, 0) : wait_st(ctl.s_ready, c - 1) && wait2(ctl.y_read, c - 1))) break;
                 tc_fence_after();
-                for (int k = 0; k < ksteps; ++k)
-                    mma_f16(tmem + T_CS, dC + st + (k >> 2) * 1024 + (k & 3) * 2, dS + k * 128, kIdCS, k > 0);
+                if (ksteps == 8) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_f16(tmem + T_CS, dC + st + (k >> 2) * 1024 + (k & 3) * 2, dS + k * 128, kIdCS, k > 0);
+                } else {
+#pragma unroll 1
+                    for (int q4 = 0; q4 < ksteps / 4; ++q4) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_f16(tmem + T_CS, dC + st + q4 * 1024 + k * 2, dS + (4 * q4 + k) * 128, kIdCS, q4 + k > 0);
+                    }
+#pragma unroll 1
+                    for (int k = ksteps & ~3; k < ksteps; ++k)
+                        mma_f16(tmem + T_CS, dC + st + (k >> 2) * 1024 + (k & 3) * 2, dS + k * 128, kIdCS, k > 0);
+                }
                 mma_commit(&ctl.cs);
                 if (!(ok = wait(&ctl.m_ready, c))) break;
                 tc_fence_after();
