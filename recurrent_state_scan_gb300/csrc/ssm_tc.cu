@@ -18,7 +18,7 @@
 // The warps' roles run side by side, a chunk apart where the data allows it.
 //
 // Bound by the chain from one chunk's y to the next (readout, M, its MMA) and by issue: a pair of
-// units takes 2.6 us a chunk (2.83 with z), of which the tensor pipe works a quarter, the issue slots
+// units takes 2.55 us a chunk (2.85 with z), of which the tensor pipe works a quarter, the issue slots
 // about half and shared memory about half.  8,192 tokens of 64 heads of 64 x 128 with z: 92 us on
 // 128 CTAs, behind 39 us of state-only pass and 5 us for the segments' states.
 // Precision: the state is fp32 and its update's operands are exact (B) or a two-term bf16 split
@@ -213,7 +213,7 @@ __device__ __forceinline__ Item item_at(const TcParams &p, int64_t place) {
 
 // The items of packed sequences in order, the long ones first: more of them than SMs are then
 // done soonest.  Six sequences of 4,096 to 20,480 tokens on 32 unit pairs took 1,180 us in their
-// own order and cut at a fair share, 892 us like this (and 728 by now).  Sequences are cut along time
+// own order and cut at a fair share, 892 us like this (and 713 by now).  Sequences are cut along time
 // only where one is long enough to be worth the state-only pass.  By one block: the
 // segments but each sequence's last in the first bin, which are all that the state-only pass needs,
 // the others in bins of a quarter of an octave of their chunks.  Atomics place the items of a bin,
@@ -450,8 +450,9 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
             if (!kState && nchunks > 0 && (ok = wait_st(ctl.full, 0))) issue_cb(0);
             for (int c = 0; ok && c < nchunks; ++c) {
                 const uint64_t st = (uint64_t)(c & (NS - 1)) * (kStageBytes<kState> >> 4);
-                if (!(ok = wait2(ctl.wx_ready, c) && wait_st(ctl.full, c) &&
-                           (kState ? c < 2 || wait_st(ctl.s_ready, c - 2) : wait2(ctl.full_x, c) && (c == 0 || wait(&ctl.s_read, c - 1)))))
+                // The state's.  (B has landed: the scores waited for it.)
+                if (!(ok = wait2(ctl.wx_ready, c) && (kState ? wait_st(ctl.full, c) && (c < 2 || wait_st(ctl.s_ready, c - 2))
+                                                             : wait2(ctl.full_x, c) && (c == 0 || wait(&ctl.s_read, c - 1)))))
                     break;
                 tc_fence_after();
                 const uint64_t xh = kState && (c & 1) ? dXH1 : dXH;
