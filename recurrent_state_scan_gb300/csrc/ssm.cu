@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(const SsmConvParams p, in
 constexpr int kStageRows = 6, kBulkRing = 4, kBulkRun = 96, kBulkChannels = 512;
 
 template <typename IO, int K>
-__global__ void __launch_bounds__(128) ssm_conv_bulk_kernel(const SsmConvParams p, int64_t run_blocks, int run) {
+__global__ void __launch_bounds__(128, 6) ssm_conv_bulk_kernel(const SsmConvParams p, int64_t run_blocks, int run) {
     using namespace tc;
     constexpr int V = 4;
     using Vec = Pack<IO, V>;
