@@ -879,11 +879,12 @@ def _rows(name: str, t, B: int, T: int, row: tuple, dtype, device: int):
         if n > 1 and s != step:
             raise GdnError(GDN_ERR_INVALID_ARG, f"{name}'s token rows must be contiguous")
         step *= n
-    if T > 1:
-        if B > 1 and stride[0] != T * stride[1]:
-            raise GdnError(GDN_ERR_INVALID_ARG, f"{name}'s token rows must be evenly spaced over the batch")
-        return t.data_ptr(), stride[1]
-    return t.data_ptr(), stride[0] if B > 1 else step
+    if T > 1 and B > 1 and stride[0] != T * stride[1]:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name}'s token rows must be evenly spaced over the batch")
+    apart = stride[1] if T > 1 else stride[0] if B > 1 else step
+    if apart < step and B * T > 1:      # (0, as of an expanded tensor, would be taken for contiguous rows)
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name}'s token rows must not overlap (an expanded tensor has to be copied)")
+    return t.data_ptr(), apart
 
 
 @contextlib.contextmanager

@@ -607,3 +607,28 @@ def test_binding_refuses_cpu_tensors():
                                             **dict(kwargs(m), z=None))):
         with pytest.raises(lib.GdnError):
             call()
+
+
+@pytest.mark.parametrize("name,row", [("xbc", (24,)), ("dt", (4,)), ("z", (4, 4)), ("dt", (1,))])
+@pytest.mark.parametrize("B,T", [(1, 512), (32, 1), (3, 7)])
+def test_expanded_rows_are_refused(name, row, B, T):
+    """A stride of 0 over several rows is not the C calls' 0 for contiguous rows: they would read what the tensor does not hold."""
+    t = torch.zeros(1, 1, *row).expand(B, T, *row)
+    with pytest.raises(lib.GdnError, match="overlap"):
+        gdn._rows(name, t, B, T, row, torch.float32, t.get_device())
+    copied = t.contiguous()
+    assert gdn._rows(name, copied, B, T, row, torch.float32, copied.get_device()) == (copied.data_ptr(), math.prod(row))
+
+
+def test_rows_closer_than_their_width_are_refused():
+    for B, T, strides in ((1, 8, (0, 2, 1)), (8, 1, (2, 0, 1)), (2, 4, (8, 2, 1))):
+        t = torch.zeros(64).as_strided((B, T, 4), strides)
+        with pytest.raises(lib.GdnError, match="overlap"):
+            gdn._rows("dt", t, B, T, (4,), torch.float32, t.get_device())
+
+
+def test_rows_of_any_wider_stride_are_taken():
+    wide = torch.zeros(2, 6, 9)
+    for t, want in ((wide[..., 2:6], 9), (wide[:, :1, 2:6], 54), (wide[:1, :1, 2:6], 4), (wide[:1, :, 2:6], 9),
+                    (wide[:, :0, 2:6], 54), (torch.zeros(1, 1, 4).expand(1, 1, 4), 4)):
+        assert gdn._rows("dt", t, *t.shape[:2], (4,), torch.float32, t.get_device()) == (t.data_ptr(), want)
