@@ -184,7 +184,7 @@ extern "C" gdn_status gdn_rotary(const gdn_rotary_shape *s, const void *q, const
     if (s->rot_offset < 0 || s->rot_offset > s->head_dim || s->rot_offset + s->rot_dim > s->head_dim)
         return refuse("the rotated part [%lld, + rot_dim) leaves head_dim %lld", s->rot_offset, s->head_dim);
     if (!(s->scale == s->scale) || isinf(s->scale)) return refuse("scale is not finite");
-    const int64_t rows = s->batch * (int64_t)s->seqlen;
+    const int64_t rows = s->seqlen > INT32_MAX ? s->seqlen : s->batch * s->seqlen;   // (the product of larger ones could pass 64 bits)
     const size_t es = s->io_dtype == GDN_F32 ? 4 : 2;
     const void *in[2] = {q, k};
     void *out[2] = {q_out, k_out};

@@ -53,7 +53,8 @@ gdn_status check(const gdn_ssm_shape *s, const gdn_ssm_params *q, bool varlen, G
     if (!(q->dt_min >= 0.0f) || !(q->dt_max >= q->dt_min) || isinf(q->dt_min))
         return fail(GDN_ERR_INVALID_ARG, "0 <= dt_min <= dt_max is needed, dt_min finite");
     g.es = s->io_dtype == GDN_F32 ? 4 : 2;
-    g.rows = varlen ? s->seqlen : s->seqlen * (int64_t)s->batch;
+    g.rows = s->seqlen;
+    if (!varlen && g.rows <= INT32_MAX) g.rows *= s->batch;      // (the product of larger ones could pass 64 bits)
     if (g.rows > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%lld token rows are not built", (long long)g.rows);
     g.hp = (int64_t)s->heads * s->head_dim;
     g.C = g.hp + 2LL * s->groups * s->d_state;

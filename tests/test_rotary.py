@@ -212,3 +212,9 @@ def test_refusals(bad):
 def test_binding_refuses_cpu_tensors():
     with pytest.raises(lib.GdnError):
         lib.gdn_rotary(torch.randn(1, 2, 3, 16), None, torch.ones(8))
+
+
+@pytest.mark.parametrize("batch,seqlen", [(4, 2 ** 62), (2, 2 ** 63 - 1), (65536, 2 ** 48), (2 ** 31 - 1, 2)])
+def test_token_counts_beyond_64_bits_are_refused(batch, seqlen):
+    """batch x seqlen is 0 or small modulo 2^64 in some of these."""
+    test_refusals(dict(batch=batch, num_seqs=batch, seqlen=seqlen))

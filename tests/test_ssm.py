@@ -632,3 +632,14 @@ def test_rows_of_any_wider_stride_are_taken():
     for t, want in ((wide[..., 2:6], 9), (wide[:, :1, 2:6], 54), (wide[:1, :1, 2:6], 4), (wide[:1, :, 2:6], 9),
                     (wide[:, :0, 2:6], 54), (torch.zeros(1, 1, 4).expand(1, 1, 4), 4)):
         assert gdn._rows("dt", t, *t.shape[:2], (4,), torch.float32, t.get_device()) == (t.data_ptr(), want)
+
+
+@pytest.mark.parametrize("batch,seqlen", [(4, 2 ** 62), (2, 2 ** 63 - 1), (65536, 2 ** 48), (3, 2 ** 31), (2 ** 31 - 1, 2)])
+def test_token_counts_beyond_64_bits_are_refused(batch, seqlen):
+    """batch x seqlen is 0 or small modulo 2^64 in some of these."""
+    shape = _ssm(batch=batch, num_seqs=batch, seqlen=seqlen)
+    assert call_prefill(shape, _params()) == gdn.GDN_ERR_UNSUPPORTED
+    assert call_decode(shape, _params()) == gdn.GDN_ERR_UNSUPPORTED
+    assert lib.load().gdn_ssm_prefill_workspace_bytes(ctypes.byref(shape), ctypes.byref(_params())) == 0
+    with pytest.raises(lib.GdnError):
+        gdn.gdn_ssm_prefill_plan(shape, _params())
