@@ -528,7 +528,7 @@ typedef struct gdn_ssm_params {
  *   state_in     [N, heads, d_state, head_dim] fp32 or NULL (zeros); state_out the same
  *                shape, and may be state_in itself.  16-byte aligned.
  *   cu_seqlens   as gdn_prefill.  A sequence with no tokens keeps its states.
- *   y            [rows, heads, head_dim], contiguous; must not overlap xbc or z.
+ *   y            [rows, heads, head_dim], contiguous; must not overlap xbc, z or dt.
  *   workspace    gdn_ssm_prefill_workspace_bytes(shape, params) bytes, 16-byte aligned; its
  *                contents need no initialisation and are not preserved.
  * Inputs are finite (an infinity or NaN can reach the whole chunk of 64 tokens that holds it,

@@ -68,7 +68,7 @@ gdn_status check(const gdn_ssm_shape *s, const gdn_ssm_params *q, bool varlen, G
     return GDN_OK;
 }
 
-gdn_status check_rows(const gdn_ssm_params *q, const Geometry &g, const void *xbc, const void *dt, const void *z,
+gdn_status check_rows(int32_t heads, const gdn_ssm_params *q, const Geometry &g, const void *xbc, const void *dt, const void *z,
                       const void *w, const void *bias, const float *A_log, const float *dt_bias, const float *D,
                       const void *y) {
     if (g.rows == 0) return GDN_OK;
@@ -81,8 +81,9 @@ gdn_status check_rows(const gdn_ssm_params *q, const Geometry &g, const void *xb
         return fail(GDN_ERR_INVALID_ARG, "A_log, dt_bias and D must be 4-byte aligned");
     const size_t yb = (size_t)g.rows * g.hp * g.es;
     if (overlaps(y, yb, xbc, ((size_t)(g.rows - 1) * g.ld_x + g.C) * g.es) ||
-        overlaps(y, yb, z, ((size_t)(g.rows - 1) * g.ld_z + g.hp) * g.es))
-        return fail(GDN_ERR_INVALID_ARG, "y overlaps xbc or z");
+        overlaps(y, yb, z, ((size_t)(g.rows - 1) * g.ld_z + g.hp) * g.es) ||
+        overlaps(y, yb, dt, ((size_t)(g.rows - 1) * g.ld_dt + heads) * g.es))
+        return fail(GDN_ERR_INVALID_ARG, "y overlaps xbc, z or dt");
     return GDN_OK;
 }
 
@@ -144,7 +145,7 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_shape *shape, const gdn_ssm_params *par
     Geometry g;
     gdn_status st = check(shape, params, cu_seqlens != nullptr, g);
     if (st != GDN_OK) return st;
-    st = check_rows(params, g, xbc, dt, z, conv_weight, conv_bias, A_log, dt_bias, D, y);
+    st = check_rows(shape->heads, params, g, xbc, dt, z, conv_weight, conv_bias, A_log, dt_bias, D, y);
     if (st != GDN_OK) return st;
     if (shape->num_seqs == 0) return GDN_OK;
     if (state_out == nullptr || A_log == nullptr) return fail(GDN_ERR_INVALID_ARG, "state_out or A_log is NULL");
@@ -212,7 +213,7 @@ gdn_status gdn_ssm_decode(const gdn_ssm_shape *shape, const gdn_ssm_params *para
     gdn_status st = check(shape, params, false, g);
     if (st != GDN_OK) return st;
     if (shape->seqlen != 1) return fail(GDN_ERR_INVALID_ARG, "decode takes seqlen 1 (got %lld)", (long long)shape->seqlen);
-    st = check_rows(params, g, xbc, dt, z, conv_weight, conv_bias, A_log, dt_bias, D, y);
+    st = check_rows(shape->heads, params, g, xbc, dt, z, conv_weight, conv_bias, A_log, dt_bias, D, y);
     if (st != GDN_OK) return st;
     if (shape->batch == 0) return GDN_OK;
     if ((int64_t)shape->batch * shape->heads > INT32_MAX)

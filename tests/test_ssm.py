@@ -643,3 +643,11 @@ def test_token_counts_beyond_64_bits_are_refused(batch, seqlen):
     assert lib.load().gdn_ssm_prefill_workspace_bytes(ctypes.byref(shape), ctypes.byref(_params())) == 0
     with pytest.raises(lib.GdnError):
         gdn.gdn_ssm_prefill_plan(shape, _params())
+
+
+@pytest.mark.parametrize("d,stride", [(0, 0), (-8, 0), (1024, 600), (-2 * 600 * 3, 600)])
+def test_y_over_dt_is_refused(d, stride):
+    """Steps are read while other heads' results are being stored.  y holds 4 x 256 values of 2 bytes; dt 4 x 4, or rows of 600."""
+    call = lambda fn, t: fn(_ssm(seqlen=t, batch=4 // t, num_seqs=4 // t, dt_stride=stride), _params(), y=off(1, -d))  # noqa: E731
+    assert call(call_prefill, 4) == call(call_decode, 1) == gdn.GDN_ERR_INVALID_ARG
+    assert b"dt" in lib.load().gdn_last_error_message()
