@@ -133,7 +133,9 @@ gdn_status gdn_ssm_prefill_plan(const gdn_ssm_shape *shape, const gdn_ssm_params
     bool seg = false;
     const int scans = tc ? ssm_tc_launches(varlen, shape->seqlen, g.rows, shape->num_seqs, shape->heads, shape->groups, shape->head_dim, &seg) : 1;
     if (path) *path = tc ? (seg ? 3 : 2) : 1;
-    if (launches) *launches = shape->num_seqs > 0 ? (layout(shape, params, g, varlen).u > 0 ? 1 : 0) + scans : 0;
+    // The convolution's pass: rows to make, or (without any) conv states to carry over.
+    const bool conv = layout(shape, params, g, varlen).u > 0 || params->conv_kernel > 1;
+    if (launches) *launches = shape->num_seqs > 0 ? conv + scans : 0;
     return GDN_OK;
 }
 

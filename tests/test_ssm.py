@@ -651,3 +651,11 @@ def test_y_over_dt_is_refused(d, stride):
     call = lambda fn, t: fn(_ssm(seqlen=t, batch=4 // t, num_seqs=4 // t, dt_stride=stride), _params(), y=off(1, -d))  # noqa: E731
     assert call(call_prefill, 4) == call(call_decode, 1) == gdn.GDN_ERR_INVALID_ARG
     assert b"dt" in lib.load().gdn_last_error_message()
+
+
+@pytest.mark.parametrize("io_dtype", [0, 1])
+@pytest.mark.parametrize("kernel,want", [(0, 1), (1, 1), (2, 2), (4, 2)])
+def test_plans_without_tokens(io_dtype, kernel, want):
+    """Sequences without tokens hand their conv states on by the convolution's launch, where there are any (K > 1)."""
+    for shape in (dict(seqlen=0), dict(seqlen=0, num_seqs=3), dict(seqlen=0, batch=5, num_seqs=5)):
+        assert gdn.gdn_ssm_prefill_plan(_ssm(io_dtype=io_dtype, **shape), _params(conv_kernel=kernel)) == (gdn.PATH_SIMT, want)
