@@ -126,7 +126,8 @@ __device__ __forceinline__ float ssm_step(float dt, float bias, float lo, float 
     return d < lo ? lo : d > hi ? hi : d;
 }
 // e^g.  A slow decay is multiplied in thousands of times, so its rounding has to be fair: expf alone
-// drifts (2,000 tokens of e^-0.0003: 1.4e-5 off, 1.0e-6 so).
-__device__ __forceinline__ float ssm_decay(float g) { return 1.f + expm1f(g); }
+// drifts (2,000 tokens of e^-0.0003: 1.4e-5 off, 1.0e-6 so).  A fast one has to keep its own digits,
+// which 1 + expm1f loses (e^-10 0.05% off, e^-17 and below nothing).
+__device__ __forceinline__ float ssm_decay(float g) { return g > -0.5f ? 1.f + expm1f(g) : expf(g); }
 
 }  // namespace gdn

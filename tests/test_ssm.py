@@ -219,6 +219,25 @@ def test_slow_decays_do_not_drift():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T", [1, 2])
+def test_fast_decays_keep_their_digits(io, T):
+    """Tokens that write nothing: the state is S0 e^g, g = -sum of steps.  The step, A and their product round 2 x 2^-23 of g in
+    all, the exponential 2 units in the last place and the product half a one, to each token: T (2 |g| + 3) 2^-23."""
+    m = draw(io, [T], 9, 64, 1, 64, 0, packed=False, z=False, seed=27)
+    m["dt"] = torch.tensor([0.0, 1.0, 3.0, 6.0, 10.0, 14.0, 17.0, 20.0, 40.0], dtype=DT[io], device="cuda").repeat(T, 1)[None]
+    m["A_log"], m["dt_bias"], m["xbc"] = torch.zeros(9, device="cuda"), torch.zeros(9, device="cuda"), torch.zeros_like(m["xbc"])
+    g = T * torch.nn.functional.softplus(m["dt"][0, 0].double().cpu(), threshold=100)
+    want = m["state"].double().cpu() * torch.exp(-g)[:, None, None]
+    stepped = m["state"].clone()
+    for t in range(T):
+        lib.gdn_ssm_decode(m["xbc"][:, t:t + 1], m["dt"][:, t:t + 1], m["A_log"], stepped, **kwargs(m))
+    for state in (prefill(m)[1], stepped):
+        for h in range(9):
+            assert rel(state[:, h], want[:, h]) <= T * (2 * float(g[h]) + 3) * 2.0 ** -23, (h, rel(state[:, h], want[:, h]))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_a_sequence_does_not_see_its_neighbours(io):
     """Rows of another sequence, infinities and NaN among them, leave a packed sequence's results bit for bit."""
