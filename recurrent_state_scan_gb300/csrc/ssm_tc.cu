@@ -80,7 +80,7 @@ struct TcParams {
     int32_t seg_chunks;                          // chunks per time segment (0: no segments)
     int32_t cut_over;                            // ssm_order cuts if a sequence has more chunks than this
     int4 *items;                                 // [slot] its sequence, segment and seg_chunks, or null: not ordered
-    float *seg_state, *seg_decay;                // [slot][unit][N][64], [slot][unit]
+    float *seg_state, *seg_total;                // [slot][unit][N][64], [slot][unit]: a segment's own end state, its Gates::total's sum
     int *status;
     long long budget;
 };
@@ -172,6 +172,19 @@ __device__ __noinline__ uint4 load_unaligned(const __nv_bfloat16 *src) {
 // ssm_step of a bf16 value, out of line as well (90 instructions).
 __device__ __noinline__ float step_of(uint32_t bits, float bias, float lo, float hi) {
     return ssm_step(__uint_as_float(bits << 16), bias, lo, hi);
+}
+
+// The decay 2^total of a chunk or a segment, and the carry for the next one (the first has 0).  A state
+// that forgets slowly is multiplied by many of them, and ex2.approx is off to one side (65,536
+// tokens, 1,024 chunks: the state 6e-6 off, 3e-5 where all steps are alike).  So slow ones are 1 + x + .. +
+// x^5 / 5! (x = total ln 2; the rest is below 6e-9), and what 1 + .. rounds away goes into the next one.
+// (Out of line, as the waits are: inlined, 65,536 rows took 733 us instead of 712.)
+__device__ __noinline__ float2 next_decay(float total, float carry) {
+    const float x = total * 0.69314718f;
+    if (x < -0.125f) return make_float2(ex2(total), 0.f);
+    const float em = fmaf(x * x, fmaf(x, fmaf(x, fmaf(x, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f), x) + carry;
+    const float d = 1.f + em;
+    return make_float2(d, em - (d - 1.f));
 }
 
 // One work item: the chunks [t0, t1) of segment k of sequence n.
@@ -578,6 +591,7 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
         const int u = (warp - kGateWarp) & 1, head = unit_head(u), first = (warp - kGateWarp) >> 1, step = kState ? 2 : 1;
         const float A = -expf(p.A_log[head]) * kLog2e, bias = p.dt_bias ? p.dt_bias[head] : 0.f;
         unsigned short n0 = 0, n1 = 0;      // bits, widened a chunk later: nothing waits for the load here
+        float carry = 0.f;
         auto load_dt = [&](int c) {
             const int64_t t = it.t0 + (int64_t)c * kL + 2 * lane;
             const unsigned short *at = reinterpret_cast<const unsigned short *>(p.dt + t * p.ld_dt + head);
@@ -602,13 +616,15 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
             float after = __shfl_down_sync(0xffffffffu, suf, 1);
             if (lane == 31) after = 0.f;
             const float l0 = __log2f(d0), l1 = __log2f(d1);   // -inf where the step is zero: no weight
+            const float2 decay = next_decay(suf, carry);      // (lane 0's is the whole chunk's)
+            carry = decay.y;
             if (c >= NS && !(ok = all(wait_st(ctl.s_ready, c - NS) && (kState || wait2(ctl.y_read, c - NS))))) break;
             Gates &G = gate[c & (NS - 1)][u];
             *reinterpret_cast<float2 *>(&G.s[2 * lane]) = make_float2(after + g1, after);
             *reinterpret_cast<float2 *>(&G.lw[2 * lane]) = make_float2(after + g1 + l0, after + l1);
             if (lane == 0) {
                 G.total = suf;
-                G.decay = ex2(suf);
+                G.decay = decay.x;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.gates[c & (NS - 1)]);
@@ -677,7 +693,7 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
 #pragma unroll
                 for (int i = 0; i < 64; i += 4)
                     *reinterpret_cast<float4 *>(p.seg_state + sseg + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
-                if (sn == 0) p.seg_decay[it.slot * nunits + sunit] = ex2(seg_total);
+                if (sn == 0) p.seg_total[it.slot * nunits + sunit] = seg_total;
             } else if (it.k + 1 == it.nseg) {
 #pragma unroll
                 for (int i = 0; i < 64; i += 4)
@@ -814,24 +830,27 @@ __global__ void __launch_bounds__(256) ssm_segment_states(const __grid_constant_
         S = *reinterpret_cast<const float4 *>(p.state_in + (((size_t)n * p.heads + head) * p.N + r) * p.P + tile * 64 + col);
     const size_t step = (size_t)nunits * p.N * 64;
     float4 *place = reinterpret_cast<float4 *>(p.seg_state + (size_t)(first * nunits + unit) * p.N * 64 + 4 * (size_t)e);
-    const float *decay = p.seg_decay + first * nunits + unit;
-    constexpr int kAhead = 8;         // segments loaded at once: the chain itself is one FMA each
+    const float *total = p.seg_total + first * nunits + unit;
+    float carry = 0.f;
+    constexpr int kAhead = 8;         // segments loaded at once: the chain itself is a decay and an FMA each
     for (int k0 = 0; k0 < nseg; k0 += kAhead) {
         float4 own[kAhead];
-        float d[kAhead];
+        float t[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
             if (k0 + i + 1 < nseg) {
                 own[i] = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(place) + (size_t)(k0 + i) * step);
-                d[i] = decay[(int64_t)(k0 + i) * nunits];
+                t[i] = total[(int64_t)(k0 + i) * nunits];
             }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (k0 + i >= nseg) break;
             *reinterpret_cast<float4 *>(reinterpret_cast<float *>(place) + (size_t)(k0 + i) * step) = S;
             if (k0 + i + 1 == nseg) break;
-            S.x = fmaf(d[i], S.x, own[i].x); S.y = fmaf(d[i], S.y, own[i].y);
-            S.z = fmaf(d[i], S.z, own[i].z); S.w = fmaf(d[i], S.w, own[i].w);
+            const float2 d = next_decay(t[i], carry);
+            carry = d.y;
+            S.x = fmaf(d.x, S.x, own[i].x); S.y = fmaf(d.x, S.y, own[i].y);
+            S.z = fmaf(d.x, S.z, own[i].z); S.w = fmaf(d.x, S.w, own[i].w);
         }
     }
 }
@@ -941,7 +960,7 @@ cudaError_t launch_ssm_tc(const SsmParams &s, void *workspace, cudaStream_t stre
     const int pairs = s.groups * p.pairs_per_group;
     if (b.seg > 0) p.cut_over = (int32_t)(kCutOver * ((s.rows + kL - 1) / kL) * pairs / kSms);
     p.seg_state = static_cast<float *>(workspace);
-    p.seg_decay = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + b.state);
+    p.seg_total = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + b.state);
     p.items = b.ordered ? reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) + b.items) : nullptr;
 
     const int64_t grid = b.slots * pairs;

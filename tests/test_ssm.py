@@ -219,6 +219,23 @@ def test_slow_decays_do_not_drift():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,n,T,path", [(64, 3, 65536, gdn.PATH_TC), (2, 1, 65536, gdn.PATH_TC_TP)])
+@pytest.mark.parametrize("A_log", [-10.0, -8.0])
+def test_slow_decays_do_not_drift_over_chunks(H, n, T, path, A_log):
+    """1,024 chunks (or 128 segments of 8) that forget next to nothing and write nothing.  Each chunk rounds its decay (2^-25) and
+    the state (2^-24), at random: sqrt(1024) times 1.5 * 2^-24; the exponent's own roundings are 2^-22 of it."""
+    m = draw("bf16", [T] * n, H, 8, 1, 16, 0, packed=False, z=False, seed=28)
+    shape = gdn.GdnSsmShape(1, n, T, n, H, 8, 1, 16, 0, 0, 0)
+    assert gdn.gdn_ssm_prefill_plan(shape, gdn.GdnSsmParams(0, 0, 0.0, 1.0))[0] == path
+    m["A_log"], m["xbc"] = torch.full((H,), A_log, device="cuda"), torch.zeros_like(m["xbc"])
+    steps = torch.nn.functional.softplus(m["dt"].double() + m["dt_bias"].double(), threshold=100).sum(1)
+    g = math.exp(A_log) * steps
+    state = prefill(m)[1].double()
+    want = m["state"].double() * torch.exp(-g)[:, :, None, None]
+    assert rel(state, want) <= 1024 ** 0.5 * 1.5 * 2.0 ** -24 + float(g.max()) * 2.0 ** -22
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("T", [1, 2])
 def test_fast_decays_keep_their_digits(io, T):
