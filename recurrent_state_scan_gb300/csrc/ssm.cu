@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(const SsmParams 
             const int64_t t = tb + e * kBatch + slice;
             if (live && t < t1) {
                 float out = fmaf(D, sx[buf][e * kBatch + slice][col], y[0]);
-                if (z) out *= silu_gate(IoType<IO>::ld(&zv[e]));
+                if (z) out *= silu_gate<IO>(IoType<IO>::ld(&zv[e]));
                 IoType<IO>::st(static_cast<IO *>(p.y) + t * (int64_t)p.heads * P + yc, out);
             }
         }
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kDecThreads, 4) ssm_decode_kernel(const SsmDec
         for (int r = 0; r < RP; ++r) out += red[r * P + tid];
         out = fmaf(D, sx[tid], out);
         const int64_t yc = (int64_t)h * P + tid;
-        if (p.z) out *= silu_gate(IoType<IO>::ld(static_cast<const IO *>(p.z) + b * p.ld_z + yc));
+        if (p.z) out *= silu_gate<IO>(IoType<IO>::ld(static_cast<const IO *>(p.z) + b * p.ld_z + yc));
         IoType<IO>::st(static_cast<IO *>(p.y) + b * (int64_t)hp + yc, out);
     }
 }
@@ -806,8 +806,9 @@ __global__ void __launch_bounds__(kDecThreads, 2) ssm_decode_stream_kernel(const
         }
         if (i + 1 < count) gather(u + 1);
         const int64_t yc = (int64_t)h * P + tid;
-        float gate = 1.f;
-        if (p.z && tid < P) gate = silu_gate(IoType<IO>::ld(static_cast<const IO *>(p.z) + b * p.ld_z + yc));
+        IO zr;                                       // (widened where it is used: nothing waits for it here)
+        IoType<IO>::st(&zr, 0.f);
+        if (p.z && tid < P) zr = static_cast<const IO *>(p.z)[b * p.ld_z + yc];
         const bool ok = mbar_wait(&full[i % kRing], (i / kRing) & 1, 4000000000LL);
         if (!ok) atomicOr(p.status, kDevTimeout);
         float4 *S = reinterpret_cast<float4 *>(ring + (size_t)(i % kRing) * bytes) + quad;
@@ -836,7 +837,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) ssm_decode_stream_kernel(const
         if (live && tid < P) {
             float out = 0.f;
             for (int r = 0; r < RP; ++r) out += red[r * P + tid];
-            out = fmaf(skip, sx[tid], out) * gate;
+            out = fmaf(skip, sx[tid], out);
+            if (p.z) out *= silu_gate<IO>(IoType<IO>::ld(&zr));
             IoType<IO>::st(static_cast<IO *>(p.y) + b * (int64_t)hp + yc, out);
         }
         __syncthreads();                             // sx, sB, sC and red are free

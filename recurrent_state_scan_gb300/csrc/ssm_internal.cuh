@@ -117,8 +117,13 @@ __device__ __forceinline__ F2 both(float a) { return {a, a}; }
 // silu as the convolution stores it: the correctly scaled exponential and a true divide,
 // so that its rounding to a 16-bit type does not hang on an approximation's last bits.
 __device__ __forceinline__ float silu_exact(float v) { return v / (1.0f + expf(-v)); }
-// silu of the gate z, which only meets the output's own rounding: fast intrinsics.
-__device__ __forceinline__ float silu_gate(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+// silu of the gate z by e^-|z|, which neither overflows nor loses a gate far below zero.  An f32 output
+// meets no other rounding, so there to fp32's own precision; a 16-bit one by the fast intrinsics, within
+// 2^-16 of it.
+template <typename IO> __device__ __forceinline__ float silu_gate(float v) {
+    const float e = sizeof(IO) == 4 ? expf(-fabsf(v)) : __expf(-fabsf(v)), num = v < 0.0f ? e : 1.0f;
+    return v * (sizeof(IO) == 4 ? num / (1.0f + e) : __fdividef(num, 1.0f + e));
+}
 
 // The step d = clamp(softplus(dt + dt_bias), dt_min, dt_max); a NaN stays one.
 __device__ __forceinline__ float ssm_step(float dt, float bias, float lo, float hi) {

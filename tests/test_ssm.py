@@ -209,6 +209,32 @@ def test_gates_far_out(io, gap):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_gates_keep_their_digits(io):
+    """Each value against the ungated one times silu(z) in 64 bits, on the FP32 cores.  The exponential is off by 2 units in the
+    last place, the sum, the quotient and the two products by half a one each: 4 x 2^-23.  In bf16 by fast intrinsics, |z| + 8
+    times 2^-23 at most, and two roundings more."""
+    far = torch.tensor([-0.5, -5.0, -20.0, -40.0, -60.0, -80.0, -86.0, -88.0, 0.0, 0.25, 5.0, 60.0, 100.0])
+    m = draw(io, [1] * 26, 2, 52, 1, 33, 0, packed=False, seed=29)
+    m["z"] = (far.repeat(2)[:, None, None, None] + 0.125 * torch.rand(26, 1, 2, 52, generator=torch.Generator().manual_seed(1))).to(DT[io]).cuda()
+    silu = m["z"].double() * torch.sigmoid(m["z"].double())
+    off = 2.0 ** -16 + 2 * 2.0 ** -8 if io == "bf16" else 4 * 2.0 ** -23
+
+    def near(gated, plain):
+        want = plain.double() * silu
+        assert ((gated.double() - want).abs() <= off * want.abs() + 2.0 ** -133).all()
+
+    near(prefill(m)[0], prefill(dict(m, z=None))[0])
+    token = lambda z: lib.gdn_ssm_decode(m["xbc"], m["dt"], m["A_log"], m["state"].clone(), **dict(kwargs(m), z=z))  # noqa: E731
+    near(token(m["z"]), token(None))
+    wide = dict(draw(io, [1] * 26, 2, 128, 1, 128, 0, packed=False, seed=30), z=None)       # (the step of larger states)
+    token = lambda z: lib.gdn_ssm_decode(wide["xbc"], wide["dt"], wide["A_log"], wide["state"].clone(), **dict(kwargs(wide), z=z))  # noqa: E731
+    m["z"] = torch.cat([m["z"], m["z"], m["z"][..., :24]], 3)
+    silu = m["z"].double() * torch.sigmoid(m["z"].double())
+    near(token(m["z"]), token(None))
+
+
+@pytest.mark.gpu
 def test_slow_decays_do_not_drift():
     """2,000 tokens that forget next to nothing.  Each rounds its decay (half a step below 1: 2^-25), the state's update
     (2^-24) and its own share (twice 2^-24, of a small part): at random, so they add up to sqrt(2000) times 2 * 2^-24 at most."""
