@@ -116,19 +116,12 @@ __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0
 __device__ __forceinline__ F2 words(uint32_t a, uint32_t b) { return {__uint_as_float(a), __uint_as_float(b)}; }
 __device__ __forceinline__ F2 widen(uint32_t v) { return {lo_f(v), hi_f(v)}; }
 __device__ __forceinline__ uint32_t pack2(F2 a) { return pack2(a.x, a.y); }
-// max(z, -41), NaN where z is.
-__device__ __forceinline__ float at_least_m41(float z) {
-    asm("max.NaN.f32 %0, %0, 0fC2240000;" : "+f"(z));
-    return z;
-}
-// a silu(z) for two values with one reciprocal: 1 / d0 = d1 / (d0 d1).  z stops at -41, so that the
-// product stays finite (silu is then -6e-17, where it is nearer to zero still); a NaN stays out of
-// the reciprocal, which is its neighbour's too.
+// a silu(z) for two values.  Below z = -87.3 the reciprocal is subnormal and flushed: the gate is 0 where
+// silu is within 1.1e-36 of it.  (One reciprocal for both, 1 / d0 = d1 / (d0 d1), needs the exponents held
+// down: at z >= -41 the gates below were wrong by orders, by e^-|z| 8,192 tokens took 183 us, not 181.)
 __device__ __forceinline__ F2 gated(F2 a, F2 z) {
-    const F2 t = mul2({fmaxf(z.x, -41.f), fmaxf(z.y, -41.f)}, both(-kLog2e));
-    z = {at_least_m41(z.x), at_least_m41(z.y)};
-    const F2 d = add2({ex2(t.x), ex2(t.y)}, both(1.f));
-    return mul2(mul2(mul2(a, z), both(rcp(d.x * d.y))), {d.y, d.x});
+    const F2 t = mul2(z, both(-kLog2e)), d = add2({ex2(t.x), ex2(t.y)}, both(1.f));
+    return mul2(a, mul2(z, {rcp(d.x), rcp(d.y)}));
 }
 
 // Tensor-memory loads have landed.  The values pass through it, so that no arithmetic on them

@@ -235,6 +235,21 @@ def test_gates_keep_their_digits(io):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("gap", [0, 1])
+def test_gates_keep_their_digits_on_the_tensor_cores(gap):
+    """Each value against the ungated one times silu(z) in 64 bits: two roundings to bf16, and |z| + 8 times 2^-23 of fast
+    intrinsics at most.  (Off 16 bytes z comes by plain loads.)"""
+    far = torch.tensor([-0.5, -5.0, -20.0, -40.0, -41.5, -44.0, -50.0, -60.0, -70.0, -80.0, -86.0, 0.0, 0.25, 5.0, 60.0, 100.0])
+    m = draw("bf16", [80], 2, 64, 1, 64, 0, seed=31, gap=(-(2 * 2 * 64 + 2 * 64 + 2)) % 8)
+    rows = far.repeat(5)[None, :, None, None] + 0.125 * torch.rand(1, 80, 2, 64, generator=torch.Generator().manual_seed(1))
+    wide = torch.empty(1, 80, 128 + gap, dtype=torch.bfloat16, device="cuda")
+    m["z"] = wide[..., gap:].unflatten(2, (2, 64)).copy_(rows)
+    silu = m["z"].double() * torch.sigmoid(m["z"].double())
+    want = prefill(dict(m, z=None))[0].double() * silu
+    assert ((prefill(m)[0].double() - want).abs() <= (2 * 2.0 ** -8 + 2.0 ** -16) * want.abs() + 2.0 ** -133).all()
+
+
+@pytest.mark.gpu
 def test_slow_decays_do_not_drift():
     """2,000 tokens that forget next to nothing.  Each rounds its decay (half a step below 1: 2^-25), the state's update
     (2^-24) and its own share (twice 2^-24, of a small part): at random, so they add up to sqrt(2000) times 2 * 2^-24 at most."""
