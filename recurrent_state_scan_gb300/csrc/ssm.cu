@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(const SsmParams 
 
     const IO *xs = static_cast<const IO *>(p.xs), *dt = static_cast<const IO *>(p.dt);
     const IO *z = static_cast<const IO *>(p.z);
-    const float A = -expf(p.A_log[h]), bias = p.dt_bias ? p.dt_bias[h] : 0.f, D = p.D ? p.D[h] : 0.f;
+    const float A = ssm_rate(p.A_log[h]), bias = p.dt_bias ? p.dt_bias[h] : 0.f, D = p.D ? p.D[h] : 0.f;
     IO rb[LOADS], rx[kXs], rd, rz[kTile / kBatch];      // (widened where they are used: nothing waits for them in load)
     const IO none = IO(0.f);
     const int64_t yc = (int64_t)h * P + c0 + col;
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kDecThreads, 4) ssm_decode_kernel(const SsmDec
     const IO *conv = p.conv ? static_cast<const IO *>(p.conv) + e * (int64_t)(p.K - 1) * p.C : nullptr;
     const float d = ssm_step(IoType<IO>::ld(static_cast<const IO *>(p.dt) + b * p.ld_dt + h), p.dt_bias ? p.dt_bias[h] : 0.f,
                              p.dt_min, p.dt_max);
-    const float a = ssm_decay(-expf(p.A_log[h]) * d), D = p.D ? p.D[h] : 0.f;
+    const float a = ssm_decay(ssm_rate(p.A_log[h]) * d), D = p.D ? p.D[h] : 0.f;
     for (int i = tid; i < P + 2 * N; i += kDecThreads) {
         if (i < P) sx[i] = conv_token(p, x, conv, h * P + i);
         else if (i < P + N) sB[i - P] = conv_token(p, x, conv, hp + g * N + i - P);
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) ssm_decode_stream_kernel(const
             (i < P ? sx[i] : i < P + N ? sB[i - P] : sC[i - P - N]) = v;
         }
         d = ssm_step(IoType<IO>::ld(&raw_dt), db, p.dt_min, p.dt_max);
-        a = ssm_decay(-expf(A) * d);
+        a = ssm_decay(ssm_rate(A) * d);
         skip = D;
     };
 

@@ -130,6 +130,12 @@ __device__ __forceinline__ float ssm_step(float dt, float bias, float lo, float 
     const float d = softplus_f(dt + bias);
     return d < lo ? lo : d > hi ? hi : d;
 }
+// -e^{A_log}, held finite (and so that its product with log2 e is): a step of 0 then has a decay of 1, not a NaN,
+// past A_log = 88 too.
+__device__ __forceinline__ float ssm_rate(float A_log) {
+    const float e = expf(A_log);
+    return e > 0x1p126f ? -0x1p126f : -e;
+}
 // e^g.  A slow decay is multiplied in thousands of times, so its rounding has to be fair: expf alone
 // drifts (2,000 tokens of e^-0.0003: 1.4e-5 off, 1.0e-6 so).  A fast one has to keep its own digits,
 // which 1 + expm1f loses (e^-10 0.05% off, e^-17 and below nothing).

@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
         // A decay of e^-111 is already nothing in fp32, so g is held above that: a reset then leaves
         // the sums over it small enough to keep the differences of the tokens before it.
         const int u = (warp - kGateWarp) & 1, head = unit_head(u), first = (warp - kGateWarp) >> 1, step = kState ? 2 : 1;
-        const float A = -expf(p.A_log[head]) * kLog2e, bias = p.dt_bias ? p.dt_bias[head] : 0.f;
+        const float A = ssm_rate(p.A_log[head]) * kLog2e, bias = p.dt_bias ? p.dt_bias[head] : 0.f;
         unsigned short n0 = 0, n1 = 0;      // bits, widened a chunk later: nothing waits for the load here
         float carry = 0.f;
         auto load_dt = [&](int c) {

@@ -194,6 +194,27 @@ def test_extreme_steps(io):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io,P", [("bf16", 64), ("bf16", 52), ("f32", 64)])
+def test_rates_beyond_fp32(io, P):
+    """e^A_log above fp32's range: every token with a step clears the state, one without (dt = -inf) leaves it, the last of a tile too."""
+    m = draw(io, [75, 5, 1], 2, P, 1, 64, 0, z=False, seed=32)
+    m["A_log"] = torch.tensor([95.0, 88.5], device="cuda")
+    m["dt"] = m["dt"].clone()
+    m["dt"][:, 60:75], m["dt"][:, 80] = -math.inf, -math.inf
+    got = prefill(m)
+    check(m, got, define(m))
+    assert torch.equal(got[1][2], m["state"][2])
+    wide = draw(io, [1, 1], 2, 128, 1, 128, 0, packed=False, z=False, seed=33)
+    for m in (draw(io, [1, 1], 2, P, 1, 64, 0, packed=False, z=False, seed=33), wide):
+        m["A_log"], m["dt"] = torch.tensor([95.0, 88.5], device="cuda"), m["dt"].clone()
+        m["dt"][1] = -math.inf
+        state = m["state"].clone()
+        y = lib.gdn_ssm_decode(m["xbc"], m["dt"], m["A_log"], state, **kwargs(m))
+        check(m, (y, state, None), define(m))
+        assert torch.equal(state[1], m["state"][1])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("gap", [0, 1])
 def test_gates_far_out(io, gap):
