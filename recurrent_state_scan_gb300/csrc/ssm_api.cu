@@ -58,7 +58,8 @@ gdn_status check(const gdn_ssm_shape *s, const gdn_ssm_params *q, bool varlen, G
     if (g.rows > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%lld token rows are not built", (long long)g.rows);
     g.hp = (int64_t)s->heads * s->head_dim;
     g.C = g.hp + 2LL * s->groups * s->d_state;
-    if (g.C > 1 << 24) return fail(GDN_ERR_UNSUPPORTED, "mixed rows of %lld elements are not built", (long long)g.C);
+    if (g.C > 65535LL * 256)       // (a grid's second extent, of the single-token conv states' 256 channels)
+        return fail(GDN_ERR_UNSUPPORTED, "mixed rows of %lld elements are not built", (long long)g.C);
     g.ld_x = s->xbc_stride ? s->xbc_stride : g.C;
     g.ld_dt = s->dt_stride ? s->dt_stride : s->heads;
     g.ld_z = s->z_stride ? s->z_stride : g.hp;

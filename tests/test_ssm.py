@@ -757,3 +757,9 @@ def test_plans_without_tokens(io_dtype, kernel, want):
     """Sequences without tokens hand their conv states on by the convolution's launch, where there are any (K > 1)."""
     for shape in (dict(seqlen=0), dict(seqlen=0, num_seqs=3), dict(seqlen=0, batch=5, num_seqs=5)):
         assert gdn.gdn_ssm_prefill_plan(_ssm(io_dtype=io_dtype, **shape), _params(conv_kernel=kernel)) == (gdn.PATH_SIMT, want)
+
+
+def test_rows_wider_than_a_grid_are_refused():
+    """The step would have run, and the launch behind it, which moves the conv states on, failed."""
+    for call, t in ((call_prefill, 4), (call_decode, 1)):      # rows of 2^24 elements
+        assert call(_ssm(heads=65535, head_dim=256, groups=1, d_state=128, seqlen=t), _params()) == gdn.GDN_ERR_UNSUPPORTED
