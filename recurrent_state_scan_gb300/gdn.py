@@ -889,6 +889,8 @@ def _rows(name: str, t, B: int, T: int, row: tuple, dtype, device: int):
 
 @contextlib.contextmanager
 def _elsewhere(device: int, stream):
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != device:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"stream must be on cuda:{device}, as the call's first tensor is")
     with torch.cuda.device(device):
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=device)

@@ -763,3 +763,13 @@ def test_rows_wider_than_a_grid_are_refused():
     """The step would have run, and the launch behind it, which moves the conv states on, failed."""
     for call, t in ((call_prefill, 4), (call_decode, 1)):      # rows of 2^24 elements
         assert call(_ssm(heads=65535, head_dim=256, groups=1, d_state=128, seqlen=t), _params()) == gdn.GDN_ERR_UNSUPPORTED
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """(Torch would have made it current on its own device, and the call have run on this one's default stream.)"""
+    class Stream:
+        device_index = 1
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    with pytest.raises(lib.GdnError, match="stream must be on cuda:0"):
+        with gdn._on(0, Stream()):
+            pass
