@@ -64,6 +64,22 @@ def test_matches_the_definition(io, interleaved, T, hq, hk, D, rot, offset):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io,T,hq,hk,D,rot,offset", [("bf16", 80003, 3, 1, 128, 128, 0), ("f16", 78000, 2, 2, 96, 32, 64),
+                                                     ("f32", 40001, 4, 1, 64, 64, 0), ("bf16", 80003, 3, 2, 42, 18, 5)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_many_rows(io, T, hq, hk, D, rot, offset, interleaved):
+    """So many rows that a CTA takes up to 32 of them and goes over its threads' rows several times."""
+    g = torch.Generator().manual_seed(T)
+    q, k = (torch.randn(1, T, h, D, generator=g).to(DT[io]).cuda() for h in (hq, hk))
+    inv_freq, _ = lib.gdn_rotary_frequencies(rot, device="cuda")
+    got = lib.gdn_rotary(q, k, inv_freq, rot_offset=offset, interleaved=interleaved)
+    for t, y in zip((q, k), got):
+        assert rel(y, turn(t, torch.arange(T)[None], inv_freq, offset, interleaved, False, 1.0)) <= tol(DT[io])
+        for r in (0, 31, 32, T // 2, T - 1):
+            assert rel(y[:, r], turn(t[:, r:r + 1], torch.tensor([[r]]), inv_freq, offset, interleaved, False, 1.0)[:, 0]) <= 2 * tol(DT[io])
+
+
+@pytest.mark.gpu
 def test_places_in_packed_rows_and_in_place():
     g = torch.Generator().manual_seed(1)
     lens = [3, 0, 70, 1]

@@ -167,6 +167,49 @@ def test_convolved_rows_on_16_bytes(io, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io,T,K,gap", [("bf16", 4000, 4, 0), ("bf16", 4000, 3, 0), ("bf16", 4001, 2, 8), ("bf16", 3999, 1, 0),
+                                        ("f16", 4000, 4, 0), ("f16", 4003, 2, 8), ("bf16", 4000, 4, 1), ("f16", 4000, 3, 2),
+                                        ("f32", 4000, 4, 0), ("f32", 4002, 2, 4), ("f32", 4000, 3, 1)])
+def test_convolved_rows_in_long_runs(io, T, K, gap):
+    """Runs of many stages (rows on 16 bytes: 42 rows in stages of 6, four at a time), sequences that begin and end inside them.
+    With C's taps 0, D 1 and no earlier state y is the convolved x: against the definition, within its one rounding (and 16 x 2^-24
+    of the sum's, the exponential's and the quotient's in fp32), and bit for bit against every row as a single token."""
+    H, P, N = 64, 64, 16
+    lens = [1000, 41, 1, 0, 7, 1500, 3, 42, 84]
+    lens.append(T - sum(lens))
+    C, hp, n = H * P + 2 * N, H * P, len(lens)
+    g = torch.Generator().manual_seed(T + K)
+    row = (3 * torch.randn(1, T, C + H + (-(C + H)) % 8 + gap, generator=g)).to(DT[io]).cuda()
+    x, dt = row[..., :C], row[..., C:C + H]
+    w = (torch.randn(C, 1, K, generator=g) * K ** -0.5).to(DT[io])
+    b = (0.1 * torch.randn(C, generator=g)).to(DT[io])
+    w[hp + N:], b[hp + N:] = 0, 0
+    w, b, past = w.cuda(), b.cuda(), torch.randn(n, K - 1, C, generator=g).to(DT[io]).cuda()
+    cu = torch.tensor([sum(lens[:i]) for i in range(n + 1)], dtype=torch.int32, device="cuda")
+    layer = dict(heads=H, head_dim=P, d_state=N, D=torch.ones(H, device="cuda"), conv_weight=w, conv_bias=b)
+    A_log = torch.zeros(H, device="cuda")
+    y, _, conv = lib.gdn_ssm_prefill(x, dt, A_log, conv_state_in=past, cu_seqlens=cu, **layer)
+    assert lib.gdn_last_device_status() == 0
+    before, pads = [], []
+    for i, L in enumerate(lens):
+        pads.append(torch.cat([past[i], x[0, cu[i]:cu[i + 1]]]))
+        before.append(torch.stack([pads[-1][j:j + L] for j in range(K)], 1))       # [L, K, C]
+    rows = torch.cat(before)
+    assert torch.equal(conv, torch.stack([p[len(p) - (K - 1):] for p in pads]))
+    u, size = b.double().expand(T, C)[:, :hp], b.double().abs().expand(T, C)[:, :hp]
+    for j in range(K):
+        u = u + w[:hp, 0, j].double() * rows[:, j, :hp].double()
+        size = size + (w[:hp, 0, j].double() * rows[:, j, :hp].double()).abs()
+    want = (u * torch.sigmoid(u)).view(1, T, H, P)
+    off = (want.abs() * torch.finfo(DT[io]).eps / 2 + 16 * 2.0 ** -24 * (size.view_as(want) + want.abs()) + torch.finfo(DT[io]).tiny)
+    assert ((y.double() - want).abs() <= off).all()
+    del u, size, want, off
+    state = torch.zeros(T, H, N, P, device="cuda")
+    tokens = lib.gdn_ssm_decode(x.transpose(0, 1), dt.transpose(0, 1), A_log, state, conv_state=rows[:, :-1].contiguous(), **layer)
+    assert lib.gdn_last_device_status() == 0 and torch.equal(tokens.view_as(y), y)
+
+
+@pytest.mark.gpu
 def test_optional_operands_and_bounds_on_the_step():
     m = draw("f32", [40, 3], 4, 32, 2, 16, 3, seed=4)
     args = dict(kwargs(m), D=None, dt_bias=None, conv_bias=None)
