@@ -14,17 +14,18 @@
 // unit 1's, and every lane quarter of tensor memory has work.  Per chunk:
 //   scores C B^T -> M (fp32 weights, rounded to bf16) -> [M0; M1] [x0 | x1]     \ y, by the y warps
 //   C [S0 | S1]                                                                  /
-//   w x split into bf16 hi + lo -> B^T [w x hi] + B^T [w x lo] -> S = e^{G_L} S + ..   by the S warps
+//   w x split into three bf16 terms -> the sum of B^T [term] -> S = e^{G_L} S + ..     by the S warps
 // The warps' roles run side by side, a chunk apart where the data allows it.
 //
 // Bound by the chain from one chunk's y to the next (readout, M, its MMA) and by issue: a pair of
 // units takes 2.55 us a chunk (2.85 with z), of which the tensor pipe works a quarter, the issue slots
 // about half and shared memory about half.  8,192 tokens of 64 heads of 64 x 128 with z: 92 us on
 // 128 CTAs, behind 39 us of state-only pass and 5 us for the segments' states.
-// Precision: the state is fp32 and its update's operands are exact (B) or a two-term bf16 split
-// (w x: 2^-17 of each product), because the state is returned in fp32 and carried on; M and
-// the S that C reads are rounded once to bf16, half a step (2^-9 of each term's size at random
-// signs), under the one rounding that y meets itself.  f16 stays on the FP32 cores: w x and M
+// Precision: the state is fp32 and its update's operands are exact (B) or a three-term bf16 split (w x, to
+// fp32's own 2^-24), because the state is returned in fp32 and carried on: it is 1.1e-7 off, as 32-bit
+// arithmetic is, where two terms left it 2.4e-6 off (in 3 to 7% less time).  M and the S that C reads are
+// rounded once to bf16, half a step (2^-9 of each term's size at random signs), under the one rounding that
+// y meets itself.  f16 stays on the FP32 cores: w x and M
 // leave its range.
 //
 // Where sequences x units leave most SMs idle, each sequence is cut along time: a state-only
@@ -34,6 +35,8 @@
 #include <cudaTypedefs.h>
 #include <stddef.h>
 #include <string.h>
+
+#include <type_traits>
 
 #include "ssm_internal.cuh"
 #include "tc_ptx.cuh"
@@ -47,17 +50,18 @@ constexpr int kL = 64;                       // tokens per chunk
 constexpr long long kBudget = 4000000000LL;  // cycles (~2 s) before a wait gives up
 
 // Shared memory (1024-byte aligned): stages of what TMA brings, then the operands the threads
-// make.  All tiles are stacks of 128-byte-swizzled rows of 64 bf16.  y takes z's place, for a
-// TMA store.  The state-only pass has no C and twice the stages.
+// make.  All tiles are stacks of 128-byte-swizzled rows of 64 bf16.  y, on its way to a TMA store, stands
+// in z's place, or, where z comes by TMA itself, in B's, which the chunk's last MMAs are done with.  The
+// state-only pass has no C, no S and twice the stages, and takes w x in two buffers.
 constexpr int ST_B = 0;                      // 2 regions of 64 state columns x 64 rows
 constexpr int ST_X = 16384;                  // 2 units x 64 rows
 constexpr int ST_C = 32768;                  // 2 regions x 128 rows: C twice
 template <bool kState> constexpr int kStageBytes = kState ? 32768 : 65536;
 template <bool kState> constexpr int kStages = kState ? 4 : 2;
-constexpr int O_Z = 131072;                  // z, then y, by chunk parity: 2 units x 64 rows each
-constexpr int O_XH = O_Z + 32768;            // w x, high part: 2 units x 64 rows
-constexpr int O_XL = O_XH + 16384;           // low part
-constexpr int O_S = O_XL + 16384;            // bf16(S): 2 units x 128 state rows
+constexpr int O_Z = 131072;                  // z or y: 2 units x 64 rows
+template <bool kState> constexpr int kWx = kState ? O_Z : O_Z + 16384;    // w x: 3 terms of 2 units x 64 rows
+constexpr int WX_TERM = 16384, WX_BYTES = 3 * WX_TERM;
+constexpr int O_S = kWx<false> + WX_BYTES;   // bf16(S): 2 units x 128 state rows
 constexpr int O_CTL = O_S + 32768;           // Ctl
 
 // Tensor memory columns; M is the A operand of the last MMA, bf16 pairs.
@@ -89,21 +93,29 @@ struct TcParams {
 // and lw_j = s_j + log2 d_j.  All that is needed follows: w_j = 2^{lw_j}, the scores' weights
 // 2^{lw_j - s_i}, and e^{G_i} = 2^{total - s_i}.
 struct alignas(16) Gates {       // read in float2 and float4
-    float lw[kL], s[kL];
+    float lw[kL];
     float total, decay;          // log2 e^{G_L}, e^{G_L}
+    float s[kL];
+};
+struct alignas(16) StateGates {  // the part of them that the state needs
+    float lw[kL];
+    float total, decay;
 };
 
 struct Ctl {
     // Barriers: pairs by chunk parity where a waiter can be a chunk behind (`full` and s_ready
     // by stage).
-    uint64_t full[4], gates[4], y_read[2], s_ready[4], wx_ready[2], ds[2], full_x[2], full_z[2];
-    uint64_t y_done[2], s_read, cb, cs, mx, m_ready, s_first, drain;
+    uint64_t full[4], gates[4], y_read[2], s_ready[4], wx_ready[2], ds[2], full_x[2];
+    uint64_t y_done[2], full_z, s_read, cb, cs, mx, m_ready, s_first, drain;
     uint32_t tmem;
     int32_t abort;   // a wait ran out
-    Gates g[2][2];   // [stage][unit] (the state-only pass, with room behind, has four stages)
+    Gates g[2][2];   // [stage][unit] (the state-only pass: StateGates of four stages)
 };
-static_assert(sizeof(Gates) % 16 == 0 && offsetof(Ctl, g) % 16 == 0 && O_CTL % 16 == 0, "vector accesses of the gates");
-constexpr int kSmem = O_CTL + sizeof(Ctl);
+static_assert(sizeof(Gates) % 16 == 0 && sizeof(StateGates) % 16 == 0 && offsetof(Ctl, g) % 16 == 0 && O_CTL % 16 == 0,
+              "vector accesses of the gates");
+static_assert(kWx<true> + 2 * WX_BYTES <= O_CTL, "w x of the state-only pass");
+constexpr int kCtlBytes = offsetof(Ctl, g) + 8 * sizeof(StateGates);       // the state-only pass's
+constexpr int kSmem = O_CTL + ((int)sizeof(Ctl) > kCtlBytes ? (int)sizeof(Ctl) : kCtlBytes);
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -308,8 +320,10 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
     // (Nothing static stands before it, so dynamic shared memory begins on a 1024-byte boundary, as
     // the swizzled tiles need; there is no room to align it here.)
     extern __shared__ __align__(1024) uint8_t sm[];
-    Ctl &ctl = *reinterpret_cast<Ctl *>(sm + (kState ? O_Z : O_CTL));
-    Gates(*const gate)[2] = reinterpret_cast<Gates(*)[2]>(reinterpret_cast<uint8_t *>(&ctl) + offsetof(Ctl, g));
+    Ctl &ctl = *reinterpret_cast<Ctl *>(sm + O_CTL);
+    using GateSet = std::conditional_t<kState, StateGates, Gates>;
+    GateSet(*const gate)[2] = reinterpret_cast<GateSet(*)[2]>(reinterpret_cast<uint8_t *>(&ctl) + offsetof(Ctl, g));
+    const Gates(*const ygate)[2] = ctl.g;            // (the y warps', which the state-only pass has not)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pairs = p.groups * p.pairs_per_group;
     const int pair = blockIdx.x % pairs;
@@ -343,9 +357,9 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
             mbar_init(&ctl.wx_ready[i], kState ? 8 : 4);
             mbar_init(&ctl.ds[i], 1);
             mbar_init(&ctl.full_x[i], 1);
-            mbar_init(&ctl.full_z[i], 1);
             mbar_init(&ctl.y_done[i], 8);
         }
+        mbar_init(&ctl.full_z, 1);
         mbar_init(&ctl.s_read, 8);
         mbar_init(&ctl.cb, 1);
         mbar_init(&ctl.cs, 1);
@@ -386,28 +400,34 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
             *reinterpret_cast<uint4 *>(st + (k >> 3) * 8192 + sw128_offset(r, k & 7)) = make_uint4(0, 0, 0, 0);
         }
     };
-    // w x of chunk c by 128 threads (256 in the state-only pass), split into two bf16 terms, at buffer `xh`.
-    auto make_wx = [&](int c, int who, uint8_t *xh) {
+    // w x of chunk c by 128 threads (256 in the state-only pass), split into three bf16 terms, at buffer `to`.
+    auto make_wx = [&](int c, int who, uint8_t *to) {
         const uint8_t *xt = stage(c) + ST_X;
         const int len = chunk_len(c);
         if (len < kL) clear_rows(c, who);
         constexpr int kStep = kState ? 32 : 16;      // tokens that the threads take at once
+        const int j0 = who >> 3;
+        const uint32_t at0 = sw128_offset(j0, who & 7);
+        const float *lw = &gate[c & (NS - 1)][0].lw[j0];
 #pragma unroll 2
         for (int v = 0; v < 128 / kStep; ++v) {
-            const int u = v / (64 / kStep), j = (who >> 3) + kStep * (v % (64 / kStep));
-            const uint32_t at = u * 8192 + sw128_offset(j, who & 7);
-            const float w = j < len ? ex2(gate[c & (NS - 1)][u].lw[j]) : 0.f;
+            const int j = j0 + kStep * (v % (64 / kStep));
+            const uint32_t at = at0 + 128 * kStep * v;
+            const float w = ex2(lw[kStep * (v % (64 / kStep)) + (v < 64 / kStep ? 0 : sizeof(GateSet) / 4)]);   // unit 0's, 1's
             const uint4 xv = j < len ? *reinterpret_cast<const uint4 *>(xt + at) : make_uint4(0, 0, 0, 0);
             const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-            uint32_t hi[4], lo[4];
+            uint32_t t[3][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const F2 a = mul2(both(w), widen(xw[i]));
-                hi[i] = pack2(a);
-                lo[i] = pack2(fma2(both(-1.f), widen(hi[i]), a));
+                F2 rest = mul2(both(w), widen(xw[i]));
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    t[k][i] = pack2(rest);
+                    if (k < 2) rest = fma2(both(-1.f), widen(t[k][i]), rest);
+                }
             }
-            *reinterpret_cast<uint4 *>(xh + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(xh + 16384 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4 *>(to + k * WX_TERM + at) = make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
         }
     };
 
@@ -433,8 +453,7 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
             // operand.)
             const uint64_t dC = sw128_desc(base + ST_C, 16, 1024), dBk = sw128_desc(base + ST_B, 16, 1024),
                            dS = sw128_desc(base + O_S, 16384, 1024), dBm = sw128_desc(base + ST_B, 8192, 1024),
-                           dXH = sw128_desc(base + O_XH, 8192, 1024), dX = sw128_desc(base + ST_X, 8192, 1024),
-                           dXH1 = sw128_desc(base + O_S, 8192, 1024);
+                           dWX = sw128_desc(base + kWx<kState>, 8192, 1024), dX = sw128_desc(base + ST_X, 8192, 1024);
             auto issue_cb = [&](int c) {
                 const uint64_t st = (uint64_t)(c & (NS - 1)) * (kStageBytes<kState> >> 4);
                 if (ksteps == 8) {
@@ -461,11 +480,11 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
                                                              : wait2(ctl.full_x, c) && (c == 0 || wait(&ctl.s_read, c - 1)))))
                     break;
                 tc_fence_after();
-                const uint64_t xh = kState && (c & 1) ? dXH1 : dXH;
+                const uint64_t wx = dWX + (kState && (c & 1) ? WX_BYTES >> 4 : 0);
                 const uint32_t dst = tmem + (kState && (c & 1) ? T_CS : T_DS);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_f16(dst, dBm + st + (k & 3) * 128, xh + (k >> 2) * 1024 + (k & 3) * 128, kIdDS, k > 0);
+                for (int k = 0; k < 12; ++k)
+                    mma_f16(dst, dBm + st + (k & 3) * 128, wx + (2 - (k >> 2)) * (WX_TERM >> 4) + (k & 3) * 128, kIdDS, k > 0);      // the smallest term first
                 mma_commit(&ctl.ds[kState ? c & 1 : 0]);
                 if (kState) continue;
                 // C S, once S is in place and the accumulators of the chunk before are read.
@@ -506,30 +525,28 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
         // ------------------------------------------------------------ TMA loads
         if (lane == 0) {
             const int regions = p.N > 64 ? 2 : 1;
-            int loaded = 0, loaded_z = 0;
+            int loaded = 0, loaded_x = 0, loaded_z = 0;
             const int tile_u[2] = {64 * unit_tile(0), 64 * unit_tile(1)}, head_u[2] = {unit_head(0), unit_head(1)};
             auto row_of = [&](int c) { return (int)(it.t0 + (int64_t)c * kL); };
-            auto load_z = [&](int c) {      // (without a z that TMA can take: its place is free)
-                uint64_t *bar = &ctl.full_z[c & 1];
+            // z, or (where it does not come by TMA) word that its place is free for y.
+            auto load_z = [&](int c) {
+                if (c >= nchunks) return;
                 loaded_z = c + 1;
                 if (kZ != kZTma) {
-                    mbar_arrive(bar);
+                    mbar_arrive(&ctl.full_z);
                     return;
                 }
-                mbar_arrive_expect_tx(bar, 16384);
-                for (int u = 0; u < 2; ++u) tma_load_3d(sm + O_Z + (c & 1) * 16384 + u * 8192, &p.tm_z, tile_u[u], head_u[u], row_of(c), bar);
+                mbar_arrive_expect_tx(&ctl.full_z, 16384);
+                for (int u = 0; u < 2; ++u) tma_load_3d(sm + O_Z + u * 8192, &p.tm_z, tile_u[u], head_u[u], row_of(c), &ctl.full_z);
             };
             for (int c = 0; ok && c < nchunks + (kState ? 0 : 2); ++c) {
-                // The stage is free when the last MMA of the chunk in it is done: its S has been taken,
+                uint8_t *st = stage(c);
+                // A stage is free when the last MMA of the chunk in it is done: its S has been taken,
                 // or its y read out (x with it).  x first: w x waits for it.
-                if (c < nchunks) {
-                    if (c >= NS && !(ok = kState ? wait_st(ctl.s_ready, c - NS) : wait2(ctl.y_read, c - NS))) break;
-                    uint8_t *st = stage(c);
-                    uint64_t *bar = &ctl.full[c & (NS - 1)], *bar_x = kState ? bar : &ctl.full_x[c & 1];
-                    const int t = row_of(c);
-                    if (!kState) mbar_arrive_expect_tx(bar_x, 16384);
-                    else mbar_arrive_expect_tx(bar, 8192u * (regions + 2));
-                    for (int u = 0; u < 2; ++u) tma_load_3d(st + ST_X + u * 8192, &p.tm_x, tile_u[u], head_u[u], t, bar_x);
+                if (c >= NS && !(ok = kState ? wait_st(ctl.s_ready, c - NS) : wait2(ctl.y_read, c - NS))) break;
+                uint64_t *bar = &ctl.full[c & (NS - 1)], *bar_x = kState ? bar : &ctl.full_x[c & 1];
+                const int t = row_of(c);
+                auto load_bc = [&]() {
                     if (!kState) mbar_arrive_expect_tx(bar, 8192u * 3 * regions);
 #pragma unroll 1
                     for (int r = 0; r < regions; ++r) {
@@ -540,28 +557,39 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
                         }
                     }
                     loaded = c + 1;
+                };
+                if (c < nchunks) {
+                    if (kState) mbar_arrive_expect_tx(bar, 8192u * (regions + 2));
+                    else mbar_arrive_expect_tx(bar_x, 16384);
+                    for (int u = 0; u < 2; ++u) tma_load_3d(st + ST_X + u * 8192, &p.tm_x, tile_u[u], head_u[u], t, bar_x);
+                    loaded_x = c + 1;
+                    if (kZ != kZTma) load_bc();
                 }
                 if (kState) continue;
-                // y of chunk c - 2 has taken z's place: out with it, and the next z in.  (A sequence's last
-                // rows, where they do not fill the chunk, are stored by their threads.)
+                // y of chunk c - 2 goes out, and then what takes its place comes in: the next B, or the next y.  (A
+                // sequence's last rows, where they do not fill the chunk, are stored by their threads.)
                 if (c >= 2) {
                     if (!(ok = wait2(ctl.y_done, c - 2))) break;
+                    if (kZ == kZTma) load_z(c - 1);
                     if (chunk_len(c - 2) == kL) {
-                        for (int u = 0; u < 1 + two; ++u)
-                            tma_store_3d(&p.tm_y, sm + O_Z + (c & 1) * 16384 + u * 8192, tile_u[u], head_u[u], row_of(c - 2));
+                        uint8_t *yt = kZ == kZTma ? st + ST_B : sm + O_Z;
+                        for (int u = 0; u < 1 + two; ++u) tma_store_3d(&p.tm_y, yt + u * 8192, tile_u[u], head_u[u], row_of(c - 2));
                         bulk_commit();
                     }
-                }
-                if (c < nchunks) {
                     bulk_wait_read();
-                    load_z(c);
+                }
+                if (kZ == kZTma) {
+                    if (c == 1) load_z(0);
+                    if (c < nchunks) load_bc();
+                } else if (c > 0) {
+                    load_z(c - 1);
                 }
             }
             // Copies still in flight finish before the CTA leaves (bounded).
             for (int c = loaded - NS < 0 ? 0 : loaded - NS; c < loaded; ++c) mbar_wait(&ctl.full[c & (NS - 1)], (c / NS) & 1, kBudget);
             if (!kState) {
-                for (int c = loaded - 2 < 0 ? 0 : loaded - 2; c < loaded; ++c) mbar_wait(&ctl.full_x[c & 1], (c >> 1) & 1, kBudget);
-                for (int c = loaded_z - 2 < 0 ? 0 : loaded_z - 2; c < loaded_z; ++c) mbar_wait(&ctl.full_z[c & 1], (c >> 1) & 1, kBudget);
+                for (int c = loaded_x - 2 < 0 ? 0 : loaded_x - 2; c < loaded_x; ++c) mbar_wait(&ctl.full_x[c & 1], (c >> 1) & 1, kBudget);
+                if (loaded_z > 0) mbar_wait(&ctl.full_z, (loaded_z - 1) & 1, kBudget);
             }
             bulk_wait_all();
             if (!ok) *abort = 1;
@@ -573,7 +601,7 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
             if (!(ok = all((c == 0 || wait(&ctl.ds[0], c - 1)) && wait2(ctl.full_x, c) && (chunk_len(c) == kL || wait_st(ctl.full, c)) &&
                            wait_st(ctl.gates, c))))
                 break;
-            make_wx(c, tid - 32 * kWxWarp, sm + O_XH);
+            make_wx(c, tid - 32 * kWxWarp, sm + kWx<kState>);
             arrive(&ctl.wx_ready[c & 1], true);
         }
         if (!ok) *abort = 1;
@@ -612,8 +640,8 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
             const float2 decay = next_decay(suf, carry);      // (lane 0's is the whole chunk's)
             carry = decay.y;
             if (c >= NS && !(ok = all(wait_st(ctl.s_ready, c - NS) && (kState || wait2(ctl.y_read, c - NS))))) break;
-            Gates &G = gate[c & (NS - 1)][u];
-            *reinterpret_cast<float2 *>(&G.s[2 * lane]) = make_float2(after + g1, after);
+            GateSet &G = gate[c & (NS - 1)][u];
+            if constexpr (!kState) *reinterpret_cast<float2 *>(&G.s[2 * lane]) = make_float2(after + g1, after);
             *reinterpret_cast<float2 *>(&G.lw[2 * lane]) = make_float2(after + g1 + l0, after + l1);
             if (lane == 0) {
                 G.total = suf;
@@ -697,7 +725,7 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
         // ------------------------------------------------------------ w x of the state-only pass, two buffers
         for (int c = 0; c < nchunks; ++c) {
             if (!(ok = all(wait_st(ctl.full, c) && wait_st(ctl.gates, c) && (c < 2 || wait2(ctl.ds, c - 2))))) break;
-            make_wx(c, tid, sm + (c & 1 ? O_S : O_XH));
+            make_wx(c, tid, sm + kWx<kState> + (c & 1) * WX_BYTES);
             arrive(&ctl.wx_ready[c & 1], true);
         }
         if (!ok) *abort = 1;
@@ -711,7 +739,7 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
         // Scores of chunk c, weighted: 0 above the diagonal (all of this warp's where its
         // columns are behind its rows).
         auto make_m = [&](int c) {
-            const Gates &G = gate[c & (NS - 1)][ru];
+            const Gates &G = ygate[c & 1][ru];
             const float si = G.s[ri];
             tc_fence_after();
 #pragma unroll 1
@@ -747,11 +775,11 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
         if (nchunks > 0) next_m(0);
         for (int c = 0; ok && c < nchunks; ++c) {
             // (The last MMA of the chunk: what was issued before it, C S among it, is done too.)
-            if (!(ok = all(wait(&ctl.mx, c) && wait2(ctl.full_x, c) && wait2(ctl.full_z, c)))) break;
+            if (!(ok = all(wait(&ctl.mx, c) && wait2(ctl.full_x, c) && wait(&ctl.full_z, c)))) break;
             tc_fence_after();
-            const uint8_t *xt = stage(c) + ST_X + ru * 8192;
-            uint8_t *zt = sm + O_Z + (c & 1) * 16384 + ru * 8192;
-            const float e = ex2(gate[c & (NS - 1)][ru].total - gate[c & (NS - 1)][ru].s[ri]);
+            const uint8_t *xt = stage(c) + ST_X + ru * 8192, *zt = sm + O_Z + ru * 8192;
+            uint8_t *yt = (kZ == kZTma ? stage(c) + ST_B : sm + O_Z) + ru * 8192;
+            const float e = ex2(ygate[c & 1][ru].total - ygate[c & 1][ru].s[ri]);
             const int len = chunk_len(c);
             __nv_bfloat16 *dst = p.y + ((it.t0 + (int64_t)c * kL + ri) * p.heads + head) * (int64_t)p.P + col;
 #pragma unroll 1
@@ -762,11 +790,10 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
                 tmem_ld8(tmem + T_CS + at, cs);
                 const uint32_t piece = sw128_offset(ri, 4 * half + b);
                 const uint4 xv = *reinterpret_cast<const uint4 *>(xt + piece);
-                uint4 *place = reinterpret_cast<uint4 *>(zt + piece);
                 const int pc = 8 * b;
                 uint4 zv = make_uint4(0, 0, 0, 0);
                 if (kZ != kZNone) {
-                    if (kZ == kZTma) zv = *place;
+                    if (kZ == kZTma) zv = *reinterpret_cast<const uint4 *>(zt + piece);
                     else if (live && ri < len && col + pc < p.P)
                         zv = load_unaligned(p.z + (it.t0 + (int64_t)c * kL + ri) * p.ld_z + (int64_t)head * p.P + col + pc);
                 }
@@ -782,8 +809,8 @@ __global__ void __launch_bounds__(kThreads<kState>, 1) ssm_chunk_scan(const __gr
                     out[i] = pack2(a);
                 }
                 const uint4 o = make_uint4(out[0], out[1], out[2], out[3]);
-                // A whole chunk's y goes out by TMA, from z's place.
-                if (len == kL) *place = o;
+                // A whole chunk's y goes out by TMA.
+                if (len == kL) *reinterpret_cast<uint4 *>(yt + piece) = o;
                 else if (live && ri < len && col + pc < p.P) *reinterpret_cast<uint4 *>(dst + pc) = o;
             }
             arrive(&ctl.y_read[c & 1], false);

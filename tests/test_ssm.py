@@ -314,6 +314,18 @@ def test_gates_keep_their_digits_on_the_tensor_cores(gap):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,packed", [([700, 64, 130, 1], True), ([1600], False)])
+def test_states_of_the_tensor_cores_are_fp32(lens, packed):
+    """bf16 prompts return a state that is carried on, so its products w x B keep fp32's digits.  A token's weight w = d e^{G - G_j} is
+    off by two units of 2^-23 for its step, as much for the logarithm, log2 w's roundings (half a unit of 2^-20 below 16, times
+    ln 2) and the exponential: 8.2 x 2^-23 at most, and the products and their sums some 2^-24 at random signs."""
+    m = draw("bf16", lens, 4, 64, 2, 128, 0, packed=packed, initial=False, seed=34, gap=(-(2 * 4 * 64 + 512 + 4)) % 8)
+    shape = gdn.GdnSsmShape(1, 1, sum(lens), len(lens), 4, 64, 2, 128, m["xbc"].stride(1), 0, 0)
+    assert gdn.gdn_ssm_prefill_plan(shape, gdn.GdnSsmParams(0, 0, 0.0, 1.0))[0] in (gdn.PATH_TC, gdn.PATH_TC_TP)
+    assert rel(prefill(m)[1], define(m)[1]) <= 2.0 ** -20
+
+
+@pytest.mark.gpu
 def test_slow_decays_do_not_drift():
     """2,000 tokens that forget next to nothing.  Each rounds its decay (half a step below 1: 2^-25), the state's update
     (2^-24) and its own share (twice 2^-24, of a small part): at random, so they add up to sqrt(2000) times 2 * 2^-24 at most."""
