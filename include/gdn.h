@@ -494,7 +494,7 @@ size_t gdn_prefill_layer_workspace_bytes(const gdn_shape *shape);
  * Head h reads B and C of group h / (heads / groups).  x, B and C lie in one mixed row
  * [x (heads x head_dim) | B (groups x d_state) | C (groups x d_state)], which a short causal
  * convolution (gdn_causal_conv's, dilation 1) may cross first; its result is rounded to the
- * I/O type, as gdn_causal_conv stores it.
+ * I/O type, alike in prompts and single tokens.
  * ---------------------------------------------------------------------------------- */
 typedef struct gdn_ssm_shape {
     int32_t io_dtype;   /* gdn_dtype of xbc, dt, z, the conv's tensors and y               */
@@ -506,8 +506,8 @@ typedef struct gdn_ssm_shape {
     int32_t groups;     /* B / C groups; heads % groups == 0                               */
     int32_t d_state;    /* 1..256                                                          */
     /* Elements between the token rows of xbc, dt and z (0: contiguous), so that slices of
-       one projection's output can be given as they lie.  Row b T + t holds token t of
-       sequence b. */
+       one projection's output can be given as they lie; below a row's width they are
+       refused.  Row b T + t holds token t of sequence b. */
     int64_t xbc_stride, dt_stride, z_stride;
 } gdn_ssm_shape;
 
@@ -604,9 +604,10 @@ gdn_status gdn_rotary(const gdn_rotary_shape *shape, const void *q, const void *
 
 typedef enum {
     GDN_ROTARY_PLAIN = 0,      /* base^(-2i / rot_dim)                                       */
-    GDN_ROTARY_LINEAR = 1,     /* every frequency / factor                                   */
-    GDN_ROTARY_BASE = 2,       /* base factor^(rot_dim / (rot_dim - 2)) in base's place      */
-    GDN_ROTARY_BANDS = 3,      /* / factor below `low` turns over trained_length, as it is above
+    GDN_ROTARY_LINEAR = 1,     /* every frequency / factor (position interpolation)          */
+    GDN_ROTARY_BASE = 2,       /* base factor^(rot_dim / (rot_dim - 2)) in base's place
+                                  (NTK-aware scaling)                                        */
+    GDN_ROTARY_BANDS = 3,      /* (YaRN) / factor below `low` turns over trained_length, as it is above
                                   `high` turns, a ramp over the indices between; scale
                                   0.1 ln(factor) + 1                                         */
     GDN_ROTARY_WAVELENGTH = 4  /* / factor below `low` turns, as it is above `high`, a ramp over

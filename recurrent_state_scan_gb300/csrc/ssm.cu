@@ -26,8 +26,8 @@ constexpr int kRun = 33, kAhead = 3;
 // Rows of a run: as many runs as fill the SMs, six CTAs to each, in whole waves of runs of up to
 // `most` rows, in whole stages.  (Runs of 72 rows: 2,002 rows of 1,792 f16 channels took 29 us, in
 // runs of 12 by bulk copies below 12 us; 1,045 f32 rows of 704 channels here 27.5 us in runs of 33, 7.6
-// in runs of 3, although each run reads K - 1 rows more.  A prompt of 8,192 rows of 4,352 channels
-// took 213 us in runs of 72, a wave and a bit, and 205 in runs of 84, one wave.)
+// in runs of 3, although each run reads K - 1 rows more.  8,192 rows of 4,352 channels take
+// 8 us more in runs of 72, a wave and a bit, than in runs of 84, one wave.)
 int rows_of_run(int64_t rows, int64_t across, int most, int stage) {
     const int64_t work = rows * across, wave = 6 * kSms, waves = (work + most * wave - 1) / (most * wave);
     const int64_t run = waves == 0 ? stage : (work + waves * wave - 1) / (waves * wave);
@@ -441,7 +441,7 @@ cudaError_t conv_dispatch(const SsmConvParams &p, cudaStream_t stream) {
 // eight lanes' partial readouts of a batch are summed by a reduce-scatter (seven shuffles for
 // eight tokens), after which lane slice s owns token s.
 // Bound by issue and latency: 2 x 1,001 f16 tokens of 24 heads of 64 columns x 128 rows take
-// 133 us, 250 cycles a token, on SMs with four or eight warps each; there is no more parallelism
+// 139 us, 260 cycles a token, on SMs with four or eight warps each; there is no more parallelism
 // than columns without cutting time.
 constexpr int kBatch = 8, kCols = 16, kScanThreads = 128;
 
@@ -693,8 +693,8 @@ __global__ void __launch_bounds__(kDecThreads, 4) ssm_decode_kernel(const SsmDec
 // copies in both directions.  The convolved B and C of a (row, group) are kept for all of its
 // heads, and the next unit's inputs are loaded while this one is computed.  Two CTAs to an SM
 // keep 128 KB of loads in flight.  Bound by reading and writing the states: 256 rows of 64 heads of
-// 64 x 128 take 182 us (6.0 TB/s of a copy's 6.8); the call took 253 us with the kernel above, and
-// 200 with this one.
+// 64 x 128 take 169 us (6.4 TB/s of a copy's 6.8); the call took 253 us with the kernel above, and takes
+// 179 with this one.
 constexpr int kStreamState = 8192, kRing = 3, kSlots = 3;
 
 template <typename IO>

@@ -17,16 +17,16 @@
 //   w x split into three bf16 terms -> the sum of B^T [term] -> S = e^{G_L} S + ..     by the S warps
 // The warps' roles run side by side, a chunk apart where the data allows it.
 //
-// Bound by the chain from one chunk's y to the next (readout, M, its MMA) and by issue: a pair of
-// units takes 2.55 us a chunk (2.85 with z), of which the tensor pipe works a quarter, the issue slots
-// about half and shared memory about half.  8,192 tokens of 64 heads of 64 x 128 with z: 92 us on
-// 128 CTAs, behind 39 us of state-only pass and 5 us for the segments' states.
+// Bound by the chain from one chunk's y to the next (the state's product, C S, M x, readout) and by issue: a pair
+// of units takes 2.4 us a chunk along a long sequence (3.1 with z over 32 chunks, what comes before the first and
+// behind the last included), of which the tensor pipe works a third, the issue slots about half and shared
+// memory more than half.  8,192 tokens of 64 heads of 64 x 128 with z: 102 us on 128 CTAs, behind 45 us of
+// state-only pass and 6 us for the segments' states.
 // Precision: the state is fp32 and its update's operands are exact (B) or a three-term bf16 split (w x, to
 // fp32's own 2^-24), because the state is returned in fp32 and carried on: it is 1.1e-7 off, as 32-bit
 // arithmetic is, where two terms left it 2.4e-6 off (in 3 to 7% less time).  M and the S that C reads are
 // rounded once to bf16, half a step (2^-9 of each term's size at random signs), under the one rounding that
-// y meets itself.  f16 stays on the FP32 cores: w x and M
-// leave its range.
+// y meets itself.  f16 stays on the FP32 cores: w x and M leave its range.
 //
 // Where sequences x units leave most SMs idle, each sequence is cut along time: a state-only
 // pass of every segment but the last from zero, a short pass that turns the segments' ends into
@@ -130,7 +130,7 @@ __device__ __forceinline__ F2 widen(uint32_t v) { return {lo_f(v), hi_f(v)}; }
 __device__ __forceinline__ uint32_t pack2(F2 a) { return pack2(a.x, a.y); }
 // a silu(z) for two values.  Below z = -87.3 the reciprocal is subnormal and flushed: the gate is 0 where
 // silu is within 1.1e-36 of it.  (One reciprocal for both, 1 / d0 = d1 / (d0 d1), needs the exponents held
-// down: at z >= -41 the gates below were wrong by orders, by e^-|z| 8,192 tokens took 183 us, not 181.)
+// down: with z held at -41 the gates below it were wrong by orders, and by way of e^-|z| 8,192 tokens took 1% longer.)
 __device__ __forceinline__ F2 gated(F2 a, F2 z) {
     const F2 t = mul2(z, both(-kLog2e)), d = add2({ex2(t.x), ex2(t.y)}, both(1.f));
     return mul2(a, mul2(z, {rcp(d.x), rcp(d.y)}));
@@ -183,7 +183,7 @@ __device__ __noinline__ float step_of(uint32_t bits, float bias, float lo, float
 // that forgets slowly is multiplied by many of them, and ex2.approx is off to one side (65,536
 // tokens, 1,024 chunks: the state 6e-6 off, 3e-5 where all steps are alike).  So slow ones are 1 + x + .. +
 // x^5 / 5! (x = total ln 2; the rest is below 6e-9), and what 1 + .. rounds away goes into the next one.
-// (Out of line, as the waits are: inlined, 65,536 rows took 733 us instead of 712.)
+// (Out of line, as the waits are: inlined, 65,536 rows took 3% longer.)
 __device__ __noinline__ float2 next_decay(float total, float carry) {
     const float x = total * 0.69314718f;
     if (x < -0.125f) return make_float2(ex2(total), 0.f);
@@ -231,7 +231,7 @@ __device__ __forceinline__ Item item_at(const TcParams &p, int64_t place) {
 
 // The items of packed sequences in order, the long ones first: more of them than SMs are then
 // done soonest.  Six sequences of 4,096 to 20,480 tokens on 32 unit pairs took 1,180 us in their
-// own order and cut at a fair share, 892 us like this (and 713 by now).  Sequences are cut along time
+// own order and cut at a fair share, 892 us like this (and 773 by now).  Sequences are cut along time
 // only where one is long enough to be worth the state-only pass.  By one block: the
 // segments but each sequence's last in the first bin, which are all that the state-only pass needs,
 // the others in bins of a quarter of an octave of their chunks.  Atomics place the items of a bin,
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kOrderThreads) ssm_order(const __grid_constant
 //   0-7    y: M from the scores, and the readout (row 32 (warp % 4) + lane, 32 columns of it)
 //   8-15   S: the state (its row n, the 64 columns of one unit, in registers)
 //   16     issues the MMAs     17  issues the TMA copies     18, 19  the gates of unit 0, 1; the
-//          state-only pass, which they bound (46 us), has 20, 21 for its odd chunks (41 us)
+//          state-only pass, which two of them bound (46 us, then 41), has 20, 21 for its odd chunks
 //   20-23  w x (the state-only pass leaves it to warps 0-7).  With the S warps making it, behind the
 //          state's update, they held the others up: 3.09 us a chunk, then 2.87.
 constexpr int kSWarp = 8, kIssueWarp = 16, kLoadWarp = 17, kGateWarp = 18, kWxWarp = 20;
@@ -880,8 +880,8 @@ int unit_pairs(int heads, int groups, int head_dim) {
     return groups * ((units + 1) / 2);
 }
 
-// A state-only chunk takes 0.45 of a whole one, so cutting into the SMs' fair shares costs 1.45 of
-// one at least, and up to 1.9 with rests: uncut sequences of up to kCutOver shares are as good.
+// A state-only chunk takes 0.45 (with z) to 0.57 of a whole one, so cutting into the SMs' fair shares costs
+// 1.5 of one at least, and up to 2 with rests: uncut sequences of up to kCutOver shares are as good.
 constexpr int kSms = 152, kMinSegChunks = 8;
 constexpr double kCutOver = 1.6;
 

@@ -951,7 +951,7 @@ def gdn_ssm_prefill(xbc, dt, A_log, *, heads: int, head_dim: int, d_state: int, 
 
     xbc [B, T, C], C = heads head_dim + 2 groups d_state, rows [x | B | C]; dt [B, T, heads]; z
     [B, T, heads, head_dim] or None: token rows may be slices of wider ones (contiguous in
-    themselves, evenly spaced).  With cu_seqlens (int32 [N + 1]) B is 1 and T the packed total.
+    themselves, evenly spaced, none over another: copy an expanded tensor).  With cu_seqlens (int32 [N + 1]) B is 1 and T the packed total.
     conv_weight [C, 1, K] (K <= 4) and conv_bias [C], or None: xbc is taken as it is.
     conv_state_in [N, K - 1, C], state_in [N, heads, d_state, head_dim] fp32: zeros when None.
     A_log, dt_bias, D [heads] fp32.  Returns (y [B, T, heads, head_dim], state_out,
@@ -1038,9 +1038,10 @@ def gdn_ssm_decode(xbc, dt, A_log, state, *, heads: int, head_dim: int, d_state:
 # ------------------------------------------------------------------ rotary positions
 def gdn_rotary_frequencies(rot_dim: int, base: float = 10000.0, kind: str = "plain", *, factor: float = 1.0,
                            trained_length: float = 0.0, low: float = 1.0, high: float = 32.0, device=None):
-    """(inv_freq [rot_dim / 2] fp32, scale) for gdn_rotary: 'plain'; 'linear' (positions / factor);
-    'base' (the base grown by factor); 'bands' and 'wavelength' (frequencies that turn less than
-    `low` times over trained_length divided by factor, those above `high` times kept)."""
+    """(inv_freq [rot_dim / 2] fp32, scale) for gdn_rotary: 'plain'; 'linear' (positions / factor:
+    position interpolation); 'base' (the base grown by factor: NTK-aware scaling); 'bands' (YaRN) and
+    'wavelength' (frequencies that turn less than `low` times over trained_length divided by factor,
+    those above `high` times kept, a ramp between, over the indices or over the turns)."""
     if kind not in ROTARY_KINDS:
         raise GdnError(GDN_ERR_INVALID_ARG, f"kind must be one of {sorted(ROTARY_KINDS)}")
     inv_freq = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float32)
