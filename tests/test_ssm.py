@@ -9,8 +9,8 @@ a rounding spread evenly over half a step each way:
   two: 2 sqrt(3) q = 2 u.
 * The fp32 state and fp32 y: sums of up to T = 700 terms in fp32 whose errors add as at most
   T u = 4e-5 in the worst case and sqrt(T) u = 1.6e-6 as they fall; exp and log1p add 2 ulp a
-  step on exponents up to 16: 1e-5 bounds both, and the two-term bf16 split of the tensor
-  cores (2^-16 of each product, at random signs) stays inside it.
+  step on exponents up to 16: 1e-5 bounds both, and the three-term bf16 split of the tensor
+  cores (2^-24 of each product) stays inside it.
 * Behind a convolution in a 16-bit type, x and B are roundings of an fp32 value whose own error, some
   8 x 2^-24 of it, puts it on the other side of a rounding's border than the 64-bit value with
   probability 2 x 8 x 2^-24 over a step (bf16 2^-8, f16 2^-11 at least): p = 2^-12, 2^-9.  It is then
