@@ -24,7 +24,7 @@
 // state-only pass and 6 us for the segments' states.
 // Precision: the state is fp32 and its update's operands are exact (B) or a three-term bf16 split (w x, to
 // fp32's own 2^-24), because the state is returned in fp32 and carried on: it is 1.1e-7 off, as 32-bit
-// arithmetic is, where two terms left it 2.4e-6 off (in 3 to 7% less time).  M and the S that C reads are
+// arithmetic is, where two terms left it 2.4e-6 off (in 3 to 8% less time).  M and the S that C reads are
 // rounded once to bf16, half a step (2^-9 of each term's size at random signs), under the one rounding that
 // y meets itself.  f16 stays on the FP32 cores: w x and M leave its range.
 //
