@@ -48,7 +48,10 @@
  * gdn_prefill_layer_workspace_bytes), and the neighbouring state-space layer:
  * gdn_ssm_prefill (with gdn_ssm_prefill_workspace_bytes and gdn_ssm_prefill_plan) and
  * gdn_ssm_decode, with
- * gdn_rotary and gdn_rotary_frequencies for positions.
+ * gdn_rotary and gdn_rotary_frequencies for positions; the diagonal recurrence, forward and
+ * backward: gdn_diag_prefill, gdn_diag_backward and gdn_diag_decode (with
+ * gdn_diag_kept_bytes and gdn_diag_backward_workspace_bytes), and the 8-bit checkpoints of
+ * rows that it can train from: gdn_checkpoint_pack and gdn_checkpoint_unpack.
  *  - gdn_last_error_message() gives a human-readable detail of the last
  *    non-OK status returned on the calling thread.
  */
@@ -566,6 +569,106 @@ gdn_status gdn_ssm_decode(const gdn_ssm_shape *shape, const gdn_ssm_params *para
                           const void *z, const void *conv_weight, const void *conv_bias, void *conv_state,
                           const float *A_log, const float *dt_bias, const float *D, float *state, int64_t pool_size,
                           const int32_t *slots, void *y, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * The diagonal recurrence: a gated linear recurrence whose state is one fp32 value per
+ * channel.  For every sequence, for each token in order,
+ *     g_t     = -exp(A_log) softplus(a_t + a_bias)      (gate SOFTPLUS: gdn's own decay)
+ *             | -exp(A_log) sigmoid(a_t + a_bias)       (gate SIGMOID)
+ *     alpha_t = exp(g_t),   i_t = sigmoid(b_t + b_bias) (1 without an input gate)
+ *     w_t     = 1 | 1 - alpha_t | sqrt(1 - alpha_t^2)   (weighting PLAIN | COMPLEMENT | NORM)
+ *     h_t     = alpha_t h_{t-1} + w_t i_t x_t,   y_t = h_t
+ * elementwise over the channels, in fp32; y is rounded once.  Results are the same bits on
+ * every call.
+ *
+ * For training the forward pass keeps what the backward pass needs beside its own inputs:
+ * h before every 64th row (rows counted over the whole call), and with GDN_DIAG_KEEP_8BIT
+ * x, a and b as well, as the 8-bit codes of gdn_checkpoint_pack.  The backward pass then
+ * takes the gradient at the values that the codes hold, h running on from each kept state.
+ * ---------------------------------------------------------------------------------- */
+typedef enum { GDN_DIAG_SOFTPLUS = 0, GDN_DIAG_SIGMOID = 1 } gdn_diag_gate;
+typedef enum { GDN_DIAG_PLAIN = 0, GDN_DIAG_COMPLEMENT = 1, GDN_DIAG_NORM = 2 } gdn_diag_weighting;
+typedef enum { GDN_DIAG_KEEP_NONE = 0, GDN_DIAG_KEEP_STATES = 1, GDN_DIAG_KEEP_8BIT = 2 } gdn_diag_keep;
+
+typedef struct gdn_diag_shape {
+    int32_t io_dtype;   /* gdn_dtype of x, a, b, y and their gradients                     */
+    int32_t batch;      /* B; must be 1 when cu_seqlens is given                           */
+    int64_t seqlen;     /* T per sequence, or the packed token total with cu_seqlens       */
+    int32_t num_seqs;   /* N: equals batch, or len(cu_seqlens) - 1 with cu_seqlens         */
+    int32_t channels;   /* C, 1 .. 4,194,240                                               */
+    int32_t gate;       /* gdn_diag_gate                                                   */
+    int32_t weighting;  /* gdn_diag_weighting                                              */
+    int32_t input_gate; /* 1: b is given; 0: i_t = 1, b, b_bias, db and db_bias unused     */
+    int32_t keep;       /* gdn_diag_keep (unread by gdn_diag_decode)                       */
+    /* Elements between token rows (0: contiguous), so that slices of wider rows can be
+       given; below C they are refused.  Row b T + t holds token t of sequence b.  y_stride
+       is dy's too; the last three are the backward pass's. */
+    int64_t x_stride, a_stride, b_stride, y_stride, dx_stride, da_stride, db_stride;
+} gdn_diag_shape;
+
+/*
+ * gdn_diag_prefill -- whole sequences.
+ *   x, a, b      [rows, C], each with its own row stride; y likewise.
+ *   A_log        [C] fp32; a_bias, b_bias [C] fp32 or NULL (zeros).
+ *   state_in     [N, C] fp32 or NULL (zeros); state_out [N, C], may be state_in itself.
+ *   cu_seqlens   as gdn_prefill, but with any malformed entry the call writes nothing (and
+ *                sets the device check word).  A sequence with no tokens keeps its state.
+ *   kept         gdn_diag_kept_bytes(shape) bytes, 16-byte aligned (unread with KEEP_NONE).
+ * An infinity or a NaN reaches the rest of its channel and sequence, no other.  Outputs may
+ * not overlap inputs or one another (slices of one wider row, side by side, do not).
+ */
+size_t gdn_diag_kept_bytes(const gdn_diag_shape *shape);
+
+gdn_status gdn_diag_prefill(const gdn_diag_shape *shape, const void *x, const void *a, const void *b, const float *A_log,
+                            const float *a_bias, const float *b_bias, const float *state_in, const int32_t *cu_seqlens, void *y,
+                            float *state_out, void *kept, size_t kept_bytes, void *stream);
+
+/*
+ * gdn_diag_backward -- the gradients of sum(y dy) + sum(state_out dstate_out), at the
+ * arguments of the forward call (the same shape, parameters, state_in and cu_seqlens).
+ *   x, a, b      the forward pass's (unread with KEEP_8BIT); kept: what it kept.
+ *   dy           [rows, C]; dstate_out [N, C] fp32 or NULL (zeros).
+ *   dx, da, db   [rows, C], each with its own row stride.
+ *   dA_log, da_bias, db_bias [C], dstate_in [N, C]: fp32, each may be NULL (not wanted).
+ *   workspace    gdn_diag_backward_workspace_bytes(shape) bytes, 16-byte aligned; its
+ *                contents need no initialisation and are not preserved.
+ * Sums run in a fixed order: the same bits on every call.  At alpha_t = 1 the gradient of
+ * w_t (NORM), which has no bound there, counts as 0.
+ */
+size_t gdn_diag_backward_workspace_bytes(const gdn_diag_shape *shape);
+
+gdn_status gdn_diag_backward(const gdn_diag_shape *shape, const void *x, const void *a, const void *b, const float *A_log,
+                             const float *a_bias, const float *b_bias, const float *state_in, const int32_t *cu_seqlens,
+                             const void *kept, size_t kept_bytes, const void *dy, const float *dstate_out, void *dx, void *da, void *db,
+                             float *dA_log, float *da_bias, float *db_bias, float *dstate_in, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_diag_decode -- one token per row (seqlen 1, batch = num_seqs), the states in place.
+ *   state        [E, C] fp32, E = pool_size with slots, else batch: row b advances entry
+ *                slots[b] (DEVICE int32 [batch]), or entry b when slots is NULL.  The rows
+ *                should name distinct entries: what a repeated entry, or a row that names
+ *                one, holds afterwards is unspecified.  A slot outside [0, pool_size) skips
+ *                its row (y and the state as they were) and sets the device check word.
+ */
+gdn_status gdn_diag_decode(const gdn_diag_shape *shape, const void *x, const void *a, const void *b, const float *A_log,
+                           const float *a_bias, const float *b_bias, float *state, int64_t pool_size, const int32_t *slots, void *y,
+                           void *stream);
+
+/*
+ * gdn_checkpoint_pack -- rows [rows, channels] (x_stride elements apart, 0: contiguous) as
+ * codes [rows, channels] and steps [rows, ceil(channels / 64)], both contiguous.  A step is
+ * the power of two 2^(s - 133), the least (s >= 16) at which its block's 64 channels of one
+ * row round to codes within 127; a code is the value over its step, rounded to the nearest
+ * integer, ties to even.  A block that holds an infinity or a NaN gets the step 255 and is
+ * read back as NaN.
+ * gdn_checkpoint_unpack -- the values code * 2^(s - 133) again: exact in bf16 and fp32, held
+ * to the largest finite value in f16 (y_stride elements apart, 0: contiguous).
+ */
+gdn_status gdn_checkpoint_pack(int32_t io_dtype, int64_t rows, int64_t channels, const void *x, int64_t x_stride, int8_t *codes,
+                               uint8_t *steps, void *stream);
+gdn_status gdn_checkpoint_unpack(int32_t io_dtype, int64_t rows, int64_t channels, const int8_t *codes, const uint8_t *steps, void *y,
+                                 int64_t y_stride, void *stream);
 
 /* ------------------------------------------------------------------------------------
  * Rotary positions, for q and k of a linear or gated rule, or C and B of a state-space

@@ -1,0 +1,413 @@
+// diag_internal.cuh -- what the diagonal recurrence's translation units share: its arguments, its gates,
+// the 8-bit codes, the sequences' edges among a warp's rows, and the exchange inside a cluster.
+#pragma once
+
+#include "ssm_internal.cuh"
+
+namespace gdn {
+
+constexpr int kDiagTile = 64;    // token rows between two kept states, and of one CTA's step
+constexpr int kDiagSlice = 64;   // channels of one CTA, and of a block of the 8-bit codes
+
+// One call (validated arguments).  Token rows are those of the whole call: t of sequence b at
+// b * seqlen + t, or the packed index.  Row strides in elements.
+struct DiagParams {
+    const void *x, *a, *b;
+    bool has_b;                          // else the input gate is 1
+    int64_t ld_x, ld_a, ld_b, ld_y;      // ld_y: y's and dy's rows
+    const float *A_log, *a_bias, *b_bias;   // the biases may be null
+    const float *state_in;               // may be null (zeros); may alias state_out
+    float *state_out;
+    void *y;
+    const int32_t *cu_seqlens;           // may be null
+    int64_t seqlen, rows;
+    int32_t num_seqs, channels;
+    int32_t parts;                       // stretches of whole sequences that run side by side
+    bool pairs;                          // every row can be read and written two channels at a time
+    int *status;
+    // What the forward pass keeps for the backward pass.
+    float *kept;                         // [tiles][slices * 64] or null: h before each tile's first row
+    int8_t *codes;                       // [x | a | b][slice][rows][64] or null
+    uint8_t *steps;                      // [x | a | b][slice][rows]
+    // The backward pass.
+    const void *dy;
+    const float *dstate_out;             // may be null (zeros)
+    void *dx, *da, *db;
+    int64_t ld_dx, ld_da, ld_db;
+    float *dA_log, *da_bias, *db_bias, *dstate_in;   // each may be null
+    float *partial;                      // [parts][3][channels]: sums of the parameters' gradients, with several parts
+};
+
+struct DiagDecodeParams {
+    const void *x, *a, *b;
+    bool has_b;
+    int64_t ld_x, ld_a, ld_b, ld_y;
+    const float *A_log, *a_bias, *b_bias;
+    float *state;                        // [pool][channels], in place
+    int64_t pool_size;
+    const int32_t *slots;                // may be null
+    void *y;
+    int32_t batch, channels;
+    bool vec;                            // four channels at a time
+    int *status;
+};
+
+int diag_slices(int channels);
+int diag_cluster(int64_t rows);
+int diag_parts(int64_t rows, int64_t num_seqs, int channels);
+cudaError_t launch_diag_prefill(const DiagParams &p, gdn_dtype io, int gate, int weighting, cudaStream_t stream);
+cudaError_t launch_diag_backward(const DiagParams &p, gdn_dtype io, int gate, int weighting, cudaStream_t stream);
+cudaError_t launch_diag_decode(const DiagDecodeParams &p, gdn_dtype io, int gate, int weighting, cudaStream_t stream);
+cudaError_t launch_checkpoint_pack(gdn_dtype io, int64_t rows, int64_t channels, const void *x, int64_t ld, int8_t *codes,
+                                   uint8_t *steps, cudaStream_t stream);
+cudaError_t launch_checkpoint_unpack(gdn_dtype io, int64_t rows, int64_t channels, const int8_t *codes, const uint8_t *steps,
+                                     void *y, int64_t ld, cudaStream_t stream);
+
+#ifdef __CUDACC__
+// ------------------------------------------------------------------ gates
+// alpha - 1 = e^g - 1 for g <= 0.  Slow decays are multiplied in thousands of times and weigh their
+// input by 1 - alpha, so both alpha and its distance from 1 have to keep their digits: down to -1/4 by
+// g + g^2 p(g), p the Chebyshev fit of (e^g - 1 - g) / g^2 (1.2e-8 of the result), whose sum with 1 is
+// then rounded once; below by the exponential, within 4e-7 of the distance.
+__device__ __forceinline__ F2 diag_expm1(F2 g, F2 &alpha) {
+    F2 p = fma2(both(0x1.f6d2c6p-8f), g, both(0x1.548062p-5f));
+    p = fma2(p, g, both(0x1.5552b2p-3f));
+    p = fma2(p, g, both(0x1.fffffep-2f));
+    const F2 near = fma2(mul2(g, g), p, g), t = mul2(g, both(kLog2e)), one = both(1.f);
+    const F2 far = {ex2(t.x), ex2(t.y)}, a = add2(near, one), m = add2(far, both(-1.f));
+    const bool nx = g.x > -0.25f, ny = g.y > -0.25f;
+    alpha = {nx ? a.x : far.x, ny ? a.y : far.y};
+    return {nx ? near.x : m.x, ny ? near.y : m.y};
+}
+// sigmoid(v + bias); `nbias` is -bias log2 e.  e^-v beyond fp32's range gives 0.
+__device__ __forceinline__ F2 diag_sigmoid(F2 v, F2 nbias) {
+    const F2 t = fma2(v, both(-kLog2e), nbias);
+    const F2 d = add2({ex2(t.x), ex2(t.y)}, both(1.f));
+    return {rcp(d.x), rcp(d.y)};
+}
+// softplus(z) = max(z, 0) + log(1 + e), e = e^-|z|, and sigmoid(z).  log(1 + e) = 2 atanh(s), s = e / (2 + e)
+// <= 1/3, by s + s^3 q(s^2), q the Chebyshev fit of the series of atanh (1.6e-8 of the result): digits
+// are kept however small e is.
+__device__ __forceinline__ F2 diag_softplus(F2 z) {
+    const F2 e = {ex2(-kLog2e * fabsf(z.x)), ex2(-kLog2e * fabsf(z.y))}, d = add2(e, both(2.f));
+    const F2 s = mul2(e, {rcp(d.x), rcp(d.y)}), q = mul2(s, s);
+    F2 p = fma2(both(0x1.131faap-3f), q, both(0x1.211da0p-3f));
+    p = fma2(p, q, both(0x1.99adb6p-3f));
+    p = fma2(p, q, both(0x1.55554cp-2f));
+    const F2 l = fma2(mul2(s, q), p, s);
+    return fma2(l, both(2.f), {z.x < 0.f ? 0.f : z.x, z.y < 0.f ? 0.f : z.y});   // (a NaN stays one)
+}
+
+// The parameters of a lane's two channels.
+struct DiagLane {
+    F2 rate, abias, nabias, nbbias;   // -e^A_log, a_bias, -a_bias log2 e, -b_bias log2 e
+};
+// What one token's gates give: g and alpha - 1, alpha, sigmoid(a + a_bias) (the softplus gate: only where
+// `grad` is set), the input gate and the input's weight w (norm: and 1 / w).
+struct DiagGates {
+    F2 g, m, alpha, s, i, w, winv;
+};
+
+template <int WEIGHT> __device__ __forceinline__ void diag_weigh(DiagGates &o) {
+    o.winv = both(0.f);
+    if (WEIGHT == GDN_DIAG_NORM) {          // sqrt(1 - alpha^2); at alpha = 1 the weight is 0 and 1 / w finite
+        const F2 q = mul2({-o.m.x, -o.m.y}, add2(o.m, both(2.f)));
+        asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(o.winv.x) : "f"(fmaxf(q.x, 0x1p-122f)));
+        asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(o.winv.y) : "f"(fmaxf(q.y, 0x1p-122f)));
+        o.w = mul2(q, o.winv);
+    } else if (WEIGHT == GDN_DIAG_COMPLEMENT) {
+        o.w = {-o.m.x, -o.m.y};
+    } else {
+        o.w = both(1.f);
+    }
+}
+
+template <int GATE, int WEIGHT, bool GRAD>
+__device__ __forceinline__ DiagGates diag_gates(F2 a, F2 b, bool has_b, const DiagLane &l) {
+    DiagGates o;
+    if (GATE == GDN_DIAG_SIGMOID) {
+        o.s = diag_sigmoid(a, l.nabias);
+        o.g = mul2(l.rate, o.s);
+    } else {
+        if (GRAD) o.s = diag_sigmoid(a, l.nabias);
+        o.g = mul2(l.rate, diag_softplus(add2(a, l.abias)));
+    }
+    // Held finite: an alpha of 0 times it is then 0, not a NaN (a NaN itself stays one).
+    o.g = {o.g.x < -1e30f ? -1e30f : o.g.x, o.g.y < -1e30f ? -1e30f : o.g.y};
+    o.m = diag_expm1(o.g, o.alpha);
+    o.i = has_b ? diag_sigmoid(b, l.nbbias) : both(1.f);
+    diag_weigh<WEIGHT>(o);
+    return o;
+}
+
+__device__ __forceinline__ DiagLane diag_lane(const float *A_log, const float *a_bias, const float *b_bias, int64_t c, int64_t C) {
+    DiagLane l{};
+    const bool one = c < C, two = c + 1 < C;
+    l.rate = {one ? ssm_rate(A_log[c]) : 0.f, two ? ssm_rate(A_log[c + 1]) : 0.f};
+    if (a_bias) l.abias = {one ? a_bias[c] : 0.f, two ? a_bias[c + 1] : 0.f};
+    F2 bb = both(0.f);
+    if (b_bias) bb = {one ? b_bias[c] : 0.f, two ? b_bias[c + 1] : 0.f};
+    l.nabias = mul2(l.abias, both(-kLog2e));
+    l.nbbias = mul2(bb, both(-kLog2e));
+    return l;
+}
+
+// ------------------------------------------------------------------ rows, two channels at a time
+template <typename IO> struct Pair;      // a lane's two channels of one row, as they lie in memory
+template <> struct Pair<float> {
+    using Raw = float2;
+    static __device__ __forceinline__ F2 wide(Raw v) { return {v.x, v.y}; }
+    static __device__ __forceinline__ Raw narrow(F2 v) { return make_float2(v.x, v.y); }
+    static __device__ __forceinline__ Raw load(const float *p) {
+        Raw v;
+        asm("ld.global.nc.L1::no_allocate.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p));
+        return v;
+    }
+    static __device__ __forceinline__ Raw join(float a, float b) { return make_float2(a, b); }
+};
+template <> struct Pair<__nv_bfloat16> {
+    using Raw = uint32_t;
+    static __device__ __forceinline__ F2 wide(Raw v) { return {__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)}; }
+    static __device__ __forceinline__ Raw narrow(F2 v) {
+        Raw r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+        return r;
+    }
+    static __device__ __forceinline__ Raw load(const __nv_bfloat16 *p) {
+        Raw v;
+        asm("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(v) : "l"(p));
+        return v;
+    }
+    static __device__ __forceinline__ Raw join(__nv_bfloat16 a, __nv_bfloat16 b) {
+        return (uint32_t)__bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16;
+    }
+};
+template <> struct Pair<__half> {
+    using Raw = uint32_t;
+    static __device__ __forceinline__ F2 wide(Raw v) {
+        const __half2 h = *reinterpret_cast<const __half2 *>(&v);
+        const float2 f = __half22float2(h);
+        return {f.x, f.y};
+    }
+    static __device__ __forceinline__ Raw narrow(F2 v) {
+        Raw r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+        return r;
+    }
+    static __device__ __forceinline__ Raw load(const __half *p) {
+        Raw v;
+        asm("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(v) : "l"(p));
+        return v;
+    }
+    static __device__ __forceinline__ Raw join(__half a, __half b) {
+        return (uint32_t)__half_as_ushort(a) | (uint32_t)__half_as_ushort(b) << 16;
+    }
+};
+
+// `n` rows from row r0 on, those outside [lo, hi) as zeros; `fast`: the slice is whole and lies on pairs.
+template <typename IO, int N>
+__device__ __forceinline__ void load_rows(typename Pair<IO>::Raw (&v)[N], const IO *base, int64_t ld, int64_t r0, int64_t lo,
+                                          int64_t hi, int64_t c, int64_t C, bool fast) {
+    const typename Pair<IO>::Raw zero{};
+    const IO *p = base + r0 * ld + c;
+    if (fast) {
+#pragma unroll
+        for (int t = 0; t < N; ++t) v[t] = r0 + t >= lo && r0 + t < hi ? Pair<IO>::load(p + t * ld) : zero;
+    } else {
+        const IO none = IO(0.f);
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+            const bool row = r0 + t >= lo && r0 + t < hi;
+            v[t] = Pair<IO>::join(row && c < C ? p[t * ld] : none, row && c + 1 < C ? p[t * ld + 1] : none);
+        }
+    }
+}
+template <typename IO>
+__device__ __forceinline__ void store_pair(IO *p, F2 v, int64_t c, int64_t C, bool fast) {
+    if (fast) {
+        *reinterpret_cast<typename Pair<IO>::Raw *>(p) = Pair<IO>::narrow(v);
+    } else {
+        if (c < C) IoType<IO>::st(p, v.x);
+        if (c + 1 < C) IoType<IO>::st(p + 1, v.y);
+    }
+}
+__device__ __forceinline__ F2 load_state(const float *p, int64_t c, int64_t C) {
+    return {c < C ? p[c] : 0.f, c + 1 < C ? p[c + 1] : 0.f};
+}
+__device__ __forceinline__ void store_state(float *p, F2 v, int64_t c, int64_t C) {
+    if (c < C) p[c] = v.x;
+    if (c + 1 < C) p[c + 1] = v.y;
+}
+
+// ------------------------------------------------------------------ 8-bit codes
+// The step of a block whose largest magnitude has the bits `most`: 2^(e - 133), e in [16, 254], the least
+// power of two that keeps rint(most / step) at 127 or below; 255: the block holds an infinity or a NaN.
+// (Adding 2^16 carries into the exponent from 255/128 of a power of two on.)
+__device__ __forceinline__ uint32_t code_step(uint32_t most) {
+    if (most >= 0x7f800000u) return 255u;
+    const uint32_t e = (most + 0x10000u) >> 23;
+    return e < 16u ? 16u : e > 254u ? 254u : e;
+}
+__device__ __forceinline__ float code_scale(uint32_t e) { return e == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((e - 6u) << 23); }
+__device__ __forceinline__ float code_inverse(uint32_t e) { return e == 255u ? 0.f : __uint_as_float((260u - e) << 23); }
+__device__ __forceinline__ int code_of(float v, float inverse) {
+    const int q = __float2int_rn(v * inverse);
+    return q > 127 ? 127 : q < -127 ? -127 : q;
+}
+__device__ __forceinline__ uint32_t magnitude(F2 v) {
+    const uint32_t a = __float_as_uint(v.x) & 0x7fffffffu, b = __float_as_uint(v.y) & 0x7fffffffu;
+    return a > b ? a : b;
+}
+
+// ------------------------------------------------------------------ the sequences among the rows
+// Row where sequence n begins (n = num_seqs: the end of the rows).
+__device__ __forceinline__ uint32_t seq_begin(const DiagParams &p, int n) {
+    return p.cu_seqlens ? (uint32_t)p.cu_seqlens[n] : (uint32_t)(n * p.seqlen);
+}
+// Whether cu_seqlens is what it has to be, looked at by all threads of the CTA alike; if not, the call does nothing.
+__device__ __forceinline__ bool offsets_ok(const DiagParams &p) {
+    if (p.cu_seqlens == nullptr) return true;
+    bool bad = false;
+    for (int n = threadIdx.x; n <= p.num_seqs; n += blockDim.x) {
+        const int v = p.cu_seqlens[n];
+        bad |= n == 0 ? v != 0 : v < p.cu_seqlens[n - 1];
+        if (n == p.num_seqs) bad |= v != p.rows;
+    }
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) atomicOr(p.status, kDevBadCuSeqlens);
+        return false;
+    }
+    return true;
+}
+// First n in [lo, num_seqs] whose sequence begins at `row` or behind it (num_seqs: none), by one warp.
+__device__ __forceinline__ int first_at(const DiagParams &p, uint32_t row, int lo, int lane) {
+    if (p.cu_seqlens == nullptr) {
+        if (p.seqlen == 0) return row == 0 ? lo : p.num_seqs;
+        const int64_t n = (row + p.seqlen - 1) / p.seqlen;
+        return n > p.num_seqs ? p.num_seqs : (int)(n < lo ? lo : n);
+    }
+    int size = p.num_seqs - lo;             // candidates [lo, lo + size); behind them num_seqs, which always is
+    while (size > 0) {
+        const int step = (size + 31) / 32, at = lo + (lane + 1) * step - 1;
+        const bool below = at < lo + size && (uint32_t)p.cu_seqlens[at] < row;
+        const int n = __popc(__ballot_sync(~0u, below));
+        lo += n * step;
+        size = n == 32 ? 0 : step == 1 ? 0 : min(step - 1, size - n * step);
+    }
+    return lo < p.num_seqs ? lo : p.num_seqs;
+}
+// Part `part`'s sequences [n0, n1) and rows [r0, r1): whole sequences, about rows / parts rows.
+struct DiagPart {
+    int n0, n1;
+    uint32_t r0, r1;
+};
+__device__ __forceinline__ DiagPart diag_part(const DiagParams &p, int part, int lane) {
+    DiagPart o;
+    if (p.parts == 1) return {0, p.num_seqs, 0u, (uint32_t)p.rows};
+    if (p.cu_seqlens == nullptr) {
+        o.n0 = (int)((int64_t)part * p.num_seqs / p.parts);
+        o.n1 = (int)((int64_t)(part + 1) * p.num_seqs / p.parts);
+    } else {
+        o.n0 = part == 0 ? 0 : first_at(p, (uint32_t)(part * p.rows / p.parts), 0, lane);
+        o.n1 = part + 1 == p.parts ? p.num_seqs : first_at(p, (uint32_t)((part + 1) * p.rows / p.parts), 0, lane);
+    }
+    o.r0 = seq_begin(p, o.n0);
+    o.r1 = seq_begin(p, o.n1);
+    return o;
+}
+// The edges between sequences at rows [w0, w0 + N], one bit each, and for each of them the first and the last
+// n that begins there (in between: sequences without tokens).  `from`: a lower bound on those n, moved on.
+template <int N>
+__device__ __forceinline__ uint32_t find_edges(const DiagParams &p, uint32_t w0, int &from, int *first, int *last, int lane) {
+    uint32_t mask = 0;
+    if (p.cu_seqlens == nullptr) from = first_at(p, w0, 0, lane);
+    for (int n0 = from, moved = 0;;) {
+        const int n = n0 + lane;
+        const uint32_t at = n <= p.num_seqs ? seq_begin(p, n) : 0xffffffffu;
+        const uint32_t below = __ballot_sync(~0u, at < w0);
+        if (below == ~0u) {
+            from = n0 = first_at(p, w0, n0 + 32 < p.num_seqs ? n0 + 32 : p.num_seqs, lane);
+            moved = 1;
+            continue;
+        }
+        if (!moved) {
+            from = n0 + __popc(below);
+            moved = 1;
+        }
+        const uint32_t d = at - w0;
+        const bool in = at >= w0 && d <= (uint32_t)N && n <= p.num_seqs;
+        const uint32_t bit = in ? 1u << d : 0u;
+        if (__any_sync(~0u, in)) {
+            const uint32_t before = __shfl_up_sync(~0u, bit, 1), after = __shfl_down_sync(~0u, bit, 1);
+            if (in && !(mask & bit) && (lane == 0 || before != bit)) first[d] = n;
+            if (in && (lane == 31 || after != bit)) last[d] = n;
+            mask |= __reduce_or_sync(~0u, bit);
+        }
+        if (__shfl_sync(~0u, (int)(n >= p.num_seqs || at > w0 + N), 31)) break;
+        n0 += 32;
+    }
+    __syncwarp();
+    return mask;
+}
+
+// ------------------------------------------------------------------ clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// A stretch of tokens as the map h -> (hi + lo) h + H: the product of its decays in two fp32 numbers, because the
+// chain of these maps over a long sequence has to keep slow decays (hi alone drifts: 65,536 equal tokens of
+// 1 - 3e-5 by up to 2e-3) as well as the digits of fast ones.  hi = -1 marks a stretch that holds an edge, the
+// same for all lanes: nothing of what came before is left behind it, an infinity or a NaN neither.
+struct DiagProduct {
+    F2 hi, lo;
+};
+__device__ __forceinline__ DiagProduct diag_product(F2 sum_g, bool edge) {
+    DiagProduct o;
+    const F2 m = diag_expm1(sum_g, o.hi), back = add2(o.hi, both(-1.f));
+    // Where 1 + m was rounded, what that lost; a far decay is hi itself.
+    o.lo = {sum_g.x > -0.25f ? m.x - back.x : 0.f, sum_g.y > -0.25f ? m.y - back.y : 0.f};
+    if (edge) o.hi = both(-1.f);
+    return o;
+}
+__device__ __forceinline__ F2 diag_apply(DiagProduct p, F2 H, F2 h) {
+    const F2 r = fma2(p.hi, h, fma2(p.lo, h, H));
+    const bool edge = p.hi.x < 0.f;
+    return {edge ? H.x : r.x, edge ? H.y : r.y};
+}
+__device__ __forceinline__ DiagProduct diag_join(DiagProduct p, DiagProduct q) {
+    DiagProduct o;
+    o.hi = mul2(p.hi, q.hi);
+    const F2 lost = fma2(p.hi, q.hi, {-o.hi.x, -o.hi.y});
+    o.lo = fma2(p.hi, q.lo, fma2(p.lo, q.hi, lost));
+    if (p.hi.x < 0.f || q.hi.x < 0.f) o.hi = both(-1.f);
+    return o;
+}
+// Maps in shared memory, one to a lane.
+struct DiagMaps {
+    float4 product[32];
+    float2 shift[32];
+};
+__device__ __forceinline__ DiagProduct get_product(const DiagMaps &m, int lane) {
+    const float4 v = m.product[lane];
+    return {{v.x, v.y}, {v.z, v.w}};
+}
+__device__ __forceinline__ F2 get_pair(const float2 *v, int lane) { return {v[lane].x, v[lane].y}; }
+__device__ __forceinline__ void put_map(DiagMaps &m, int lane, DiagProduct p, F2 H) {
+    m.product[lane] = make_float4(p.hi.x, p.hi.y, p.lo.x, p.lo.y);
+    m.shift[lane] = make_float2(H.x, H.y);
+}
+// The same at another CTA of the cluster.
+__device__ __forceinline__ void put_map_at(DiagMaps &m, uint32_t rank, int lane, DiagProduct p, F2 H) {
+    uint32_t a, b;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&m.product[lane]))), "r"(rank));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&m.shift[lane]))), "r"(rank));
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(p.hi.x), "f"(p.hi.y), "f"(p.lo.x), "f"(p.lo.y) : "memory");
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(b), "f"(H.x), "f"(H.y) : "memory");
+}
+#endif  // __CUDACC__
+
+}  // namespace gdn

@@ -1,0 +1,171 @@
+// diag_step.cu -- single tokens of the diagonal recurrence, and rows as 8-bit codes.
+#include "diag_internal.cuh"
+
+namespace gdn {
+namespace {
+
+// One token per row: h = alpha h + w i x in place, y = h rounded.  Bound by the state's and the rows' bytes (16 a
+// channel in 16 bits); a thread takes four channels, and rows of a large batch in turn with one set of parameters.
+template <typename IO, int GATE, int WEIGHT, bool VEC>
+__global__ void __launch_bounds__(128) diag_decode_kernel(const __grid_constant__ DiagDecodeParams p) {
+    constexpr int N = VEC ? 2 : 1;          // pairs of channels
+    const int64_t C = p.channels, c = ((int64_t)blockIdx.x * 128 + threadIdx.x) * 2 * N;
+    if (c >= C) return;
+    DiagLane l[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) l[k] = diag_lane(p.A_log, p.a_bias, p.b_bias, c + 2 * k, C);
+    for (int64_t row = blockIdx.y; row < p.batch; row += gridDim.y) {
+        const int64_t e = p.slots ? p.slots[row] : row;
+        if (e < 0 || e >= p.pool_size) {
+            if (c == 0) atomicOr(p.status, kDevBadSlot);
+            continue;
+        }
+        float *state = p.state + e * C + c;
+        const IO *x = (const IO *)p.x + row * p.ld_x + c, *a = (const IO *)p.a + row * p.ld_a + c;
+        const IO *b = (const IO *)p.b + row * p.ld_b + c;
+        IO *y = (IO *)p.y + row * p.ld_y + c;
+        F2 xv[N], av[N], bv[N], h[N];
+        if (VEC) {
+            using Raw = typename Pair<IO>::Raw;
+            struct __align__(2 * sizeof(Raw)) Two {
+                Raw v[2];
+            };
+            const Two rx = *reinterpret_cast<const Two *>(x), ra = *reinterpret_cast<const Two *>(a);
+            Two rb{};
+            if (p.has_b) rb = *reinterpret_cast<const Two *>(b);
+            const float4 s = *reinterpret_cast<const float4 *>(state);
+            h[0] = {s.x, s.y};
+            h[N - 1] = {s.z, s.w};
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                xv[k] = Pair<IO>::wide(rx.v[k]);
+                av[k] = Pair<IO>::wide(ra.v[k]);
+                bv[k] = Pair<IO>::wide(rb.v[k]);
+            }
+        } else {
+            const bool two = c + 1 < C;
+            xv[0] = {IoType<IO>::ld(x), two ? IoType<IO>::ld(x + 1) : 0.f};
+            av[0] = {IoType<IO>::ld(a), two ? IoType<IO>::ld(a + 1) : 0.f};
+            bv[0] = both(0.f);
+            if (p.has_b) bv[0] = {IoType<IO>::ld(b), two ? IoType<IO>::ld(b + 1) : 0.f};
+            h[0] = {state[0], two ? state[1] : 0.f};
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const DiagGates o = diag_gates<GATE, WEIGHT, false>(av[k], bv[k], p.has_b, l[k]);
+            F2 v = mul2(o.i, xv[k]);
+            v = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(o.w, v);
+            h[k] = fma2(o.alpha, h[k], v);
+        }
+        if (VEC) {
+            *reinterpret_cast<float4 *>(state) = make_float4(h[0].x, h[0].y, h[N - 1].x, h[N - 1].y);
+            typename Pair<IO>::Raw r[2] = {Pair<IO>::narrow(h[0]), Pair<IO>::narrow(h[N - 1])};
+            if (sizeof(IO) == 4) {
+                *reinterpret_cast<float4 *>(y) = make_float4(h[0].x, h[0].y, h[N - 1].x, h[N - 1].y);
+            } else {
+                *reinterpret_cast<uint2 *>(y) = *reinterpret_cast<const uint2 *>(r);
+            }
+        } else {
+            state[0] = h[0].x;
+            IoType<IO>::st(y, h[0].x);
+            if (c + 1 < C) {
+                state[1] = h[0].y;
+                IoType<IO>::st(y + 1, h[0].y);
+            }
+        }
+    }
+}
+
+template <typename IO, int GATE, int WEIGHT> cudaError_t launch(const DiagDecodeParams &p, cudaStream_t stream) {
+    const int64_t per = 128 * (p.vec ? 4 : 2), blocks = (p.channels + per - 1) / per;
+    int64_t rows = (152 * 16 + blocks - 1) / blocks;
+    if (rows > p.batch) rows = p.batch;
+    const dim3 grid((unsigned)blocks, (unsigned)rows);
+    if (p.vec) diag_decode_kernel<IO, GATE, WEIGHT, true><<<grid, 128, 0, stream>>>(p);
+    else diag_decode_kernel<IO, GATE, WEIGHT, false><<<grid, 128, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename IO> cudaError_t by_kind(const DiagDecodeParams &p, int gate, int weighting, cudaStream_t s) {
+    if (gate == GDN_DIAG_SOFTPLUS)
+        return weighting == GDN_DIAG_NORM         ? launch<IO, GDN_DIAG_SOFTPLUS, GDN_DIAG_NORM>(p, s)
+               : weighting == GDN_DIAG_COMPLEMENT ? launch<IO, GDN_DIAG_SOFTPLUS, GDN_DIAG_COMPLEMENT>(p, s)
+                                                  : launch<IO, GDN_DIAG_SOFTPLUS, GDN_DIAG_PLAIN>(p, s);
+    return weighting == GDN_DIAG_NORM         ? launch<IO, GDN_DIAG_SIGMOID, GDN_DIAG_NORM>(p, s)
+           : weighting == GDN_DIAG_COMPLEMENT ? launch<IO, GDN_DIAG_SIGMOID, GDN_DIAG_COMPLEMENT>(p, s)
+                                              : launch<IO, GDN_DIAG_SIGMOID, GDN_DIAG_PLAIN>(p, s);
+}
+
+// ------------------------------------------------------------------ 8-bit codes
+// A warp takes one block of 64 channels of one row, two to a lane.
+template <typename IO>
+__global__ void __launch_bounds__(256) pack_kernel(int64_t rows, int64_t C, const IO *x, int64_t ld, int8_t *codes, uint8_t *steps) {
+    const int lane = threadIdx.x % 32;
+    const int64_t blocks = (C + kDiagSlice - 1) / kDiagSlice, all = rows * blocks, warps = (int64_t)gridDim.x * 8;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; i < all; i += warps) {
+        const int64_t row = i / blocks, k = i - row * blocks, c = k * kDiagSlice + 2 * lane;
+        const IO *p = x + row * ld + c;
+        const F2 v = {c < C ? IoType<IO>::ld(p) : 0.f, c + 1 < C ? IoType<IO>::ld(p + 1) : 0.f};
+        const uint32_t e = code_step(__reduce_max_sync(~0u, magnitude(v)));
+        const float inv = code_inverse(e);
+        if (c < C) codes[row * C + c] = (int8_t)code_of(v.x, inv);
+        if (c + 1 < C) codes[row * C + c + 1] = (int8_t)code_of(v.y, inv);
+        if (lane == 0) steps[i] = (uint8_t)e;
+    }
+}
+
+// The value in the type that it is read back in: f16's range is the only one that a code can pass.
+template <typename IO> __device__ __forceinline__ float held(float v) { return v; }
+template <> __device__ __forceinline__ float held<__half>(float v) { return v > 65504.f ? 65504.f : v < -65504.f ? -65504.f : v; }
+
+template <typename IO>
+__global__ void __launch_bounds__(256) unpack_kernel(int64_t rows, int64_t C, const int8_t *codes, const uint8_t *steps, IO *y, int64_t ld) {
+    const int lane = threadIdx.x % 32;
+    const int64_t blocks = (C + kDiagSlice - 1) / kDiagSlice, all = rows * blocks, warps = (int64_t)gridDim.x * 8;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; i < all; i += warps) {
+        const int64_t row = i / blocks, k = i - row * blocks, c = k * kDiagSlice + 2 * lane;
+        const float s = code_scale(steps[i]);
+        IO *p = y + row * ld + c;
+        if (c < C) IoType<IO>::st(p, held<IO>(s * codes[row * C + c]));
+        if (c + 1 < C) IoType<IO>::st(p + 1, held<IO>(s * codes[row * C + c + 1]));
+    }
+}
+
+unsigned code_blocks(int64_t rows, int64_t C) {
+    const int64_t n = (rows * ((C + kDiagSlice - 1) / kDiagSlice) + 7) / 8, most = 152 * 8 * 4;
+    return (unsigned)(n < most ? n : most);
+}
+
+}  // namespace
+
+cudaError_t launch_diag_decode(const DiagDecodeParams &p, gdn_dtype io, int gate, int weighting, cudaStream_t stream) {
+    switch (io) {
+        case GDN_F32: return by_kind<float>(p, gate, weighting, stream);
+        case GDN_BF16: return by_kind<__nv_bfloat16>(p, gate, weighting, stream);
+        default: return by_kind<__half>(p, gate, weighting, stream);
+    }
+}
+
+cudaError_t launch_checkpoint_pack(gdn_dtype io, int64_t rows, int64_t C, const void *x, int64_t ld, int8_t *codes, uint8_t *steps,
+                                   cudaStream_t stream) {
+    const unsigned n = code_blocks(rows, C);
+    switch (io) {
+        case GDN_F32: pack_kernel<float><<<n, 256, 0, stream>>>(rows, C, (const float *)x, ld, codes, steps); break;
+        case GDN_BF16: pack_kernel<__nv_bfloat16><<<n, 256, 0, stream>>>(rows, C, (const __nv_bfloat16 *)x, ld, codes, steps); break;
+        default: pack_kernel<__half><<<n, 256, 0, stream>>>(rows, C, (const __half *)x, ld, codes, steps);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_checkpoint_unpack(gdn_dtype io, int64_t rows, int64_t C, const int8_t *codes, const uint8_t *steps, void *y, int64_t ld,
+                                     cudaStream_t stream) {
+    const unsigned n = code_blocks(rows, C);
+    switch (io) {
+        case GDN_F32: unpack_kernel<float><<<n, 256, 0, stream>>>(rows, C, codes, steps, (float *)y, ld); break;
+        case GDN_BF16: unpack_kernel<__nv_bfloat16><<<n, 256, 0, stream>>>(rows, C, codes, steps, (__nv_bfloat16 *)y, ld); break;
+        default: unpack_kernel<__half><<<n, 256, 0, stream>>>(rows, C, codes, steps, (__half *)y, ld);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

@@ -11,7 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -30,7 +30,9 @@ EXPORTS = ("gdn_prefill_workspace_bytes", "gdn_prefill", "gdn_decode_step",
            "gdn_gated_rmsnorm", "gdn_set_wait_budget", "gdn_decode_layer", "gdn_prefill_variant",
            "gdn_prefill_norm", "gdn_prefill_variant_workspace_bytes", "gdn_prefill_variant_plan",
            "gdn_prefill_layer", "gdn_prefill_layer_workspace_bytes", "gdn_ssm_prefill_workspace_bytes",
-           "gdn_ssm_prefill", "gdn_ssm_prefill_plan", "gdn_ssm_decode", "gdn_rotary", "gdn_rotary_frequencies")
+           "gdn_ssm_prefill", "gdn_ssm_prefill_plan", "gdn_ssm_decode", "gdn_rotary", "gdn_rotary_frequencies",
+           "gdn_diag_kept_bytes", "gdn_diag_prefill", "gdn_diag_backward_workspace_bytes", "gdn_diag_backward",
+           "gdn_diag_decode", "gdn_checkpoint_pack", "gdn_checkpoint_unpack")
 PATH_SIMT, PATH_TC, PATH_TC_TP = 1, 2, 3
 # gdn_rule codes.
 RULES = {"gated_delta": 0, "delta": 1, "gated": 2, "linear": 3}
@@ -38,6 +40,12 @@ RULES = {"gated_delta": 0, "delta": 1, "gated": 2, "linear": 3}
 ACTIVATIONS = {"none": 0, "silu": 1, "swish": 1, "sigmoid": 2}
 # gdn_rotary_kind codes.
 ROTARY_KINDS = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "wavelength": 4}
+# gdn_diag_gate, gdn_diag_weighting and gdn_diag_keep codes.
+DIAG_GATES = {"softplus": 0, "sigmoid": 1}
+DIAG_WEIGHTINGS = {"plain": 0, "complement": 1, "norm": 2}
+DIAG_KEEPS = {None: 0, "states": 1, "8bit": 2}
+# Channels that share a step of the 8-bit codes.
+CHECKPOINT_BLOCK = 64
 
 
 class GdnShape(ctypes.Structure):
@@ -94,6 +102,30 @@ class GdnRotaryShape(ctypes.Structure):
 class GdnRotaryScaling(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
                 ("trained_length", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class GdnDiagShape(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("seqlen", ctypes.c_int64), ("num_seqs", ctypes.c_int32),
+                ("channels", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("weighting", ctypes.c_int32), ("input_gate", ctypes.c_int32),
+                ("keep", ctypes.c_int32)] + \
+               [(name, ctypes.c_int64) for name in (
+                   "x_stride", "a_stride", "b_stride", "y_stride", "dx_stride", "da_stride", "db_stride")]
+
+
+class GdnDiagKept(NamedTuple):
+    """What gdn_diag_prefill keeps for gdn_diag_backward: the buffer, and the call that it belongs to."""
+    data: torch.Tensor
+    io: torch.dtype
+    batch: int
+    seqlen: int
+    num_seqs: int
+    channels: int
+    gate: str
+    weighting: str
+    input_gate: bool
+    keep: str
 
 
 class GdnError(RuntimeError):
@@ -184,6 +216,22 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.gdn_rotary_frequencies.restype = ctypes.c_int
     lib.gdn_rotary_frequencies.argtypes = [ctypes.POINTER(GdnRotaryScaling), ctypes.c_int32, P,
                                            ctypes.POINTER(ctypes.c_float)]
+    DS = ctypes.POINTER(GdnDiagShape)
+    lib.gdn_diag_kept_bytes.restype = ctypes.c_size_t
+    lib.gdn_diag_kept_bytes.argtypes = [DS]
+    lib.gdn_diag_backward_workspace_bytes.restype = ctypes.c_size_t
+    lib.gdn_diag_backward_workspace_bytes.argtypes = [DS]
+    lib.gdn_diag_prefill.restype = ctypes.c_int
+    lib.gdn_diag_prefill.argtypes = [DS, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.gdn_diag_backward.restype = ctypes.c_int
+    lib.gdn_diag_backward.argtypes = [DS, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P, P, P, P, P, P, P, P, P, P,
+                                      ctypes.c_size_t, P]
+    lib.gdn_diag_decode.restype = ctypes.c_int
+    lib.gdn_diag_decode.argtypes = [DS, P, P, P, P, P, P, P, ctypes.c_int64, P, P, P]
+    lib.gdn_checkpoint_pack.restype = ctypes.c_int
+    lib.gdn_checkpoint_pack.argtypes = [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, P, ctypes.c_int64, P, P, P]
+    lib.gdn_checkpoint_unpack.restype = ctypes.c_int
+    lib.gdn_checkpoint_unpack.argtypes = [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, P, P, P, ctypes.c_int64, P]
     lib.gdn_decode_layer.restype = ctypes.c_int
     lib.gdn_decode_layer.argtypes = [S, ctypes.POINTER(GdnLayerParams), P, P, P, P, P, P, P, P, P,
                                      P, ctypes.c_float, P, P, P, P]
@@ -1032,6 +1080,179 @@ def gdn_ssm_decode(xbc, dt, A_log, state, *, heads: int, head_dim: int, d_state:
                                   _arg("state", state, (E, heads, d_state, head_dim), f32, dev), E,
                                   _arg("slots", slots, (B,), torch.int32, dev),
                                   _arg("y", y, (B, T, heads, head_dim), io, dev), _raw_stream(dev)))
+    return y
+
+
+# ------------------------------------------------------------------ the diagonal recurrence
+def _diag_kinds(gate, weighting, keep=None):
+    if gate not in DIAG_GATES or weighting not in DIAG_WEIGHTINGS or keep not in DIAG_KEEPS:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"gate must be one of {sorted(DIAG_GATES)}, weighting of {sorted(DIAG_WEIGHTINGS)}, "
+                                            "keep None, 'states' or '8bit'")
+    return DIAG_GATES[gate], DIAG_WEIGHTINGS[weighting], DIAG_KEEPS[keep]
+
+
+def _diag_params(A_log, a_bias, b_bias, C: int, input_gate: bool, dev: int):
+    if b_bias is not None and not input_gate:
+        raise GdnError(GDN_ERR_INVALID_ARG, "b_bias belongs to an input gate: b is needed")
+    if A_log is None:
+        raise GdnError(GDN_ERR_INVALID_ARG, "A_log is needed")
+    return tuple(_arg(name, t, (C,), torch.float32, dev) for name, t in (("A_log", A_log), ("a_bias", a_bias), ("b_bias", b_bias)))
+
+
+def gdn_diag_kept_bytes(shape: GdnDiagShape) -> int:
+    return int(load().gdn_diag_kept_bytes(ctypes.byref(shape)))
+
+
+def gdn_diag_backward_workspace_bytes(shape: GdnDiagShape) -> int:
+    return int(load().gdn_diag_backward_workspace_bytes(ctypes.byref(shape)))
+
+
+def gdn_diag_prefill(x, a, b, A_log, *, a_bias=None, b_bias=None, gate: str = "softplus", weighting: str = "norm", state_in=None,
+                     cu_seqlens=None, keep=None, y=None, state_out=None, kept=None, stream=None):
+    """The diagonal recurrence over whole sequences: h_t = alpha_t h_{t-1} + w_t sigmoid(b_t + b_bias) x_t per channel, with
+    alpha_t = exp(-exp(A_log) softplus(a_t + a_bias)) (gate 'softplus') or exp(-exp(A_log) sigmoid(a_t + a_bias))
+    ('sigmoid') and w_t = 1 ('plain'), 1 - alpha_t ('complement') or sqrt(1 - alpha_t^2) ('norm').
+
+    x, a, b [B, T, C] (b None: no input gate); token rows may be slices of wider ones (contiguous in themselves, evenly
+    spaced, none over another).  With cu_seqlens (int32 [N + 1]) B is 1 and T the packed total.  A_log, a_bias, b_bias
+    [C] fp32; state_in [N, C] fp32 or None (zeros).  keep: what a backward pass will need, 'states' (beside x, a and b
+    themselves), '8bit' (instead of them) or None; `kept` may give the uint8 buffer.  Returns (y, state_out, a
+    GdnDiagKept or None)."""
+    lib = _lib or load()
+    dev = _first("x", x, 3)
+    kinds = _diag_kinds(gate, weighting, keep)
+    io, (B, T, C) = x.dtype, x.shape
+    n = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    f32, states, rows = torch.float32, (max(n, 0), C), (B, T, C)
+    px, ldx = _rows("x", x, B, T, (C,), io, dev)
+    pa, lda = _rows("a", a, B, T, (C,), io, dev)
+    pb, ldb = (None, 0) if b is None else _rows("b", b, B, T, (C,), io, dev)
+    pA, pab, pbb = _diag_params(A_log, a_bias, b_bias, C, b is not None, dev)
+    pcu = _arg("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, dev)
+    psi = _arg("state_in", state_in, states, f32, dev)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty(rows, dtype=io, device=x.device)
+        if state_out is None:
+            state_out = torch.empty(states, dtype=f32, device=x.device)
+        py, ldy = _rows("y", y, B, T, (C,), io, dev)
+        shape = GdnDiagShape(_DTYPE_CODE[io], B, T, n, C, kinds[0], kinds[1], b is not None, kinds[2], ldx, lda, ldb, ldy, 0, 0, 0)
+        ref = ctypes.byref(shape)
+        if keep is not None and kept is None:
+            kept = torch.empty(lib.gdn_diag_kept_bytes(ref), dtype=torch.uint8, device=x.device)
+        held = 0 if kept is None else kept.numel()
+        _check(lib.gdn_diag_prefill(ref, px, pa, pb, pA, pab, pbb, psi, pcu, py, _arg("state_out", state_out, states, f32, dev),
+                                    _arg("kept", kept, None, torch.uint8, dev), held, _raw_stream(dev)))
+    return y, state_out, None if keep is None else GdnDiagKept(kept, io, B, T, n, C, gate, weighting, b is not None, keep)
+
+
+def gdn_diag_backward(dy, kept: GdnDiagKept, A_log, *, x=None, a=None, b=None, a_bias=None, b_bias=None, state_in=None,
+                      cu_seqlens=None, dstate_out=None, dx=None, da=None, db=None, workspace=None, stream=None):
+    """The gradients of sum(y dy) + sum(state_out dstate_out) of a gdn_diag_prefill call, from what it kept.
+
+    dy [B, T, C]; dstate_out [N, C] fp32 or None (zeros); A_log, the biases, state_in and cu_seqlens as the forward
+    call had them, and x, a, b too unless it kept '8bit' (they are then not read, and the gradients are those at the
+    values that the codes hold).  dx, da, db may give their rows, as slices of a wider one too.  Returns (dx, da, db,
+    dA_log, da_bias, db_bias, dstate_in), None for what the forward call did not have."""
+    lib = _lib or load()
+    if not isinstance(kept, GdnDiagKept):
+        raise GdnError(GDN_ERR_INVALID_ARG, "kept must be what gdn_diag_prefill kept")
+    dev = _first("dy", dy, 3)
+    io, B, T, n, C, has_b = kept.io, kept.batch, kept.seqlen, kept.num_seqs, kept.channels, kept.input_gate
+    kinds = _diag_kinds(kept.gate, kept.weighting, kept.keep)
+    f32, states, rows = torch.float32, (max(n, 0), C), (B, T, C)
+    pdy, lddy = _rows("dy", dy, B, T, (C,), io, dev)
+    pA, pab, pbb = _diag_params(A_log, a_bias, b_bias, C, has_b, dev)
+    pcu = _arg("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, dev)
+    if cu_seqlens is None and n != B:
+        raise GdnError(GDN_ERR_INVALID_ARG, "cu_seqlens is needed: the forward call was packed")
+    psi, pdo = _arg("state_in", state_in, states, f32, dev), _arg("dstate_out", dstate_out, states, f32, dev)
+    pk = _arg("kept", kept.data, None, torch.uint8, dev)
+    ins, lds = [None] * 3, [0] * 3
+    if kept.keep == "states":
+        for i, (name, t) in enumerate((("x", x), ("a", a), ("b", b))):
+            if name != "b" or has_b:
+                ins[i], lds[i] = _rows(name, t, B, T, (C,), io, dev)
+    with _on(dev, stream):
+        new = lambda shape, dtype=f32: torch.empty(shape, dtype=dtype, device=dy.device)  # noqa: E731
+        dx, da = new(rows, io) if dx is None else dx, new(rows, io) if da is None else da
+        db = None if not has_b else new(rows, io) if db is None else db
+        outs = [_rows("dx", dx, B, T, (C,), io, dev), _rows("da", da, B, T, (C,), io, dev),
+                _rows("db", db, B, T, (C,), io, dev) if has_b else (None, 0)]
+        dA_log, da_bias, db_bias = new((C,)), None if a_bias is None else new((C,)), None if b_bias is None else new((C,))
+        dstate_in = None if state_in is None else new(states)
+        shape = GdnDiagShape(_DTYPE_CODE[io], B, T, n, C, kinds[0], kinds[1], has_b, kinds[2], *lds, lddy, *(ld for _, ld in outs))
+        ref = ctypes.byref(shape)
+        need = lib.gdn_diag_backward_workspace_bytes(ref)
+        if workspace is None and need > 0:
+            workspace = new(need, torch.uint8)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(lib.gdn_diag_backward(ref, *ins, pA, pab, pbb, psi, pcu, pk, kept.data.numel(), pdy, pdo, *(p for p, _ in outs),
+                                     *(None if t is None else t.data_ptr() for t in (dA_log, da_bias, db_bias, dstate_in)),
+                                     None if workspace is None else _arg("workspace", workspace, None, workspace.dtype, dev),
+                                     ws_bytes, _raw_stream(dev)))
+    return dx, da, db, dA_log, da_bias, db_bias, dstate_in
+
+
+def gdn_diag_decode(x, a, b, A_log, state, *, a_bias=None, b_bias=None, gate: str = "softplus", weighting: str = "norm",
+                    slots=None, y=None, stream=None):
+    """One token of the diagonal recurrence per row: gdn_diag_prefill's arguments at T = 1, with ``state`` [E, C] fp32
+    advanced in place.  With slots (int32 [B], distinct) row b uses entry slots[b], else entry b (E = B).  Returns y
+    [B, 1, C]."""
+    lib = _lib or load()
+    dev = _first("x", x, 3)
+    kinds = _diag_kinds(gate, weighting)
+    io, (B, T, C) = x.dtype, x.shape
+    if not isinstance(state, torch.Tensor) or state.dim() != 2:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"state must be [E, {C}]")
+    E = B if slots is None else state.shape[0]
+    px, ldx = _rows("x", x, B, T, (C,), io, dev)
+    pa, lda = _rows("a", a, B, T, (C,), io, dev)
+    pb, ldb = (None, 0) if b is None else _rows("b", b, B, T, (C,), io, dev)
+    pA, pab, pbb = _diag_params(A_log, a_bias, b_bias, C, b is not None, dev)
+    ps, pslots = _arg("state", state, (E, C), torch.float32, dev), _arg("slots", slots, (B,), torch.int32, dev)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty((B, T, C), dtype=io, device=x.device)
+        py, ldy = _rows("y", y, B, T, (C,), io, dev)
+        shape = GdnDiagShape(_DTYPE_CODE[io], B, T, B, C, kinds[0], kinds[1], b is not None, 0, ldx, lda, ldb, ldy, 0, 0, 0)
+        _check(lib.gdn_diag_decode(ctypes.byref(shape), px, pa, pb, pA, pab, pbb, ps, E, pslots, py, _raw_stream(dev)))
+    return y
+
+
+def gdn_checkpoint_pack(x, *, codes=None, steps=None, stream=None):
+    """x [B, T, C] (token rows may be slices of wider ones) in 8 bits: (codes int8 [B, T, C], steps uint8 [B, T,
+    ceil(C / 64)]).  64 channels of a row share the step 2^(s - 133), the least at which they round within 127; one
+    with an infinity or a NaN among them is read back as NaN."""
+    lib = _lib or load()
+    dev = _first("x", x, 3)
+    B, T, C = x.shape
+    px, ldx = _rows("x", x, B, T, (C,), x.dtype, dev)
+    blocks = (B, T, -(-C // CHECKPOINT_BLOCK))
+    with _on(dev, stream):
+        if codes is None:
+            codes = torch.empty((B, T, C), dtype=torch.int8, device=x.device)
+        if steps is None:
+            steps = torch.empty(blocks, dtype=torch.uint8, device=x.device)
+        _check(lib.gdn_checkpoint_pack(_DTYPE_CODE[x.dtype], B * T, C, px, ldx, _arg("codes", codes, (B, T, C), torch.int8, dev),
+                                       _arg("steps", steps, blocks, torch.uint8, dev), _raw_stream(dev)))
+    return codes, steps
+
+
+def gdn_checkpoint_unpack(codes, steps, dtype=torch.bfloat16, *, y=None, stream=None):
+    """The rows that gdn_checkpoint_pack packed, [B, T, C] in dtype: exact in bfloat16 and float32, held to the largest
+    finite value in float16."""
+    lib = _lib or load()
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 3 or not codes.is_cuda or dtype not in _DTYPE_CODE:
+        raise GdnError(GDN_ERR_INVALID_ARG, "codes must be a CUDA tensor of 3 axes, dtype float32, bfloat16 or float16")
+    dev, (B, T, C) = codes.get_device(), codes.shape
+    pc = _arg("codes", codes, None, torch.int8, dev)
+    ps = _arg("steps", steps, (B, T, -(-C // CHECKPOINT_BLOCK)), torch.uint8, dev)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty((B, T, C), dtype=dtype, device=codes.device)
+        py, ldy = _rows("y", y, B, T, (C,), dtype, dev)
+        _check(lib.gdn_checkpoint_unpack(_DTYPE_CODE[dtype], B * T, C, pc, ps, py, ldy, _raw_stream(dev)))
     return y
 
 
