@@ -90,7 +90,7 @@ gdn_status check(const gdn_diag_shape *s, bool varlen, Geometry &g) {
     const size_t slices = diag_slices(s->channels), tiles = (size_t)(g.rows + kDiagTile - 1) / kDiagTile;
     g.kept_states = s->keep != GDN_DIAG_KEEP_NONE ? tiles * slices * kDiagSlice * 4 : 0;
     g.kept = g.kept_states;
-    if (s->keep == GDN_DIAG_KEEP_8BIT) g.kept += (size_t)(2 + s->input_gate) * slices * g.rows * (kDiagSlice + 1);
+    if (s->keep == GDN_DIAG_KEEP_8BIT) g.kept += (size_t)(2 + s->input_gate) * slices * tiles * kDiagTile * (kDiagSlice + 1);
     return GDN_OK;
 }
 
@@ -133,6 +133,11 @@ size_t partial_bytes(const Geometry &g) {
     return parts > 1 ? (size_t)parts * 3 * g.C * 4 : 0;
 }
 
+void set_widths(DiagParams &p, const Geometry &g, std::initializer_list<Span> ins, std::initializer_list<Span> outs) {
+    p.wide = by(16 / (int)g.es, g, ins) ? 16 : by(2, g, ins) ? 2 * (int)g.es : 0;
+    p.pairs = by(2, g, outs);
+}
+
 DiagParams params(const gdn_diag_shape *s, const Geometry &g, void *kept) {
     DiagParams p{};
     p.has_b = s->input_gate != 0;
@@ -142,7 +147,7 @@ DiagParams params(const gdn_diag_shape *s, const Geometry &g, void *kept) {
     if (s->keep != GDN_DIAG_KEEP_NONE) p.kept = static_cast<float *>(kept);
     if (s->keep == GDN_DIAG_KEEP_8BIT) {
         p.codes = static_cast<int8_t *>(kept) + g.kept_states;
-        p.steps = reinterpret_cast<uint8_t *>(p.codes) + (size_t)(2 + s->input_gate) * diag_slices(s->channels) * g.rows * kDiagSlice;
+        p.steps = reinterpret_cast<uint8_t *>(p.codes) + (g.kept - g.kept_states) / (kDiagSlice + 1) * kDiagSlice;
     }
     return p;
 }
@@ -204,7 +209,7 @@ gdn_status gdn_diag_prefill(const gdn_diag_shape *shape, const void *x, const vo
     p.x = x; p.a = a; p.b = b; p.y = y;
     p.A_log = A_log; p.a_bias = a_bias; p.b_bias = has_b ? b_bias : nullptr;
     p.state_in = state_in; p.state_out = state_out; p.cu_seqlens = cu_seqlens;
-    p.pairs = by(2, g, {sx, sa, sb, sy});
+    set_widths(p, g, {sx, sa, sb}, {sy});
     const cudaError_t e = launch_diag_prefill(p, (gdn_dtype)shape->io_dtype, shape->gate, shape->weighting, (cudaStream_t)stream);
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "diagonal recurrence launch: %s", cudaGetErrorString(e));
     return GDN_OK;
@@ -254,7 +259,7 @@ gdn_status gdn_diag_backward(const gdn_diag_shape *shape, const void *x, const v
     p.state_in = state_in; p.cu_seqlens = cu_seqlens; p.dstate_out = dstate_out; p.dstate_in = dstate_in;
     p.dA_log = dA_log; p.da_bias = da_bias; p.db_bias = has_b ? db_bias : nullptr;
     p.partial = static_cast<float *>(workspace);
-    p.pairs = by(2, g, {sx, sa, sb, sdy, sdx, sda, sdb});
+    set_widths(p, g, {sx, sa, sb, sdy}, {sdx, sda, sdb});
     const cudaError_t e = launch_diag_backward(p, (gdn_dtype)shape->io_dtype, shape->gate, shape->weighting, (cudaStream_t)stream);
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "diagonal recurrence's backward launch: %s", cudaGetErrorString(e));
     return GDN_OK;

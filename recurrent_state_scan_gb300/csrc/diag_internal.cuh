@@ -23,12 +23,13 @@ struct DiagParams {
     int64_t seqlen, rows;
     int32_t num_seqs, channels;
     int32_t parts;                       // stretches of whole sequences that run side by side
-    bool pairs;                          // every row can be read and written two channels at a time
+    int32_t wide;                        // bytes that every input row can be copied by: 16, a pair's, or 0: by the element
+    bool pairs;                          // every output row can be written two channels at a time
     int *status;
     // What the forward pass keeps for the backward pass.
     float *kept;                         // [tiles][slices * 64] or null: h before each tile's first row
-    int8_t *codes;                       // [x | a | b][slice][rows][64] or null
-    uint8_t *steps;                      // [x | a | b][slice][rows]
+    int8_t *codes;                       // [x | a | b][slice][rows, in whole tiles][64] or null
+    uint8_t *steps;                      // [x | a | b][slice][rows, in whole tiles]
     // The backward pass.
     const void *dy;
     const float *dstate_out;             // may be null (zeros)
@@ -55,6 +56,8 @@ struct DiagDecodeParams {
 int diag_slices(int channels);
 int diag_cluster(int64_t rows);
 int diag_parts(int64_t rows, int64_t num_seqs, int channels);
+template <typename IO> cudaError_t diag_prefill_by_kind(const DiagParams &p, int gate, int weighting, cudaStream_t s);
+template <typename IO> cudaError_t diag_backward_by_kind(const DiagParams &p, int gate, int weighting, cudaStream_t s);
 cudaError_t launch_diag_prefill(const DiagParams &p, gdn_dtype io, int gate, int weighting, cudaStream_t stream);
 cudaError_t launch_diag_backward(const DiagParams &p, gdn_dtype io, int gate, int weighting, cudaStream_t stream);
 cudaError_t launch_diag_decode(const DiagDecodeParams &p, gdn_dtype io, int gate, int weighting, cudaStream_t stream);
@@ -102,10 +105,9 @@ __device__ __forceinline__ F2 diag_softplus(F2 z) {
 struct DiagLane {
     F2 rate, abias, nabias, nbbias;   // -e^A_log, a_bias, -a_bias log2 e, -b_bias log2 e
 };
-// What one token's gates give: g and alpha - 1, alpha, sigmoid(a + a_bias) (the softplus gate: only where
-// `grad` is set), the input gate and the input's weight w (norm: and 1 / w).
+// What one token's gates give: g, alpha and alpha - 1, the input gate and the input's weight w (norm: and 1 / w).
 struct DiagGates {
-    F2 g, m, alpha, s, i, w, winv;
+    F2 g, m, alpha, i, w, winv;
 };
 
 template <int WEIGHT> __device__ __forceinline__ void diag_weigh(DiagGates &o) {
@@ -122,18 +124,13 @@ template <int WEIGHT> __device__ __forceinline__ void diag_weigh(DiagGates &o) {
     }
 }
 
-template <int GATE, int WEIGHT, bool GRAD>
+template <int GATE, int WEIGHT>
 __device__ __forceinline__ DiagGates diag_gates(F2 a, F2 b, bool has_b, const DiagLane &l) {
     DiagGates o;
-    if (GATE == GDN_DIAG_SIGMOID) {
-        o.s = diag_sigmoid(a, l.nabias);
-        o.g = mul2(l.rate, o.s);
-    } else {
-        if (GRAD) o.s = diag_sigmoid(a, l.nabias);
-        o.g = mul2(l.rate, diag_softplus(add2(a, l.abias)));
-    }
+    o.g = mul2(l.rate, GATE == GDN_DIAG_SIGMOID ? diag_sigmoid(a, l.nabias) : diag_softplus(add2(a, l.abias)));
     // Held finite: an alpha of 0 times it is then 0, not a NaN (a NaN itself stays one).
-    o.g = {o.g.x < -1e30f ? -1e30f : o.g.x, o.g.y < -1e30f ? -1e30f : o.g.y};
+    asm("max.NaN.f32 %0, %0, 0fF149F2CA;" : "+f"(o.g.x));      // -1e30
+    asm("max.NaN.f32 %0, %0, 0fF149F2CA;" : "+f"(o.g.y));
     o.m = diag_expm1(o.g, o.alpha);
     o.i = has_b ? diag_sigmoid(b, l.nbbias) : both(1.f);
     diag_weigh<WEIGHT>(o);
@@ -204,23 +201,64 @@ template <> struct Pair<__half> {
     }
 };
 
-// `n` rows from row r0 on, those outside [lo, hi) as zeros; `fast`: the slice is whole and lies on pairs.
+// A token row's bits of -infinity: rows that a call does not have are staged with it as `a` and 0 as x and b, and
+// are then the identity (alpha 1, input 0) without a test.
+template <typename IO> __device__ __forceinline__ uint32_t shut_bits() { return sizeof(IO) == 4 ? 0xff800000u : 0u; }
+template <> __device__ __forceinline__ uint32_t shut_bits<__nv_bfloat16>() { return 0xff80ff80u; }
+template <> __device__ __forceinline__ uint32_t shut_bits<__half>() { return 0xfc00fc00u; }
+
+// Copies rows [r0, r0 + N) of a slice (channels c0 ..) to shared memory, [N][64], asynchronously where `wide` allows, by one
+// warp for itself.  Rows outside [lo, hi) become `outside`, channels behind C zeros.
 template <typename IO, int N>
-__device__ __forceinline__ void load_rows(typename Pair<IO>::Raw (&v)[N], const IO *base, int64_t ld, int64_t r0, int64_t lo,
-                                          int64_t hi, int64_t c, int64_t C, bool fast) {
-    const typename Pair<IO>::Raw zero{};
-    const IO *p = base + r0 * ld + c;
-    if (fast) {
+__device__ __forceinline__ void stage_rows(IO *to, const IO *base, int64_t ld, int64_t r0, int64_t lo, int64_t hi, int64_t c0, int64_t C,
+                                           int wide, uint32_t outside, int lane) {
+    constexpr int kRow = kDiagSlice * sizeof(IO) / 16, kStep = 32 / kRow;    // 16-byte pieces of a row; rows at a time
+    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    if (wide == 16) {
+        const int piece = lane % kRow;
+        const int64_t c = c0 + piece * (16 / (int)sizeof(IO));
+        const int bytes = c >= C ? 0 : (C - c) * (int64_t)sizeof(IO) >= 16 ? 16 : (int)((C - c) * sizeof(IO));
+        const IO *from = base + (r0 + lane / kRow) * ld + (bytes ? c : 0);
+        const uint32_t at = dst + (lane / kRow * kRow + piece) * 16;
 #pragma unroll
-        for (int t = 0; t < N; ++t) v[t] = r0 + t >= lo && r0 + t < hi ? Pair<IO>::load(p + t * ld) : zero;
-    } else {
-        const IO none = IO(0.f);
-#pragma unroll
-        for (int t = 0; t < N; ++t) {
-            const bool row = r0 + t >= lo && r0 + t < hi;
-            v[t] = Pair<IO>::join(row && c < C ? p[t * ld] : none, row && c + 1 < C ? p[t * ld + 1] : none);
+        for (int i = 0; i < N / kStep; ++i) {
+            const int64_t row = r0 + lane / kRow + i * kStep;
+            if (row >= lo && row < hi)
+                asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(at + i * 512), "l"(from + i * kStep * ld), "r"(bytes) : "memory");
+            else
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + i * 512), "r"(outside) : "memory");
+        }
+        return;
+    }
+    using Raw = typename Pair<IO>::Raw;
+    const int64_t c = c0 + 2 * lane;
+    const IO *from = base + r0 * ld + c;
+    const uint32_t at = dst + lane * (uint32_t)sizeof(Raw);
+#pragma unroll 4
+    for (int t = 0; t < N; ++t) {
+        const bool row = r0 + t >= lo && r0 + t < hi;
+        if (row && wide == (int)sizeof(Raw) && c + 1 < C) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at + t * 32 * (uint32_t)sizeof(Raw)), "l"(from + t * ld), "n"(sizeof(Raw)) : "memory");
+        } else {
+            IO *q = to + t * kDiagSlice + 2 * lane;
+            if (row) {
+                q[0] = c < C ? from[t * ld] : IO(0.f);
+                q[1] = c + 1 < C ? from[t * ld + 1] : IO(0.f);
+            } else {
+                uint32_t *v = reinterpret_cast<uint32_t *>(q);
+                v[0] = outside;
+                if (sizeof(IO) == 4) v[1] = outside;
+            }
         }
     }
+}
+__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void stage_wait() {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+}
+template <typename IO> __device__ __forceinline__ F2 staged(const IO *rows, int t, int lane) {
+    return Pair<IO>::wide(reinterpret_cast<const typename Pair<IO>::Raw *>(rows)[t * 32 + lane]);
 }
 template <typename IO>
 __device__ __forceinline__ void store_pair(IO *p, F2 v, int64_t c, int64_t C, bool fast) {
@@ -250,9 +288,13 @@ __device__ __forceinline__ uint32_t code_step(uint32_t most) {
 }
 __device__ __forceinline__ float code_scale(uint32_t e) { return e == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((e - 6u) << 23); }
 __device__ __forceinline__ float code_inverse(uint32_t e) { return e == 255u ? 0.f : __uint_as_float((260u - e) << 23); }
-__device__ __forceinline__ int code_of(float v, float inverse) {
-    const int q = __float2int_rn(v * inverse);
-    return q > 127 ? 127 : q < -127 ? -127 : q;
+// Two codes as the bytes of an integer: v / step, exact, plus 1.5 x 2^23 is rounded to the nearest integer, whose low byte is the
+// code.  Only values next to fp32's largest could reach 128.
+__device__ __forceinline__ uint32_t codes_of(F2 v, uint32_t e) {
+    const float inv = code_inverse(e);
+    if (e == 254u) v = {fminf(fmaxf(v.x, -127.f / inv), 127.f / inv), fminf(fmaxf(v.y, -127.f / inv), 127.f / inv)};
+    const F2 q = fma2(v, both(inv), both(12582912.f));
+    return __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x0040);
 }
 __device__ __forceinline__ uint32_t magnitude(F2 v) {
     const uint32_t a = __float_as_uint(v.x) & 0x7fffffffu, b = __float_as_uint(v.y) & 0x7fffffffu;
@@ -315,36 +357,38 @@ __device__ __forceinline__ DiagPart diag_part(const DiagParams &p, int part, int
     o.r1 = seq_begin(p, o.n1);
     return o;
 }
+// 32 sequences' first rows, one to a lane, kept while a warp walks along the rows.
+struct EdgeWindow {
+    int n0;
+    uint32_t at;        // row where sequence n0 + lane begins (behind num_seqs: none)
+};
+__device__ __forceinline__ EdgeWindow edge_window(const DiagParams &p, int n0, int lane) {
+    return {n0, n0 + lane <= p.num_seqs ? seq_begin(p, n0 + lane) : 0xffffffffu};
+}
 // The edges between sequences at rows [w0, w0 + N], one bit each, and for each of them the first and the last
-// n that begins there (in between: sequences without tokens).  `from`: a lower bound on those n, moved on.
+// n that begins there (in between: sequences without tokens).  `base`: the least n that counts; `behind`: how far
+// ahead of the rows the window is laid (for a walk towards the first rows).
 template <int N>
-__device__ __forceinline__ uint32_t find_edges(const DiagParams &p, uint32_t w0, int &from, int *first, int *last, int lane) {
+__device__ __forceinline__ uint32_t find_edges(const DiagParams &p, EdgeWindow &win, uint32_t w0, int base, int behind, int *first, int *last,
+                                               int lane) {
+    const uint32_t top = __shfl_sync(~0u, win.at, 31), bottom = __shfl_sync(~0u, win.at, 0);
+    if (top < w0 || (behind > 0 && bottom >= w0 && win.n0 > base)) {
+        const int n = first_at(p, w0, base, lane) - behind;
+        win = edge_window(p, n > base ? n : base, lane);
+    }
     uint32_t mask = 0;
-    if (p.cu_seqlens == nullptr) from = first_at(p, w0, 0, lane);
-    for (int n0 = from, moved = 0;;) {
-        const int n = n0 + lane;
-        const uint32_t at = n <= p.num_seqs ? seq_begin(p, n) : 0xffffffffu;
-        const uint32_t below = __ballot_sync(~0u, at < w0);
-        if (below == ~0u) {
-            from = n0 = first_at(p, w0, n0 + 32 < p.num_seqs ? n0 + 32 : p.num_seqs, lane);
-            moved = 1;
-            continue;
-        }
-        if (!moved) {
-            from = n0 + __popc(below);
-            moved = 1;
-        }
-        const uint32_t d = at - w0;
-        const bool in = at >= w0 && d <= (uint32_t)N && n <= p.num_seqs;
-        const uint32_t bit = in ? 1u << d : 0u;
+    for (EdgeWindow v = win;;) {
+        const uint32_t d = v.at - w0;
+        const bool in = v.at >= w0 && d <= (uint32_t)N;
         if (__any_sync(~0u, in)) {
+            const uint32_t bit = in ? 1u << d : 0u;
             const uint32_t before = __shfl_up_sync(~0u, bit, 1), after = __shfl_down_sync(~0u, bit, 1);
-            if (in && !(mask & bit) && (lane == 0 || before != bit)) first[d] = n;
-            if (in && (lane == 31 || after != bit)) last[d] = n;
+            if (in && !(mask & bit) && (lane == 0 || before != bit)) first[d] = v.n0 + lane;
+            if (in && (lane == 31 || after != bit)) last[d] = v.n0 + lane;
             mask |= __reduce_or_sync(~0u, bit);
         }
-        if (__shfl_sync(~0u, (int)(n >= p.num_seqs || at > w0 + N), 31)) break;
-        n0 += 32;
+        if (__shfl_sync(~0u, v.at, 31) > w0 + N) break;        // (none behind num_seqs: 2^32 - 1)
+        v = edge_window(p, v.n0 + 32, lane);
     }
     __syncwarp();
     return mask;

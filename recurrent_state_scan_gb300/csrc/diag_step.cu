@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(128) diag_decode_kernel(const __grid_constant_
         }
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const DiagGates o = diag_gates<GATE, WEIGHT, false>(av[k], bv[k], p.has_b, l[k]);
+            const DiagGates o = diag_gates<GATE, WEIGHT>(av[k], bv[k], p.has_b, l[k]);
             F2 v = mul2(o.i, xv[k]);
             v = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(o.w, v);
             h[k] = fma2(o.alpha, h[k], v);
@@ -107,9 +107,9 @@ __global__ void __launch_bounds__(256) pack_kernel(int64_t rows, int64_t C, cons
         const IO *p = x + row * ld + c;
         const F2 v = {c < C ? IoType<IO>::ld(p) : 0.f, c + 1 < C ? IoType<IO>::ld(p + 1) : 0.f};
         const uint32_t e = code_step(__reduce_max_sync(~0u, magnitude(v)));
-        const float inv = code_inverse(e);
-        if (c < C) codes[row * C + c] = (int8_t)code_of(v.x, inv);
-        if (c + 1 < C) codes[row * C + c + 1] = (int8_t)code_of(v.y, inv);
+        const uint32_t q = codes_of(v, e);
+        if (c < C) codes[row * C + c] = (int8_t)(q & 255);
+        if (c + 1 < C) codes[row * C + c + 1] = (int8_t)(q >> 8);
         if (lane == 0) steps[i] = (uint8_t)e;
     }
 }
