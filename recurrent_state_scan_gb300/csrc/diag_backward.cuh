@@ -6,9 +6,11 @@
 //     da = dg g (1 - s) (sigmoid gate) | -dg e^A_log s (softplus gate),
 //     dA_log = sum dg g,  da_bias = sum da,  db_bias = sum db,  dstate_in = alpha G at a sequence's first row.
 // The walk is the forward pass's, from the last rows to the first: warps fold their rows to G's map and, from the kept
-// h before each tile, to h's, both with the same product of decays.  Of what the gates give only g, h and alpha (in shared
-// memory) stay for the second pass over the rows; the rest is made again from the staged rows.
+// h before each tile, to h's, both with the same product of decays.  Of what the gates give, the decays' exponents G and h stay
+// in registers for the second pass over the rows and alpha in shared memory, over the staged a; the rest is made again.
 #pragma once
+
+#include <type_traits>
 
 #include "diag_internal.cuh"
 
@@ -18,11 +20,11 @@ namespace {
 constexpr int LT = 16, W = kDiagTile / LT;      // a warp's rows; warps
 
 template <typename IO, bool CODES> struct Staged {
-    IO x[LT][kDiagSlice], a[LT][kDiagSlice], b[LT][kDiagSlice], dy[LT][kDiagSlice];
+    IO x[LT][kDiagSlice], b[LT][kDiagSlice], dy[LT][kDiagSlice], a[LT][kDiagSlice];
 };
 template <typename IO> struct Staged<IO, true> {
-    int8_t x[LT][kDiagSlice], a[LT][kDiagSlice], b[LT][kDiagSlice];
-    uint8_t xs[LT], as[LT], bs[LT];
+    int8_t x[LT][kDiagSlice], b[LT][kDiagSlice], a[LT][kDiagSlice];
+    uint8_t xs[LT], bs[LT], as[LT];
     IO dy[LT][kDiagSlice];
 };
 template <typename IO, bool CODES> struct Shared {
@@ -74,14 +76,22 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
             store_state(p.dstate_in + n * C, p.dstate_out ? load_state(p.dstate_out + n * C, c, C) : both(0.f), c, C);
         }
     const DiagLane l = diag_lane(p.A_log, p.a_bias, p.b_bias, c, C);
-    const F2 unrate = {1.f / l.rate.x, 1.f / l.rate.y};     // (a rate is a normal number or 0, whose channel's opening then counts as 0)
-    const F2 inverse = {l.rate.x != 0.f ? unrate.x : 0.f, l.rate.y != 0.f ? unrate.y : 0.f};
-    const bool fast = p.pairs && c0 + kDiagSlice <= C, has_b = p.has_b;
+    // (A rate is a normal number or 0, whose channel's gate then counts as shut.)
+    const F2 inverse = {l.rate.x != 0.f ? 1.f / l.rate.x : 0.f, l.rate.y != 0.f ? 1.f / l.rate.y : 0.f};
+    const bool fast = p.pairs && c0 + kDiagSlice <= C, has_b = p.has_b, near = diag_near<GATE>(l);
     const int64_t tile0 = part.r0 / kDiagTile, lo = part.r0, hi = part.r1;
     const int64_t tiles = hi > lo ? (hi + kDiagTile - 1) / kDiagTile - tile0 : 0;
     Staged<IO, CODES> &st = sh.rows[w];
     float2 *salpha = &sh.alpha[w][0][0];
-    const uint32_t shut = shut_bits<IO>();
+    const uint32_t shut = infinity_bits<IO>(true);
+    if (!has_b) {                   // codes of 1 with the largest step are as good as infinity
+        if constexpr (CODES) {
+            fill_rows<int8_t, LT>(&st.b[0][0], 0x01010101u, lane);
+            if (lane < LT) st.bs[lane] = 254;
+        } else {
+            fill_rows<IO, LT>(&st.b[0][0], infinity_bits<IO>(false), lane);
+        }
+    }
     auto stage = [&](int64_t w0) {
         if constexpr (CODES) {
             stage_codes(&st.x[0][0], st.xs, p, 0, slice, slices, w0, lo, hi, 0u, lane);
@@ -104,7 +114,6 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
         else return staged(&st.a[0][0], t, lane);
     };
     auto get_b = [&](int t) -> F2 {
-        if (!has_b) return both(0.f);
         if constexpr (CODES) return code_pair(&st.b[0][0], st.bs, t, lane);
         else return staged(&st.b[0][0], t, lane);
     };
@@ -116,7 +125,7 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
         const int64_t tile = tile0 + tiles - 1 - j0 - rank, w0 = tile * kDiagTile + w * LT;     // (below tile0: nothing to do)
         const int buf = step & 1;
         const bool some = tile >= tile0 && w0 < hi && w0 + LT > lo, full = some && w0 >= lo && w0 + LT <= hi;
-        F2 g[LT], u[LT], sum_g = both(0.f), H = both(0.f), D = both(0.f);
+        F2 G[LT], h[LT], sum_G = both(0.f), H = both(0.f), D = both(0.f);
         uint32_t begins = 0, ends = 0;
         if (some) {
             const uint32_t edges = find_edges<LT>(p, window, (uint32_t)w0, part.n0, 28, sh.edge_first[w], sh.edge_last[w], lane);
@@ -135,23 +144,29 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
             return v;
         };
         stage_wait();
+        const uint32_t special = begins | ends;
         if (some) {
             F2 through = both(1.f);
+            auto take = [&](auto only_near) {
 #pragma unroll
-            for (int t = 0; t < LT; ++t) {
-                const DiagGates o = diag_gates<GATE, WEIGHT>(get_a(t), get_b(t), has_b, l);
-                const F2 v = mul2(o.i, get_x(t));
-                g[t] = o.g;
-                u[t] = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(o.w, v);
-                salpha[t * 32 + lane] = make_float2(o.alpha.x, o.alpha.y);
-                sum_g = add2(sum_g, o.g);
-                if ((begins | ends) == 0) {
-                    H = fma2(o.alpha, H, u[t]);
-                    through = mul2(through, o.alpha);
+                for (int t = 0; t < LT; ++t) {
+                    G[t] = diag_exponent<GATE>(get_a(t), l);
+                    const DiagDecay d = diag_decay<decltype(only_near)::value>(G[t]);
+                    const F2 v = mul2(diag_sigmoid(get_b(t), l.nbbias), get_x(t));
+                    h[t] = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n).w, v);       // (the input, until h is known)
+                    salpha[t * 32 + lane] = make_float2(d.alpha.x, d.alpha.y);
+                    sum_G = add2(sum_G, G[t]);
+                    H = fma2(d.alpha, H, h[t]);
+                    through = mul2(through, d.alpha);
                     D = fma2(through, staged(&st.dy[0][0], t, lane), D);
                 }
-            }
-            if (begins | ends) {
+            };
+            if (near) take(std::true_type{});
+            else take(std::false_type{});
+            if (special) {
+                through = both(1.f);
+                D = both(0.f);
+                H = both(0.f);
 #pragma unroll 1
                 for (int t = 0; t < LT; ++t) {
                     if (begins & ((2u << t) - 1)) break;        // (nothing behind a sequence's first row comes back to here)
@@ -161,14 +176,14 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
 #pragma unroll
                 for (int t = 0; t < LT; ++t) {
                     if (begins >> t & 1) H = p.state_in ? load_state(p.state_in + sh.edge_last[w][t] * C, c, C) : both(0.f);
-                    H = fma2(get_pair(salpha + t * 32, lane), H, u[t]);
+                    H = fma2(get_pair(salpha + t * 32, lane), H, h[t]);
                 }
             }
         }
-        put_map(sh.maps[buf][w], lane, diag_product(sum_g, begins != 0), H);
+        put_map(sh.maps[buf][w], lane, diag_product(sum_G, begins != 0), H);
         sh.back[buf][w][lane] = make_float2(D.x, D.y);
         __syncthreads();
-        F2 G = carry;   // what comes back from the rows behind the CTA's, then behind the warp's
+        F2 next = carry;        // what comes back from the rows behind the CTA's, then behind the warp's
         if (cl > 1) {
             DiagProduct all = get_product(sh.maps[buf][W - 1], lane);
             F2 shift = get_pair(sh.back[buf][W - 1], lane);
@@ -183,80 +198,67 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
             cluster_arrive();
             cluster_wait();
             for (int r = 0; r < cl; ++r) {
-                if (r == rank) G = carry;
+                if (r == rank) next = carry;
                 carry = diag_apply(get_product(sh.cta_maps[buf][r], lane), get_pair(sh.cta_maps[buf][r].shift, lane), carry);
             }
         }
-        F2 back = G;
+        F2 back = next;
 #pragma unroll
         for (int k = W - 1; k >= 0; --k) {
-            if (k == w) back = G;
-            G = diag_apply(get_product(sh.maps[buf][k], lane), get_pair(sh.back[buf][k], lane), G);
+            if (k == w) back = next;
+            next = diag_apply(get_product(sh.maps[buf][k], lane), get_pair(sh.back[buf][k], lane), next);
         }
-        if (cl == 1) carry = G;
+        if (cl == 1) carry = next;
         if (some) {
-            F2 h = both(0.f);
-            if (tile * kDiagTile > lo) h = get_pair(reinterpret_cast<const float2 *>(p.kept + (tile * slices + slice) * kDiagSlice), lane);
+            F2 at = both(0.f);
+            if (tile * kDiagTile > lo) at = get_pair(reinterpret_cast<const float2 *>(p.kept + (tile * slices + slice) * kDiagSlice), lane);
 #pragma unroll
-            for (int k = 0; k < W; ++k)
-                if (k < w) h = diag_apply(get_product(sh.maps[buf][k], lane), get_pair(sh.maps[buf][k].shift, lane), h);
+            for (int k = 0; k < W - 1; ++k)
+                if (k < w) at = diag_apply(get_product(sh.maps[buf][k], lane), get_pair(sh.maps[buf][k].shift, lane), at);
 #pragma unroll
-            for (int t = 0; t < LT; ++t) {          // u[t] becomes the h before row t
-                if (begins >> t & 1) h = p.state_in ? load_state(p.state_in + sh.edge_last[w][t] * C, c, C) : both(0.f);
-                const F2 next = fma2(get_pair(salpha + t * 32, lane), h, u[t]);
-                u[t] = h;
-                h = next;
+            for (int t = 0; t < LT; ++t) {          // h before row t
+                if (begins >> t & 1) at = p.state_in ? load_state(p.state_in + sh.edge_last[w][t] * C, c, C) : both(0.f);
+                const F2 to = fma2(get_pair(salpha + t * 32, lane), at, h[t]);
+                h[t] = at;
+                at = to;
             }
-            IO *dx = (IO *)p.dx + w0 * p.ld_dx + c, *da = (IO *)p.da + w0 * p.ld_da + c, *db = (IO *)p.db + w0 * p.ld_db + c;
+            IO *dx = (IO *)p.dx + (w0 + LT - 1) * p.ld_dx + c, *da = (IO *)p.da + (w0 + LT - 1) * p.ld_da + c;
+            IO *db = (IO *)p.db + (w0 + LT - 1) * p.ld_db + c;
+            auto give = [&](auto only_near) {
 #pragma unroll
-            for (int t = LT - 1; t >= 0; --t) {
-                if (!full && (w0 + t < lo || w0 + t >= hi)) continue;
-                const F2 Gt = add2(get_dy(t), back), alpha = get_pair(salpha + t * 32, lane), x = get_x(t);
-                F2 in = both(1.f), nin = both(0.f);         // i and 1 - i = e^-z i
-                if (has_b) {
-                    const F2 z = fma2(get_b(t), both(-kLog2e), l.nbbias);
-                    F2 e = {ex2(z.x), ex2(z.y)};
-                    const F2 d = add2(e, both(1.f));
-                    in = {rcp(d.x), rcp(d.y)};
-                    nin = {in.x > 0.f ? e.x * in.x : 1.f, in.y > 0.f ? e.y * in.y : 1.f};
+                for (int t = LT - 1; t >= 0; --t, dx -= p.ld_dx, da -= p.ld_da, db -= p.ld_db) {
+                    F2 g = add2(staged(&st.dy[0][0], t, lane), back);          // the gradient at h_t
+                    if ((ends >> t & 1) && p.dstate_out) g = add2(g, load_state(p.dstate_out + (sh.edge_first[w][t + 1] - 1) * C, c, C));
+                    const F2 i = diag_sigmoid(get_b(t), l.nbbias), v = mul2(i, get_x(t));
+                    const DiagDecay d = diag_decay<decltype(only_near)::value>(G[t]);
+                    const DiagWeight o = diag_weigh<WEIGHT>(d.n);
+                    const F2 minus = both(-1.f);
+                    F2 slope = h[t];                                            // dg / (g alpha)
+                    if (WEIGHT == GDN_DIAG_NORM) slope = fma2(mul2(v, mul2(d.alpha, minus)), o.winv, slope);
+                    if (WEIGHT == GDN_DIAG_COMPLEMENT) slope = fma2(v, minus, slope);
+                    const F2 ag = mul2(d.alpha, g), dv = WEIGHT == GDN_DIAG_PLAIN ? g : mul2(g, o.w);
+                    const F2 dG = mul2(mul2(ag, slope), minus);                 // the gradient at G = -g
+                    const F2 dGG = mul2(dG, F2{fminf(G[t].x, 1e30f), fminf(G[t].y, 1e30f)});        // (0 of a decay to 0)
+                    const F2 sp = mul2(G[t], inverse);                          // the gate's opening
+                    const F2 da_ = GATE == GDN_DIAG_SIGMOID ? fma2(dGG, mul2(sp, minus), dGG) : mul2(dG, mul2(l.rate, diag_decay<false>(sp).n));
+                    const F2 dx_ = mul2(dv, i), dvv = mul2(dv, v), db_ = fma2(dvv, mul2(i, minus), dvv);
+                    if (full || (w0 + t >= lo && w0 + t < hi)) {
+                        sum_A = add2(sum_A, dGG);
+                        sum_a = add2(sum_a, da_);
+                        sum_b = add2(sum_b, db_);
+                        store_pair<IO>(dx, dx_, c, C, fast);
+                        store_pair<IO>(da, da_, c, C, fast);
+                        if (has_b) store_pair<IO>(db, db_, c, C, fast);
+                    }
+                    back = ag;
+                    if (begins >> t & 1) {
+                        if (p.dstate_in) store_state(p.dstate_in + sh.edge_last[w][t] * C, back, c, C);
+                        back = both(0.f);
+                    }
                 }
-                const F2 v = mul2(in, x);
-                DiagGates o;
-                F2 unused;
-                o.m = diag_expm1(g[t], unused);
-                diag_weigh<WEIGHT>(o);
-                F2 dg = mul2(alpha, u[t]);
-                if (WEIGHT == GDN_DIAG_NORM) dg = fma2(mul2(v, mul2(alpha, alpha)), F2{-o.winv.x, -o.winv.y}, dg);
-                if (WEIGHT == GDN_DIAG_COMPLEMENT) dg = fma2(v, F2{-alpha.x, -alpha.y}, dg);
-                dg = mul2(dg, Gt);
-                F2 dv = Gt;
-                if (WEIGHT != GDN_DIAG_PLAIN) dv = mul2(dv, o.w);
-                const F2 dx_ = mul2(dv, in), dgg = mul2(dg, g[t]);
-                F2 da_;
-                if (GATE == GDN_DIAG_SIGMOID) {             // dg g (1 - s), 1 - s = e^-z s, s = g / rate
-                    const F2 z = fma2(get_a(t), both(-kLog2e), l.nabias), s = mul2(g[t], inverse);
-                    const F2 e = {fminf(ex2(z.x), 0x1p126f), fminf(ex2(z.y), 0x1p126f)};
-                    da_ = mul2(dgg, mul2(e, s));
-                } else {                                    // dg rate s, s = 1 - e^-softplus, softplus = g / rate
-                    const F2 sp = mul2(g[t], inverse);
-                    const F2 s = diag_expm1({-sp.x, -sp.y}, unused);
-                    da_ = mul2(dg, mul2(l.rate, F2{-s.x, -s.y}));
-                }
-                sum_A = add2(sum_A, dgg);
-                sum_a = add2(sum_a, da_);
-                store_pair<IO>(dx + t * p.ld_dx, dx_, c, C, fast);
-                store_pair<IO>(da + t * p.ld_da, da_, c, C, fast);
-                if (has_b) {
-                    const F2 db_ = mul2(mul2(dv, v), nin);
-                    sum_b = add2(sum_b, db_);
-                    store_pair<IO>(db + t * p.ld_db, db_, c, C, fast);
-                }
-                back = mul2(alpha, Gt);
-                if (begins >> t & 1) {
-                    if (p.dstate_in) store_state(p.dstate_in + sh.edge_last[w][t] * C, back, c, C);
-                    back = both(0.f);
-                }
-            }
+            };
+            if (near) give(std::true_type{});
+            else give(std::false_type{});
         }
         __syncwarp();
         if (tile - cl >= tile0) stage(w0 - cl * kDiagTile);

@@ -68,19 +68,22 @@ cudaError_t launch_checkpoint_unpack(gdn_dtype io, int64_t rows, int64_t channel
 
 #ifdef __CUDACC__
 // ------------------------------------------------------------------ gates
-// alpha - 1 = e^g - 1 for g <= 0.  Slow decays are multiplied in thousands of times and weigh their
-// input by 1 - alpha, so both alpha and its distance from 1 have to keep their digits: down to -1/4 by
-// g + g^2 p(g), p the Chebyshev fit of (e^g - 1 - g) / g^2 (1.2e-8 of the result), whose sum with 1 is
-// then rounded once; below by the exponential, within 4e-7 of the distance.
-__device__ __forceinline__ F2 diag_expm1(F2 g, F2 &alpha) {
-    F2 p = fma2(both(0x1.f6d2c6p-8f), g, both(0x1.548062p-5f));
-    p = fma2(p, g, both(0x1.5552b2p-3f));
-    p = fma2(p, g, both(0x1.fffffep-2f));
-    const F2 near = fma2(mul2(g, g), p, g), t = mul2(g, both(kLog2e)), one = both(1.f);
-    const F2 far = {ex2(t.x), ex2(t.y)}, a = add2(near, one), m = add2(far, both(-1.f));
-    const bool nx = g.x > -0.25f, ny = g.y > -0.25f;
-    alpha = {nx ? a.x : far.x, ny ? a.y : far.y};
-    return {nx ? near.x : m.x, ny ? near.y : m.y};
+// n = 1 - e^-G and alpha = e^-G for a decay's exponent G >= 0.  Slow decays are multiplied in thousands of times and weigh their
+// input by n, so both have to keep their digits: up to 1/4 by G + G^2 r(G), r the Chebyshev fit of (1 - e^-G - G) / G^2
+// (1.2e-8 of the result), alpha being its difference from 1 rounded once; beyond by the exponential, n within 4e-7 of itself.
+// NEAR: no G is beyond.
+struct DiagDecay {
+    F2 n, alpha;
+};
+template <bool NEAR> __device__ __forceinline__ DiagDecay diag_decay(F2 G) {
+    F2 r = fma2(G, both(0x1.f6d2c6p-8f), both(-0x1.548062p-5f));
+    r = fma2(r, G, both(0x1.5552b2p-3f));
+    r = fma2(r, G, both(-0x1.fffffep-2f));
+    const F2 n = fma2(mul2(G, G), r, G), a = fma2(n, both(-1.f), both(1.f));
+    if (NEAR) return {n, a};
+    const F2 t = mul2(G, both(-kLog2e)), e = {ex2(t.x), ex2(t.y)}, far = fma2(e, both(-1.f), both(1.f));
+    const bool x = G.x < 0.25f, y = G.y < 0.25f;
+    return {{x ? n.x : far.x, y ? n.y : far.y}, {x ? a.x : e.x, y ? a.y : e.y}};
 }
 // sigmoid(v + bias); `nbias` is -bias log2 e.  e^-v beyond fp32's range gives 0.
 __device__ __forceinline__ F2 diag_sigmoid(F2 v, F2 nbias) {
@@ -88,9 +91,9 @@ __device__ __forceinline__ F2 diag_sigmoid(F2 v, F2 nbias) {
     const F2 d = add2({ex2(t.x), ex2(t.y)}, both(1.f));
     return {rcp(d.x), rcp(d.y)};
 }
-// softplus(z) = max(z, 0) + log(1 + e), e = e^-|z|, and sigmoid(z).  log(1 + e) = 2 atanh(s), s = e / (2 + e)
-// <= 1/3, by s + s^3 q(s^2), q the Chebyshev fit of the series of atanh (1.6e-8 of the result): digits
-// are kept however small e is.
+// softplus(z) = max(z, 0) + log(1 + e), e = e^-|z|.  log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by
+// s + s^3 q(s^2), q the Chebyshev fit of the series of atanh (1.6e-8 of the result): digits are kept however
+// small e is.
 __device__ __forceinline__ F2 diag_softplus(F2 z) {
     const F2 e = {ex2(-kLog2e * fabsf(z.x)), ex2(-kLog2e * fabsf(z.y))}, d = add2(e, both(2.f));
     const F2 s = mul2(e, {rcp(d.x), rcp(d.y)}), q = mul2(s, s);
@@ -103,44 +106,30 @@ __device__ __forceinline__ F2 diag_softplus(F2 z) {
 
 // The parameters of a lane's two channels.
 struct DiagLane {
-    F2 rate, abias, nabias, nbbias;   // -e^A_log, a_bias, -a_bias log2 e, -b_bias log2 e
+    F2 rate, abias, nabias, nbbias;   // e^A_log, a_bias, -a_bias log2 e, -b_bias log2 e
 };
-// What one token's gates give: g, alpha and alpha - 1, the input gate and the input's weight w (norm: and 1 / w).
-struct DiagGates {
-    F2 g, m, alpha, i, w, winv;
+// The input's weight, and for `norm` (sqrt(1 - alpha^2)) 1 / w: at alpha = 1 the weight is 0 and 1 / w finite.
+struct DiagWeight {
+    F2 w, winv;
 };
-
-template <int WEIGHT> __device__ __forceinline__ void diag_weigh(DiagGates &o) {
-    o.winv = both(0.f);
-    if (WEIGHT == GDN_DIAG_NORM) {          // sqrt(1 - alpha^2); at alpha = 1 the weight is 0 and 1 / w finite
-        const F2 q = mul2({-o.m.x, -o.m.y}, add2(o.m, both(2.f)));
-        asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(o.winv.x) : "f"(fmaxf(q.x, 0x1p-122f)));
-        asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(o.winv.y) : "f"(fmaxf(q.y, 0x1p-122f)));
-        o.w = mul2(q, o.winv);
-    } else if (WEIGHT == GDN_DIAG_COMPLEMENT) {
-        o.w = {-o.m.x, -o.m.y};
-    } else {
-        o.w = both(1.f);
-    }
-}
-
-template <int GATE, int WEIGHT>
-__device__ __forceinline__ DiagGates diag_gates(F2 a, F2 b, bool has_b, const DiagLane &l) {
-    DiagGates o;
-    o.g = mul2(l.rate, GATE == GDN_DIAG_SIGMOID ? diag_sigmoid(a, l.nabias) : diag_softplus(add2(a, l.abias)));
-    // Held finite: an alpha of 0 times it is then 0, not a NaN (a NaN itself stays one).
-    asm("max.NaN.f32 %0, %0, 0fF149F2CA;" : "+f"(o.g.x));      // -1e30
-    asm("max.NaN.f32 %0, %0, 0fF149F2CA;" : "+f"(o.g.y));
-    o.m = diag_expm1(o.g, o.alpha);
-    o.i = has_b ? diag_sigmoid(b, l.nbbias) : both(1.f);
-    diag_weigh<WEIGHT>(o);
+template <int WEIGHT> __device__ __forceinline__ DiagWeight diag_weigh(F2 n) {
+    if (WEIGHT == GDN_DIAG_COMPLEMENT) return {n, both(0.f)};
+    if (WEIGHT == GDN_DIAG_PLAIN) return {both(1.f), both(0.f)};
+    const F2 t = fma2(n, both(-1.f), both(2.f)), q = mul2(n, t), some = fma2(n, t, both(0x1p-122f));
+    DiagWeight o;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(o.winv.x) : "f"(some.x));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(o.winv.y) : "f"(some.y));
+    o.w = mul2(q, o.winv);
     return o;
+}
+template <int GATE> __device__ __forceinline__ F2 diag_exponent(F2 a, const DiagLane &l) {
+    return mul2(l.rate, GATE == GDN_DIAG_SIGMOID ? diag_sigmoid(a, l.nabias) : diag_softplus(add2(a, l.abias)));
 }
 
 __device__ __forceinline__ DiagLane diag_lane(const float *A_log, const float *a_bias, const float *b_bias, int64_t c, int64_t C) {
     DiagLane l{};
     const bool one = c < C, two = c + 1 < C;
-    l.rate = {one ? ssm_rate(A_log[c]) : 0.f, two ? ssm_rate(A_log[c + 1]) : 0.f};
+    l.rate = {one ? -ssm_rate(A_log[c]) : 0.f, two ? -ssm_rate(A_log[c + 1]) : 0.f};
     if (a_bias) l.abias = {one ? a_bias[c] : 0.f, two ? a_bias[c + 1] : 0.f};
     F2 bb = both(0.f);
     if (b_bias) bb = {one ? b_bias[c] : 0.f, two ? b_bias[c + 1] : 0.f};
@@ -148,19 +137,23 @@ __device__ __forceinline__ DiagLane diag_lane(const float *A_log, const float *a
     l.nbbias = mul2(bb, both(-kLog2e));
     return l;
 }
+// Whether no channel of a warp's can pass diag_decay's polynomial: a sigmoid gate's exponent is the rate at most.
+template <int GATE> __device__ __forceinline__ bool diag_near(const DiagLane &l) {
+    return GATE == GDN_DIAG_SIGMOID && __all_sync(~0u, l.rate.x < 0.25f && l.rate.y < 0.25f);
+}
 
 // ------------------------------------------------------------------ rows, two channels at a time
+template <typename IO> struct IoBits {
+    static constexpr bool kHalf = false;
+};
+template <> struct IoBits<__half> {
+    static constexpr bool kHalf = true;
+};
 template <typename IO> struct Pair;      // a lane's two channels of one row, as they lie in memory
 template <> struct Pair<float> {
     using Raw = float2;
     static __device__ __forceinline__ F2 wide(Raw v) { return {v.x, v.y}; }
     static __device__ __forceinline__ Raw narrow(F2 v) { return make_float2(v.x, v.y); }
-    static __device__ __forceinline__ Raw load(const float *p) {
-        Raw v;
-        asm("ld.global.nc.L1::no_allocate.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p));
-        return v;
-    }
-    static __device__ __forceinline__ Raw join(float a, float b) { return make_float2(a, b); }
 };
 template <> struct Pair<__nv_bfloat16> {
     using Raw = uint32_t;
@@ -169,14 +162,6 @@ template <> struct Pair<__nv_bfloat16> {
         Raw r;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
         return r;
-    }
-    static __device__ __forceinline__ Raw load(const __nv_bfloat16 *p) {
-        Raw v;
-        asm("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(v) : "l"(p));
-        return v;
-    }
-    static __device__ __forceinline__ Raw join(__nv_bfloat16 a, __nv_bfloat16 b) {
-        return (uint32_t)__bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16;
     }
 };
 template <> struct Pair<__half> {
@@ -191,21 +176,14 @@ template <> struct Pair<__half> {
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
         return r;
     }
-    static __device__ __forceinline__ Raw load(const __half *p) {
-        Raw v;
-        asm("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(v) : "l"(p));
-        return v;
-    }
-    static __device__ __forceinline__ Raw join(__half a, __half b) {
-        return (uint32_t)__half_as_ushort(a) | (uint32_t)__half_as_ushort(b) << 16;
-    }
 };
 
-// A token row's bits of -infinity: rows that a call does not have are staged with it as `a` and 0 as x and b, and
-// are then the identity (alpha 1, input 0) without a test.
-template <typename IO> __device__ __forceinline__ uint32_t shut_bits() { return sizeof(IO) == 4 ? 0xff800000u : 0u; }
-template <> __device__ __forceinline__ uint32_t shut_bits<__nv_bfloat16>() { return 0xff80ff80u; }
-template <> __device__ __forceinline__ uint32_t shut_bits<__half>() { return 0xfc00fc00u; }
+// The bits of -infinity and of infinity, over four bytes: rows that a call does not have are staged as x and b 0 and a -infinity,
+// and are then the identity (alpha 1, input 0) without a test; an input gate that it does not have as b infinity.
+template <typename IO> __device__ __forceinline__ uint32_t infinity_bits(bool negative) {
+    const uint32_t b = sizeof(IO) == 4 ? 0x7f800000u : sizeof(IO) == 2 && IoBits<IO>::kHalf ? 0x7c007c00u : 0x7f807f80u;
+    return negative ? b | (sizeof(IO) == 4 ? 0x80000000u : 0x80008000u) : b;
+}
 
 // Copies rows [r0, r0 + N) of a slice (channels c0 ..) to shared memory, [N][64], asynchronously where `wide` allows, by one
 // warp for itself.  Rows outside [lo, hi) become `outside`, channels behind C zeros.
@@ -219,14 +197,21 @@ __device__ __forceinline__ void stage_rows(IO *to, const IO *base, int64_t ld, i
         const int64_t c = c0 + piece * (16 / (int)sizeof(IO));
         const int bytes = c >= C ? 0 : (C - c) * (int64_t)sizeof(IO) >= 16 ? 16 : (int)((C - c) * sizeof(IO));
         const IO *from = base + (r0 + lane / kRow) * ld + (bytes ? c : 0);
-        const uint32_t at = dst + (lane / kRow * kRow + piece) * 16;
+        const int64_t apart = kStep * ld;
+        const uint32_t at = dst + lane * 16;
+        if (r0 >= lo && r0 + N <= hi) {
 #pragma unroll
-        for (int i = 0; i < N / kStep; ++i) {
-            const int64_t row = r0 + lane / kRow + i * kStep;
-            if (row >= lo && row < hi)
-                asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(at + i * 512), "l"(from + i * kStep * ld), "r"(bytes) : "memory");
-            else
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + i * 512), "r"(outside) : "memory");
+            for (int i = 0; i < N / kStep; ++i, from += apart)
+                asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(at + i * 512), "l"(from), "r"(bytes) : "memory");
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < N / kStep; ++i, from += apart) {
+                const int64_t row = r0 + lane / kRow + i * kStep;
+                if (row >= lo && row < hi)
+                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(at + i * 512), "l"(from), "r"(bytes) : "memory");
+                else
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + i * 512), "r"(outside) : "memory");
+            }
         }
         return;
     }
@@ -251,6 +236,10 @@ __device__ __forceinline__ void stage_rows(IO *to, const IO *base, int64_t ld, i
             }
         }
     }
+}
+// Fills N staged rows with four bytes.
+template <typename IO, int N> __device__ __forceinline__ void fill_rows(IO *to, uint32_t bits, int lane) {
+    for (int i = lane; i < N * kDiagSlice * (int)sizeof(IO) / 4; i += 32) reinterpret_cast<uint32_t *>(to)[i] = bits;
 }
 __device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void stage_wait() {
@@ -409,12 +398,13 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 struct DiagProduct {
     F2 hi, lo;
 };
-__device__ __forceinline__ DiagProduct diag_product(F2 sum_g, bool edge) {
+__device__ __forceinline__ DiagProduct diag_product(F2 sum_G, bool edge) {
+    const DiagDecay d = diag_decay<false>(sum_G);
     DiagProduct o;
-    const F2 m = diag_expm1(sum_g, o.hi), back = add2(o.hi, both(-1.f));
-    // Where 1 + m was rounded, what that lost; a far decay is hi itself.
-    o.lo = {sum_g.x > -0.25f ? m.x - back.x : 0.f, sum_g.y > -0.25f ? m.y - back.y : 0.f};
-    if (edge) o.hi = both(-1.f);
+    // Where 1 - n was rounded, what that lost; a far decay is hi itself.
+    const F2 lost = add2(fma2(d.alpha, both(-1.f), both(1.f)), {-d.n.x, -d.n.y});
+    o.hi = edge ? both(-1.f) : d.alpha;
+    o.lo = {sum_G.x < 0.25f ? lost.x : 0.f, sum_G.y < 0.25f ? lost.y : 0.f};
     return o;
 }
 __device__ __forceinline__ F2 diag_apply(DiagProduct p, F2 H, F2 h) {

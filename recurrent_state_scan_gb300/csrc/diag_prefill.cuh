@@ -9,6 +9,8 @@
 // long ones cost the same.
 #pragma once
 
+#include <type_traits>
+
 #include "diag_internal.cuh"
 
 namespace gdn {
@@ -37,10 +39,11 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 3 : 4) diag_prefill_
     if (part.r0 >= part.r1) return;
     if (cl > 1) cluster_arrive();
     const DiagLane l = diag_lane(p.A_log, p.a_bias, p.b_bias, c, C);
-    const bool fast = p.pairs && c0 + kDiagSlice <= C, has_b = p.has_b;
+    const bool fast = p.pairs && c0 + kDiagSlice <= C, has_b = p.has_b, near = diag_near<GATE>(l);
     const int64_t tile0 = part.r0 / kDiagTile, tiles = (part.r1 + kDiagTile - 1) / kDiagTile - tile0, lo = part.r0, hi = part.r1;
     IO *sx = &sh.rows[w][0][0][0], *sa = &sh.rows[w][1][0][0], *sb = &sh.rows[w][2][0][0];
-    const uint32_t shut = shut_bits<IO>();
+    const uint32_t shut = infinity_bits<IO>(true);
+    if (!has_b) fill_rows<IO, LT>(sb, infinity_bits<IO>(false), lane);
     auto stage = [&](int64_t w0) {
         stage_rows<IO, LT>(sx, (const IO *)p.x, p.ld_x, w0, lo, hi, c0, C, p.wide, 0u, lane);
         stage_rows<IO, LT>(sa, (const IO *)p.a, p.ld_a, w0, lo, hi, c0, C, p.wide, shut, lane);
@@ -54,7 +57,7 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 3 : 4) diag_prefill_
         const int64_t tile = tile0 + j0 + rank, w0 = tile * kDiagTile + w * LT;
         const int buf = step & 1;
         const bool some = w0 < hi && w0 + LT > lo, full = w0 >= lo && w0 + LT <= hi;
-        F2 alpha[LT], u[LT], sum_g = both(0.f), H = both(0.f);
+        F2 alpha[LT], u[LT], sum_G = both(0.f), H = both(0.f);
         uint32_t begins = 0, ends = 0;
         if (some) {
             const uint32_t edges = find_edges<LT>(p, window, (uint32_t)w0, part.n0, 0, sh.edge_first[w], sh.edge_last[w], lane);
@@ -68,14 +71,19 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 3 : 4) diag_prefill_
         }
         stage_wait();
         if (some) {
+            auto take = [&](auto only_near) {
 #pragma unroll
-            for (int t = 0; t < LT; ++t) {
-                const DiagGates o = diag_gates<GATE, WEIGHT>(staged(sa, t, lane), has_b ? staged(sb, t, lane) : both(0.f), has_b, l);
-                const F2 v = mul2(o.i, staged(sx, t, lane));
-                alpha[t] = o.alpha;
-                u[t] = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(o.w, v);
-                sum_g = add2(sum_g, o.g);
-            }
+                for (int t = 0; t < LT; ++t) {
+                    const F2 G = diag_exponent<GATE>(staged(sa, t, lane), l), i = diag_sigmoid(staged(sb, t, lane), l.nbbias);
+                    const DiagDecay d = diag_decay<decltype(only_near)::value>(G);
+                    const F2 v = mul2(i, staged(sx, t, lane));
+                    alpha[t] = d.alpha;
+                    u[t] = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n).w, v);
+                    sum_G = add2(sum_G, G);
+                }
+            };
+            if (near) take(std::true_type{});
+            else take(std::false_type{});
             if (CODES) {
                 const int64_t all = (p.rows + kDiagTile - 1) / kDiagTile * kDiagTile;
 #pragma unroll 1
@@ -113,7 +121,7 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 3 : 4) diag_prefill_
                 }
             }
         }
-        put_map(sh.maps[buf][w], lane, diag_product(sum_g, begins != 0), H);
+        put_map(sh.maps[buf][w], lane, diag_product(sum_G, begins != 0), H);
         __syncthreads();
         F2 h = carry;
         if (cl > 1) {

@@ -52,10 +52,10 @@ __global__ void __launch_bounds__(128) diag_decode_kernel(const __grid_constant_
         }
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const DiagGates o = diag_gates<GATE, WEIGHT>(av[k], bv[k], p.has_b, l[k]);
-            F2 v = mul2(o.i, xv[k]);
-            v = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(o.w, v);
-            h[k] = fma2(o.alpha, h[k], v);
+            const DiagDecay d = diag_decay<false>(diag_exponent<GATE>(av[k], l[k]));
+            F2 v = p.has_b ? mul2(diag_sigmoid(bv[k], l[k].nbbias), xv[k]) : xv[k];
+            v = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n).w, v);
+            h[k] = fma2(d.alpha, h[k], v);
         }
         if (VEC) {
             *reinterpret_cast<float4 *>(state) = make_float4(h[0].x, h[0].y, h[N - 1].x, h[N - 1].y);
