@@ -18,6 +18,7 @@ namespace gdn {
 namespace {
 
 constexpr int LT = 16, W = kDiagTile / LT;      // a warp's rows; warps
+constexpr int kGroup = 4;                       // rows whose loads go out together
 
 template <typename IO, bool CODES> struct Staged {
     IO x[LT][kDiagSlice], b[LT][kDiagSlice], dy[LT][kDiagSlice], a[LT][kDiagSlice];
@@ -149,16 +150,30 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
             F2 through = both(1.f);
             auto take = [&](auto only_near) {
 #pragma unroll
-                for (int t = 0; t < LT; ++t) {
-                    G[t] = diag_exponent<GATE>(get_a(t), l);
-                    const DiagDecay d = diag_decay<decltype(only_near)::value>(G[t]);
-                    const F2 v = mul2(diag_sigmoid(get_b(t), l.nbbias), get_x(t));
-                    h[t] = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n).w, v);       // (the input, until h is known)
-                    salpha[t * 32 + lane] = make_float2(d.alpha.x, d.alpha.y);
-                    sum_G = add2(sum_G, G[t]);
-                    H = fma2(d.alpha, H, h[t]);
-                    through = mul2(through, d.alpha);
-                    D = fma2(through, staged(&st.dy[0][0], t, lane), D);
+                for (int t0 = 0; t0 < LT; t0 += kGroup) {       // (loads of a group first: none could pass the stores of alpha)
+                    F2 a[kGroup], b[kGroup], x[kGroup], dy[kGroup], alpha[kGroup];
+#pragma unroll
+                    for (int k = 0; k < kGroup; ++k) {
+                        a[k] = get_a(t0 + k);
+                        b[k] = get_b(t0 + k);
+                        x[k] = get_x(t0 + k);
+                        dy[k] = staged(&st.dy[0][0], t0 + k, lane);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kGroup; ++k) {
+                        const int t = t0 + k;
+                        G[t] = diag_exponent<GATE>(a[k], l);
+                        const DiagDecay d = diag_decay<decltype(only_near)::value>(G[t]);
+                        const F2 v = mul2(diag_sigmoid(b[k], l.nbbias), x[k]);
+                        h[t] = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n).w, v);       // (the input, until h is known)
+                        alpha[k] = d.alpha;
+                        sum_G = add2(sum_G, G[t]);
+                        H = fma2(d.alpha, H, h[t]);
+                        through = mul2(through, d.alpha);
+                        D = fma2(through, dy[k], D);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kGroup; ++k) salpha[(t0 + k) * 32 + lane] = make_float2(alpha[k].x, alpha[k].y);
                 }
             };
             if (near) take(std::true_type{});
@@ -197,7 +212,9 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
             for (int r = w; r < cl; r += W) put_map_at(sh.cta_maps[buf][rank], r, lane, all, shift);
             cluster_arrive();
             cluster_wait();
-            for (int r = 0; r < cl; ++r) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                if (r >= cl) break;
                 if (r == rank) next = carry;
                 carry = diag_apply(get_product(sh.cta_maps[buf][r], lane), get_pair(sh.cta_maps[buf][r].shift, lane), carry);
             }
@@ -224,41 +241,64 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
             }
             IO *dx = (IO *)p.dx + (w0 + LT - 1) * p.ld_dx + c, *da = (IO *)p.da + (w0 + LT - 1) * p.ld_da + c;
             IO *db = (IO *)p.db + (w0 + LT - 1) * p.ld_db + c;
-            auto give = [&](auto only_near) {
+            // PLAIN: all rows are there, stored by pairs, and no sequence begins or ends.
+            auto give = [&](auto only_near, auto plain) {
+                constexpr bool kPlain = decltype(plain)::value;
 #pragma unroll
-                for (int t = LT - 1; t >= 0; --t, dx -= p.ld_dx, da -= p.ld_da, db -= p.ld_db) {
-                    F2 g = add2(staged(&st.dy[0][0], t, lane), back);          // the gradient at h_t
-                    if ((ends >> t & 1) && p.dstate_out) g = add2(g, load_state(p.dstate_out + (sh.edge_first[w][t + 1] - 1) * C, c, C));
-                    const F2 i = diag_sigmoid(get_b(t), l.nbbias), v = mul2(i, get_x(t));
-                    const DiagDecay d = diag_decay<decltype(only_near)::value>(G[t]);
-                    const DiagWeight o = diag_weigh<WEIGHT>(d.n);
-                    const F2 minus = both(-1.f);
-                    F2 slope = h[t];                                            // dg / (g alpha)
-                    if (WEIGHT == GDN_DIAG_NORM) slope = fma2(mul2(v, mul2(d.alpha, minus)), o.winv, slope);
-                    if (WEIGHT == GDN_DIAG_COMPLEMENT) slope = fma2(v, minus, slope);
-                    const F2 ag = mul2(d.alpha, g), dv = WEIGHT == GDN_DIAG_PLAIN ? g : mul2(g, o.w);
-                    const F2 dG = mul2(mul2(ag, slope), minus);                 // the gradient at G = -g
-                    const F2 dGG = mul2(dG, F2{fminf(G[t].x, 1e30f), fminf(G[t].y, 1e30f)});        // (0 of a decay to 0)
-                    const F2 sp = mul2(G[t], inverse);                          // the gate's opening
-                    const F2 da_ = GATE == GDN_DIAG_SIGMOID ? fma2(dGG, mul2(sp, minus), dGG) : mul2(dG, mul2(l.rate, diag_decay<false>(sp).n));
-                    const F2 dx_ = mul2(dv, i), dvv = mul2(dv, v), db_ = fma2(dvv, mul2(i, minus), dvv);
-                    if (full || (w0 + t >= lo && w0 + t < hi)) {
-                        sum_A = add2(sum_A, dGG);
-                        sum_a = add2(sum_a, da_);
-                        sum_b = add2(sum_b, db_);
-                        store_pair<IO>(dx, dx_, c, C, fast);
-                        store_pair<IO>(da, da_, c, C, fast);
-                        if (has_b) store_pair<IO>(db, db_, c, C, fast);
+                for (int t0 = LT - kGroup; t0 >= 0; t0 -= kGroup) {
+                    F2 b[kGroup], x[kGroup], dy[kGroup], alpha[kGroup];
+#pragma unroll
+                    for (int k = 0; k < kGroup; ++k) {
+                        b[k] = get_b(t0 + k);
+                        x[k] = get_x(t0 + k);
+                        dy[k] = staged(&st.dy[0][0], t0 + k, lane);
+                        alpha[k] = get_pair(salpha + (t0 + k) * 32, lane);
                     }
-                    back = ag;
-                    if (begins >> t & 1) {
-                        if (p.dstate_in) store_state(p.dstate_in + sh.edge_last[w][t] * C, back, c, C);
-                        back = both(0.f);
+                    F2 out_x[kGroup], out_a[kGroup], out_b[kGroup];
+#pragma unroll
+                    for (int k = kGroup - 1; k >= 0; --k) {
+                        const int t = t0 + k;
+                        F2 g = add2(dy[k], back);           // the gradient at h_t
+                        if (!kPlain && (ends >> t & 1) && p.dstate_out)
+                            g = add2(g, load_state(p.dstate_out + (sh.edge_first[w][t + 1] - 1) * C, c, C));
+                        const F2 i = diag_sigmoid(b[k], l.nbbias), v = mul2(i, x[k]), minus = both(-1.f);
+                        const DiagDecay d = diag_decay<decltype(only_near)::value>(G[t]);
+                        const DiagWeight o = diag_weigh<WEIGHT>(d.n);
+                        F2 slope = h[t];                                            // dg / (g alpha)
+                        if (WEIGHT == GDN_DIAG_NORM) slope = fma2(mul2(v, mul2(d.alpha, minus)), o.winv, slope);
+                        if (WEIGHT == GDN_DIAG_COMPLEMENT) slope = fma2(v, minus, slope);
+                        const F2 ag = mul2(alpha[k], g), dv = WEIGHT == GDN_DIAG_PLAIN ? g : mul2(g, o.w);
+                        const F2 dG = mul2(mul2(ag, slope), minus);                 // the gradient at G = -g
+                        const F2 dGG = mul2(dG, F2{fminf(G[t].x, 1e30f), fminf(G[t].y, 1e30f)});        // (0 of a decay to 0)
+                        const F2 sp = mul2(G[t], inverse);                          // the gate's opening
+                        const F2 da_ = GATE == GDN_DIAG_SIGMOID ? fma2(dGG, mul2(sp, minus), dGG) : mul2(dG, mul2(l.rate, diag_decay<false>(sp).n));
+                        const F2 dvv = mul2(dv, v), db_ = fma2(dvv, mul2(i, minus), dvv);
+                        out_x[k] = mul2(dv, i);
+                        out_a[k] = da_;
+                        out_b[k] = db_;
+                        if (kPlain || (w0 + t >= lo && w0 + t < hi)) {
+                            sum_A = add2(sum_A, dGG);
+                            sum_a = add2(sum_a, da_);
+                            sum_b = add2(sum_b, db_);
+                        }
+                        back = ag;
+                        if (!kPlain && (begins >> t & 1)) {
+                            if (p.dstate_in) store_state(p.dstate_in + sh.edge_last[w][t] * C, back, c, C);
+                            back = both(0.f);
+                        }
+                    }
+#pragma unroll
+                    for (int k = kGroup - 1; k >= 0; --k, dx -= p.ld_dx, da -= p.ld_da, db -= p.ld_db) {
+                        if (!kPlain && (w0 + t0 + k < lo || w0 + t0 + k >= hi)) continue;
+                        store_pair<IO>(dx, out_x[k], c, C, kPlain || fast);
+                        store_pair<IO>(da, out_a[k], c, C, kPlain || fast);
+                        if (has_b) store_pair<IO>(db, out_b[k], c, C, kPlain || fast);
                     }
                 }
             };
-            if (near) give(std::true_type{});
-            else give(std::false_type{});
+            if (!full || !fast || special) give(std::false_type{}, std::false_type{});
+            else if (near) give(std::true_type{}, std::true_type{});
+            else give(std::false_type{}, std::true_type{});
         }
         __syncwarp();
         if (tile - cl >= tile0) stage(w0 - cl * kDiagTile);

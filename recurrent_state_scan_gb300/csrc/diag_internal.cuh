@@ -350,9 +350,10 @@ __device__ __forceinline__ DiagPart diag_part(const DiagParams &p, int part, int
 struct EdgeWindow {
     int n0;
     uint32_t at;        // row where sequence n0 + lane begins (behind num_seqs: none)
+    uint32_t lo, hi;    // no edge is at rows [lo, hi)
 };
 __device__ __forceinline__ EdgeWindow edge_window(const DiagParams &p, int n0, int lane) {
-    return {n0, n0 + lane <= p.num_seqs ? seq_begin(p, n0 + lane) : 0xffffffffu};
+    return {n0, n0 + lane <= p.num_seqs ? seq_begin(p, n0 + lane) : 0xffffffffu, 0u, 0u};
 }
 // The edges between sequences at rows [w0, w0 + N], one bit each, and for each of them the first and the last
 // n that begins there (in between: sequences without tokens).  `base`: the least n that counts; `behind`: how far
@@ -360,6 +361,7 @@ __device__ __forceinline__ EdgeWindow edge_window(const DiagParams &p, int n0, i
 template <int N>
 __device__ __forceinline__ uint32_t find_edges(const DiagParams &p, EdgeWindow &win, uint32_t w0, int base, int behind, int *first, int *last,
                                                int lane) {
+    if (w0 >= win.lo && w0 + N < win.hi) return 0u;
     const uint32_t top = __shfl_sync(~0u, win.at, 31), bottom = __shfl_sync(~0u, win.at, 0);
     if (top < w0 || (behind > 0 && bottom >= w0 && win.n0 > base)) {
         const int n = first_at(p, w0, base, lane) - behind;
@@ -378,6 +380,11 @@ __device__ __forceinline__ uint32_t find_edges(const DiagParams &p, EdgeWindow &
         }
         if (__shfl_sync(~0u, v.at, 31) > w0 + N) break;        // (none behind num_seqs: 2^32 - 1)
         v = edge_window(p, v.n0 + 32, lane);
+    }
+    if (mask == 0 && __shfl_sync(~0u, win.at, 31) > w0 + N) {
+        win.lo = __reduce_max_sync(~0u, win.at < w0 ? win.at + 1 : 0u);
+        if (__shfl_sync(~0u, win.at, 0) >= w0 && win.n0 > base) win.lo = w0;
+        win.hi = __reduce_min_sync(~0u, win.at > w0 + N ? win.at : 0xffffffffu);
     }
     __syncwarp();
     return mask;

@@ -137,7 +137,9 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 3 : 4) diag_prefill_
             for (int r = w; r < cl; r += W) put_map_at(sh.cta_maps[buf][rank], r, lane, all, shift);
             cluster_arrive();
             cluster_wait();
-            for (int r = 0; r < cl; ++r) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                if (r >= cl) break;
                 if (r == rank) h = carry;
                 carry = diag_apply(get_product(sh.cta_maps[buf][r], lane), get_pair(sh.cta_maps[buf][r].shift, lane), carry);
             }
