@@ -17,43 +17,47 @@
 namespace gdn {
 namespace {
 
-constexpr int LT = 16, W = kDiagTile / LT;      // a warp's rows; warps
+constexpr int LT = 8, W = kDiagTile / LT;      // a warp's rows; warps
 constexpr int kGroup = 4;                       // rows whose loads go out together
 
+// (Each array is copied to 16 bytes at a time, the steps 8.)
 template <typename IO, bool CODES> struct Staged {
-    IO x[LT][kDiagSlice], b[LT][kDiagSlice], dy[LT][kDiagSlice], a[LT][kDiagSlice];
+    alignas(16) IO x[LT][kDiagSlice], b[LT][kDiagSlice], dy[LT][kDiagSlice], a[LT][kDiagSlice];
 };
 template <typename IO> struct Staged<IO, true> {
-    int8_t x[LT][kDiagSlice], b[LT][kDiagSlice], a[LT][kDiagSlice];
-    uint8_t xs[LT], bs[LT], as[LT];
-    IO dy[LT][kDiagSlice];
+    alignas(16) int8_t x[LT][kDiagSlice], b[LT][kDiagSlice], a[LT][kDiagSlice];
+    alignas(16) IO dy[LT][kDiagSlice];
+    alignas(16) uint8_t xs[LT], bs[LT], as[LT];
 };
+static_assert(LT * kDiagSlice % 16 == 0 && LT % 8 == 0, "what follows an array is aligned as it is");
 template <typename IO, bool CODES> struct Shared {
     Staged<IO, CODES> rows[W];
     float2 alpha[W][LT][32];
-    DiagMaps maps[2][W], cta_maps[2][8];        // (maps: h's; with `back`, G's)
-    float2 back[2][W][32];
+    DiagMaps maps[W];                   // a warp's rows: h's map, and with `back` G's
+    float2 back[W][32];
+    DiagMaps behind[W], cta_maps[2][8];             // G's: the tile's rows behind a warp's; the cluster's tiles
+    float2 start[32];                               // what comes back to the tile
     int edge_first[W][LT + 1], edge_last[W][LT + 1];
 };
 
 // Rows [r0, r0 + LT) of codes; those outside [lo, hi) as `outside`, with a step of 0 (-1.1e37: a code of 1 shuts a gate).
-__device__ __forceinline__ void stage_codes(int8_t *to, uint8_t *to_steps, const DiagParams &p, int k, int slice, int slices, int64_t r0,
-                                            int64_t lo, int64_t hi, uint32_t outside, int lane) {
+__device__ __forceinline__ void stage_codes(int8_t *to, uint8_t *to_steps, const DiagParams &p, int k, int slice, int slices, int r0,
+                                            int lo, int hi, uint32_t outside, int lane) {
     const int64_t all = (p.rows + kDiagTile - 1) / kDiagTile * kDiagTile, at = ((int64_t)k * slices + slice) * all + r0;
     const int8_t *from = p.codes + at * kDiagSlice;
     const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to)), ds = static_cast<uint32_t>(__cvta_generic_to_shared(to_steps));
     const bool full = r0 >= lo && r0 + LT <= hi;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < LT / 8; ++i) {
         const int piece = i * 32 + lane;
-        const int64_t row = r0 + piece / 4;
+        const int row = r0 + piece / 4;
         if (full || (row >= lo && row < hi))
             asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst + piece * 16), "l"(from + piece * 16) : "memory");
         else
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + piece * 16), "r"(outside) : "memory");
     }
     if (full) {
-        if (lane == 0) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ds), "l"(p.steps + at) : "memory");
+        if (lane == 0) asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ds), "l"(p.steps + at), "n"(LT) : "memory");
     } else if (lane < LT) {
         to_steps[lane] = r0 + lane >= lo && r0 + lane < hi ? p.steps[at + lane] : (uint8_t)0;
     }
@@ -64,24 +68,24 @@ __device__ __forceinline__ F2 code_pair(const int8_t *rows, const uint8_t *steps
 }
 
 template <typename IO, int GATE, int WEIGHT, bool CODES>
-__global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward_kernel(const __grid_constant__ DiagParams p) {
+__global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_constant__ DiagParams p) {
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Shared<IO, CODES> &sh = *reinterpret_cast<Shared<IO, CODES> *>(raw_shared);
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32, cl = gridDim.x, rank = blockIdx.x, slice = blockIdx.y, slices = gridDim.y;
-    const int64_t C = p.channels, c0 = (int64_t)slice * kDiagSlice, c = c0 + 2 * lane;
+    const int C = p.channels, c0 = slice * kDiagSlice, c = c0 + 2 * lane;
     if (!offsets_ok(p)) return;
     const DiagPart part = diag_part(p, blockIdx.z, lane);
     if (p.dstate_in)
         for (int n = part.n0 + rank * W + w; n < part.n1; n += cl * W) {     // sequences without tokens
             if (seq_begin(p, n) != seq_begin(p, n + 1)) continue;
-            store_state(p.dstate_in + n * C, p.dstate_out ? load_state(p.dstate_out + n * C, c, C) : both(0.f), c, C);
+            store_state(p.dstate_in + (int64_t)n * C, p.dstate_out ? load_state(p.dstate_out + (int64_t)n * C, c, C) : both(0.f), c, C);
         }
     const DiagLane l = diag_lane(p.A_log, p.a_bias, p.b_bias, c, C);
     // (A rate is a normal number or 0, whose channel's gate then counts as shut.)
     const F2 inverse = {l.rate.x != 0.f ? 1.f / l.rate.x : 0.f, l.rate.y != 0.f ? 1.f / l.rate.y : 0.f};
     const bool fast = p.pairs && c0 + kDiagSlice <= C, has_b = p.has_b, near = diag_near<GATE>(l);
-    const int64_t tile0 = part.r0 / kDiagTile, lo = part.r0, hi = part.r1;
-    const int64_t tiles = hi > lo ? (hi + kDiagTile - 1) / kDiagTile - tile0 : 0;
+    const int tile0 = part.r0 / kDiagTile, lo = part.r0, hi = part.r1;
+    const int tiles = hi > lo ? (hi + kDiagTile - 1) / kDiagTile - tile0 : 0;
     Staged<IO, CODES> &st = sh.rows[w];
     float2 *salpha = &sh.alpha[w][0][0];
     const uint32_t shut = infinity_bits<IO>(true);
@@ -93,7 +97,7 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
             fill_rows<IO, LT>(&st.b[0][0], infinity_bits<IO>(false), lane);
         }
     }
-    auto stage = [&](int64_t w0) {
+    auto stage = [&](int w0) {
         if constexpr (CODES) {
             stage_codes(&st.x[0][0], st.xs, p, 0, slice, slices, w0, lo, hi, 0u, lane);
             stage_codes(&st.a[0][0], st.as, p, 1, slice, slices, w0, lo, hi, 0x01010101u, lane);
@@ -122,8 +126,8 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
     if (tiles > rank) stage((tile0 + tiles - 1 - rank) * kDiagTile + w * LT);
     EdgeWindow window = edge_window(p, part.n0, lane);
     F2 carry = both(0.f), sum_A = both(0.f), sum_a = both(0.f), sum_b = both(0.f);
-    for (int64_t j0 = 0, step = 0; j0 < tiles; j0 += cl, ++step) {
-        const int64_t tile = tile0 + tiles - 1 - j0 - rank, w0 = tile * kDiagTile + w * LT;     // (below tile0: nothing to do)
+    for (int j0 = 0, step = 0; j0 < tiles; j0 += cl, ++step) {
+        const int tile = tile0 + tiles - 1 - j0 - rank, w0 = tile * kDiagTile + w * LT;     // (below tile0: nothing to do)
         const int buf = step & 1;
         const bool some = tile >= tile0 && w0 < hi && w0 + LT > lo, full = some && w0 >= lo && w0 + LT <= hi;
         F2 G[LT], h[LT], sum_G = both(0.f), H = both(0.f), D = both(0.f);
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
         // dy, with a final state's gradient at a sequence's last row
         auto get_dy = [&](int t) -> F2 {
             F2 v = staged(&st.dy[0][0], t, lane);
-            if ((ends >> t & 1) && p.dstate_out) v = add2(v, load_state(p.dstate_out + (sh.edge_first[w][t + 1] - 1) * C, c, C));
+            if ((ends >> t & 1) && p.dstate_out) v = add2(v, load_state(p.dstate_out + (int64_t)(sh.edge_first[w][t + 1] - 1) * C, c, C));
             return v;
         };
         stage_wait();
@@ -190,57 +194,73 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
                 }
 #pragma unroll
                 for (int t = 0; t < LT; ++t) {
-                    if (begins >> t & 1) H = p.state_in ? load_state(p.state_in + sh.edge_last[w][t] * C, c, C) : both(0.f);
+                    if (begins >> t & 1) H = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t] * C, c, C) : both(0.f);
                     H = fma2(get_pair(salpha + t * 32, lane), H, h[t]);
                 }
             }
         }
-        put_map(sh.maps[buf][w], lane, diag_product(sum_G, begins != 0), H);
-        sh.back[buf][w][lane] = make_float2(D.x, D.y);
+        put_map(sh.maps[w], lane, diag_product(sum_G, begins != 0), H);
+        sh.back[w][lane] = make_float2(D.x, D.y);
         __syncthreads();
-        F2 next = carry;        // what comes back from the rows behind the CTA's, then behind the warp's
-        if (cl > 1) {
-            DiagProduct all = get_product(sh.maps[buf][W - 1], lane);
-            F2 shift = get_pair(sh.back[buf][W - 1], lane);
+        DiagProduct all;
+        F2 shift;
+        if (w == W - 1) {
+            all = get_product(sh.maps[W - 1], lane);
+            shift = get_pair(sh.back[W - 1], lane);
 #pragma unroll
             for (int k = W - 2; k >= 0; --k) {
-                const DiagProduct m = get_product(sh.maps[buf][k], lane);
-                shift = diag_apply(m, get_pair(sh.back[buf][k], lane), shift);
+                put_map(sh.behind[k], lane, all, shift);
+                const DiagProduct m = get_product(sh.maps[k], lane);
+                shift = diag_apply(m, get_pair(sh.back[k], lane), shift);
                 all = diag_join(all, m);
             }
+        }
+        if (cl > 1) {
             if (step == 0) cluster_wait();      // (every CTA of the cluster has started)
-            for (int r = w; r < cl; r += W) put_map_at(sh.cta_maps[buf][rank], r, lane, all, shift);
-            cluster_arrive();
-            cluster_wait();
+            if (w == W - 1) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                if (r >= cl) break;
-                if (r == rank) next = carry;
-                carry = diag_apply(get_product(sh.cta_maps[buf][r], lane), get_pair(sh.cta_maps[buf][r].shift, lane), carry);
+                for (int r = 0; r < 8; ++r) {
+                    if (r >= cl) break;
+                    put_map_at(sh.cta_maps[buf][rank], r, lane, all, shift);
+                }
             }
+            cluster_arrive();
         }
-        F2 back = next;
-#pragma unroll
-        for (int k = W - 1; k >= 0; --k) {
-            if (k == w) back = next;
-            next = diag_apply(get_product(sh.maps[buf][k], lane), get_pair(sh.back[buf][k], lane), next);
-        }
-        if (cl == 1) carry = next;
-        if (some) {
+        if (some) {             // h before each row, while the cluster's maps are on their way
             F2 at = both(0.f);
-            if (tile * kDiagTile > lo) at = get_pair(reinterpret_cast<const float2 *>(p.kept + (tile * slices + slice) * kDiagSlice), lane);
+            if (tile * kDiagTile > lo) at = get_pair(reinterpret_cast<const float2 *>(p.kept + ((int64_t)tile * slices + slice) * kDiagSlice), lane);
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
-                if (k < w) at = diag_apply(get_product(sh.maps[buf][k], lane), get_pair(sh.maps[buf][k].shift, lane), at);
+                if (k < w) at = diag_apply(get_product(sh.maps[k], lane), get_pair(sh.maps[k].shift, lane), at);
 #pragma unroll
-            for (int t = 0; t < LT; ++t) {          // h before row t
-                if (begins >> t & 1) at = p.state_in ? load_state(p.state_in + sh.edge_last[w][t] * C, c, C) : both(0.f);
+            for (int t = 0; t < LT; ++t) {
+                if (begins >> t & 1) at = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t] * C, c, C) : both(0.f);
                 const F2 to = fma2(get_pair(salpha + t * 32, lane), at, h[t]);
                 h[t] = at;
                 at = to;
             }
-            IO *dx = (IO *)p.dx + (w0 + LT - 1) * p.ld_dx + c, *da = (IO *)p.da + (w0 + LT - 1) * p.ld_da + c;
-            IO *db = (IO *)p.db + (w0 + LT - 1) * p.ld_db + c;
+        }
+        if (cl > 1) cluster_wait();
+        if (w == W - 1) {
+            F2 next = carry;
+            if (cl > 1) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    if (r >= cl) break;
+                    if (r == rank) next = carry;
+                    carry = diag_apply(get_product(sh.cta_maps[buf][r], lane), get_pair(sh.cta_maps[buf][r].shift, lane), carry);
+                }
+            } else {
+                carry = diag_apply(all, shift, carry);
+            }
+            sh.start[lane] = make_float2(next.x, next.y);
+        }
+        __syncthreads();
+        F2 back = get_pair(sh.start, lane);     // what comes back from the rows behind the warp's
+        if (w < W - 1) back = diag_apply(get_product(sh.behind[w], lane), get_pair(sh.behind[w].shift, lane), back);
+        if (some) {
+            IO *dx = (IO *)p.dx + (int64_t)(w0 + LT - 1) * p.ld_dx + c, *da = (IO *)p.da + (int64_t)(w0 + LT - 1) * p.ld_da + c;
+            IO *db = (IO *)p.db + (int64_t)(w0 + LT - 1) * p.ld_db + c;
             // PLAIN: all rows are there, stored by pairs, and no sequence begins or ends.
             auto give = [&](auto only_near, auto plain) {
                 constexpr bool kPlain = decltype(plain)::value;
@@ -260,7 +280,7 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
                         const int t = t0 + k;
                         F2 g = add2(dy[k], back);           // the gradient at h_t
                         if (!kPlain && (ends >> t & 1) && p.dstate_out)
-                            g = add2(g, load_state(p.dstate_out + (sh.edge_first[w][t + 1] - 1) * C, c, C));
+                            g = add2(g, load_state(p.dstate_out + (int64_t)(sh.edge_first[w][t + 1] - 1) * C, c, C));
                         const F2 i = diag_sigmoid(b[k], l.nbbias), v = mul2(i, x[k]), minus = both(-1.f);
                         const DiagDecay d = diag_decay<decltype(only_near)::value>(G[t]);
                         const DiagWeight o = diag_weigh<WEIGHT>(d.n);
@@ -283,7 +303,7 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
                         }
                         back = ag;
                         if (!kPlain && (begins >> t & 1)) {
-                            if (p.dstate_in) store_state(p.dstate_in + sh.edge_last[w][t] * C, back, c, C);
+                            if (p.dstate_in) store_state(p.dstate_in + (int64_t)sh.edge_last[w][t] * C, back, c, C);
                             back = both(0.f);
                         }
                     }
@@ -305,6 +325,7 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
     }
     // The parameters' gradients: over the CTA's warps, the cluster's CTAs, the parts, in their order.
     __syncthreads();
+    static_assert(sizeof(sh.alpha) >= (8 + W) * 3 * kDiagSlice * sizeof(float), "the sums lie over alpha");
     float (*sums)[3][kDiagSlice] = reinterpret_cast<float (*)[3][kDiagSlice]>(&sh.alpha[0][0][0]);     // the warps' [W], then rank 0's [8]
     const F2 all[3] = {sum_A, sum_a, sum_b};
 #pragma unroll
@@ -333,7 +354,7 @@ __global__ void __launch_bounds__(W * 32, sizeof(IO) == 4 ? 2 : 3) diag_backward
                 for (int r = 0; r < cl; ++r) total[k] += sums[r][k][threadIdx.x];
             }
     }
-    const int64_t ch = c0 + threadIdx.x;
+    const int ch = c0 + threadIdx.x;
     if (threadIdx.x < kDiagSlice && ch < C) {
         float *out[3] = {p.dA_log, p.da_bias, p.db_bias};
         for (int k = 0; k < 3; ++k) {

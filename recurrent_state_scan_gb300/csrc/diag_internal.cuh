@@ -126,7 +126,7 @@ template <int GATE> __device__ __forceinline__ F2 diag_exponent(F2 a, const Diag
     return mul2(l.rate, GATE == GDN_DIAG_SIGMOID ? diag_sigmoid(a, l.nabias) : diag_softplus(add2(a, l.abias)));
 }
 
-__device__ __forceinline__ DiagLane diag_lane(const float *A_log, const float *a_bias, const float *b_bias, int64_t c, int64_t C) {
+__device__ __forceinline__ DiagLane diag_lane(const float *A_log, const float *a_bias, const float *b_bias, int c, int C) {
     DiagLane l{};
     const bool one = c < C, two = c + 1 < C;
     l.rate = {one ? -ssm_rate(A_log[c]) : 0.f, two ? -ssm_rate(A_log[c + 1]) : 0.f};
@@ -188,15 +188,15 @@ template <typename IO> __device__ __forceinline__ uint32_t infinity_bits(bool ne
 // Copies rows [r0, r0 + N) of a slice (channels c0 ..) to shared memory, [N][64], asynchronously where `wide` allows, by one
 // warp for itself.  Rows outside [lo, hi) become `outside`, channels behind C zeros.
 template <typename IO, int N>
-__device__ __forceinline__ void stage_rows(IO *to, const IO *base, int64_t ld, int64_t r0, int64_t lo, int64_t hi, int64_t c0, int64_t C,
+__device__ __forceinline__ void stage_rows(IO *to, const IO *base, int64_t ld, int r0, int lo, int hi, int c0, int C,
                                            int wide, uint32_t outside, int lane) {
     constexpr int kRow = kDiagSlice * sizeof(IO) / 16, kStep = 32 / kRow;    // 16-byte pieces of a row; rows at a time
     const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
     if (wide == 16) {
         const int piece = lane % kRow;
-        const int64_t c = c0 + piece * (16 / (int)sizeof(IO));
-        const int bytes = c >= C ? 0 : (C - c) * (int64_t)sizeof(IO) >= 16 ? 16 : (int)((C - c) * sizeof(IO));
-        const IO *from = base + (r0 + lane / kRow) * ld + (bytes ? c : 0);
+        const int c = c0 + piece * (16 / (int)sizeof(IO));
+        const int bytes = c >= C ? 0 : min(16, (C - c) * (int)sizeof(IO));
+        const IO *from = base + (int64_t)(r0 + lane / kRow) * ld + (bytes ? c : 0);
         const int64_t apart = kStep * ld;
         const uint32_t at = dst + lane * 16;
         if (r0 >= lo && r0 + N <= hi) {
@@ -206,7 +206,7 @@ __device__ __forceinline__ void stage_rows(IO *to, const IO *base, int64_t ld, i
         } else {
 #pragma unroll 1
             for (int i = 0; i < N / kStep; ++i, from += apart) {
-                const int64_t row = r0 + lane / kRow + i * kStep;
+                const int row = r0 + lane / kRow + i * kStep;
                 if (row >= lo && row < hi)
                     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(at + i * 512), "l"(from), "r"(bytes) : "memory");
                 else
@@ -216,8 +216,8 @@ __device__ __forceinline__ void stage_rows(IO *to, const IO *base, int64_t ld, i
         return;
     }
     using Raw = typename Pair<IO>::Raw;
-    const int64_t c = c0 + 2 * lane;
-    const IO *from = base + r0 * ld + c;
+    const int c = c0 + 2 * lane;
+    const IO *from = base + (int64_t)r0 * ld + c;
     const uint32_t at = dst + lane * (uint32_t)sizeof(Raw);
 #pragma unroll 4
     for (int t = 0; t < N; ++t) {
@@ -250,7 +250,7 @@ template <typename IO> __device__ __forceinline__ F2 staged(const IO *rows, int 
     return Pair<IO>::wide(reinterpret_cast<const typename Pair<IO>::Raw *>(rows)[t * 32 + lane]);
 }
 template <typename IO>
-__device__ __forceinline__ void store_pair(IO *p, F2 v, int64_t c, int64_t C, bool fast) {
+__device__ __forceinline__ void store_pair(IO *p, F2 v, int c, int C, bool fast) {
     if (fast) {
         *reinterpret_cast<typename Pair<IO>::Raw *>(p) = Pair<IO>::narrow(v);
     } else {
@@ -258,10 +258,10 @@ __device__ __forceinline__ void store_pair(IO *p, F2 v, int64_t c, int64_t C, bo
         if (c + 1 < C) IoType<IO>::st(p + 1, v.y);
     }
 }
-__device__ __forceinline__ F2 load_state(const float *p, int64_t c, int64_t C) {
+__device__ __forceinline__ F2 load_state(const float *p, int c, int C) {
     return {c < C ? p[c] : 0.f, c + 1 < C ? p[c + 1] : 0.f};
 }
-__device__ __forceinline__ void store_state(float *p, F2 v, int64_t c, int64_t C) {
+__device__ __forceinline__ void store_state(float *p, F2 v, int c, int C) {
     if (c < C) p[c] = v.x;
     if (c + 1 < C) p[c + 1] = v.y;
 }

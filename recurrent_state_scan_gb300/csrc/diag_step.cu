@@ -13,7 +13,7 @@ __global__ void __launch_bounds__(128) diag_decode_kernel(const __grid_constant_
     if (c >= C) return;
     DiagLane l[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) l[k] = diag_lane(p.A_log, p.a_bias, p.b_bias, c + 2 * k, C);
+    for (int k = 0; k < N; ++k) l[k] = diag_lane(p.A_log, p.a_bias, p.b_bias, (int)c + 2 * k, (int)C);
     for (int64_t row = blockIdx.y; row < p.batch; row += gridDim.y) {
         const int64_t e = p.slots ? p.slots[row] : row;
         if (e < 0 || e >= p.pool_size) {
