@@ -50,7 +50,7 @@
  * gdn_ssm_decode, with
  * gdn_rotary and gdn_rotary_frequencies for positions; the diagonal recurrence, forward and
  * backward: gdn_diag_prefill, gdn_diag_backward and gdn_diag_decode (with
- * gdn_diag_kept_bytes and gdn_diag_backward_workspace_bytes), and the 8-bit checkpoints of
+ * gdn_diag_kept_bytes and the workspace sizes of the first two), and the 8-bit checkpoints of
  * rows that it can train from: gdn_checkpoint_pack and gdn_checkpoint_unpack.
  *  - gdn_last_error_message() gives a human-readable detail of the last
  *    non-OK status returned on the calling thread.
@@ -614,14 +614,18 @@ typedef struct gdn_diag_shape {
  *   cu_seqlens   as gdn_prefill, but with any malformed entry the call writes nothing (and
  *                sets the device check word).  A sequence with no tokens keeps its state.
  *   kept         gdn_diag_kept_bytes(shape) bytes, 16-byte aligned (unread with KEEP_NONE).
+ *   workspace    gdn_diag_prefill_workspace_bytes(shape) bytes (0 up to 64 rows), 16-byte
+ *                aligned; its contents need no initialisation and are not preserved.
  * An infinity or a NaN reaches the rest of its channel and sequence, no other.  Outputs may
  * not overlap inputs or one another (slices of one wider row, side by side, do not).
  */
 size_t gdn_diag_kept_bytes(const gdn_diag_shape *shape);
+size_t gdn_diag_prefill_workspace_bytes(const gdn_diag_shape *shape);
 
 gdn_status gdn_diag_prefill(const gdn_diag_shape *shape, const void *x, const void *a, const void *b, const float *A_log,
                             const float *a_bias, const float *b_bias, const float *state_in, const int32_t *cu_seqlens, void *y,
-                            float *state_out, void *kept, size_t kept_bytes, void *stream);
+                            float *state_out, void *kept, size_t kept_bytes, void *workspace, size_t workspace_bytes,
+                            void *stream);
 
 /*
  * gdn_diag_backward -- the gradients of sum(y dy) + sum(state_out dstate_out), at the

@@ -7,7 +7,7 @@ from .gdn import (GdnDiagKept, GdnDiagShape, GdnError, GdnShape, gdn_causal_conv
                   gdn_checkpoint_pack, gdn_checkpoint_unpack,
                   gdn_decode_layer, gdn_decode_step, gdn_prefill_layer, gdn_decode_step_slots,
                   gdn_diag_backward, gdn_diag_backward_workspace_bytes, gdn_diag_decode, gdn_diag_kept_bytes,
-                  gdn_diag_prefill, gdn_gated_rmsnorm,
+                  gdn_diag_prefill, gdn_diag_prefill_workspace_bytes, gdn_gated_rmsnorm,
                   gdn_last_device_status,
                   gdn_prefill, gdn_prefill_noalloc, gdn_prefill_norm, gdn_prefill_variant,
                   gdn_prefill_variant_plan, gdn_prefill_variant_workspace_bytes,

@@ -88,6 +88,8 @@ gdn_status check(const gdn_diag_shape *s, bool varlen, Geometry &g) {
         if (g.rows > 1 && *to[i] > INT64_MAX / 8 / g.rows) return fail(GDN_ERR_UNSUPPORTED, "rows that far apart are not built");
     }
     const size_t slices = diag_slices(s->channels), tiles = (size_t)(g.rows + kDiagTile - 1) / kDiagTile;
+    if (tiles * slices > INT32_MAX / 2)
+        return fail(GDN_ERR_UNSUPPORTED, "%lld rows of %d channels are not built", (long long)g.rows, s->channels);
     g.kept_states = s->keep != GDN_DIAG_KEEP_NONE ? tiles * slices * kDiagSlice * 4 : 0;
     g.kept = g.kept_states;
     if (s->keep == GDN_DIAG_KEEP_8BIT) g.kept += (size_t)(2 + s->input_gate) * slices * tiles * kDiagTile * (kDiagSlice + 1);
@@ -127,10 +129,21 @@ bool by(int n, const Geometry &g, std::initializer_list<Span> spans) {
     return true;
 }
 
-// The backward pass's workspace: the parts' sums of the parameters' gradients.
-size_t partial_bytes(const Geometry &g) {
-    const int parts = diag_parts(g.rows, g.n, (int)g.C);
-    return parts > 1 ? (size_t)parts * 3 * g.C * 4 : 0;
+// Workspaces: the walk over the tiles, and in the backward pass the tiles' sums of the parameters' gradients.
+size_t walk_bytes(const Geometry &g) {
+    size_t zeroed;
+    return diag_walk_bytes(g.rows, (int)g.C, &zeroed);
+}
+size_t back_bytes(const Geometry &g) {
+    const int64_t tiles = diag_tiles(g.rows);
+    return tiles > 1 ? walk_bytes(g) + (size_t)tiles * 3 * g.C * 4 : 0;
+}
+gdn_status check_workspace(const void *workspace, size_t bytes, size_t need) {
+    if (need == 0) return GDN_OK;
+    if (workspace == nullptr || bytes < need)
+        return fail(GDN_ERR_INVALID_ARG, "workspace of %zu bytes is below the %zu this call needs", workspace == nullptr ? (size_t)0 : bytes, need);
+    if (!aligned(workspace, 16)) return fail(GDN_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    return GDN_OK;
 }
 
 void set_widths(DiagParams &p, const Geometry &g, std::initializer_list<Span> ins, std::initializer_list<Span> outs) {
@@ -143,7 +156,8 @@ DiagParams params(const gdn_diag_shape *s, const Geometry &g, void *kept) {
     p.has_b = s->input_gate != 0;
     p.ld_x = g.x; p.ld_a = g.a; p.ld_b = g.b; p.ld_y = g.y; p.ld_dx = g.dx; p.ld_da = g.da; p.ld_db = g.db;
     p.seqlen = s->seqlen; p.rows = g.rows; p.num_seqs = s->num_seqs; p.channels = s->channels;
-    p.parts = diag_parts(g.rows, g.n, s->channels);
+    const long long budget = __atomic_load_n(&g_wait_budget, __ATOMIC_RELAXED);
+    p.budget = budget > 0 ? budget : 4000000000ll;      // (about two seconds)
     if (s->keep != GDN_DIAG_KEEP_NONE) p.kept = static_cast<float *>(kept);
     if (s->keep == GDN_DIAG_KEEP_8BIT) {
         p.codes = static_cast<int8_t *>(kept) + g.kept_states;
@@ -176,15 +190,20 @@ size_t gdn_diag_kept_bytes(const gdn_diag_shape *shape) {
     return shape != nullptr && check(shape, shape->batch != shape->num_seqs, g) == GDN_OK ? g.kept : 0;
 }
 
+size_t gdn_diag_prefill_workspace_bytes(const gdn_diag_shape *shape) {
+    Geometry g;
+    return shape != nullptr && check(shape, shape->batch != shape->num_seqs, g) == GDN_OK ? walk_bytes(g) : 0;
+}
+
 size_t gdn_diag_backward_workspace_bytes(const gdn_diag_shape *shape) {
     Geometry g;
     if (shape == nullptr || check(shape, shape->batch != shape->num_seqs, g) != GDN_OK) return 0;
-    return partial_bytes(g);
+    return back_bytes(g);
 }
 
 gdn_status gdn_diag_prefill(const gdn_diag_shape *shape, const void *x, const void *a, const void *b, const float *A_log,
                             const float *a_bias, const float *b_bias, const float *state_in, const int32_t *cu_seqlens, void *y,
-                            float *state_out, void *kept, size_t kept_bytes, void *stream) {
+                            float *state_out, void *kept, size_t kept_bytes, void *workspace, size_t workspace_bytes, void *stream) {
     Geometry g;
     gdn_status st = check(shape, cu_seqlens != nullptr, g);
     if (st != GDN_OK) return st;
@@ -199,11 +218,15 @@ gdn_status gdn_diag_prefill(const gdn_diag_shape *shape, const void *x, const vo
     if (A_log == nullptr || state_out == nullptr) return fail(GDN_ERR_INVALID_ARG, "A_log or state_out is NULL");
     const size_t sbytes = (size_t)g.n * g.C * 4;
     const Span si = flat("state_in", state_in == state_out ? nullptr : state_in, sbytes);
-    const Span outs[] = {sy, flat("state_out", state_out, sbytes), flat("kept", g.kept ? kept : nullptr, g.kept)};
+    const size_t need = walk_bytes(g);
+    const Span outs[] = {sy, flat("state_out", state_out, sbytes), flat("kept", g.kept ? kept : nullptr, g.kept),
+                         flat("workspace", need ? workspace : nullptr, need)};
     const Span ins[] = {sx, sa, sb, si};
-    st = none_overlap(outs, 3, ins, 4);
+    st = check_workspace(workspace, workspace_bytes, need);
+    if (st == GDN_OK) st = none_overlap(outs, 4, ins, 4);
     if (st != GDN_OK) return st;
     DiagParams p = params(shape, g, kept);
+    diag_walk_layout(p, workspace);
     st = device_check_word(&p.status);
     if (st != GDN_OK) return st;
     p.x = x; p.a = a; p.b = b; p.y = y;
@@ -237,16 +260,14 @@ gdn_status gdn_diag_backward(const gdn_diag_shape *shape, const void *x, const v
     if (A_log == nullptr) return fail(GDN_ERR_INVALID_ARG, "A_log is NULL");
     const size_t sbytes = (size_t)g.n * g.C * 4, cbytes = (size_t)g.C * 4;
     DiagParams p = params(shape, g, const_cast<void *>(kept));
-    const size_t used = partial_bytes(g);
-    if (used > 0) {
-        if (workspace == nullptr || workspace_bytes < used)
-            return fail(GDN_ERR_INVALID_ARG, "workspace of %zu bytes is below the %zu this call needs",
-                        workspace == nullptr ? (size_t)0 : workspace_bytes, used);
-        if (!aligned(workspace, 16)) return fail(GDN_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
-    }
+    const size_t need = back_bytes(g);
+    st = check_workspace(workspace, workspace_bytes, need);
+    if (st != GDN_OK) return st;
+    diag_walk_layout(p, workspace);
+    if (need > 0) p.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + walk_bytes(g));
     const Span outs[] = {sdx, sda, sdb, flat("dA_log", dA_log, cbytes), flat("da_bias", da_bias, cbytes),
                          flat("db_bias", has_b ? db_bias : nullptr, cbytes), flat("dstate_in", dstate_in, sbytes),
-                         flat("workspace", used ? workspace : nullptr, used)};
+                         flat("workspace", need ? workspace : nullptr, need)};
     const Span ins[] = {sx, sa, sb, sdy, flat("A_log", A_log, cbytes), flat("a_bias", a_bias, cbytes),
                         flat("b_bias", has_b ? b_bias : nullptr, cbytes), flat("state_in", state_in, sbytes),
                         flat("dstate_out", dstate_out, sbytes), flat("kept", kept, g.kept)};
@@ -258,7 +279,6 @@ gdn_status gdn_diag_backward(const gdn_diag_shape *shape, const void *x, const v
     p.A_log = A_log; p.a_bias = a_bias; p.b_bias = has_b ? b_bias : nullptr;
     p.state_in = state_in; p.cu_seqlens = cu_seqlens; p.dstate_out = dstate_out; p.dstate_in = dstate_in;
     p.dA_log = dA_log; p.da_bias = da_bias; p.db_bias = has_b ? db_bias : nullptr;
-    p.partial = static_cast<float *>(workspace);
     set_widths(p, g, {sx, sa, sb, sdy}, {sdx, sda, sdb});
     const cudaError_t e = launch_diag_backward(p, (gdn_dtype)shape->io_dtype, shape->gate, shape->weighting, (cudaStream_t)stream);
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "diagonal recurrence's backward launch: %s", cudaGetErrorString(e));

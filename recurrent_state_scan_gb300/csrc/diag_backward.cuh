@@ -5,7 +5,7 @@
 //     dx = G w i,   db = dx x (1 - i),   dg = G (alpha h_{t-1} + i x w'(g)),   w' = -alpha^2 / w | -alpha | 0,
 //     da = dg g (1 - s) (sigmoid gate) | -dg e^A_log s (softplus gate),
 //     dA_log = sum dg g,  da_bias = sum da,  db_bias = sum db,  dstate_in = alpha G at a sequence's first row.
-// The walk is the forward pass's, from the last rows to the first: warps fold their rows to G's map and, from the kept
+// The walk is the forward pass's, from the last tile to the first: warps fold their rows to G's map and, from the kept
 // h before each tile, to h's, both with the same product of decays.  Of what the gates give, the decays' exponents G and h stay
 // in registers for the second pass over the rows and alpha in shared memory, over the staged a; the rest is made again.
 #pragma once
@@ -35,8 +35,10 @@ template <typename IO, bool CODES> struct Shared {
     float2 alpha[W][LT][32];
     DiagMaps maps[W];                   // a warp's rows: h's map, and with `back` G's
     float2 back[W][32];
-    DiagMaps behind[W], cta_maps[2][8];             // G's: the tile's rows behind a warp's; the cluster's tiles
-    float2 start[32];                               // what comes back to the tile
+    DiagMaps behind[W];                 // G's: the tile's rows behind a warp's
+    float2 start[32];                   // what comes back to the tile
+    float2 sums[W][3][32];              // the parameters' gradients
+    uint32_t next;
     int edge_first[W][LT + 1], edge_last[W][LT + 1];
 };
 
@@ -71,21 +73,17 @@ template <typename IO, int GATE, int WEIGHT, bool CODES>
 __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_constant__ DiagParams p) {
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Shared<IO, CODES> &sh = *reinterpret_cast<Shared<IO, CODES> *>(raw_shared);
-    const int lane = threadIdx.x % 32, w = threadIdx.x / 32, cl = gridDim.x, rank = blockIdx.x, slice = blockIdx.y, slices = gridDim.y;
-    const int C = p.channels, c0 = slice * kDiagSlice, c = c0 + 2 * lane;
+    const int lane = threadIdx.x % 32, w = threadIdx.x / 32, C = p.channels, slices = (C + kDiagSlice - 1) / kDiagSlice;
     if (!offsets_ok(p)) return;
-    const DiagPart part = diag_part(p, blockIdx.z, lane);
     if (p.dstate_in)
-        for (int n = part.n0 + rank * W + w; n < part.n1; n += cl * W) {     // sequences without tokens
+        for (int n = blockIdx.x; n < p.num_seqs; n += gridDim.x) {      // sequences without tokens
             if (seq_begin(p, n) != seq_begin(p, n + 1)) continue;
-            store_state(p.dstate_in + (int64_t)n * C, p.dstate_out ? load_state(p.dstate_out + (int64_t)n * C, c, C) : both(0.f), c, C);
+            for (int c = threadIdx.x; c < C; c += W * 32) p.dstate_in[(int64_t)n * C + c] = p.dstate_out ? p.dstate_out[(int64_t)n * C + c] : 0.f;
         }
-    const DiagLane l = diag_lane(p.A_log, p.a_bias, p.b_bias, c, C);
-    // (A rate is a normal number or 0, whose channel's gate then counts as shut.)
-    const F2 inverse = {l.rate.x != 0.f ? 1.f / l.rate.x : 0.f, l.rate.y != 0.f ? 1.f / l.rate.y : 0.f};
-    const bool fast = p.pairs && c0 + kDiagSlice <= C, has_b = p.has_b, near = diag_near<GATE>(l);
-    const int tile0 = part.r0 / kDiagTile, lo = part.r0, hi = part.r1;
-    const int tiles = hi > lo ? (hi + kDiagTile - 1) / kDiagTile - tile0 : 0;
+    const int rows = (int)p.rows, tiles = (rows + kDiagTile - 1) / kDiagTile;
+    const DiagWalk walk{p, tiles, slices, lane};
+    const uint32_t items = walk.items();
+    const bool has_b = p.has_b;
     Staged<IO, CODES> &st = sh.rows[w];
     float2 *salpha = &sh.alpha[w][0][0];
     const uint32_t shut = infinity_bits<IO>(true);
@@ -97,17 +95,18 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
             fill_rows<IO, LT>(&st.b[0][0], infinity_bits<IO>(false), lane);
         }
     }
-    auto stage = [&](int w0) {
+    auto stage = [&](uint32_t item) {
+        const int slice = item % slices, w0 = (tiles - 1 - (int)(item / slices)) * kDiagTile + w * LT, c0 = slice * kDiagSlice;
         if constexpr (CODES) {
-            stage_codes(&st.x[0][0], st.xs, p, 0, slice, slices, w0, lo, hi, 0u, lane);
-            stage_codes(&st.a[0][0], st.as, p, 1, slice, slices, w0, lo, hi, 0x01010101u, lane);
-            if (has_b) stage_codes(&st.b[0][0], st.bs, p, 2, slice, slices, w0, lo, hi, 0u, lane);
+            stage_codes(&st.x[0][0], st.xs, p, 0, slice, slices, w0, 0, rows, 0u, lane);
+            stage_codes(&st.a[0][0], st.as, p, 1, slice, slices, w0, 0, rows, 0x01010101u, lane);
+            if (has_b) stage_codes(&st.b[0][0], st.bs, p, 2, slice, slices, w0, 0, rows, 0u, lane);
         } else {
-            stage_rows<IO, LT>(&st.x[0][0], (const IO *)p.x, p.ld_x, w0, lo, hi, c0, C, p.wide, 0u, lane);
-            stage_rows<IO, LT>(&st.a[0][0], (const IO *)p.a, p.ld_a, w0, lo, hi, c0, C, p.wide, shut, lane);
-            if (has_b) stage_rows<IO, LT>(&st.b[0][0], (const IO *)p.b, p.ld_b, w0, lo, hi, c0, C, p.wide, 0u, lane);
+            stage_rows<IO, LT>(&st.x[0][0], (const IO *)p.x, p.ld_x, w0, 0, rows, c0, C, p.wide, 0u, lane);
+            stage_rows<IO, LT>(&st.a[0][0], (const IO *)p.a, p.ld_a, w0, 0, rows, c0, C, p.wide, shut, lane);
+            if (has_b) stage_rows<IO, LT>(&st.b[0][0], (const IO *)p.b, p.ld_b, w0, 0, rows, c0, C, p.wide, 0u, lane);
         }
-        stage_rows<IO, LT>(&st.dy[0][0], (const IO *)p.dy, p.ld_y, w0, lo, hi, c0, C, p.wide, 0u, lane);
+        stage_rows<IO, LT>(&st.dy[0][0], (const IO *)p.dy, p.ld_y, w0, 0, rows, c0, C, p.wide, 0u, lane);
         stage_commit();
     };
     auto get_x = [&](int t) -> F2 {
@@ -122,23 +121,34 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
         if constexpr (CODES) return code_pair(&st.b[0][0], st.bs, t, lane);
         else return staged(&st.b[0][0], t, lane);
     };
-    if (tiles > 0 && cl > 1) cluster_arrive();
-    if (tiles > rank) stage((tile0 + tiles - 1 - rank) * kDiagTile + w * LT);
-    EdgeWindow window = edge_window(p, part.n0, lane);
-    F2 carry = both(0.f), sum_A = both(0.f), sum_a = both(0.f), sum_b = both(0.f);
-    for (int j0 = 0, step = 0; j0 < tiles; j0 += cl, ++step) {
-        const int tile = tile0 + tiles - 1 - j0 - rank, w0 = tile * kDiagTile + w * LT;     // (below tile0: nothing to do)
-        const int buf = step & 1;
-        const bool some = tile >= tile0 && w0 < hi && w0 + LT > lo, full = some && w0 >= lo && w0 + LT <= hi;
+    // The parameters' gradients of an item, over the CTA's warps in their order.
+    auto put_sums = [&](uint32_t item) {
+        const int k = threadIdx.x / kDiagSlice, ch = item % slices * kDiagSlice + threadIdx.x % kDiagSlice;
+        if (k > 2 || ch >= C) return;
+        float total = 0.f;
+        for (int r = 0; r < W; ++r) total += reinterpret_cast<const float *>(sh.sums[r][k])[threadIdx.x % kDiagSlice];
+        float *one[3] = {p.dA_log, p.da_bias, p.db_bias};
+        if (tiles > 1) p.partial[((int64_t)(item / slices) * 3 + k) * C + ch] = total;
+        else if (one[k]) one[k][ch] = total;
+    };
+    EdgeWindow window = edge_window(p, 0, lane);
+    uint32_t item = walk.first(sh.next), last = items;
+    if (item < items) stage(item);
+    while (item < items) {
+        if (threadIdx.x == 0) sh.next = walk.ticket();
+        const int j = item / slices, tile = tiles - 1 - j, slice = item % slices, w0 = tile * kDiagTile + w * LT, c0 = slice * kDiagSlice;
+        const int c = c0 + 2 * lane;
+        const DiagLane l = diag_lane(p.A_log, p.a_bias, p.b_bias, c, C);
+        // (A rate is a normal number or 0, whose channel's gate then counts as shut.)
+        const F2 inverse = {l.rate.x != 0.f ? 1.f / l.rate.x : 0.f, l.rate.y != 0.f ? 1.f / l.rate.y : 0.f};
+        const bool fast = p.pairs && c0 + kDiagSlice <= C, near = diag_near<GATE>(l);
+        F2 sum_A = both(0.f), sum_a = both(0.f), sum_b = both(0.f);
+        const bool some = w0 < rows, full = w0 + LT <= rows;
         F2 G[LT], h[LT], sum_G = both(0.f), H = both(0.f), D = both(0.f);
         uint32_t begins = 0, ends = 0;
         if (some) {
-            const uint32_t edges = find_edges<LT>(p, window, (uint32_t)w0, part.n0, 28, sh.edge_first[w], sh.edge_last[w], lane);
-            uint32_t live = (1u << LT) - 1;
-            if (!full) {
-                if (w0 < lo) live &= ~0u << (lo - w0);
-                if (w0 + LT > hi) live &= (1u << (hi - w0)) - 1;
-            }
+            const uint32_t edges = find_edges<LT>(p, window, (uint32_t)w0, 0, 28, sh.edge_first[w], sh.edge_last[w], lane);
+            const uint32_t live = (1u << (full ? LT : rows - w0)) - 1;
             begins = edges & live;
             ends = edges >> 1 & live;
         }
@@ -202,11 +212,11 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
         put_map(sh.maps[w], lane, diag_product(sum_G, begins != 0), H);
         sh.back[w][lane] = make_float2(D.x, D.y);
         __syncthreads();
-        DiagProduct all;
-        F2 shift;
+        const uint32_t next = sh.next;
+        if (last < items) put_sums(last);
         if (w == W - 1) {
-            all = get_product(sh.maps[W - 1], lane);
-            shift = get_pair(sh.back[W - 1], lane);
+            DiagProduct all = get_product(sh.maps[W - 1], lane);
+            F2 shift = get_pair(sh.back[W - 1], lane);
 #pragma unroll
             for (int k = W - 2; k >= 0; --k) {
                 put_map(sh.behind[k], lane, all, shift);
@@ -214,21 +224,14 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
                 shift = diag_apply(m, get_pair(sh.back[k], lane), shift);
                 all = diag_join(all, m);
             }
+            if (tile > 0) walk.hand_on_map(j, slice, all, shift);
+            const F2 in = walk.come_in(j, slice);
+            sh.start[lane] = make_float2(in.x, in.y);
+            if (tile > 0) walk.hand_on(j, slice, diag_apply(all, shift, in));
         }
-        if (cl > 1) {
-            if (step == 0) cluster_wait();      // (every CTA of the cluster has started)
-            if (w == W - 1) {
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    if (r >= cl) break;
-                    put_map_at(sh.cta_maps[buf][rank], r, lane, all, shift);
-                }
-            }
-            cluster_arrive();
-        }
-        if (some) {             // h before each row, while the cluster's maps are on their way
+        if (some) {             // h before each row, while the last warp waits
             F2 at = both(0.f);
-            if (tile * kDiagTile > lo) at = get_pair(reinterpret_cast<const float2 *>(p.kept + ((int64_t)tile * slices + slice) * kDiagSlice), lane);
+            if (tile > 0) at = get_pair(reinterpret_cast<const float2 *>(p.kept + ((int64_t)tile * slices + slice) * kDiagSlice), lane);
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
                 if (k < w) at = diag_apply(get_product(sh.maps[k], lane), get_pair(sh.maps[k].shift, lane), at);
@@ -239,21 +242,6 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
                 h[t] = at;
                 at = to;
             }
-        }
-        if (cl > 1) cluster_wait();
-        if (w == W - 1) {
-            F2 next = carry;
-            if (cl > 1) {
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    if (r >= cl) break;
-                    if (r == rank) next = carry;
-                    carry = diag_apply(get_product(sh.cta_maps[buf][r], lane), get_pair(sh.cta_maps[buf][r].shift, lane), carry);
-                }
-            } else {
-                carry = diag_apply(all, shift, carry);
-            }
-            sh.start[lane] = make_float2(next.x, next.y);
         }
         __syncthreads();
         F2 back = get_pair(sh.start, lane);     // what comes back from the rows behind the warp's
@@ -296,7 +284,7 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
                         out_x[k] = mul2(dv, i);
                         out_a[k] = da_;
                         out_b[k] = db_;
-                        if (kPlain || (w0 + t >= lo && w0 + t < hi)) {
+                        if (kPlain || w0 + t < rows) {
                             sum_A = add2(sum_A, dGG);
                             sum_a = add2(sum_a, da_);
                             sum_b = add2(sum_b, db_);
@@ -309,7 +297,7 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
                     }
 #pragma unroll
                     for (int k = kGroup - 1; k >= 0; --k, dx -= p.ld_dx, da -= p.ld_da, db -= p.ld_db) {
-                        if (!kPlain && (w0 + t0 + k < lo || w0 + t0 + k >= hi)) continue;
+                        if (!kPlain && w0 + t0 + k >= rows) continue;
                         store_pair<IO>(dx, out_x[k], c, C, kPlain || fast);
                         store_pair<IO>(da, out_a[k], c, C, kPlain || fast);
                         if (has_b) store_pair<IO>(db, out_b[k], c, C, kPlain || fast);
@@ -320,68 +308,26 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
             else if (near) give(std::true_type{}, std::true_type{});
             else give(std::false_type{}, std::true_type{});
         }
-        __syncwarp();
-        if (tile - cl >= tile0) stage(w0 - cl * kDiagTile);
-    }
-    // The parameters' gradients: over the CTA's warps, the cluster's CTAs, the parts, in their order.
-    __syncthreads();
-    static_assert(sizeof(sh.alpha) >= (8 + W) * 3 * kDiagSlice * sizeof(float), "the sums lie over alpha");
-    float (*sums)[3][kDiagSlice] = reinterpret_cast<float (*)[3][kDiagSlice]>(&sh.alpha[0][0][0]);     // the warps' [W], then rank 0's [8]
-    const F2 all[3] = {sum_A, sum_a, sum_b};
+        const F2 all_sums[3] = {sum_A, sum_a, sum_b};
 #pragma unroll
-    for (int k = 0; k < 3; ++k) *reinterpret_cast<float2 *>(&sums[8 + w][k][2 * lane]) = make_float2(all[k].x, all[k].y);
+        for (int k = 0; k < 3; ++k) sh.sums[w][k][lane] = make_float2(all_sums[k].x, all_sums[k].y);
+        __syncwarp();
+        if (next < items) stage(next);
+        last = item;
+        item = next;
+    }
     __syncthreads();
-    float total[3] = {0.f, 0.f, 0.f};
-    if (threadIdx.x < kDiagSlice)
-        for (int k = 0; k < 3; ++k)
-            for (int r = 0; r < W; ++r) total[k] += sums[8 + r][k][threadIdx.x];
-    if (cl > 1) {
-        cluster_arrive();               // (every CTA is done with its alphas)
-        cluster_wait();
-        if (threadIdx.x < kDiagSlice)
-            for (int k = 0; k < 3; ++k) {
-                const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(&sums[rank][k][threadIdx.x]));
-                uint32_t there;
-                asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(here));
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(total[k]) : "memory");
-            }
-        cluster_arrive();
-        cluster_wait();
-        if (rank != 0) return;
-        if (threadIdx.x < kDiagSlice)
-            for (int k = 0; k < 3; ++k) {
-                total[k] = 0.f;
-                for (int r = 0; r < cl; ++r) total[k] += sums[r][k][threadIdx.x];
-            }
-    }
-    const int ch = c0 + threadIdx.x;
-    if (threadIdx.x < kDiagSlice && ch < C) {
-        float *out[3] = {p.dA_log, p.da_bias, p.db_bias};
-        for (int k = 0; k < 3; ++k) {
-            if (p.parts > 1) p.partial[((int64_t)blockIdx.z * 3 + k) * C + ch] = total[k];
-            else if (out[k]) out[k][ch] = total[k];
-        }
-    }
+    if (last < items) put_sums(last);
 }
 
 template <typename IO, int GATE, int WEIGHT> cudaError_t launch(const DiagParams &p, cudaStream_t stream) {
     const auto kernel = p.codes ? diag_backward_kernel<IO, GATE, WEIGHT, true> : diag_backward_kernel<IO, GATE, WEIGHT, false>;
     const size_t shared = p.codes ? sizeof(Shared<IO, true>) : sizeof(Shared<IO, false>);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+    if (e == cudaSuccess) e = diag_clear(p, stream);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    const int cl = diag_cluster(p.rows);
-    cfg.gridDim = dim3(cl, diag_slices(p.channels), p.parts);
-    cfg.blockDim = dim3(W * 32);
-    cfg.dynamicSmemBytes = shared;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = cl;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    kernel<<<diag_grid(p, 2), W * 32, shared, stream>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace

@@ -22,7 +22,6 @@ struct DiagParams {
     const int32_t *cu_seqlens;           // may be null
     int64_t seqlen, rows;
     int32_t num_seqs, channels;
-    int32_t parts;                       // stretches of whole sequences that run side by side
     int32_t wide;                        // bytes that every input row can be copied by: 16, a pair's, or 0: by the element
     bool pairs;                          // every output row can be written two channels at a time
     int *status;
@@ -36,7 +35,12 @@ struct DiagParams {
     void *dx, *da, *db;
     int64_t ld_dx, ld_da, ld_db;
     float *dA_log, *da_bias, *db_bias, *dstate_in;   // each may be null
-    float *partial;                      // [parts][3][channels]: sums of the parameters' gradients, with several parts
+    float *partial;                      // [tiles][3][channels]: a tile's sums of the parameters' gradients
+    // The walk over the tiles (see DiagWalk).
+    uint32_t *ticket, *flags;
+    float4 *product;
+    float2 *shift, *after;
+    long long budget;                    // cycles that a wait for an earlier tile may take
 };
 
 struct DiagDecodeParams {
@@ -54,8 +58,13 @@ struct DiagDecodeParams {
 };
 
 int diag_slices(int channels);
-int diag_cluster(int64_t rows);
-int diag_parts(int64_t rows, int64_t num_seqs, int channels);
+int64_t diag_tiles(int64_t rows);
+// Bytes of a walk's workspace, of which the first `zeroed` are cleared by the launch (0: one tile a slice, nothing to hand on).
+size_t diag_walk_bytes(int64_t rows, int channels, size_t *zeroed);
+void diag_walk_layout(DiagParams &p, void *workspace);
+cudaError_t diag_clear(const DiagParams &p, cudaStream_t stream);
+// CTAs of a walk: one for each item, up to `per_sm` on each of 152 SMs (a single row of tiles: always one for each).
+unsigned diag_grid(const DiagParams &p, int per_sm);
 template <typename IO> cudaError_t diag_prefill_by_kind(const DiagParams &p, int gate, int weighting, cudaStream_t s);
 template <typename IO> cudaError_t diag_backward_by_kind(const DiagParams &p, int gate, int weighting, cudaStream_t s);
 cudaError_t launch_diag_prefill(const DiagParams &p, gdn_dtype io, int gate, int weighting, cudaStream_t stream);
@@ -327,25 +336,6 @@ __device__ __forceinline__ int first_at(const DiagParams &p, uint32_t row, int l
     }
     return lo < p.num_seqs ? lo : p.num_seqs;
 }
-// Part `part`'s sequences [n0, n1) and rows [r0, r1): whole sequences, about rows / parts rows.
-struct DiagPart {
-    int n0, n1;
-    uint32_t r0, r1;
-};
-__device__ __forceinline__ DiagPart diag_part(const DiagParams &p, int part, int lane) {
-    DiagPart o;
-    if (p.parts == 1) return {0, p.num_seqs, 0u, (uint32_t)p.rows};
-    if (p.cu_seqlens == nullptr) {
-        o.n0 = (int)((int64_t)part * p.num_seqs / p.parts);
-        o.n1 = (int)((int64_t)(part + 1) * p.num_seqs / p.parts);
-    } else {
-        o.n0 = part == 0 ? 0 : first_at(p, (uint32_t)(part * p.rows / p.parts), 0, lane);
-        o.n1 = part + 1 == p.parts ? p.num_seqs : first_at(p, (uint32_t)((part + 1) * p.rows / p.parts), 0, lane);
-    }
-    o.r0 = seq_begin(p, o.n0);
-    o.r1 = seq_begin(p, o.n1);
-    return o;
-}
 // 32 sequences' first rows, one to a lane, kept while a warp walks along the rows.
 struct EdgeWindow {
     int n0;
@@ -390,14 +380,7 @@ __device__ __forceinline__ uint32_t find_edges(const DiagParams &p, EdgeWindow &
     return mask;
 }
 
-// ------------------------------------------------------------------ clusters
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// ------------------------------------------------------------------ maps
 // A stretch of tokens as the map h -> (hi + lo) h + H: the product of its decays in two fp32 numbers, because the
 // chain of these maps over a long sequence has to keep slow decays (hi alone drifts: 65,536 equal tokens of
 // 1 - 3e-5 by up to 2e-3) as well as the digits of fast ones.  hi = -1 marks a stretch that holds an edge, the
@@ -441,14 +424,76 @@ __device__ __forceinline__ void put_map(DiagMaps &m, int lane, DiagProduct p, F2
     m.product[lane] = make_float4(p.hi.x, p.hi.y, p.lo.x, p.lo.y);
     m.shift[lane] = make_float2(H.x, H.y);
 }
-// The same at another CTA of the cluster.
-__device__ __forceinline__ void put_map_at(DiagMaps &m, uint32_t rank, int lane, DiagProduct p, F2 H) {
-    uint32_t a, b;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&m.product[lane]))), "r"(rank));
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&m.shift[lane]))), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(p.hi.x), "f"(p.hi.y), "f"(p.lo.x), "f"(p.lo.y) : "memory");
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(b), "f"(H.x), "f"(H.y) : "memory");
-}
+
+// ------------------------------------------------------------------ the walk over the tiles
+// CTAs take (tile, slice) items off one counter, tile by tile in the order of the walk, each while it works on the item before,
+// whose rows' place the next ones are fetched to.  An item hands on its map as soon as it has it, and what is behind it (h after
+// the tile, G before it) once it knows what came in: that is found from the nearest earlier item that has handed on the
+// latter, and the maps between, applied in the order of the rows: the same arithmetic from whichever item it starts, so results do
+// not depend on timing.  The earliest unfinished item never waits, and its CTA is running, so every wait ends.
+struct DiagWalk {
+    const DiagParams &p;
+    int tiles, slices, lane;
+
+    __device__ __forceinline__ uint32_t items() const { return (uint32_t)tiles * (uint32_t)slices; }
+    // The next item: only CTAs that run hold any.  (A single row of tiles has nothing to wait for: an item for each CTA.)
+    __device__ __forceinline__ uint32_t ticket() const { return tiles > 1 ? atomicAdd(p.ticket, 1u) : items(); }
+    __device__ __forceinline__ uint32_t first(uint32_t &shared) const {
+        if (threadIdx.x == 0) shared = tiles > 1 ? atomicAdd(p.ticket, 1u) : blockIdx.x;
+        __syncthreads();
+        const uint32_t item = shared;
+        __syncthreads();
+        return item;
+    }
+    __device__ __forceinline__ int64_t at(int j, int slice) const { return (int64_t)slice * tiles + j; }
+    __device__ __forceinline__ void flag(int64_t i, uint32_t v) const {
+        __syncwarp();
+        if (lane == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.flags + i), "r"(v) : "memory");
+    }
+    __device__ __forceinline__ void hand_on_map(int j, int slice, DiagProduct m, F2 H) const {
+        const int64_t i = at(j, slice);
+        __stcg(p.product + i * 32 + lane, make_float4(m.hi.x, m.hi.y, m.lo.x, m.lo.y));
+        __stcg(p.shift + i * 32 + lane, make_float2(H.x, H.y));
+        flag(i, 1u);
+    }
+    __device__ __forceinline__ void hand_on(int j, int slice, F2 h) const {
+        const int64_t i = at(j, slice);
+        __stcg(p.after + i * 32 + lane, make_float2(h.x, h.y));
+        flag(i, 2u);
+    }
+    // What comes in to the j-th tile of a slice, by one warp.  A wait that runs out is reported, and takes 0.
+    __device__ __forceinline__ F2 come_in(int j, int slice) const {
+        if (j == 0) return both(0.f);
+        const int64_t base = at(0, slice);
+        const int k = j - 1 - lane;
+        int maps = 0;
+        const long long t0 = clock64();
+        for (;;) {
+            uint32_t f = 2;
+            if (k >= 0) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(f) : "l"(p.flags + base + k) : "memory");
+            const uint32_t done = __ballot_sync(~0u, f == 2), some = __ballot_sync(~0u, f != 0);
+            maps = __ffs(done) - 1;
+            if (done != 0 && (~some & ((1u << maps) - 1)) == 0) break;
+            if (__any_sync(~0u, clock64() - t0 > p.budget)) {
+                if (lane == 0) atomicOr(p.status, kDevTimeout);
+                return both(0.f);
+            }
+        }
+        F2 h = both(0.f);
+        int from = j - 1 - maps;
+        if (from >= 0) {
+            const float2 v = __ldcg(p.after + (base + from) * 32 + lane);
+            h = {v.x, v.y};
+        }
+#pragma unroll 4
+        for (++from; from < j; ++from) {
+            const float4 m = __ldcg(p.product + (base + from) * 32 + lane);
+            const float2 v = __ldcg(p.shift + (base + from) * 32 + lane);
+            h = diag_apply({{m.x, m.y}, {m.z, m.w}}, {v.x, v.y}, h);
+        }
+        return h;
+    }
+};
 #endif  // __CUDACC__
 
 }  // namespace gdn

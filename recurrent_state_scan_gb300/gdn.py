@@ -31,7 +31,7 @@ EXPORTS = ("gdn_prefill_workspace_bytes", "gdn_prefill", "gdn_decode_step",
            "gdn_prefill_norm", "gdn_prefill_variant_workspace_bytes", "gdn_prefill_variant_plan",
            "gdn_prefill_layer", "gdn_prefill_layer_workspace_bytes", "gdn_ssm_prefill_workspace_bytes",
            "gdn_ssm_prefill", "gdn_ssm_prefill_plan", "gdn_ssm_decode", "gdn_rotary", "gdn_rotary_frequencies",
-           "gdn_diag_kept_bytes", "gdn_diag_prefill", "gdn_diag_backward_workspace_bytes", "gdn_diag_backward",
+           "gdn_diag_kept_bytes", "gdn_diag_prefill_workspace_bytes", "gdn_diag_prefill", "gdn_diag_backward_workspace_bytes", "gdn_diag_backward",
            "gdn_diag_decode", "gdn_checkpoint_pack", "gdn_checkpoint_unpack")
 PATH_SIMT, PATH_TC, PATH_TC_TP = 1, 2, 3
 # gdn_rule codes.
@@ -219,10 +219,12 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     DS = ctypes.POINTER(GdnDiagShape)
     lib.gdn_diag_kept_bytes.restype = ctypes.c_size_t
     lib.gdn_diag_kept_bytes.argtypes = [DS]
+    lib.gdn_diag_prefill_workspace_bytes.restype = ctypes.c_size_t
+    lib.gdn_diag_prefill_workspace_bytes.argtypes = [DS]
     lib.gdn_diag_backward_workspace_bytes.restype = ctypes.c_size_t
     lib.gdn_diag_backward_workspace_bytes.argtypes = [DS]
     lib.gdn_diag_prefill.restype = ctypes.c_int
-    lib.gdn_diag_prefill.argtypes = [DS, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.gdn_diag_prefill.argtypes = [DS, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P, ctypes.c_size_t, P]
     lib.gdn_diag_backward.restype = ctypes.c_int
     lib.gdn_diag_backward.argtypes = [DS, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P, P, P, P, P, P, P, P, P, P,
                                       ctypes.c_size_t, P]
@@ -1103,12 +1105,16 @@ def gdn_diag_kept_bytes(shape: GdnDiagShape) -> int:
     return int(load().gdn_diag_kept_bytes(ctypes.byref(shape)))
 
 
+def gdn_diag_prefill_workspace_bytes(shape: GdnDiagShape) -> int:
+    return int(load().gdn_diag_prefill_workspace_bytes(ctypes.byref(shape)))
+
+
 def gdn_diag_backward_workspace_bytes(shape: GdnDiagShape) -> int:
     return int(load().gdn_diag_backward_workspace_bytes(ctypes.byref(shape)))
 
 
 def gdn_diag_prefill(x, a, b, A_log, *, a_bias=None, b_bias=None, gate: str = "softplus", weighting: str = "norm", state_in=None,
-                     cu_seqlens=None, keep=None, y=None, state_out=None, kept=None, stream=None):
+                     cu_seqlens=None, keep=None, y=None, state_out=None, kept=None, workspace=None, stream=None):
     """The diagonal recurrence over whole sequences: h_t = alpha_t h_{t-1} + w_t sigmoid(b_t + b_bias) x_t per channel, with
     alpha_t = exp(-exp(A_log) softplus(a_t + a_bias)) (gate 'softplus') or exp(-exp(A_log) sigmoid(a_t + a_bias))
     ('sigmoid') and w_t = 1 ('plain'), 1 - alpha_t ('complement') or sqrt(1 - alpha_t^2) ('norm').
@@ -1140,9 +1146,14 @@ def gdn_diag_prefill(x, a, b, A_log, *, a_bias=None, b_bias=None, gate: str = "s
         ref = ctypes.byref(shape)
         if keep is not None and kept is None:
             kept = torch.empty(lib.gdn_diag_kept_bytes(ref), dtype=torch.uint8, device=x.device)
-        held = 0 if kept is None else kept.numel()
+        need = lib.gdn_diag_prefill_workspace_bytes(ref)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _check(lib.gdn_diag_prefill(ref, px, pa, pb, pA, pab, pbb, psi, pcu, py, _arg("state_out", state_out, states, f32, dev),
-                                    _arg("kept", kept, None, torch.uint8, dev), held, _raw_stream(dev)))
+                                    _arg("kept", kept, None, torch.uint8, dev), 0 if kept is None else kept.numel(),
+                                    None if workspace is None else _arg("workspace", workspace, None, workspace.dtype, dev), ws_bytes,
+                                    _raw_stream(dev)))
     return y, state_out, None if keep is None else GdnDiagKept(kept, io, B, T, n, C, gate, weighting, b is not None, keep)
 
 

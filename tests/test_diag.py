@@ -213,7 +213,7 @@ GOOD = dict(io_dtype=gdn.GDN_BF16, batch=2, seqlen=8, num_seqs=2, channels=64, g
 WHERE = {name: 0x100000 * (k + 1) for k, name in enumerate(
     ("x", "a", "b", "A_log", "a_bias", "b_bias", "state_in", "y", "state_out", "kept", "dy", "dstate_out", "dx", "da", "db", "dA_log", "da_bias",
      "db_bias", "dstate_in", "workspace", "state"))}
-CALLS = {"prefill": ("x", "a", "b", "A_log", "a_bias", "b_bias", "state_in", "cu", "y", "state_out", "kept", "kept_bytes", "stream"),
+CALLS = {"prefill": ("x", "a", "b", "A_log", "a_bias", "b_bias", "state_in", "cu", "y", "state_out", "kept", "kept_bytes", "workspace", "workspace_bytes", "stream"),
          "backward": ("x", "a", "b", "A_log", "a_bias", "b_bias", "state_in", "cu", "kept", "kept_bytes", "dy", "dstate_out", "dx", "da", "db",
                       "dA_log", "da_bias", "db_bias", "dstate_in", "workspace", "workspace_bytes", "stream"),
          "decode": ("x", "a", "b", "A_log", "a_bias", "b_bias", "state", "pool_size", "slots", "y", "stream")}
@@ -231,7 +231,7 @@ def call(which, shape=None, **where):
     (dict(io_dtype=3), 1), (dict(seqlen=-1), 1), (dict(batch=-2, num_seqs=-2), 1), (dict(num_seqs=3), 1), (dict(channels=0), 1),
     (dict(channels=-5), 1), (dict(channels=65535 * 64 + 1), 2), (dict(gate=2), 1), (dict(gate=-1), 1), (dict(weighting=3), 1),
     (dict(input_gate=2), 1), (dict(keep=3), 1), (dict(x_stride=63), 1), (dict(b_stride=1), 1), (dict(y_stride=-64), 1), (dict(dx_stride=2), 1),
-    (dict(seqlen=1 << 30), 2), (dict(seqlen=1 << 62), 2), (dict(x_stride=1 << 62), 2)])
+    (dict(seqlen=1 << 30), 2), (dict(seqlen=1 << 62), 2), (dict(x_stride=1 << 62), 2), (dict(seqlen=1 << 29, channels=1 << 20), 2)])
 def test_refused_shapes(which, shape, status):
     assert call(which, shape) == status
     assert gdn.load().gdn_last_error_message().decode()
@@ -256,14 +256,13 @@ def test_refused_pointers(which, where):
     assert gdn.load().gdn_last_error_message().decode()
 
 
-def test_refusals_of_the_backward_pass():
+def test_refused_workspaces():
     assert call("backward", dict(keep=0)) == gdn.GDN_ERR_INVALID_ARG
-    several = dict(batch=4, num_seqs=4, seqlen=2048)
-    need = gdn.gdn_diag_backward_workspace_bytes(gdn.GdnDiagShape(**dict(GOOD, **several)))
-    assert need > 0
-    assert call("backward", several, workspace_bytes=need - 1) == gdn.GDN_ERR_INVALID_ARG
-    assert call("backward", several, workspace=None) == gdn.GDN_ERR_INVALID_ARG
-    assert call("backward", several, workspace=WHERE["workspace"] + 4) == gdn.GDN_ERR_INVALID_ARG
+    long = dict(batch=4, num_seqs=4, seqlen=20)
+    for which, size in (("prefill", gdn.gdn_diag_prefill_workspace_bytes), ("backward", gdn.gdn_diag_backward_workspace_bytes)):
+        assert size(gdn.GdnDiagShape(**GOOD)) == 0 < (need := size(gdn.GdnDiagShape(**dict(GOOD, **long))))
+        for bad in (dict(workspace_bytes=need - 1), dict(workspace=None), dict(workspace=WHERE["workspace"] + 4), dict(workspace=WHERE["a"])):
+            assert call(which, long, **bad) == gdn.GDN_ERR_INVALID_ARG, (which, bad)
 
 
 def test_slices_of_one_row_lie_beside_one_another():
@@ -375,7 +374,7 @@ def test_long_rows(lens, packed, C, keep):
     """Many steps of a cluster, and several parts side by side."""
     m = draw("f32", lens, C, packed=packed, seed=11)
     shape = gdn.GdnDiagShape(0, 1 if packed else len(lens), sum(lens) if packed else lens[0], len(lens), C, 1, 2, 1, 1)
-    assert (gdn.gdn_diag_backward_workspace_bytes(shape) > 0) == (len(lens) > 1)
+    assert gdn.gdn_diag_backward_workspace_bytes(shape) > gdn.gdn_diag_prefill_workspace_bytes(shape) > 0
     y, state, kept = prefill(m, keep)
     check(m, (y, state))
     check_gradients(m, backward(m, kept), keep == "8bit")
@@ -726,6 +725,39 @@ def test_a_pool_beyond_32_bits():
 
 
 # ------------------------------------------------------------------ streams, graphs
+@pytest.mark.gpu
+def test_a_wait_that_runs_out_is_reported():
+    """A budget below one poll of an earlier tile: the call says so, ends, and the next ones are as before."""
+    m = draw("bf16", [5300, 300], 256, seed=14)
+    y, state, kept = prefill(m, "states")
+    want = (y, state, *backward(m, kept))
+    gdn.gdn_set_wait_budget(1)
+    try:
+        lib.gdn_diag_prefill(m["x"], m["a"], m["b"], m["A_log"], state_in=m["state"], cu_seqlens=m["cu"], keep="states", **kinds(m))
+        assert lib.gdn_last_device_status() == gdn.GDN_ERR_TIMEOUT
+        lib.gdn_diag_backward(m["dy"], kept, m["A_log"], x=m["x"], a=m["a"], b=m["b"], a_bias=m["a_bias"], b_bias=m["b_bias"],
+                              state_in=m["state"], cu_seqlens=m["cu"])
+        assert lib.gdn_last_device_status() == gdn.GDN_ERR_TIMEOUT
+    finally:
+        gdn.gdn_set_wait_budget(0)
+    y, state, kept = prefill(m, "states")
+    assert all(torch.equal(s, t) for s, t in zip((y, state, *backward(m, kept)), want))
+
+
+@pytest.mark.gpu
+def test_one_workspace_for_calls_in_turn():
+    """Whatever an earlier call, or nothing, left in it."""
+    m = draw("f32", [700, 500], 130, seed=15)
+    shape = gdn.GdnDiagShape(0, 1, 1200, 2, 130, 1, 2, 1, 1)
+    work = torch.full((gdn.gdn_diag_backward_workspace_bytes(shape),), 255, dtype=torch.uint8, device="cuda")
+    y, state, kept = prefill(m, "states")
+    want = backward(m, kept)
+    for _ in range(3):
+        y2, state2, kept2 = prefill(m, "states", workspace=work)
+        got = backward(m, kept2, workspace=work)
+        assert torch.equal(y, y2) and torch.equal(state, state2) and all(torch.equal(s, t) for s, t in zip(want, got))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("keep", ["states", "8bit"])
 def test_two_graphs_and_an_eager_call(keep):
