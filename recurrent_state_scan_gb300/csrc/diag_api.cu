@@ -130,10 +130,7 @@ bool by(int n, const Geometry &g, std::initializer_list<Span> spans) {
 }
 
 // Workspaces: the walk over the tiles, and in the backward pass the tiles' sums of the parameters' gradients.
-size_t walk_bytes(const Geometry &g) {
-    size_t zeroed;
-    return diag_walk_bytes(g.rows, (int)g.C, &zeroed);
-}
+size_t walk_bytes(const Geometry &g) { return diag_walk_bytes(g.rows, (int)g.C); }
 size_t back_bytes(const Geometry &g) {
     const int64_t tiles = diag_tiles(g.rows);
     return tiles > 1 ? walk_bytes(g) + (size_t)tiles * 3 * g.C * 4 : 0;

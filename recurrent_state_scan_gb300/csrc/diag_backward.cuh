@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
         }
     }
     auto stage = [&](uint32_t item) {
-        const int slice = item % slices, w0 = (tiles - 1 - (int)(item / slices)) * kDiagTile + w * LT, c0 = slice * kDiagSlice;
+        const int j = walk.tile_of(item), slice = (int)item - j * slices, w0 = (tiles - 1 - j) * kDiagTile + w * LT, c0 = slice * kDiagSlice;
         if constexpr (CODES) {
             stage_codes(&st.x[0][0], st.xs, p, 0, slice, slices, w0, 0, rows, 0u, lane);
             stage_codes(&st.a[0][0], st.as, p, 1, slice, slices, w0, 0, rows, 0x01010101u, lane);
@@ -123,12 +123,12 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
     };
     // The parameters' gradients of an item, over the CTA's warps in their order.
     auto put_sums = [&](uint32_t item) {
-        const int k = threadIdx.x / kDiagSlice, ch = item % slices * kDiagSlice + threadIdx.x % kDiagSlice;
+        const int k = threadIdx.x / kDiagSlice, j = walk.tile_of(item), ch = ((int)item - j * slices) * kDiagSlice + threadIdx.x % kDiagSlice;
         if (k > 2 || ch >= C) return;
         float total = 0.f;
         for (int r = 0; r < W; ++r) total += reinterpret_cast<const float *>(sh.sums[r][k])[threadIdx.x % kDiagSlice];
         float *one[3] = {p.dA_log, p.da_bias, p.db_bias};
-        if (tiles > 1) p.partial[((int64_t)(item / slices) * 3 + k) * C + ch] = total;
+        if (tiles > 1) p.partial[((int64_t)j * 3 + k) * C + ch] = total;
         else if (one[k]) one[k][ch] = total;
     };
     EdgeWindow window = edge_window(p, 0, lane);
@@ -136,11 +136,9 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
     if (item < items) stage(item);
     while (item < items) {
         if (threadIdx.x == 0) sh.next = walk.ticket();
-        const int j = item / slices, tile = tiles - 1 - j, slice = item % slices, w0 = tile * kDiagTile + w * LT, c0 = slice * kDiagSlice;
+        const int j = walk.tile_of(item), tile = tiles - 1 - j, slice = (int)item - j * slices, w0 = tile * kDiagTile + w * LT, c0 = slice * kDiagSlice;
         const int c = c0 + 2 * lane;
-        const DiagLane l = diag_lane(p.A_log, p.a_bias, p.b_bias, c, C);
-        // (A rate is a normal number or 0, whose channel's gate then counts as shut.)
-        const F2 inverse = {l.rate.x != 0.f ? 1.f / l.rate.x : 0.f, l.rate.y != 0.f ? 1.f / l.rate.y : 0.f};
+        const DiagLane l = diag_lane(p, c, slices);
         const bool fast = p.pairs && c0 + kDiagSlice <= C, near = diag_near<GATE>(l);
         F2 sum_A = both(0.f), sum_a = both(0.f), sum_b = both(0.f);
         const bool some = w0 < rows, full = w0 + LT <= rows;
@@ -278,7 +276,7 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
                         const F2 ag = mul2(alpha[k], g), dv = WEIGHT == GDN_DIAG_PLAIN ? g : mul2(g, o.w);
                         const F2 dG = mul2(mul2(ag, slope), minus);                 // the gradient at G = -g
                         const F2 dGG = mul2(dG, F2{fminf(G[t].x, 1e30f), fminf(G[t].y, 1e30f)});        // (0 of a decay to 0)
-                        const F2 sp = mul2(G[t], inverse);                          // the gate's opening
+                        const F2 sp = mul2(G[t], l.inverse);                          // the gate's opening
                         const F2 da_ = GATE == GDN_DIAG_SIGMOID ? fma2(dGG, mul2(sp, minus), dGG) : mul2(dG, mul2(l.rate, diag_decay<false>(sp).n));
                         const F2 dvv = mul2(dv, v), db_ = fma2(dvv, mul2(i, minus), dvv);
                         out_x[k] = mul2(dv, i);
@@ -324,7 +322,7 @@ template <typename IO, int GATE, int WEIGHT> cudaError_t launch(const DiagParams
     const auto kernel = p.codes ? diag_backward_kernel<IO, GATE, WEIGHT, true> : diag_backward_kernel<IO, GATE, WEIGHT, false>;
     const size_t shared = p.codes ? sizeof(Shared<IO, true>) : sizeof(Shared<IO, false>);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
-    if (e == cudaSuccess) e = diag_clear(p, stream);
+    if (e == cudaSuccess) e = diag_begin(p, stream);
     if (e != cudaSuccess) return e;
     kernel<<<diag_grid(p, 2), W * 32, shared, stream>>>(p);
     return cudaGetLastError();

@@ -40,6 +40,8 @@ struct DiagParams {
     uint32_t *ticket, *flags;
     float4 *product;
     float2 *shift, *after;
+    float *table;                        // [5][slices * 64]: the channels' parameters (DiagLane), or null
+    uint32_t magic, magic_shift;         // item / slices as (item * magic) >> magic_shift, for items below 2^31
     long long budget;                    // cycles that a wait for an earlier tile may take
 };
 
@@ -59,10 +61,11 @@ struct DiagDecodeParams {
 
 int diag_slices(int channels);
 int64_t diag_tiles(int64_t rows);
-// Bytes of a walk's workspace, of which the first `zeroed` are cleared by the launch (0: one tile a slice, nothing to hand on).
-size_t diag_walk_bytes(int64_t rows, int channels, size_t *zeroed);
+// Bytes of a walk's workspace (0: one tile a slice, nothing to hand on).
+size_t diag_walk_bytes(int64_t rows, int channels);
 void diag_walk_layout(DiagParams &p, void *workspace);
-cudaError_t diag_clear(const DiagParams &p, cudaStream_t stream);
+// The walk's first kernel: clears the counter and the flags and makes the table.
+cudaError_t diag_begin(const DiagParams &p, cudaStream_t stream);
 // CTAs of a walk: one for each item, up to `per_sm` on each of 152 SMs (a single row of tiles: always one for each).
 unsigned diag_grid(const DiagParams &p, int per_sm);
 template <typename IO> cudaError_t diag_prefill_by_kind(const DiagParams &p, int gate, int weighting, cudaStream_t s);
@@ -115,7 +118,7 @@ __device__ __forceinline__ F2 diag_softplus(F2 z) {
 
 // The parameters of a lane's two channels.
 struct DiagLane {
-    F2 rate, abias, nabias, nbbias;   // e^A_log, a_bias, -a_bias log2 e, -b_bias log2 e
+    F2 rate, inverse, abias, nabias, nbbias;   // e^A_log, 1 / e^A_log (or 0), a_bias, -a_bias log2 e, -b_bias log2 e
 };
 // The input's weight, and for `norm` (sqrt(1 - alpha^2)) 1 / w: at alpha = 1 the weight is 0 and 1 / w finite.
 struct DiagWeight {
@@ -139,12 +142,22 @@ __device__ __forceinline__ DiagLane diag_lane(const float *A_log, const float *a
     DiagLane l{};
     const bool one = c < C, two = c + 1 < C;
     l.rate = {one ? -ssm_rate(A_log[c]) : 0.f, two ? -ssm_rate(A_log[c + 1]) : 0.f};
+    // (A rate is a normal number or 0, whose channel's gate then counts as shut.)
+    l.inverse = {l.rate.x != 0.f ? 1.f / l.rate.x : 0.f, l.rate.y != 0.f ? 1.f / l.rate.y : 0.f};
     if (a_bias) l.abias = {one ? a_bias[c] : 0.f, two ? a_bias[c + 1] : 0.f};
     F2 bb = both(0.f);
     if (b_bias) bb = {one ? b_bias[c] : 0.f, two ? b_bias[c + 1] : 0.f};
     l.nabias = mul2(l.abias, both(-kLog2e));
     l.nbbias = mul2(bb, both(-kLog2e));
     return l;
+}
+// The same from the walk's table, which its first kernel makes.
+__device__ __forceinline__ DiagLane diag_lane(const DiagParams &p, int c, int slices) {
+    if (p.table == nullptr) return diag_lane(p.A_log, p.a_bias, p.b_bias, c, p.channels);
+    const float2 *t = reinterpret_cast<const float2 *>(p.table + c);
+    const int row = slices * (kDiagSlice / 2);
+    const float2 v[5] = {t[0], t[row], t[2 * row], t[3 * row], t[4 * row]};
+    return {{v[0].x, v[0].y}, {v[1].x, v[1].y}, {v[2].x, v[2].y}, {v[3].x, v[3].y}, {v[4].x, v[4].y}};
 }
 // Whether no channel of a warp's can pass diag_decay's polynomial: a sigmoid gate's exponent is the rate at most.
 template <int GATE> __device__ __forceinline__ bool diag_near(const DiagLane &l) {
@@ -436,6 +449,7 @@ struct DiagWalk {
     int tiles, slices, lane;
 
     __device__ __forceinline__ uint32_t items() const { return (uint32_t)tiles * (uint32_t)slices; }
+    __device__ __forceinline__ int tile_of(uint32_t item) const { return (int)((uint64_t)item * p.magic >> p.magic_shift); }
     // The next item: only CTAs that run hold any.  (A single row of tiles has nothing to wait for: an item for each CTA.)
     __device__ __forceinline__ uint32_t ticket() const { return tiles > 1 ? atomicAdd(p.ticket, 1u) : items(); }
     __device__ __forceinline__ uint32_t first(uint32_t &shared) const {

@@ -6,26 +6,57 @@ namespace gdn {
 int diag_slices(int channels) { return (int)(((int64_t)channels + kDiagSlice - 1) / kDiagSlice); }
 int64_t diag_tiles(int64_t rows) { return (rows + kDiagTile - 1) / kDiagTile; }
 
-size_t diag_walk_bytes(int64_t rows, int channels, size_t *zeroed) {
-    const size_t items = (size_t)diag_tiles(rows) * diag_slices(channels);
-    if (diag_tiles(rows) < 2) return *zeroed = 0;
-    *zeroed = 256 + (items * 4 + 255) / 256 * 256;
-    return *zeroed + items * (sizeof(float4) + 2 * sizeof(float2)) * 32;
+namespace {
+struct WalkLayout {
+    size_t flags, table, product, shift, after, total;      // behind the counter, which comes first
+};
+WalkLayout walk_layout(int64_t rows, int channels) {
+    const size_t slices = diag_slices(channels), items = (size_t)diag_tiles(rows) * slices;
+    WalkLayout l;
+    l.flags = 256;
+    l.table = l.flags + (items * 4 + 255) / 256 * 256;
+    l.product = l.table + 5 * slices * kDiagSlice * sizeof(float);
+    l.shift = l.product + items * 32 * sizeof(float4);
+    l.after = l.shift + items * 32 * sizeof(float2);
+    l.total = l.after + items * 32 * sizeof(float2);
+    return l;
 }
+
+__global__ void __launch_bounds__(256) diag_begin_kernel(const __grid_constant__ DiagParams p, uint32_t words) {
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x, all = gridDim.x * 256;
+    for (uint32_t k = i; k < words; k += all) p.ticket[k] = 0u;         // (the flags lie behind it)
+    const int slices = (p.channels + kDiagSlice - 1) / kDiagSlice, row = slices * kDiagSlice;
+    for (int c = 2 * (int)i; c < row; c += 2 * (int)all) {
+        const DiagLane l = diag_lane(p.A_log, p.a_bias, p.b_bias, c, p.channels);
+        const F2 v[5] = {l.rate, l.inverse, l.abias, l.nabias, l.nbbias};
+        for (int k = 0; k < 5; ++k) *reinterpret_cast<float2 *>(p.table + (int64_t)k * row + c) = make_float2(v[k].x, v[k].y);
+    }
+}
+}  // namespace
+
+size_t diag_walk_bytes(int64_t rows, int channels) { return diag_tiles(rows) < 2 ? 0 : walk_layout(rows, channels).total; }
 void diag_walk_layout(DiagParams &p, void *workspace) {
-    size_t zeroed;
-    if (diag_walk_bytes(p.rows, p.channels, &zeroed) == 0) return;
+    const uint32_t slices = diag_slices(p.channels);
+    int bits = 0;
+    while ((1ull << bits) < slices) ++bits;
+    p.magic = (uint32_t)(((1ull << (31 + bits)) + slices - 1) / slices);
+    p.magic_shift = 31 + bits;
+    if (diag_tiles(p.rows) < 2) return;
+    const WalkLayout l = walk_layout(p.rows, p.channels);
     uint8_t *at = static_cast<uint8_t *>(workspace);
-    const size_t items = (size_t)diag_tiles(p.rows) * diag_slices(p.channels);
     p.ticket = reinterpret_cast<uint32_t *>(at);
-    p.flags = reinterpret_cast<uint32_t *>(at + 256);
-    p.product = reinterpret_cast<float4 *>(at + zeroed);
-    p.shift = reinterpret_cast<float2 *>(p.product + items * 32);
-    p.after = p.shift + items * 32;
+    p.flags = reinterpret_cast<uint32_t *>(at + l.flags);
+    p.table = reinterpret_cast<float *>(at + l.table);
+    p.product = reinterpret_cast<float4 *>(at + l.product);
+    p.shift = reinterpret_cast<float2 *>(at + l.shift);
+    p.after = reinterpret_cast<float2 *>(at + l.after);
 }
-cudaError_t diag_clear(const DiagParams &p, cudaStream_t stream) {
-    size_t zeroed;
-    return diag_walk_bytes(p.rows, p.channels, &zeroed) == 0 ? cudaSuccess : cudaMemsetAsync(p.ticket, 0, zeroed, stream);
+cudaError_t diag_begin(const DiagParams &p, cudaStream_t stream) {
+    if (diag_tiles(p.rows) < 2) return cudaSuccess;
+    const uint32_t words = (uint32_t)((uint8_t *)p.table - (uint8_t *)p.ticket) / 4;
+    const uint32_t blocks = (words + 1023) / 1024;
+    diag_begin_kernel<<<blocks < 16 ? 16 : blocks > 608 ? 608 : blocks, 256, 0, stream>>>(p, words);
+    return cudaGetLastError();
 }
 unsigned diag_grid(const DiagParams &p, int per_sm) {
     const int64_t items = diag_tiles(p.rows) * diag_slices(p.channels), most = 152 * per_sm;
