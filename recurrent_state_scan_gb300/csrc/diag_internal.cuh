@@ -37,9 +37,8 @@ struct DiagParams {
     float *dA_log, *da_bias, *db_bias, *dstate_in;   // each may be null
     float *partial;                      // [tiles][3][channels]: a tile's sums of the parameters' gradients
     // The walk over the tiles (see DiagWalk).
-    uint32_t *ticket, *flags;
-    float4 *product;
-    float2 *shift, *after;
+    uint32_t *ticket;
+    unsigned long long *words;           // [slice][tile][4][32]: what the tiles hand on
     float *table;                        // [5][slices * 64]: the channels' parameters (DiagLane), or null
     uint32_t magic, magic_shift;         // item / slices as (item * magic) >> magic_shift, for items below 2^31
     long long budget;                    // cycles that a wait for an earlier tile may take
@@ -64,7 +63,7 @@ int64_t diag_tiles(int64_t rows);
 // Bytes of a walk's workspace (0: one tile a slice, nothing to hand on).
 size_t diag_walk_bytes(int64_t rows, int channels);
 void diag_walk_layout(DiagParams &p, void *workspace);
-// The walk's first kernel: clears the counter and the flags and makes the table.
+// The walk's first kernel: clears the counter and the words and makes the table.
 cudaError_t diag_begin(const DiagParams &p, cudaStream_t stream);
 // CTAs of a walk: one for each item, up to `per_sm` on each of 152 SMs (a single row of tiles: always one for each).
 unsigned diag_grid(const DiagParams &p, int per_sm);
@@ -439,11 +438,14 @@ __device__ __forceinline__ void put_map(DiagMaps &m, int lane, DiagProduct p, F2
 }
 
 // ------------------------------------------------------------------ the walk over the tiles
-// CTAs take (tile, slice) items off one counter, tile by tile in the order of the walk, each while it works on the item before,
-// whose rows' place the next ones are fetched to.  An item hands on its map as soon as it has it, and what is behind it (h after
-// the tile, G before it) once it knows what came in: that is found from the nearest earlier item that has handed on the
-// latter, and the maps between, applied in the order of the rows: the same arithmetic from whichever item it starts, so results do
-// not depend on timing.  The earliest unfinished item never waits, and its CTA is running, so every wait ends.
+// CTAs take (tile, slice) items off one counter, tile by tile in the order of the walk.  An item hands on its map as soon as it
+// has it, and what is behind it (h after the tile, G before it) once it knows what came in: that is found from the nearest
+// earlier item that has handed on the latter, and the maps between, applied in the order of the rows: the same arithmetic from
+// whichever item it starts, so results do not depend on timing.  The earliest unfinished item never waits, and its CTA is
+// running, so every wait ends.
+// What is handed on are 64-bit words, two channels each, that say themselves whether they are there (kNone: not yet), so that
+// neither side needs a fence: with flags and release stores an item cost its CTA 8,500 cycles, so 3,000.
+constexpr unsigned long long kNone = ~0ull;
 struct DiagWalk {
     const DiagParams &p;
     int tiles, slices, lane;
@@ -459,33 +461,48 @@ struct DiagWalk {
         __syncthreads();
         return item;
     }
-    __device__ __forceinline__ int64_t at(int j, int slice) const { return (int64_t)slice * tiles + j; }
-    __device__ __forceinline__ void flag(int64_t i, uint32_t v) const {
-        __syncwarp();
-        if (lane == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.flags + i), "r"(v) : "memory");
+    __device__ __forceinline__ unsigned long long *at(int j, int slice) const { return p.words + ((int64_t)slice * tiles + j) * 128 + lane; }
+    static __device__ __forceinline__ void put(unsigned long long *to, F2 v) {
+        unsigned long long w = bits(v);
+        if (w == kNone) w = 0x7fffffff7fffffffull;          // (a NaN like any other)
+        asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(to), "l"(w) : "memory");
+    }
+    static __device__ __forceinline__ unsigned long long get(const unsigned long long *from) {
+        unsigned long long w;
+        asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(from) : "memory");
+        return w;
     }
     __device__ __forceinline__ void hand_on_map(int j, int slice, DiagProduct m, F2 H) const {
-        const int64_t i = at(j, slice);
-        __stcg(p.product + i * 32 + lane, make_float4(m.hi.x, m.hi.y, m.lo.x, m.lo.y));
-        __stcg(p.shift + i * 32 + lane, make_float2(H.x, H.y));
-        flag(i, 1u);
+        unsigned long long *to = at(j, slice);
+        put(to, m.hi);
+        put(to + 32, m.lo);
+        put(to + 64, H);
     }
-    __device__ __forceinline__ void hand_on(int j, int slice, F2 h) const {
-        const int64_t i = at(j, slice);
-        __stcg(p.after + i * 32 + lane, make_float2(h.x, h.y));
-        flag(i, 2u);
-    }
+    __device__ __forceinline__ void hand_on(int j, int slice, F2 h) const { put(at(j, slice) + 96, h); }
     // What comes in to the j-th tile of a slice, by one warp.  A wait that runs out is reported, and takes 0.
     __device__ __forceinline__ F2 come_in(int j, int slice) const {
         if (j == 0) return both(0.f);
-        const int64_t base = at(0, slice);
-        const int k = j - 1 - lane;
-        int maps = 0;
+        constexpr int D = 6;                                // tiles back
+        const unsigned long long *from = at(j, slice);
+        unsigned long long hi[D], lo[D], H[D], after[D];
+        int maps;
         const long long t0 = clock64();
         for (;;) {
-            uint32_t f = 2;
-            if (k >= 0) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(f) : "l"(p.flags + base + k) : "memory");
-            const uint32_t done = __ballot_sync(~0u, f == 2), some = __ballot_sync(~0u, f != 0);
+#pragma unroll
+            for (int q = 0; q < D; ++q) {
+                const unsigned long long *w = from - (q + 1) * 128;
+                const bool is = j > q;                      // (before the first tile: 0)
+                after[q] = is ? get(w + 96) : 0ull;
+                hi[q] = is ? get(w) : 0ull;
+                lo[q] = is ? get(w + 32) : 0ull;
+                H[q] = is ? get(w + 64) : 0ull;
+            }
+            uint32_t done = 0, some = 0;
+#pragma unroll
+            for (int q = 0; q < D; ++q) {
+                done |= (uint32_t)__all_sync(~0u, after[q] != kNone) << q;
+                some |= (uint32_t)__all_sync(~0u, hi[q] != kNone && lo[q] != kNone && H[q] != kNone) << q;
+            }
             maps = __ffs(done) - 1;
             if (done != 0 && (~some & ((1u << maps) - 1)) == 0) break;
             if (__any_sync(~0u, clock64() - t0 > p.budget)) {
@@ -494,16 +511,10 @@ struct DiagWalk {
             }
         }
         F2 h = both(0.f);
-        int from = j - 1 - maps;
-        if (from >= 0) {
-            const float2 v = __ldcg(p.after + (base + from) * 32 + lane);
-            h = {v.x, v.y};
-        }
-#pragma unroll 4
-        for (++from; from < j; ++from) {
-            const float4 m = __ldcg(p.product + (base + from) * 32 + lane);
-            const float2 v = __ldcg(p.shift + (base + from) * 32 + lane);
-            h = diag_apply({{m.x, m.y}, {m.z, m.w}}, {v.x, v.y}, h);
+#pragma unroll
+        for (int q = D - 1; q >= 0; --q) {
+            if (q == maps) h = pair(after[q]);
+            if (q < maps) h = diag_apply({pair(hi[q]), pair(lo[q])}, pair(H[q]), h);
         }
         return h;
     }

@@ -8,23 +8,22 @@ int64_t diag_tiles(int64_t rows) { return (rows + kDiagTile - 1) / kDiagTile; }
 
 namespace {
 struct WalkLayout {
-    size_t flags, table, product, shift, after, total;      // behind the counter, which comes first
+    size_t table, words, total;      // behind the counter, which comes first
 };
 WalkLayout walk_layout(int64_t rows, int channels) {
     const size_t slices = diag_slices(channels), items = (size_t)diag_tiles(rows) * slices;
     WalkLayout l;
-    l.flags = 256;
-    l.table = l.flags + (items * 4 + 255) / 256 * 256;
-    l.product = l.table + 5 * slices * kDiagSlice * sizeof(float);
-    l.shift = l.product + items * 32 * sizeof(float4);
-    l.after = l.shift + items * 32 * sizeof(float2);
-    l.total = l.after + items * 32 * sizeof(float2);
+    l.table = 256;
+    l.words = l.table + 5 * slices * kDiagSlice * sizeof(float);
+    l.total = l.words + items * 128 * sizeof(unsigned long long);
     return l;
 }
 
-__global__ void __launch_bounds__(256) diag_begin_kernel(const __grid_constant__ DiagParams p, uint32_t words) {
+__global__ void __launch_bounds__(256) diag_begin_kernel(const __grid_constant__ DiagParams p, uint32_t items) {
     const uint32_t i = blockIdx.x * 256 + threadIdx.x, all = gridDim.x * 256;
-    for (uint32_t k = i; k < words; k += all) p.ticket[k] = 0u;         // (the flags lie behind it)
+    if (i == 0) *p.ticket = 0u;
+    static_assert(kNone == ~0ull, "all bits set");
+    for (uint64_t k = i; k < (uint64_t)items * 64; k += all) reinterpret_cast<uint4 *>(p.words)[k] = make_uint4(~0u, ~0u, ~0u, ~0u);
     const int slices = (p.channels + kDiagSlice - 1) / kDiagSlice, row = slices * kDiagSlice;
     for (int c = 2 * (int)i; c < row; c += 2 * (int)all) {
         const DiagLane l = diag_lane(p.A_log, p.a_bias, p.b_bias, c, p.channels);
@@ -45,17 +44,13 @@ void diag_walk_layout(DiagParams &p, void *workspace) {
     const WalkLayout l = walk_layout(p.rows, p.channels);
     uint8_t *at = static_cast<uint8_t *>(workspace);
     p.ticket = reinterpret_cast<uint32_t *>(at);
-    p.flags = reinterpret_cast<uint32_t *>(at + l.flags);
     p.table = reinterpret_cast<float *>(at + l.table);
-    p.product = reinterpret_cast<float4 *>(at + l.product);
-    p.shift = reinterpret_cast<float2 *>(at + l.shift);
-    p.after = reinterpret_cast<float2 *>(at + l.after);
+    p.words = reinterpret_cast<unsigned long long *>(at + l.words);
 }
 cudaError_t diag_begin(const DiagParams &p, cudaStream_t stream) {
     if (diag_tiles(p.rows) < 2) return cudaSuccess;
-    const uint32_t words = (uint32_t)((uint8_t *)p.table - (uint8_t *)p.ticket) / 4;
-    const uint32_t blocks = (words + 1023) / 1024;
-    diag_begin_kernel<<<blocks < 16 ? 16 : blocks > 608 ? 608 : blocks, 256, 0, stream>>>(p, words);
+    const uint32_t items = (uint32_t)(diag_tiles(p.rows) * diag_slices(p.channels)), blocks = (items * 64ull + 1023) / 1024;
+    diag_begin_kernel<<<blocks < 16 ? 16 : blocks > 1216 ? 1216 : blocks, 256, 0, stream>>>(p, items);
     return cudaGetLastError();
 }
 unsigned diag_grid(const DiagParams &p, int per_sm) {
