@@ -6,8 +6,10 @@
 //     da = dg g (1 - s) (sigmoid gate) | -dg e^A_log s (softplus gate),
 //     dA_log = sum dg g,  da_bias = sum da,  db_bias = sum db,  dstate_in = alpha G at a sequence's first row.
 // The walk is the forward pass's, from the last tile to the first: warps fold their rows to G's map and, from the kept
-// h before each tile, to h's, both with the same product of decays.  Of what the gates give, the decays' exponents G and h stay
-// in registers for the second pass over the rows and alpha in shared memory, over the staged a; the rest is made again.
+// h before each tile, to h's, both with the same product of decays; a fifth warp
+// hands G's on.  Of what the gates give, the decays' exponents G and h stay
+// in shared memory for the second pass over the rows; the rest is made again, in loops of four rows (all 16 in a row, their code
+// did not fit the instruction cache: 440 us where these take XXX).
 #pragma once
 
 #include <type_traits>
@@ -17,22 +19,27 @@
 namespace gdn {
 namespace {
 
-constexpr int LT = 8, W = kDiagTile / LT;      // a warp's rows; warps
+constexpr int LT = 16, W = kDiagTile / LT;      // a warp's rows; the warps that take rows
+constexpr int kThreads = (W + 1) * 32;
 constexpr int kGroup = 4;                       // rows whose loads go out together
 
-// (Each array is copied to 16 bytes at a time, the steps 8.)
+// A warp's rows as they are staged, and of what the gates give the decays' exponents G and the inputs w i x, which become h.  The
+// staged a lies at the end of G's place: G's rows are written when a's that lie there have been read.  (Each array is copied to 16
+// bytes at a time, the steps too.)
 template <typename IO, bool CODES> struct Staged {
-    alignas(16) IO x[LT][kDiagSlice], b[LT][kDiagSlice], dy[LT][kDiagSlice], a[LT][kDiagSlice];
+    alignas(16) IO x[LT][kDiagSlice], b[LT][kDiagSlice], dy[LT][kDiagSlice];
+    alignas(16) float2 G[LT][32], h[LT][32];
+    __device__ __forceinline__ IO *a() { return reinterpret_cast<IO *>(G + LT) - LT * kDiagSlice; }
 };
 template <typename IO> struct Staged<IO, true> {
-    alignas(16) int8_t x[LT][kDiagSlice], b[LT][kDiagSlice], a[LT][kDiagSlice];
+    alignas(16) int8_t x[LT][kDiagSlice], b[LT][kDiagSlice], codes_a[LT][kDiagSlice];
     alignas(16) IO dy[LT][kDiagSlice];
     alignas(16) uint8_t xs[LT], bs[LT], as[LT];
+    alignas(16) float2 G[LT][32], h[LT][32];
 };
-static_assert(LT * kDiagSlice % 16 == 0 && LT % 8 == 0, "what follows an array is aligned as it is");
+static_assert(LT * kDiagSlice % 16 == 0 && LT == 16, "what follows an array is aligned as it is");
 template <typename IO, bool CODES> struct Shared {
     Staged<IO, CODES> rows[W];
-    float2 alpha[W][LT][32];
     DiagMaps maps[W];                   // a warp's rows: h's map, and with `back` G's
     float2 back[W][32];
     DiagMaps behind[W];                 // G's: the tile's rows behind a warp's
@@ -70,7 +77,7 @@ __device__ __forceinline__ F2 code_pair(const int8_t *rows, const uint8_t *steps
 }
 
 template <typename IO, int GATE, int WEIGHT, bool CODES>
-__global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_constant__ DiagParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backward_kernel(const __grid_constant__ DiagParams p) {
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Shared<IO, CODES> &sh = *reinterpret_cast<Shared<IO, CODES> *>(raw_shared);
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32, C = p.channels, slices = (C + kDiagSlice - 1) / kDiagSlice;
@@ -78,14 +85,58 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
     if (p.dstate_in)
         for (int n = blockIdx.x; n < p.num_seqs; n += gridDim.x) {      // sequences without tokens
             if (seq_begin(p, n) != seq_begin(p, n + 1)) continue;
-            for (int c = threadIdx.x; c < C; c += W * 32) p.dstate_in[(int64_t)n * C + c] = p.dstate_out ? p.dstate_out[(int64_t)n * C + c] : 0.f;
+            for (int c = threadIdx.x; c < C; c += kThreads) p.dstate_in[(int64_t)n * C + c] = p.dstate_out ? p.dstate_out[(int64_t)n * C + c] : 0.f;
         }
     const int rows = (int)p.rows, tiles = (rows + kDiagTile - 1) / kDiagTile;
     const DiagWalk walk{p, tiles, slices, lane};
     const uint32_t items = walk.items();
+    uint32_t item = walk.first(sh.next);
+    if (w == W) {
+        // The parameters' gradients of an item, over the rows' warps in their order.
+        auto put_sums = [&](uint32_t of) {
+            const int j = walk.tile_of(of), c = ((int)of - j * slices) * kDiagSlice + 2 * lane;
+            float *one[3] = {p.dA_log, p.da_bias, p.db_bias};
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                F2 total = get_pair(sh.sums[0][k], lane);
+#pragma unroll
+                for (int r = 1; r < W; ++r) total = add2(total, get_pair(sh.sums[r][k], lane));
+                if (tiles > 1) store_state(p.partial + ((int64_t)j * 3 + k) * C, total, c, C);
+                else if (one[k]) store_state(one[k], total, c, C);
+            }
+        };
+        uint32_t last = items;
+        while (item < items) {
+            const int j = walk.tile_of(item), slice = (int)item - j * slices;
+            const uint32_t later = lane == 0 ? walk.ticket() : 0u;
+            side_sync<kThreads>(1);
+            DiagProduct all = get_product(sh.maps[W - 1], lane);
+            F2 shift = get_pair(sh.back[W - 1], lane);
+#pragma unroll
+            for (int r = W - 2; r >= 0; --r) {
+                put_map(sh.behind[r], lane, all, shift);
+                const DiagProduct m = get_product(sh.maps[r], lane);
+                shift = diag_apply(m, get_pair(sh.back[r], lane), shift);
+                all = diag_join(all, m);
+            }
+            if (j + 1 < tiles) walk.hand_on_map(j, slice, all, shift);
+            if (last < items) put_sums(last);
+            const F2 in = walk.come_in(j, slice);
+            if (j + 1 < tiles) walk.hand_on(j, slice, diag_apply(all, shift, in));
+            sh.start[lane] = make_float2(in.x, in.y);
+            if (lane == 0) sh.next = later;
+            __syncwarp();
+            side_arrive<kThreads>(2);
+            last = item;
+            item = __shfl_sync(~0u, later, 0);
+        }
+        side_sync<kThreads>(1);
+        if (last < items) put_sums(last);
+        return;
+    }
     const bool has_b = p.has_b;
     Staged<IO, CODES> &st = sh.rows[w];
-    float2 *salpha = &sh.alpha[w][0][0];
+    float2 *sG = &st.G[0][0], *sh_ = &st.h[0][0];
     const uint32_t shut = infinity_bits<IO>(true);
     if (!has_b) {                   // codes of 1 with the largest step are as good as infinity
         if constexpr (CODES) {
@@ -99,11 +150,11 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
         const int j = walk.tile_of(item), slice = (int)item - j * slices, w0 = (tiles - 1 - j) * kDiagTile + w * LT, c0 = slice * kDiagSlice;
         if constexpr (CODES) {
             stage_codes(&st.x[0][0], st.xs, p, 0, slice, slices, w0, 0, rows, 0u, lane);
-            stage_codes(&st.a[0][0], st.as, p, 1, slice, slices, w0, 0, rows, 0x01010101u, lane);
+            stage_codes(&st.codes_a[0][0], st.as, p, 1, slice, slices, w0, 0, rows, 0x01010101u, lane);
             if (has_b) stage_codes(&st.b[0][0], st.bs, p, 2, slice, slices, w0, 0, rows, 0u, lane);
         } else {
             stage_rows<IO, LT>(&st.x[0][0], (const IO *)p.x, p.ld_x, w0, 0, rows, c0, C, p.wide, 0u, lane);
-            stage_rows<IO, LT>(&st.a[0][0], (const IO *)p.a, p.ld_a, w0, 0, rows, c0, C, p.wide, shut, lane);
+            stage_rows<IO, LT>(st.a(), (const IO *)p.a, p.ld_a, w0, 0, rows, c0, C, p.wide, shut, lane);
             if (has_b) stage_rows<IO, LT>(&st.b[0][0], (const IO *)p.b, p.ld_b, w0, 0, rows, c0, C, p.wide, 0u, lane);
         }
         stage_rows<IO, LT>(&st.dy[0][0], (const IO *)p.dy, p.ld_y, w0, 0, rows, c0, C, p.wide, 0u, lane);
@@ -114,35 +165,23 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
         else return staged(&st.x[0][0], t, lane);
     };
     auto get_a = [&](int t) -> F2 {
-        if constexpr (CODES) return code_pair(&st.a[0][0], st.as, t, lane);
-        else return staged(&st.a[0][0], t, lane);
+        if constexpr (CODES) return code_pair(&st.codes_a[0][0], st.as, t, lane);
+        else return staged(st.a(), t, lane);
     };
     auto get_b = [&](int t) -> F2 {
         if constexpr (CODES) return code_pair(&st.b[0][0], st.bs, t, lane);
         else return staged(&st.b[0][0], t, lane);
     };
-    // The parameters' gradients of an item, over the CTA's warps in their order.
-    auto put_sums = [&](uint32_t item) {
-        const int k = threadIdx.x / kDiagSlice, j = walk.tile_of(item), ch = ((int)item - j * slices) * kDiagSlice + threadIdx.x % kDiagSlice;
-        if (k > 2 || ch >= C) return;
-        float total = 0.f;
-        for (int r = 0; r < W; ++r) total += reinterpret_cast<const float *>(sh.sums[r][k])[threadIdx.x % kDiagSlice];
-        float *one[3] = {p.dA_log, p.da_bias, p.db_bias};
-        if (tiles > 1) p.partial[((int64_t)j * 3 + k) * C + ch] = total;
-        else if (one[k]) one[k][ch] = total;
-    };
     EdgeWindow window = edge_window(p, 0, lane);
-    uint32_t item = walk.first(sh.next), last = items;
     if (item < items) stage(item);
     while (item < items) {
-        if (threadIdx.x == 0) sh.next = walk.ticket();
         const int j = walk.tile_of(item), tile = tiles - 1 - j, slice = (int)item - j * slices, w0 = tile * kDiagTile + w * LT, c0 = slice * kDiagSlice;
         const int c = c0 + 2 * lane;
         const DiagLane l = diag_lane(p, c, slices);
         const bool fast = p.pairs && c0 + kDiagSlice <= C, near = diag_near<GATE>(l);
         F2 sum_A = both(0.f), sum_a = both(0.f), sum_b = both(0.f);
         const bool some = w0 < rows, full = w0 + LT <= rows;
-        F2 G[LT], h[LT], sum_G = both(0.f), H = both(0.f), D = both(0.f);
+        F2 sum_G = both(0.f), H = both(0.f), D = both(0.f);
         uint32_t begins = 0, ends = 0;
         if (some) {
             const uint32_t edges = find_edges<LT>(p, window, (uint32_t)w0, 0, 28, sh.edge_first[w], sh.edge_last[w], lane);
@@ -150,20 +189,14 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
             begins = edges & live;
             ends = edges >> 1 & live;
         }
-        // dy, with a final state's gradient at a sequence's last row
-        auto get_dy = [&](int t) -> F2 {
-            F2 v = staged(&st.dy[0][0], t, lane);
-            if ((ends >> t & 1) && p.dstate_out) v = add2(v, load_state(p.dstate_out + (int64_t)(sh.edge_first[w][t + 1] - 1) * C, c, C));
-            return v;
-        };
-        stage_wait();
         const uint32_t special = begins | ends;
-        if (some) {
+        stage_wait();
+        {
             F2 through = both(1.f);
             auto take = [&](auto only_near) {
-#pragma unroll
-                for (int t0 = 0; t0 < LT; t0 += kGroup) {       // (loads of a group first: none could pass the stores of alpha)
-                    F2 a[kGroup], b[kGroup], x[kGroup], dy[kGroup], alpha[kGroup];
+#pragma unroll 1
+                for (int t0 = 0; t0 < LT; t0 += kGroup) {       // (the loads of a group go out before its stores)
+                    F2 a[kGroup], b[kGroup], x[kGroup], dy[kGroup], G[kGroup], in[kGroup];
 #pragma unroll
                     for (int k = 0; k < kGroup; ++k) {
                         a[k] = get_a(t0 + k);
@@ -171,21 +204,23 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
                         x[k] = get_x(t0 + k);
                         dy[k] = staged(&st.dy[0][0], t0 + k, lane);
                     }
+                    __syncwarp();
 #pragma unroll
                     for (int k = 0; k < kGroup; ++k) {
-                        const int t = t0 + k;
-                        G[t] = diag_exponent<GATE>(a[k], l);
-                        const DiagDecay d = diag_decay<decltype(only_near)::value>(G[t]);
+                        G[k] = diag_exponent<GATE>(a[k], l);
+                        const DiagDecay d = diag_decay<decltype(only_near)::value>(G[k]);
                         const F2 v = mul2(diag_sigmoid(b[k], l.nbbias), x[k]);
-                        h[t] = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n).w, v);       // (the input, until h is known)
-                        alpha[k] = d.alpha;
-                        sum_G = add2(sum_G, G[t]);
-                        H = fma2(d.alpha, H, h[t]);
+                        in[k] = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n).w, v);
+                        sum_G = add2(sum_G, G[k]);
+                        H = fma2(d.alpha, H, in[k]);
                         through = mul2(through, d.alpha);
                         D = fma2(through, dy[k], D);
                     }
 #pragma unroll
-                    for (int k = 0; k < kGroup; ++k) salpha[(t0 + k) * 32 + lane] = make_float2(alpha[k].x, alpha[k].y);
+                    for (int k = 0; k < kGroup; ++k) {
+                        sG[(t0 + k) * 32 + lane] = make_float2(G[k].x, G[k].y);
+                        sh_[(t0 + k) * 32 + lane] = make_float2(in[k].x, in[k].y);
+                    }
                 }
             };
             if (near) take(std::true_type{});
@@ -194,54 +229,58 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
                 through = both(1.f);
                 D = both(0.f);
                 H = both(0.f);
+                bool open = true;               // (nothing behind a sequence's first row comes back to here)
 #pragma unroll 1
                 for (int t = 0; t < LT; ++t) {
-                    if (begins & ((2u << t) - 1)) break;        // (nothing behind a sequence's first row comes back to here)
-                    through = mul2(through, get_pair(salpha + t * 32, lane));
-                    D = fma2(through, get_dy(t), D);
-                }
-#pragma unroll
-                for (int t = 0; t < LT; ++t) {
-                    if (begins >> t & 1) H = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t] * C, c, C) : both(0.f);
-                    H = fma2(get_pair(salpha + t * 32, lane), H, h[t]);
+                    const F2 alpha = diag_decay<false>(get_pair(sG + t * 32, lane)).alpha;
+                    if (begins >> t & 1) {
+                        H = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t] * C, c, C) : both(0.f);
+                        open = false;
+                    }
+                    H = fma2(alpha, H, get_pair(sh_ + t * 32, lane));
+                    if (open) {
+                        F2 dy = staged(&st.dy[0][0], t, lane);
+                        if ((ends >> t & 1) && p.dstate_out)
+                            dy = add2(dy, load_state(p.dstate_out + (int64_t)(sh.edge_first[w][t + 1] - 1) * C, c, C));
+                        through = mul2(through, alpha);
+                        D = fma2(through, dy, D);
+                    }
                 }
             }
         }
         put_map(sh.maps[w], lane, diag_product(sum_G, begins != 0), H);
         sh.back[w][lane] = make_float2(D.x, D.y);
-        __syncthreads();
-        const uint32_t next = sh.next;
-        if (last < items) put_sums(last);
-        if (w == W - 1) {
-            DiagProduct all = get_product(sh.maps[W - 1], lane);
-            F2 shift = get_pair(sh.back[W - 1], lane);
-#pragma unroll
-            for (int k = W - 2; k >= 0; --k) {
-                put_map(sh.behind[k], lane, all, shift);
-                const DiagProduct m = get_product(sh.maps[k], lane);
-                shift = diag_apply(m, get_pair(sh.back[k], lane), shift);
-                all = diag_join(all, m);
-            }
-            if (tile > 0) walk.hand_on_map(j, slice, all, shift);
-            const F2 in = walk.come_in(j, slice);
-            sh.start[lane] = make_float2(in.x, in.y);
-            if (tile > 0) walk.hand_on(j, slice, diag_apply(all, shift, in));
-        }
-        if (some) {             // h before each row, while the last warp waits
+        __syncwarp();
+        side_sync<kThreads>(1);
+        {                       // h before each row, while the fifth warp hands on and waits
             F2 at = both(0.f);
             if (tile > 0) at = get_pair(reinterpret_cast<const float2 *>(p.kept + ((int64_t)tile * slices + slice) * kDiagSlice), lane);
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
                 if (k < w) at = diag_apply(get_product(sh.maps[k], lane), get_pair(sh.maps[k].shift, lane), at);
+            auto follow = [&](auto only_near) {
+#pragma unroll 1
+                for (int t0 = 0; t0 < LT; t0 += kGroup) {
+                    F2 alpha[kGroup], in[kGroup];
 #pragma unroll
-            for (int t = 0; t < LT; ++t) {
-                if (begins >> t & 1) at = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t] * C, c, C) : both(0.f);
-                const F2 to = fma2(get_pair(salpha + t * 32, lane), at, h[t]);
-                h[t] = at;
-                at = to;
-            }
+                    for (int k = 0; k < kGroup; ++k) {
+                        alpha[k] = diag_decay<decltype(only_near)::value>(get_pair(sG + (t0 + k) * 32, lane)).alpha;
+                        in[k] = get_pair(sh_ + (t0 + k) * 32, lane);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kGroup; ++k) {
+                        if (begins >> (t0 + k) & 1)
+                            at = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t0 + k] * C, c, C) : both(0.f);
+                        sh_[(t0 + k) * 32 + lane] = make_float2(at.x, at.y);
+                        at = fma2(alpha[k], at, in[k]);
+                    }
+                }
+            };
+            if (near) follow(std::true_type{});
+            else follow(std::false_type{});
         }
-        __syncthreads();
+        side_sync<kThreads>(2);
+        const uint32_t next = sh.next;
         F2 back = get_pair(sh.start, lane);     // what comes back from the rows behind the warp's
         if (w < W - 1) back = diag_apply(get_product(sh.behind[w], lane), get_pair(sh.behind[w].shift, lane), back);
         if (some) {
@@ -250,33 +289,35 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
             // PLAIN: all rows are there, stored by pairs, and no sequence begins or ends.
             auto give = [&](auto only_near, auto plain) {
                 constexpr bool kPlain = decltype(plain)::value;
+                constexpr int N = kPlain ? kGroup : 1;
+#pragma unroll 1
+                for (int t0 = LT - N; t0 >= 0; t0 -= N) {
+                    F2 b[N], x[N], dy[N], G[N], h[N];
 #pragma unroll
-                for (int t0 = LT - kGroup; t0 >= 0; t0 -= kGroup) {
-                    F2 b[kGroup], x[kGroup], dy[kGroup], alpha[kGroup];
-#pragma unroll
-                    for (int k = 0; k < kGroup; ++k) {
+                    for (int k = 0; k < N; ++k) {
                         b[k] = get_b(t0 + k);
                         x[k] = get_x(t0 + k);
                         dy[k] = staged(&st.dy[0][0], t0 + k, lane);
-                        alpha[k] = get_pair(salpha + (t0 + k) * 32, lane);
+                        G[k] = get_pair(sG + (t0 + k) * 32, lane);
+                        h[k] = get_pair(sh_ + (t0 + k) * 32, lane);
                     }
-                    F2 out_x[kGroup], out_a[kGroup], out_b[kGroup];
+                    F2 out_x[N], out_a[N], out_b[N];
 #pragma unroll
-                    for (int k = kGroup - 1; k >= 0; --k) {
+                    for (int k = N - 1; k >= 0; --k) {
                         const int t = t0 + k;
                         F2 g = add2(dy[k], back);           // the gradient at h_t
                         if (!kPlain && (ends >> t & 1) && p.dstate_out)
                             g = add2(g, load_state(p.dstate_out + (int64_t)(sh.edge_first[w][t + 1] - 1) * C, c, C));
                         const F2 i = diag_sigmoid(b[k], l.nbbias), v = mul2(i, x[k]), minus = both(-1.f);
-                        const DiagDecay d = diag_decay<decltype(only_near)::value>(G[t]);
+                        const DiagDecay d = diag_decay<decltype(only_near)::value>(G[k]);
                         const DiagWeight o = diag_weigh<WEIGHT>(d.n);
-                        F2 slope = h[t];                                            // dg / (g alpha)
+                        F2 slope = h[k];                                            // dg / (g alpha)
                         if (WEIGHT == GDN_DIAG_NORM) slope = fma2(mul2(v, mul2(d.alpha, minus)), o.winv, slope);
                         if (WEIGHT == GDN_DIAG_COMPLEMENT) slope = fma2(v, minus, slope);
-                        const F2 ag = mul2(alpha[k], g), dv = WEIGHT == GDN_DIAG_PLAIN ? g : mul2(g, o.w);
+                        const F2 ag = mul2(d.alpha, g), dv = WEIGHT == GDN_DIAG_PLAIN ? g : mul2(g, o.w);
                         const F2 dG = mul2(mul2(ag, slope), minus);                 // the gradient at G = -g
-                        const F2 dGG = mul2(dG, F2{fminf(G[t].x, 1e30f), fminf(G[t].y, 1e30f)});        // (0 of a decay to 0)
-                        const F2 sp = mul2(G[t], l.inverse);                          // the gate's opening
+                        const F2 dGG = mul2(dG, F2{fminf(G[k].x, 1e30f), fminf(G[k].y, 1e30f)});        // (0 of a decay to 0)
+                        const F2 sp = mul2(G[k], l.inverse);                        // the gate's opening
                         const F2 da_ = GATE == GDN_DIAG_SIGMOID ? fma2(dGG, mul2(sp, minus), dGG) : mul2(dG, mul2(l.rate, diag_decay<false>(sp).n));
                         const F2 dvv = mul2(dv, v), db_ = fma2(dvv, mul2(i, minus), dvv);
                         out_x[k] = mul2(dv, i);
@@ -294,7 +335,7 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
                         }
                     }
 #pragma unroll
-                    for (int k = kGroup - 1; k >= 0; --k, dx -= p.ld_dx, da -= p.ld_da, db -= p.ld_db) {
+                    for (int k = N - 1; k >= 0; --k, dx -= p.ld_dx, da -= p.ld_da, db -= p.ld_db) {
                         if (!kPlain && w0 + t0 + k >= rows) continue;
                         store_pair<IO>(dx, out_x[k], c, C, kPlain || fast);
                         store_pair<IO>(da, out_a[k], c, C, kPlain || fast);
@@ -311,11 +352,9 @@ __global__ void __launch_bounds__(W * 32, 2) diag_backward_kernel(const __grid_c
         for (int k = 0; k < 3; ++k) sh.sums[w][k][lane] = make_float2(all_sums[k].x, all_sums[k].y);
         __syncwarp();
         if (next < items) stage(next);
-        last = item;
         item = next;
     }
-    __syncthreads();
-    if (last < items) put_sums(last);
+    side_sync<kThreads>(1);
 }
 
 template <typename IO, int GATE, int WEIGHT> cudaError_t launch(const DiagParams &p, cudaStream_t stream) {
@@ -324,7 +363,7 @@ template <typename IO, int GATE, int WEIGHT> cudaError_t launch(const DiagParams
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
     if (e == cudaSuccess) e = diag_begin(p, stream);
     if (e != cudaSuccess) return e;
-    kernel<<<diag_grid(p, 2), W * 32, shared, stream>>>(p);
+    kernel<<<diag_grid(p, sizeof(IO) == 4 ? 2 : 3), kThreads, shared, stream>>>(p);
     return cudaGetLastError();
 }
 

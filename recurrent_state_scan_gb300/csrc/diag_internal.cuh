@@ -438,6 +438,10 @@ __device__ __forceinline__ void put_map(DiagMaps &m, int lane, DiagProduct p, F2
 }
 
 // ------------------------------------------------------------------ the walk over the tiles
+// Barriers between the warps that take rows and the one that hands maps on.
+template <int THREADS> __device__ __forceinline__ void side_arrive(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(THREADS) : "memory"); }
+template <int THREADS> __device__ __forceinline__ void side_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory"); }
+
 // CTAs take (tile, slice) items off one counter, tile by tile in the order of the walk.  An item hands on its map as soon as it
 // has it, and what is behind it (h after the tile, G before it) once it knows what came in: that is found from the nearest
 // earlier item that has handed on the latter, and the maps between, applied in the order of the rows: the same arithmetic from

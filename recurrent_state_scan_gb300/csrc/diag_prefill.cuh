@@ -27,10 +27,6 @@ template <typename IO> struct Shared {
     int edge_first[2][W][LT + 1], edge_last[2][W][LT + 1];
 };
 
-// Barriers between the rows' warps and the fifth one, two of each kind in turn: the one side cannot be two steps ahead.
-__device__ __forceinline__ void side_arrive(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kThreads) : "memory"); }
-__device__ __forceinline__ void side_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory"); }
-
 template <typename IO, int GATE, int WEIGHT, bool CODES>
 __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_prefill_kernel(const __grid_constant__ DiagParams p) {
     extern __shared__ __align__(16) unsigned char raw_shared[];
@@ -50,7 +46,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_prefil
         uint32_t next = second;
         for (int k = 0; item < items; ++k) {
             const int buf = k & 1, tile = walk.tile_of(item), slice = (int)item - tile * slices;
-            side_sync(1 + buf);
+            side_sync<kThreads>(1 + buf);      // (two barriers of each kind in turn: the one side cannot be two steps ahead)
             // The item behind the next one, as late as can be: one that its CTA has not begun holds up all that come after it.
             const uint32_t later = lane == 0 && next < items ? walk.ticket() : items;
             DiagProduct all = get_product(sh.maps[buf][0], lane);
@@ -68,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_prefil
             sh.start[buf][lane] = make_float2(h.x, h.y);
             if (lane == 0) sh.items[buf] = later;
             __syncwarp();
-            side_arrive(3 + buf);
+            side_arrive<kThreads>(3 + buf);
             item = next;
             next = __shfl_sync(~0u, later, 0);
             if (p.kept && tile > 0)
@@ -92,14 +88,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_prefil
     uint32_t begins = 0, ends = 0;
     int old_w0 = 0, old_c = 0;
     uint32_t old_begins = 0, old_ends = 0;
-    if (item < items) stage(item);
+    DiagLane l{};
+    auto parameters = [&](uint32_t of) { l = diag_lane(p, ((int)of - walk.tile_of(of) * slices) * kDiagSlice + 2 * lane, slices); };
+    if (item < items) {
+        stage(item);
+        parameters(item);
+    }
     for (int k = 0;; ++k) {
         const bool more = item < items;
         const int buf = k & 1, tile = walk.tile_of(item), slice = (int)item - tile * slices, w0 = tile * kDiagTile + w * LT;
         const int c0 = slice * kDiagSlice, c = c0 + 2 * lane;
         F2 alpha[LT], u[LT];
         if (more) {
-            const DiagLane l = diag_lane(p, c, slices);
             const bool near = diag_near<GATE>(l), full = w0 + LT <= rows;
             F2 sum_G = both(0.f), H = both(0.f);
             begins = ends = 0;
@@ -156,11 +156,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_prefil
             }
             put_map(sh.maps[buf][w], lane, diag_product(sum_G, begins != 0), H);
             __syncwarp();
-            side_arrive(1 + buf);
+            side_arrive<kThreads>(1 + buf);
         }
-        if (k > 0) side_sync(3 + (buf ^ 1));
+        if (k > 0) side_sync<kThreads>(3 + (buf ^ 1));
         const uint32_t next = !more ? items : k == 0 ? second : sh.items[buf ^ 1];
-        if (next < items) stage(next);
+        if (next < items) {
+            stage(next);
+            parameters(next);
+        }
         if (k > 0) {
             F2 h = get_pair(sh.start[buf ^ 1], lane);
             if (w > 0) h = diag_apply(get_product(sh.before[buf ^ 1][w], lane), get_pair(sh.before[buf ^ 1][w].shift, lane), h);
