@@ -71,9 +71,10 @@ __device__ __forceinline__ void stage_codes(int8_t *to, uint8_t *to_steps, const
         to_steps[lane] = r0 + lane >= lo && r0 + lane < hi ? p.steps[at + lane] : (uint8_t)0;
     }
 }
-__device__ __forceinline__ F2 code_pair(const int8_t *rows, const uint8_t *steps, int t, int lane) {
-    const char2 q = reinterpret_cast<const char2 *>(rows)[t * 32 + lane];
-    return mul2({(float)q.x, (float)q.y}, both(code_scale(steps[t])));
+// The pair of row t, whose step lane t holds.
+__device__ __forceinline__ F2 code_pair(const int8_t *rows, float step, int t, int lane) {
+    const uint32_t q = reinterpret_cast<const uint16_t *>(rows)[t * 32 + lane];
+    return mul2(code_values(q), both(__shfl_sync(~0u, step, t)));
 }
 
 template <typename IO, int GATE, int WEIGHT, bool CODES>
@@ -160,16 +161,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         stage_rows<IO, LT>(&st.dy[0][0], (const IO *)p.dy, p.ld_y, w0, 0, rows, c0, C, p.wide, 0u, lane);
         stage_commit();
     };
+    float step_x = 0.f, step_a = 0.f, step_b = 0.f;
     auto get_x = [&](int t) -> F2 {
-        if constexpr (CODES) return code_pair(&st.x[0][0], st.xs, t, lane);
+        if constexpr (CODES) return code_pair(&st.x[0][0], step_x, t, lane);
         else return staged(&st.x[0][0], t, lane);
     };
     auto get_a = [&](int t) -> F2 {
-        if constexpr (CODES) return code_pair(&st.codes_a[0][0], st.as, t, lane);
+        if constexpr (CODES) return code_pair(&st.codes_a[0][0], step_a, t, lane);
         else return staged(st.a(), t, lane);
     };
     auto get_b = [&](int t) -> F2 {
-        if constexpr (CODES) return code_pair(&st.b[0][0], st.bs, t, lane);
+        if constexpr (CODES) return code_pair(&st.b[0][0], step_b, t, lane);
         else return staged(&st.b[0][0], t, lane);
     };
     EdgeWindow window = edge_window(p, 0, lane);
@@ -191,6 +193,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         }
         const uint32_t special = begins | ends;
         stage_wait();
+        if constexpr (CODES) {
+            step_x = code_scale(st.xs[lane % LT]);
+            step_a = code_scale(st.as[lane % LT]);
+            step_b = code_scale(st.bs[lane % LT]);
+        }
         {
             F2 through = both(1.f);
             auto take = [&](auto only_near) {

@@ -299,12 +299,24 @@ __device__ __forceinline__ uint32_t code_step(uint32_t most) {
 __device__ __forceinline__ float code_scale(uint32_t e) { return e == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((e - 6u) << 23); }
 __device__ __forceinline__ float code_inverse(uint32_t e) { return e == 255u ? 0.f : __uint_as_float((260u - e) << 23); }
 // Two codes as the bytes of an integer: v / step, exact, plus 1.5 x 2^23 is rounded to the nearest integer, whose low byte is the
-// code.  Only values next to fp32's largest could reach 128.
-__device__ __forceinline__ uint32_t codes_of(F2 v, uint32_t e) {
-    const float inv = code_inverse(e);
-    if (e == 254u) v = {fminf(fmaxf(v.x, -127.f / inv), 127.f / inv), fminf(fmaxf(v.y, -127.f / inv), 127.f / inv)};
-    const F2 q = fma2(v, both(inv), both(12582912.f));
+// code.  Only at the step 254 could values next to fp32's largest reach 128.
+__device__ __forceinline__ uint32_t code_bytes(F2 v, float inverse) {
+    const F2 q = fma2(v, both(inverse), both(12582912.f));
     return __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x0040);
+}
+__device__ __forceinline__ F2 code_range(F2 v, float inverse) {
+    const float top = 127.f / inverse;
+    return {fminf(fmaxf(v.x, -top), top), fminf(fmaxf(v.y, -top), top)};
+}
+__device__ __forceinline__ uint32_t codes_of(F2 v, uint32_t e) {
+    const float inverse = code_inverse(e);
+    return code_bytes(e == 254u ? code_range(v, inverse) : v, inverse);
+}
+// The two codes in the low bytes of q as numbers: a byte plus 128 in the low byte of 2^23 is 2^23 + 128 more than the code.
+__device__ __forceinline__ F2 code_values(uint32_t q) {
+    q ^= 0x8080u;
+    const F2 v = {__uint_as_float(__byte_perm(q, 0x4b000000u, 0x7540)), __uint_as_float(__byte_perm(q, 0x4b000000u, 0x7541))};
+    return add2(v, both(-8388736.f));
 }
 __device__ __forceinline__ uint32_t magnitude(F2 v) {
     const uint32_t a = __float_as_uint(v.x) & 0x7fffffffu, b = __float_as_uint(v.y) & 0x7fffffffu;

@@ -97,7 +97,68 @@ template <typename IO> cudaError_t by_kind(const DiagDecodeParams &p, int gate, 
 }
 
 // ------------------------------------------------------------------ 8-bit codes
-// A warp takes one block of 64 channels of one row, two to a lane.
+// By eight channels: 16 bytes of 16-bit rows (32 of fp32) to a lane, eight lanes to a block, R rows of four blocks to a warp, so
+// that R loads are on their way together; codes go out eight to a lane.
+constexpr int R = 4;
+template <typename IO> struct Eight {
+    F2 v[4];
+    static __device__ __forceinline__ Eight load(const IO *p) {
+        Eight e;
+        if (sizeof(IO) == 4) {
+            const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+            e.v[0] = {a.x, a.y}, e.v[1] = {a.z, a.w}, e.v[2] = {b.x, b.y}, e.v[3] = {b.z, b.w};
+        } else {
+            const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(p));
+            const uint32_t r[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e.v[i] = Pair<IO>::wide(*reinterpret_cast<const typename Pair<IO>::Raw *>(&r[i]));
+        }
+        return e;
+    }
+    __device__ __forceinline__ void store(IO *p) const {
+        if (sizeof(IO) == 4) {
+            reinterpret_cast<float4 *>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+            reinterpret_cast<float4 *>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+        } else {
+            uint32_t r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const typename Pair<IO>::Raw n = Pair<IO>::narrow(v[i]);
+                r[i] = *reinterpret_cast<const uint32_t *>(&n);
+            }
+            *reinterpret_cast<uint4 *>(p) = make_uint4(r[0], r[1], r[2], r[3]);
+        }
+    }
+};
+
+template <typename IO>
+__global__ void __launch_bounds__(256) pack_wide_kernel(int64_t rows, int C, const IO *x, int64_t ld, int8_t *codes, uint8_t *steps) {
+    const int lane = threadIdx.x % 32, c = (blockIdx.x * 32 + lane) * 8, blocks = (C + kDiagSlice - 1) / kDiagSlice;
+    const int64_t r0 = ((int64_t)blockIdx.y * 8 + threadIdx.x / 32) * R;
+    const bool in = c < C;
+    Eight<IO> e[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        e[r] = Eight<IO>{};
+        if (in && r0 + r < rows) e[r] = Eight<IO>::load(x + (r0 + r) * ld + c);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, magnitude(e[r].v[i]));
+        m = max(m, __shfl_xor_sync(~0u, m, 1));
+        m = max(m, __shfl_xor_sync(~0u, m, 2));
+        m = max(m, __shfl_xor_sync(~0u, m, 4));
+        const uint32_t s = code_step(m);
+        if (!in || r0 + r >= rows) continue;
+        const uint32_t a = codes_of(e[r].v[0], s), b = codes_of(e[r].v[1], s), d = codes_of(e[r].v[2], s), f = codes_of(e[r].v[3], s);
+        *reinterpret_cast<uint2 *>(codes + (r0 + r) * C + c) = make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(d, f, 0x5410));
+        if (lane % 8 == 0) steps[(r0 + r) * blocks + c / kDiagSlice] = (uint8_t)s;
+    }
+}
+
+// Any width and address: a warp takes one block of one row, two channels to a lane.
 template <typename IO>
 __global__ void __launch_bounds__(256) pack_kernel(int64_t rows, int64_t C, const IO *x, int64_t ld, int8_t *codes, uint8_t *steps) {
     const int lane = threadIdx.x % 32;
@@ -117,6 +178,37 @@ __global__ void __launch_bounds__(256) pack_kernel(int64_t rows, int64_t C, cons
 // The value in the type that it is read back in: f16's range is the only one that a code can pass.
 template <typename IO> __device__ __forceinline__ float held(float v) { return v; }
 template <> __device__ __forceinline__ float held<__half>(float v) { return v > 65504.f ? 65504.f : v < -65504.f ? -65504.f : v; }
+
+template <typename IO>
+__global__ void __launch_bounds__(256) unpack_wide_kernel(int64_t rows, int C, const int8_t *codes, const uint8_t *steps, IO *y, int64_t ld) {
+    const int lane = threadIdx.x % 32, c = (blockIdx.x * 32 + lane) * 8, blocks = (C + kDiagSlice - 1) / kDiagSlice;
+    const int64_t r0 = ((int64_t)blockIdx.y * 8 + threadIdx.x / 32) * R;
+    if (c >= C) return;
+    uint2 q[R];
+    uint32_t s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        q[r] = make_uint2(0, 0);
+        s[r] = 16;
+        if (r0 + r < rows) {
+            q[r] = __ldcs(reinterpret_cast<const uint2 *>(codes + (r0 + r) * C + c));
+            s[r] = steps[(r0 + r) * blocks + c / kDiagSlice];
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (r0 + r >= rows) break;
+        const F2 step = both(code_scale(s[r]));
+        Eight<IO> e;
+        e.v[0] = mul2(code_values(q[r].x & 0xffff), step);
+        e.v[1] = mul2(code_values(q[r].x >> 16), step);
+        e.v[2] = mul2(code_values(q[r].y & 0xffff), step);
+        e.v[3] = mul2(code_values(q[r].y >> 16), step);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e.v[i] = {held<IO>(e.v[i].x), held<IO>(e.v[i].y)};
+        e.store(y + (r0 + r) * ld + c);
+    }
+}
 
 template <typename IO>
 __global__ void __launch_bounds__(256) unpack_kernel(int64_t rows, int64_t C, const int8_t *codes, const uint8_t *steps, IO *y, int64_t ld) {
@@ -146,24 +238,43 @@ cudaError_t launch_diag_decode(const DiagDecodeParams &p, gdn_dtype io, int gate
     }
 }
 
+// Whether rows are taken by eight channels: widths, strides and addresses have to allow it, and a grid's second extent the rows.
+bool code_wide(gdn_dtype io, int64_t rows, int64_t C, const void *x, int64_t ld, const void *codes) {
+    const size_t es = io == GDN_F32 ? 4 : 2;
+    return C % 8 == 0 && C <= INT32_MAX - 256 && ld % 8 == 0 && (uintptr_t)x % 16 == 0 && (uintptr_t)codes % 8 == 0 &&
+           (rows + 8 * R - 1) / (8 * R) <= 65535 && es * 8 % 16 == 0;
+}
+dim3 code_grid(int64_t rows, int64_t C) { return dim3((unsigned)((C + 255) / 256), (unsigned)((rows + 8 * R - 1) / (8 * R))); }
+
+template <typename IO>
+void pack(int64_t rows, int64_t C, const void *x, int64_t ld, int8_t *codes, uint8_t *steps, bool wide, cudaStream_t stream) {
+    if (wide) pack_wide_kernel<IO><<<code_grid(rows, C), 256, 0, stream>>>(rows, (int)C, (const IO *)x, ld, codes, steps);
+    else pack_kernel<IO><<<code_blocks(rows, C), 256, 0, stream>>>(rows, C, (const IO *)x, ld, codes, steps);
+}
+template <typename IO>
+void unpack(int64_t rows, int64_t C, const int8_t *codes, const uint8_t *steps, void *y, int64_t ld, bool wide, cudaStream_t stream) {
+    if (wide) unpack_wide_kernel<IO><<<code_grid(rows, C), 256, 0, stream>>>(rows, (int)C, codes, steps, (IO *)y, ld);
+    else unpack_kernel<IO><<<code_blocks(rows, C), 256, 0, stream>>>(rows, C, codes, steps, (IO *)y, ld);
+}
+
 cudaError_t launch_checkpoint_pack(gdn_dtype io, int64_t rows, int64_t C, const void *x, int64_t ld, int8_t *codes, uint8_t *steps,
                                    cudaStream_t stream) {
-    const unsigned n = code_blocks(rows, C);
+    const bool wide = code_wide(io, rows, C, x, ld, codes);
     switch (io) {
-        case GDN_F32: pack_kernel<float><<<n, 256, 0, stream>>>(rows, C, (const float *)x, ld, codes, steps); break;
-        case GDN_BF16: pack_kernel<__nv_bfloat16><<<n, 256, 0, stream>>>(rows, C, (const __nv_bfloat16 *)x, ld, codes, steps); break;
-        default: pack_kernel<__half><<<n, 256, 0, stream>>>(rows, C, (const __half *)x, ld, codes, steps);
+        case GDN_F32: pack<float>(rows, C, x, ld, codes, steps, wide, stream); break;
+        case GDN_BF16: pack<__nv_bfloat16>(rows, C, x, ld, codes, steps, wide, stream); break;
+        default: pack<__half>(rows, C, x, ld, codes, steps, wide, stream);
     }
     return cudaGetLastError();
 }
 
 cudaError_t launch_checkpoint_unpack(gdn_dtype io, int64_t rows, int64_t C, const int8_t *codes, const uint8_t *steps, void *y, int64_t ld,
                                      cudaStream_t stream) {
-    const unsigned n = code_blocks(rows, C);
+    const bool wide = code_wide(io, rows, C, y, ld, codes);
     switch (io) {
-        case GDN_F32: unpack_kernel<float><<<n, 256, 0, stream>>>(rows, C, codes, steps, (float *)y, ld); break;
-        case GDN_BF16: unpack_kernel<__nv_bfloat16><<<n, 256, 0, stream>>>(rows, C, codes, steps, (__nv_bfloat16 *)y, ld); break;
-        default: unpack_kernel<__half><<<n, 256, 0, stream>>>(rows, C, codes, steps, (__half *)y, ld);
+        case GDN_F32: unpack<float>(rows, C, codes, steps, y, ld, wide, stream); break;
+        case GDN_BF16: unpack<__nv_bfloat16>(rows, C, codes, steps, y, ld, wide, stream); break;
+        default: unpack<__half>(rows, C, codes, steps, y, ld, wide, stream);
     }
     return cudaGetLastError();
 }
