@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             fill_rows<IO, LT>(&st.b[0][0], infinity_bits<IO>(false), lane);
         }
     }
+    const Stager<IO, LT> from_x(p.x, p.ld_x, lane), from_a(p.a, p.ld_a, lane), from_b(p.b, p.ld_b, lane), from_dy(p.dy, p.ld_y, lane);
     auto stage = [&](uint32_t item) {
         const int j = walk.tile_of(item), slice = (int)item - j * slices, w0 = (tiles - 1 - j) * kDiagTile + w * LT, c0 = slice * kDiagSlice;
         if constexpr (CODES) {
@@ -154,11 +155,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             stage_codes(&st.codes_a[0][0], st.as, p, 1, slice, slices, w0, 0, rows, 0x01010101u, lane);
             if (has_b) stage_codes(&st.b[0][0], st.bs, p, 2, slice, slices, w0, 0, rows, 0u, lane);
         } else {
-            stage_rows<IO, LT>(&st.x[0][0], (const IO *)p.x, p.ld_x, w0, 0, rows, c0, C, p.wide, 0u, lane);
-            stage_rows<IO, LT>(st.a(), (const IO *)p.a, p.ld_a, w0, 0, rows, c0, C, p.wide, shut, lane);
-            if (has_b) stage_rows<IO, LT>(&st.b[0][0], (const IO *)p.b, p.ld_b, w0, 0, rows, c0, C, p.wide, 0u, lane);
+            from_x.rows(&st.x[0][0], w0, rows, c0, C, p.wide, 0u, lane);
+            from_a.rows(st.a(), w0, rows, c0, C, p.wide, shut, lane);
+            if (has_b) from_b.rows(&st.b[0][0], w0, rows, c0, C, p.wide, 0u, lane);
         }
-        stage_rows<IO, LT>(&st.dy[0][0], (const IO *)p.dy, p.ld_y, w0, 0, rows, c0, C, p.wide, 0u, lane);
+        from_dy.rows(&st.dy[0][0], w0, rows, c0, C, p.wide, 0u, lane);
         stage_commit();
     };
     float step_x = 0.f, step_a = 0.f, step_b = 0.f;
@@ -215,6 +216,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
 #pragma unroll
                     for (int k = 0; k < kGroup; ++k) {
                         G[k] = diag_exponent<GATE>(a[k], l);
+                        if (!decltype(only_near)::value) {      // held finite, for a decay to 0 times it; a NaN stays one
+                            asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(G[k].x));
+                            asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(G[k].y));
+                        }
                         const DiagDecay d = diag_decay<decltype(only_near)::value>(G[k]);
                         const F2 v = mul2(diag_sigmoid(b[k], l.nbbias), x[k]);
                         in[k] = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n).w, v);
@@ -276,15 +281,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                     }
 #pragma unroll
                     for (int k = 0; k < kGroup; ++k) {
-                        if (begins >> (t0 + k) & 1)
-                            at = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t0 + k] * C, c, C) : both(0.f);
                         sh_[(t0 + k) * 32 + lane] = make_float2(at.x, at.y);
                         at = fma2(alpha[k], at, in[k]);
                     }
                 }
             };
-            if (near) follow(std::true_type{});
-            else follow(std::false_type{});
+            if (begins) {
+#pragma unroll 1
+                for (int t = 0; t < LT; ++t) {
+                    if (begins >> t & 1) at = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t] * C, c, C) : both(0.f);
+                    const F2 in = get_pair(sh_ + t * 32, lane);
+                    sh_[t * 32 + lane] = make_float2(at.x, at.y);
+                    at = fma2(diag_decay<false>(get_pair(sG + t * 32, lane)).alpha, at, in);
+                }
+            } else if (near) {
+                follow(std::true_type{});
+            } else {
+                follow(std::false_type{});
+            }
         }
         side_sync<kThreads>(2);
         const uint32_t next = sh.next;
@@ -318,16 +332,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                         const F2 i = diag_sigmoid(b[k], l.nbbias), v = mul2(i, x[k]), minus = both(-1.f);
                         const DiagDecay d = diag_decay<decltype(only_near)::value>(G[k]);
                         const DiagWeight o = diag_weigh<WEIGHT>(d.n);
-                        F2 slope = h[k];                                            // dg / (g alpha)
-                        if (WEIGHT == GDN_DIAG_NORM) slope = fma2(mul2(v, mul2(d.alpha, minus)), o.winv, slope);
-                        if (WEIGHT == GDN_DIAG_COMPLEMENT) slope = fma2(v, minus, slope);
+                        F2 slope;                                                   // dG / (g alpha), G = -g
+                        if (WEIGHT == GDN_DIAG_NORM) slope = fma2(mul2(v, d.alpha), o.winv, mul2(h[k], minus));
+                        else slope = fma2(h[k], minus, WEIGHT == GDN_DIAG_COMPLEMENT ? v : both(0.f));
                         const F2 ag = mul2(d.alpha, g), dv = WEIGHT == GDN_DIAG_PLAIN ? g : mul2(g, o.w);
-                        const F2 dG = mul2(mul2(ag, slope), minus);                 // the gradient at G = -g
-                        const F2 dGG = mul2(dG, F2{fminf(G[k].x, 1e30f), fminf(G[k].y, 1e30f)});        // (0 of a decay to 0)
-                        const F2 sp = mul2(G[k], l.inverse);                        // the gate's opening
-                        const F2 da_ = GATE == GDN_DIAG_SIGMOID ? fma2(dGG, mul2(sp, minus), dGG) : mul2(dG, mul2(l.rate, diag_decay<false>(sp).n));
-                        const F2 dvv = mul2(dv, v), db_ = fma2(dvv, mul2(i, minus), dvv);
+                        const F2 dG = mul2(ag, slope), dGG = mul2(dG, G[k]);
+                        const F2 nsp = mul2(G[k], l.ninverse);                      // the gate's opening, negative
+                        const F2 da_ = GATE == GDN_DIAG_SIGMOID ? fma2(dGG, nsp, dGG)
+                                                                : mul2(dG, mul2(l.rate, diag_decay<false>(F2{-nsp.x, -nsp.y}).n));
                         out_x[k] = mul2(dv, i);
+                        const F2 db_ = mul2(out_x[k], fma2(v, minus, x[k]));        // dx x (1 - i)
                         out_a[k] = da_;
                         out_b[k] = db_;
                         if (kPlain || w0 + t < rows) {

@@ -117,7 +117,7 @@ __device__ __forceinline__ F2 diag_softplus(F2 z) {
 
 // The parameters of a lane's two channels.
 struct DiagLane {
-    F2 rate, inverse, abias, nabias, nbbias;   // e^A_log, 1 / e^A_log (or 0), a_bias, -a_bias log2 e, -b_bias log2 e
+    F2 rate, ninverse, abias, nabias, nbbias;   // e^A_log, -1 / e^A_log (or 0), a_bias, -a_bias log2 e, -b_bias log2 e
 };
 // The input's weight, and for `norm` (sqrt(1 - alpha^2)) 1 / w: at alpha = 1 the weight is 0 and 1 / w finite.
 struct DiagWeight {
@@ -142,7 +142,7 @@ __device__ __forceinline__ DiagLane diag_lane(const float *A_log, const float *a
     const bool one = c < C, two = c + 1 < C;
     l.rate = {one ? -ssm_rate(A_log[c]) : 0.f, two ? -ssm_rate(A_log[c + 1]) : 0.f};
     // (A rate is a normal number or 0, whose channel's gate then counts as shut.)
-    l.inverse = {l.rate.x != 0.f ? 1.f / l.rate.x : 0.f, l.rate.y != 0.f ? 1.f / l.rate.y : 0.f};
+    l.ninverse = {l.rate.x != 0.f ? -1.f / l.rate.x : 0.f, l.rate.y != 0.f ? -1.f / l.rate.y : 0.f};
     if (a_bias) l.abias = {one ? a_bias[c] : 0.f, two ? a_bias[c + 1] : 0.f};
     F2 bb = both(0.f);
     if (b_bias) bb = {one ? b_bias[c] : 0.f, two ? b_bias[c + 1] : 0.f};
@@ -206,58 +206,59 @@ template <typename IO> __device__ __forceinline__ uint32_t infinity_bits(bool ne
     return negative ? b | (sizeof(IO) == 4 ? 0x80000000u : 0x80008000u) : b;
 }
 
-// Copies rows [r0, r0 + N) of a slice (channels c0 ..) to shared memory, [N][64], asynchronously where `wide` allows, by one
-// warp for itself.  Rows outside [lo, hi) become `outside`, channels behind C zeros.
-template <typename IO, int N>
-__device__ __forceinline__ void stage_rows(IO *to, const IO *base, int64_t ld, int r0, int lo, int hi, int c0, int C,
-                                           int wide, uint32_t outside, int lane) {
-    constexpr int kRow = kDiagSlice * sizeof(IO) / 16, kStep = 32 / kRow;    // 16-byte pieces of a row; rows at a time
-    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
-    if (wide == 16) {
-        const int piece = lane % kRow;
-        const int c = c0 + piece * (16 / (int)sizeof(IO));
-        const int bytes = c >= C ? 0 : min(16, (C - c) * (int)sizeof(IO));
-        const IO *from = base + (int64_t)(r0 + lane / kRow) * ld + (bytes ? c : 0);
-        const int64_t apart = kStep * ld;
-        const uint32_t at = dst + lane * 16;
-        if (r0 >= lo && r0 + N <= hi) {
+// Copies N rows of a slice to shared memory, [N][64], by one warp for itself, asynchronously where `wide` allows.  Rows from
+// `rows` on become `outside`, channels behind C zeros.
+template <typename IO, int N> struct Stager {
+    static constexpr int kRow = kDiagSlice * sizeof(IO) / 16, kStep = 32 / kRow;    // 16-byte pieces of a row; rows at a time
+    const IO *base;         // this lane's piece of row 0 of slice 0
+    int64_t ld;
+    __device__ __forceinline__ Stager(const void *from, int64_t ld_, int lane)
+        : base(static_cast<const IO *>(from) + (lane / kRow) * ld_ + lane % kRow * (16 / (int)sizeof(IO))), ld(ld_) {}
+
+    __device__ __forceinline__ void rows(IO *to, int r0, int rows, int c0, int C, int wide, uint32_t outside, int lane) const {
+        const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to)) + lane * 16;
+        const IO *from = base + (int64_t)r0 * ld + c0;
+        if (wide == 16 && r0 + N <= rows && c0 + kDiagSlice <= C) {
 #pragma unroll
-            for (int i = 0; i < N / kStep; ++i, from += apart)
-                asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(at + i * 512), "l"(from), "r"(bytes) : "memory");
-        } else {
-#pragma unroll 1
-            for (int i = 0; i < N / kStep; ++i, from += apart) {
-                const int row = r0 + lane / kRow + i * kStep;
-                if (row >= lo && row < hi)
-                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(at + i * 512), "l"(from), "r"(bytes) : "memory");
-                else
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + i * 512), "r"(outside) : "memory");
+            for (int i = 0; i < N / kStep; ++i) {
+                asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst + i * 512), "l"(from) : "memory");
+                from += kStep * ld;
             }
+            return;
         }
-        return;
+        some_rows(to, from, r0, rows, c0, C, wide, outside, lane);
     }
-    using Raw = typename Pair<IO>::Raw;
-    const int c = c0 + 2 * lane;
-    const IO *from = base + (int64_t)r0 * ld + c;
-    const uint32_t at = dst + lane * (uint32_t)sizeof(Raw);
-#pragma unroll 4
-    for (int t = 0; t < N; ++t) {
-        const bool row = r0 + t >= lo && r0 + t < hi;
-        if (row && wide == (int)sizeof(Raw) && c + 1 < C) {
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at + t * 32 * (uint32_t)sizeof(Raw)), "l"(from + t * ld), "n"(sizeof(Raw)) : "memory");
-        } else {
+    __device__ __noinline__ void some_rows(IO *to, const IO *from, int r0, int rows, int c0, int C, int wide, uint32_t outside, int lane) const {
+        const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+        if (wide == 16) {
+            const int left = (C - c0) * (int)sizeof(IO) - lane % kRow * 16, bytes = left < 0 ? 0 : left > 16 ? 16 : left;
+            if (bytes == 0) from = base;
+            for (int i = 0; i < N / kStep; ++i, from += bytes ? kStep * ld : 0) {
+                if (r0 + lane / kRow + i * kStep < rows)
+                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst + lane * 16 + i * 512), "l"(from), "r"(bytes) : "memory");
+                else
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + lane * 16 + i * 512), "r"(outside) : "memory");
+            }
+            return;
+        }
+        using Raw = typename Pair<IO>::Raw;
+        const int c = c0 + 2 * lane;
+        from = base - (lane / kRow) * ld - lane % kRow * (16 / (int)sizeof(IO)) + (int64_t)r0 * ld + c;
+        for (int t = 0; t < N; ++t, from += ld) {
             IO *q = to + t * kDiagSlice + 2 * lane;
-            if (row) {
-                q[0] = c < C ? from[t * ld] : IO(0.f);
-                q[1] = c + 1 < C ? from[t * ld + 1] : IO(0.f);
-            } else {
+            if (r0 + t >= rows) {
                 uint32_t *v = reinterpret_cast<uint32_t *>(q);
                 v[0] = outside;
                 if (sizeof(IO) == 4) v[1] = outside;
+            } else if (wide == (int)sizeof(Raw) && c + 1 < C) {
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst + (t * 32 + lane) * (uint32_t)sizeof(Raw)), "l"(from), "n"(sizeof(Raw)) : "memory");
+            } else {
+                q[0] = c < C ? from[0] : IO(0.f);
+                q[1] = c + 1 < C ? from[1] : IO(0.f);
             }
         }
     }
-}
+};
 // Fills N staged rows with four bytes.
 template <typename IO, int N> __device__ __forceinline__ void fill_rows(IO *to, uint32_t bits, int lane) {
     for (int i = lane; i < N * kDiagSlice * (int)sizeof(IO) / 4; i += 32) reinterpret_cast<uint32_t *>(to)[i] = bits;

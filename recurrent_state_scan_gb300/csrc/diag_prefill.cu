@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(256) diag_begin_kernel(const __grid_constant__
     const int slices = (p.channels + kDiagSlice - 1) / kDiagSlice, row = slices * kDiagSlice;
     for (int c = 2 * (int)i; c < row; c += 2 * (int)all) {
         const DiagLane l = diag_lane(p.A_log, p.a_bias, p.b_bias, c, p.channels);
-        const F2 v[5] = {l.rate, l.inverse, l.abias, l.nabias, l.nbbias};
+        const F2 v[5] = {l.rate, l.ninverse, l.abias, l.nabias, l.nbbias};
         for (int k = 0; k < 5; ++k) *reinterpret_cast<float2 *>(p.table + (int64_t)k * row + c) = make_float2(v[k].x, v[k].y);
     }
 }

@@ -77,11 +77,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_prefil
     float4 *held = &sh.held[w][0][lane];
     const uint32_t shut = infinity_bits<IO>(true);
     if (!has_b) fill_rows<IO, LT>(sb, infinity_bits<IO>(false), lane);
+    const Stager<IO, LT> from_x(p.x, p.ld_x, lane), from_a(p.a, p.ld_a, lane), from_b(p.b, p.ld_b, lane);
     auto stage = [&](uint32_t item) {
         const int tile = walk.tile_of(item), w0 = tile * kDiagTile + w * LT, c0 = ((int)item - tile * slices) * kDiagSlice;
-        stage_rows<IO, LT>(sx, (const IO *)p.x, p.ld_x, w0, 0, rows, c0, C, p.wide, 0u, lane);
-        stage_rows<IO, LT>(sa, (const IO *)p.a, p.ld_a, w0, 0, rows, c0, C, p.wide, shut, lane);
-        if (has_b) stage_rows<IO, LT>(sb, (const IO *)p.b, p.ld_b, w0, 0, rows, c0, C, p.wide, 0u, lane);
+        from_x.rows(sx, w0, rows, c0, C, p.wide, 0u, lane);
+        from_a.rows(sa, w0, rows, c0, C, p.wide, shut, lane);
+        if (has_b) from_b.rows(sb, w0, rows, c0, C, p.wide, 0u, lane);
         stage_commit();
     };
     EdgeWindow window = edge_window(p, 0, lane);
