@@ -581,10 +581,11 @@ gdn_status gdn_ssm_decode(const gdn_ssm_shape *shape, const gdn_ssm_params *para
  * elementwise over the channels, in fp32; y is rounded once.  Results are the same bits on
  * every call.
  *
- * For training the forward pass keeps what the backward pass needs beside its own inputs:
- * h before every 64th row (rows counted over the whole call), and with GDN_DIAG_KEEP_8BIT
- * x, a and b as well, as the 8-bit codes of gdn_checkpoint_pack.  The backward pass then
- * takes the gradient at the values that the codes hold, h running on from each kept state.
+ * For training the forward pass keeps what the backward pass needs: with KEEP_STATES some of
+ * h, beside x, a and b themselves; with KEEP_8BIT x, a and b as the 8-bit codes of
+ * gdn_checkpoint_pack, and h before every 64th row (rows counted over the whole call).  The
+ * backward pass then takes the gradient at the values that the codes hold, h running on from
+ * each kept state.
  * ---------------------------------------------------------------------------------- */
 typedef enum { GDN_DIAG_SOFTPLUS = 0, GDN_DIAG_SIGMOID = 1 } gdn_diag_gate;
 typedef enum { GDN_DIAG_PLAIN = 0, GDN_DIAG_COMPLEMENT = 1, GDN_DIAG_NORM = 2 } gdn_diag_weighting;

@@ -90,7 +90,8 @@ gdn_status check(const gdn_diag_shape *s, bool varlen, Geometry &g) {
     const size_t slices = diag_slices(s->channels), tiles = (size_t)(g.rows + kDiagTile - 1) / kDiagTile;
     if (tiles * slices > INT32_MAX / 2)
         return fail(GDN_ERR_UNSUPPORTED, "%lld rows of %d channels are not built", (long long)g.rows, s->channels);
-    g.kept_states = s->keep != GDN_DIAG_KEEP_NONE ? tiles * slices * kDiagSlice * 4 : 0;
+    const size_t held = s->keep == GDN_DIAG_KEEP_8BIT ? tiles : s->keep == GDN_DIAG_KEEP_STATES ? tiles * (kDiagTile / kDiagRows) : 0;
+    g.kept_states = held * slices * kDiagSlice * 4;
     g.kept = g.kept_states;
     if (s->keep == GDN_DIAG_KEEP_8BIT) g.kept += (size_t)(2 + s->input_gate) * slices * tiles * kDiagTile * (kDiagSlice + 1);
     return GDN_OK;

@@ -19,7 +19,7 @@
 namespace gdn {
 namespace {
 
-constexpr int LT = 16, W = kDiagTile / LT;      // a warp's rows; the warps that take rows
+constexpr int LT = kDiagRows, W = kDiagTile / LT;      // a warp's rows; the warps that take rows
 constexpr int kThreads = (W + 1) * 32;
 constexpr int kGroup = 4;                       // rows whose loads go out together
 
@@ -193,6 +193,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             ends = edges >> 1 & live;
         }
         const uint32_t special = begins | ends;
+        // Without codes h is there before each warp's rows; else before the tile's.
+        F2 at = both(0.f);
+        if (some && (CODES ? tile : w0) > 0)
+            at = get_pair(reinterpret_cast<const float2 *>(p.kept + (int64_t)(CODES ? tile : w0 / LT) * slices * kDiagSlice + c0), lane);
+        const bool direct = !CODES && special == 0;
         stage_wait();
         if constexpr (CODES) {
             step_x = code_scale(st.xs[lane % LT]);
@@ -201,10 +206,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         }
         {
             F2 through = both(1.f);
-            auto take = [&](auto only_near) {
+            // DIRECT: -h before each row goes to shared memory at once, else the input, until h is known.
+            auto take = [&](auto only_near, auto directly) {
+                constexpr bool kNear = decltype(only_near)::value, kDirect = decltype(directly)::value;
+                F2 nat = mul2(at, both(-1.f));
 #pragma unroll 1
                 for (int t0 = 0; t0 < LT; t0 += kGroup) {       // (the loads of a group go out before its stores)
-                    F2 a[kGroup], b[kGroup], x[kGroup], dy[kGroup], G[kGroup], in[kGroup];
+                    F2 a[kGroup], b[kGroup], x[kGroup], dy[kGroup], G[kGroup], out[kGroup];
 #pragma unroll
                     for (int k = 0; k < kGroup; ++k) {
                         a[k] = get_a(t0 + k);
@@ -216,27 +224,38 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
 #pragma unroll
                     for (int k = 0; k < kGroup; ++k) {
                         G[k] = diag_exponent<GATE>(a[k], l);
-                        if (!decltype(only_near)::value) {      // held finite, for a decay to 0 times it; a NaN stays one
+                        if (!kNear) {       // held finite, for a decay to 0 times it; a NaN stays one
                             asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(G[k].x));
                             asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(G[k].y));
                         }
-                        const DiagDecay d = diag_decay<decltype(only_near)::value>(G[k]);
-                        const F2 v = mul2(diag_sigmoid(b[k], l.nbbias), x[k]);
-                        in[k] = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n).w, v);
+                        const DiagDecay d = diag_decay<kNear>(G[k]);
+                        const F2 v = mul2(kDirect ? diag_minus_sigmoid(b[k], l.nbbias) : diag_sigmoid(b[k], l.nbbias), x[k]);
+                        const F2 in = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n), v);
                         sum_G = add2(sum_G, G[k]);
-                        H = fma2(d.alpha, H, in[k]);
+                        if (kDirect) {
+                            out[k] = nat;
+                            nat = fma2(d.alpha, nat, in);
+                        } else {
+                            out[k] = in;
+                            H = fma2(d.alpha, H, in);
+                        }
                         through = mul2(through, d.alpha);
                         D = fma2(through, dy[k], D);
                     }
 #pragma unroll
                     for (int k = 0; k < kGroup; ++k) {
                         sG[(t0 + k) * 32 + lane] = make_float2(G[k].x, G[k].y);
-                        sh_[(t0 + k) * 32 + lane] = make_float2(in[k].x, in[k].y);
+                        sh_[(t0 + k) * 32 + lane] = make_float2(out[k].x, out[k].y);
                     }
                 }
             };
-            if (near) take(std::true_type{});
-            else take(std::false_type{});
+            if (!direct) {
+                if (near) take(std::true_type{}, std::false_type{});
+                else take(std::false_type{}, std::false_type{});
+            } else if constexpr (!CODES) {
+                if (near) take(std::true_type{}, std::true_type{});
+                else take(std::false_type{}, std::true_type{});
+            }
             if (special) {
                 through = both(1.f);
                 D = both(0.f);
@@ -264,12 +283,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         sh.back[w][lane] = make_float2(D.x, D.y);
         __syncwarp();
         side_sync<kThreads>(1);
-        {                       // h before each row, while the fifth warp hands on and waits
-            F2 at = both(0.f);
-            if (tile > 0) at = get_pair(reinterpret_cast<const float2 *>(p.kept + ((int64_t)tile * slices + slice) * kDiagSlice), lane);
+        if (!direct) {          // -h before each row, while the fifth warp hands on and waits
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
-                if (k < w) at = diag_apply(get_product(sh.maps[k], lane), get_pair(sh.maps[k].shift, lane), at);
+                if (CODES && k < w) at = diag_apply(get_product(sh.maps[k], lane), get_pair(sh.maps[k].shift, lane), at);
             auto follow = [&](auto only_near) {
 #pragma unroll 1
                 for (int t0 = 0; t0 < LT; t0 += kGroup) {
@@ -281,17 +298,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                     }
 #pragma unroll
                     for (int k = 0; k < kGroup; ++k) {
-                        sh_[(t0 + k) * 32 + lane] = make_float2(at.x, at.y);
+                        sh_[(t0 + k) * 32 + lane] = make_float2(-at.x, -at.y);
                         at = fma2(alpha[k], at, in[k]);
                     }
                 }
             };
-            if (begins) {
+            if (begins || !CODES) {
 #pragma unroll 1
                 for (int t = 0; t < LT; ++t) {
                     if (begins >> t & 1) at = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t] * C, c, C) : both(0.f);
                     const F2 in = get_pair(sh_ + t * 32, lane);
-                    sh_[t * 32 + lane] = make_float2(at.x, at.y);
+                    sh_[t * 32 + lane] = make_float2(-at.x, -at.y);
                     at = fma2(diag_decay<false>(get_pair(sG + t * 32, lane)).alpha, at, in);
                 }
             } else if (near) {
@@ -331,11 +348,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                             g = add2(g, load_state(p.dstate_out + (int64_t)(sh.edge_first[w][t + 1] - 1) * C, c, C));
                         const F2 i = diag_sigmoid(b[k], l.nbbias), v = mul2(i, x[k]), minus = both(-1.f);
                         const DiagDecay d = diag_decay<decltype(only_near)::value>(G[k]);
-                        const DiagWeight o = diag_weigh<WEIGHT>(d.n);
-                        F2 slope;                                                   // dG / (g alpha), G = -g
-                        if (WEIGHT == GDN_DIAG_NORM) slope = fma2(mul2(v, d.alpha), o.winv, mul2(h[k], minus));
-                        else slope = fma2(h[k], minus, WEIGHT == GDN_DIAG_COMPLEMENT ? v : both(0.f));
-                        const F2 ag = mul2(d.alpha, g), dv = WEIGHT == GDN_DIAG_PLAIN ? g : mul2(g, o.w);
+                        F2 slope = h[k];                                            // dG / (g alpha), G = -g (h: negative)
+                        if (WEIGHT == GDN_DIAG_NORM) slope = fma2(mul2(v, d.alpha), diag_unweigh(d.n), slope);
+                        if (WEIGHT == GDN_DIAG_COMPLEMENT) slope = add2(v, slope);
+                        const F2 ag = mul2(d.alpha, g), dv = WEIGHT == GDN_DIAG_PLAIN ? g : mul2(g, diag_weigh<WEIGHT>(d.n));
                         const F2 dG = mul2(ag, slope), dGG = mul2(dG, G[k]);
                         const F2 nsp = mul2(G[k], l.ninverse);                      // the gate's opening, negative
                         const F2 da_ = GATE == GDN_DIAG_SIGMOID ? fma2(dGG, nsp, dGG)

@@ -7,6 +7,7 @@
 namespace gdn {
 
 constexpr int kDiagTile = 64;    // token rows between two kept states, and of one CTA's step
+constexpr int kDiagRows = 16;    // of one warp
 constexpr int kDiagSlice = 64;   // channels of one CTA, and of a block of the 8-bit codes
 
 // One call (validated arguments).  Token rows are those of the whole call: t of sequence b at
@@ -26,7 +27,7 @@ struct DiagParams {
     bool pairs;                          // every output row can be written two channels at a time
     int *status;
     // What the forward pass keeps for the backward pass.
-    float *kept;                         // [tiles][slices * 64] or null: h before each tile's first row
+    float *kept;                         // h before rows, [.][slices * 64], or null: with codes before every 64th, else every 16th
     int8_t *codes;                       // [x | a | b][slice][rows, in whole tiles][64] or null
     uint8_t *steps;                      // [x | a | b][slice][rows, in whole tiles]
     // The backward pass.
@@ -102,6 +103,12 @@ __device__ __forceinline__ F2 diag_sigmoid(F2 v, F2 nbias) {
     const F2 d = add2({ex2(t.x), ex2(t.y)}, both(1.f));
     return {rcp(d.x), rcp(d.y)};
 }
+// Its negative, by the same steps.
+__device__ __forceinline__ F2 diag_minus_sigmoid(F2 v, F2 nbias) {
+    const F2 t = fma2(v, both(-kLog2e), nbias);
+    const F2 d = fma2({ex2(t.x), ex2(t.y)}, both(-1.f), both(-1.f));
+    return {rcp(d.x), rcp(d.y)};
+}
 // softplus(z) = max(z, 0) + log(1 + e), e = e^-|z|.  log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by
 // s + s^3 q(s^2), q the Chebyshev fit of the series of atanh (1.6e-8 of the result): digits are kept however
 // small e is.
@@ -119,19 +126,22 @@ __device__ __forceinline__ F2 diag_softplus(F2 z) {
 struct DiagLane {
     F2 rate, ninverse, abias, nabias, nbbias;   // e^A_log, -1 / e^A_log (or 0), a_bias, -a_bias log2 e, -b_bias log2 e
 };
-// The input's weight, and for `norm` (sqrt(1 - alpha^2)) 1 / w: at alpha = 1 the weight is 0 and 1 / w finite.
-struct DiagWeight {
-    F2 w, winv;
-};
-template <int WEIGHT> __device__ __forceinline__ DiagWeight diag_weigh(F2 n) {
-    if (WEIGHT == GDN_DIAG_COMPLEMENT) return {n, both(0.f)};
-    if (WEIGHT == GDN_DIAG_PLAIN) return {both(1.f), both(0.f)};
-    const F2 t = fma2(n, both(-1.f), both(2.f)), q = mul2(n, t), some = fma2(n, t, both(0x1p-122f));
-    DiagWeight o;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(o.winv.x) : "f"(some.x));
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(o.winv.y) : "f"(some.y));
-    o.w = mul2(q, o.winv);
-    return o;
+// The input's weight, and for the backward pass and `norm` (sqrt(1 - alpha^2)) 1 / w, finite at alpha = 1 where the weight is 0.
+template <int WEIGHT> __device__ __forceinline__ F2 diag_weigh(F2 n) {
+    if (WEIGHT == GDN_DIAG_COMPLEMENT) return n;
+    if (WEIGHT == GDN_DIAG_PLAIN) return both(1.f);
+    const F2 q = mul2(n, fma2(n, both(-1.f), both(2.f)));
+    F2 w;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(w.x) : "f"(q.x));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(w.y) : "f"(q.y));
+    return w;
+}
+__device__ __forceinline__ F2 diag_unweigh(F2 n) {
+    const F2 q = fma2(n, fma2(n, both(-1.f), both(2.f)), both(0x1p-122f));
+    F2 r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(q.x));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(q.y));
+    return r;
 }
 template <int GATE> __device__ __forceinline__ F2 diag_exponent(F2 a, const DiagLane &l) {
     return mul2(l.rate, GATE == GDN_DIAG_SIGMOID ? diag_sigmoid(a, l.nabias) : diag_softplus(add2(a, l.abias)));

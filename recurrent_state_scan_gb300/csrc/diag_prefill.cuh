@@ -15,7 +15,7 @@
 namespace gdn {
 namespace {
 
-constexpr int LT = 16, W = kDiagTile / LT;      // a warp's rows; the warps that take rows
+constexpr int LT = kDiagRows, W = kDiagTile / LT;      // a warp's rows; the warps that take rows
 constexpr int kThreads = (W + 1) * 32;
 
 template <typename IO> struct Shared {
@@ -67,8 +67,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_prefil
             side_arrive<kThreads>(3 + buf);
             item = next;
             next = __shfl_sync(~0u, later, 0);
-            if (p.kept && tile > 0)
-                *reinterpret_cast<float2 *>(p.kept + ((int64_t)tile * slices + slice) * kDiagSlice + 2 * lane) = make_float2(h.x, h.y);
         }
         return;
     }
@@ -146,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_prefil
                     const DiagDecay d = diag_decay<decltype(only_near)::value>(G);
                     const F2 v = mul2(i, staged(sx, t, lane));
                     alpha[t] = d.alpha;
-                    u[t] = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n).w, v);
+                    u[t] = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n), v);
                     sum_G = add2(sum_G, G);
                     H = fma2(d.alpha, H, u[t]);
                 }
@@ -178,6 +176,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_prefil
         if (k > 0) {
             F2 h = get_pair(sh.start[buf ^ 1], lane);
             if (w > 0) h = diag_apply(get_product(sh.before[buf ^ 1][w], lane), get_pair(sh.before[buf ^ 1][w].shift, lane), h);
+            if (p.kept && old_w0 < rows && (!CODES || w == 0)) {
+                const int64_t row = CODES ? old_w0 / kDiagTile : old_w0 / LT;
+                *reinterpret_cast<float2 *>(p.kept + row * slices * kDiagSlice + old_c) = make_float2(h.x, h.y);
+            }
             const bool fast = p.pairs && (old_c | (kDiagSlice - 1)) < C;
             IO *y = (IO *)p.y + (int64_t)old_w0 * p.ld_y + old_c;
             if (old_w0 + LT <= rows && fast && (old_begins | old_ends) == 0) {

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(128) diag_decode_kernel(const __grid_constant_
         for (int k = 0; k < N; ++k) {
             const DiagDecay d = diag_decay<false>(diag_exponent<GATE>(av[k], l[k]));
             F2 v = p.has_b ? mul2(diag_sigmoid(bv[k], l[k].nbbias), xv[k]) : xv[k];
-            v = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n).w, v);
+            v = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n), v);
             h[k] = fma2(d.alpha, h[k], v);
         }
         if (VEC) {

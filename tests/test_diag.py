@@ -573,16 +573,23 @@ def test_gradients_against_differences(gate, weighting):
 @pytest.mark.gpu
 @pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("C,lens", [(130, [63, 1, 0, 200, 64]), (64, [1500])])
-def test_8_bits_in_the_backward_pass_are_those_of_pack(io, C, lens):
-    """Bit for bit the backward pass from the same kept states at unpack(pack(x)) and so on."""
+def test_the_kept_codes_are_those_of_pack(io, C, lens):
+    """Bit for bit, [x | a | b][slice of 64 channels][rows in whole tiles of 64][64] behind h before every 64th row; what else the
+    forward pass returns does not change with what it keeps."""
     m = draw(io, lens, C, seed=12)
     y, state, kept = prefill(m, "8bit")
-    plain = prefill(m)
-    assert torch.equal(y, plain[0]) and torch.equal(state, plain[1])
-    got = backward(m, kept)
-    held = dict(m, **{k: lib.gdn_checkpoint_unpack(*lib.gdn_checkpoint_pack(m[k]), m["io"]) for k in ("x", "a", "b")})
-    same = backward(held, prefill(m, "states")[2])
-    assert all(torch.equal(s, t) for s, t in zip(got, same))
+    for keep in (None, "states"):
+        other = prefill(m, keep)
+        assert torch.equal(y, other[0]) and torch.equal(state, other[1])
+    rows, slices = sum(lens), -(-C // 64)
+    tiles = -(-rows // 64)
+    data = kept.data[tiles * slices * 256:]
+    codes = data[:3 * slices * tiles * 4096].view(torch.int8).view(3, slices, tiles * 64, 64)
+    steps = data[3 * slices * tiles * 4096:].view(3, slices, tiles * 64)
+    for k, name in enumerate(("x", "a", "b")):
+        want, want_steps = lib.gdn_checkpoint_pack(m[name])
+        assert torch.equal(codes[k, :, :rows].transpose(0, 1).reshape(rows, -1)[:, :C], want[0])
+        assert torch.equal(steps[k, :, :rows].T, want_steps[0])
 
 
 @pytest.mark.gpu
