@@ -29,6 +29,7 @@ constexpr int kGroup = 4;                       // rows whose loads go out toget
 template <typename IO, bool CODES> struct Staged {
     alignas(16) IO x[LT][kDiagSlice], b[LT][kDiagSlice], dy[LT][kDiagSlice];
     alignas(16) float2 G[LT][32], h[LT][32];
+    alignas(16) float table[5][kDiagSlice], kept[kDiagSlice];       // the channels' parameters, h before the rows
     __device__ __forceinline__ IO *a() { return reinterpret_cast<IO *>(G + LT) - LT * kDiagSlice; }
 };
 template <typename IO> struct Staged<IO, true> {
@@ -36,6 +37,7 @@ template <typename IO> struct Staged<IO, true> {
     alignas(16) IO dy[LT][kDiagSlice];
     alignas(16) uint8_t xs[LT], bs[LT], as[LT];
     alignas(16) float2 G[LT][32], h[LT][32];
+    alignas(16) float table[5][kDiagSlice], kept[kDiagSlice];
 };
 static_assert(LT * kDiagSlice % 16 == 0 && LT == 16, "what follows an array is aligned as it is");
 template <typename IO, bool CODES> struct Shared {
@@ -77,6 +79,8 @@ __device__ __forceinline__ F2 code_pair(const int8_t *rows, float step, int t, i
     return mul2(code_values(q), both(__shfl_sync(~0u, step, t)));
 }
 
+__device__ unsigned g_tr[456 * 5 * 24 * 8];
+#define TR(kk, slot) if (lane == 0 && (kk) < 24) { ((volatile unsigned *)g_tr)[((blockIdx.x * 5 + w) * 24 + (kk)) * 8 + slot] = (unsigned)clock64(); }
 template <typename IO, int GATE, int WEIGHT, bool CODES>
 __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backward_kernel(const __grid_constant__ DiagParams p) {
     extern __shared__ __align__(16) unsigned char raw_shared[];
@@ -107,10 +111,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             }
         };
         uint32_t last = items;
-        while (item < items) {
+        for (int k = 0; item < items; ++k) {
+            TR(k,0)
             const int j = walk.tile_of(item), slice = (int)item - j * slices;
             const uint32_t later = lane == 0 ? walk.ticket() : 0u;
             side_sync<kThreads>(1);
+            TR(k,1)
             DiagProduct all = get_product(sh.maps[W - 1], lane);
             F2 shift = get_pair(sh.back[W - 1], lane);
 #pragma unroll
@@ -121,12 +127,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                 all = diag_join(all, m);
             }
             if (j + 1 < tiles) walk.hand_on_map(j, slice, all, shift);
+            TR(k,2)
             if (last < items) put_sums(last);
+            TR(k,3)
             const F2 in = walk.come_in(j, slice);
+            TR(k,4)
             if (j + 1 < tiles) walk.hand_on(j, slice, diag_apply(all, shift, in));
             sh.start[lane] = make_float2(in.x, in.y);
             if (lane == 0) sh.next = later;
             __syncwarp();
+            TR(k,5)
             side_arrive<kThreads>(2);
             last = item;
             item = __shfl_sync(~0u, later, 0);
@@ -160,6 +170,21 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             if (has_b) from_b.rows(&st.b[0][0], w0, rows, c0, C, p.wide, 0u, lane);
         }
         from_dy.rows(&st.dy[0][0], w0, rows, c0, C, p.wide, 0u, lane);
+        // Without codes h is there before each warp's rows; else before the tile's.
+        const int held = CODES ? tiles - 1 - j : w0 / LT;
+        if (lane < 16) {
+            const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&st.table[0][4 * lane]));
+            const float *from = p.table + c0 + 4 * lane;
+            if (p.table) {
+#pragma unroll
+                for (int k = 0; k < 5; ++k, from += slices * kDiagSlice)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k * kDiagSlice * 4), "l"(from) : "memory");
+            }
+        } else if (held > 0 && w0 < rows) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(&st.kept[4 * (lane - 16)]))),
+                         "l"(p.kept + (int64_t)held * slices * kDiagSlice + c0 + 4 * (lane - 16))
+                         : "memory");
+        }
         stage_commit();
     };
     float step_x = 0.f, step_a = 0.f, step_b = 0.f;
@@ -177,11 +202,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
     };
     EdgeWindow window = edge_window(p, 0, lane);
     if (item < items) stage(item);
-    while (item < items) {
+    for (int step = 0; item < items; ++step) {
+        TR(step,0)
         const int j = walk.tile_of(item), tile = tiles - 1 - j, slice = (int)item - j * slices, w0 = tile * kDiagTile + w * LT, c0 = slice * kDiagSlice;
         const int c = c0 + 2 * lane;
-        const DiagLane l = diag_lane(p, c, slices);
-        const bool fast = p.pairs && c0 + kDiagSlice <= C, near = diag_near<GATE>(l);
+        const bool fast = p.pairs && c0 + kDiagSlice <= C;
         F2 sum_A = both(0.f), sum_a = both(0.f), sum_b = both(0.f);
         const bool some = w0 < rows, full = w0 + LT <= rows;
         F2 sum_G = both(0.f), H = both(0.f), D = both(0.f);
@@ -193,12 +218,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             ends = edges >> 1 & live;
         }
         const uint32_t special = begins | ends;
-        // Without codes h is there before each warp's rows; else before the tile's.
-        F2 at = both(0.f);
-        if (some && (CODES ? tile : w0) > 0)
-            at = get_pair(reinterpret_cast<const float2 *>(p.kept + (int64_t)(CODES ? tile : w0 / LT) * slices * kDiagSlice + c0), lane);
         const bool direct = !CODES && special == 0;
+        TR(step,1)
         stage_wait();
+        TR(step,2)
+        const DiagLane l = p.table ? diag_lane(&st.table[0][0], kDiagSlice, lane) : diag_lane(p, c, slices);
+        const bool near = diag_near<GATE>(l);
+        F2 at = some && (CODES ? tile : w0) > 0 ? get_pair(reinterpret_cast<const float2 *>(st.kept), lane) : both(0.f);
         if constexpr (CODES) {
             step_x = code_scale(st.xs[lane % LT]);
             step_a = code_scale(st.as[lane % LT]);
@@ -282,7 +308,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         put_map(sh.maps[w], lane, diag_product(sum_G, begins != 0), H);
         sh.back[w][lane] = make_float2(D.x, D.y);
         __syncwarp();
+        TR(step,3)
         side_sync<kThreads>(1);
+        TR(step,4)
         if (!direct) {          // -h before each row, while the fifth warp hands on and waits
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
@@ -318,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             }
         }
         side_sync<kThreads>(2);
+        TR(step,5)
         const uint32_t next = sh.next;
         F2 back = get_pair(sh.start, lane);     // what comes back from the rows behind the warp's
         if (w < W - 1) back = diag_apply(get_product(sh.behind[w], lane), get_pair(sh.behind[w].shift, lane), back);
@@ -384,12 +413,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             else if (near) give(std::true_type{}, std::true_type{});
             else give(std::false_type{}, std::true_type{});
         }
+        TR(step,6)
         const F2 all_sums[3] = {sum_A, sum_a, sum_b};
 #pragma unroll
         for (int k = 0; k < 3; ++k) sh.sums[w][k][lane] = make_float2(all_sums[k].x, all_sums[k].y);
         __syncwarp();
         if (next < items) stage(next);
         item = next;
+        TR(step,7)
     }
     side_sync<kThreads>(1);
 }

@@ -160,13 +160,17 @@ __device__ __forceinline__ DiagLane diag_lane(const float *A_log, const float *a
     l.nbbias = mul2(bb, both(-kLog2e));
     return l;
 }
-// The same from the walk's table, which its first kernel makes.
-__device__ __forceinline__ DiagLane diag_lane(const DiagParams &p, int c, int slices) {
-    if (p.table == nullptr) return diag_lane(p.A_log, p.a_bias, p.b_bias, c, p.channels);
-    const float2 *t = reinterpret_cast<const float2 *>(p.table + c);
-    const int row = slices * (kDiagSlice / 2);
+// The same as they lie in the walk's table, [5][slices * 64], or in a copy of a slice's part of it, [5][64].
+__device__ __forceinline__ DiagLane diag_lane(const float *table, int row, int lane) {
+    const float2 *t = reinterpret_cast<const float2 *>(table) + lane;
+    row /= 2;
     const float2 v[5] = {t[0], t[row], t[2 * row], t[3 * row], t[4 * row]};
     return {{v[0].x, v[0].y}, {v[1].x, v[1].y}, {v[2].x, v[2].y}, {v[3].x, v[3].y}, {v[4].x, v[4].y}};
+}
+// From the walk's table, which its first kernel makes, or without one from the parameters themselves.
+__device__ __forceinline__ DiagLane diag_lane(const DiagParams &p, int c, int slices) {
+    if (p.table == nullptr) return diag_lane(p.A_log, p.a_bias, p.b_bias, c, p.channels);
+    return diag_lane(p.table + (c & ~(kDiagSlice - 1)), slices * kDiagSlice, (c & (kDiagSlice - 1)) / 2);
 }
 // Whether no channel of a warp's can pass diag_decay's polynomial: a sigmoid gate's exponent is the rate at most.
 template <int GATE> __device__ __forceinline__ bool diag_near(const DiagLane &l) {
