@@ -79,8 +79,6 @@ __device__ __forceinline__ F2 code_pair(const int8_t *rows, float step, int t, i
     return mul2(code_values(q), both(__shfl_sync(~0u, step, t)));
 }
 
-__device__ unsigned g_tr[456 * 5 * 24 * 8];
-#define TR(kk, slot) if (lane == 0 && (kk) < 24) { ((volatile unsigned *)g_tr)[((blockIdx.x * 5 + w) * 24 + (kk)) * 8 + slot] = (unsigned)clock64(); }
 template <typename IO, int GATE, int WEIGHT, bool CODES>
 __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backward_kernel(const __grid_constant__ DiagParams p) {
     extern __shared__ __align__(16) unsigned char raw_shared[];
@@ -111,12 +109,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             }
         };
         uint32_t last = items;
-        for (int k = 0; item < items; ++k) {
-            TR(k,0)
+        while (item < items) {
             const int j = walk.tile_of(item), slice = (int)item - j * slices;
             const uint32_t later = lane == 0 ? walk.ticket() : 0u;
             side_sync<kThreads>(1);
-            TR(k,1)
             DiagProduct all = get_product(sh.maps[W - 1], lane);
             F2 shift = get_pair(sh.back[W - 1], lane);
 #pragma unroll
@@ -127,16 +123,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                 all = diag_join(all, m);
             }
             if (j + 1 < tiles) walk.hand_on_map(j, slice, all, shift);
-            TR(k,2)
             if (last < items) put_sums(last);
-            TR(k,3)
             const F2 in = walk.come_in(j, slice);
-            TR(k,4)
             if (j + 1 < tiles) walk.hand_on(j, slice, diag_apply(all, shift, in));
             sh.start[lane] = make_float2(in.x, in.y);
             if (lane == 0) sh.next = later;
             __syncwarp();
-            TR(k,5)
             side_arrive<kThreads>(2);
             last = item;
             item = __shfl_sync(~0u, later, 0);
@@ -202,8 +194,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
     };
     EdgeWindow window = edge_window(p, 0, lane);
     if (item < items) stage(item);
-    for (int step = 0; item < items; ++step) {
-        TR(step,0)
+    while (item < items) {
         const int j = walk.tile_of(item), tile = tiles - 1 - j, slice = (int)item - j * slices, w0 = tile * kDiagTile + w * LT, c0 = slice * kDiagSlice;
         const int c = c0 + 2 * lane;
         const bool fast = p.pairs && c0 + kDiagSlice <= C;
@@ -219,9 +210,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         }
         const uint32_t special = begins | ends;
         const bool direct = !CODES && special == 0;
-        TR(step,1)
         stage_wait();
-        TR(step,2)
         const DiagLane l = p.table ? diag_lane(&st.table[0][0], kDiagSlice, lane) : diag_lane(p, c, slices);
         const bool near = diag_near<GATE>(l);
         F2 at = some && (CODES ? tile : w0) > 0 ? get_pair(reinterpret_cast<const float2 *>(st.kept), lane) : both(0.f);
@@ -308,9 +297,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         put_map(sh.maps[w], lane, diag_product(sum_G, begins != 0), H);
         sh.back[w][lane] = make_float2(D.x, D.y);
         __syncwarp();
-        TR(step,3)
         side_sync<kThreads>(1);
-        TR(step,4)
         if (!direct) {          // -h before each row, while the fifth warp hands on and waits
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
@@ -346,7 +333,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             }
         }
         side_sync<kThreads>(2);
-        TR(step,5)
         const uint32_t next = sh.next;
         F2 back = get_pair(sh.start, lane);     // what comes back from the rows behind the warp's
         if (w < W - 1) back = diag_apply(get_product(sh.behind[w], lane), get_pair(sh.behind[w].shift, lane), back);
@@ -413,14 +399,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             else if (near) give(std::true_type{}, std::true_type{});
             else give(std::false_type{}, std::true_type{});
         }
-        TR(step,6)
         const F2 all_sums[3] = {sum_A, sum_a, sum_b};
 #pragma unroll
         for (int k = 0; k < 3; ++k) sh.sums[w][k][lane] = make_float2(all_sums[k].x, all_sums[k].y);
         __syncwarp();
         if (next < items) stage(next);
         item = next;
-        TR(step,7)
     }
     side_sync<kThreads>(1);
 }

@@ -4,5 +4,3 @@
 namespace gdn {
 template cudaError_t diag_backward_by_kind<__nv_bfloat16>(const DiagParams &p, int gate, int weighting, cudaStream_t s);
 }  // namespace gdn
-
-extern "C" void *diag_trace() { void *q = nullptr; cudaGetSymbolAddress(&q, gdn::g_tr); return q; }
