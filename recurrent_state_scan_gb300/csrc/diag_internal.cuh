@@ -64,6 +64,22 @@ int64_t diag_tiles(int64_t rows);
 // Bytes of a walk's workspace (0: one tile a slice, nothing to hand on).
 size_t diag_walk_bytes(int64_t rows, int channels);
 void diag_walk_layout(DiagParams &p, void *workspace);
+// Launches a walk's kernel behind its first one, as a dependent of it: its CTAs start while that one still runs (in which
+// DiagWalk::begin waits for it).
+template <typename Kernel>
+cudaError_t diag_launch(Kernel kernel, unsigned grid, int threads, size_t shared, const DiagParams &p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = p.table ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 // The walk's first kernel: clears the counter and the words and makes the table.
 cudaError_t diag_begin(const DiagParams &p, cudaStream_t stream);
 // CTAs of a walk: one for each item, up to `per_sm` on each of 152 SMs (a single row of tiles: always one for each).
@@ -486,6 +502,7 @@ struct DiagWalk {
     // The next item: only CTAs that run hold any.  (A single row of tiles has nothing to wait for: an item for each CTA.)
     __device__ __forceinline__ uint32_t ticket() const { return tiles > 1 ? atomicAdd(p.ticket, 1u) : items(); }
     __device__ __forceinline__ uint32_t first(uint32_t &shared) const {
+        asm volatile("griddepcontrol.wait;" ::: "memory");      // for the walk's first kernel
         if (threadIdx.x == 0) shared = tiles > 1 ? atomicAdd(p.ticket, 1u) : blockIdx.x;
         __syncthreads();
         const uint32_t item = shared;

@@ -20,6 +20,7 @@ WalkLayout walk_layout(int64_t rows, int channels) {
 }
 
 __global__ void __launch_bounds__(256) diag_begin_kernel(const __grid_constant__ DiagParams p, uint32_t items) {
+    asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t i = blockIdx.x * 256 + threadIdx.x, all = gridDim.x * 256;
     if (i == 0) *p.ticket = 0u;
     static_assert(kNone == ~0ull, "all bits set");

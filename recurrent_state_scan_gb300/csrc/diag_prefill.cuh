@@ -216,8 +216,7 @@ template <typename IO, int GATE, int WEIGHT> cudaError_t launch(const DiagParams
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared<IO>));
     if (e == cudaSuccess) e = diag_begin(p, stream);
     if (e != cudaSuccess) return e;
-    kernel<<<diag_grid(p, sizeof(IO) == 4 ? 2 : 3), kThreads, sizeof(Shared<IO>), stream>>>(p);
-    return cudaGetLastError();
+    return diag_launch(kernel, diag_grid(p, sizeof(IO) == 4 ? 2 : 3), kThreads, sizeof(Shared<IO>), p, stream);
 }
 
 }  // namespace

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -1086,11 +1087,25 @@ def gdn_ssm_decode(xbc, dt, A_log, state, *, heads: int, head_dim: int, d_state:
 
 
 # ------------------------------------------------------------------ the diagonal recurrence
-def _diag_kinds(gate, weighting, keep=None):
+# The device time of a small call is a few microseconds, so what a call's sizes say is worked out once for each set of them.
+@functools.lru_cache(maxsize=1024)
+def _diag_shape(io, B, T, n, C, gate, weighting, has_b, keep, *strides):
+    """(reference to the shape, bytes kept, workspace bytes of the forward and of the backward pass)."""
     if gate not in DIAG_GATES or weighting not in DIAG_WEIGHTINGS or keep not in DIAG_KEEPS:
         raise GdnError(GDN_ERR_INVALID_ARG, f"gate must be one of {sorted(DIAG_GATES)}, weighting of {sorted(DIAG_WEIGHTINGS)}, "
                                             "keep None, 'states' or '8bit'")
-    return DIAG_GATES[gate], DIAG_WEIGHTINGS[weighting], DIAG_KEEPS[keep]
+    lib = load()
+    ref = ctypes.byref(GdnDiagShape(_DTYPE_CODE[io], B, T, n, C, DIAG_GATES[gate], DIAG_WEIGHTINGS[weighting], has_b, DIAG_KEEPS[keep], *strides))
+    return ref, lib.gdn_diag_kept_bytes(ref), lib.gdn_diag_prefill_workspace_bytes(ref), lib.gdn_diag_backward_workspace_bytes(ref)
+
+
+def _row3(name: str, t, rows, dtype, device: int):
+    """_rows for t [B, T, C]; what lies as it mostly does is seen at once."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == rows and t.get_device() == device:
+        (B, T, C), (s0, s1, s2) = rows, t.stride()
+        if s2 == 1 and (s1 >= C and s0 == T * s1 if T > 1 else s0 >= C):
+            return t.data_ptr(), s1 if T > 1 else s0
+    return _rows(name, t, rows[0], rows[1], (rows[2],), dtype, device)
 
 
 def _diag_params(A_log, a_bias, b_bias, C: int, input_gate: bool, dev: int):
@@ -1098,7 +1113,17 @@ def _diag_params(A_log, a_bias, b_bias, C: int, input_gate: bool, dev: int):
         raise GdnError(GDN_ERR_INVALID_ARG, "b_bias belongs to an input gate: b is needed")
     if A_log is None:
         raise GdnError(GDN_ERR_INVALID_ARG, "A_log is needed")
-    return tuple(_arg(name, t, (C,), torch.float32, dev) for name, t in (("A_log", A_log), ("a_bias", a_bias), ("b_bias", b_bias)))
+    per, f32 = (C,), torch.float32
+    return _arg("A_log", A_log, per, f32, dev), _arg("a_bias", a_bias, per, f32, dev), _arg("b_bias", b_bias, per, f32, dev)
+
+
+def _workspace(workspace, need: int, device, dev: int):
+    """(the workspace, its address, its bytes), made where it is needed and not given."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, _arg("workspace", workspace, None, workspace.dtype, dev), workspace.numel() * workspace.element_size()
 
 
 def gdn_diag_kept_bytes(shape: GdnDiagShape) -> int:
@@ -1126,14 +1151,14 @@ def gdn_diag_prefill(x, a, b, A_log, *, a_bias=None, b_bias=None, gate: str = "s
     GdnDiagKept or None)."""
     lib = _lib or load()
     dev = _first("x", x, 3)
-    kinds = _diag_kinds(gate, weighting, keep)
-    io, (B, T, C) = x.dtype, x.shape
+    io, rows, has_b, f32 = x.dtype, x.shape, b is not None, torch.float32
+    B, T, C = rows
     n = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    f32, states, rows = torch.float32, (max(n, 0), C), (B, T, C)
-    px, ldx = _rows("x", x, B, T, (C,), io, dev)
-    pa, lda = _rows("a", a, B, T, (C,), io, dev)
-    pb, ldb = (None, 0) if b is None else _rows("b", b, B, T, (C,), io, dev)
-    pA, pab, pbb = _diag_params(A_log, a_bias, b_bias, C, b is not None, dev)
+    states = (max(n, 0), C)
+    px, ldx = _row3("x", x, rows, io, dev)
+    pa, lda = _row3("a", a, rows, io, dev)
+    pb, ldb = _row3("b", b, rows, io, dev) if has_b else (None, 0)
+    pA, pab, pbb = _diag_params(A_log, a_bias, b_bias, C, has_b, dev)
     pcu = _arg("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, dev)
     psi = _arg("state_in", state_in, states, f32, dev)
     with _on(dev, stream):
@@ -1141,20 +1166,15 @@ def gdn_diag_prefill(x, a, b, A_log, *, a_bias=None, b_bias=None, gate: str = "s
             y = torch.empty(rows, dtype=io, device=x.device)
         if state_out is None:
             state_out = torch.empty(states, dtype=f32, device=x.device)
-        py, ldy = _rows("y", y, B, T, (C,), io, dev)
-        shape = GdnDiagShape(_DTYPE_CODE[io], B, T, n, C, kinds[0], kinds[1], b is not None, kinds[2], ldx, lda, ldb, ldy, 0, 0, 0)
-        ref = ctypes.byref(shape)
+        py, ldy = _row3("y", y, rows, io, dev)
+        ref, bytes_, need, _ = _diag_shape(io, B, T, n, C, gate, weighting, has_b, keep, ldx, lda, ldb, ldy)
         if keep is not None and kept is None:
-            kept = torch.empty(lib.gdn_diag_kept_bytes(ref), dtype=torch.uint8, device=x.device)
-        need = lib.gdn_diag_prefill_workspace_bytes(ref)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+            kept = torch.empty(bytes_, dtype=torch.uint8, device=x.device)
+        workspace, pw, ws_bytes = _workspace(workspace, need, x.device, dev)
         _check(lib.gdn_diag_prefill(ref, px, pa, pb, pA, pab, pbb, psi, pcu, py, _arg("state_out", state_out, states, f32, dev),
-                                    _arg("kept", kept, None, torch.uint8, dev), 0 if kept is None else kept.numel(),
-                                    None if workspace is None else _arg("workspace", workspace, None, workspace.dtype, dev), ws_bytes,
+                                    _arg("kept", kept, None, torch.uint8, dev), 0 if kept is None else kept.numel(), pw, ws_bytes,
                                     _raw_stream(dev)))
-    return y, state_out, None if keep is None else GdnDiagKept(kept, io, B, T, n, C, gate, weighting, b is not None, keep)
+    return y, state_out, None if keep is None else GdnDiagKept(kept, io, B, T, n, C, gate, weighting, has_b, keep)
 
 
 def gdn_diag_backward(dy, kept: GdnDiagKept, A_log, *, x=None, a=None, b=None, a_bias=None, b_bias=None, state_in=None,
@@ -1169,38 +1189,35 @@ def gdn_diag_backward(dy, kept: GdnDiagKept, A_log, *, x=None, a=None, b=None, a
     if not isinstance(kept, GdnDiagKept):
         raise GdnError(GDN_ERR_INVALID_ARG, "kept must be what gdn_diag_prefill kept")
     dev = _first("dy", dy, 3)
-    io, B, T, n, C, has_b = kept.io, kept.batch, kept.seqlen, kept.num_seqs, kept.channels, kept.input_gate
-    kinds = _diag_kinds(kept.gate, kept.weighting, kept.keep)
+    data, io, B, T, n, C, gate, weighting, has_b, keep = kept
     f32, states, rows = torch.float32, (max(n, 0), C), (B, T, C)
-    pdy, lddy = _rows("dy", dy, B, T, (C,), io, dev)
+    pdy, lddy = _row3("dy", dy, rows, io, dev)
     pA, pab, pbb = _diag_params(A_log, a_bias, b_bias, C, has_b, dev)
     pcu = _arg("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, dev)
     if cu_seqlens is None and n != B:
         raise GdnError(GDN_ERR_INVALID_ARG, "cu_seqlens is needed: the forward call was packed")
     psi, pdo = _arg("state_in", state_in, states, f32, dev), _arg("dstate_out", dstate_out, states, f32, dev)
-    pk = _arg("kept", kept.data, None, torch.uint8, dev)
-    ins, lds = [None] * 3, [0] * 3
-    if kept.keep == "states":
-        for i, (name, t) in enumerate((("x", x), ("a", a), ("b", b))):
-            if name != "b" or has_b:
-                ins[i], lds[i] = _rows(name, t, B, T, (C,), io, dev)
+    pk = _arg("kept", data, None, torch.uint8, dev)
+    px = pa = pb = None
+    ldx = lda = ldb = 0
+    if keep == "states":
+        px, ldx = _row3("x", x, rows, io, dev)
+        pa, lda = _row3("a", a, rows, io, dev)
+        if has_b:
+            pb, ldb = _row3("b", b, rows, io, dev)
     with _on(dev, stream):
         new = lambda shape, dtype=f32: torch.empty(shape, dtype=dtype, device=dy.device)  # noqa: E731
         dx, da = new(rows, io) if dx is None else dx, new(rows, io) if da is None else da
         db = None if not has_b else new(rows, io) if db is None else db
-        outs = [_rows("dx", dx, B, T, (C,), io, dev), _rows("da", da, B, T, (C,), io, dev),
-                _rows("db", db, B, T, (C,), io, dev) if has_b else (None, 0)]
+        pdx, lddx = _row3("dx", dx, rows, io, dev)
+        pda, ldda = _row3("da", da, rows, io, dev)
+        pdb, lddb = _row3("db", db, rows, io, dev) if has_b else (None, 0)
         dA_log, da_bias, db_bias = new((C,)), None if a_bias is None else new((C,)), None if b_bias is None else new((C,))
         dstate_in = None if state_in is None else new(states)
-        shape = GdnDiagShape(_DTYPE_CODE[io], B, T, n, C, kinds[0], kinds[1], has_b, kinds[2], *lds, lddy, *(ld for _, ld in outs))
-        ref = ctypes.byref(shape)
-        need = lib.gdn_diag_backward_workspace_bytes(ref)
-        if workspace is None and need > 0:
-            workspace = new(need, torch.uint8)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib.gdn_diag_backward(ref, *ins, pA, pab, pbb, psi, pcu, pk, kept.data.numel(), pdy, pdo, *(p for p, _ in outs),
-                                     *(None if t is None else t.data_ptr() for t in (dA_log, da_bias, db_bias, dstate_in)),
-                                     None if workspace is None else _arg("workspace", workspace, None, workspace.dtype, dev),
+        ref, _, _, need = _diag_shape(io, B, T, n, C, gate, weighting, has_b, keep, ldx, lda, ldb, lddy, lddx, ldda, lddb)
+        workspace, pw, ws_bytes = _workspace(workspace, need, dy.device, dev)
+        _check(lib.gdn_diag_backward(ref, px, pa, pb, pA, pab, pbb, psi, pcu, pk, data.numel(), pdy, pdo, pdx, pda, pdb,
+                                     *(None if t is None else t.data_ptr() for t in (dA_log, da_bias, db_bias, dstate_in)), pw,
                                      ws_bytes, _raw_stream(dev)))
     return dx, da, db, dA_log, da_bias, db_bias, dstate_in
 
@@ -1212,22 +1229,22 @@ def gdn_diag_decode(x, a, b, A_log, state, *, a_bias=None, b_bias=None, gate: st
     [B, 1, C]."""
     lib = _lib or load()
     dev = _first("x", x, 3)
-    kinds = _diag_kinds(gate, weighting)
-    io, (B, T, C) = x.dtype, x.shape
+    io, rows, has_b = x.dtype, x.shape, b is not None
+    B, T, C = rows
     if not isinstance(state, torch.Tensor) or state.dim() != 2:
         raise GdnError(GDN_ERR_INVALID_ARG, f"state must be [E, {C}]")
     E = B if slots is None else state.shape[0]
-    px, ldx = _rows("x", x, B, T, (C,), io, dev)
-    pa, lda = _rows("a", a, B, T, (C,), io, dev)
-    pb, ldb = (None, 0) if b is None else _rows("b", b, B, T, (C,), io, dev)
-    pA, pab, pbb = _diag_params(A_log, a_bias, b_bias, C, b is not None, dev)
+    px, ldx = _row3("x", x, rows, io, dev)
+    pa, lda = _row3("a", a, rows, io, dev)
+    pb, ldb = _row3("b", b, rows, io, dev) if has_b else (None, 0)
+    pA, pab, pbb = _diag_params(A_log, a_bias, b_bias, C, has_b, dev)
     ps, pslots = _arg("state", state, (E, C), torch.float32, dev), _arg("slots", slots, (B,), torch.int32, dev)
     with _on(dev, stream):
         if y is None:
-            y = torch.empty((B, T, C), dtype=io, device=x.device)
-        py, ldy = _rows("y", y, B, T, (C,), io, dev)
-        shape = GdnDiagShape(_DTYPE_CODE[io], B, T, B, C, kinds[0], kinds[1], b is not None, 0, ldx, lda, ldb, ldy, 0, 0, 0)
-        _check(lib.gdn_diag_decode(ctypes.byref(shape), px, pa, pb, pA, pab, pbb, ps, E, pslots, py, _raw_stream(dev)))
+            y = torch.empty(rows, dtype=io, device=x.device)
+        py, ldy = _row3("y", y, rows, io, dev)
+        ref = _diag_shape(io, B, T, B, C, gate, weighting, has_b, None, ldx, lda, ldb, ldy)[0]
+        _check(lib.gdn_diag_decode(ref, px, pa, pb, pA, pab, pbb, ps, E, pslots, py, _raw_stream(dev)))
     return y
 
 
@@ -1238,7 +1255,7 @@ def gdn_checkpoint_pack(x, *, codes=None, steps=None, stream=None):
     lib = _lib or load()
     dev = _first("x", x, 3)
     B, T, C = x.shape
-    px, ldx = _rows("x", x, B, T, (C,), x.dtype, dev)
+    px, ldx = _row3("x", x, x.shape, x.dtype, dev)
     blocks = (B, T, -(-C // CHECKPOINT_BLOCK))
     with _on(dev, stream):
         if codes is None:
@@ -1262,7 +1279,7 @@ def gdn_checkpoint_unpack(codes, steps, dtype=torch.bfloat16, *, y=None, stream=
     with _on(dev, stream):
         if y is None:
             y = torch.empty((B, T, C), dtype=dtype, device=codes.device)
-        py, ldy = _rows("y", y, B, T, (C,), dtype, dev)
+        py, ldy = _row3("y", y, codes.shape, dtype, dev)
         _check(lib.gdn_checkpoint_unpack(_DTYPE_CODE[dtype], B * T, C, pc, ps, py, ldy, _raw_stream(dev)))
     return y
 
