@@ -530,7 +530,7 @@ struct DiagWalk {
     // What comes in to the j-th tile of a slice, by one warp.  A wait that runs out is reported, and takes 0.
     __device__ __forceinline__ F2 come_in(int j, int slice) const {
         if (j == 0) return both(0.f);
-        constexpr int D = 6;                                // tiles back
+        constexpr int D = 4;                                // tiles back (3 to 12 tried: the traffic of more costs what they find)
         const unsigned long long *from = at(j, slice);
         unsigned long long hi[D], lo[D], H[D], after[D];
         int maps;
