@@ -354,6 +354,47 @@ __device__ __forceinline__ uint32_t magnitude(F2 v) {
     return a > b ? a : b;
 }
 
+// 16 staged rows of 64 channels in 16 bits as codes [16][64] and steps [16], the first `live` of them, by one warp: half a row to
+// a lane, 16 bytes at a time (its pieces in an order that starts at the row, so that eight lanes meet all banks).
+template <typename IO> __device__ __forceinline__ void code_rows(const IO *rows, int8_t *codes, uint8_t *steps, int live, int lane) {
+    const int r = lane / 2, half = lane % 2;
+    const uint4 *from = reinterpret_cast<const uint4 *>(rows) + r * 8 + half * 4;
+    uint4 q[4];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        q[i] = from[(i + r) % 4];
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(q[i].x & 0x7fff7fffu, q[i].y & 0x7fff7fffu), __vmaxu2(q[i].z & 0x7fff7fffu, q[i].w & 0x7fff7fffu)));
+    }
+    m = __vmaxu2(m, __shfl_xor_sync(~0u, m, 1));
+    m = max(m & 0xffffu, m >> 16);
+    const uint32_t e = code_step(IoBits<IO>::kHalf ? __float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) : m << 16);
+    const float inverse = code_inverse(e);
+    const bool top = __any_sync(~0u, e == 254u);
+    uint2 c[4];
+    auto two = [&](uint32_t a) {
+        const F2 v = Pair<IO>::wide(a);
+        return top ? codes_of(v, e) : code_bytes(v, inverse);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        c[i] = make_uint2(__byte_perm(two(q[i].x), two(q[i].y), 0x5410), __byte_perm(two(q[i].z), two(q[i].w), 0x5410));
+    // Back in order: piece i is at (i + r) % 4.
+    if (r & 1) {
+        const uint2 t = c[3];
+        c[3] = c[2], c[2] = c[1], c[1] = c[0], c[0] = t;
+    }
+    if (r & 2) {
+        const uint2 t = c[0], u = c[1];
+        c[0] = c[2], c[1] = c[3], c[2] = t, c[3] = u;
+    }
+    if (r >= live) return;
+    uint4 *to = reinterpret_cast<uint4 *>(codes) + r * 4 + half * 2;
+    to[0] = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
+    to[1] = make_uint4(c[2].x, c[2].y, c[3].x, c[3].y);
+    if (half == 0) steps[r] = (uint8_t)e;
+}
+
 // ------------------------------------------------------------------ the sequences among the rows
 // Row where sequence n begins (n = num_seqs: the end of the rows).
 __device__ __forceinline__ uint32_t seq_begin(const DiagParams &p, int n) {

@@ -115,26 +115,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_prefil
                 for (int q = 0; q < (has_b ? 3 : 2); ++q) {
                     const IO *from = sx + q * LT * kDiagSlice;
                     const int64_t at = ((int64_t)q * slices + slice) * all + w0;
-                    uint32_t most = 0;                  // of row `lane`
-#pragma unroll
-                    for (int t = 0; t < LT; ++t) {
-                        const uint32_t m = __reduce_max_sync(~0u, magnitude(staged(from, t, lane)));
-                        most = lane == t ? m : most;
-                    }
-                    const uint32_t e = code_step(most);
-                    const float inverse = code_inverse(e);
-                    int8_t *to = p.codes + at * kDiagSlice + 2 * lane;
-                    if (full && !__any_sync(~0u, e == 254u)) {
-#pragma unroll
-                        for (int t = 0; t < LT; ++t)
-                            *reinterpret_cast<uint16_t *>(to + t * kDiagSlice) =
-                                (uint16_t)code_bytes(staged(from, t, lane), __shfl_sync(~0u, inverse, t));
+                    if constexpr (sizeof(IO) == 2) {
+                        code_rows<IO>(from, p.codes + at * kDiagSlice, p.steps + at, rows - w0, lane);
                     } else {
-#pragma unroll 1
-                        for (int t = 0; t < LT && w0 + t < rows; ++t)
-                            *reinterpret_cast<uint16_t *>(to + t * kDiagSlice) = (uint16_t)codes_of(staged(from, t, lane), __shfl_sync(~0u, e, t));
+#pragma unroll 4
+                        for (int t = 0; t < LT; ++t) {
+                            const F2 v = staged(from, t, lane);
+                            const uint32_t e = code_step(__reduce_max_sync(~0u, magnitude(v)));
+                            if (w0 + t >= rows) break;
+                            *reinterpret_cast<uint16_t *>(p.codes + (at + t) * kDiagSlice + 2 * lane) = (uint16_t)codes_of(v, e);
+                            if (lane == 0) p.steps[at + t] = (uint8_t)e;
+                        }
                     }
-                    if (lane < LT && w0 + lane < rows) p.steps[at + lane] = (uint8_t)e;
                 }
             }
             auto take = [&](auto only_near) {
