@@ -616,7 +616,8 @@ typedef struct gdn_diag_shape {
  *                sets the device check word).  A sequence with no tokens keeps its state.
  *   kept         gdn_diag_kept_bytes(shape) bytes, 16-byte aligned (unread with KEEP_NONE).
  *   workspace    gdn_diag_prefill_workspace_bytes(shape) bytes (0 up to 64 rows), 16-byte
- *                aligned; its contents need no initialisation and are not preserved.
+ *                aligned; its contents need no initialisation and are not preserved.  Calls
+ *                that overlap on the GPU need one each.
  * An infinity or a NaN reaches the rest of its channel and sequence, no other.  Outputs may
  * not overlap inputs or one another (slices of one wider row, side by side, do not).
  */
@@ -756,8 +757,9 @@ gdn_status gdn_prefill_plan(const gdn_shape *shape, int32_t *path, int32_t *laun
  * gdn_set_wait_budget -- a test hook, process-wide and not part of the operation: the
  * cycles a bounded wait of the tensor-core prefill kernels (chunk prep and state scan)
  * or of the causal conv's bulk-copy pipeline (16-bit rows of 64 tokens or more) may take
- * before the waiting CTA gives up, for calls made after it (0 = the default, about two
- * seconds).  A wait that runs out makes the CTA let the copies and MMAs it has issued
+ * before the waiting CTA gives up, or the wait for an earlier tile of the diagonal
+ * recurrence (more than 64 rows) before it goes on without what it waited for, for calls
+ * made after it (0 = the default, about two seconds).  A wait that runs out makes the CTA let the copies and MMAs it has issued
  * finish under the full two-second budget, free its tensor memory and leave;
  * gdn_last_device_status() then returns GDN_ERR_TIMEOUT and the call's outputs are
  * undefined.  Nothing is left running or waiting on the device.

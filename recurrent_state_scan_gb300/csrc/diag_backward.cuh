@@ -9,7 +9,10 @@
 // h, to h's, both with the same product of decays; a fifth warp
 // hands G's on.  Of what the gates give, the decays' exponents G and h stay
 // in shared memory for the second pass over the rows; the rest is made again, in loops of four rows (all 16 in a row, their code
-// did not fit the instruction cache: 440 us for 16,384 rows of 4,096 where these take 267).
+// did not fit the instruction cache: 440 us for 16,384 rows of 4,096 where these take 258).
+//
+// Bound by instructions and by the multiply pipe: 71 a value (91 from codes), at half the issue slots.  8,192 bf16 rows of 4,096
+// channels take 131 us (3.6 TB/s; from codes 141), of which the bytes alone would take 69 (54).
 #pragma once
 
 #include <type_traits>

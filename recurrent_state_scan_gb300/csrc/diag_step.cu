@@ -5,7 +5,8 @@ namespace gdn {
 namespace {
 
 // One token per row: h = alpha h + w i x in place, y = h rounded.  Bound by the state's and the rows' bytes (16 a
-// channel in 16 bits); a thread takes four channels, and rows of a large batch in turn with one set of parameters.
+// channel in 16 bits) and, at the sizes of a batch of requests, by latency: 256 rows of 4,096 channels take 7.8 us on an idle GPU,
+// 2.5 by their bytes.  A thread takes four channels, and rows of a large batch in turn with one set of parameters.
 template <typename IO, int GATE, int WEIGHT, bool VEC>
 __global__ void __launch_bounds__(128) diag_decode_kernel(const __grid_constant__ DiagDecodeParams p) {
     constexpr int N = VEC ? 2 : 1;          // pairs of channels
@@ -98,7 +99,8 @@ template <typename IO> cudaError_t by_kind(const DiagDecodeParams &p, int gate, 
 
 // ------------------------------------------------------------------ 8-bit codes
 // By eight channels: 16 bytes of 16-bit rows (32 of fp32) to a lane, eight lanes to a block, R rows of four blocks to a warp, so
-// that R loads are on their way together; codes go out eight to a lane.
+// that R loads are on their way together; codes go out eight to a lane.  Bound by memory: 16,384 bf16 rows of 4,096 channels are
+// packed in 38 us and read back in 29 (a value to a thread: 118 and 102), 30 each by their bytes.
 constexpr int R = 4;
 template <typename IO> struct Eight {
     F2 v[4];
