@@ -274,6 +274,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                 if (near) take(std::true_type{}, std::true_type{});
                 else take(std::false_type{}, std::true_type{});
             }
+            if (!full) {            // rows outside are the identity, whatever the parameters make of them (an infinite bias: NaN)
+                sum_G = H = D = both(0.f);
+#pragma unroll 1
+                for (int t = 0; t < LT; ++t) {
+                    if (w0 + t < rows) sum_G = add2(sum_G, get_pair(sG + t * 32, lane));
+                    else sG[t * 32 + lane] = sh_[t * 32 + lane] = make_float2(0.f, 0.f);
+                }
+            }
             if (special) {
                 through = both(1.f);
                 D = both(0.f);

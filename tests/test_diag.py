@@ -417,6 +417,25 @@ def test_gates_far_out(gate, weighting):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("gate,weighting", KINDS)
+@pytest.mark.parametrize("keep", ["states", "8bit"])
+@pytest.mark.parametrize("lens", [[7], [20, 50], [64, 65]])
+def test_infinite_biases(gate, weighting, keep, lens):
+    """A gate that its bias holds open or shut, in rows that do not fill their tiles: the gradients are those of biases so far
+    out that in 64 bits nothing is left of the gate's other side (e^-800 is 0)."""
+    m = draw("f32", lens, 64, gate=gate, weighting=weighting, seed=25)
+    m["a_bias"], m["b_bias"] = m["a_bias"].clone(), m["b_bias"].clone()
+    m["A_log"][3] = 0.0
+    m["a_bias"][3], m["a_bias"][4], m["b_bias"][5], m["b_bias"][6] = math.inf, -math.inf, math.inf, -math.inf
+    y, state, kept = prefill(m, keep)
+    got = backward(m, kept)
+    assert all(torch.isfinite(t).all() for t in (y, state, *got))
+    far = dict(m, a_bias=m["a_bias"].clamp(-800, 800), b_bias=m["b_bias"].clamp(-800, 800))
+    check(far, (y, state))
+    check_gradients(far, got, keep == "8bit")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("gate", ["softplus", "sigmoid"])
 def test_fast_decays_keep_their_digits(gate):
     """Tokens that write nothing: h = h0 e^(sum g), every value on its own.  A token's g rounds (|z| + 8) 2^-23 of itself,
