@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Shared<IO, CODES> &sh = *reinterpret_cast<Shared<IO, CODES> *>(raw_shared);
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32, C = p.channels, slices = (C + kDiagSlice - 1) / kDiagSlice;
-    if (!offsets_ok(p)) return;
+    if (!offsets_ok(p)) return DiagWalk::wait_for_first();
     if (p.dstate_in)
         for (int n = blockIdx.x; n < p.num_seqs; n += gridDim.x) {      // sequences without tokens
             if (seq_begin(p, n) != seq_begin(p, n + 1)) continue;

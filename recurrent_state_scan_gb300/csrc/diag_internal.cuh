@@ -542,8 +542,11 @@ struct DiagWalk {
     __device__ __forceinline__ int tile_of(uint32_t item) const { return (int)((uint64_t)item * p.magic >> p.magic_shift); }
     // The next item: only CTAs that run hold any.  (A single row of tiles has nothing to wait for: an item for each CTA.)
     __device__ __forceinline__ uint32_t ticket() const { return tiles > 1 ? atomicAdd(p.ticket, 1u) : items(); }
+    // For the walk's first kernel to end; every thread, before it ends itself too: what comes behind the call waits for this kernel
+    // alone, and may have the workspace for its own.
+    static __device__ __forceinline__ void wait_for_first() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
     __device__ __forceinline__ uint32_t first(uint32_t &shared) const {
-        asm volatile("griddepcontrol.wait;" ::: "memory");      // for the walk's first kernel
+        wait_for_first();
         if (threadIdx.x == 0) shared = tiles > 1 ? atomicAdd(p.ticket, 1u) : blockIdx.x;
         __syncthreads();
         const uint32_t item = shared;

@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_prefil
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Shared<IO> &sh = *reinterpret_cast<Shared<IO> *>(raw_shared);
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32, C = p.channels, slices = (C + kDiagSlice - 1) / kDiagSlice;
-    if (!offsets_ok(p)) return;
+    if (!offsets_ok(p)) return DiagWalk::wait_for_first();
     for (int n = blockIdx.x; n < p.num_seqs; n += gridDim.x) {          // sequences without tokens keep their state
         if (seq_begin(p, n) != seq_begin(p, n + 1)) continue;
         for (int c = threadIdx.x; c < C; c += kThreads) p.state_out[(int64_t)n * C + c] = p.state_in ? p.state_in[(int64_t)n * C + c] : 0.f;
