@@ -219,9 +219,11 @@ gdn_status gdn_diag_prefill(const gdn_diag_shape *shape, const void *x, const vo
     const size_t need = walk_bytes(g);
     const Span outs[] = {sy, flat("state_out", state_out, sbytes), flat("kept", g.kept ? kept : nullptr, g.kept),
                          flat("workspace", need ? workspace : nullptr, need)};
-    const Span ins[] = {sx, sa, sb, si};
+    const size_t cbytes = (size_t)g.C * 4;
+    const Span ins[] = {sx, sa, sb, si, flat("A_log", A_log, cbytes), flat("a_bias", a_bias, cbytes),
+                        flat("b_bias", has_b ? b_bias : nullptr, cbytes), flat("cu_seqlens", cu_seqlens, ((size_t)g.n + 1) * 4)};
     st = check_workspace(workspace, workspace_bytes, need);
-    if (st == GDN_OK) st = none_overlap(outs, 4, ins, 4);
+    if (st == GDN_OK) st = none_overlap(outs, 4, ins, 8);
     if (st != GDN_OK) return st;
     DiagParams p = params(shape, g, kept);
     diag_walk_layout(p, workspace);
@@ -268,8 +270,9 @@ gdn_status gdn_diag_backward(const gdn_diag_shape *shape, const void *x, const v
                          flat("workspace", need ? workspace : nullptr, need)};
     const Span ins[] = {sx, sa, sb, sdy, flat("A_log", A_log, cbytes), flat("a_bias", a_bias, cbytes),
                         flat("b_bias", has_b ? b_bias : nullptr, cbytes), flat("state_in", state_in, sbytes),
-                        flat("dstate_out", dstate_out, sbytes), flat("kept", kept, g.kept)};
-    st = none_overlap(outs, 8, ins, 10);
+                        flat("dstate_out", dstate_out, sbytes), flat("kept", kept, g.kept),
+                        flat("cu_seqlens", cu_seqlens, ((size_t)g.n + 1) * 4)};
+    st = none_overlap(outs, 8, ins, 11);
     if (st != GDN_OK) return st;
     st = device_check_word(&p.status);
     if (st != GDN_OK) return st;
@@ -301,8 +304,11 @@ gdn_status gdn_diag_decode(const gdn_diag_shape *shape, const void *x, const voi
     if (slots != nullptr && pool_size <= 0) return fail(GDN_ERR_INVALID_ARG, "pool_size %lld <= 0", (long long)pool_size);
     const int64_t pool = slots ? pool_size : g.n;
     if (pool > INT64_MAX / 8 / g.C) return fail(GDN_ERR_INVALID_ARG, "pool_size %lld is beyond an address's range", (long long)pool);
-    const Span outs[] = {sy, flat("state", state, (size_t)pool * g.C * 4)}, ins[] = {sx, sa, sb};
-    st = none_overlap(outs, 2, ins, 3);
+    const size_t cbytes = (size_t)g.C * 4;
+    const Span outs[] = {sy, flat("state", state, (size_t)pool * g.C * 4)};
+    const Span ins[] = {sx, sa, sb, flat("A_log", A_log, cbytes), flat("a_bias", a_bias, cbytes),
+                        flat("b_bias", has_b ? b_bias : nullptr, cbytes), flat("slots", slots, (size_t)g.n * 4)};
+    st = none_overlap(outs, 2, ins, 7);
     if (st != GDN_OK) return st;
     DiagDecodeParams p{};
     st = device_check_word(&p.status);
@@ -322,8 +328,9 @@ gdn_status gdn_checkpoint_pack(int32_t io_dtype, int64_t rows, int64_t channels,
                                uint8_t *steps, void *stream) {
     Geometry g;
     gdn_status st = check_codes(io_dtype, rows, channels, x_stride, g);
+    if (st != GDN_OK) return st;
     const Span sx = io_rows("x", x, g, x_stride);
-    if (st == GDN_OK) st = check_io(g, {sx});
+    st = check_io(g, {sx});
     if (st != GDN_OK || g.rows == 0) return st;
     if (codes == nullptr || steps == nullptr) return fail(GDN_ERR_INVALID_ARG, "codes or steps is NULL");
     const Span outs[] = {flat("codes", codes, (size_t)(rows * channels)),
@@ -339,8 +346,9 @@ gdn_status gdn_checkpoint_unpack(int32_t io_dtype, int64_t rows, int64_t channel
                                  int64_t y_stride, void *stream) {
     Geometry g;
     gdn_status st = check_codes(io_dtype, rows, channels, y_stride, g);
+    if (st != GDN_OK) return st;
     const Span sy = io_rows("y", y, g, y_stride);
-    if (st == GDN_OK) st = check_io(g, {sy});
+    st = check_io(g, {sy});
     if (st != GDN_OK || g.rows == 0) return st;
     if (codes == nullptr || steps == nullptr) return fail(GDN_ERR_INVALID_ARG, "codes or steps is NULL");
     const Span ins[] = {flat("codes", codes, (size_t)(rows * channels)),

@@ -250,10 +250,19 @@ def test_refused_shapes(which, shape, status):
     ("backward", dict(dx=WHERE["x"])), ("backward", dict(da=WHERE["dx"] + 128)), ("backward", dict(db=WHERE["dy"])),
     ("backward", dict(dstate_in=WHERE["state_in"])), ("backward", dict(dstate_in=WHERE["dstate_out"])), ("backward", dict(dA_log=WHERE["A_log"])),
     ("backward", dict(dx=WHERE["kept"])), ("decode", dict(y=WHERE["x"])), ("decode", dict(y=WHERE["state"])), ("decode", dict(state=WHERE["b"])),
-    ("decode", dict(slots=0x3000, pool_size=0)), ("decode", dict(slots=0x3000, pool_size=-4))])
+    *[("prefill", {o: WHERE[k] + 16 * (o != "y")}) for o in ("y", "state_out", "kept") for k in ("A_log", "a_bias", "b_bias")],
+    *[("decode", {o: WHERE[k]}) for o in ("y", "state") for k in ("A_log", "a_bias", "b_bias")], ("decode", dict(slots=WHERE["y"])),
+    ("decode", dict(slots=WHERE["state"] + 512)), ("decode", dict(slots=0x3000, pool_size=0)), ("decode", dict(slots=0x3000, pool_size=-4))])
 def test_refused_pointers(which, where):
     assert call(which, None, **where) == gdn.GDN_ERR_INVALID_ARG
     assert gdn.load().gdn_last_error_message().decode()
+
+
+@pytest.mark.parametrize("which,out", [("prefill", "y"), ("prefill", "state_out"), ("backward", "dx"), ("backward", "dstate_in")])
+def test_refused_offsets(which, out):
+    packed = dict(batch=1, num_seqs=3, seqlen=16)
+    assert call(which, packed, cu=WHERE[out] + 16) == gdn.GDN_ERR_INVALID_ARG
+    assert "cu_seqlens" in gdn.load().gdn_last_error_message().decode()
 
 
 def test_refused_workspaces():
