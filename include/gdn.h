@@ -600,7 +600,7 @@ typedef struct gdn_diag_shape {
     int32_t gate;       /* gdn_diag_gate                                                   */
     int32_t weighting;  /* gdn_diag_weighting                                              */
     int32_t input_gate; /* 1: b is given; 0: i_t = 1, b, b_bias, db and db_bias unused     */
-    int32_t keep;       /* gdn_diag_keep (unread by gdn_diag_decode)                       */
+    int32_t keep;       /* gdn_diag_keep (of no effect in gdn_diag_decode)                 */
     /* Elements between token rows (0: contiguous), so that slices of wider rows can be
        given; below C they are refused.  Row b T + t holds token t of sequence b.  y_stride
        is dy's too; the last three are the backward pass's. */

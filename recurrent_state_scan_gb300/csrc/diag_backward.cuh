@@ -6,10 +6,9 @@
 //     da = dg g (1 - s) (sigmoid gate) | -dg e^A_log s (softplus gate),
 //     dA_log = sum dg g,  da_bias = sum da,  db_bias = sum db,  dstate_in = alpha G at a sequence's first row.
 // The walk is the forward pass's, from the last tile to the first: warps fold their rows to G's map and, from the kept
-// h, to h's, both with the same product of decays; a fifth warp
-// hands G's on.  Of what the gates give, the decays' exponents G and h stay
-// in shared memory for the second pass over the rows; the rest is made again, in loops of four rows (all 16 in a row, their code
-// did not fit the instruction cache: 440 us for 16,384 rows of 4,096 where these take 258).
+// h, to h's, both with the same product of decays; a fifth warp hands G's on.  Of what the gates give, the decays' exponents G and
+// h stay in shared memory for the second pass over the rows; the rest is made again, in loops of four rows (all 16 in a row, their
+// code did not fit the instruction cache: 440 us for 16,384 rows of 4,096 where these take 258).
 //
 // Bound by instructions and by the multiply pipe: 71 a value (91 from codes), at half the issue slots.  8,192 bf16 rows of 4,096
 // channels take 131 us (3.6 TB/s; from codes 141), of which the bytes alone would take 69 (54).

@@ -1,14 +1,14 @@
 // diag_internal.cuh -- what the diagonal recurrence's translation units share: its arguments, its gates,
-// the 8-bit codes, the sequences' edges among a warp's rows, and the exchange inside a cluster.
+// the 8-bit codes, the sequences' edges among a warp's rows, and the walk over the tiles.
 #pragma once
 
 #include "ssm_internal.cuh"
 
 namespace gdn {
 
-constexpr int kDiagTile = 64;    // token rows between two kept states, and of one CTA's step
-constexpr int kDiagRows = 16;    // of one warp
-constexpr int kDiagSlice = 64;   // channels of one CTA, and of a block of the 8-bit codes
+constexpr int kDiagTile = 64;    // token rows of an item of the walk, and with codes between two kept states
+constexpr int kDiagRows = 16;    // of one warp, and without codes between two kept states
+constexpr int kDiagSlice = 64;   // channels of an item, and of a block of the 8-bit codes
 
 // One call (validated arguments).  Token rows are those of the whole call: t of sequence b at
 // b * seqlen + t, or the packed index.  Row strides in elements.
@@ -64,8 +64,8 @@ int64_t diag_tiles(int64_t rows);
 // Bytes of a walk's workspace (0: one tile a slice, nothing to hand on).
 size_t diag_walk_bytes(int64_t rows, int channels);
 void diag_walk_layout(DiagParams &p, void *workspace);
-// Launches a walk's kernel behind its first one, as a dependent of it: its CTAs start while that one still runs (in which
-// DiagWalk::begin waits for it).
+// Launches a walk's kernel behind its first one, as a dependent of it: its CTAs start while that one still runs, and
+// DiagWalk::first waits for it.
 template <typename Kernel>
 cudaError_t diag_launch(Kernel kernel, unsigned grid, int threads, size_t shared, const DiagParams &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};

@@ -241,10 +241,9 @@ cudaError_t launch_diag_decode(const DiagDecodeParams &p, gdn_dtype io, int gate
 }
 
 // Whether rows are taken by eight channels: widths, strides and addresses have to allow it, and a grid's second extent the rows.
-bool code_wide(gdn_dtype io, int64_t rows, int64_t C, const void *x, int64_t ld, const void *codes) {
-    const size_t es = io == GDN_F32 ? 4 : 2;
+bool code_wide(int64_t rows, int64_t C, const void *x, int64_t ld, const void *codes) {
     return C % 8 == 0 && C <= INT32_MAX - 256 && ld % 8 == 0 && (uintptr_t)x % 16 == 0 && (uintptr_t)codes % 8 == 0 &&
-           (rows + 8 * R - 1) / (8 * R) <= 65535 && es * 8 % 16 == 0;
+           (rows + 8 * R - 1) / (8 * R) <= 65535;
 }
 dim3 code_grid(int64_t rows, int64_t C) { return dim3((unsigned)((C + 255) / 256), (unsigned)((rows + 8 * R - 1) / (8 * R))); }
 
@@ -261,7 +260,7 @@ void unpack(int64_t rows, int64_t C, const int8_t *codes, const uint8_t *steps, 
 
 cudaError_t launch_checkpoint_pack(gdn_dtype io, int64_t rows, int64_t C, const void *x, int64_t ld, int8_t *codes, uint8_t *steps,
                                    cudaStream_t stream) {
-    const bool wide = code_wide(io, rows, C, x, ld, codes);
+    const bool wide = code_wide(rows, C, x, ld, codes);
     switch (io) {
         case GDN_F32: pack<float>(rows, C, x, ld, codes, steps, wide, stream); break;
         case GDN_BF16: pack<__nv_bfloat16>(rows, C, x, ld, codes, steps, wide, stream); break;
@@ -272,7 +271,7 @@ cudaError_t launch_checkpoint_pack(gdn_dtype io, int64_t rows, int64_t C, const 
 
 cudaError_t launch_checkpoint_unpack(gdn_dtype io, int64_t rows, int64_t C, const int8_t *codes, const uint8_t *steps, void *y, int64_t ld,
                                      cudaStream_t stream) {
-    const bool wide = code_wide(io, rows, C, y, ld, codes);
+    const bool wide = code_wide(rows, C, y, ld, codes);
     switch (io) {
         case GDN_F32: unpack<float>(rows, C, codes, steps, y, ld, wide, stream); break;
         case GDN_BF16: unpack<__nv_bfloat16>(rows, C, codes, steps, y, ld, wide, stream); break;

@@ -353,7 +353,7 @@ def test_prompts_match_the_definition(io, gate, weighting, b):
                                          ([8] * 70, False), ([0] * 70 + [3, 0, 0] * 40, True)])
 @pytest.mark.parametrize("initial", [False, True])
 def test_lengths(io, lens, packed, initial):
-    """Forward and backward, sequences shorter and longer than a warp's rows, a tile and a cluster's step, and empty ones."""
+    """Forward and backward, sequences shorter and longer than a warp's rows and a tile, and empty ones."""
     m = draw(io, lens, 70, packed=packed, initial=initial, seed=len(lens))
     y, state, kept = prefill(m, "states")
     check(m, (y, state))
@@ -380,7 +380,7 @@ def test_widths_and_strides(io, C, gap):
 @pytest.mark.parametrize("lens,packed,C", [([2000], False, 64), ([1999, 2001], True, 40), ([600] * 9, False, 64), ([1300, 5, 2500, 0, 700], True, 128)])
 @pytest.mark.parametrize("keep", ["states", "8bit"])
 def test_long_rows(lens, packed, C, keep):
-    """Many steps of a cluster, and several parts side by side."""
+    """Many tiles, each waiting for what the one before it hands on."""
     m = draw("f32", lens, C, packed=packed, seed=11)
     shape = gdn.GdnDiagShape(0, 1 if packed else len(lens), sum(lens) if packed else lens[0], len(lens), C, 1, 2, 1, 1)
     assert gdn.gdn_diag_backward_workspace_bytes(shape) > gdn.gdn_diag_prefill_workspace_bytes(shape) > 0
@@ -836,6 +836,26 @@ def test_on_another_stream():
     side.synchronize()
     assert torch.equal(y, want[0]) and torch.equal(state, want[1]) and all(torch.equal(s, t) for s, t in zip(got, grads))
     assert torch.equal(codes, lib.gdn_checkpoint_unpack(*lib.gdn_checkpoint_pack(m["x"]), m["io"])) and step.shape == (1, 1, 128)
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams_at_once():
+    """Each has its own workspace, and its tiles wait for its own alone."""
+    m = [draw("bf16", lens, 1024, seed=24) for lens in ([2000, 1], [900, 1200, 300])]
+    want = [(lambda y, s, k: (y, s, *backward(q, k)))(*prefill(q, "states")) for q in m]
+    sides = [torch.cuda.Stream() for _ in m]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for q, side, outs in zip(m, sides, got):
+            y, s, kept = lib.gdn_diag_prefill(q["x"], q["a"], q["b"], q["A_log"], state_in=q["state"], cu_seqlens=q["cu"], keep="states",
+                                              stream=side, **kinds(q))
+            outs.append((y, s, *lib.gdn_diag_backward(q["dy"], kept, q["A_log"], x=q["x"], a=q["a"], b=q["b"], a_bias=q["a_bias"],
+                                                      b_bias=q["b_bias"], state_in=q["state"], cu_seqlens=q["cu"], dstate_out=q["dstate"],
+                                                      stream=side)))
+    torch.cuda.synchronize()
+    assert lib.gdn_last_device_status() == 0
+    assert all(torch.equal(s, t) for w, outs in zip(want, got) for out in outs for s, t in zip(w, out))
 
 
 # ------------------------------------------------------------------ a run of them together
