@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         const bool fast = p.pairs && c0 + kDiagSlice <= C;
         F2 sum_A = both(0.f), sum_a = both(0.f), sum_b = both(0.f);
         const bool some = w0 < rows, full = w0 + LT <= rows;
-        F2 sum_G = both(0.f), H = both(0.f), D = both(0.f);
+        F2 sum_G = both(0.f), D = both(0.f);
         uint32_t begins = 0, ends = 0;
         if (some) {
             const uint32_t edges = find_edges<LT>(p, window, (uint32_t)w0, 0, 28, sh.edge_first[w], sh.edge_last[w], lane);
@@ -211,7 +211,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             ends = edges >> 1 & live;
         }
         const uint32_t special = begins | ends;
-        const bool direct = !CODES && special == 0;
         stage_wait();
         const DiagLane l = p.table ? diag_lane(&st.table[0][0], kDiagSlice, lane) : diag_lane(p, c, slices);
         const bool near = diag_near<GATE>(l);
@@ -221,127 +220,123 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             step_a = code_scale(st.as[lane % LT]);
             step_b = code_scale(st.bs[lane % LT]);
         }
-        {
-            F2 through = both(1.f);
-            // DIRECT: -h before each row goes to shared memory at once, else the input, until h is known.
-            auto take = [&](auto only_near, auto directly) {
-                constexpr bool kNear = decltype(only_near)::value, kDirect = decltype(directly)::value;
-                F2 nat = mul2(at, both(-1.f));
+        // What G's map needs, for the fifth warp to hand on; with codes h's map as well, from which the other warps find their h.
+        F2 through = both(1.f), H = both(0.f);
+        auto minus_input = [&](F2 b, F2 x, F2 n) {
+            const F2 v = mul2(diag_minus_sigmoid(b, l.nbbias), x);
+            return WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(n), v);
+        };
+        auto take = [&](auto only_near) {
+            constexpr bool kNear = decltype(only_near)::value;
 #pragma unroll 1
-                for (int t0 = 0; t0 < LT; t0 += kGroup) {       // (the loads of a group go out before its stores)
-                    F2 a[kGroup], b[kGroup], x[kGroup], dy[kGroup], G[kGroup], out[kGroup];
+            for (int t0 = 0; t0 < LT; t0 += kGroup) {       // (the loads of a group go out before its stores)
+                F2 a[kGroup], b[kGroup], x[kGroup], dy[kGroup], G[kGroup];
 #pragma unroll
-                    for (int k = 0; k < kGroup; ++k) {
-                        a[k] = get_a(t0 + k);
+                for (int k = 0; k < kGroup; ++k) {
+                    a[k] = get_a(t0 + k);
+                    dy[k] = staged(&st.dy[0][0], t0 + k, lane);
+                    if (CODES) {
                         b[k] = get_b(t0 + k);
                         x[k] = get_x(t0 + k);
-                        dy[k] = staged(&st.dy[0][0], t0 + k, lane);
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int k = 0; k < kGroup; ++k) {
-                        G[k] = diag_exponent<GATE>(a[k], l);
-                        if (!kNear) {       // held finite, for a decay to 0 times it; a NaN stays one
-                            asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(G[k].x));
-                            asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(G[k].y));
-                        }
-                        const DiagDecay d = diag_decay<kNear>(G[k]);
-                        const F2 v = mul2(kDirect ? diag_minus_sigmoid(b[k], l.nbbias) : diag_sigmoid(b[k], l.nbbias), x[k]);
-                        const F2 in = WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(d.n), v);
-                        sum_G = add2(sum_G, G[k]);
-                        if (kDirect) {
-                            out[k] = nat;
-                            nat = fma2(d.alpha, nat, in);
-                        } else {
-                            out[k] = in;
-                            H = fma2(d.alpha, H, in);
-                        }
-                        through = mul2(through, d.alpha);
-                        D = fma2(through, dy[k], D);
-                    }
-#pragma unroll
-                    for (int k = 0; k < kGroup; ++k) {
-                        sG[(t0 + k) * 32 + lane] = make_float2(G[k].x, G[k].y);
-                        sh_[(t0 + k) * 32 + lane] = make_float2(out[k].x, out[k].y);
                     }
                 }
-            };
-            if (!direct) {
-                if (near) take(std::true_type{}, std::false_type{});
-                else take(std::false_type{}, std::false_type{});
-            } else if constexpr (!CODES) {
-                if (near) take(std::true_type{}, std::true_type{});
-                else take(std::false_type{}, std::true_type{});
-            }
-            if (!full) {            // rows outside are the identity, whatever the parameters make of them (an infinite bias: NaN)
-                sum_G = H = D = both(0.f);
-#pragma unroll 1
-                for (int t = 0; t < LT; ++t) {
-                    if (w0 + t < rows) sum_G = add2(sum_G, get_pair(sG + t * 32, lane));
-                    else sG[t * 32 + lane] = sh_[t * 32 + lane] = make_float2(0.f, 0.f);
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    G[k] = diag_exponent<GATE>(a[k], l);
+                    if (!kNear) {       // held finite, for a decay to 0 times it; a NaN stays one
+                        asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(G[k].x));
+                        asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(G[k].y));
+                    }
+                    sum_G = add2(sum_G, G[k]);
+                    const DiagDecay d = diag_decay<kNear>(G[k]);
+                    through = mul2(through, d.alpha);
+                    D = fma2(through, dy[k], D);
+                    if (CODES) {
+                        x[k] = minus_input(b[k], x[k], d.n);
+                        H = fma2(d.alpha, H, x[k]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    sG[(t0 + k) * 32 + lane] = make_float2(G[k].x, G[k].y);
+                    if (CODES) sh_[(t0 + k) * 32 + lane] = make_float2(x[k].x, x[k].y);
                 }
             }
-            if (special) {
-                through = both(1.f);
-                D = both(0.f);
-                H = both(0.f);
-                bool open = true;               // (nothing behind a sequence's first row comes back to here)
+        };
+        if (near) take(std::true_type{});
+        else take(std::false_type{});
+        if (!full) {            // rows outside are the identity, whatever the parameters make of them (an infinite bias: NaN)
+            sum_G = D = both(0.f);
 #pragma unroll 1
-                for (int t = 0; t < LT; ++t) {
-                    const F2 alpha = diag_decay<false>(get_pair(sG + t * 32, lane)).alpha;
-                    if (begins >> t & 1) {
-                        H = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t] * C, c, C) : both(0.f);
-                        open = false;
-                    }
-                    H = fma2(alpha, H, get_pair(sh_ + t * 32, lane));
-                    if (open) {
-                        F2 dy = staged(&st.dy[0][0], t, lane);
-                        if ((ends >> t & 1) && p.dstate_out)
-                            dy = add2(dy, load_state(p.dstate_out + (int64_t)(sh.edge_first[w][t + 1] - 1) * C, c, C));
-                        through = mul2(through, alpha);
-                        D = fma2(through, dy, D);
-                    }
-                }
+            for (int t = 0; t < LT; ++t) {
+                if (w0 + t < rows) sum_G = add2(sum_G, get_pair(sG + t * 32, lane));
+                else sG[t * 32 + lane] = make_float2(0.f, 0.f);
             }
         }
-        put_map(sh.maps[w], lane, diag_product(sum_G, begins != 0), H);
+        if (special) {          // nothing behind a sequence's first row comes back to here
+            through = both(1.f);
+            D = both(0.f);
+#pragma unroll 1
+            for (int t = 0; t < LT && !(begins >> t & 1); ++t) {
+                F2 dy = staged(&st.dy[0][0], t, lane);
+                if ((ends >> t & 1) && p.dstate_out)
+                    dy = add2(dy, load_state(p.dstate_out + (int64_t)(sh.edge_first[w][t + 1] - 1) * C, c, C));
+                through = mul2(through, diag_decay<false>(get_pair(sG + t * 32, lane)).alpha);
+                D = fma2(through, dy, D);
+            }
+        }
+        // -h before each row, or from 0 the map's; with codes the inputs are in h's place.
+        auto follow_edges = [&](F2 nat, bool map) {
+#pragma unroll 1
+            for (int t = 0; t < LT; ++t) {
+                const DiagDecay d = diag_decay<false>(get_pair(sG + t * 32, lane));
+                if (begins >> t & 1) {
+                    nat = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t] * C, c, C) : both(0.f);
+                    nat = mul2(nat, both(-1.f));
+                }
+                const F2 in = CODES ? get_pair(sh_ + t * 32, lane) : minus_input(get_b(t), get_x(t), d.n);
+                if (!map) sh_[t * 32 + lane] = make_float2(nat.x, nat.y);
+                nat = fma2(d.alpha, nat, in);
+            }
+            return nat;
+        };
+        if (CODES && begins) H = follow_edges(both(0.f), true);
+        put_map(sh.maps[w], lane, diag_product(sum_G, begins != 0), {-H.x, -H.y});
         sh.back[w][lane] = make_float2(D.x, D.y);
         __syncwarp();
-        side_sync<kThreads>(1);
-        if (!direct) {          // -h before each row, while the fifth warp hands on and waits
+        side_arrive<kThreads>(1);
+        // -h before each row, while the fifth warp hands on and waits.
+        auto follow = [&](auto only_near) {
+            F2 nat = mul2(at, both(-1.f));
+#pragma unroll 1
+            for (int t0 = 0; t0 < LT; t0 += kGroup) {
+                F2 G[kGroup], b[kGroup], x[kGroup], out[kGroup];
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    G[k] = get_pair(sG + (t0 + k) * 32, lane);
+                    if (!CODES) b[k] = get_b(t0 + k);
+                    x[k] = CODES ? get_pair(sh_ + (t0 + k) * 32, lane) : get_x(t0 + k);
+                }
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    const DiagDecay d = diag_decay<decltype(only_near)::value>(G[k]);
+                    out[k] = nat;
+                    nat = fma2(d.alpha, nat, CODES ? x[k] : minus_input(b[k], x[k], d.n));
+                }
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) sh_[(t0 + k) * 32 + lane] = make_float2(out[k].x, out[k].y);
+            }
+        };
+        if constexpr (CODES) {
+            side_sync<W * 32>(3);
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
-                if (CODES && k < w) at = diag_apply(get_product(sh.maps[k], lane), get_pair(sh.maps[k].shift, lane), at);
-            auto follow = [&](auto only_near) {
-#pragma unroll 1
-                for (int t0 = 0; t0 < LT; t0 += kGroup) {
-                    F2 alpha[kGroup], in[kGroup];
-#pragma unroll
-                    for (int k = 0; k < kGroup; ++k) {
-                        alpha[k] = diag_decay<decltype(only_near)::value>(get_pair(sG + (t0 + k) * 32, lane)).alpha;
-                        in[k] = get_pair(sh_ + (t0 + k) * 32, lane);
-                    }
-#pragma unroll
-                    for (int k = 0; k < kGroup; ++k) {
-                        sh_[(t0 + k) * 32 + lane] = make_float2(-at.x, -at.y);
-                        at = fma2(alpha[k], at, in[k]);
-                    }
-                }
-            };
-            if (begins || !CODES) {
-#pragma unroll 1
-                for (int t = 0; t < LT; ++t) {
-                    if (begins >> t & 1) at = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t] * C, c, C) : both(0.f);
-                    const F2 in = get_pair(sh_ + t * 32, lane);
-                    sh_[t * 32 + lane] = make_float2(-at.x, -at.y);
-                    at = fma2(diag_decay<false>(get_pair(sG + t * 32, lane)).alpha, at, in);
-                }
-            } else if (near) {
-                follow(std::true_type{});
-            } else {
-                follow(std::false_type{});
-            }
+                if (k < w) at = diag_apply(get_product(sh.maps[k], lane), get_pair(sh.maps[k].shift, lane), at);
         }
+        if (begins) follow_edges(mul2(at, both(-1.f)), false);
+        else if (near) follow(std::true_type{});
+        else follow(std::false_type{});
         side_sync<kThreads>(2);
         const uint32_t next = sh.next;
         F2 back = get_pair(sh.start, lane);     // what comes back from the rows behind the warp's
@@ -373,10 +368,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                             g = add2(g, load_state(p.dstate_out + (int64_t)(sh.edge_first[w][t + 1] - 1) * C, c, C));
                         const F2 i = diag_sigmoid(b[k], l.nbbias), v = mul2(i, x[k]), minus = both(-1.f);
                         const DiagDecay d = diag_decay<decltype(only_near)::value>(G[k]);
-                        F2 slope = h[k];                                            // dG / (g alpha), G = -g (h: negative)
-                        if (WEIGHT == GDN_DIAG_NORM) slope = fma2(mul2(v, d.alpha), diag_unweigh(d.n), slope);
+                        F2 slope = h[k], weight = d.n;                              // dG / (g alpha), G = -g (h: negative)
+                        if (WEIGHT == GDN_DIAG_NORM) {
+                            const F2 unweight = diag_unweigh(d.n);
+                            slope = fma2(mul2(v, d.alpha), unweight, slope);
+                            weight = mul2(mul2(d.n, fma2(d.n, both(-1.f), both(2.f))), unweight);
+                        }
                         if (WEIGHT == GDN_DIAG_COMPLEMENT) slope = add2(v, slope);
-                        const F2 ag = mul2(d.alpha, g), dv = WEIGHT == GDN_DIAG_PLAIN ? g : mul2(g, diag_weigh<WEIGHT>(d.n));
+                        const F2 ag = mul2(d.alpha, g), dv = WEIGHT == GDN_DIAG_PLAIN ? g : mul2(g, weight);
                         const F2 dG = mul2(ag, slope), dGG = mul2(dG, G[k]);
                         const F2 nsp = mul2(G[k], l.ninverse);                      // the gate's opening, negative
                         const F2 da_ = GATE == GDN_DIAG_SIGMOID ? fma2(dGG, nsp, dGG)
@@ -416,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         if (next < items) stage(next);
         item = next;
     }
-    side_sync<kThreads>(1);
+    side_arrive<kThreads>(1);
 }
 
 template <typename IO, int GATE, int WEIGHT> cudaError_t launch(const DiagParams &p, cudaStream_t stream) {
