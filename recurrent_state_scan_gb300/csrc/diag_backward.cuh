@@ -38,6 +38,7 @@ template <typename IO> struct Staged<IO, true> {
     alignas(16) int8_t x[LT][kDiagSlice], b[LT][kDiagSlice], codes_a[LT][kDiagSlice];
     alignas(16) IO dy[LT][kDiagSlice];
     alignas(16) uint8_t xs[LT], bs[LT], as[LT];
+    alignas(16) float step_x[LT], gate_a[LT], gate_b[LT];       // steps; those of the sigmoids' arguments times -log2 e
     alignas(16) float2 G[LT][32], h[LT][32];
     alignas(16) float table[5][kDiagSlice], kept[kDiagSlice];
 };
@@ -75,11 +76,26 @@ __device__ __forceinline__ void stage_codes(int8_t *to, uint8_t *to_steps, const
         to_steps[lane] = r0 + lane >= lo && r0 + lane < hi ? p.steps[at + lane] : (uint8_t)0;
     }
 }
-// The pair of row t, whose step lane t holds.
-__device__ __forceinline__ F2 code_pair(const int8_t *rows, float step, int t, int lane) {
-    const uint32_t q = reinterpret_cast<const uint16_t *>(rows)[t * 32 + lane];
-    return mul2(code_values(q), both(__shfl_sync(~0u, step, t)));
-}
+// The pair of row t, in units of its step.
+__device__ __forceinline__ F2 code_pair(const int8_t *rows, int t, int lane) { return code_values(reinterpret_cast<const uint16_t *>(rows)[t * 32 + lane]); }
+// A gate's argument: with codes in units of their step, `by` being that times what the gate multiplies it by.
+struct Argument {
+    F2 v;
+    float by;
+};
+// What belongs to N rows, alike for all lanes.
+template <int N> struct PerRow {
+    float v[N];
+    __device__ __forceinline__ PerRow(const float *from) {
+        if constexpr (N == 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(from);
+            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = from[k];
+        }
+    }
+};
 
 template <typename IO, int GATE, int WEIGHT, bool CODES>
 __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backward_kernel(const __grid_constant__ DiagParams p) {
@@ -193,18 +209,39 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             }
         }
     };
-    float step_x = 0.f, step_a = 0.f, step_b = 0.f;
-    auto get_x = [&](int t) -> F2 {
-        if constexpr (CODES) return code_pair(&st.x[0][0], step_x, t, lane);
-        else return staged(&st.x[0][0], t, lane);
+    // Rows' pairs: x, and the gates' arguments beside what the gate multiplies them by.
+    auto get_x = [&](auto &to, int t0) {
+        constexpr int N = sizeof(to) / sizeof(F2);
+        if constexpr (CODES) {
+            const PerRow<N> step(&st.step_x[t0]);
+#pragma unroll
+            for (int k = 0; k < N; ++k) to[k] = mul2(code_pair(&st.x[0][0], t0 + k, lane), both(step.v[k]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) to[k] = staged(&st.x[0][0], t0 + k, lane);
+        }
     };
-    auto get_a = [&](int t) -> F2 {
-        if constexpr (CODES) return code_pair(&st.codes_a[0][0], step_a, t, lane);
-        else return staged(st.a(), t, lane);
+    auto get_a = [&](auto &to, int t0) {
+        constexpr int N = sizeof(to) / sizeof(Argument);
+        if constexpr (CODES) {
+            const PerRow<N> by(&st.gate_a[t0]);
+#pragma unroll
+            for (int k = 0; k < N; ++k) to[k] = {code_pair(&st.codes_a[0][0], t0 + k, lane), by.v[k]};
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) to[k] = {staged(st.a(), t0 + k, lane), kGateUnit<GATE>};
+        }
     };
-    auto get_b = [&](int t) -> F2 {
-        if constexpr (CODES) return code_pair(&st.b[0][0], step_b, t, lane);
-        else return staged(&st.b[0][0], t, lane);
+    auto get_b = [&](auto &to, int t0) {
+        constexpr int N = sizeof(to) / sizeof(Argument);
+        if constexpr (CODES) {
+            const PerRow<N> by(&st.gate_b[t0]);
+#pragma unroll
+            for (int k = 0; k < N; ++k) to[k] = {code_pair(&st.b[0][0], t0 + k, lane), by.v[k]};
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) to[k] = {staged(&st.b[0][0], t0 + k, lane), -kLog2e};
+        }
     };
     EdgeWindow window = edge_window(p, 0, lane);
     if (item < items) stage(item);
@@ -228,34 +265,36 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         const bool near = diag_near<GATE>(l);
         F2 at = some && (CODES ? tile : w0) > 0 ? get_pair(reinterpret_cast<const float2 *>(st.kept), lane) : both(0.f);
         if constexpr (CODES) {
-            step_x = code_scale(st.xs[lane % LT]);
-            step_a = code_scale(st.as[lane % LT]);
-            step_b = code_scale(st.bs[lane % LT]);
+            if (lane < LT) {
+                st.step_x[lane] = code_scale(st.xs[lane]);
+                st.gate_a[lane] = kGateUnit<GATE> * code_scale(st.as[lane]);
+                st.gate_b[lane] = -kLog2e * code_scale(st.bs[lane]);
+            }
+            __syncwarp();
         }
         // What G's map needs, for the fifth warp to hand on; with codes h's map as well, from which the other warps find their h.
         F2 through = both(1.f), H = both(0.f);
-        auto minus_input = [&](F2 b, F2 x, F2 n) {
-            const F2 v = mul2(diag_minus_sigmoid(b, l.nbbias), x);
+        auto minus_input = [&](Argument b, F2 x, F2 n) {
+            const F2 v = mul2(diag_minus_sigmoid(b.v, l.nbbias, b.by), x);
             return WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(n), v);
         };
         auto take = [&](auto only_near) {
             constexpr bool kNear = decltype(only_near)::value;
 #pragma unroll 1
             for (int t0 = 0; t0 < LT; t0 += kGroup) {       // (the loads of a group go out before its stores)
-                F2 a[kGroup], b[kGroup], x[kGroup], dy[kGroup], G[kGroup];
-#pragma unroll
-                for (int k = 0; k < kGroup; ++k) {
-                    a[k] = get_a(t0 + k);
-                    dy[k] = staged(&st.dy[0][0], t0 + k, lane);
-                    if (CODES) {
-                        b[k] = get_b(t0 + k);
-                        x[k] = get_x(t0 + k);
-                    }
+                Argument a[kGroup], b[kGroup];
+                F2 x[kGroup], dy[kGroup], G[kGroup];
+                get_a(a, t0);
+                if (CODES) {
+                    get_b(b, t0);
+                    get_x(x, t0);
                 }
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) dy[k] = staged(&st.dy[0][0], t0 + k, lane);
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k) {
-                    G[k] = diag_exponent<GATE>(a[k], l);
+                    G[k] = diag_exponent<GATE>(a[k].v, l, a[k].by);
                     if (!kNear) {       // held finite, for a decay to 0 times it; a NaN stays one
                         asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(G[k].x));
                         asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(G[k].y));
@@ -307,7 +346,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                     nat = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t] * C, c, C) : both(0.f);
                     nat = mul2(nat, both(-1.f));
                 }
-                const F2 in = CODES ? get_pair(sh_ + t * 32, lane) : minus_input(get_b(t), get_x(t), d.n);
+                F2 in;
+                if (CODES) {
+                    in = get_pair(sh_ + t * 32, lane);
+                } else {
+                    Argument b[1];
+                    F2 x[1];
+                    get_b(b, t);
+                    get_x(x, t);
+                    in = minus_input(b[0], x[0], d.n);
+                }
                 if (!map) sh_[t * 32 + lane] = make_float2(nat.x, nat.y);
                 nat = fma2(d.alpha, nat, in);
             }
@@ -323,12 +371,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             F2 nat = mul2(at, both(-1.f));
 #pragma unroll 1
             for (int t0 = 0; t0 < LT; t0 += kGroup) {
-                F2 G[kGroup], b[kGroup], x[kGroup], out[kGroup];
+                Argument b[kGroup];
+                F2 G[kGroup], x[kGroup], out[kGroup];
+                if (!CODES) {
+                    get_b(b, t0);
+                    get_x(x, t0);
+                }
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k) {
                     G[k] = get_pair(sG + (t0 + k) * 32, lane);
-                    if (!CODES) b[k] = get_b(t0 + k);
-                    x[k] = CODES ? get_pair(sh_ + (t0 + k) * 32, lane) : get_x(t0 + k);
+                    if (CODES) x[k] = get_pair(sh_ + (t0 + k) * 32, lane);
                 }
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k) {
@@ -362,11 +414,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                 constexpr int N = kPlain ? kGroup : 1;
 #pragma unroll 1
                 for (int t0 = LT - N; t0 >= 0; t0 -= N) {
-                    F2 b[N], x[N], dy[N], G[N], h[N];
+                    Argument b[N];
+                    F2 x[N], dy[N], G[N], h[N];
+                    get_b(b, t0);
+                    get_x(x, t0);
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
-                        b[k] = get_b(t0 + k);
-                        x[k] = get_x(t0 + k);
                         dy[k] = staged(&st.dy[0][0], t0 + k, lane);
                         G[k] = get_pair(sG + (t0 + k) * 32, lane);
                         h[k] = get_pair(sh_ + (t0 + k) * 32, lane);
@@ -378,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                         F2 g = add2(dy[k], back);           // the gradient at h_t
                         if (!kPlain && (ends >> t & 1) && p.dstate_out)
                             g = add2(g, load_state(p.dstate_out + (int64_t)(sh.edge_first[w][t + 1] - 1) * C, c, C));
-                        const F2 i = diag_sigmoid(b[k], l.nbbias), v = mul2(i, x[k]), minus = both(-1.f);
+                        const F2 i = diag_sigmoid(b[k].v, l.nbbias, b[k].by), v = mul2(i, x[k]), minus = both(-1.f);
                         const DiagDecay d = diag_decay<decltype(only_near)::value>(G[k]);
                         F2 slope = h[k], weight = d.n;                              // dG / (g alpha), G = -g (h: negative)
                         if (WEIGHT == GDN_DIAG_NORM) {

@@ -113,15 +113,16 @@ template <bool NEAR> __device__ __forceinline__ DiagDecay diag_decay(F2 G) {
     const bool x = G.x < 0.25f, y = G.y < 0.25f;
     return {{x ? n.x : far.x, y ? n.y : far.y}, {x ? a.x : e.x, y ? a.y : e.y}};
 }
-// sigmoid(v + bias); `nbias` is -bias log2 e.  e^-v beyond fp32's range gives 0.
-__device__ __forceinline__ F2 diag_sigmoid(F2 v, F2 nbias) {
-    const F2 t = fma2(v, both(-kLog2e), nbias);
+// sigmoid(v + bias); `nbias` is -bias log2 e.  e^-v beyond fp32's range gives 0.  (`k`: for v in units of a power of two, its
+// multiple of -log2 e, by which the product rounds alike.)
+__device__ __forceinline__ F2 diag_sigmoid(F2 v, F2 nbias, float k = -kLog2e) {
+    const F2 t = fma2(v, both(k), nbias);
     const F2 d = add2({ex2(t.x), ex2(t.y)}, both(1.f));
     return {rcp(d.x), rcp(d.y)};
 }
 // Its negative, by the same steps.
-__device__ __forceinline__ F2 diag_minus_sigmoid(F2 v, F2 nbias) {
-    const F2 t = fma2(v, both(-kLog2e), nbias);
+__device__ __forceinline__ F2 diag_minus_sigmoid(F2 v, F2 nbias, float k = -kLog2e) {
+    const F2 t = fma2(v, both(k), nbias);
     const F2 d = fma2({ex2(t.x), ex2(t.y)}, both(-1.f), both(-1.f));
     return {rcp(d.x), rcp(d.y)};
 }
@@ -159,8 +160,10 @@ __device__ __forceinline__ F2 diag_unweigh(F2 n) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(q.y));
     return r;
 }
-template <int GATE> __device__ __forceinline__ F2 diag_exponent(F2 a, const DiagLane &l) {
-    return mul2(l.rate, GATE == GDN_DIAG_SIGMOID ? diag_sigmoid(a, l.nabias) : diag_softplus(add2(a, l.abias)));
+// (`by`: for a in units of a power of two, which it then holds as a factor.)
+template <int GATE> constexpr float kGateUnit = GATE == GDN_DIAG_SIGMOID ? -kLog2e : 1.f;
+template <int GATE> __device__ __forceinline__ F2 diag_exponent(F2 a, const DiagLane &l, float by = kGateUnit<GATE>) {
+    return mul2(l.rate, GATE == GDN_DIAG_SIGMOID ? diag_sigmoid(a, l.nabias, by) : diag_softplus(fma2(a, both(by), l.abias)));
 }
 
 __device__ __forceinline__ DiagLane diag_lane(const float *A_log, const float *a_bias, const float *b_bias, int c, int C) {
