@@ -45,11 +45,11 @@ template <typename IO> struct Staged<IO, true> {
 static_assert(LT * kDiagSlice % 16 == 0 && LT == 16, "what follows an array is aligned as it is");
 template <typename IO, bool CODES> struct Shared {
     Staged<IO, CODES> rows[W];
-    DiagMaps maps[W];                   // a warp's rows: h's map, and with `back` G's
-    float2 back[W][32];
-    DiagMaps behind[W];                 // G's: the tile's rows behind a warp's
+    DiagMaps maps[W];                   // a warp's rows, G's
+    float2 shift[CODES ? W : 1][32];    // with codes: h's, whose product is the same
+    DiagMaps behind[W - 1];             // G's: the tile's rows behind a warp's
     float2 start[32];                   // what comes back to the tile
-    float2 sums[W][3][32];              // the parameters' gradients
+    float2 sums[2][W][3][32];           // the parameters' gradients, of two items in turn
     uint32_t next;
     int edge_first[W][LT + 1], edge_last[W][LT + 1];
 };
@@ -114,45 +114,46 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
     uint32_t item = walk.first(sh.next);
     if (w == W) {
         // The parameters' gradients of an item, over the rows' warps in their order.
-        auto put_sums = [&](uint32_t of) {
+        auto put_sums = [&](uint32_t of, const float2 (*sums)[3][32]) {
             const int j = walk.tile_of(of), c = ((int)of - j * slices) * kDiagSlice + 2 * lane;
             float *one[3] = {p.dA_log, p.da_bias, p.db_bias};
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
-                F2 total = get_pair(sh.sums[0][k], lane);
+                F2 total = get_pair(sums[0][k], lane);
 #pragma unroll
-                for (int r = 1; r < W; ++r) total = add2(total, get_pair(sh.sums[r][k], lane));
+                for (int r = 1; r < W; ++r) total = add2(total, get_pair(sums[r][k], lane));
                 if (tiles > 1) store_state(p.partial + ((int64_t)j * 3 + k) * C, total, c, C);
                 else if (one[k]) store_state(one[k], total, c, C);
             }
         };
         uint32_t last = items;
-        while (item < items) {
+        int turn = 0;
+        for (; item < items; turn ^= 1) {
             const int j = walk.tile_of(item), slice = (int)item - j * slices;
             const uint32_t later = lane == 0 ? walk.ticket() : 0u;
             side_sync<kThreads>(1);
             DiagProduct all = get_product(sh.maps[W - 1], lane);
-            F2 shift = get_pair(sh.back[W - 1], lane);
+            F2 shift = get_pair(sh.maps[W - 1].shift, lane);
 #pragma unroll
             for (int r = W - 2; r >= 0; --r) {
                 put_map(sh.behind[r], lane, all, shift);
                 const DiagProduct m = get_product(sh.maps[r], lane);
-                shift = diag_apply(m, get_pair(sh.back[r], lane), shift);
+                shift = diag_apply(m, get_pair(sh.maps[r].shift, lane), shift);
                 all = diag_join(all, m);
             }
             if (j + 1 < tiles) walk.hand_on_map(j, slice, all, shift);
-            if (last < items) put_sums(last);
             const F2 in = walk.come_in(j, slice);
             if (j + 1 < tiles) walk.hand_on(j, slice, diag_apply(all, shift, in));
             sh.start[lane] = make_float2(in.x, in.y);
             if (lane == 0) sh.next = later;
             __syncwarp();
             side_arrive<kThreads>(2);
+            if (last < items) put_sums(last, sh.sums[turn ^ 1]);        // (out of the way of what is handed on)
             last = item;
             item = __shfl_sync(~0u, later, 0);
         }
         side_sync<kThreads>(1);
-        if (last < items) put_sums(last);
+        if (last < items) put_sums(last, sh.sums[turn ^ 1]);
         return;
     }
     const bool has_b = p.has_b;
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
     };
     EdgeWindow window = edge_window(p, 0, lane);
     if (item < items) stage(item);
-    while (item < items) {
+    for (int turn = 0; item < items; turn ^= 1) {
         const int j = walk.tile_of(item), tile = tiles - 1 - j, slice = (int)item - j * slices, w0 = tile * kDiagTile + w * LT, c0 = slice * kDiagSlice;
         const int c = c0 + 2 * lane;
         const bool fast = p.pairs && c0 + kDiagSlice <= C;
@@ -362,8 +363,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             return nat;
         };
         if (CODES && begins) H = follow_edges(both(0.f), true);
-        put_map(sh.maps[w], lane, diag_product(sum_G, begins != 0), {-H.x, -H.y});
-        sh.back[w][lane] = make_float2(D.x, D.y);
+        put_map(sh.maps[w], lane, diag_product(sum_G, begins != 0), D);
+        if (CODES) sh.shift[w][lane] = make_float2(-H.x, -H.y);
         __syncwarp();
         side_arrive<kThreads>(1);
         // -h before each row, while the fifth warp hands on and waits.
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             side_sync<W * 32>(3);
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
-                if (k < w) at = diag_apply(get_product(sh.maps[k], lane), get_pair(sh.maps[k].shift, lane), at);
+                if (k < w) at = diag_apply(get_product(sh.maps[k], lane), get_pair(sh.shift[k], lane), at);
         }
         if (begins) follow_edges(mul2(at, both(-1.f)), false);
         else if (near) follow(std::true_type{});
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         }
         const F2 all_sums[3] = {sum_A, sum_a, sum_b};
 #pragma unroll
-        for (int k = 0; k < 3; ++k) sh.sums[w][k][lane] = make_float2(all_sums[k].x, all_sums[k].y);
+        for (int k = 0; k < 3; ++k) sh.sums[turn][w][k][lane] = make_float2(all_sums[k].x, all_sums[k].y);
         __syncwarp();
         if (next < items) stage(next);
         item = next;
