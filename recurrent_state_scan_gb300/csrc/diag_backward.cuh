@@ -5,13 +5,15 @@
 //     dx = G w i,   db = dx x (1 - i),   dg = G (alpha h_{t-1} + i x w'(g)),   w' = -alpha^2 / w | -alpha | 0,
 //     da = dg g (1 - s) (sigmoid gate) | -dg e^A_log s (softplus gate),
 //     dA_log = sum dg g,  da_bias = sum da,  db_bias = sum db,  dstate_in = alpha G at a sequence's first row.
-// The walk is the forward pass's, from the last tile to the first: warps fold their rows to G's map and, from the kept
-// h, to h's, both with the same product of decays; a fifth warp hands G's on.  Of what the gates give, the decays' exponents G and
-// h stay in shared memory for the second pass over the rows; the rest is made again, in loops of four rows (all 16 in a row, their
-// code did not fit the instruction cache: 440 us for 16,384 rows of 4,096 where these take 258).
+// The walk is the forward pass's, from the last tile to the first: warps fold their rows to G's map, a fifth warp hands it on, and
+// while that one waits they run h forward again from the kept states.  Of what the gates give, the decays' exponents G and h stay in
+// shared memory for the last pass over the rows; the rest is made again, in loops of four rows (all 16 in a row, their code did
+// not fit the instruction cache: 440 us for 16,384 rows of 4,096 where these take 245).  The rows that come an iteration later are
+// fetched into L2 meanwhile (247 us; without 255).
 //
-// Bound by instructions and by the multiply pipe: 71 a value (91 from codes), at half the issue slots.  8,192 bf16 rows of 4,096
-// channels take 131 us (3.6 TB/s; from codes 141), of which the bytes alone would take 69 (54).
+// Bound by instructions: 78 a value (89 from codes), at 58% of the issue slots; with the gates' arithmetic taken out and no wait
+// for other tiles the same loads, stores and barriers took 190 us of then 255.  8,192 bf16 rows of 4,096 channels take 119 us
+// (3.9 TB/s; from codes 136), of which the bytes alone would take 69 (54).
 #pragma once
 
 #include <type_traits>
