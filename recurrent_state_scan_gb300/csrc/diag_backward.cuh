@@ -203,10 +203,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         if (item < items) {
             const int j = walk.tile_of(item), r0 = (tiles - 1 - j) * kDiagTile + w * LT, f0 = ((int)item - j * slices) * kDiagSlice;
             if constexpr (!CODES) {
-                fetch_rows<IO>(p.x, p.ld_x, p.a, p.ld_a, r0, rows, f0, lane);
-                fetch_rows<IO>(p.dy, p.ld_y, has_b ? p.b : nullptr, p.ld_b, r0, rows, f0, lane);
+                fetch_rows<IO>(p.x, p.ld_x, p.a, p.ld_a, r0, rows, f0, C, lane);
+                fetch_rows<IO>(p.dy, p.ld_y, has_b ? p.b : nullptr, p.ld_b, r0, rows, f0, C, lane);
             } else {
-                fetch_rows<IO>(p.dy, p.ld_y, nullptr, 0, r0, rows, f0, lane);
+                fetch_rows<IO>(p.dy, p.ld_y, nullptr, 0, r0, rows, f0, C, lane);
                 const int64_t all = (int64_t)tiles * kDiagTile, k = lane / 8;
                 if (k < 2 + has_b) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.codes + ((k * slices + f0 / kDiagSlice) * all + r0) * kDiagSlice + lane % 8 * 128));
             }

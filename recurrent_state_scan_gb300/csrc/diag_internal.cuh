@@ -292,14 +292,15 @@ template <typename IO, int N> struct Stager {
         }
     }
 };
-// Has 16 rows of a slice of two arrays (the second may be null) fetched into L2, by one warp.
+// Has 16 rows of a slice of two arrays (the second may be null) fetched into L2, by one warp: no address outside them.
 template <typename IO>
-__device__ __forceinline__ void fetch_rows(const void *one, int64_t ld_one, const void *two, int64_t ld_two, int r0, int rows, int c0, int lane) {
+__device__ __forceinline__ void fetch_rows(const void *one, int64_t ld_one, const void *two, int64_t ld_two, int r0, int rows, int c0, int C, int lane) {
     const int row = r0 + lane % 16;
     const IO *from = lane < 16 ? static_cast<const IO *>(one) + row * ld_one : static_cast<const IO *>(two) + row * ld_two;
     if (row >= rows || (lane >= 16 && two == nullptr)) return;
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(IO) / 2; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + c0 + i * 32));
+    for (int c = c0; c < c0 + kDiagSlice; c += 128 / (int)sizeof(IO))
+        if (c < C) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + c));
 }
 // Fills N staged rows with four bytes.
 template <typename IO, int N> __device__ __forceinline__ void fill_rows(IO *to, uint32_t bits, int lane) {
