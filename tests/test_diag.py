@@ -563,6 +563,25 @@ def test_gradients_match_the_definition(io, gate, weighting, b, keep):
     check_gradients(m, backward(m, kept), keep == "8bit")
 
 
+def slow_rates(C, seed):
+    """A_log of sigmoid gates whose decays are 0.9 to 0.999 where they are open."""
+    return torch.log(-torch.log(0.9 + 0.099 * torch.rand(C, generator=torch.Generator().manual_seed(seed)))).cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("weighting", ["norm", "complement", "plain"])
+@pytest.mark.parametrize("keep", ["states", "8bit"])
+@pytest.mark.parametrize("C,lens", [(64, [300]), (128, [70, 0, 261, 33]), (130, [200])])
+def test_slow_sigmoid_gates(io, weighting, keep, C, lens):
+    """No rate above 1/4 in a slice of 64 channels: decays without an exponential, forward and backward."""
+    m = draw(io, lens, C, weighting=weighting, seed=C)
+    m["A_log"] = slow_rates(C, C + 1)
+    y, state, kept = prefill(m, keep)
+    check(m, (y, state))
+    check_gradients(m, backward(m, kept), keep == "8bit")
+
+
 @pytest.mark.gpu
 def test_gradients_without_a_final_states_gradient():
     for keep in ("states", "8bit"):
