@@ -586,6 +586,10 @@ gdn_status gdn_ssm_decode(const gdn_ssm_shape *shape, const gdn_ssm_params *para
  * gdn_checkpoint_pack, and h before every 64th row (rows counted over the whole call).  The
  * backward pass then takes the gradient at the values that the codes hold, h running on from
  * each kept state.
+ *
+ * A gate is held shut by -infinity in a (alpha_t = 1, and with COMPLEMENT and NORM w_t = 0: the
+ * token leaves h as it is; with PLAIN w_t stays 1) or in b (i_t = 0).  The codes keep such
+ * entries beside the others of their block, which a large finite value would round away.
  * ---------------------------------------------------------------------------------- */
 typedef enum { GDN_DIAG_SOFTPLUS = 0, GDN_DIAG_SIGMOID = 1 } gdn_diag_gate;
 typedef enum { GDN_DIAG_PLAIN = 0, GDN_DIAG_COMPLEMENT = 1, GDN_DIAG_NORM = 2 } gdn_diag_weighting;
@@ -618,8 +622,9 @@ typedef struct gdn_diag_shape {
  *   workspace    gdn_diag_prefill_workspace_bytes(shape) bytes (0 up to 64 rows), 16-byte
  *                aligned; its contents need no initialisation and are not preserved.  Calls
  *                that overlap on the GPU need one each.
- * An infinity or a NaN reaches the rest of its channel and sequence, no other.  Outputs may
- * not overlap inputs or one another (slices of one wider row, side by side, do not).
+ * An infinity or a NaN reaches the rest of its channel and sequence, no other (in the backward
+ * pass with KEEP_8BIT the other channels of its block of 64 too, unless it is a -infinity that
+ * holds a gate shut).  Outputs may not overlap inputs or one another (slices of one wider row, side by side, do not).
  */
 size_t gdn_diag_kept_bytes(const gdn_diag_shape *shape);
 size_t gdn_diag_prefill_workspace_bytes(const gdn_diag_shape *shape);

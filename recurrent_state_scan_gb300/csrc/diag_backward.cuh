@@ -85,6 +85,12 @@ struct Argument {
     F2 v;
     float by;
 };
+// Codes of gates that are held shut, as what they stand for.
+template <int N> __device__ __forceinline__ void shut_gates(Argument (&to)[N]) {
+    const float minus = __uint_as_float(0xff800000u);
+#pragma unroll
+    for (int k = 0; k < N; ++k) to[k].v = {to[k].v.x == kShutCode ? minus : to[k].v.x, to[k].v.y == kShutCode ? minus : to[k].v.y};
+}
 // What belongs to N rows, alike for all lanes.
 template <int N> struct PerRow {
     float v[N];
@@ -224,23 +230,25 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             for (int k = 0; k < N; ++k) to[k] = staged(&st.x[0][0], t0 + k, lane);
         }
     };
-    auto get_a = [&](auto &to, int t0) {
+    auto get_a = [&](auto &to, int t0, bool masked) {
         constexpr int N = sizeof(to) / sizeof(Argument);
         if constexpr (CODES) {
             const PerRow<N> by(&st.gate_a[t0]);
 #pragma unroll
             for (int k = 0; k < N; ++k) to[k] = {code_pair(&st.codes_a[0][0], t0 + k, lane), by.v[k]};
+            if (masked) shut_gates(to);
         } else {
 #pragma unroll
             for (int k = 0; k < N; ++k) to[k] = {staged(st.a(), t0 + k, lane), kGateUnit<GATE>};
         }
     };
-    auto get_b = [&](auto &to, int t0) {
+    auto get_b = [&](auto &to, int t0, bool masked) {
         constexpr int N = sizeof(to) / sizeof(Argument);
         if constexpr (CODES) {
             const PerRow<N> by(&st.gate_b[t0]);
 #pragma unroll
             for (int k = 0; k < N; ++k) to[k] = {code_pair(&st.b[0][0], t0 + k, lane), by.v[k]};
+            if (masked) shut_gates(to);
         } else {
 #pragma unroll
             for (int k = 0; k < N; ++k) to[k] = {staged(&st.b[0][0], t0 + k, lane), -kLog2e};
@@ -267,7 +275,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         const DiagLane l = p.table ? diag_lane(&st.table[0][0], kDiagSlice, lane) : diag_lane(p, c, slices);
         const bool near = diag_near<GATE>(l);
         F2 at = some && (CODES ? tile : w0) > 0 ? get_pair(reinterpret_cast<const float2 *>(st.kept), lane) : both(0.f);
+        bool masked = false;            // whether codes of a or b are -128
         if constexpr (CODES) {
+            masked = any_shut(&st.codes_a[0][0], &st.b[0][0], lane);
             if (lane < LT) {
                 st.step_x[lane] = code_scale(st.xs[lane]);
                 st.gate_a[lane] = kGateUnit<GATE> * code_scale(st.as[lane]);
@@ -281,15 +291,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             const F2 v = mul2(diag_minus_sigmoid(b.v, l.nbbias, b.by), x);
             return WEIGHT == GDN_DIAG_PLAIN ? v : mul2(diag_weigh<WEIGHT>(n), v);
         };
-        auto take = [&](auto only_near) {
+        auto take = [&](auto only_near, auto masks) {
             constexpr bool kNear = decltype(only_near)::value;
 #pragma unroll 1
             for (int t0 = 0; t0 < LT; t0 += kGroup) {       // (the loads of a group go out before its stores)
                 Argument a[kGroup], b[kGroup];
                 F2 x[kGroup], dy[kGroup], G[kGroup];
-                get_a(a, t0);
+                get_a(a, t0, decltype(masks)::value);
                 if (CODES) {
-                    get_b(b, t0);
+                    get_b(b, t0, decltype(masks)::value);
                     get_x(x, t0);
                 }
 #pragma unroll
@@ -318,8 +328,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                 }
             }
         };
-        if (near) take(std::true_type{});
-        else take(std::false_type{});
+        if (CODES && masked) take(std::false_type{}, std::true_type{});
+        else if (near) take(std::true_type{}, std::false_type{});
+        else take(std::false_type{}, std::false_type{});
         if (!full) {            // rows outside are the identity, whatever the parameters make of them (an infinite bias: NaN)
             sum_G = D = both(0.f);
 #pragma unroll 1
@@ -355,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                 } else {
                     Argument b[1];
                     F2 x[1];
-                    get_b(b, t);
+                    get_b(b, t, false);
                     get_x(x, t);
                     in = minus_input(b[0], x[0], d.n);
                 }
@@ -377,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                 Argument b[kGroup];
                 F2 G[kGroup], x[kGroup], out[kGroup];
                 if (!CODES) {
-                    get_b(b, t0);
+                    get_b(b, t0, false);
                     get_x(x, t0);
                 }
 #pragma unroll
@@ -411,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         if (some) {
             IO *dx = (IO *)p.dx + (int64_t)(w0 + LT - 1) * p.ld_dx + c, *da = (IO *)p.da + (int64_t)(w0 + LT - 1) * p.ld_da + c;
             IO *db = (IO *)p.db + (int64_t)(w0 + LT - 1) * p.ld_db + c;
-            // PLAIN: all rows are there, stored by pairs, and no sequence begins or ends.
+            // PLAIN: all rows are there, stored by pairs, no sequence begins or ends, and no code holds a gate shut.
             auto give = [&](auto only_near, auto plain) {
                 constexpr bool kPlain = decltype(plain)::value;
                 constexpr int N = kPlain ? kGroup : 1;
@@ -419,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                 for (int t0 = LT - N; t0 >= 0; t0 -= N) {
                     Argument b[N];
                     F2 x[N], dy[N], G[N], h[N];
-                    get_b(b, t0);
+                    get_b(b, t0, !kPlain && masked);
                     get_x(x, t0);
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
@@ -472,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                     }
                 }
             };
-            if (!full || !fast || special) give(std::false_type{}, std::false_type{});
+            if (!full || !fast || special || masked) give(std::false_type{}, std::false_type{});
             else if (near) give(std::true_type{}, std::true_type{});
             else give(std::false_type{}, std::true_type{});
         }

@@ -119,18 +119,21 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_prefil
                 for (int q = 0; q < (has_b ? 3 : 2); ++q) {
                     const IO *from = sx + q * LT * kDiagSlice;
                     const int64_t at = ((int64_t)q * slices + slice) * all + w0;
+                    bool infinite = false;
                     if constexpr (sizeof(IO) == 2) {
-                        code_rows<IO>(from, p.codes + at * kDiagSlice, p.steps + at, rows - w0, lane);
+                        infinite = code_rows<IO>(from, p.codes + at * kDiagSlice, p.steps + at, rows - w0, lane);
                     } else {
 #pragma unroll 4
                         for (int t = 0; t < LT; ++t) {
                             const F2 v = staged(from, t, lane);
-                            const uint32_t e = code_step(__reduce_max_sync(~0u, magnitude(v)));
+                            const uint32_t most = __reduce_max_sync(~0u, magnitude(v)), e = code_step(most);
                             if (w0 + t >= rows) break;
+                            infinite |= most == 0x7f800000u;
                             *reinterpret_cast<uint16_t *>(p.codes + (at + t) * kDiagSlice + 2 * lane) = (uint16_t)codes_of(v, e);
                             if (lane == 0) p.steps[at + t] = (uint8_t)e;
                         }
                     }
+                    if (infinite && q > 0) code_gate_rows<IO>(from, p.codes + at * kDiagSlice, p.steps + at, rows - w0, lane);
                 }
             }
             auto take = [&](auto only_near) {

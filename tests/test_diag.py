@@ -582,6 +582,49 @@ def test_slow_sigmoid_gates(io, weighting, keep, C, lens):
     check_gradients(m, backward(m, kept), keep == "8bit")
 
 
+def on_the_codes(m):
+    """The call with x, a and b rounded to what 8 bits hold of them, so that codes lose nothing."""
+    return dict(m, **{k: stored(m[k].double().cpu().view(-1, m["C"])).to(m["io"]).view(m[k].shape).cuda() for k in ("x", "a", "b")})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("gate,weighting", KINDS)
+@pytest.mark.parametrize("keep", ["states", "8bit"])
+def test_masked_gates(io, gate, weighting, keep):
+    """-infinity in a and b, in whole rows, parts of a block of 64 channels and single values: the definition's results and gradients
+    at arguments so low that in 64 bits nothing is left of the gate (e^-800 is 0)."""
+    m = on_the_codes(draw(io, [150, 3, 90], 130, gate=gate, weighting=weighting, seed=31))
+    g = torch.Generator().manual_seed(32)
+    shut, closed = ((torch.rand(1, 243, 130, generator=g) < 0.1).cuda() for _ in range(2))
+    shut[:, 20:60], shut[:, 64, 64:], shut[:, 70:80, 7], closed[:, 30:70] = True, True, True, True
+    m["a"], m["b"] = m["a"].masked_fill(shut, -math.inf), m["b"].masked_fill(closed, -math.inf)
+    y, state, kept = prefill(m, keep)
+    got = backward(m, kept)
+    assert all(torch.isfinite(t).all() for t in (y, state, *got))
+    far = dict(m, a=m["a"].float().clamp_min(-800), b=m["b"].float().clamp_min(-800))
+    check(far, (y, state))
+    check_gradients(far, got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
+def test_a_masked_gate_leaves_its_block(io):
+    """One channel's mask, and codes that are not exact: the others' gradients are the same bits.  (The masked entries are 0 before, so
+    they are no block's largest.)  Another infinity, or a NaN, makes its block NaN."""
+    m = draw(io, [90], 128, seed=33)
+    m["a"], m["b"] = m["a"].clone(), m["b"].clone()
+    m["a"][:, 10:30, 5], m["b"][:, 20, 100] = 0, 0
+    before = backward(m, prefill(m, "8bit")[2])
+    m["a"][:, 10:30, 5], m["b"][:, 20, 100] = -math.inf, -math.inf
+    after = backward(m, prefill(m, "8bit")[2])
+    others = [c for c in range(128) if c not in (5, 100)]
+    assert all(torch.equal(s[..., others], t[..., others]) and torch.isfinite(t).all() for s, t in zip(before, after))
+    for bad in (math.inf, math.nan):
+        m["a"][:, 40, 70] = bad
+        assert backward(m, prefill(m, "8bit")[2])[1][0, 40, 64:].isnan().all()
+
+
 @pytest.mark.gpu
 def test_gradients_without_a_final_states_gradient():
     for keep in ("states", "8bit"):
