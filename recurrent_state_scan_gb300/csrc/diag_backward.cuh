@@ -6,9 +6,10 @@
 //     da = dg g (1 - s) (sigmoid gate) | -dg e^A_log s (softplus gate),
 //     dA_log = sum dg g,  da_bias = sum da,  db_bias = sum db,  dstate_in = alpha G at a sequence's first row.
 // The walk is the forward pass's, from the last tile to the first: warps fold their rows to G's map, a fifth warp hands it on, and
-// while that one waits they run h forward again from the kept states.  Of what the gates give, the decays' exponents G and h stay in
-// shared memory for the last pass over the rows; the rest is made again, in loops of four rows (all 16 in a row, their code did
-// not fit the instruction cache: 440 us for 16,384 rows of 4,096 where these take 245).  The rows that come an iteration later are
+// while that one waits they run h forward again from the kept states.  Of what the gates give, the decays' exponents G (of a sigmoid
+// gate its e^-z, from which s, G and 1 - s follow; with G alone 1 - s = 1 - G / e^A_log loses the digits of a gate that is nearly open,
+// and takes 255 us in place of 268) and h stay in shared memory for the last pass over the rows; the rest is made again, in loops of
+// four rows (all 16 in a row, their code did not fit the instruction cache: 440 us for 16,384 rows of 4,096 where these take 245).  The rows that come an iteration later are
 // fetched into L2 meanwhile (247 us; without 255).
 //
 // Bound by instructions: 78 a value (89 from codes), at 58% of the issue slots; with the gates' arithmetic taken out and no wait
@@ -27,9 +28,9 @@ constexpr int LT = kDiagRows, W = kDiagTile / LT;      // a warp's rows; the war
 constexpr int kThreads = (W + 1) * 32;
 constexpr int kGroup = 4;                       // rows whose loads go out together
 
-// A warp's rows as they are staged, and of what the gates give the decays' exponents G and the inputs w i x, which become h.  The
-// staged a lies at the end of G's place: G's rows are written when a's that lie there have been read.  (Each array is copied to 16
-// bytes at a time, the steps too.)
+// A warp's rows as they are staged, and of what the gates give the decays' exponents (or what they follow from) in G and the inputs
+// w i x, which become h.  The staged a lies at the end of G's place: G's rows are written when a's that lie there have been read.
+// (Each array is copied to 16 bytes at a time, the steps too.)
 template <typename IO, bool CODES> struct Staged {
     alignas(16) IO x[LT][kDiagSlice], b[LT][kDiagSlice], dy[LT][kDiagSlice];
     alignas(16) float2 G[LT][32], h[LT][32];
@@ -285,6 +286,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
             }
             __syncwarp();
         }
+        // Of what stays in G's place, the exponent.
+        auto exponent = [&](F2 held) { return GATE == GDN_DIAG_SIGMOID ? mul2(l.rate, diag_opening(held)) : held; };
         // What G's map needs, for the fifth warp to hand on; with codes h's map as well, from which the other warps find their h.
         F2 through = both(1.f), H = both(0.f);
         auto minus_input = [&](Argument b, F2 x, F2 n) {
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
 #pragma unroll 1
             for (int t0 = 0; t0 < LT; t0 += kGroup) {       // (the loads of a group go out before its stores)
                 Argument a[kGroup], b[kGroup];
-                F2 x[kGroup], dy[kGroup], G[kGroup];
+                F2 x[kGroup], dy[kGroup], held[kGroup];
                 get_a(a, t0, decltype(masks)::value);
                 if (CODES) {
                     get_b(b, t0, decltype(masks)::value);
@@ -307,13 +310,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k) {
-                    G[k] = diag_exponent<GATE>(a[k].v, l, a[k].by);
-                    if (!kNear) {       // held finite, for a decay to 0 times it; a NaN stays one
-                        asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(G[k].x));
-                        asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(G[k].y));
+                    if (GATE == GDN_DIAG_SIGMOID) {
+                        held[k] = diag_closing(a[k].v, l.nabias, a[k].by);
+                    } else {            // finite, for a decay to 0 times it; a NaN stays one
+                        held[k] = diag_exponent<GATE>(a[k].v, l, a[k].by);
+                        asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(held[k].x));
+                        asm("min.NaN.f32 %0, %0, 0f7149F2CA;" : "+f"(held[k].y));
                     }
-                    sum_G = add2(sum_G, G[k]);
-                    const DiagDecay d = diag_decay<kNear>(G[k]);
+                    const F2 G = exponent(held[k]);
+                    sum_G = add2(sum_G, G);
+                    const DiagDecay d = diag_decay<kNear>(G);
                     through = mul2(through, d.alpha);
                     D = fma2(through, dy[k], D);
                     if (CODES) {
@@ -323,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                 }
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k) {
-                    sG[(t0 + k) * 32 + lane] = make_float2(G[k].x, G[k].y);
+                    sG[(t0 + k) * 32 + lane] = make_float2(held[k].x, held[k].y);
                     if (CODES) sh_[(t0 + k) * 32 + lane] = make_float2(x[k].x, x[k].y);
                 }
             }
@@ -332,11 +338,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         else if (near) take(std::true_type{}, std::false_type{});
         else take(std::false_type{}, std::false_type{});
         if (!full) {            // rows outside are the identity, whatever the parameters make of them (an infinite bias: NaN)
+            const float none = GATE == GDN_DIAG_SIGMOID ? __uint_as_float(0x7f800000u) : 0.f;
             sum_G = D = both(0.f);
 #pragma unroll 1
             for (int t = 0; t < LT; ++t) {
-                if (w0 + t < rows) sum_G = add2(sum_G, get_pair(sG + t * 32, lane));
-                else sG[t * 32 + lane] = make_float2(0.f, 0.f);
+                if (w0 + t < rows) sum_G = add2(sum_G, exponent(get_pair(sG + t * 32, lane)));
+                else sG[t * 32 + lane] = make_float2(none, none);
             }
         }
         if (special) {          // nothing behind a sequence's first row comes back to here
@@ -347,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                 F2 dy = staged(&st.dy[0][0], t, lane);
                 if ((ends >> t & 1) && p.dstate_out)
                     dy = add2(dy, load_state(p.dstate_out + (int64_t)(sh.edge_first[w][t + 1] - 1) * C, c, C));
-                through = mul2(through, diag_decay<false>(get_pair(sG + t * 32, lane)).alpha);
+                through = mul2(through, diag_decay<false>(exponent(get_pair(sG + t * 32, lane))).alpha);
                 D = fma2(through, dy, D);
             }
         }
@@ -355,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
         auto follow_edges = [&](F2 nat, bool map) {
 #pragma unroll 1
             for (int t = 0; t < LT; ++t) {
-                const DiagDecay d = diag_decay<false>(get_pair(sG + t * 32, lane));
+                const DiagDecay d = diag_decay<false>(exponent(get_pair(sG + t * 32, lane)));
                 if (begins >> t & 1) {
                     nat = p.state_in ? load_state(p.state_in + (int64_t)sh.edge_last[w][t] * C, c, C) : both(0.f);
                     nat = mul2(nat, both(-1.f));
@@ -393,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                 }
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k) {
-                    G[k] = get_pair(sG + (t0 + k) * 32, lane);
+                    G[k] = exponent(get_pair(sG + (t0 + k) * 32, lane));
                     if (CODES) x[k] = get_pair(sh_ + (t0 + k) * 32, lane);
                 }
 #pragma unroll
@@ -429,13 +436,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
 #pragma unroll 1
                 for (int t0 = LT - N; t0 >= 0; t0 -= N) {
                     Argument b[N];
-                    F2 x[N], dy[N], G[N], h[N];
+                    F2 x[N], dy[N], held[N], h[N];
                     get_b(b, t0, !kPlain && masked);
                     get_x(x, t0);
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
                         dy[k] = staged(&st.dy[0][0], t0 + k, lane);
-                        G[k] = get_pair(sG + (t0 + k) * 32, lane);
+                        held[k] = get_pair(sG + (t0 + k) * 32, lane);
                         h[k] = get_pair(sh_ + (t0 + k) * 32, lane);
                     }
                     F2 out_x[N], out_a[N], out_b[N];
@@ -445,8 +452,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                         F2 g = add2(dy[k], back);           // the gradient at h_t
                         if (!kPlain && (ends >> t & 1) && p.dstate_out)
                             g = add2(g, load_state(p.dstate_out + (int64_t)(sh.edge_first[w][t + 1] - 1) * C, c, C));
-                        const F2 i = diag_sigmoid(b[k].v, l.nbbias, b[k].by), v = mul2(i, x[k]), minus = both(-1.f);
-                        const DiagDecay d = diag_decay<decltype(only_near)::value>(G[k]);
+                        const F2 close_b = diag_closing(b[k].v, l.nbbias, b[k].by), i = diag_opening(close_b), v = mul2(i, x[k]);
+                        const F2 s = diag_opening(held[k]), G = GATE == GDN_DIAG_SIGMOID ? mul2(l.rate, s) : held[k];
+                        const DiagDecay d = diag_decay<decltype(only_near)::value>(G);
                         F2 slope = h[k], weight = d.n;                              // dG / (g alpha), G = -g (h: negative)
                         if (WEIGHT == GDN_DIAG_NORM) {
                             const F2 unweight = diag_unweigh(d.n);
@@ -455,12 +463,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                         }
                         if (WEIGHT == GDN_DIAG_COMPLEMENT) slope = add2(v, slope);
                         const F2 ag = mul2(d.alpha, g), dv = WEIGHT == GDN_DIAG_PLAIN ? g : mul2(g, weight);
-                        const F2 dG = mul2(ag, slope), dGG = mul2(dG, G[k]);
-                        const F2 nsp = mul2(G[k], l.ninverse);                      // the gate's opening, negative
-                        const F2 da_ = GATE == GDN_DIAG_SIGMOID ? fma2(dGG, nsp, dGG)
+                        const F2 dG = mul2(ag, slope), dGG = mul2(dG, G);
+                        const F2 nsp = mul2(G, l.ninverse);                         // a softplus gate's opening, negative
+                        const F2 da_ = GATE == GDN_DIAG_SIGMOID ? mul2(dGG, diag_closed(held[k], s))
                                                                 : mul2(dG, mul2(l.rate, diag_decay<false>(F2{-nsp.x, -nsp.y}).n));
                         out_x[k] = mul2(dv, i);
-                        const F2 db_ = mul2(out_x[k], fma2(v, minus, x[k]));        // dx x (1 - i)
+                        const F2 db_ = mul2(out_x[k], mul2(diag_closed(close_b, i), x[k]));     // dx x (1 - i)
                         out_a[k] = da_;
                         out_b[k] = db_;
                         if (kPlain || w0 + t < rows) {

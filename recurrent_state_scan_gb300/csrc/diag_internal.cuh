@@ -120,7 +120,24 @@ __device__ __forceinline__ F2 diag_sigmoid(F2 v, F2 nbias, float k = -kLog2e) {
     const F2 d = add2({ex2(t.x), ex2(t.y)}, both(1.f));
     return {rcp(d.x), rcp(d.y)};
 }
-// Its negative, by the same steps.
+// e = e^-(v + bias), of which the gate is s = diag_opening(e), as diag_sigmoid has it, and 1 - s = e s, which keeps its digits however
+// far the gate is open (as a difference from 1 it has lost half of them at v = 8, all at 16).  Where e has become infinite and s 0, the
+// saturated product is 0 in place of 1: what it multiplies is 0 there.
+__device__ __forceinline__ F2 diag_closing(F2 v, F2 nbias, float k = -kLog2e) {
+    const F2 t = fma2(v, both(k), nbias);
+    return {ex2(t.x), ex2(t.y)};
+}
+__device__ __forceinline__ F2 diag_opening(F2 e) {
+    const F2 d = add2(e, both(1.f));
+    return {rcp(d.x), rcp(d.y)};
+}
+__device__ __forceinline__ F2 diag_closed(F2 e, F2 s) {
+    F2 r;
+    asm("mul.sat.f32 %0, %1, %2;" : "=f"(r.x) : "f"(e.x), "f"(s.x));
+    asm("mul.sat.f32 %0, %1, %2;" : "=f"(r.y) : "f"(e.y), "f"(s.y));
+    return r;
+}
+// The sigmoid's negative, by the same steps.
 __device__ __forceinline__ F2 diag_minus_sigmoid(F2 v, F2 nbias, float k = -kLog2e) {
     const F2 t = fma2(v, both(k), nbias);
     const F2 d = fma2({ex2(t.x), ex2(t.y)}, both(-1.f), both(-1.f));

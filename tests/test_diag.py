@@ -626,6 +626,28 @@ def test_a_masked_gate_leaves_its_block(io):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("gate,weighting", KINDS)
+@pytest.mark.parametrize("keep", ["states", "8bit"])
+@pytest.mark.parametrize("slow", [False, True])
+def test_open_gates_keep_their_digits(gate, weighting, keep, slow):
+    """Gates open by z of 5 to 19, every gradient on its own.  1 - s = e s has e^-z off by the argument's roundings, 3 x 2^-24 log2 e
+    (16 + 3) ln 2 = 3.4e-6, and by 4 x 2^-23 of the exponential, the quotient and the product: inside F.  The other factors are off by F of
+    their terms: x and the states are positive, so that h has no cancellation.  (Multiples of 1/4 that the codes hold.)"""
+    T, C = 48, 64
+    m = draw("f32", [T], C, gate=gate, weighting=weighting, seed=33)
+    g = torch.Generator().manual_seed(34)
+    quarters = lambda lo, hi: (torch.randint(4 * lo, 4 * hi + 1, (1, T, C), generator=g) / 4).cuda()  # noqa: E731
+    m.update(a=quarters(8, 16), b=quarters(8, 16), x=quarters(1, 4), state=m["state"].abs())
+    if slow:
+        m["A_log"] = slow_rates(C, 35)
+    _, _, kept = prefill(m, keep)
+    want = define_gradients(m)
+    for name, t in zip(NAMES, backward(m, kept)):
+        off = (t.double().cpu().view(want[name][0].shape) - want[name][0]).abs()
+        assert (off <= 2 * F * want[name][1]).all(), (name, float((off / want[name][1]).max()))
+
+
+@pytest.mark.gpu
 def test_gradients_without_a_final_states_gradient():
     for keep in ("states", "8bit"):
         m = draw("f32", [63, 0, 200], 70, seed=2)
