@@ -463,10 +463,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_backwa
                         }
                         if (WEIGHT == GDN_DIAG_COMPLEMENT) slope = add2(v, slope);
                         const F2 ag = mul2(d.alpha, g), dv = WEIGHT == GDN_DIAG_PLAIN ? g : mul2(g, weight);
-                        const F2 dG = mul2(ag, slope), dGG = mul2(dG, G);
+                        // (The products with G come first: a shut gate's is 0, whatever x is.)
+                        const F2 dGG = mul2(mul2(ag, G), slope);
                         const F2 nsp = mul2(G, l.ninverse);                         // a softplus gate's opening, negative
                         const F2 da_ = GATE == GDN_DIAG_SIGMOID ? mul2(dGG, diag_closed(held[k], s))
-                                                                : mul2(dG, mul2(l.rate, diag_decay<false>(F2{-nsp.x, -nsp.y}).n));
+                                                                : mul2(mul2(ag, mul2(l.rate, diag_decay<false>(F2{-nsp.x, -nsp.y}).n)), slope);
                         out_x[k] = mul2(dv, i);
                         const F2 db_ = mul2(out_x[k], mul2(diag_closed(close_b, i), x[k]));     // dx x (1 - i)
                         out_a[k] = da_;

@@ -160,7 +160,7 @@ __device__ __forceinline__ F2 diag_softplus(F2 z) {
 struct DiagLane {
     F2 rate, ninverse, abias, nabias, nbbias;   // e^A_log, -1 / e^A_log (or 0), a_bias, -a_bias log2 e, -b_bias log2 e
 };
-// The input's weight, and for the backward pass and `norm` (sqrt(1 - alpha^2)) 1 / w, finite at alpha = 1 where the weight is 0.
+// The input's weight, and for the backward pass and `norm` (sqrt(1 - alpha^2)) 1 / w, which counts as 0 where the weight is 0.
 template <int WEIGHT> __device__ __forceinline__ F2 diag_weigh(F2 n) {
     if (WEIGHT == GDN_DIAG_COMPLEMENT) return n;
     if (WEIGHT == GDN_DIAG_PLAIN) return both(1.f);
@@ -171,11 +171,11 @@ template <int WEIGHT> __device__ __forceinline__ F2 diag_weigh(F2 n) {
     return w;
 }
 __device__ __forceinline__ F2 diag_unweigh(F2 n) {
-    const F2 q = fma2(n, fma2(n, both(-1.f), both(2.f)), both(0x1p-122f));
+    const F2 q = mul2(n, fma2(n, both(-1.f), both(2.f)));
     F2 r;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(q.x));
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(q.y));
-    return r;
+    return {q.x < 0x1p-126f ? 0.f : r.x, q.y < 0x1p-126f ? 0.f : r.y};
 }
 // (`by`: for a in units of a power of two, which it then holds as a factor.)
 template <int GATE> constexpr float kGateUnit = GATE == GDN_DIAG_SIGMOID ? -kLog2e : 1.f;

@@ -648,6 +648,28 @@ def test_open_gates_keep_their_digits(gate, weighting, keep, slow):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", ["softplus", "sigmoid"])
+@pytest.mark.parametrize("weighting", ["norm", "complement"])
+@pytest.mark.parametrize("keep", ["states", "8bit"])
+@pytest.mark.parametrize("slow", [False, True])
+def test_large_values_behind_a_mask(io, gate, weighting, keep, slow):
+    """A shut gate's token has the weight 0: what finite x it brings reaches nothing."""
+    m = draw(io, [150], 64, gate=gate, weighting=weighting, seed=35)
+    if slow:
+        m["A_log"] = slow_rates(64, 36)
+    m["a"], m["x"] = m["a"].clone(), m["x"].clone()
+    m["a"][:, 40:75] = -math.inf
+    outs = []
+    for value in (0.0, 1e30, -torch.finfo(m["io"]).max):
+        m["x"][:, 40:75] = value
+        y, state, kept = prefill(m, keep)
+        outs.append((y, state, *backward(m, kept)))
+    for out in outs[1:]:
+        assert all(torch.equal(s, t) for s, t in zip(outs[0], out))
+
+
+@pytest.mark.gpu
 def test_gradients_without_a_final_states_gradient():
     for keep in ("states", "8bit"):
         m = draw("f32", [63, 0, 200], 70, seed=2)
