@@ -187,8 +187,8 @@ __device__ __forceinline__ DiagLane diag_lane(const float *A_log, const float *a
     DiagLane l{};
     const bool one = c < C, two = c + 1 < C;
     l.rate = {one ? -ssm_rate(A_log[c]) : 0.f, two ? -ssm_rate(A_log[c + 1]) : 0.f};
-    // (A rate is a normal number or 0, whose channel's gate then counts as shut.)
-    l.ninverse = {l.rate.x != 0.f ? -1.f / l.rate.x : 0.f, l.rate.y != 0.f ? -1.f / l.rate.y : 0.f};
+    // (Held finite for rates below the normal numbers, A_log < -87, whose products with the gate are below 2^-126 whatever it is.)
+    l.ninverse = {l.rate.x != 0.f ? fmaxf(-1.f / l.rate.x, -0x1p127f) : 0.f, l.rate.y != 0.f ? fmaxf(-1.f / l.rate.y, -0x1p127f) : 0.f};
     if (a_bias) l.abias = {one ? a_bias[c] : 0.f, two ? a_bias[c + 1] : 0.f};
     F2 bb = both(0.f);
     if (b_bias) bb = {one ? b_bias[c] : 0.f, two ? b_bias[c + 1] : 0.f};

@@ -670,6 +670,27 @@ def test_large_values_behind_a_mask(io, gate, weighting, keep, slow):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("gate,weighting", KINDS)
+@pytest.mark.parametrize("keep", ["states", "8bit"])
+def test_rates_below_the_normal_range(gate, weighting, keep):
+    """e^A_log down to 0, some gates shut: decays of 1 in fp32, and no gradient is NaN or infinite."""
+    m = on_the_codes(draw("f32", [100], 64, gate=gate, weighting=weighting, seed=36))
+    m["A_log"] = m["A_log"].clone()
+    m["A_log"][:8] = torch.tensor([-87.0, -87.5, -88.5, -90.0, -95.0, -103.0, -110.0, -math.inf])
+    m["a"] = m["a"].clone()
+    m["a"][:, 10:20] = -math.inf
+    y, state, kept = prefill(m, keep)
+    got = backward(m, kept)
+    assert all(torch.isfinite(t).all() for t in (y, state, *got))
+    far = dict(m, a=m["a"].clamp_min(-800))
+    check(far, (y, state))
+    check_gradients(far, got)
+    states = m["state"].clone()
+    lib.gdn_diag_decode(*(m[k][:, :1] for k in ("x", "a", "b")), m["A_log"], states, **kinds(m))
+    assert torch.isfinite(states).all() and (weighting == "plain" or torch.equal(states[:, 1:8], m["state"][:, 1:8]))
+
+
+@pytest.mark.gpu
 def test_gradients_without_a_final_states_gradient():
     for keep in ("states", "8bit"):
         m = draw("f32", [63, 0, 200], 70, seed=2)
