@@ -622,7 +622,8 @@ typedef struct gdn_diag_shape {
  *   workspace    gdn_diag_prefill_workspace_bytes(shape) bytes (0 up to 64 rows), 16-byte
  *                aligned; its contents need no initialisation and are not preserved.  Calls
  *                that overlap on the GPU need one each.
- * An infinity or a NaN reaches the rest of its channel and sequence, no other (in the backward
+ * An infinity or a NaN reaches the rest of its channel and sequence, no other: an infinite h stays
+ * infinite, and is a NaN from a decay on that is 0 in fp32 (in the backward
  * pass with KEEP_8BIT the other channels of its block of 64 too, unless it is a -infinity that
  * holds a gate shut).  Outputs may not overlap inputs or one another (slices of one wider row, side by side, do not).
  */

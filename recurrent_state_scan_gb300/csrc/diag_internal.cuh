@@ -540,7 +540,10 @@ __device__ __forceinline__ uint32_t find_edges(const DiagParams &p, EdgeWindow &
 // A stretch of tokens as the map h -> (hi + lo) h + H: the product of its decays in two fp32 numbers, because the
 // chain of these maps over a long sequence has to keep slow decays (hi alone drifts: 65,536 equal tokens of
 // 1 - 3e-5 by up to 2e-3) as well as the digits of fast ones.  hi = -1 marks a stretch that holds an edge, the
-// same for all lanes: nothing of what came before is left behind it, an infinity or a NaN neither.
+// same for all lanes: nothing of what came before is left behind it, an infinity or a NaN neither.  In the forward pass hi is 0 only
+// where a token's decay is: it is held at 2^-149 where only the product has become 0, so that an infinite h stays infinite over
+// the stretch as it does token by token.
+constexpr float kLeast = 0x1p-149f;
 struct DiagProduct {
     F2 hi, lo;
 };
@@ -554,15 +557,17 @@ __device__ __forceinline__ DiagProduct diag_product(F2 sum_G, bool edge) {
     return o;
 }
 __device__ __forceinline__ F2 diag_apply(DiagProduct p, F2 H, F2 h) {
-    const F2 r = fma2(p.hi, h, fma2(p.lo, h, H));
+    const F2 r = fma2(p.hi, h, fma2(p.lo, h, H)), far = fma2(p.hi, h, H);       // (lo times an infinite h has a sign of its own, or is NaN)
     const bool edge = p.hi.x < 0.f;
-    return {edge ? H.x : r.x, edge ? H.y : r.y};
+    return {edge ? H.x : isinf(h.x) ? far.x : r.x, edge ? H.y : isinf(h.y) ? far.y : r.y};
 }
 __device__ __forceinline__ DiagProduct diag_join(DiagProduct p, DiagProduct q) {
     DiagProduct o;
     o.hi = mul2(p.hi, q.hi);
     const F2 lost = fma2(p.hi, q.hi, {-o.hi.x, -o.hi.y});
     o.lo = fma2(p.hi, q.lo, fma2(p.lo, q.hi, lost));
+    if (o.hi.x == 0.f && p.hi.x != 0.f && q.hi.x != 0.f) o.hi.x = kLeast;
+    if (o.hi.y == 0.f && p.hi.y != 0.f && q.hi.y != 0.f) o.hi.y = kLeast;
     if (p.hi.x < 0.f || q.hi.x < 0.f) o.hi = both(-1.f);
     return o;
 }

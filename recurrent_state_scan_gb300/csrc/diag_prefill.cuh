@@ -162,7 +162,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3) diag_prefil
                     }
                 }
             }
-            put_map(sh.maps[buf][w], lane, diag_product(sum_G, begins != 0), H);
+            DiagProduct product = diag_product(sum_G, begins != 0);
+            if (product.hi.x == 0.f || product.hi.y == 0.f) {
+                F2 least = both(1.f);
+#pragma unroll
+                for (int t = 0; t < LT; ++t) least = {fminf(least.x, alpha[t].x), fminf(least.y, alpha[t].y)};
+                if (product.hi.x == 0.f && least.x > 0.f) product.hi.x = kLeast;
+                if (product.hi.y == 0.f && least.y > 0.f) product.hi.y = kLeast;
+            }
+            put_map(sh.maps[buf][w], lane, product, H);
             __syncwarp();
             side_arrive<kThreads>(1 + buf);
         }

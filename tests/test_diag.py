@@ -519,6 +519,44 @@ def test_a_sequence_does_not_see_its_neighbours(io, keep):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rate", [-4.0, 0.5, 2.0])
+def test_an_infinite_state_stays_infinite(io, rate):
+    """Behind warps' rows and tiles too, where decays' products have long become 0."""
+    m = draw(io, [400, 9, 200], 130, gate="softplus", weighting="complement", seed=37)
+    m["A_log"] = torch.full((130,), rate, device="cuda")
+    m["x"], m["state"] = m["x"].clone(), m["state"].clone()
+    m["state"][0, 3], m["state"][0, 70], m["state"][2, 5] = math.inf, -math.inf, math.inf
+    m["x"][0, 101, 9], m["x"][0, 63, 129], m["x"][0, 350, 3] = -math.inf, math.inf, -math.inf
+    y, state, _ = prefill(m)
+    h, states, _ = define(m)
+    assert h.isinf().sum() > 1000
+    for got, want in ((y[0], h), (state, states)):
+        got = got.double().cpu()
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+        assert torch.equal(got[want.isinf()], want[want.isinf()])
+
+
+@pytest.mark.gpu
+def test_an_infinite_state_ends_at_a_decay_of_0():
+    """e^-100 of it is 0 in fp32: NaN from there on, in one call, in two and token by token."""
+    m = draw("f32", [200], 64, gate="softplus", weighting="plain", packed=False, seed=38)
+    m["A_log"], m["state"], m["a"] = torch.zeros(64, device="cuda"), m["state"].clone(), m["a"].clone()
+    m["state"][0, 7], m["a"][0, 90] = math.inf, 110.0
+    y, state, _ = prefill(m)
+    assert y[0, :90, 7].isinf().all() and y[0, 90:, 7].isnan().all() and state[0, 7].isnan()
+    cut = lambda lo, hi: dict(m, **{k: m[k][:, lo:hi].contiguous() for k in ("x", "a", "b")})  # noqa: E731
+    for at in (50, 90, 91, 130):
+        y0, s, _ = prefill(cut(0, at))
+        y1, s, _ = prefill(dict(cut(at, 200), state=s))
+        assert torch.equal(torch.cat([y0, y1], 1).isnan(), y.isnan()) and s[0, 7].isnan()
+    s, rows = m["state"].clone(), []
+    for t in range(200):
+        rows.append(lib.gdn_diag_decode(*(m[k][:, t:t + 1] for k in ("x", "a", "b")), m["A_log"], s, **kinds(m)))
+    assert torch.equal(torch.cat(rows, 1).isnan(), y.isnan())
+
+
+@pytest.mark.gpu
 def test_chained_calls_and_states_in_place():
     m = draw("bf16", [300], 96, packed=False, seed=7)
     y, state, _ = prefill(m)
