@@ -599,7 +599,7 @@ typedef struct gdn_diag_shape {
     int32_t io_dtype;   /* gdn_dtype of x, a, b, y and their gradients                     */
     int32_t batch;      /* B; must be 1 when cu_seqlens is given                           */
     int64_t seqlen;     /* T per sequence, or the packed token total with cu_seqlens       */
-    int32_t num_seqs;   /* N: equals batch, or len(cu_seqlens) - 1 with cu_seqlens         */
+    int32_t num_seqs;   /* N: equals batch, or len(cu_seqlens) - 1 (below 2^30) with it    */
     int32_t channels;   /* C, 1 .. 4,194,240                                               */
     int32_t gate;       /* gdn_diag_gate                                                   */
     int32_t weighting;  /* gdn_diag_weighting                                              */

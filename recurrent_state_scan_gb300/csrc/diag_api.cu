@@ -64,6 +64,8 @@ gdn_status check(const gdn_diag_shape *s, bool varlen, Geometry &g) {
     if (varlen ? s->batch != 1 : s->batch != s->num_seqs)
         return fail(GDN_ERR_INVALID_ARG, "batch must be 1 with cu_seqlens, and equal num_seqs without (batch %d, num_seqs %d)",
                     s->batch, s->num_seqs);
+    // (What looks through cu_seqlens adds up to 1,024 to an index, and 32 parts of what is left of them.)
+    if (varlen && s->num_seqs > INT32_MAX / 2) return fail(GDN_ERR_UNSUPPORTED, "%d sequences are not built", s->num_seqs);
     if (s->channels <= 0) return fail(GDN_ERR_INVALID_ARG, "channels (%d) must be positive", s->channels);
     if (s->channels > 65535 * kDiagSlice) return fail(GDN_ERR_UNSUPPORTED, "%d channels are not built", s->channels);
     if (s->gate != GDN_DIAG_SOFTPLUS && s->gate != GDN_DIAG_SIGMOID)

@@ -258,6 +258,14 @@ def test_refused_pointers(which, where):
     assert gdn.load().gdn_last_error_message().decode()
 
 
+@pytest.mark.parametrize("which", ["prefill", "backward"])
+@pytest.mark.parametrize("num_seqs", [2 ** 30, 2 ** 31 - 200, 2 ** 31 - 1])
+def test_refused_numbers_of_sequences(which, num_seqs):
+    """More than the search through cu_seqlens can count to."""
+    assert call(which, dict(batch=1, num_seqs=num_seqs, seqlen=16), cu=1 << 40) == gdn.GDN_ERR_UNSUPPORTED
+    assert "sequences" in gdn.load().gdn_last_error_message().decode()
+
+
 @pytest.mark.parametrize("which,out", [("prefill", "y"), ("prefill", "state_out"), ("backward", "dx"), ("backward", "dstate_in")])
 def test_refused_offsets(which, out):
     packed = dict(batch=1, num_seqs=3, seqlen=16)
