@@ -1094,6 +1094,8 @@ def _diag_shape(io, B, T, n, C, gate, weighting, has_b, keep, *strides):
     if gate not in DIAG_GATES or weighting not in DIAG_WEIGHTINGS or keep not in DIAG_KEEPS:
         raise GdnError(GDN_ERR_INVALID_ARG, f"gate must be one of {sorted(DIAG_GATES)}, weighting of {sorted(DIAG_WEIGHTINGS)}, "
                                             "keep None, 'states' or '8bit'")
+    if max(B, n, C) > 2 ** 31 - 1:          # (the shape's fields would keep their low 32 bits)
+        raise GdnError(GDN_ERR_UNSUPPORTED, f"a batch of {B}, {n} sequences or {C} channels is not built")
     lib = load()
     ref = ctypes.byref(GdnDiagShape(_DTYPE_CODE[io], B, T, n, C, DIAG_GATES[gate], DIAG_WEIGHTINGS[weighting], has_b, DIAG_KEEPS[keep], *strides))
     return ref, lib.gdn_diag_kept_bytes(ref), lib.gdn_diag_prefill_workspace_bytes(ref), lib.gdn_diag_backward_workspace_bytes(ref)

@@ -266,6 +266,14 @@ def test_refused_numbers_of_sequences(which, num_seqs):
     assert "sequences" in gdn.load().gdn_last_error_message().decode()
 
 
+@pytest.mark.parametrize("B,n,C", [((1 << 32) + 1, (1 << 32) + 1, 64), (1, (1 << 32) + 3, 64), (1, 1, (1 << 32) + 64), (1 << 31, 1 << 31, 1)])
+def test_the_binding_refuses_sizes_beyond_32_bits(B, n, C):
+    """Their low 32 bits would be another call's."""
+    with pytest.raises(gdn.GdnError) as refused:
+        gdn._diag_shape(torch.bfloat16, B, 1, n, C, "sigmoid", "norm", True, None, C, C, C, C)
+    assert refused.value.status == gdn.GDN_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("which,out", [("prefill", "y"), ("prefill", "state_out"), ("backward", "dx"), ("backward", "dstate_in")])
 def test_refused_offsets(which, out):
     packed = dict(batch=1, num_seqs=3, seqlen=16)
