@@ -644,6 +644,7 @@ gdn_status gdn_diag_prefill(const gdn_diag_shape *shape, const void *x, const vo
  *   dA_log, da_bias, db_bias [C], dstate_in [N, C]: fp32, each may be NULL (not wanted).
  *   workspace    gdn_diag_backward_workspace_bytes(shape) bytes, 16-byte aligned; its
  *                contents need no initialisation and are not preserved.
+ * An infinite gradient may become a NaN on its way back through its channel and sequence.
  * Sums run in a fixed order: the same bits on every call.  At alpha_t = 1 the gradient of
  * w_t (NORM), which has no bound there, counts as 0.
  */

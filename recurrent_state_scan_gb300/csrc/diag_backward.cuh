@@ -7,14 +7,14 @@
 //     dA_log = sum dg g,  da_bias = sum da,  db_bias = sum db,  dstate_in = alpha G at a sequence's first row.
 // The walk is the forward pass's, from the last tile to the first: warps fold their rows to G's map, a fifth warp hands it on, and
 // while that one waits they run h forward again from the kept states.  Of what the gates give, the decays' exponents G (of a sigmoid
-// gate its e^-z, from which s, G and 1 - s follow; with G alone 1 - s = 1 - G / e^A_log loses the digits of a gate that is nearly open,
-// and takes 255 us in place of 268) and h stay in shared memory for the last pass over the rows; the rest is made again, in loops of
-// four rows (all 16 in a row, their code did not fit the instruction cache: 440 us for 16,384 rows of 4,096 where these take 245).  The rows that come an iteration later are
-// fetched into L2 meanwhile (247 us; without 255).
+// gate its e^-z, from which s, G and 1 - s follow; with G alone 1 - s = 1 - G / e^A_log loses the digits of a gate that is nearly open:
+// 16,384 rows of 4,096 in 255 us, so in 268) and h stay in shared memory for the last pass over the rows; the rest is made again, in
+// loops of four rows (all 16 in a row, their code did not fit the instruction cache: 440 us where these took 245).  The rows that come
+// an iteration later are fetched into L2 meanwhile (247 us then; without 255).
 //
-// Bound by instructions: 78 a value (89 from codes), at 58% of the issue slots; with the gates' arithmetic taken out and no wait
-// for other tiles the same loads, stores and barriers took 190 us of then 255.  8,192 bf16 rows of 4,096 channels take 119 us
-// (3.9 TB/s; from codes 136), of which the bytes alone would take 69 (54).
+// Bound by instructions: 86 a value (99 from codes), at 60% of the issue slots; with the gates' arithmetic taken out and no wait
+// for other tiles the same loads, stores and barriers took 190 us of then 255.  8,192 bf16 rows of 4,096 channels take 128 us
+// (3.7 TB/s; from codes 145), of which the bytes alone would take 69 (54).
 #pragma once
 
 #include <type_traits>

@@ -7,8 +7,8 @@
 // memory, and store h.  Every input is read once and every output written once; all sequences are one run of rows with
 // edges where h starts anew, so short and long ones cost the same.
 //
-// Bound by instructions: 36 a value (56 with codes), at half the issue slots of the 12 row warps that registers and shared memory
-// leave an SM.  8,192 bf16 rows of 4,096 channels take 64 us (4.2 TB/s; with codes 91), of which the bytes alone would take 40
+// Bound by instructions: 36 a value (58 with codes), at half the issue slots of the 12 row warps that registers and shared memory
+// leave an SM.  8,192 bf16 rows of 4,096 channels take 65 us (4.1 TB/s; with codes 93), of which the bytes alone would take 40
 // (54).  Clusters of CTAs that walk down a slice in step took 82.
 #pragma once
 

@@ -1149,8 +1149,8 @@ def gdn_diag_prefill(x, a, b, A_log, *, a_bias=None, b_bias=None, gate: str = "s
     x, a, b [B, T, C] (b None: no input gate); token rows may be slices of wider ones (contiguous in themselves, evenly
     spaced, none over another).  With cu_seqlens (int32 [N + 1]) B is 1 and T the packed total.  A_log, a_bias, b_bias
     [C] fp32; state_in [N, C] fp32 or None (zeros).  -infinity in a or b holds that gate shut.  keep: what a backward pass will need, 'states' (beside x, a and b
-    themselves), '8bit' (instead of them) or None; `kept` may give the uint8 buffer.  Returns (y, state_out, a
-    GdnDiagKept or None)."""
+    themselves), '8bit' (instead of them) or None; `kept` may give the uint8 buffer.  No autograd graph is recorded, whatever the
+    inputs require: gradients are gdn_diag_backward's.  Returns (y, state_out, a GdnDiagKept or None)."""
     lib = _lib or load()
     dev = _first("x", x, 3)
     io, rows, has_b, f32 = x.dtype, x.shape, b is not None, torch.float32
