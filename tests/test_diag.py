@@ -745,6 +745,44 @@ def test_rates_below_the_normal_range(gate, weighting, keep):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("lens", [[90], [64, 7]])
+def test_the_kept_codes_of_masked_gates(io, lens):
+    """-128 where -infinity was, beside the codes and steps of the row with 0 in its place: up to the type's largest values, in rows that
+    are masked altogether, and in the rows of a tile's end."""
+    C, rows = 130, sum(lens)
+    m = draw(io, lens, C, seed=34)
+    shut = (torch.rand(1, rows, C, generator=torch.Generator().manual_seed(35)) < 0.2).cuda()
+    shut[:, 20:40], shut[:, 3] = True, False
+    for name in ("a", "b"):
+        m[name] = m[name].clone()
+        m[name][:, 5], m[name][:, 6, ::2] = torch.finfo(m["io"]).max, -torch.finfo(m["io"]).max
+        m[name] = m[name].masked_fill(shut, -math.inf)
+    kept = prefill(m, "8bit")[2]
+    slices, tiles = -(-C // 64), -(-rows // 64)
+    data = kept.data[tiles * slices * 256:]
+    codes = data[:3 * slices * tiles * 4096].view(torch.int8).view(3, slices, tiles * 64, 64)
+    steps = data[3 * slices * tiles * 4096:].view(3, slices, tiles * 64)
+    for k, name in enumerate(("a", "b")):
+        want, want_steps = lib.gdn_checkpoint_pack(m[name].masked_fill(shut, 0))
+        assert torch.equal(codes[k + 1, :, :rows].transpose(0, 1).reshape(rows, -1)[:, :C], want[0].masked_fill(shut[0], -128))
+        assert torch.equal(steps[k + 1, :, :rows].T, want_steps[0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate,weighting", KINDS)
+def test_masked_tokens(gate, weighting):
+    """A token whose gates are shut: with COMPLEMENT and NORM, or with both shut, the states stay bit for bit."""
+    m = draw("bf16", [1] * 5, 130, gate=gate, weighting=weighting, packed=False, seed=36)
+    m["a"], m["b"] = torch.full_like(m["a"], -math.inf), m["b"].clone()
+    if weighting == "plain":
+        m["b"].fill_(-math.inf)
+    state = m["state"].clone()
+    y = lib.gdn_diag_decode(m["x"], m["a"], m["b"], m["A_log"], state, **kinds(m))
+    assert torch.equal(state, m["state"]) and torch.equal(y[:, 0], state.bfloat16())
+
+
+@pytest.mark.gpu
 def test_gradients_without_a_final_states_gradient():
     for keep in ("states", "8bit"):
         m = draw("f32", [63, 0, 200], 70, seed=2)
